@@ -23,7 +23,7 @@ EXPORTS = ("csa_decode_create", "csa_decode_destroy", "csa_indexer_topk", "csa_s
            "csa_decode_step", "csa_indexer_scores", "csa_topk_select", "csa_check_batch",
            "csa_get_status", "csa_last_error", "csa_last_launch_count", "csa_abi_version",
            "csa_profile_enable", "csa_profile_read", "csa_indexer_topk_static", "csa_cache_writeback",
-           "csa_debug_set_wait_polls")
+           "csa_debug_set_wait_polls", "csa_norm_rows")
 STAGES = ("plan", "indexer", "topk", "attention")
 
 
@@ -58,6 +58,13 @@ class CBatch(ctypes.Structure):
                 ("raw_block", ctypes.c_int32), ("cmp_block", ctypes.c_int32),
                 ("idx_block", ctypes.c_int32), ("hca_block", ctypes.c_int32),
                 ("table_stride", ctypes.c_int32)]
+
+
+class CNorm(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in ("n", "width", "dtype", "norm")] + [
+        ("eps", ctypes.c_float), ("x", _P), ("x_stride", _I64), ("residual", _P), ("residual_stride", _I64),
+        ("residual_out", _P), ("residual_out_stride", _I64), ("weight", _P), ("out", _P), ("out_stride", _I64),
+        ("codes", _P), ("codes_stride", _I64), ("scale", _P), ("scale_stride", _I64)]
 
 
 _lib = None
@@ -101,10 +108,11 @@ def lib(path: str | None = None):
                                                   vp, vp, vp]
             L.csa_cache_writeback.argtypes = [vp, ctypes.c_int64, vp, i32, vp, ctypes.c_int64,
                                               ctypes.c_int64, ctypes.c_int64, vp, vp]
+            L.csa_norm_rows.argtypes = [ctypes.POINTER(CNorm), vp]
             for name in ("csa_decode_create", "csa_indexer_topk", "csa_sparse_attn", "csa_decode_step",
                          "csa_indexer_scores", "csa_topk_select", "csa_check_batch", "csa_get_status",
                          "csa_profile_enable", "csa_profile_read", "csa_indexer_topk_static",
-                         "csa_cache_writeback", "csa_debug_set_wait_polls"):
+                         "csa_cache_writeback", "csa_debug_set_wait_polls", "csa_norm_rows"):
                 getattr(L, name).restype = ctypes.c_int
             _lib = L
     return _lib
@@ -256,3 +264,133 @@ class Decoder:
         n = (ctypes.c_int32 * 4)()
         _check(lib().csa_profile_read(self.handle, ms, n))
         return {STAGES[i]: (float(ms[i]), int(n[i])) for i in range(4)}
+
+
+# -- operators around the step ------------------------------------------------
+# Each object keeps one call's arguments (the C struct), its output buffers and
+# references to the tensors it points at, and launches when called; a serving
+# loop builds it once and calls it every step on the same buffers.  Like a
+# handle, an object belongs to the device of its tensors and is used with that
+# device current; its calls share its output buffers, so they must be ordered.
+
+_CTYPE = {"torch.bfloat16": CSA_DTYPE_BF16, "torch.float32": CSA_DTYPE_F32}
+
+
+def _dtype_code(t) -> int:
+    c = _CTYPE.get(str(t.dtype))
+    if c is None:
+        raise CsaError(CSA_ERR_UNSUPPORTED, f"dtype must be bfloat16 or float32, got {t.dtype}")
+    return c
+
+
+def _bad(msg: str):
+    raise CsaError(CSA_ERR_INVALID_ARG, msg)
+
+
+def _rows2d(name: str, t, n: int, width: int, dtype=None):
+    """A matrix [n, width] whose rows are contiguous (any row stride)."""
+    if t.dim() != 2 or tuple(t.shape) != (n, width):
+        _bad(f"{name} must have shape ({n}, {width}), got {tuple(t.shape)}")
+    if width > 1 and t.stride(1) != 1:
+        _bad(f"{name}: the elements of a row must be contiguous")
+    if dtype is not None and t.dtype != dtype:
+        _bad(f"{name} must be {dtype}, got {t.dtype}")
+
+
+def _row_stride(t, unit: int = 1) -> int:
+    """Row stride of [n, width]; a single row's stride is never used and given as a valid one."""
+    return int(t.stride(0)) if t.shape[0] > 1 else -(-int(t.shape[1]) // unit) * unit
+
+
+def _empty_rows(like, n: int, width: int, dtype):
+    """[n, width] whose rows start on 16-byte boundaries."""
+    import torch
+    unit = 16 // torch.empty(0, dtype=dtype).element_size()
+    return torch.empty(n, -(-width // unit) * unit, dtype=dtype, device=like.device)[:, :width]
+
+
+class _Operator:
+    """What the operators' objects share: the tensors kept alive, the device and the launch."""
+
+    def _bind(self, entry, struct, tensors):
+        self._entry, self.struct, self._arg = entry, struct, ctypes.byref(struct)
+        self._keep = [t for t in tensors if t is not None]
+        devs = {t.device for t in self._keep}
+        if len(devs) != 1:
+            _bad(f"tensors on different devices: {sorted(map(str, devs))}")
+        dev = devs.pop()
+        self.device = dev.index if dev.type == "cuda" else None
+
+    def _launch(self, stream):
+        import torch
+        if self.device is None:
+            _bad("the tensors are not on a CUDA device")
+        if torch.cuda.current_device() != self.device:
+            _bad(f"the tensors are on cuda:{self.device}, which is not the current device")
+        _check(self._entry(self._arg, torch._C._cuda_getCurrentRawStream(self.device) if stream is None
+                           else _stream(stream)))
+
+
+class NormRows(_Operator):
+    """csa_norm_rows: residual addition, RMS norm, output in x's dtype and / or E4M3 codes with scales.
+
+    x [n, width] bf16 or fp32, residual [n, width] (residual_out: where the sum goes, a buffer of the
+    object by default, `residual` itself for in place), weight [width] or None (ones).  norm=False:
+    the rows as they are.  out / codes: which outputs to make, or the tensors to fill (codes uint8 or
+    float8_e4m3fn [n, width], scale fp32 [n, ceil(width / 128)]).  Calling the object returns
+    {"residual", "out", "codes", "scale"} as far as they are made."""
+
+    def __init__(self, x, weight=None, residual=None, norm: bool = True, eps: float = 1e-6, out=False,
+                 codes=True, scale=None, residual_out=None):
+        import torch
+        dt = _dtype_code(x)
+        if x.dim() != 2:
+            _bad("x must have two dimensions")
+        n, width = (int(v) for v in x.shape)
+        _rows2d("x", x, n, width)
+        if residual is not None:
+            _rows2d("residual", residual, n, width, x.dtype)
+            if residual_out is None:
+                residual_out = _empty_rows(x, n, width, x.dtype)
+            _rows2d("residual_out", residual_out, n, width, x.dtype)
+        elif residual_out is not None:
+            _bad("residual_out given without residual")
+        if weight is not None and (tuple(weight.shape) != (width,) or weight.dtype != x.dtype or
+                                   not weight.is_contiguous()):
+            _bad(f"weight must be contiguous {x.dtype} of shape ({width},)")
+        if out is True:
+            out = _empty_rows(x, n, width, x.dtype)
+        if codes is True:
+            codes = _empty_rows(x, n, width, torch.uint8)
+        out, codes = (None if t is False else t for t in (out, codes))
+        if out is not None:
+            _rows2d("out", out, n, width, x.dtype)
+        if codes is not None:
+            if codes.dtype not in (torch.uint8, torch.float8_e4m3fn):
+                _bad(f"codes must be uint8 or float8_e4m3fn, got {codes.dtype}")
+            _rows2d("codes", codes, n, width)
+            if scale is None:
+                scale = torch.empty(n, -(-width // 128), dtype=torch.float32, device=x.device)
+            _rows2d("scale", scale, n, -(-width // 128), torch.float32)
+        elif scale is not None:
+            _bad("scale given without codes")
+        unit = 8 if dt == CSA_DTYPE_BF16 else 4
+        st = CNorm(n=n, width=width, dtype=dt, norm=1 if norm else 0, eps=eps, x=_ptr(x), x_stride=_row_stride(x, unit),
+                   weight=_ptr(weight))
+        for name, t, u in (("residual", residual, unit), ("residual_out", residual_out, unit), ("out", out, unit),
+                           ("codes", codes, 16), ("scale", scale, 1)):
+            if t is not None:
+                setattr(st, name, _ptr(t))
+                setattr(st, name + "_stride", _row_stride(t, u))
+        self._bind(lib().csa_norm_rows, st, (x, weight, residual, residual_out, out, codes, scale))
+        self._out = {}
+        if residual is not None:
+            self._out["residual"] = residual_out
+        if out is not None:
+            self._out["out"] = out
+        if codes is not None:
+            self._out["codes"], self._out["scale"] = codes.view(torch.float8_e4m3fn), scale
+
+    def __call__(self, stream=None) -> dict:
+        self._launch(stream)
+        return self._out

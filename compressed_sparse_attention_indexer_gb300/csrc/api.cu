@@ -275,6 +275,32 @@ int run_attention(csa_handle* h, const csa_batch* b, const csa::DevBatch& db, co
   return csa::launch_attention(h->dc, db, h->ws, idx, cnt, out, lse, h->num_sms, st, pdl);
 }
 
+// SM count of the current device, asked once per device.
+int device_sms(int* sms) {
+  static std::atomic<int> known[csa::kMaxDevices];
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return cuda_fail(e, "cudaGetDevice");
+  if (dev < 0 || dev >= csa::kMaxDevices) return cuda_fail(cudaErrorInvalidDevice, "cudaGetDevice");
+  *sms = known[dev].load(std::memory_order_relaxed);
+  if (*sms > 0) return CSA_OK;
+  e = cudaDeviceGetAttribute(sms, cudaDevAttrMultiProcessorCount, dev);
+  if (e != cudaSuccess) return cuda_fail(e, "cudaDeviceGetAttribute");
+  known[dev].store(*sms, std::memory_order_relaxed);
+  return CSA_OK;
+}
+
+// A matrix argument of the handle-free operators: its rows start on 16-byte
+// boundaries and do not overlap.
+int check_rows(const char* name, const void* p, int64_t stride, int64_t width, int es) {
+  if (!p) return fail(CSA_ERR_INVALID_ARG, "%s is NULL", name);
+  if (!aligned16(p)) return fail(CSA_ERR_INVALID_ARG, "%s is not 16-byte aligned", name);
+  if (stride < width) return fail(CSA_ERR_INVALID_ARG, "%s_stride below the row width", name);
+  if ((stride * es) % 16 != 0)
+    return fail(CSA_ERR_INVALID_ARG, "%s_stride * element size is not a multiple of 16", name);
+  return CSA_OK;
+}
+
 struct Launches {
   int n = 0;
   bool ok = true;
@@ -284,6 +310,15 @@ struct Launches {
 };
 
 thread_local std::string g_launch_why;  // see csa::launch_fail
+
+// The same for a handle-free entry point with the result of its launch helper.
+int finish_free(int launched) {
+  std::string why;
+  why.swap(g_launch_why);
+  if (launched < 0) return fail(CSA_ERR_CUDA, "kernel launch: %s", why.empty() ? "failed" : why.c_str());
+  g_err.clear();
+  return CSA_OK;
+}
 
 int finish(csa_handle* h, const Launches& L) {
   h->last_launches = L.n;
@@ -749,6 +784,52 @@ int csa_cache_writeback(const void* rows, int64_t rows_stride, const int64_t* sl
   }
   g_err.clear();
   return CSA_OK;
+}
+
+int csa_norm_rows(const csa_norm* a, void* stream) {
+  if (!a) return fail(CSA_ERR_INVALID_ARG, "args is NULL");
+  if (a->dtype != CSA_DTYPE_BF16 && a->dtype != CSA_DTYPE_F32)
+    return fail(CSA_ERR_UNSUPPORTED, "dtype must be CSA_DTYPE_F32 or CSA_DTYPE_BF16");
+  if (a->n < 0 || a->width < 1) return fail(CSA_ERR_INVALID_ARG, "need n >= 0 and width >= 1");
+  if (a->width > csa::norm_max_width(a->dtype))
+    return fail(CSA_ERR_UNSUPPORTED, "width %d above %d", a->width, csa::norm_max_width(a->dtype));
+  if (a->norm != 0 && a->norm != 1) return fail(CSA_ERR_INVALID_ARG, "norm must be 0 or 1");
+  if (!(a->eps >= 0.f)) return fail(CSA_ERR_INVALID_ARG, "eps must be >= 0");
+  if (!a->norm && a->weight) return fail(CSA_ERR_INVALID_ARG, "weight given with norm = 0");
+  if (!a->residual != !a->residual_out)
+    return fail(CSA_ERR_INVALID_ARG, "residual and residual_out go together");
+  if (!a->codes != !a->scale) return fail(CSA_ERR_INVALID_ARG, "codes and scale go together");
+  if (!a->out && !a->codes) return fail(CSA_ERR_INVALID_ARG, "neither out nor codes given");
+  if (a->n == 0) { g_err.clear(); return CSA_OK; }
+  const int es = a->dtype == CSA_DTYPE_BF16 ? 2 : 4;
+  int rc = check_rows("x", a->x, a->x_stride, a->width, es);
+  if (!rc && a->residual) rc = check_rows("residual", a->residual, a->residual_stride, a->width, es);
+  if (!rc && a->residual)
+    rc = check_rows("residual_out", a->residual_out, a->residual_out_stride, a->width, es);
+  if (!rc && a->weight && !aligned16(a->weight))
+    rc = fail(CSA_ERR_INVALID_ARG, "weight is not 16-byte aligned");
+  if (!rc && a->out) rc = check_rows("out", a->out, a->out_stride, a->width, es);
+  if (!rc && a->codes) rc = check_rows("codes", a->codes, a->codes_stride, a->width, 1);
+  if (rc) return rc;
+  if (a->scale) {
+    if ((reinterpret_cast<uintptr_t>(a->scale) & 3u) != 0)
+      return fail(CSA_ERR_INVALID_ARG, "scale is not 4-byte aligned");
+    if (a->scale_stride < (a->width + 127) / 128)
+      return fail(CSA_ERR_INVALID_ARG, "scale_stride below the row's scales");
+  }
+  int sms = 0;
+  rc = device_sms(&sms);
+  if (rc) return rc;
+  csa::NormArgs k;
+  k.n = a->n; k.width = a->width; k.norm = a->norm; k.eps = a->eps;
+  k.x = a->x; k.x_stride = a->x_stride;
+  k.residual = a->residual; k.residual_stride = a->residual_stride;
+  k.residual_out = a->residual_out; k.residual_out_stride = a->residual_out_stride;
+  k.weight = a->weight;
+  k.out = a->out; k.out_stride = a->out_stride;
+  k.codes = a->codes; k.codes_stride = a->codes_stride;
+  k.scale = a->scale; k.scale_stride = a->scale_stride;
+  return finish_free(csa::launch_norm(k, a->dtype, sms, static_cast<cudaStream_t>(stream), use_pdl()));
 }
 
 int csa_debug_set_wait_polls(csa_handle* h, int32_t polls) {

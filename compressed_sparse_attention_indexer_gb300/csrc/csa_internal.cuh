@@ -371,6 +371,21 @@ int launch_indexer_tc5(const DevCfg& c, const DevBatch& b, const Workspace& ws,
 int launch_writeback(const void* src, int64_t src_stride, const int64_t* slot, int n, void* pool,
                      int64_t pool_stride, int64_t pool_rows, int64_t row_bytes, int* status,
                      cudaStream_t st, bool pdl);
+// Residual addition, RMS norm and quantisation of rows (csa_norm_rows): the
+// arguments of csa_norm with checked pointers; strides in elements.
+struct NormArgs {
+  int n, width, norm;
+  float eps;
+  const void* x; int64_t x_stride;
+  const void* residual; int64_t residual_stride;
+  void* residual_out; int64_t residual_out_stride;
+  const void* weight;
+  void* out; int64_t out_stride;
+  uint8_t* codes; int64_t codes_stride;
+  float* scale; int64_t scale_stride;
+};
+int norm_max_width(int dtype);
+int launch_norm(const NormArgs& a, int dtype, int num_sms, cudaStream_t st, bool pdl);
 // early: this library's own kernel of the same call runs right before (the
 // lengths are then read before the grid dependency wait)
 // ready / epoch: when ready is not NULL, each query's block stores `epoch`

@@ -261,6 +261,52 @@ CSA_API int csa_cache_writeback(const void *rows, int64_t rows_stride, const int
                                 int32_t n, void *pool, int64_t pool_stride, int64_t pool_rows,
                                 int64_t row_bytes, int32_t *status, void *stream);
 
+/* ---- operators around the step: what makes its inputs, and dense attention ----
+ *
+ * Handle-free calls like csa_cache_writeback: they launch on `stream`, do not
+ * synchronise and allocate nothing.  Every pointer is device memory of the
+ * device that is current at the call; strides are in ELEMENTS unless said
+ * otherwise; the struct is read during the call only. */
+
+/* Rows before an 8-bit product or an 8-bit cache: residual addition, RMS norm
+ * and the output in the layer's type and / or as E4M3 codes with one fp32
+ * scale per 128 elements.  Row t < n, elements i < width:
+ *   s = x + residual                        (residual NULL: s = x)
+ *   residual_out = s, rounded to dtype
+ *   y = s * (sum_i s^2 / width + eps)^(-1/2) * weight    (norm = 0: y = s)
+ *   out = y, rounded to dtype (y comes from the unrounded s)
+ *   scale[t][j] = max(max|y| / 448, 2^-126) over elements 128 j .. 128 j + 127
+ *                 (the last block may be shorter), 1 where they are all zero
+ *   codes = y / scale[t][j] to the nearest E4M3 value (ties to even)
+ * With width 128 codes and scale are the FP8 indexer-key pool's row and row
+ * scale (csa_config.idx_dtype).  s and its squares are summed in fp32 and must
+ * stay in its range.  A NaN element does not count in max|y| and becomes the
+ * NaN code; an infinite one makes its block's scale infinite, its code NaN and
+ * the block's finite codes zero. */
+typedef struct {
+    int32_t n, width;         /* rows (0: a no-op), elements per row               */
+    int32_t dtype;            /* CSA_DTYPE_BF16 or CSA_DTYPE_F32: x, residual, weight, out */
+    int32_t norm;             /* 1: RMS norm; 0: rows as they are (weight must be NULL) */
+    float eps;                /* >= 0                                              */
+    const void *x; int64_t x_stride;                   /* [n, width]               */
+    const void *residual; int64_t residual_stride;     /* [n, width] or NULL       */
+    void *residual_out; int64_t residual_out_stride;   /* given exactly when residual is; may be
+                                                          residual itself (in place) */
+    const void *weight;       /* [width], NULL = ones                              */
+    void *out; int64_t out_stride;                     /* [n, width] or NULL; may be x itself */
+    uint8_t *codes; int64_t codes_stride;              /* [n, width] E4M3 bytes or NULL */
+    float *scale; int64_t scale_stride;                /* [n, ceil(width / 128)], given exactly
+                                                          when codes is              */
+} csa_norm;
+
+/* One of out and codes at least.  Rows of x, residual, residual_out, weight,
+ * out and codes start on 16-byte boundaries (pointer and stride * element size
+ * multiples of 16); widths are any from 1 to 32768 (bf16) or 16384 (fp32), and
+ * nothing past `width` is read or written.  An output may be the input named
+ * above with the same pointer and stride; any other overlap is undefined.
+ * Returns CSA_ERR_INVALID_ARG or CSA_ERR_UNSUPPORTED (dtype, width). */
+CSA_API int csa_norm_rows(const csa_norm *a, void *stream);
+
 /* Host-side checks of a batch against a config, exactly those every entry
  * point runs before launching (null / misaligned pointers, strides, sizes
  * against the maxima, ctx_len_host values).  Touches no device memory and
