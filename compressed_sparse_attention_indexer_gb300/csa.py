@@ -23,7 +23,7 @@ EXPORTS = ("csa_decode_create", "csa_decode_destroy", "csa_indexer_topk", "csa_s
            "csa_decode_step", "csa_indexer_scores", "csa_topk_select", "csa_check_batch",
            "csa_get_status", "csa_last_error", "csa_last_launch_count", "csa_abi_version",
            "csa_profile_enable", "csa_profile_read", "csa_indexer_topk_static", "csa_cache_writeback",
-           "csa_debug_set_wait_polls", "csa_norm_rows")
+           "csa_debug_set_wait_polls", "csa_norm_rows", "csa_fp8_matmul")
 STAGES = ("plan", "indexer", "topk", "attention")
 
 
@@ -65,6 +65,13 @@ class CNorm(ctypes.Structure):
         ("eps", ctypes.c_float), ("x", _P), ("x_stride", _I64), ("residual", _P), ("residual_stride", _I64),
         ("residual_out", _P), ("residual_out_stride", _I64), ("weight", _P), ("out", _P), ("out_stride", _I64),
         ("codes", _P), ("codes_stride", _I64), ("scale", _P), ("scale_stride", _I64)]
+
+
+class CFp8Mm(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in ("M", "N", "K", "out_dtype")] + [
+        ("a", _P), ("a_stride", _I64), ("a_scale", _P), ("a_scale_stride", _I64),
+        ("b", _P), ("b_stride", _I64), ("b_scale", _P), ("b_scale_stride", _I64),
+        ("out", _P), ("out_stride", _I64), ("status", _P)]
 
 
 _lib = None
@@ -109,10 +116,12 @@ def lib(path: str | None = None):
             L.csa_cache_writeback.argtypes = [vp, ctypes.c_int64, vp, i32, vp, ctypes.c_int64,
                                               ctypes.c_int64, ctypes.c_int64, vp, vp]
             L.csa_norm_rows.argtypes = [ctypes.POINTER(CNorm), vp]
+            L.csa_fp8_matmul.argtypes = [ctypes.POINTER(CFp8Mm), vp]
             for name in ("csa_decode_create", "csa_indexer_topk", "csa_sparse_attn", "csa_decode_step",
                          "csa_indexer_scores", "csa_topk_select", "csa_check_batch", "csa_get_status",
                          "csa_profile_enable", "csa_profile_read", "csa_indexer_topk_static",
-                         "csa_cache_writeback", "csa_debug_set_wait_polls", "csa_norm_rows"):
+                         "csa_cache_writeback", "csa_debug_set_wait_polls", "csa_norm_rows",
+                         "csa_fp8_matmul"):
                 getattr(L, name).restype = ctypes.c_int
             _lib = L
     return _lib
@@ -392,5 +401,49 @@ class NormRows(_Operator):
             self._out["codes"], self._out["scale"] = codes.view(torch.float8_e4m3fn), scale
 
     def __call__(self, stream=None) -> dict:
+        self._launch(stream)
+        return self._out
+
+
+_E4M3_DTYPES = ("torch.uint8", "torch.float8_e4m3fn")
+
+
+def _status_word(status):
+    if status is not None and (str(status.dtype) != "torch.int32" or status.numel() != 1):
+        _bad("status must be one int32")
+
+
+class Fp8Matmul(_Operator):
+    """csa_fp8_matmul: out [M, N] = a [M, K] times b [N, K] transposed, both E4M3 codes (uint8 or
+    float8_e4m3fn) with fp32 scales a_scale [M, ceil(K / 128)] and b_scale [ceil(N / 128), ceil(K / 128)].
+
+    out: the tensor to fill (bf16 or fp32), by default a buffer of the object in out_dtype.  status: an
+    int32 on the device that records a wait that gave up.  Calling the object returns out."""
+
+    def __init__(self, a, a_scale, b, b_scale, out=None, out_dtype=None, status=None):
+        import torch
+        for name, t in (("a", a), ("b", b)):
+            if t.dim() != 2 or str(t.dtype) not in _E4M3_DTYPES:
+                _bad(f"{name} must be a matrix of uint8 or float8_e4m3fn")
+        (m, k), n = (int(v) for v in a.shape), int(b.shape[0])
+        kb = -(-k // 128)
+        _rows2d("a", a, m, k)
+        _rows2d("b", b, n, k)
+        _rows2d("a_scale", a_scale, m, kb, torch.float32)
+        _rows2d("b_scale", b_scale, -(-n // 128), kb, torch.float32)
+        if out is None:
+            out = torch.empty(m, n, dtype=out_dtype or torch.bfloat16, device=a.device)
+        elif out_dtype is not None and out.dtype != out_dtype:
+            _bad(f"out is {out.dtype}, not {out_dtype}")
+        _rows2d("out", out, m, n)
+        _status_word(status)
+        st = CFp8Mm(M=m, N=n, K=k, out_dtype=_dtype_code(out), status=_ptr(status))
+        for name, t, u in (("a", a, 16), ("a_scale", a_scale, 1), ("b", b, 16), ("b_scale", b_scale, 1), ("out", out, 1)):
+            setattr(st, name, _ptr(t))
+            setattr(st, name + "_stride", _row_stride(t, u))
+        self._bind(lib().csa_fp8_matmul, st, (a, a_scale, b, b_scale, out, status))
+        self._out = out
+
+    def __call__(self, stream=None):
         self._launch(stream)
         return self._out

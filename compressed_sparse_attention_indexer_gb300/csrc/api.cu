@@ -832,6 +832,41 @@ int csa_norm_rows(const csa_norm* a, void* stream) {
   return finish_free(csa::launch_norm(k, a->dtype, sms, static_cast<cudaStream_t>(stream), use_pdl()));
 }
 
+int csa_fp8_matmul(const csa_fp8_mm* a, void* stream) {
+  if (!a) return fail(CSA_ERR_INVALID_ARG, "args is NULL");
+  if (a->out_dtype != CSA_DTYPE_BF16 && a->out_dtype != CSA_DTYPE_F32)
+    return fail(CSA_ERR_UNSUPPORTED, "out_dtype must be CSA_DTYPE_F32 or CSA_DTYPE_BF16");
+  if (a->M < 0 || a->N < 0 || a->K < 1) return fail(CSA_ERR_INVALID_ARG, "need M >= 0, N >= 0 and K >= 1");
+  if (a->M == 0 || a->N == 0) { g_err.clear(); return CSA_OK; }
+  int rc = check_rows("a", a->a, a->a_stride, a->K, 1);
+  if (!rc) rc = check_rows("b", a->b, a->b_stride, a->K, 1);
+  if (rc) return rc;
+  const int es = a->out_dtype == CSA_DTYPE_BF16 ? 2 : 4;
+  const int64_t kb = ((int64_t)a->K + 127) / 128;
+  struct P { const void* p; int align; const char* n; } ptrs[] = {
+      {a->a_scale, 4, "a_scale"}, {a->b_scale, 4, "b_scale"}, {a->out, es, "out"}};
+  for (const P& x : ptrs) {
+    if (!x.p) return fail(CSA_ERR_INVALID_ARG, "%s is NULL", x.n);
+    if (reinterpret_cast<uintptr_t>(x.p) % x.align != 0)
+      return fail(CSA_ERR_INVALID_ARG, "%s is not %d-byte aligned", x.n, x.align);
+  }
+  if ((reinterpret_cast<uintptr_t>(a->status) & 3u) != 0)
+    return fail(CSA_ERR_INVALID_ARG, "status is not 4-byte aligned");
+  if (a->a_scale_stride < kb || a->b_scale_stride < kb)
+    return fail(CSA_ERR_INVALID_ARG, "a scale stride below the row's scales");
+  if (a->out_stride < a->N) return fail(CSA_ERR_INVALID_ARG, "out_stride below the row width");
+  int sms = 0;
+  rc = device_sms(&sms);
+  if (rc) return rc;
+  csa::MmArgs k;
+  k.M = a->M; k.N = a->N; k.K = a->K;
+  k.a = a->a; k.a_stride = a->a_stride; k.a_scale = a->a_scale; k.a_scale_stride = a->a_scale_stride;
+  k.b = a->b; k.b_stride = a->b_stride; k.b_scale = a->b_scale; k.b_scale_stride = a->b_scale_stride;
+  k.out = a->out; k.out_stride = a->out_stride; k.status = a->status;
+  k.vec = aligned16(a->out) && (a->out_stride * es) % 16 == 0;
+  return finish_free(csa::launch_fp8_matmul(k, a->out_dtype, sms, static_cast<cudaStream_t>(stream), use_pdl()));
+}
+
 int csa_debug_set_wait_polls(csa_handle* h, int32_t polls) {
   if (!h) return fail(CSA_ERR_INVALID_ARG, "handle is NULL");
   h->dc.wait_polls = polls < 0 ? -1 : polls;

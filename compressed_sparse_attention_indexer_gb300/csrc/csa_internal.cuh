@@ -384,6 +384,20 @@ struct NormArgs {
   uint8_t* codes; int64_t codes_stride;
   float* scale; int64_t scale_stride;
 };
+// Product of E4M3 codes with block scales (csa_fp8_matmul): the arguments of
+// csa_fp8_mm with checked pointers.  vec: rows of out start on 16-byte
+// boundaries.
+struct MmArgs {
+  int M, N, K;
+  const uint8_t* a; int64_t a_stride;
+  const float* a_scale; int64_t a_scale_stride;
+  const uint8_t* b; int64_t b_stride;
+  const float* b_scale; int64_t b_scale_stride;
+  void* out; int64_t out_stride;
+  int* status;
+  bool vec;
+};
+int launch_fp8_matmul(const MmArgs& g, int out_dtype, int num_sms, cudaStream_t st, bool pdl);
 int norm_max_width(int dtype);
 int launch_norm(const NormArgs& a, int dtype, int num_sms, cudaStream_t st, bool pdl);
 // early: this library's own kernel of the same call runs right before (the

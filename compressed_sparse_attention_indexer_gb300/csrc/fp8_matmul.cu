@@ -1,0 +1,378 @@
+// Matrix product of E4M3 codes with a scale for each block of 128:
+//   out[m][n] = sum_kb sa[m][kb] * sb[n / 128][kb] * sum_{k in block kb} a[m][k] * b[n][k]
+//
+// The inner sums run on the tensor cores (tcgen05 kind::f8f6f4, fp32
+// accumulators in TMEM): one 128-byte row of the 128-byte swizzle is one
+// block of 128 codes, so a pipeline stage is one block and its product lands
+// in a TMEM buffer of its own.  The scales are full fp32 numbers, so the
+// outer sum cannot stay in the accumulator: the epilogue warps read every
+// block's product back from TMEM and add it, times its scale, to fp32
+// registers, while the MMAs of the next block fill another buffer.
+//
+//   warp 0      producer: per block one TMA box of each operand into a ring
+//   warp 1      TMEM allocation; one thread issues four K = 32 MMAs per block
+//   warps 4..   epilogue: thread = TMEM lane (row of P), its columns of Q
+//
+// The operand in the TMEM lanes (P, 128 rows per tile) and the one in its
+// columns (Q, NT rows per tile) are a and b, or with `kSwap` b and a: for a
+// few rows of a (M <= 64) the weights then fill the 128 lanes and only as
+// many columns as there are rows are computed, and the product is bound by
+// streaming the weights.
+// Cluster of `split` CTAs: each takes a part of the blocks of one tile, and
+// the partial sums are added through distributed shared memory in rank order,
+// so that few tiles still keep every SM loading; no workspace, no atomics.
+// Every mbarrier wait is bounded; one that gives up sets bit 1 of the status.
+#include <cudaTypedefs.h>
+
+#include "csa_internal.cuh"
+#include "tc5.cuh"
+
+namespace csa {
+
+namespace {
+
+constexpr int kMmBlock = 128;                 // codes per scale, bytes per stage row
+constexpr int kMmPBytes = 128 * kMmBlock;     // P tile: 128 rows
+constexpr int kMmMaxStages = 12;
+
+template <int NT, bool kSwap>
+struct MmShape {
+  static constexpr int kEpiWarps = kSwap ? 4 : 8;
+  static constexpr int kThreads = 128 + 32 * kEpiWarps;
+  static constexpr int kCols = NT / (kEpiWarps / 4);       // columns per epilogue thread
+  static constexpr int kAccCols = NT < 32 ? 32 : NT;       // TMEM columns per buffer
+  static constexpr int kBufs = kSwap ? 4 : 2;
+  static constexpr int kTmemCols = kAccCols * kBufs;
+  static constexpr int kStageBytes = kMmPBytes + NT * kMmBlock;
+  static constexpr int kCtasPerSm = kSwap ? 2 : 1;
+  static constexpr int kStages = (kSwap ? 108 * 1024 : 200 * 1024) / kStageBytes;
+  static constexpr int kSmem = kStages * kStageBytes + 1024;
+  // fp32 partials for the cluster's reduction, in the ring's memory
+  static_assert(128 * NT * 4 <= kStages * kStageBytes, "partials exceed the ring");
+  static_assert(kStages <= kMmMaxStages && kTmemCols <= 512 / kCtasPerSm, "ring or TMEM");
+};
+
+struct MmSmem {
+  uint64_t full[kMmMaxStages], empty[kMmMaxStages], tfull[4], tempty[4];
+  uint32_t tmem_base;
+  int abort;
+};
+
+__device__ __forceinline__ uint32_t cluster_rank() {
+  uint32_t r;
+  asm volatile("mov.u32 %0, %%cluster_ctarank;\n" : "=r"(r));
+  return r;
+}
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release.aligned;\nbarrier.cluster.wait.acquire.aligned;\n" ::: "memory");
+}
+__device__ __forceinline__ float ld_cluster_f32(uint32_t saddr, uint32_t rank) {
+  float v;
+  asm volatile(
+      "{\n .reg .b32 a;\n mapa.shared::cluster.u32 a, %1, %2;\n ld.shared::cluster.f32 %0, [a];\n}\n"
+      : "=f"(v)
+      : "r"(saddr), "r"(rank)
+      : "memory");
+  return v;
+}
+// d += a * b on two packed fp32 values.
+__device__ __forceinline__ void fma2(uint64_t& d, uint64_t a, uint64_t b) {
+  asm("fma.rn.f32x2 %0, %1, %2, %0;\n" : "+l"(d) : "l"(a), "l"(b));
+}
+__device__ __forceinline__ uint64_t pack2(float lo, float hi) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};\n" : "=l"(r) : "f"(lo), "f"(hi));
+  return r;
+}
+__device__ __forceinline__ void unpack2(uint64_t v, float& lo, float& hi) {
+  asm("mov.b64 {%0, %1}, %2;\n" : "=f"(lo), "=f"(hi) : "l"(v));
+}
+
+template <typename T>
+__device__ __forceinline__ T to_out(float v);
+template <>
+__device__ __forceinline__ float to_out<float>(float v) { return v; }
+template <>
+__device__ __forceinline__ __nv_bfloat16 to_out<__nv_bfloat16>(float v) { return __float2bfloat16_rn(v); }
+
+// One column strip of a row: cnt consecutive elements of out.
+template <typename T, int CNT>
+__device__ __forceinline__ void store_strip(T* dst, const float* v, int64_t left, bool vec) {
+  constexpr int E = 16 / (int)sizeof(T);
+  if (vec && left >= CNT) {
+#pragma unroll
+    for (int i = 0; i < CNT / E; ++i) {
+      T t[E];
+#pragma unroll
+      for (int e = 0; e < E; ++e) t[e] = to_out<T>(v[i * E + e]);
+      uint4 r;
+      memcpy(&r, t, 16);
+      reinterpret_cast<uint4*>(dst)[i] = r;
+    }
+    return;
+  }
+#pragma unroll
+  for (int i = 0; i < CNT; ++i)
+    if (i < left) dst[i] = to_out<T>(v[i]);
+}
+
+template <int NT, bool kSwap, typename T>
+__global__ void __launch_bounds__(MmShape<NT, kSwap>::kThreads, MmShape<NT, kSwap>::kCtasPerSm)
+    mm_kernel(const __grid_constant__ CUtensorMap pmap, const __grid_constant__ CUtensorMap qmap,
+              const MmArgs g, int split, int ptiles, int qtiles) {
+  using Sh = MmShape<NT, kSwap>;
+  extern __shared__ __align__(16) uint8_t smem_raw[];
+  __shared__ MmSmem sm;
+  const uint32_t base = (smem_u32(smem_raw) + 1023u) & ~1023u;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int KB = (g.K + kMmBlock - 1) / kMmBlock;
+  const int rank = split > 1 ? (int)cluster_rank() : 0;
+  const int kb0 = (int)((int64_t)rank * KB / split), kb1 = (int)((int64_t)(rank + 1) * KB / split);
+  const int tiles = ptiles * qtiles;
+  const int first = blockIdx.x / split, step = gridDim.x / split;  // split > 1: one tile per cluster
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < Sh::kStages; ++i) {
+      tc5::mbar_init(smem_u32(&sm.full[i]), 1);
+      tc5::mbar_init(smem_u32(&sm.empty[i]), 1);
+    }
+    for (int i = 0; i < Sh::kBufs; ++i) {
+      tc5::mbar_init(smem_u32(&sm.tfull[i]), 1);
+      tc5::mbar_init(smem_u32(&sm.tempty[i]), Sh::kEpiWarps);
+    }
+    sm.abort = 0;
+    tc5::fence_mbar_init();
+    tc5::prefetch_tmap(&pmap);
+    tc5::prefetch_tmap(&qmap);
+  }
+  // Before the allocation: a kernel in front that triggers its dependents
+  // before it has its own TMEM must not find it taken by a CTA that waits for
+  // that kernel's end.
+  pdl_wait();
+  if (warp == 1) {
+    tc5::tmem_alloc(smem_u32(&sm.tmem_base), Sh::kTmemCols);
+    tc5::tmem_relinquish();
+  }
+  tc5::fence_before_sync();
+  __syncthreads();
+  tc5::fence_after_sync();
+  const uint32_t tmem = sm.tmem_base;
+  volatile int* abort = &sm.abort;
+  pdl_trigger();
+
+  // tile t: its P and Q tile
+  auto p_of = [&](int t) { return t % ptiles; };
+  auto q_of = [&](int t) { return t / ptiles; };
+
+  if (warp == 0) {
+    if (lane == 0) {
+      int st = 0, n = 0;
+      uint32_t ph = 0;
+      for (int t = first; t < tiles && !*abort; t += step)
+        for (int kb = kb0; kb < kb1; ++kb, ++n) {
+          if (n >= Sh::kStages && !tc5::mbar_wait(smem_u32(&sm.empty[st]), ph ^ 1u, abort)) goto loaded;
+          const uint32_t bar = smem_u32(&sm.full[st]), dst = base + st * Sh::kStageBytes;
+          tc5::mbar_expect_tx(bar, Sh::kStageBytes);
+          tc5::tma_load_2d(dst, &pmap, kb * kMmBlock, p_of(t) * 128, bar);
+          tc5::tma_load_2d(dst + kMmPBytes, &qmap, kb * kMmBlock, q_of(t) * NT, bar);
+          if (++st == Sh::kStages) st = 0, ph ^= 1u;
+        }
+    loaded:
+      // copies still in flight land before the block exits
+      for (int k = n > Sh::kStages ? n - Sh::kStages : 0; k < n; ++k)
+        tc5::mbar_wait_drain(smem_u32(&sm.full[k % Sh::kStages]), (k / Sh::kStages) & 1);
+    }
+  } else if (warp == 1) {
+    if (lane == 0) {
+      int st = 0, buf = 0, n = 0;
+      uint32_t ph = 0, bph = 0;
+      const uint32_t idesc = tc5::idesc_e4m3_f32(128, NT);
+      for (int t = first; t < tiles && !*abort; t += step)
+        for (int kb = kb0; kb < kb1; ++kb, ++n) {
+          if (n >= Sh::kBufs && !tc5::mbar_wait(smem_u32(&sm.tempty[buf]), bph ^ 1u, abort)) goto issued;
+          if (!tc5::mbar_wait(smem_u32(&sm.full[st]), ph, abort)) goto issued;
+          tc5::fence_after_sync();
+          const uint64_t pd = tc5::sdesc_k_sw128(base + st * Sh::kStageBytes);
+          const uint64_t qd = tc5::sdesc_k_sw128(base + st * Sh::kStageBytes + kMmPBytes);
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            tc5::mma_e4m3(tmem + buf * Sh::kAccCols, pd + 2 * i, qd + 2 * i, idesc, i > 0);
+          tc5::mma_commit(smem_u32(&sm.empty[st]));
+          tc5::mma_commit(smem_u32(&sm.tfull[buf]));
+          if (++st == Sh::kStages) st = 0, ph ^= 1u;
+          if (++buf == Sh::kBufs) buf = 0, bph ^= 1u;
+        }
+    issued:
+      // MMAs still in flight finish before TMEM is freed
+      for (int k = n > Sh::kBufs ? n - Sh::kBufs : 0; k < n; ++k)
+        tc5::mbar_wait_drain(smem_u32(&sm.tfull[k % Sh::kBufs]), (k / Sh::kBufs) & 1);
+    }
+  } else if (warp >= 4) {
+    const int ew = warp - 4, quarter = ew & 3, group = ew >> 2;
+    const int row = quarter * 32 + lane;                 // TMEM lane: row of the P tile
+    const uint32_t tcol = tmem + ((uint32_t)(quarter * 32) << 16) + group * Sh::kCols;
+    int buf = 0;
+    uint32_t bph = 0;
+    for (int t = first; t < tiles && !*abort; t += step) {
+      const int64_t p0 = (int64_t)p_of(t) * 128, q0 = (int64_t)q_of(t) * NT + group * Sh::kCols;
+      uint64_t acc[Sh::kCols / 2];
+#pragma unroll
+      for (int i = 0; i < Sh::kCols / 2; ++i) acc[i] = 0;
+      bool ok = true;
+      for (int kb = kb0; kb < kb1; ++kb) {
+        // scales of the block: !kSwap one factor per thread, kSwap one per column
+        float f = 0.f;
+        if (!kSwap) {
+          if (p0 + row < g.M && q0 < g.N)
+            f = __ldg(g.a_scale + (p0 + row) * g.a_scale_stride + kb) *
+                __ldg(g.b_scale + (q0 / 128) * g.b_scale_stride + kb);
+        } else {
+          f = __ldg(g.b_scale + (p0 / 128) * g.b_scale_stride + kb);
+        }
+        if (!tc5::mbar_wait(smem_u32(&sm.tfull[buf]), bph, abort)) { ok = false; break; }
+        tc5::fence_after_sync();
+#pragma unroll
+        for (int c = 0; c < Sh::kCols; c += 32) {
+          float v[32];
+          tc5::tmem_ld32(tcol + buf * Sh::kAccCols + c, v);
+#pragma unroll
+          for (int i = 0; i < 32 && c + i < Sh::kCols; i += 2) {
+            uint64_t s;
+            if (kSwap) {
+              const float s0 = q0 + c + i < g.M ? __ldg(g.a_scale + (q0 + c + i) * g.a_scale_stride + kb) : 0.f;
+              const float s1 = q0 + c + i + 1 < g.M ? __ldg(g.a_scale + (q0 + c + i + 1) * g.a_scale_stride + kb) : 0.f;
+              s = pack2(s0 * f, s1 * f);
+            } else {
+              s = pack2(f, f);
+            }
+            fma2(acc[(c + i) / 2], pack2(v[i], v[i + 1]), s);
+          }
+        }
+        tc5::fence_before_sync();
+        __syncwarp();
+        if (lane == 0) tc5::mbar_arrive(smem_u32(&sm.tempty[buf]));
+        if (++buf == Sh::kBufs) buf = 0, bph ^= 1u;
+      }
+      if (!ok) break;
+      float v[Sh::kCols];
+#pragma unroll
+      for (int i = 0; i < Sh::kCols / 2; ++i) unpack2(acc[i], v[2 * i], v[2 * i + 1]);
+      if (split > 1) {
+        // [column][lane] partials in the ring, which every copy and MMA of this
+        // CTA's only tile has left
+        const uint32_t part = base + (uint32_t)((group * Sh::kCols * 128 + row) * 4);
+#pragma unroll
+        for (int i = 0; i < Sh::kCols; ++i)
+          asm volatile("st.shared.f32 [%0], %1;\n" ::"r"(part + i * 512), "f"(v[i]) : "memory");
+      } else if (kSwap) {
+        if (p0 + row < g.N) {
+#pragma unroll
+          for (int i = 0; i < Sh::kCols; ++i)
+            if (q0 + i < g.M) static_cast<T*>(g.out)[(q0 + i) * g.out_stride + p0 + row] = to_out<T>(v[i]);
+        }
+      } else if (p0 + row < g.M) {
+        T* dst = static_cast<T*>(g.out) + (p0 + row) * g.out_stride + q0;
+#pragma unroll
+        for (int c = 0; c < Sh::kCols; c += 32)
+          if (q0 + c < g.N) store_strip<T, 32>(dst + c, v + c, g.N - q0 - c, g.vec);
+      }
+    }
+  }
+  if (split > 1) {
+    __syncwarp();
+    cluster_sync();
+    const int t = first;
+    if (warp >= 4 && t < tiles) {
+      // columns c0 .. c1 of the tile, summed over the ranks in order
+      const int c0 = rank * NT / split, c1 = (rank + 1) * NT / split;
+      const int ew = warp - 4, quarter = ew & 3, group = ew >> 2;
+      const int64_t p = (int64_t)p_of(t) * 128 + quarter * 32 + lane, q0 = (int64_t)q_of(t) * NT;
+      const uint32_t part = base + (uint32_t)((quarter * 32 + lane) * 4);
+      for (int c = c0 + group; c < c1; c += Sh::kEpiWarps / 4) {
+        float v = 0.f;
+        for (int r = 0; r < split; ++r) v += ld_cluster_f32(part + c * 512, (uint32_t)r);
+        const int64_t m = kSwap ? q0 + c : p, n = kSwap ? p : q0 + c;
+        if (m < g.M && n < g.N) static_cast<T*>(g.out)[m * g.out_stride + n] = to_out<T>(v);
+      }
+    }
+    cluster_sync();  // no CTA leaves while another reads its partials
+  }
+  tc5::fence_before_sync();
+  __syncthreads();
+  tc5::fence_after_sync();
+  if (threadIdx.x == 0 && sm.abort && g.status) set_status(g.status, kStatusTimeout);
+  if (warp == 1) tc5::tmem_dealloc(tmem, Sh::kTmemCols);
+}
+
+bool make_mm_map(CUtensorMap* m, const void* ptr, uint64_t rows, uint64_t cols, uint64_t stride, uint32_t box_rows) {
+  auto fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(tensor_map_encoder());
+  if (!fn) return false;
+  cuuint64_t dims[2] = {cols, rows};
+  cuuint64_t strides[1] = {stride};
+  cuuint32_t box[2] = {(cuuint32_t)kMmBlock, box_rows};
+  cuuint32_t estr[2] = {1, 1};
+  return fn(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(ptr), dims, strides, box, estr,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <int NT, bool kSwap, typename T>
+int launch_shape(const MmArgs& g, int num_sms, cudaStream_t st, bool pdl) {
+  using Sh = MmShape<NT, kSwap>;
+  CUtensorMap pmap, qmap;
+  const bool ok = kSwap ? make_mm_map(&pmap, g.b, g.N, g.K, g.b_stride, 128) &&
+                              make_mm_map(&qmap, g.a, g.M, g.K, g.a_stride, NT)
+                        : make_mm_map(&pmap, g.a, g.M, g.K, g.a_stride, 128) &&
+                              make_mm_map(&qmap, g.b, g.N, g.K, g.b_stride, NT);
+  if (!ok) return launch_fail("cuTensorMapEncodeTiled(a, b)", cudaSuccess);
+  auto kern = mm_kernel<NT, kSwap, T>;
+  static PerDeviceOnce attr;
+  if (const cudaError_t e = attr.run([&] { return allow_max_dynamic_smem(kern); }))
+    return launch_fail("cudaFuncSetAttribute(mm_kernel)", e);
+  const int ptiles = (int)(((kSwap ? g.N : g.M) + 127) / 128), qtiles = (int)(((kSwap ? g.M : g.N) + NT - 1) / NT);
+  const int64_t tiles = (int64_t)ptiles * qtiles;
+  if (tiles > 0x7fffffff) return launch_fail("too many tiles", cudaSuccess);
+  const int slots = num_sms * Sh::kCtasPerSm;
+  const int KB = (g.K + kMmBlock - 1) / kMmBlock;
+  // a tile's blocks over the CTAs of a cluster while that still adds CTAs
+  int split = 1;
+  while (split < 8 && tiles * split * 2 <= slots && KB >= split * 2 * 2) split *= 2;
+  int grid = split > 1 ? (int)tiles * split : (int)(tiles < slots ? tiles : slots);
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(grid);
+  cfg.blockDim = dim3(Sh::kThreads);
+  cfg.dynamicSmemBytes = Sh::kSmem;
+  cfg.stream = st;
+  cudaLaunchAttribute at[2];
+  int na = 0;
+  if (pdl) {
+    at[na].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[na++].val.programmaticStreamSerializationAllowed = 1;
+  }
+  if (split > 1) {
+    at[na].id = cudaLaunchAttributeClusterDimension;
+    at[na].val.clusterDim.x = split;
+    at[na].val.clusterDim.y = 1;
+    at[na++].val.clusterDim.z = 1;
+  }
+  cfg.attrs = at;
+  cfg.numAttrs = na;
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, kern, pmap, qmap, g, split, ptiles, qtiles);
+  return e == cudaSuccess ? 1 : launch_fail("cudaLaunchKernelEx", e);
+}
+
+template <typename T>
+int launch_out(const MmArgs& g, int num_sms, cudaStream_t st, bool pdl) {
+  if (g.M <= 16) return launch_shape<16, true, T>(g, num_sms, st, pdl);
+  if (g.M <= 32) return launch_shape<32, true, T>(g, num_sms, st, pdl);
+  if (g.M <= 64) return launch_shape<64, true, T>(g, num_sms, st, pdl);
+  return launch_shape<128, false, T>(g, num_sms, st, pdl);
+}
+
+}  // namespace
+
+int launch_fp8_matmul(const MmArgs& g, int out_dtype, int num_sms, cudaStream_t st, bool pdl) {
+  return out_dtype == CSA_DTYPE_BF16 ? launch_out<__nv_bfloat16>(g, num_sms, st, pdl)
+                                     : launch_out<float>(g, num_sms, st, pdl);
+}
+
+}  // namespace csa

@@ -307,6 +307,32 @@ typedef struct {
  * Returns CSA_ERR_INVALID_ARG or CSA_ERR_UNSUPPORTED (dtype, width). */
 CSA_API int csa_norm_rows(const csa_norm *a, void *stream);
 
+/* Matrix product of E4M3 codes with a scale for each block of 128:
+ *   out[m][n] = sum_kb a_scale[m][kb] * b_scale[n / 128][kb]
+ *               * sum_{k in block kb} a[m][k] * b[n][k]
+ * a [M, K] (activations, as csa_norm_rows writes them: a scale per row and 128
+ * elements), b [N, K] (weights, one row per output element: a scale per 128
+ * rows and 128 elements), block kb = elements 128 kb .. 128 kb + 127, the last
+ * one may be shorter.  The sums are fp32, out is rounded once.  a_scale and
+ * b_scale may be any fp32 numbers. */
+typedef struct {
+    int32_t M, N, K;          /* M = 0 or N = 0: a no-op; K >= 1                    */
+    int32_t out_dtype;        /* CSA_DTYPE_BF16 or CSA_DTYPE_F32                    */
+    const uint8_t *a; int64_t a_stride;                /* [M, K]                    */
+    const float *a_scale; int64_t a_scale_stride;      /* [M, ceil(K / 128)]        */
+    const uint8_t *b; int64_t b_stride;                /* [N, K]                    */
+    const float *b_scale; int64_t b_scale_stride;      /* [ceil(N / 128), ceil(K / 128)] */
+    void *out; int64_t out_stride;                     /* [M, N]                    */
+    int32_t *status;          /* NULL or a device int32: bit 1 (value 2) is set when a
+                                 device wait gave up (out is then undefined)        */
+} csa_fp8_mm;
+
+/* Rows of a and b start on 16-byte boundaries (pointer and stride multiples of
+ * 16); out needs the alignment of its element only, and nothing past N is
+ * written; out must not overlap an input.  Returns CSA_ERR_INVALID_ARG or
+ * CSA_ERR_UNSUPPORTED (out_dtype). */
+CSA_API int csa_fp8_matmul(const csa_fp8_mm *a, void *stream);
+
 /* Host-side checks of a batch against a config, exactly those every entry
  * point runs before launching (null / misaligned pointers, strides, sizes
  * against the maxima, ctx_len_host values).  Touches no device memory and
