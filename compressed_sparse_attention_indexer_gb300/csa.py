@@ -23,7 +23,8 @@ EXPORTS = ("csa_decode_create", "csa_decode_destroy", "csa_indexer_topk", "csa_s
            "csa_decode_step", "csa_indexer_scores", "csa_topk_select", "csa_check_batch",
            "csa_get_status", "csa_last_error", "csa_last_launch_count", "csa_abi_version",
            "csa_profile_enable", "csa_profile_read", "csa_indexer_topk_static", "csa_cache_writeback",
-           "csa_debug_set_wait_polls", "csa_norm_rows", "csa_fp8_matmul")
+           "csa_debug_set_wait_polls", "csa_norm_rows", "csa_fp8_matmul",
+           "csa_paged_attn", "csa_paged_attn_workspace")
 STAGES = ("plan", "indexer", "topk", "attention")
 
 
@@ -74,6 +75,15 @@ class CFp8Mm(ctypes.Structure):
         ("out", _P), ("out_stride", _I64), ("status", _P)]
 
 
+class CPaged(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in
+                ("B", "S", "heads", "kv_heads", "dim", "kv_dtype", "win", "max_len")] + [
+        ("softmax_scale", ctypes.c_float), ("block", ctypes.c_int32), ("table_stride", ctypes.c_int32),
+        ("ctx_len", _P), ("q", _P), ("q_stride", _I64), ("k", _P), ("v", _P), ("k_stride", _I64), ("v_stride", _I64),
+        ("rows", _I64), ("k_scale", _P), ("v_scale", _P), ("scale_stride", _I64), ("off", _P), ("table", _P),
+        ("out", _P), ("out_stride", _I64), ("lse", _P), ("status", _P), ("workspace", _P), ("workspace_bytes", _I64)]
+
+
 _lib = None
 _lock = threading.Lock()
 
@@ -117,11 +127,14 @@ def lib(path: str | None = None):
                                               ctypes.c_int64, ctypes.c_int64, vp, vp]
             L.csa_norm_rows.argtypes = [ctypes.POINTER(CNorm), vp]
             L.csa_fp8_matmul.argtypes = [ctypes.POINTER(CFp8Mm), vp]
+            L.csa_paged_attn.argtypes = [ctypes.POINTER(CPaged), vp]
+            L.csa_paged_attn_workspace.argtypes = [i32]
+            L.csa_paged_attn_workspace.restype = ctypes.c_int64
             for name in ("csa_decode_create", "csa_indexer_topk", "csa_sparse_attn", "csa_decode_step",
                          "csa_indexer_scores", "csa_topk_select", "csa_check_batch", "csa_get_status",
                          "csa_profile_enable", "csa_profile_read", "csa_indexer_topk_static",
                          "csa_cache_writeback", "csa_debug_set_wait_polls", "csa_norm_rows",
-                         "csa_fp8_matmul"):
+                         "csa_fp8_matmul", "csa_paged_attn"):
                 getattr(L, name).restype = ctypes.c_int
             _lib = L
     return _lib
@@ -445,5 +458,102 @@ class Fp8Matmul(_Operator):
         self._out = out
 
     def __call__(self, stream=None):
+        self._launch(stream)
+        return self._out
+
+
+def paged_attn_workspace(dim: int) -> int:
+    """Bytes of workspace csa_paged_attn needs on the current device (dim: 64, 128 or 256)."""
+    return int(lib().csa_paged_attn_workspace(int(dim)))
+
+
+class PagedAttention(_Operator):
+    """csa_paged_attn: dense causal attention of each request's S newest tokens over its cache.
+
+    q [B, S, heads, dim] bf16; k, v [rows, kv_heads, dim] bf16, or E4M3 codes (uint8 or float8_e4m3fn) with
+    k_scale, v_scale fp32 [rows, kv_heads]; ctx_len [B] int32 including the S new tokens; the rows of a
+    request through table [B, blocks] int32 and block, or off [B] int64.  max_len bounds every length
+    (default with a table: what the table can hold).  win: sliding window (0: none).  scale <= 0:
+    1/sqrt(dim).  out (bf16, like q), lse (fp32 [B, S, heads]; False: not made), workspace (uint8, at
+    least paged_attn_workspace(dim) bytes) are buffers of the object by default.  Calling the object
+    returns {"out", "lse"}."""
+
+    def __init__(self, q, k, v, ctx_len, table=None, block: int = 0, off=None, k_scale=None, v_scale=None,
+                 win: int = 0, scale: float = 0.0, max_len: int | None = None, out=None, lse=True, status=None,
+                 workspace=None):
+        import torch
+        if q.dim() != 4 or k.dim() != 3:
+            _bad("q must be [B, S, heads, dim] and k, v [rows, kv_heads, dim]")
+        b, s, heads, dim = (int(x) for x in q.shape)
+        rows, kv_heads = int(k.shape[0]), int(k.shape[1])
+        if out is None:
+            out = torch.empty(b, s, heads, dim, dtype=q.dtype, device=q.device)
+        strides = []
+        for name, t in (("q", q), ("out", out)):
+            if tuple(t.shape) != (b, s, heads, dim) or t.dtype != torch.bfloat16:
+                _bad(f"{name} must be bfloat16 of shape ({b}, {s}, {heads}, {dim})")
+            if (dim > 1 and t.stride(3) != 1) or (heads > 1 and t.stride(2) != dim):
+                _bad(f"{name}: a token's heads must be contiguous")
+            step = t.stride(1) if s > 1 else t.stride(0) if b > 1 else heads * dim
+            if b > 1 and s > 1 and t.stride(0) != s * step:
+                _bad(f"{name}: the tokens must be evenly spaced")
+            strides.append(int(step))
+        fp8 = str(k.dtype) in _E4M3_DTYPES
+        for name, t in (("k", k), ("v", v)):
+            if tuple(t.shape) != (rows, kv_heads, dim) or (str(t.dtype) not in _E4M3_DTYPES if fp8
+                                                           else t.dtype != torch.bfloat16):
+                _bad(f"{name} must be bfloat16 or E4M3 codes, like k, of shape ({rows}, {kv_heads}, {dim})")
+            if (dim > 1 and t.stride(2) != 1) or (kv_heads > 1 and t.stride(1) != dim):
+                _bad(f"{name}: the heads of a row must be contiguous")
+        if fp8:
+            for name, t in (("k_scale", k_scale), ("v_scale", v_scale)):
+                if t is None:
+                    _bad(f"{name} is needed with E4M3 codes")
+                _rows2d(name, t, rows, kv_heads, torch.float32)
+            if rows > 1 and k_scale.stride(0) != v_scale.stride(0):
+                _bad("k_scale and v_scale must have the same row stride")
+        elif k_scale is not None or v_scale is not None:
+            _bad("scales given with a bfloat16 pool")
+        if tuple(ctx_len.shape) != (b,) or ctx_len.dtype != torch.int32 or not ctx_len.is_contiguous():
+            _bad(f"ctx_len must be contiguous int32 of shape ({b},)")
+        if (table is None) == (off is None):
+            _bad("give either table and block, or off")
+        if table is not None:
+            if table.dtype != torch.int32 or table.dim() != 2 or table.shape[0] != b or not table.is_contiguous():
+                _bad(f"table must be contiguous int32 of shape ({b}, blocks)")
+            if max_len is None:
+                max_len = int(table.shape[1]) * int(block)
+        else:
+            if off.dtype != torch.int64 or tuple(off.shape) != (b,) or not off.is_contiguous():
+                _bad(f"off must be contiguous int64 of shape ({b},)")
+            if max_len is None:
+                _bad("max_len is needed with off")
+        if lse is True:
+            lse = torch.empty(b, s, heads, dtype=torch.float32, device=q.device)
+        elif lse is False:
+            lse = None
+        if lse is not None and (tuple(lse.shape) != (b, s, heads) or lse.dtype != torch.float32 or
+                                not lse.is_contiguous()):
+            _bad(f"lse must be contiguous float32 of shape ({b}, {s}, {heads})")
+        _status_word(status)
+        if workspace is None and q.is_cuda:
+            with torch.cuda.device(q.device):
+                workspace = torch.empty(paged_attn_workspace(dim), dtype=torch.uint8, device=q.device)
+        st = CPaged(B=b, S=s, heads=heads, kv_heads=kv_heads, dim=dim,
+                    kv_dtype=CSA_DTYPE_FP8_E4M3 if fp8 else CSA_DTYPE_BF16, win=win, max_len=max_len,
+                    softmax_scale=scale, block=block, table_stride=0 if table is None else int(table.shape[1]),
+                    ctx_len=_ptr(ctx_len), q=_ptr(q), q_stride=strides[0], k=_ptr(k), v=_ptr(v),
+                    k_stride=int(k.stride(0)) if rows > 1 else kv_heads * dim,
+                    v_stride=int(v.stride(0)) if rows > 1 else kv_heads * dim, rows=rows,
+                    k_scale=_ptr(k_scale), v_scale=_ptr(v_scale),
+                    scale_stride=0 if not fp8 else int(k_scale.stride(0)) if rows > 1 else kv_heads,
+                    off=_ptr(off), table=_ptr(table), out=_ptr(out), out_stride=strides[1], lse=_ptr(lse),
+                    status=_ptr(status), workspace=_ptr(workspace),
+                    workspace_bytes=0 if workspace is None else workspace.numel() * workspace.element_size())
+        self._bind(lib().csa_paged_attn, st, (q, k, v, ctx_len, table, off, k_scale, v_scale, out, lse, status,
+                                              workspace))
+        self._out = {"out": out} if lse is None else {"out": out, "lse": lse}
+
+    def __call__(self, stream=None) -> dict:
         self._launch(stream)
         return self._out

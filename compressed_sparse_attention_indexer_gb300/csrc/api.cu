@@ -867,6 +867,66 @@ int csa_fp8_matmul(const csa_fp8_mm* a, void* stream) {
   return finish_free(csa::launch_fp8_matmul(k, a->out_dtype, sms, static_cast<cudaStream_t>(stream), use_pdl()));
 }
 
+int64_t csa_paged_attn_workspace(int32_t dim) {
+  int sms = 0;
+  if (device_sms(&sms) != CSA_OK) return 0;
+  return (int64_t)csa::paged_attn_workspace(dim, sms);
+}
+
+int csa_paged_attn(const csa_paged* a, void* stream) {
+  if (!a) return fail(CSA_ERR_INVALID_ARG, "args is NULL");
+  if (a->kv_dtype != 0 && a->kv_dtype != CSA_DTYPE_BF16 && a->kv_dtype != CSA_DTYPE_FP8_E4M3)
+    return fail(CSA_ERR_UNSUPPORTED, "kv_dtype must be CSA_DTYPE_BF16 or CSA_DTYPE_FP8_E4M3");
+  const bool fp8 = a->kv_dtype == CSA_DTYPE_FP8_E4M3;
+  if (a->dim != 128 && (fp8 || (a->dim != 64 && a->dim != 256)))
+    return fail(CSA_ERR_UNSUPPORTED, "dim must be 64, 128 or 256, and 128 with E4M3 pools");
+  if (a->B < 0 || a->S < 1) return fail(CSA_ERR_INVALID_ARG, "need B >= 0 and S >= 1");
+  if (a->heads < 1 || a->kv_heads < 1 || a->heads % a->kv_heads != 0)
+    return fail(CSA_ERR_INVALID_ARG, "heads must be a positive multiple of kv_heads");
+  if (a->win < 0 || a->max_len < 0) return fail(CSA_ERR_INVALID_ARG, "need win >= 0 and max_len >= 0");
+  if (a->max_len > (1 << 30) || a->S > (1 << 16) || (int64_t)a->S * a->heads > (1 << 20))
+    return fail(CSA_ERR_UNSUPPORTED, "max_len above 2^30, S above 2^16 or S * heads above 2^20");
+  if (a->B == 0) { g_err.clear(); return CSA_OK; }
+  int rc = check_rows("q", a->q, a->q_stride, (int64_t)a->heads * a->dim, 2);
+  if (!rc) rc = check_rows("out", a->out, a->out_stride, (int64_t)a->heads * a->dim, 2);
+  if (!rc) rc = check_rows("k", a->k, a->k_stride, (int64_t)a->kv_heads * a->dim, fp8 ? 1 : 2);
+  if (!rc) rc = check_rows("v", a->v, a->v_stride, (int64_t)a->kv_heads * a->dim, fp8 ? 1 : 2);
+  if (rc) return rc;
+  if (a->rows < 0 || a->rows > 0x7fffffff) return fail(CSA_ERR_INVALID_ARG, "rows outside [0, 2^31)");
+  if (!a->ctx_len) return fail(CSA_ERR_INVALID_ARG, "ctx_len is NULL");
+  if (fp8) {
+    if (!a->k_scale || !a->v_scale) return fail(CSA_ERR_INVALID_ARG, "E4M3 pools need k_scale and v_scale");
+    if (a->scale_stride < a->kv_heads) return fail(CSA_ERR_INVALID_ARG, "scale_stride below kv_heads");
+  }
+  if (!a->table && !a->off) return fail(CSA_ERR_INVALID_ARG, "neither table nor off given");
+  if (a->table && (a->block < 1 || a->table_stride < 1))
+    return fail(CSA_ERR_INVALID_ARG, "block and table_stride must be >= 1 with a table");
+  struct P { const void* p; int align; const char* n; } ptrs[] = {
+      {a->ctx_len, 4, "ctx_len"}, {a->k_scale, 4, "k_scale"}, {a->v_scale, 4, "v_scale"}, {a->off, 8, "off"},
+      {a->table, 4, "table"}, {a->lse, 4, "lse"}, {a->status, 4, "status"}, {a->workspace, 16, "workspace"}};
+  for (const P& x : ptrs)
+    if (reinterpret_cast<uintptr_t>(x.p) % x.align != 0)
+      return fail(CSA_ERR_INVALID_ARG, "%s is not %d-byte aligned", x.n, x.align);
+  int sms = 0;
+  rc = device_sms(&sms);
+  if (rc) return rc;
+  if (!a->workspace || a->workspace_bytes < (int64_t)csa::paged_attn_workspace(a->dim, sms))
+    return fail(CSA_ERR_WORKSPACE, "workspace of %lld bytes, need %lld", (long long)a->workspace_bytes,
+                (long long)csa::paged_attn_workspace(a->dim, sms));
+  csa::PagedArgs k;
+  k.B = a->B; k.S = a->S; k.heads = a->heads; k.kv_heads = a->kv_heads; k.dim = a->dim;
+  k.win = a->win; k.max_len = a->max_len;
+  k.scale = a->softmax_scale > 0.f ? a->softmax_scale : (float)(1.0 / sqrt((double)a->dim));
+  k.ctx_len = a->ctx_len;
+  k.q = a->q; k.q_stride = a->q_stride;
+  k.k = a->k; k.v = a->v; k.k_stride = a->k_stride; k.v_stride = a->v_stride; k.rows = a->rows;
+  k.k_scale = a->k_scale; k.v_scale = a->v_scale; k.scale_stride = a->scale_stride;
+  k.off = a->off; k.table = a->table; k.block = a->block; k.table_stride = a->table_stride;
+  k.out = a->out; k.out_stride = a->out_stride; k.lse = a->lse; k.status = a->status;
+  k.workspace = a->workspace;
+  return finish_free(csa::launch_paged_attn(k, fp8, sms, static_cast<cudaStream_t>(stream), use_pdl()));
+}
+
 int csa_debug_set_wait_polls(csa_handle* h, int32_t polls) {
   if (!h) return fail(CSA_ERR_INVALID_ARG, "handle is NULL");
   h->dc.wait_polls = polls < 0 ? -1 : polls;

@@ -398,6 +398,24 @@ struct MmArgs {
   bool vec;
 };
 int launch_fp8_matmul(const MmArgs& g, int out_dtype, int num_sms, cudaStream_t st, bool pdl);
+// Dense attention over paged K / V pools (csa_paged_attn): the arguments of
+// csa_paged with checked pointers; strides in elements of the pool.
+struct PagedArgs {
+  int B, S, heads, kv_heads, dim, win, max_len;
+  float scale;
+  const int* ctx_len;
+  const void* q; int64_t q_stride;
+  const void* k; const void* v; int64_t k_stride, v_stride, rows;
+  const float* k_scale; const float* v_scale; int64_t scale_stride;
+  const int64_t* off;
+  const int* table; int block, table_stride;
+  void* out; int64_t out_stride;
+  float* lse;
+  int* status;
+  void* workspace;
+};
+size_t paged_attn_workspace(int dim, int num_sms);
+int launch_paged_attn(const PagedArgs& a, bool fp8, int num_sms, cudaStream_t st, bool pdl);
 int norm_max_width(int dtype);
 int launch_norm(const NormArgs& a, int dtype, int num_sms, cudaStream_t st, bool pdl);
 // early: this library's own kernel of the same call runs right before (the

@@ -1,0 +1,728 @@
+// Dense causal attention of the S newest tokens of each request over its
+// whole cache: grouped heads, K and V rows in (paged) pools, bf16 or E4M3
+// with a scale per row and head, optional sliding window.
+//   pos = L - S + s;  rows max(0, pos - win + 1) .. pos (win = 0: 0 .. pos)
+//   out[s][h] = sum_r softmax_r(scale q[s][h] . k[r]) v[r],  lse = ln sum_r exp(.)
+//
+// HBM bound: a K / V row is read once and serves every query row of its group
+// (S * heads / kv_heads, folded into the M = 16 rows of the warp MMA), so the
+// arithmetic per byte stays far below the tensor rate and the kernel is a
+// stream of row copies.
+//
+// Split of the work.  A unit is (request, kv head, chunk of 16 MT query
+// rows); its cost is its number of 128-row tiles.  The units' tiles form one
+// list, cut evenly over the CTAs (one per SM), so that a ragged batch or a
+// single long request fills the device alike; the lengths are read on the
+// device, so a captured graph follows them.  Within a tile each warp owns 16
+// rows: it copies them itself (16-byte cp.async into its own ring, several
+// tiles ahead, across unit boundaries), and keeps its own running maximum,
+// sum and output in registers: no barrier per tile.  At the end of a unit (or
+// of the CTA's share) the warps' states are joined through shared memory; a
+// unit cut between CTAs leaves fp32 partials (m, l, O) in the workspace, which
+// a second kernel, launched ahead as a programmatic dependent, joins in CTA
+// order.
+//
+// Scores, maxima, sums and O are fp32.  The weights are rounded to bf16 for
+// the PV product (the operand type: at most 2^-8 relative each, unbiased);
+// the sum l adds the unrounded ones, so lse is exact to fp32.
+// Rows outside a query's range never reach its output: they are not loaded,
+// or their scores become -inf and, where another query of the same MMA sees
+// them, their V rows are masked out, so a NaN or infinity there stays there.
+#include "csa_internal.cuh"
+#include "ptx.cuh"
+
+namespace csa {
+
+namespace {
+
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLn2 = 0.6931471805599453f;
+constexpr float kRescaleAbove = 8.f;  // the reference maximum moves when exceeded by this (log2 units)
+
+template <int D, int MT, bool kFp8>
+struct PaShape {
+  static constexpr int kWarps = D == 256 ? 4 : 8;
+  static constexpr int kThreads = 32 * kWarps;
+  static constexpr int kTile = 16 * kWarps;                      // rows per tile
+  static constexpr int kRows = 16 * MT;                          // query rows per unit
+  static constexpr int kRowBytes = D * (kFp8 ? 1 : 2);
+  static constexpr int kChunks = kRowBytes / 16;                 // 16-byte chunks per row
+  static constexpr int kWarpStage = 2 * 16 * kRowBytes + (kFp8 ? 128 : 0);
+  static constexpr bool kQReg = MT == 1 && D <= 128;             // Q fragments in registers
+  static constexpr int kQBytes = kQReg ? 0 : kRows * D * 2;
+  static constexpr int kSlots = kWarps / 2;
+  static constexpr int kSlotFloats = kRows * D;
+  static constexpr int kSlotBytes = kSlots * (kSlotFloats + 2 * kRows) * 4;
+  static constexpr int kRoom = (224 * 1024 - kQBytes - kSlotBytes) / (kWarps * kWarpStage);
+  static constexpr int kStages = kRoom > 6 ? 6 : kRoom;
+  static constexpr int kRing = kStages * kWarps * kWarpStage;
+  static constexpr int kSmem = kRing + kQBytes + kSlotBytes;
+  static_assert(kStages >= 2, "no room for two stages");
+};
+
+// What a CTA leaves for the join of the unit that starts in it and goes on in
+// the next CTAs (count = 0: none).
+struct PaJoin {
+  int count;         // CTAs that hold a piece
+  int slot;          // the first piece's slot in this CTA (0 or 1)
+  int b, unit;
+};
+
+__device__ __forceinline__ float fast_exp2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;\n" : "=f"(y) : "f"(x));
+  return y;
+}
+// Two E4M3 codes (low byte first) to bf16x2, exactly.
+__device__ __forceinline__ uint32_t e4m3x2_to_bf16x2(uint32_t pair) {
+  uint32_t o;
+  asm("{\n .reg .b32 h2;\n .reg .b16 a, b, c;\n .reg .f32 fa, fb;\n cvt.u16.u32 c, %1;\n"
+      " cvt.rn.f16x2.e4m3x2 h2, c;\n mov.b32 {a, b}, h2;\n"
+      " cvt.f32.f16 fa, a;\n cvt.f32.f16 fb, b;\n cvt.rn.bf16x2.f32 %0, fb, fa;\n}\n"
+      : "=r"(o)
+      : "r"(pair));
+  return o;
+}
+__device__ __forceinline__ void cp_async4(uint32_t dst, const void* src, int src_bytes) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;\n" ::"r"(dst), "l"(src), "r"(src_bytes) : "memory");
+}
+__device__ __forceinline__ float lds_f32(uint32_t a) {
+  float v;
+  asm volatile("ld.shared.f32 %0, [%1];\n" : "=f"(v) : "r"(a));
+  return v;
+}
+__device__ __forceinline__ uint4 lds_u4(uint32_t a) {
+  uint4 v;
+  asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];\n" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a));
+  return v;
+}
+__device__ __forceinline__ uint2 lds_u2(uint32_t a) {
+  uint2 v;
+  asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];\n" : "=r"(v.x), "=r"(v.y) : "r"(a));
+  return v;
+}
+
+// Where 16-byte chunk ch of a warp's row lies in the row's shared memory.
+// bf16: the eight rows of an ldmatrix at one chunk fall on different banks.
+// E4M3: the quad-wise 16-byte reads of K (two neighbouring rows, four chunks
+// per phase) and of V (four even or odd rows, two chunks) do.
+template <bool kFp8>
+__device__ __forceinline__ int swizzle(int row, int ch) {
+  return kFp8 ? ch ^ ((((row >> 1) & 3) << 1) ^ ((row & 1) << 2)) : ch ^ (row & 7);
+}
+
+// Tiles of a request (at least one, so that every unit is visited and
+// written): the rows any of its S queries sees are [lo, L).
+template <int kTile>
+struct Span {
+  int L, lo, t0, tiles;
+  __device__ __forceinline__ void set(const PagedArgs& a, int len) {
+    L = len < 0 || len > a.max_len ? 0 : len;  // a bad length reads nothing
+    const int p0 = L - a.S;
+    lo = a.win > 0 && p0 - a.win + 1 > 0 ? p0 - a.win + 1 : 0;
+    t0 = lo / kTile;
+    tiles = (L + kTile - 1) / kTile - t0;
+    if (tiles < 1) tiles = 1;
+  }
+};
+
+// Position in the list of tiles: request b, unit (kv head, chunk), tile.
+template <int kTile>
+struct Cursor {
+  int b, unit, tile;
+  Span<kTile> sp;
+  __device__ __forceinline__ void next(const PagedArgs& a, int units) {
+    if (++tile < sp.tiles) return;
+    tile = 0;
+    if (++unit < units) return;
+    unit = 0;
+    if (++b < a.B) sp.set(a, a.ctx_len[b]);
+  }
+};
+
+template <int D, int MT, bool kFp8>
+__global__ void __launch_bounds__(PaShape<D, MT, kFp8>::kThreads, 1)
+    paged_attn_kernel(const PagedArgs a, int chunks, float* __restrict__ part, PaJoin* __restrict__ joins) {
+  using Sh = PaShape<D, MT, kFp8>;
+  constexpr int kTile = Sh::kTile;
+  extern __shared__ __align__(128) uint8_t smem_raw[];
+  __shared__ int scan_tmp[33];
+  __shared__ int64_t start_at;
+  __shared__ int start_b;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const uint32_t ring = smem_u32(smem_raw) + warp * (Sh::kStages * Sh::kWarpStage);
+  const uint32_t qsm = smem_u32(smem_raw) + Sh::kRing;
+  float* slots = reinterpret_cast<float*>(smem_raw + Sh::kRing + Sh::kQBytes);
+  const int group = a.heads / a.kv_heads;
+  const int qrows = a.S * group;                    // query rows per kv head
+  const int units = a.kv_heads * chunks;
+  pdl_wait();
+  pdl_trigger();
+
+  // ---- this CTA's share of the list
+  int64_t total = 0;
+  for (int b0 = 0; b0 < a.B; b0 += Sh::kThreads) {
+    Span<kTile> sp;
+    int n = 0, sum;
+    if (b0 + tid < a.B) sp.set(a, a.ctx_len[b0 + tid]), n = sp.tiles;
+    block_exclusive_scan(n, scan_tmp, &sum);
+    total += sum;
+  }
+  total *= units;
+  const int64_t G = total < gridDim.x ? total : gridDim.x;
+  if (blockIdx.x >= G) {
+    if (tid == 0) joins[blockIdx.x].count = 0;
+    return;
+  }
+  const int64_t lo = blockIdx.x * total / G, hi = (blockIdx.x + 1) * total / G;
+  int64_t before = 0;
+  for (int b0 = 0; b0 < a.B; b0 += Sh::kThreads) {
+    Span<kTile> sp;
+    int n = 0, sum;
+    if (b0 + tid < a.B) {
+      const int len = a.ctx_len[b0 + tid];
+      sp.set(a, len);
+      n = sp.tiles;
+      if (blockIdx.x == 0 && a.status && (len < 0 || len > a.max_len)) set_status(a.status, kStatusBadIndex);
+    }
+    const int64_t p = (before + block_exclusive_scan(n, scan_tmp, &sum)) * units;
+    if (n > 0 && p <= lo && lo < p + (int64_t)n * units) start_b = b0 + tid, start_at = lo - p;
+    before += sum;
+  }
+  __syncthreads();
+  Cursor<kTile> ld;  // the loader's position, several tiles ahead of the products
+  ld.b = start_b;
+  ld.sp.set(a, a.ctx_len[ld.b]);
+  ld.unit = (int)(start_at / ld.sp.tiles);
+  ld.tile = (int)(start_at - (int64_t)ld.unit * ld.sp.tiles);
+  Cursor<kTile> cu = ld;
+  const int steps = (int)(hi - lo);
+  int loaded = 0;
+
+  // ---- row copies: lane r < 16 looks up the pool row of the warp's row r,
+  // one tile ahead of the copies that use it (-1: nothing to read)
+  int prow = -1;
+  auto lookup = [&](const Cursor<kTile>& c) {
+    int p = -1;
+    if (lane < 16) {
+      const int r = (c.sp.t0 + c.tile) * kTile + warp * 16 + lane;
+      if (r >= c.sp.lo && r < c.sp.L) {
+        const int64_t x = pool_row(a.table, a.block, a.table_stride, a.off, c.b, r);
+        if (x >= 0 && x < a.rows) p = (int)x;
+        else if (a.status) set_status(a.status, kStatusBadIndex);
+      }
+    }
+    return p;
+  };
+  auto copy = [&](int stage) {
+    const uint32_t kdst = ring + stage * Sh::kWarpStage, vdst = kdst + 16 * Sh::kRowBytes;
+    const int h = ld.unit / chunks;
+    constexpr int kSpan = Sh::kChunks > 32 ? 32 : Sh::kChunks;           // lanes per row and copy
+    constexpr int kPer = 32 / kSpan;                                     // rows per warp-wide copy
+#pragma unroll
+    for (int i = 0; i < 16 / kPer; ++i) {
+      const int row = i * kPer + lane / kSpan, ch = lane % kSpan;
+      const int p = __shfl_sync(0xffffffffu, prow, row);
+      const int64_t x = p < 0 ? 0 : p;
+      const uint32_t at = row * Sh::kRowBytes + swizzle<kFp8>(row, ch) * 16;
+      constexpr int es = kFp8 ? 1 : 2;
+      const uint8_t* ks = static_cast<const uint8_t*>(a.k) + (x * a.k_stride + h * D) * es + ch * 16;
+      const uint8_t* vs = static_cast<const uint8_t*>(a.v) + (x * a.v_stride + h * D) * es + ch * 16;
+      cp_async16(kdst + at, ks, p < 0 ? 0 : 16);
+      cp_async16(vdst + at, vs, p < 0 ? 0 : 16);
+    }
+    if (kFp8) {  // lanes 0..15: K scales, 16..31: V scales
+      const int p = __shfl_sync(0xffffffffu, prow, lane & 15);
+      const float* s = (lane < 16 ? a.k_scale : a.v_scale) + (int64_t)(p < 0 ? 0 : p) * a.scale_stride + h;
+      cp_async4(kdst + 32 * Sh::kRowBytes + lane * 4, s, p < 0 ? 0 : 4);
+    }
+  };
+  auto load_step = [&] {
+    if (loaded < steps) {
+      copy(loaded % Sh::kStages);
+      ++loaded;
+      if (loaded < steps) {
+        ld.next(a, units);
+        prow = lookup(ld);
+      }
+    }
+    cp_async_commit();
+  };
+  prow = lookup(ld);
+#pragma unroll
+  for (int i = 0; i < Sh::kStages - 1; ++i) load_step();
+
+  // ---- per-unit state
+  const int g = lane >> 2, c = lane & 3;
+  uint32_t qf[Sh::kQReg ? D / 16 : 1][4];
+  float o[MT][D / 8][4], m[MT][2], l[MT][2];
+  int pos[MT][2], sq[MT][2];                       // last visible row and token of the thread's query rows
+  int seg_first = 0;                               // step at which the current piece started
+  bool seg_new = true;
+  const float scale2 = a.scale * kLog2e;
+
+  for (int step = 0; step < steps; ++step) {
+    const int h = cu.unit / chunks, row0 = (cu.unit - h * chunks) * Sh::kRows;
+    if (seg_new) {
+      seg_new = false;
+      seg_first = step;
+      const __nv_bfloat16* q0 = static_cast<const __nv_bfloat16*>(a.q) + (int64_t)cu.b * a.S * a.q_stride;
+      auto q_at = [&](int i) {  // query row i of the unit's kv head: token i / group, head h * group + i % group
+        const int s = i / group;
+        return q0 + (int64_t)s * a.q_stride + (h * group + i - s * group) * D;
+      };
+#pragma unroll
+      for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const int i = row0 + mt * 16 + g + 8 * e;
+          sq[mt][e] = i < qrows ? i / group : a.S;
+          pos[mt][e] = i < qrows ? cu.sp.L - a.S + i / group : -1;
+          m[mt][e] = -INFINITY;
+          l[mt][e] = 0.f;
+        }
+#pragma unroll
+      for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+        for (int j = 0; j < D / 8; ++j) o[mt][j][0] = o[mt][j][1] = o[mt][j][2] = o[mt][j][3] = 0.f;
+      if constexpr (Sh::kQReg) {
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const int i = row0 + g + 8 * e;
+          const bool in = i < qrows;
+          const __nv_bfloat16* q = q_at(in ? i : 0);
+#pragma unroll
+          for (int ks = 0; ks < D / 16; ++ks) {
+            if constexpr (kFp8) {  // the k order of the E4M3 fragments, see below
+              const uint2 v = in ? *reinterpret_cast<const uint2*>(q + (ks / 4) * 64 + c * 16 + (ks % 4) * 4)
+                                 : make_uint2(0, 0);
+              qf[ks][e] = v.x;
+              qf[ks][2 + e] = v.y;
+            } else {
+              qf[ks][e] = in ? *reinterpret_cast<const uint32_t*>(q + ks * 16 + c * 2) : 0;
+              qf[ks][2 + e] = in ? *reinterpret_cast<const uint32_t*>(q + ks * 16 + 8 + c * 2) : 0;
+            }
+          }
+        }
+      } else {
+        for (int x = tid; x < Sh::kRows * (D / 8); x += Sh::kThreads) {
+          const int r = x / (D / 8), ch = x % (D / 8);
+          uint4 v = make_uint4(0, 0, 0, 0);
+          if (row0 + r < qrows) v = *reinterpret_cast<const uint4*>(q_at(row0 + r) + ch * 8);
+          *reinterpret_cast<uint4*>(smem_raw + Sh::kRing + r * D * 2 + ((ch ^ (r & 7)) * 16)) = v;
+        }
+        __syncthreads();
+      }
+    }
+    load_step();
+    cp_async_wait<Sh::kStages - 1>();
+    __syncwarp();
+    const uint32_t kt = ring + (step % Sh::kStages) * Sh::kWarpStage, vt = kt + 16 * Sh::kRowBytes;
+    const int base = (cu.sp.t0 + cu.tile) * kTile + warp * 16;   // first row of the warp's 16
+    if (base < cu.sp.L && base + 15 >= cu.sp.lo) {
+      // ---- S = Q K^T: 16 MT query rows x 16 rows (two n = 8 tiles)
+      float s[MT][2][4];
+#pragma unroll
+      for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+        for (int n = 0; n < 2; ++n) s[mt][n][0] = s[mt][n][1] = s[mt][n][2] = s[mt][n][3] = 0.f;
+      auto q_frag = [&](int mt, int ks, uint32_t* f) {
+        if constexpr (Sh::kQReg) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) f[i] = qf[ks][i];
+        } else if constexpr (kFp8) {
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            const int r = mt * 16 + g + 8 * e, ch = (ks / 4) * 8 + c * 2 + ((ks % 4) >> 1);
+            const uint2 v = lds_u2(qsm + r * D * 2 + ((ch ^ (r & 7)) * 16) + (ks & 1) * 8);
+            f[e] = v.x;
+            f[2 + e] = v.y;
+          }
+        } else {
+          const int r = mt * 16 + (lane & 15), ch = ks * 2 + (lane >> 4);
+          ldsm_x4(qsm + r * D * 2 + ((ch ^ (r & 7)) * 16), f[0], f[1], f[2], f[3]);
+        }
+      };
+      if constexpr (kFp8) {
+        // The order of the products over d is free: thread c of a quad takes
+        // 16 consecutive codes of its row per 64 dims, four per K = 16 step
+        // (q's fragments above take the same dims).
+#pragma unroll
+        for (int j = 0; j < D / 64; ++j) {
+          uint32_t w[2][4];
+#pragma unroll
+          for (int n = 0; n < 2; ++n) {
+            const int r = n * 8 + g;
+            const uint4 v = lds_u4(kt + r * Sh::kRowBytes + swizzle<true>(r, j * 4 + c) * 16);
+            w[n][0] = v.x; w[n][1] = v.y; w[n][2] = v.z; w[n][3] = v.w;
+          }
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            uint32_t b[2][2];
+#pragma unroll
+            for (int n = 0; n < 2; ++n) {
+              b[n][0] = e4m3x2_to_bf16x2(w[n][i]);
+              b[n][1] = e4m3x2_to_bf16x2(w[n][i] >> 16);
+            }
+#pragma unroll
+            for (int mt = 0; mt < MT; ++mt) {
+              uint32_t f[4];
+              q_frag(mt, j * 4 + i, f);
+              mma_bf16_16816(s[mt][0], f, b[0][0], b[0][1]);
+              mma_bf16_16816(s[mt][1], f, b[1][0], b[1][1]);
+            }
+          }
+        }
+      } else {
+#pragma unroll
+        for (int ks = 0; ks < D / 16; ++ks) {
+          const int r = ((lane >> 4) << 3) + (lane & 7), ch = ks * 2 + ((lane >> 3) & 1);
+          uint32_t b0, b1, b2, b3;
+          ldsm_x4(kt + r * Sh::kRowBytes + swizzle<false>(r, ch) * 16, b0, b1, b2, b3);
+#pragma unroll
+          for (int mt = 0; mt < MT; ++mt) {
+            uint32_t f[4];
+            q_frag(mt, ks, f);
+            mma_bf16_16816(s[mt][0], f, b0, b1);
+            mma_bf16_16816(s[mt][1], f, b2, b3);
+          }
+        }
+      }
+      // ---- scores in log2 units; rows outside a query's range weigh nothing
+      float ksc[2][2], vsc[2][2];
+#pragma unroll
+      for (int n = 0; n < 2; ++n)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          ksc[n][e] = scale2;
+          vsc[n][e] = 1.f;
+          if (kFp8) {
+            const uint32_t sc = kt + 32 * Sh::kRowBytes + (n * 8 + c * 2 + e) * 4;
+            ksc[n][e] *= lds_f32(sc);
+            vsc[n][e] = lds_f32(sc + 64);
+          }
+        }
+      const int p_first = cu.sp.L - a.S;   // the first token's position
+      const bool edge = base < cu.sp.lo || base + 15 > p_first ||
+                        (a.win > 0 && base < cu.sp.L - a.win);  // some query does not see all 16 rows
+      uint32_t pf[MT][4];
+#pragma unroll
+      for (int mt = 0; mt < MT; ++mt) {
+#pragma unroll
+        for (int n = 0; n < 2; ++n)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            float x = s[mt][n][i] * ksc[n][i & 1];
+            if (edge) {
+              const int r = base + n * 8 + c * 2 + (i & 1), last = pos[mt][i >> 1];
+              if (r > last || (a.win > 0 && r <= last - a.win)) x = -INFINITY;
+            }
+            s[mt][n][i] = x;
+          }
+        float top[2];
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          float t = fmaxf(fmaxf(s[mt][0][2 * e], s[mt][0][2 * e + 1]), fmaxf(s[mt][1][2 * e], s[mt][1][2 * e + 1]));
+          t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, 1));
+          top[e] = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, 2));
+        }
+        const bool grow = top[0] > m[mt][0] + kRescaleAbove || top[1] > m[mt][1] + kRescaleAbove;
+        if (__any_sync(0xffffffffu, grow)) {
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            if (top[e] > m[mt][e] + kRescaleAbove) {
+              const float f = fast_exp2(m[mt][e] - top[e]);
+              m[mt][e] = top[e];
+              l[mt][e] *= f;
+#pragma unroll
+              for (int j = 0; j < D / 8; ++j) {
+                o[mt][j][2 * e] *= f;
+                o[mt][j][2 * e + 1] *= f;
+              }
+            }
+          }
+        }
+        float p[2][4];
+#pragma unroll
+        for (int n = 0; n < 2; ++n)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const float ref = m[mt][i >> 1] == -INFINITY ? 0.f : m[mt][i >> 1];
+            p[n][i] = fast_exp2(s[mt][n][i] - ref);
+            l[mt][i >> 1] += p[n][i];
+            // a row that weighs nothing stays at zero whatever its scale
+            if (kFp8) p[n][i] = p[n][i] == 0.f ? 0.f : p[n][i] * vsc[n][i & 1];
+          }
+        pf[mt][0] = pack_bf16x2(p[0][0], p[0][1]);
+        pf[mt][1] = pack_bf16x2(p[0][2], p[0][3]);
+        pf[mt][2] = pack_bf16x2(p[1][0], p[1][1]);
+        pf[mt][3] = pack_bf16x2(p[1][2], p[1][3]);
+      }
+      // ---- O += P V.  Where tokens of one MMA see different rows (S > 1 at
+      // an end of their ranges), one pass per token with its own V rows kept
+      // and its own query rows added (a zero weight times a NaN is a NaN).
+      const int passes = edge && a.S > 1 ? a.S : 1;
+      for (int t = 0; t < passes; ++t) {
+        uint32_t keep[2] = {0xffffffffu, 0xffffffffu};
+        auto pv = [&](int mt, int j, uint32_t b0, uint32_t b1) {
+          if (passes == 1) {
+            mma_bf16_16816(o[mt][j], pf[mt], b0, b1);
+          } else {
+            float x[4] = {0.f, 0.f, 0.f, 0.f};
+            mma_bf16_16816(x, pf[mt], b0 & keep[0], b1 & keep[1]);
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+              if (sq[mt][i >> 1] == t) o[mt][j][i] += x[i];
+          }
+        };
+        if (passes > 1) {
+          const int last = p_first + t;
+#pragma unroll
+          for (int n = 0; n < 2; ++n) {
+            keep[n] = 0;
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              const int r = base + n * 8 + c * 2 + e;
+              if (r <= last && (a.win == 0 || r > last - a.win)) keep[n] |= e ? 0xffff0000u : 0xffffu;
+            }
+          }
+        }
+        if constexpr (kFp8) {
+          // n-tile j holds dims 16 n + j (n = 0..7): thread g takes codes 16 g .. 16 g + 15 of its four rows
+          uint32_t w[4][4];
+#pragma unroll
+          for (int x = 0; x < 4; ++x) {
+            const int r = (x >> 1) * 8 + c * 2 + (x & 1);
+            const uint4 v = lds_u4(vt + r * Sh::kRowBytes + swizzle<true>(r, g) * 16);
+            w[x][0] = v.x; w[x][1] = v.y; w[x][2] = v.z; w[x][3] = v.w;
+          }
+#pragma unroll
+          for (int y = 0; y < 4; ++y) {
+            const uint32_t lo01 = __byte_perm(w[0][y], w[1][y], 0x5140), hi01 = __byte_perm(w[0][y], w[1][y], 0x7362);
+            const uint32_t lo23 = __byte_perm(w[2][y], w[3][y], 0x5140), hi23 = __byte_perm(w[2][y], w[3][y], 0x7362);
+#pragma unroll
+            for (int z = 0; z < 4; ++z) {
+              const uint32_t b0 = e4m3x2_to_bf16x2((z < 2 ? lo01 : hi01) >> (16 * (z & 1)));
+              const uint32_t b1 = e4m3x2_to_bf16x2((z < 2 ? lo23 : hi23) >> (16 * (z & 1)));
+#pragma unroll
+              for (int mt = 0; mt < MT; ++mt) pv(mt, y * 4 + z, b0, b1);
+            }
+          }
+        } else {
+#pragma unroll
+          for (int dt = 0; dt < D / 16; ++dt) {
+            const int r = (((lane >> 3) & 1) << 3) + (lane & 7), ch = dt * 2 + (lane >> 4);
+            uint32_t b0, b1, b2, b3;
+            ldsm_x4_trans(vt + r * Sh::kRowBytes + swizzle<false>(r, ch) * 16, b0, b1, b2, b3);
+#pragma unroll
+            for (int mt = 0; mt < MT; ++mt) {
+              pv(mt, dt * 2, b0, b1);
+              pv(mt, dt * 2 + 1, b2, b3);
+            }
+          }
+        }
+      }
+    }
+    __syncwarp();
+
+    // ---- end of the unit or of this CTA's share: join the warps
+    const bool unit_end = cu.tile + 1 == cu.sp.tiles;
+    if (unit_end || step + 1 == steps) {
+#pragma unroll
+      for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          l[mt][e] += __shfl_xor_sync(0xffffffffu, l[mt][e], 1);
+          l[mt][e] += __shfl_xor_sync(0xffffffffu, l[mt][e], 2);
+        }
+      float* so = slots + (warp % Sh::kSlots) * Sh::kSlotFloats;
+      float* sml = slots + Sh::kSlots * Sh::kSlotFloats + (warp % Sh::kSlots) * 2 * Sh::kRows;
+      auto dim_of = [&](int j, int e) { return kFp8 ? 32 * c + 16 * e + j : 8 * j + 2 * c + e; };
+      auto put = [&] {
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            const int r = mt * 16 + g + 8 * e;
+            if (c == 0) sml[r] = m[mt][e], sml[Sh::kRows + r] = l[mt][e];
+#pragma unroll
+            for (int j = 0; j < D / 8; ++j) {
+              so[r * D + dim_of(j, 0)] = o[mt][j][2 * e];
+              so[r * D + dim_of(j, 1)] = o[mt][j][2 * e + 1];
+            }
+          }
+      };
+      __syncthreads();   // the slots' last readers are done
+      if (warp >= Sh::kSlots) put();
+      __syncthreads();
+      if (warp < Sh::kSlots) {
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            const int r = mt * 16 + g + 8 * e;
+            const float m2 = sml[r], top = fmaxf(m[mt][e], m2), ref = top == -INFINITY ? 0.f : top;
+            const float f1 = fast_exp2(m[mt][e] - ref), f2 = fast_exp2(m2 - ref);
+            l[mt][e] = l[mt][e] * f1 + sml[Sh::kRows + r] * f2;
+            m[mt][e] = top;
+#pragma unroll
+            for (int j = 0; j < D / 8; ++j) {
+              o[mt][j][2 * e] = o[mt][j][2 * e] * f1 + so[r * D + dim_of(j, 0)] * f2;
+              o[mt][j][2 * e + 1] = o[mt][j][2 * e + 1] * f1 + so[r * D + dim_of(j, 1)] * f2;
+            }
+          }
+        __syncwarp();
+        put();
+      }
+      __syncthreads();
+      // the kSlots states, a warp per row: a lane owns D / 32 neighbouring dims
+      const bool whole = unit_end && cu.tile == step - seg_first;   // the piece is the whole unit
+      const float* ml = slots + Sh::kSlots * Sh::kSlotFloats;
+      const int slot = seg_first == 0 ? 0 : 1;
+      const int64_t pslot = (int64_t)blockIdx.x * 2 + slot;
+      for (int r = warp; r < Sh::kRows && row0 + r < qrows; r += Sh::kWarps) {
+        float top = -INFINITY;
+#pragma unroll
+        for (int x = 0; x < Sh::kSlots; ++x) top = fmaxf(top, ml[x * 2 * Sh::kRows + r]);
+        const float ref = top == -INFINITY ? 0.f : top;
+        float sum = 0.f, acc[D / 32];
+#pragma unroll
+        for (int i = 0; i < D / 32; ++i) acc[i] = 0.f;
+#pragma unroll
+        for (int x = 0; x < Sh::kSlots; ++x) {
+          const float f = fast_exp2(ml[x * 2 * Sh::kRows + r] - ref);
+          sum += ml[x * 2 * Sh::kRows + Sh::kRows + r] * f;
+#pragma unroll
+          for (int i = 0; i < D / 32; ++i)
+            acc[i] += slots[x * Sh::kSlotFloats + r * D + lane * (D / 32) + i] * f;
+        }
+        if (whole) {
+          const int i = row0 + r, s = i / group, hd = h * group + i - s * group;
+          const bool any = sum > 0.f || sum != sum;   // some row weighs (a NaN is passed on)
+          const float inv = any ? 1.f / sum : 0.f;
+          __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(a.out) + ((int64_t)cu.b * a.S + s) * a.out_stride + hd * D +
+                               lane * (D / 32);
+#pragma unroll
+          for (int x = 0; x < D / 32; x += 2)
+            *reinterpret_cast<uint32_t*>(dst + x) = pack_bf16x2(acc[x] * inv, acc[x + 1] * inv);
+          if (a.lse && lane == 0)
+            a.lse[((int64_t)cu.b * a.S + s) * a.heads + hd] = any ? (top + log2f(sum)) * kLn2 : -INFINITY;
+        } else {
+          float* dst = part + (pslot * Sh::kRows + r) * (D + 2);
+#pragma unroll
+          for (int x = 0; x < D / 32; ++x) dst[lane * (D / 32) + x] = acc[x];
+          if (lane == 0) dst[D] = top, dst[D + 1] = sum;
+        }
+      }
+      if (tid == 0 && step + 1 == steps) {
+        // the unit starts here (in its first tile) and goes on in the next
+        // CTAs: this CTA's entry names the pieces
+        PaJoin j;
+        j.count = 0;
+        j.slot = slot;
+        j.b = cu.b;
+        j.unit = cu.unit;
+        if (!unit_end && cu.tile == step - seg_first) {
+          const int64_t last = lo + seg_first + cu.sp.tiles - 1;     // the unit's last tile in the list
+          j.count = (int)(((last + 1) * G - 1) / total) - (int)blockIdx.x + 1;
+        }
+        joins[blockIdx.x] = j;
+      }
+      seg_new = true;
+    }
+    cu.next(a, units);
+  }
+}
+
+// Joins the pieces of the units cut between CTAs: block (x, y) does query row
+// y of the unit that starts in CTA x, its warps a part of the pieces each.
+constexpr int kJoinWarps = 8;
+template <int D>
+__global__ void __launch_bounds__(32 * kJoinWarps)
+    paged_join_kernel(const PagedArgs a, int chunks, int rows, const float* __restrict__ part,
+                      const PaJoin* __restrict__ joins) {
+  __shared__ float sm_o[kJoinWarps][D], sm_m[kJoinWarps], sm_l[kJoinWarps];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  pdl_wait();
+  pdl_trigger();
+  const PaJoin j = joins[blockIdx.x];
+  if (j.count == 0) return;
+  const int group = a.heads / a.kv_heads, h = j.unit / chunks, i = (j.unit - h * chunks) * rows + blockIdx.y;
+  if (i >= a.S * group) return;
+  float m = -INFINITY, l = 0.f, acc[D / 32];
+#pragma unroll
+  for (int x = 0; x < D / 32; ++x) acc[x] = 0.f;
+  for (int p = warp; p < j.count; p += kJoinWarps) {
+    const int64_t slot = p == 0 ? (int64_t)blockIdx.x * 2 + j.slot : (int64_t)(blockIdx.x + p) * 2;
+    const float* src = part + (slot * rows + blockIdx.y) * (D + 2);
+    const float m2 = src[D], l2 = src[D + 1];
+    const float top = fmaxf(m, m2), ref = top == -INFINITY ? 0.f : top;
+    const float f1 = fast_exp2(m - ref), f2 = fast_exp2(m2 - ref);
+    l = l * f1 + l2 * f2;
+    m = top;
+#pragma unroll
+    for (int x = 0; x < D / 32; ++x) acc[x] = acc[x] * f1 + src[lane + 32 * x] * f2;
+  }
+  if (lane == 0) sm_m[warp] = m, sm_l[warp] = l;
+#pragma unroll
+  for (int x = 0; x < D / 32; ++x) sm_o[warp][lane + 32 * x] = acc[x];
+  __syncthreads();
+  float top = -INFINITY;
+#pragma unroll
+  for (int w = 0; w < kJoinWarps; ++w) top = fmaxf(top, sm_m[w]);
+  const float ref = top == -INFINITY ? 0.f : top;
+  float sum = 0.f, f[kJoinWarps];
+#pragma unroll
+  for (int w = 0; w < kJoinWarps; ++w) f[w] = fast_exp2(sm_m[w] - ref), sum += sm_l[w] * f[w];
+  const bool any = sum > 0.f || sum != sum;
+  const int s = i / group, hd = h * group + i - s * group;
+  const int64_t tok = (int64_t)j.b * a.S + s;
+  if (threadIdx.x < D) {
+    const int d = threadIdx.x;
+    float v = 0.f;
+#pragma unroll
+    for (int w = 0; w < kJoinWarps; ++w) v += sm_o[w][d] * f[w];
+    static_cast<__nv_bfloat16*>(a.out)[tok * a.out_stride + hd * D + d] = __float2bfloat16_rn(any ? v / sum : 0.f);
+  }
+  if (a.lse && threadIdx.x == 0) a.lse[tok * a.heads + hd] = any ? (top + log2f(sum)) * kLn2 : -INFINITY;
+}
+
+template <int D, int MT, bool kFp8>
+int launch_shape(const PagedArgs& a, int num_sms, cudaStream_t st, bool pdl) {
+  using Sh = PaShape<D, MT, kFp8>;
+  auto kern = paged_attn_kernel<D, MT, kFp8>;
+  static PerDeviceOnce attr;
+  if (const cudaError_t e = attr.run([&] { return allow_max_dynamic_smem(kern); }))
+    return launch_fail("cudaFuncSetAttribute(paged_attn_kernel)", e);
+  const int qrows = a.S * (a.heads / a.kv_heads), chunks = (qrows + Sh::kRows - 1) / Sh::kRows;
+  float* part = static_cast<float*>(a.workspace);
+  PaJoin* joins = reinterpret_cast<PaJoin*>(part + (size_t)num_sms * 2 * Sh::kRows * (D + 2));
+  // at most the tiles that the bound on the lengths allows
+  const int64_t tiles = (int64_t)a.B * a.kv_heads * chunks * ((a.max_len + Sh::kTile - 1) / Sh::kTile + 1);
+  const int grid = tiles < num_sms ? (int)tiles : num_sms;
+  const int r = launch_kernel(kern, dim3(grid), dim3(Sh::kThreads), Sh::kSmem, st, pdl, a, chunks, part, joins);
+  if (r < 0) return r;
+  const int rows = qrows < Sh::kRows ? qrows : Sh::kRows;
+  const int r2 = launch_kernel(paged_join_kernel<D>, dim3(grid, rows), dim3(32 * kJoinWarps), 0, st, pdl, a, chunks,
+                               (int)Sh::kRows, (const float*)part, (const PaJoin*)joins);
+  return r2 < 0 ? r2 : r + r2;
+}
+
+}  // namespace
+
+// Partials of two pieces per CTA of up to 32 query rows, and the join list.
+size_t paged_attn_workspace(int dim, int num_sms) {
+  return (size_t)num_sms * (2 * 32 * (dim + 2) * sizeof(float) + sizeof(PaJoin));
+}
+
+int launch_paged_attn(const PagedArgs& a, bool fp8, int num_sms, cudaStream_t st, bool pdl) {
+  const bool two = a.S * (a.heads / a.kv_heads) > 16;
+  if (fp8) return two ? launch_shape<128, 2, true>(a, num_sms, st, pdl) : launch_shape<128, 1, true>(a, num_sms, st, pdl);
+  switch (a.dim) {
+    case 64: return two ? launch_shape<64, 2, false>(a, num_sms, st, pdl) : launch_shape<64, 1, false>(a, num_sms, st, pdl);
+    case 128: return two ? launch_shape<128, 2, false>(a, num_sms, st, pdl) : launch_shape<128, 1, false>(a, num_sms, st, pdl);
+    default: return launch_shape<256, 1, false>(a, num_sms, st, pdl);
+  }
+}
+
+}  // namespace csa

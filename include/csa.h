@@ -333,6 +333,58 @@ typedef struct {
  * CSA_ERR_UNSUPPORTED (out_dtype). */
 CSA_API int csa_fp8_matmul(const csa_fp8_mm *a, void *stream);
 
+/* Dense causal attention of the S newest tokens of each request over all of
+ * its cache (S = 1: one new token), for layers that select nothing: heads /
+ * kv_heads query heads share a K and a V row.  Query s of request b sits at
+ * pos = L_b - S + s and sees the cache rows max(0, pos - win + 1) .. pos
+ * (win = 0: 0 .. pos; pos < 0: none):
+ *   out[b][s][h] = sum_r softmax_r(softmax_scale q[b][s][h] . k[r]) v[r]
+ *   lse[b][s][h] = ln sum_r exp(softmax_scale q . k[r])
+ * A query that sees no row (L_b = 0 is a padding request) gets zeros and -inf.
+ * Cache rows hold kv_heads x dim elements, head g at g * dim; k and v may be
+ * two halves of one pool.  Row r of request b is pool row off[b] + r, or
+ * table[b * table_stride + r / block] * block + r % block with a block table,
+ * as in csa_batch.  Scores, the softmax's maximum and sum, and the sum over
+ * rows are fp32; the weights are rounded to bf16 for the product with v. */
+typedef struct {
+    int32_t B, S;             /* requests (0: a no-op), new tokens per request      */
+    int32_t heads, kv_heads;  /* heads a multiple of kv_heads                       */
+    int32_t dim;              /* 64, 128 or 256 (128 with E4M3 pools)               */
+    int32_t kv_dtype;         /* 0 or CSA_DTYPE_BF16; CSA_DTYPE_FP8_E4M3 with a scale
+                                 per pool row and kv head. q and out are bf16       */
+    int32_t win;              /* sliding window, 0 = none                           */
+    int32_t max_len;          /* bound on every L_b: sizes the grid                 */
+    float softmax_scale;      /* <= 0 selects 1/sqrt(dim)                           */
+    int32_t block, table_stride;                       /* with a table              */
+    const int32_t *ctx_len;   /* [B] L_b, including the S new tokens; 0 <= L_b <= max_len */
+    const void *q; int64_t q_stride;                   /* [B, S, heads, dim]; q_stride elements
+                                                          from one token to the next */
+    const void *k, *v; int64_t k_stride, v_stride;     /* pools [rows, kv_heads, dim]; strides
+                                                          from one row to the next   */
+    int64_t rows;             /* rows of either pool                                */
+    const float *k_scale, *v_scale; int64_t scale_stride;  /* [rows, kv_heads], E4M3 only */
+    const int64_t *off;       /* [B], without a table                               */
+    const int32_t *table;     /* [B * table_stride] or NULL                         */
+    void *out; int64_t out_stride;                     /* [B, S, heads, dim] bf16; out_stride elements
+                                                          from one token to the next */
+    float *lse;               /* [B, S, heads] or NULL                              */
+    int32_t *status;          /* NULL or a device int32: bit 0 (value 1) is set by a length
+                                 outside [0, max_len] (its queries get zeros and -inf) or
+                                 a row that is unmapped or outside the pool (it weighs as a
+                                 row of zeros)                                      */
+    void *workspace; int64_t workspace_bytes;          /* csa_paged_attn_workspace() bytes; calls
+                                                          that share it must be ordered  */
+} csa_paged;
+
+/* q, k, v and out start on 16-byte boundaries and their strides keep the rows
+ * there.  Returns CSA_ERR_INVALID_ARG, CSA_ERR_UNSUPPORTED (dim, kv_dtype) or
+ * CSA_ERR_WORKSPACE (workspace_bytes too small). */
+CSA_API int csa_paged_attn(const csa_paged *a, void *stream);
+
+/* Bytes of workspace csa_paged_attn needs on the current device for heads of
+ * `dim` elements, whatever the batch; 0 when the device cannot be asked. */
+CSA_API int64_t csa_paged_attn_workspace(int32_t dim);
+
 /* Host-side checks of a batch against a config, exactly those every entry
  * point runs before launching (null / misaligned pointers, strides, sizes
  * against the maxima, ctx_len_host values).  Touches no device memory and

@@ -1,0 +1,400 @@
+"""csa_paged_attn: dense causal attention of each request's newest tokens over (paged) K / V pools, against a
+plain fp64 implementation.
+
+Tolerances.  Scores are fp32 sums of exact bf16 products: with |scale q . k| terms adding up to A they are off
+by at most (dim + 4) 2^-23 A, so lse is too, plus 2^-22 for exp2 and n 2^-24 for the sum of n weights (lse is a
+convex function of the scores with gradient 1) and 2^-23 |lse| for its rounding; the tests' scores have A below
+64 for dim up to 256, so 64 (260) 2^-23 = 2e-3 would be the worst case and 2e-4 holds with a wide margin
+for the random inputs here, whose rounding errors add up like a random walk (sqrt(dim) 2^-24 A < 4e-5 each).
+A weight is rounded to bf16 (u = 2^-8) before the product with v: |out - exact| <= u max_r |v| over the visible
+rows (a convex combination of rows, each weight off by u relative), plus the output's own u |out|; with the
+E4M3 pools the weight times the row's scale is what is rounded, the same bound.
+"""
+import ctypes
+import math
+
+import pytest
+import torch
+
+from compressed_sparse_attention_indexer_gb300 import build as csa_build
+from compressed_sparse_attention_indexer_gb300 import csa
+
+DEV = "cuda:0"
+U = 2.0 ** -8
+LSE_TOL = 2e-4
+
+
+# ---------------------------------------------------------------------------
+# CPU: refusals
+
+@pytest.fixture(scope="module")
+def L():
+    csa_build.build()
+    return csa.lib()
+
+
+def _call(L, **kw):
+    a = 0x10000
+    base = dict(B=2, S=1, heads=8, kv_heads=2, dim=128, kv_dtype=csa.CSA_DTYPE_BF16, win=0, max_len=1000,
+                softmax_scale=0.0, block=64, table_stride=16, ctx_len=a, q=a, q_stride=1024, k=a, v=a, k_stride=256,
+                v_stride=256, rows=100, k_scale=None, v_scale=None, scale_stride=0, off=None, table=a, out=a,
+                out_stride=1024, lse=None, status=None, workspace=a, workspace_bytes=1 << 40)
+    base.update(kw)
+    return L.csa_paged_attn(ctypes.byref(csa.CPaged(**base)), None)
+
+
+FP8 = dict(kv_dtype=csa.CSA_DTYPE_FP8_E4M3, k_scale=0x10000, v_scale=0x10000, scale_stride=2)
+
+
+def test_empty_batch_is_a_no_op(L):
+    assert _call(L, B=0) == csa.CSA_OK
+
+
+@pytest.mark.parametrize("kw,code", [
+    (dict(kv_dtype=7), csa.CSA_ERR_UNSUPPORTED),
+    (dict(dim=96), csa.CSA_ERR_UNSUPPORTED),
+    (dict(FP8, dim=64), csa.CSA_ERR_UNSUPPORTED),
+    (dict(B=-1), csa.CSA_ERR_INVALID_ARG),
+    (dict(S=0), csa.CSA_ERR_INVALID_ARG),
+    (dict(heads=7), csa.CSA_ERR_INVALID_ARG),                # not a multiple of kv_heads
+    (dict(kv_heads=0), csa.CSA_ERR_INVALID_ARG),
+    (dict(win=-1), csa.CSA_ERR_INVALID_ARG),
+    (dict(max_len=-1), csa.CSA_ERR_INVALID_ARG),
+    (dict(max_len=(1 << 30) + 1), csa.CSA_ERR_UNSUPPORTED),
+    (dict(q=None), csa.CSA_ERR_INVALID_ARG),
+    (dict(q=0x10008), csa.CSA_ERR_INVALID_ARG),
+    (dict(q_stride=1023), csa.CSA_ERR_INVALID_ARG),
+    (dict(q_stride=1028), csa.CSA_ERR_INVALID_ARG),
+    (dict(out=None), csa.CSA_ERR_INVALID_ARG),
+    (dict(out_stride=1000), csa.CSA_ERR_INVALID_ARG),
+    (dict(k=None), csa.CSA_ERR_INVALID_ARG),
+    (dict(v=0x10004), csa.CSA_ERR_INVALID_ARG),
+    (dict(k_stride=255), csa.CSA_ERR_INVALID_ARG),
+    (dict(v_stride=260), csa.CSA_ERR_INVALID_ARG),
+    (dict(FP8, v_stride=264), csa.CSA_ERR_INVALID_ARG),      # 264 bytes
+    (dict(FP8, k_scale=None), csa.CSA_ERR_INVALID_ARG),
+    (dict(FP8, scale_stride=1), csa.CSA_ERR_INVALID_ARG),
+    (dict(rows=-1), csa.CSA_ERR_INVALID_ARG),
+    (dict(rows=1 << 31), csa.CSA_ERR_INVALID_ARG),
+    (dict(ctx_len=None), csa.CSA_ERR_INVALID_ARG),
+    (dict(table=None), csa.CSA_ERR_INVALID_ARG),             # neither table nor off
+    (dict(block=0), csa.CSA_ERR_INVALID_ARG),
+    (dict(table_stride=0), csa.CSA_ERR_INVALID_ARG),
+    (dict(off=0x10004, table=None), csa.CSA_ERR_INVALID_ARG),
+    (dict(lse=0x10002), csa.CSA_ERR_INVALID_ARG),
+    (dict(workspace=0x10008), csa.CSA_ERR_INVALID_ARG),
+])
+def test_refusals(L, kw, code):
+    assert _call(L, **kw) == code
+    assert csa.last_error()
+
+
+def test_null_args(L):
+    assert L.csa_paged_attn(None, None) == csa.CSA_ERR_INVALID_ARG
+
+
+def test_object_refusals(L):
+    bf = torch.bfloat16
+    q, k = torch.zeros(2, 1, 8, 128, dtype=bf), torch.zeros(100, 2, 128, dtype=bf)
+    n, t = torch.zeros(2, dtype=torch.int32), torch.zeros(2, 4, dtype=torch.int32)
+    good = dict(table=t, block=16)
+    for args, kw in (((q.float(), k, k, n), good), ((q, k, k.float(), n), good), ((q, k, k[:50], n), good),
+                     ((q, k, k, n.long()), good), ((q, k, k, n), {}), ((q, k, k, n), dict(good, off=n.long())),
+                     ((q, k, k, n), dict(table=t.long(), block=16)), ((q, k, k, n), dict(off=n.long())),
+                     ((q, k.byte(), k.byte(), n), good), ((q, k, k, n), dict(good, k_scale=torch.zeros(100, 2))),
+                     ((q, k, k, n), dict(good, lse=torch.zeros(2, 8))),
+                     ((q, k, k, n), dict(good, out=torch.zeros(2, 1, 8, 64, dtype=bf))),
+                     ((torch.zeros(2, 1, 8, 256, dtype=bf)[..., ::2], k, k, n), good)):
+        with pytest.raises(csa.CsaError):
+            csa.PagedAttention(*args, **kw)
+
+
+# ---------------------------------------------------------------------------
+# GPU
+
+def _gpu():
+    if not torch.cuda.is_available():
+        pytest.skip("no GPU")
+    csa_build.build()
+    torch.cuda.set_device(0)
+
+
+def _pool(lens, hk, d, block, seed, fp8=False, spare=3):
+    """K and V pools with each request's rows in shuffled blocks; every other row is NaN.
+    Returns a dict of device tensors and the dense fp64 rows."""
+    g = torch.Generator().manual_seed(seed)
+    nblk = [-(-n // block) for n in lens]
+    total = sum(nblk) + spare
+    perm = torch.randperm(total, generator=g)
+    table = torch.full((len(lens), max(1, max(nblk))), -1, dtype=torch.int32)
+    at = 0
+    k, v = (torch.full((total * block, hk, d), float("nan")) for _ in range(2))
+    for b, n in enumerate(lens):
+        table[b, :nblk[b]] = perm[at:at + nblk[b]].int()
+        at += nblk[b]
+        if n:
+            r = torch.arange(n)
+            rows = table[b].long()[r // block] * block + r % block
+            k[rows] = torch.randn(n, hk, d, generator=g)
+            v[rows] = torch.randn(n, hk, d, generator=g)
+    out = dict(table=table.to(DEV), block=block)
+    if fp8:
+        for name, t in (("k", k), ("v", v)):
+            amax = t.abs().amax(2)
+            scale = torch.where(amax > 0, amax / 448, torch.ones_like(amax))
+            codes = (t / scale[..., None]).to(torch.float8_e4m3fn)
+            out[name], out[name + "_scale"] = codes.view(torch.uint8).to(DEV), scale.to(DEV)
+        k, v = (out[x].cpu().view(torch.float8_e4m3fn).double() * out[x + "_scale"].cpu().double()[..., None]
+                for x in ("k", "v"))
+    else:
+        out["k"], out["v"] = k.bfloat16().to(DEV), v.bfloat16().to(DEV)
+        k, v = out["k"].cpu().double(), out["v"].cpu().double()
+    return out, k, v
+
+
+def _exact(q, k, v, lens, table, block, win, scale):
+    b, s, h, d = q.shape
+    hk = k.shape[1]
+    out = torch.zeros(b, s, h, d, dtype=torch.float64)
+    lse = torch.full((b, s, h), -math.inf, dtype=torch.float64)
+    big = torch.zeros(b, s, h, 1, dtype=torch.float64)
+    for i, n in enumerate(lens):
+        r = torch.arange(max(n, 0))
+        rows = table[i].long()[r // block] * block + r % block if n > 0 else r
+        for t in range(s):
+            pos = n - s + t
+            if pos < 0:
+                continue
+            at = rows[max(0, pos - win + 1) if win else 0:pos + 1]
+            kk, vv = k[at].repeat_interleave(h // hk, 1), v[at].repeat_interleave(h // hk, 1)
+            sc = torch.einsum("hd,lhd->hl", q[i, t].double(), kk) * scale
+            lse[i, t] = torch.logsumexp(sc, 1)
+            out[i, t] = torch.einsum("hl,lhd->hd", torch.softmax(sc, 1), vv)
+            big[i, t] = vv.abs().amax((0, 2))[:, None]
+    return out, lse, big
+
+
+def _check(got, want, what=""):
+    out, lse, big = want
+    o, l = got["out"].cpu().double(), got["lse"].cpu().double()
+    empty = torch.isinf(lse)
+    assert (l[empty] == -math.inf).all() and (o[empty] == 0).all(), what
+    err = (l - lse)[~empty].abs()
+    assert err.numel() == 0 or err.max() <= LSE_TOL, (what, float(err.max()))
+    tol = 1.01 * U * (big + out.abs()) + 1e-5 * big
+    assert ((o - out).abs() <= tol).all(), (what, float(((o - out).abs() / tol.clamp_min(1e-30)).max()))
+
+
+def _run(lens, s, h, hk, d, block, win=0, fp8=False, seed=0, qstd=1.0, **kw):
+    pool, k, v = _pool(lens, hk, d, block, seed, fp8)
+    g = torch.Generator().manual_seed(seed + 1)
+    q = (torch.randn(len(lens), s, h, d, generator=g) * qstd).bfloat16()
+    n = torch.tensor(lens, dtype=torch.int32, device=DEV)
+    status = torch.zeros(1, dtype=torch.int32, device=DEV)
+    op = csa.PagedAttention(q.to(DEV), pool.pop("k"), pool.pop("v"), n, win=win, status=status, **pool, **kw)
+    got = op()
+    torch.cuda.synchronize()
+    assert int(status.item()) == 0
+    want = _exact(q, k, v, lens, pool["table"].cpu(), block, win, d ** -0.5)
+    _check(got, want, (lens, s, h, hk, d, block, win, fp8))
+    return op, want
+
+
+EDGE = [1, 2, 15, 16, 17, 127, 128, 129, 0, 255, 256, 300, 1, 0, 1000, 63]
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("h,hk,d,fp8", [(8, 8, 64, False), (8, 2, 128, False), (4, 1, 256, False), (6, 2, 128, True),
+                                        (48, 2, 128, False), (34, 2, 64, False), (40, 1, 256, False), (64, 2, 128, True)])
+@pytest.mark.parametrize("block", [16, 48])
+def test_single_tokens_over_edge_lengths(h, hk, d, fp8, block):
+    _gpu()
+    _run(EDGE, 1, h, hk, d, block, fp8=fp8, seed=h + d)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("s,h,hk,d,fp8", [(2, 8, 8, 64, False), (4, 8, 2, 128, False), (3, 4, 1, 256, False),
+                                          (5, 14, 2, 128, True), (7, 12, 2, 128, False), (8, 16, 1, 64, False),
+                                          (20, 4, 4, 128, True)])
+@pytest.mark.parametrize("win", [0, 1, 37, 200])
+def test_several_tokens_and_windows(s, h, hk, d, fp8, win):
+    # lengths below S leave the first tokens without a row
+    _gpu()
+    _run([0, 1, 2, 5, 16, 40, 130, 257, 700], s, h, hk, d, 64, win=win, fp8=fp8, seed=s + win)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("d,fp8", [(64, False), (128, False), (256, False), (128, True)])
+@pytest.mark.parametrize("lens", [[20011], [1], [9000, 3, 1, 12001, 640], [77] * 300])
+def test_long_requests_are_split_and_joined(lens, d, fp8):
+    _gpu()
+    _run(lens, 1, 4, 2, d, 128, fp8=fp8, seed=d)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("fp8", [False, True])
+def test_a_window_of_a_long_request(fp8):
+    _gpu()
+    _run([20011, 5000, 100], 2, 4, 1, 128, 64, win=4097, fp8=fp8)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("qstd", [0.0, 16.0])
+def test_flat_and_peaked_weights(qstd):
+    # peaked: a few weights dominate and the reference maximum moves often; scores have |q . k| scale up to
+    # about 16 x 5, A (see above) up to 16 x 9: LSE_TOL still covers 128 random roundings of 2^-24 of A
+    _gpu()
+    _run([3000, 700, 129], 1, 8, 2, 128, 64, qstd=qstd)
+
+
+@pytest.mark.gpu
+def test_offsets_strides_and_one_pool_for_both():
+    # contiguous rows by offset, K and V interleaved in one pool with extra columns, q and out slices of wider
+    # rows; nothing outside out's columns is written
+    _gpu()
+    lens, h, hk, d = [200, 64, 517], 8, 2, 128
+    g = torch.Generator().manual_seed(3)
+    pool = torch.full((900, 2 * hk + 1, d), float("nan"))
+    off = torch.tensor([5, 230, 310])
+    for b, n in enumerate(lens):
+        pool[off[b]:off[b] + n, :2 * hk] = torch.randn(n, 2 * hk, d, generator=g)
+    pool = pool.bfloat16().to(DEV)
+    wide = torch.randn(3, 1, h + 4, d, generator=g).bfloat16().to(DEV)
+    outw = torch.full((3, 1, h + 4, d), 7.0, dtype=torch.bfloat16, device=DEV)
+    op = csa.PagedAttention(wide[:, :, 2:2 + h], pool[:, :hk], pool[:, hk:2 * hk],
+                            torch.tensor(lens, dtype=torch.int32, device=DEV), off=off.to(DEV), max_len=600,
+                            out=outw[:, :, 4:], scale=0.05)
+    got = op()
+    torch.cuda.synchronize()
+    k, v = pool[:, :hk].cpu().double(), pool[:, hk:2 * hk].cpu().double()
+    out, lse, big = (torch.zeros(3, 1, h, d, dtype=torch.float64), torch.zeros(3, 1, h, dtype=torch.float64),
+                     torch.zeros(3, 1, h, 1, dtype=torch.float64))
+    for i, n in enumerate(lens):
+        rows = torch.arange(n) + off[i]
+        kk, vv = k[rows].repeat_interleave(4, 1), v[rows].repeat_interleave(4, 1)
+        sc = torch.einsum("hd,lhd->hl", wide[i, 0, 2:2 + h].cpu().double(), kk) * 0.05
+        lse[i, 0], out[i, 0] = torch.logsumexp(sc, 1), torch.einsum("hl,lhd->hd", torch.softmax(sc, 1), vv)
+        big[i, 0] = vv.abs().amax((0, 2))[:, None]
+    _check(got, (out, lse, big))
+    assert (outw[:, :, :4] == 7).all()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("win", [0, 20])
+def test_nan_in_a_row_reaches_only_the_tokens_that_see_it(fp8, win):
+    # the last rows (seen by the last tokens only) and, with a window, the first rows (seen by the first tokens
+    # only) hold NaN and infinity: the other tokens' outputs do not change by a bit
+    _gpu()
+    lens, s, h, hk, d, block = [100, 37], 4, 8, 2, 128, 16
+    pool, _, _ = _pool(lens, hk, d, block, 11, fp8)
+    q = torch.randn(2, s, h, d, generator=torch.Generator().manual_seed(1)).bfloat16().to(DEV)
+    n = torch.tensor(lens, dtype=torch.int32, device=DEV)
+    op = csa.PagedAttention(q, pool["k"], pool["v"], n, table=pool["table"], block=block, win=win,
+                            k_scale=pool.get("k_scale"), v_scale=pool.get("v_scale"))
+    clean = {x: t.clone() for x, t in op().items()}
+    torch.cuda.synchronize()
+    for i, length in enumerate(lens):
+        for r in [length - 1] + ([length - s - win + 1] if win else []):
+            row = int(pool["table"][i, r // block]) * block + r % block
+            if fp8:
+                pool["k_scale"][row], pool["v_scale"][row] = float("nan"), float("inf")
+            else:
+                pool["k"][row], pool["v"][row] = float("nan"), float("inf")
+    got = op()
+    torch.cuda.synchronize()
+    sees = [3] + ([0] if win else [])
+    for t in range(s):
+        if t in sees:
+            assert torch.isnan(got["out"][:, t]).all() and torch.isnan(got["lse"][:, t]).all()
+        else:
+            assert torch.equal(got["out"][:, t], clean["out"][:, t]) and torch.equal(got["lse"][:, t], clean["lse"][:, t])
+
+
+@pytest.mark.gpu
+def test_bad_lengths_and_pages_are_reported_and_leave_the_others_alone():
+    _gpu()
+    lens, h, hk, d, block = [100, 300, 200, 50], 4, 2, 128, 16
+    pool, k, v = _pool(lens, hk, d, block, 5)
+    q = torch.randn(4, 1, h, d, generator=torch.Generator().manual_seed(1)).bfloat16()
+    want = _exact(q, k, v, lens, pool["table"].cpu(), block, 0, d ** -0.5)
+    status = torch.zeros(1, dtype=torch.int32, device=DEV)
+
+    def run(n, table):
+        status.zero_()
+        got = csa.PagedAttention(q.to(DEV), pool["k"], pool["v"], torch.tensor(n, dtype=torch.int32, device=DEV),
+                                 table=table, block=block, status=status, max_len=304)()
+        torch.cuda.synchronize()
+        return got, int(status.item())
+
+    got, st = run([100, 305, -1, 50], pool["table"])        # above max_len, negative
+    assert st == 1
+    assert (got["out"][1:3] == 0).all() and (got["lse"][1:3] == -math.inf).all()
+    keep = torch.tensor([0, 3])
+    _check({x: t.cpu()[keep] for x, t in got.items()}, tuple(t[keep] for t in want))
+    for bad in (-1, 1 << 20):                               # unmapped, outside the pool
+        t = pool["table"].clone()
+        t[1, 3] = bad
+        got, st = run(lens, t)
+        assert st == 1 and torch.isfinite(got["out"]).all()
+        keep = torch.tensor([0, 2, 3])
+        _check({x: y.cpu()[keep] for x, y in got.items()}, tuple(y[keep] for y in want))
+    got, st = run(lens, pool["table"])
+    assert st == 0
+    _check(got, want)
+
+
+@pytest.mark.gpu
+def test_a_graph_follows_the_lengths_and_repeats_bit_for_bit():
+    _gpu()
+    lens, h, hk, d, block = [4000, 100, 2500, 0], 8, 2, 128, 64
+    pool, k, v = _pool(lens, hk, d, block, 6)
+    q = torch.randn(4, 1, h, d, generator=torch.Generator().manual_seed(1)).bfloat16()
+    n = torch.tensor(lens, dtype=torch.int32, device=DEV)
+    op = csa.PagedAttention(q.to(DEV), pool["k"], pool["v"], n, table=pool["table"], block=block)
+    first = {x: t.clone() for x, t in op().items()}
+    for _ in range(10):
+        again = op()
+    torch.cuda.synchronize()
+    assert all(torch.equal(again[x], first[x]) for x in first)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        op()
+    for now in ([1, 100, 2500, 0], lens, [3999, 0, 1, 0]):
+        n.copy_(torch.tensor(now, dtype=torch.int32))
+        graph.replay()
+        torch.cuda.synchronize()
+        _check(op._out, _exact(q, k, v, now, pool["table"].cpu(), block, 0, d ** -0.5), now)
+    n.copy_(torch.tensor(lens, dtype=torch.int32))
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    other = csa.PagedAttention(q.to(DEV), pool["k"], pool["v"], n, table=pool["table"], block=block)
+    side.wait_stream(torch.cuda.current_stream())
+    other(stream=side)                                      # its own workspace: beside a call on this stream
+    op()
+    torch.cuda.synchronize()
+    assert all(torch.equal(other._out[x], first[x]) and torch.equal(op._out[x], first[x]) for x in first)
+
+
+@pytest.mark.gpu
+def test_rows_past_32_bit_offsets():
+    # a pool of more than 2^31 elements: the request's last blocks lie behind it
+    _gpu()
+    rows, hk, d, block = 2_200_000, 8, 128, 64
+    k = torch.zeros(rows, hk, d, dtype=torch.bfloat16, device=DEV)
+    v = torch.zeros(rows, hk, d, dtype=torch.bfloat16, device=DEV)
+    n = 300
+    last = rows // block - 1
+    table = torch.tensor([[last, 3, last - 7, 1, last - 1]], dtype=torch.int32)
+    g = torch.Generator().manual_seed(2)
+    r = torch.arange(n)
+    at = table[0].long()[r // block] * block + r % block
+    kk, vv = torch.randn(n, hk, d, generator=g).bfloat16(), torch.randn(n, hk, d, generator=g).bfloat16()
+    k[at.to(DEV)], v[at.to(DEV)] = kk.to(DEV), vv.to(DEV)
+    q = torch.randn(1, 1, 16, d, generator=g).bfloat16()
+    got = csa.PagedAttention(q.to(DEV), k, v, torch.tensor([n], dtype=torch.int32, device=DEV), table=table.to(DEV),
+                             block=block)()
+    torch.cuda.synchronize()
+    dense = torch.arange(5, dtype=torch.int32)[None]
+    pad = torch.zeros(20, hk, d).double()
+    _check(got, _exact(q, torch.cat([kk.double(), pad]), torch.cat([vv.double(), pad]), [n], dense, block, 0, d ** -0.5))
