@@ -45,15 +45,25 @@ struct MmShape {
   static constexpr int kTmemCols = kAccCols * kBufs;
   static constexpr int kStageBytes = kMmPBytes + NT * kMmBlock;
   static constexpr int kCtasPerSm = kSwap ? 2 : 1;
-  static constexpr int kStages = (kSwap ? 108 * 1024 : 200 * 1024) / kStageBytes;
-  static constexpr int kSmem = kStages * kStageBytes + 1024;
+  // !kSwap: a 4 KB patch per epilogue warp, through which the output leaves in
+  // whole 128-byte lines
+  static constexpr int kPatchBytes = kSwap ? 0 : kEpiWarps * 4096;
+  static constexpr int kStages = (kSwap ? 108 * 1024 : 225 * 1024 - kPatchBytes) / kStageBytes;
+  static constexpr int kSmem = kStages * kStageBytes + kPatchBytes + 1024;
+  // 256 columns: 128 fp32 sums per epilogue thread.  The launch has 168
+  // registers for each of the 384 threads; the four warps that only issue keep
+  // 40 and the eight epilogue warps take 232 (40 + 2 * 232 = 3 * 168).
+  static constexpr bool kMoveRegs = kCols > 64;
   // fp32 partials for the cluster's reduction, in the ring's memory
   static_assert(128 * NT * 4 <= kStages * kStageBytes, "partials exceed the ring");
+  static_assert(kSmem + 1024 <= 227 * 1024, "shared memory");
   static_assert(kStages <= kMmMaxStages && kTmemCols <= 512 / kCtasPerSm, "ring or TMEM");
 };
 
-struct MmSmem {
+template <bool kSwap>
+struct alignas(16) MmSmem {
   uint64_t full[kMmMaxStages], empty[kMmMaxStages], tfull[4], tempty[4];
+  float factor[kSwap ? 4 : 1][kSwap ? 2 : 1][kSwap ? 64 : 4];  // kSwap: per epilogue warp, the scales of a block's columns (two blocks)
   uint32_t tmem_base;
   int abort;
 };
@@ -95,25 +105,51 @@ __device__ __forceinline__ float to_out<float>(float v) { return v; }
 template <>
 __device__ __forceinline__ __nv_bfloat16 to_out<__nv_bfloat16>(float v) { return __float2bfloat16_rn(v); }
 
-// One column strip of a row: cnt consecutive elements of out.
-template <typename T, int CNT>
-__device__ __forceinline__ void store_strip(T* dst, const float* v, int64_t left, bool vec) {
+__device__ __forceinline__ void sts_u4(uint32_t a, uint4 v) {
+  asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};\n" ::"r"(a), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
+}
+__device__ __forceinline__ uint4 lds_u4(uint32_t a) {
+  uint4 v;
+  asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];\n" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a) : "memory");
+  return v;
+}
+
+// 32 rows (one per lane) x 128 bytes of output from registers to out: through
+// the warp's patch (16-byte chunks swizzled by the row, so that neither the
+// row-wise writes nor the line-wise reads conflict), then four rows' lines per
+// warp store.  rows / cols: how many of the patch exist.
+template <typename T>
+__device__ __forceinline__ void store_patch(uint32_t patch, const float* v, int lane, T* out, int64_t stride, int rows,
+                                            int cols, bool vec) {
   constexpr int E = 16 / (int)sizeof(T);
-  if (vec && left >= CNT) {
 #pragma unroll
-    for (int i = 0; i < CNT / E; ++i) {
-      T t[E];
+  for (int j = 0; j < 8; ++j) {
+    T t[E];
 #pragma unroll
-      for (int e = 0; e < E; ++e) t[e] = to_out<T>(v[i * E + e]);
-      uint4 r;
-      memcpy(&r, t, 16);
-      reinterpret_cast<uint4*>(dst)[i] = r;
-    }
-    return;
+    for (int e = 0; e < E; ++e) t[e] = to_out<T>(v[j * E + e]);
+    uint4 r;
+    memcpy(&r, t, 16);
+    sts_u4(patch + lane * 128 + ((j ^ (lane & 7)) * 16), r);
   }
+  __syncwarp();
 #pragma unroll
-  for (int i = 0; i < CNT; ++i)
-    if (i < left) dst[i] = to_out<T>(v[i]);
+  for (int i = 0; i < 8; ++i) {
+    const int r = i * 4 + lane / 8, j = lane % 8;
+    const uint4 x = lds_u4(patch + r * 128 + ((j ^ (r & 7)) * 16));
+    if (r < rows) {
+      T* dst = out + r * stride + j * E;
+      if (vec && (j + 1) * E <= cols) {
+        *reinterpret_cast<uint4*>(dst) = x;
+      } else {
+        T t[E];
+        memcpy(t, &x, 16);
+#pragma unroll
+        for (int e = 0; e < E; ++e)
+          if (j * E + e < cols) dst[e] = t[e];
+      }
+    }
+  }
+  __syncwarp();
 }
 
 template <int NT, bool kSwap, typename T>
@@ -122,7 +158,7 @@ __global__ void __launch_bounds__(MmShape<NT, kSwap>::kThreads, MmShape<NT, kSwa
               const MmArgs g, int split, int ptiles, int qtiles) {
   using Sh = MmShape<NT, kSwap>;
   extern __shared__ __align__(16) uint8_t smem_raw[];
-  __shared__ MmSmem sm;
+  __shared__ MmSmem<kSwap> sm;
   const uint32_t base = (smem_u32(smem_raw) + 1023u) & ~1023u;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int KB = (g.K + kMmBlock - 1) / kMmBlock;
@@ -163,8 +199,9 @@ __global__ void __launch_bounds__(MmShape<NT, kSwap>::kThreads, MmShape<NT, kSwa
   auto p_of = [&](int t) { return t % ptiles; };
   auto q_of = [&](int t) { return t / ptiles; };
 
-  if (warp == 0) {
-    if (lane == 0) {
+  if (warp < 4) {
+    if constexpr (Sh::kMoveRegs) asm volatile("setmaxnreg.dec.sync.aligned.u32 40;\n");
+    if (warp == 0 && lane == 0) {
       int st = 0, n = 0;
       uint32_t ph = 0;
       for (int t = first; t < tiles && !*abort; t += step)
@@ -180,9 +217,7 @@ __global__ void __launch_bounds__(MmShape<NT, kSwap>::kThreads, MmShape<NT, kSwa
       // copies still in flight land before the block exits
       for (int k = n > Sh::kStages ? n - Sh::kStages : 0; k < n; ++k)
         tc5::mbar_wait_drain(smem_u32(&sm.full[k % Sh::kStages]), (k / Sh::kStages) & 1);
-    }
-  } else if (warp == 1) {
-    if (lane == 0) {
+    } else if (warp == 1 && lane == 0) {
       int st = 0, buf = 0, n = 0;
       uint32_t ph = 0, bph = 0;
       const uint32_t idesc = tc5::idesc_e4m3_f32(128, NT);
@@ -206,7 +241,8 @@ __global__ void __launch_bounds__(MmShape<NT, kSwap>::kThreads, MmShape<NT, kSwa
       for (int k = n > Sh::kBufs ? n - Sh::kBufs : 0; k < n; ++k)
         tc5::mbar_wait_drain(smem_u32(&sm.tfull[k % Sh::kBufs]), (k / Sh::kBufs) & 1);
     }
-  } else if (warp >= 4) {
+  } else {
+    if constexpr (Sh::kMoveRegs) asm volatile("setmaxnreg.inc.sync.aligned.u32 232;\n");
     const int ew = warp - 4, quarter = ew & 3, group = ew >> 2;
     const int row = quarter * 32 + lane;                 // TMEM lane: row of the P tile
     const uint32_t tcol = tmem + ((uint32_t)(quarter * 32) << 16) + group * Sh::kCols;
@@ -218,33 +254,48 @@ __global__ void __launch_bounds__(MmShape<NT, kSwap>::kThreads, MmShape<NT, kSwa
 #pragma unroll
       for (int i = 0; i < Sh::kCols / 2; ++i) acc[i] = 0;
       bool ok = true;
-      for (int kb = kb0; kb < kb1; ++kb) {
-        // scales of the block: !kSwap one factor per thread, kSwap one per column
-        float f = 0.f;
-        if (!kSwap) {
-          if (p0 + row < g.M && q0 < g.N)
-            f = __ldg(g.a_scale + (p0 + row) * g.a_scale_stride + kb) *
-                __ldg(g.b_scale + (q0 / 128) * g.b_scale_stride + kb);
-        } else {
-          f = __ldg(g.b_scale + (p0 / 128) * g.b_scale_stride + kb);
+      // scales: !kSwap one factor per thread, kSwap one per column (lane l
+      // fetches columns l and l + 32, the warp shares them through shared
+      // memory); fetched one block ahead
+      constexpr int kFetch = kSwap ? (NT + 31) / 32 : 1;
+      float ahead[kFetch], ahead_b = 0.f;
+      auto fetch = [&](int kb) {
+        const int64_t nb = (kSwap ? p0 : q0) / 128;
+        ahead_b = nb * 128 < g.N ? __ldg(g.b_scale + nb * g.b_scale_stride + kb) : 0.f;
+#pragma unroll
+        for (int i = 0; i < kFetch; ++i) {
+          const int64_t m = kSwap ? q0 + i * 32 + lane : p0 + row;
+          ahead[i] = m < g.M && (!kSwap || i * 32 + lane < NT) ? __ldg(g.a_scale + m * g.a_scale_stride + kb) : 0.f;
         }
+      };
+      fetch(kb0);
+      for (int kb = kb0; kb < kb1; ++kb) {
+        const float f = ahead[0] * ahead_b;
+        float* factor = sm.factor[kSwap ? quarter : 0][kSwap ? kb & 1 : 0];
+        if (kSwap) {
+#pragma unroll
+          for (int i = 0; i < kFetch; ++i)
+            if (i * 32 + lane < NT) factor[i * 32 + lane] = ahead[i] * ahead_b;
+        }
+        if (kb + 1 < kb1) fetch(kb + 1);
+        if (kSwap) __syncwarp();
         if (!tc5::mbar_wait(smem_u32(&sm.tfull[buf]), bph, abort)) { ok = false; break; }
         tc5::fence_after_sync();
+        const uint64_t f2 = pack2(f, f);
 #pragma unroll
         for (int c = 0; c < Sh::kCols; c += 32) {
           float v[32];
           tc5::tmem_ld32(tcol + buf * Sh::kAccCols + c, v);
 #pragma unroll
-          for (int i = 0; i < 32 && c + i < Sh::kCols; i += 2) {
-            uint64_t s;
+          for (int i = 0; i < 32 && c + i < Sh::kCols; i += 4) {
             if (kSwap) {
-              const float s0 = q0 + c + i < g.M ? __ldg(g.a_scale + (q0 + c + i) * g.a_scale_stride + kb) : 0.f;
-              const float s1 = q0 + c + i + 1 < g.M ? __ldg(g.a_scale + (q0 + c + i + 1) * g.a_scale_stride + kb) : 0.f;
-              s = pack2(s0 * f, s1 * f);
+              const float4 s = *reinterpret_cast<const float4*>(factor + c + i);
+              fma2(acc[(c + i) / 2], pack2(v[i], v[i + 1]), pack2(s.x, s.y));
+              fma2(acc[(c + i) / 2 + 1], pack2(v[i + 2], v[i + 3]), pack2(s.z, s.w));
             } else {
-              s = pack2(f, f);
+              fma2(acc[(c + i) / 2], pack2(v[i], v[i + 1]), f2);
+              fma2(acc[(c + i) / 2 + 1], pack2(v[i + 2], v[i + 3]), f2);
             }
-            fma2(acc[(c + i) / 2], pack2(v[i], v[i + 1]), s);
           }
         }
         tc5::fence_before_sync();
@@ -269,11 +320,18 @@ __global__ void __launch_bounds__(MmShape<NT, kSwap>::kThreads, MmShape<NT, kSwa
           for (int i = 0; i < Sh::kCols; ++i)
             if (q0 + i < g.M) static_cast<T*>(g.out)[(q0 + i) * g.out_stride + p0 + row] = to_out<T>(v[i]);
         }
-      } else if (p0 + row < g.M) {
-        T* dst = static_cast<T*>(g.out) + (p0 + row) * g.out_stride + q0;
+      } else {
+        constexpr int kStep = 128 / (int)sizeof(T);   // columns per 128-byte line
+        const uint32_t patch = base + Sh::kStages * Sh::kStageBytes + ew * 4096;
+        const int64_t m0 = p0 + quarter * 32;
+        const int rows = (int)(g.M - m0 < 32 ? g.M - m0 : 32);
 #pragma unroll
-        for (int c = 0; c < Sh::kCols; c += 32)
-          if (q0 + c < g.N) store_strip<T, 32>(dst + c, v + c, g.N - q0 - c, g.vec);
+        for (int c = 0; c < Sh::kCols; c += kStep) {
+          const int64_t left = g.N - q0 - c;
+          if (rows > 0 && left > 0)
+            store_patch<T>(patch, v + c, lane, static_cast<T*>(g.out) + m0 * g.out_stride + q0 + c, g.out_stride, rows,
+                           (int)(left < kStep ? left : kStep), g.vec);
+        }
       }
     }
   }
@@ -365,7 +423,9 @@ int launch_out(const MmArgs& g, int num_sms, cudaStream_t st, bool pdl) {
   if (g.M <= 16) return launch_shape<16, true, T>(g, num_sms, st, pdl);
   if (g.M <= 32) return launch_shape<32, true, T>(g, num_sms, st, pdl);
   if (g.M <= 64) return launch_shape<64, true, T>(g, num_sms, st, pdl);
-  return launch_shape<128, false, T>(g, num_sms, st, pdl);
+  // 256 columns per tile halve the reads of a, 128 keep more SMs busy
+  const int64_t tiles = (int64_t)((g.M + 127) / 128) * ((g.N + 255) / 256);
+  return tiles >= num_sms ? launch_shape<256, false, T>(g, num_sms, st, pdl) : launch_shape<128, false, T>(g, num_sms, st, pdl);
 }
 
 }  // namespace
