@@ -37,23 +37,23 @@ constexpr int kMmMaxStages = 12;
 
 template <int NT, bool kSwap>
 struct MmShape {
-  static constexpr int kEpiWarps = kSwap ? 4 : 8;
+  // 64 sums per epilogue thread at most; with 256 columns sixteen warps, four
+  // per scheduler, hide each other's TMEM reads
+  static constexpr int kEpiWarps = kSwap ? 4 : NT == 256 ? 16 : 8;
   static constexpr int kThreads = 128 + 32 * kEpiWarps;
   static constexpr int kCols = NT / (kEpiWarps / 4);       // columns per epilogue thread
+  static constexpr int kChunk = kSwap || NT == 256 ? 16 : 32;  // columns per TMEM read
   static constexpr int kAccCols = NT < 32 ? 32 : NT;       // TMEM columns per buffer
   static constexpr int kBufs = kSwap ? 4 : 2;
   static constexpr int kTmemCols = kAccCols * kBufs;
   static constexpr int kStageBytes = kMmPBytes + NT * kMmBlock;
   static constexpr int kCtasPerSm = kSwap ? 2 : 1;
-  // !kSwap: a 4 KB patch per epilogue warp, through which the output leaves in
-  // whole 128-byte lines
-  static constexpr int kPatchBytes = kSwap ? 0 : kEpiWarps * 4096;
+  // !kSwap: a patch per epilogue warp, through which the output leaves in
+  // 64- or 128-byte pieces of a row
+  static constexpr int kLine = NT == 256 ? 64 : 128;
+  static constexpr int kPatchBytes = kSwap ? 0 : kEpiWarps * 32 * kLine;
   static constexpr int kStages = (kSwap ? 108 * 1024 : 225 * 1024 - kPatchBytes) / kStageBytes;
   static constexpr int kSmem = kStages * kStageBytes + kPatchBytes + 1024;
-  // 256 columns: 128 fp32 sums per epilogue thread.  The launch has 168
-  // registers for each of the 384 threads; the four warps that only issue keep
-  // 40 and the eight epilogue warps take 232 (40 + 2 * 232 = 3 * 168).
-  static constexpr bool kMoveRegs = kCols > 64;
   // fp32 partials for the cluster's reduction, in the ring's memory
   static_assert(128 * NT * 4 <= kStages * kStageBytes, "partials exceed the ring");
   static_assert(kSmem + 1024 <= 227 * 1024, "shared memory");
@@ -98,6 +98,40 @@ __device__ __forceinline__ void unpack2(uint64_t v, float& lo, float& hi) {
   asm("mov.b64 {%0, %1}, %2;\n" : "=f"(lo), "=f"(hi) : "l"(v));
 }
 
+// 16 or 32 columns of the warp's TMEM lanes, asked for and (tmem_arrive) waited
+// for apart, so that the sums of one chunk run while the next is on its way.
+template <int N>
+__device__ __forceinline__ void tmem_ask(uint32_t taddr, uint32_t* r) {
+  if constexpr (N == 32)
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,"
+        "%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];\n"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+          "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]),
+          "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
+          "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+        : "r"(taddr)
+        : "memory");
+  else
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];\n"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+          "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+        : "r"(taddr)
+        : "memory");
+}
+template <int N>
+__device__ __forceinline__ void tmem_arrive(uint32_t* r) {
+  if constexpr (N == 32)
+    tc5::tmem_wait_ld(r);
+  else
+    asm volatile("tcgen05.wait::ld.sync.aligned;\n"
+                 : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]),
+                   "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15])
+                 :
+                 : "memory");
+}
+
 template <typename T>
 __device__ __forceinline__ T to_out(float v);
 template <>
@@ -114,28 +148,29 @@ __device__ __forceinline__ uint4 lds_u4(uint32_t a) {
   return v;
 }
 
-// 32 rows (one per lane) x 128 bytes of output from registers to out: through
+// 32 rows (one per lane) x kLine bytes of output from registers to out: through
 // the warp's patch (16-byte chunks swizzled by the row, so that neither the
-// row-wise writes nor the line-wise reads conflict), then four rows' lines per
-// warp store.  rows / cols: how many of the patch exist.
-template <typename T>
+// row-wise writes nor the line-wise reads conflict), then whole lines of
+// several rows per warp store.  rows / cols: how many of the patch exist.
+template <typename T, int kLine>
 __device__ __forceinline__ void store_patch(uint32_t patch, const float* v, int lane, T* out, int64_t stride, int rows,
                                             int cols, bool vec) {
-  constexpr int E = 16 / (int)sizeof(T);
+  constexpr int E = 16 / (int)sizeof(T), C = kLine / 16;
+  auto at = [&](int r, int j) { return patch + r * kLine + ((j ^ ((C == 8 ? r : r >> 1) & (C - 1))) * 16); };
 #pragma unroll
-  for (int j = 0; j < 8; ++j) {
+  for (int j = 0; j < C; ++j) {
     T t[E];
 #pragma unroll
     for (int e = 0; e < E; ++e) t[e] = to_out<T>(v[j * E + e]);
     uint4 r;
     memcpy(&r, t, 16);
-    sts_u4(patch + lane * 128 + ((j ^ (lane & 7)) * 16), r);
+    sts_u4(at(lane, j), r);
   }
   __syncwarp();
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const int r = i * 4 + lane / 8, j = lane % 8;
-    const uint4 x = lds_u4(patch + r * 128 + ((j ^ (r & 7)) * 16));
+  for (int i = 0; i < C; ++i) {
+    const int r = i * (32 / C) + lane / C, j = lane % C;
+    const uint4 x = lds_u4(at(r, j));
     if (r < rows) {
       T* dst = out + r * stride + j * E;
       if (vec && (j + 1) * E <= cols) {
@@ -200,7 +235,6 @@ __global__ void __launch_bounds__(MmShape<NT, kSwap>::kThreads, MmShape<NT, kSwa
   auto q_of = [&](int t) { return t / ptiles; };
 
   if (warp < 4) {
-    if constexpr (Sh::kMoveRegs) asm volatile("setmaxnreg.dec.sync.aligned.u32 40;\n");
     if (warp == 0 && lane == 0) {
       int st = 0, n = 0;
       uint32_t ph = 0;
@@ -242,7 +276,6 @@ __global__ void __launch_bounds__(MmShape<NT, kSwap>::kThreads, MmShape<NT, kSwa
         tc5::mbar_wait_drain(smem_u32(&sm.tfull[k % Sh::kBufs]), (k / Sh::kBufs) & 1);
     }
   } else {
-    if constexpr (Sh::kMoveRegs) asm volatile("setmaxnreg.inc.sync.aligned.u32 232;\n");
     const int ew = warp - 4, quarter = ew & 3, group = ew >> 2;
     const int row = quarter * 32 + lane;                 // TMEM lane: row of the P tile
     const uint32_t tcol = tmem + ((uint32_t)(quarter * 32) << 16) + group * Sh::kCols;
@@ -282,25 +315,32 @@ __global__ void __launch_bounds__(MmShape<NT, kSwap>::kThreads, MmShape<NT, kSwa
         if (!tc5::mbar_wait(smem_u32(&sm.tfull[buf]), bph, abort)) { ok = false; break; }
         tc5::fence_after_sync();
         const uint64_t f2 = pack2(f, f);
+        constexpr int kChunk = Sh::kChunk, kParts = Sh::kCols / kChunk;
+        const uint32_t t0 = tcol + buf * Sh::kAccCols;
 #pragma unroll
-        for (int c = 0; c < Sh::kCols; c += 32) {
-          float v[32];
-          tc5::tmem_ld32(tcol + buf * Sh::kAccCols + c, v);
+        for (int x = 0; x < kParts; ++x) {
+          uint32_t v[kChunk];
+          tmem_ask<kChunk>(t0 + x * kChunk, v);
+          tmem_arrive<kChunk>(v);
+          if (x + 1 == kParts) {  // the buffer is read: the next block's MMAs may have it
+            tc5::fence_before_sync();
+            __syncwarp();
+            if (lane == 0) tc5::mbar_arrive(smem_u32(&sm.tempty[buf]));
+          }
 #pragma unroll
-          for (int i = 0; i < 32 && c + i < Sh::kCols; i += 4) {
+          for (int i = 0; i < kChunk; i += 4) {
+            const uint32_t* r = v + i;
+            const int at = (x * kChunk + i) / 2;
+            uint64_t s01 = f2, s23 = f2;
             if (kSwap) {
-              const float4 s = *reinterpret_cast<const float4*>(factor + c + i);
-              fma2(acc[(c + i) / 2], pack2(v[i], v[i + 1]), pack2(s.x, s.y));
-              fma2(acc[(c + i) / 2 + 1], pack2(v[i + 2], v[i + 3]), pack2(s.z, s.w));
-            } else {
-              fma2(acc[(c + i) / 2], pack2(v[i], v[i + 1]), f2);
-              fma2(acc[(c + i) / 2 + 1], pack2(v[i + 2], v[i + 3]), f2);
+              const float4 s = *reinterpret_cast<const float4*>(factor + x * kChunk + i);
+              s01 = pack2(s.x, s.y);
+              s23 = pack2(s.z, s.w);
             }
+            fma2(acc[at], pack2(__uint_as_float(r[0]), __uint_as_float(r[1])), s01);
+            fma2(acc[at + 1], pack2(__uint_as_float(r[2]), __uint_as_float(r[3])), s23);
           }
         }
-        tc5::fence_before_sync();
-        __syncwarp();
-        if (lane == 0) tc5::mbar_arrive(smem_u32(&sm.tempty[buf]));
         if (++buf == Sh::kBufs) buf = 0, bph ^= 1u;
       }
       if (!ok) break;
@@ -321,15 +361,15 @@ __global__ void __launch_bounds__(MmShape<NT, kSwap>::kThreads, MmShape<NT, kSwa
             if (q0 + i < g.M) static_cast<T*>(g.out)[(q0 + i) * g.out_stride + p0 + row] = to_out<T>(v[i]);
         }
       } else {
-        constexpr int kStep = 128 / (int)sizeof(T);   // columns per 128-byte line
-        const uint32_t patch = base + Sh::kStages * Sh::kStageBytes + ew * 4096;
+        constexpr int kStep = Sh::kLine / (int)sizeof(T);   // columns per patch
+        const uint32_t patch = base + Sh::kStages * Sh::kStageBytes + ew * 32 * Sh::kLine;
         const int64_t m0 = p0 + quarter * 32;
         const int rows = (int)(g.M - m0 < 32 ? g.M - m0 : 32);
 #pragma unroll
         for (int c = 0; c < Sh::kCols; c += kStep) {
           const int64_t left = g.N - q0 - c;
           if (rows > 0 && left > 0)
-            store_patch<T>(patch, v + c, lane, static_cast<T*>(g.out) + m0 * g.out_stride + q0 + c, g.out_stride, rows,
+            store_patch<T, Sh::kLine>(patch, v + c, lane, static_cast<T*>(g.out) + m0 * g.out_stride + q0 + c, g.out_stride, rows,
                            (int)(left < kStep ? left : kStep), g.vec);
         }
       }
