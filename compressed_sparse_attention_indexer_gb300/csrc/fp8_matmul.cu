@@ -54,8 +54,12 @@ struct MmShape {
   static constexpr int kPatchBytes = kSwap ? 0 : kEpiWarps * 32 * kLine;
   static constexpr int kStages = (kSwap ? 108 * 1024 : 225 * 1024 - kPatchBytes) / kStageBytes;
   static constexpr int kSmem = kStages * kStageBytes + kPatchBytes + 1024;
-  // fp32 partials for the cluster's reduction, in the ring's memory
-  static_assert(128 * NT * 4 <= kStages * kStageBytes, "partials exceed the ring");
+  // fp32 sums of the tile in the ring's memory, laid out like the output: rows
+  // of kSumCols neighbouring columns of out, the pitch chosen so that neither
+  // the writes nor the reads conflict
+  static constexpr int kSumRows = kSwap ? NT : 128, kSumCols = kSwap ? 128 : NT;
+  static constexpr int kPitch = kSumCols * 4 + (kSwap ? 0 : 16);
+  static_assert(kSumRows * kPitch <= kStages * kStageBytes, "sums exceed the ring");
   static_assert(kSmem + 1024 <= 227 * 1024, "shared memory");
   static_assert(kStages <= kMmMaxStages && kTmemCols <= 512 / kCtasPerSm, "ring or TMEM");
 };
@@ -76,13 +80,18 @@ __device__ __forceinline__ uint32_t cluster_rank() {
 __device__ __forceinline__ void cluster_sync() {
   asm volatile("barrier.cluster.arrive.release.aligned;\nbarrier.cluster.wait.acquire.aligned;\n" ::: "memory");
 }
-__device__ __forceinline__ float ld_cluster_f32(uint32_t saddr, uint32_t rank) {
-  float v;
-  asm volatile(
-      "{\n .reg .b32 a;\n mapa.shared::cluster.u32 a, %1, %2;\n ld.shared::cluster.f32 %0, [a];\n}\n"
-      : "=f"(v)
-      : "r"(saddr), "r"(rank)
-      : "memory");
+// The same shared-memory address in the cluster's CTA `rank`, and a load from it.
+__device__ __forceinline__ uint32_t cluster_addr(uint32_t saddr, uint32_t rank) {
+  uint32_t a;
+  asm("mapa.shared::cluster.u32 %0, %1, %2;\n" : "=r"(a) : "r"(saddr), "r"(rank));
+  return a;
+}
+__device__ __forceinline__ float4 ld_cluster_f4(uint32_t addr) {
+  float4 v;
+  asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];\n"
+               : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+               : "r"(addr)
+               : "memory");
   return v;
 }
 // d += a * b on two packed fp32 values.
@@ -200,7 +209,7 @@ __global__ void __launch_bounds__(MmShape<NT, kSwap>::kThreads, MmShape<NT, kSwa
   const int rank = split > 1 ? (int)cluster_rank() : 0;
   const int kb0 = (int)((int64_t)rank * KB / split), kb1 = (int)((int64_t)(rank + 1) * KB / split);
   const int tiles = ptiles * qtiles;
-  const int first = blockIdx.x / split, step = gridDim.x / split;  // split > 1: one tile per cluster
+  const int first = blockIdx.x / split, step = gridDim.x / split;
   if (threadIdx.x == 0) {
     for (int i = 0; i < Sh::kStages; ++i) {
       tc5::mbar_init(smem_u32(&sm.full[i]), 1);
@@ -347,18 +356,19 @@ __global__ void __launch_bounds__(MmShape<NT, kSwap>::kThreads, MmShape<NT, kSwa
       float v[Sh::kCols];
 #pragma unroll
       for (int i = 0; i < Sh::kCols / 2; ++i) unpack2(acc[i], v[2 * i], v[2 * i + 1]);
-      if (split > 1) {
-        // [column][lane] partials in the ring, which every copy and MMA of this
-        // CTA's only tile has left
-        const uint32_t part = base + (uint32_t)((group * Sh::kCols * 128 + row) * 4);
-#pragma unroll
-        for (int i = 0; i < Sh::kCols; ++i)
-          asm volatile("st.shared.f32 [%0], %1;\n" ::"r"(part + i * 512), "f"(v[i]) : "memory");
-      } else if (kSwap) {
-        if (p0 + row < g.N) {
+      if (kSwap || split > 1) {
+        // into the ring, which every copy and MMA of this CTA's only tile has left
+        if (kSwap) {
+          const uint32_t at = base + row * 4;
 #pragma unroll
           for (int i = 0; i < Sh::kCols; ++i)
-            if (q0 + i < g.M) static_cast<T*>(g.out)[(q0 + i) * g.out_stride + p0 + row] = to_out<T>(v[i]);
+            asm volatile("st.shared.f32 [%0], %1;\n" ::"r"(at + i * Sh::kPitch), "f"(v[i]) : "memory");
+        } else {
+          const uint32_t at = base + row * Sh::kPitch + group * Sh::kCols * 4;
+#pragma unroll
+          for (int i = 0; i < Sh::kCols; i += 4)
+            sts_u4(at + i * 4, make_uint4(__float_as_uint(v[i]), __float_as_uint(v[i + 1]), __float_as_uint(v[i + 2]),
+                                          __float_as_uint(v[i + 3])));
         }
       } else {
         constexpr int kStep = Sh::kLine / (int)sizeof(T);   // columns per patch
@@ -375,24 +385,55 @@ __global__ void __launch_bounds__(MmShape<NT, kSwap>::kThreads, MmShape<NT, kSwa
       }
     }
   }
-  if (split > 1) {
+  if (kSwap || split > 1) {
+    // one tile per cluster: its sums, added over the ranks in order, leave in
+    // pieces of four neighbouring columns, an equal share from each rank
     __syncwarp();
-    cluster_sync();
-    const int t = first;
-    if (warp >= 4 && t < tiles) {
-      // columns c0 .. c1 of the tile, summed over the ranks in order
-      const int c0 = rank * NT / split, c1 = (rank + 1) * NT / split;
-      const int ew = warp - 4, quarter = ew & 3, group = ew >> 2;
-      const int64_t p = (int64_t)p_of(t) * 128 + quarter * 32 + lane, q0 = (int64_t)q_of(t) * NT;
-      const uint32_t part = base + (uint32_t)((quarter * 32 + lane) * 4);
-      for (int c = c0 + group; c < c1; c += Sh::kEpiWarps / 4) {
-        float v = 0.f;
-        for (int r = 0; r < split; ++r) v += ld_cluster_f32(part + c * 512, (uint32_t)r);
-        const int64_t m = kSwap ? q0 + c : p, n = kSwap ? p : q0 + c;
-        if (m < g.M && n < g.N) static_cast<T*>(g.out)[m * g.out_stride + n] = to_out<T>(v);
+    if (split > 1)
+      cluster_sync();
+    else
+      __syncthreads();
+    const int64_t p0 = (int64_t)p_of(first) * 128, q0 = (int64_t)q_of(first) * NT;
+    const int64_t m0 = kSwap ? q0 : p0, n0 = kSwap ? p0 : q0;
+    const int rows = (int)(g.M - m0 < Sh::kSumRows ? g.M - m0 : Sh::kSumRows);
+    constexpr int kQuads = Sh::kSumCols / 4;
+    const int all = rows * kQuads, i1 = (rank + 1) * all / split;
+    for (int i = rank * all / split + threadIdx.x; i < i1; i += Sh::kThreads) {
+      const int r = i / kQuads, c = (i - r * kQuads) * 4;
+      const uint32_t at = base + r * Sh::kPitch + c * 4;
+      float4 t[8];
+#pragma unroll
+      for (int x = 0; x < 8; ++x)
+        if (x < split) t[x] = ld_cluster_f4(split > 1 ? cluster_addr(at, x) : at);
+      float v[4] = {t[0].x, t[0].y, t[0].z, t[0].w};
+#pragma unroll
+      for (int x = 1; x < 8; ++x)
+        if (x < split) v[0] += t[x].x, v[1] += t[x].y, v[2] += t[x].z, v[3] += t[x].w;
+      const int64_t n = n0 + c;
+      T* dst = static_cast<T*>(g.out) + (m0 + r) * g.out_stride + n;
+      T o[4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) o[e] = to_out<T>(v[e]);
+      if (g.vec && n + 4 <= g.N) {
+        if constexpr (sizeof(T) == 2) {
+          uint2 x;
+          memcpy(&x, o, 8);
+          *reinterpret_cast<uint2*>(dst) = x;
+        } else {
+          uint4 x;
+          memcpy(&x, o, 16);
+          *reinterpret_cast<uint4*>(dst) = x;
+        }
+      } else {
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          if (n + e < g.N) dst[e] = o[e];
       }
     }
-    cluster_sync();  // no CTA leaves while another reads its partials
+    if (split > 1) {
+      __syncwarp();
+      cluster_sync();  // no CTA leaves while another reads its sums
+    }
   }
   tc5::fence_before_sync();
   __syncthreads();
@@ -428,15 +469,16 @@ int launch_shape(const MmArgs& g, int num_sms, cudaStream_t st, bool pdl) {
     return launch_fail("cudaFuncSetAttribute(mm_kernel)", e);
   const int ptiles = (int)(((kSwap ? g.N : g.M) + 127) / 128), qtiles = (int)(((kSwap ? g.M : g.N) + NT - 1) / NT);
   const int64_t tiles = (int64_t)ptiles * qtiles;
-  if (tiles > 0x7fffffff) return launch_fail("too many tiles", cudaSuccess);
+  if (tiles > 0x7fffffff / 8) return launch_fail("too many tiles", cudaSuccess);
   const int slots = num_sms * Sh::kCtasPerSm;
   const int KB = (g.K + kMmBlock - 1) / kMmBlock;
   // a tile's blocks over the CTAs of a cluster while that still adds CTAs
   int split = 1;
   while (split < 8 && tiles * split * 2 <= slots && KB >= split * 2 * 2) split *= 2;
-  int grid = split > 1 ? (int)tiles * split : (int)(tiles < slots ? tiles : slots);
+  // kSwap and split tiles leave through the ring's memory: one tile per cluster
+  const int64_t grid = kSwap || split > 1 ? tiles * split : (tiles < slots ? tiles : slots);
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(grid);
+  cfg.gridDim = dim3((unsigned)grid);
   cfg.blockDim = dim3(Sh::kThreads);
   cfg.dynamicSmemBytes = Sh::kSmem;
   cfg.stream = st;
