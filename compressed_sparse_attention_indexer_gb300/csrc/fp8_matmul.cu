@@ -196,6 +196,58 @@ __device__ __forceinline__ void store_patch(uint32_t patch, const float* v, int 
   __syncwarp();
 }
 
+// This rank's share of a cluster's tile: the kSplit CTAs' sums of four
+// neighbouring columns added in rank order and written to out.  Every load of
+// a thread is asked for before the first is used.
+template <typename Sh, typename T, int kSplit>
+__device__ __forceinline__ void add_sums(uint32_t base, int rank, int rows, int64_t left, T* out, int64_t stride, bool vec) {
+  constexpr int kQuads = Sh::kSumCols / 4;
+  constexpr int kEach = (Sh::kSumRows * kQuads / kSplit + Sh::kThreads - 1) / Sh::kThreads;
+  constexpr int kStep = kEach * kSplit <= 8 ? kEach : 8 / kSplit;   // pieces in flight per thread
+  const int all = rows * kQuads, i0 = rank * all / kSplit, i1 = (rank + 1) * all / kSplit;
+  uint32_t from[kSplit];
+#pragma unroll
+  for (int x = 0; x < kSplit; ++x) from[x] = kSplit > 1 ? cluster_addr(base, x) : base;
+  for (int first = i0 + threadIdx.x; first < i1; first += kStep * Sh::kThreads) {
+    float4 t[kStep][kSplit];
+#pragma unroll
+    for (int j = 0; j < kStep; ++j) {
+      const int i = first + j * Sh::kThreads, r = i / kQuads, c = i % kQuads;
+      if (i < i1) {
+#pragma unroll
+        for (int x = 0; x < kSplit; ++x) t[j][x] = ld_cluster_f4(from[x] + r * Sh::kPitch + c * 16);
+      }
+    }
+#pragma unroll
+    for (int j = 0; j < kStep; ++j) {
+      const int i = first + j * Sh::kThreads, r = i / kQuads, n = (i % kQuads) * 4;
+      if (i >= i1) continue;
+      float v[4] = {t[j][0].x, t[j][0].y, t[j][0].z, t[j][0].w};
+#pragma unroll
+      for (int x = 1; x < kSplit; ++x) v[0] += t[j][x].x, v[1] += t[j][x].y, v[2] += t[j][x].z, v[3] += t[j][x].w;
+      T* dst = out + r * stride + n;
+      T o[4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) o[e] = to_out<T>(v[e]);
+      if (vec && n + 4 <= left) {
+        if constexpr (sizeof(T) == 2) {
+          uint2 x;
+          memcpy(&x, o, 8);
+          *reinterpret_cast<uint2*>(dst) = x;
+        } else {
+          uint4 x;
+          memcpy(&x, o, 16);
+          *reinterpret_cast<uint4*>(dst) = x;
+        }
+      } else {
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          if (n + e < left) dst[e] = o[e];
+      }
+    }
+  }
+}
+
 template <int NT, bool kSwap, typename T>
 __global__ void __launch_bounds__(MmShape<NT, kSwap>::kThreads, MmShape<NT, kSwap>::kCtasPerSm)
     mm_kernel(const __grid_constant__ CUtensorMap pmap, const __grid_constant__ CUtensorMap qmap,
@@ -396,39 +448,13 @@ __global__ void __launch_bounds__(MmShape<NT, kSwap>::kThreads, MmShape<NT, kSwa
     const int64_t p0 = (int64_t)p_of(first) * 128, q0 = (int64_t)q_of(first) * NT;
     const int64_t m0 = kSwap ? q0 : p0, n0 = kSwap ? p0 : q0;
     const int rows = (int)(g.M - m0 < Sh::kSumRows ? g.M - m0 : Sh::kSumRows);
-    constexpr int kQuads = Sh::kSumCols / 4;
-    const int all = rows * kQuads, i1 = (rank + 1) * all / split;
-    for (int i = rank * all / split + threadIdx.x; i < i1; i += Sh::kThreads) {
-      const int r = i / kQuads, c = (i - r * kQuads) * 4;
-      const uint32_t at = base + r * Sh::kPitch + c * 4;
-      float4 t[8];
-#pragma unroll
-      for (int x = 0; x < 8; ++x)
-        if (x < split) t[x] = ld_cluster_f4(split > 1 ? cluster_addr(at, x) : at);
-      float v[4] = {t[0].x, t[0].y, t[0].z, t[0].w};
-#pragma unroll
-      for (int x = 1; x < 8; ++x)
-        if (x < split) v[0] += t[x].x, v[1] += t[x].y, v[2] += t[x].z, v[3] += t[x].w;
-      const int64_t n = n0 + c;
-      T* dst = static_cast<T*>(g.out) + (m0 + r) * g.out_stride + n;
-      T o[4];
-#pragma unroll
-      for (int e = 0; e < 4; ++e) o[e] = to_out<T>(v[e]);
-      if (g.vec && n + 4 <= g.N) {
-        if constexpr (sizeof(T) == 2) {
-          uint2 x;
-          memcpy(&x, o, 8);
-          *reinterpret_cast<uint2*>(dst) = x;
-        } else {
-          uint4 x;
-          memcpy(&x, o, 16);
-          *reinterpret_cast<uint4*>(dst) = x;
-        }
-      } else {
-#pragma unroll
-        for (int e = 0; e < 4; ++e)
-          if (n + e < g.N) dst[e] = o[e];
-      }
+    const int64_t left = g.N - n0;
+    T* out = static_cast<T*>(g.out) + m0 * g.out_stride + n0;
+    switch (split) {
+      case 1: add_sums<Sh, T, 1>(base, rank, rows, left, out, g.out_stride, g.vec); break;
+      case 2: add_sums<Sh, T, 2>(base, rank, rows, left, out, g.out_stride, g.vec); break;
+      case 4: add_sums<Sh, T, 4>(base, rank, rows, left, out, g.out_stride, g.vec); break;
+      default: add_sums<Sh, T, 8>(base, rank, rows, left, out, g.out_stride, g.vec); break;
     }
     if (split > 1) {
       __syncwarp();
