@@ -35,8 +35,9 @@ constexpr int kMmBlock = 128;                 // codes per scale, bytes per stag
 constexpr int kMmPBytes = 128 * kMmBlock;     // P tile: 128 rows
 constexpr int kMmMaxStages = 12;
 
-template <int NT, bool kSwap>
+template <int NT, bool kSwap, bool kPair>
 struct MmShape {
+  static constexpr int kQRows = kPair ? NT / 2 : NT;       // rows of the Q tile in this CTA's shared memory
   // 64 sums per epilogue thread at most; with 256 columns sixteen warps, four
   // per scheduler, hide each other's TMEM reads
   static constexpr int kEpiWarps = kSwap ? 4 : NT == 256 ? 16 : 8;
@@ -46,28 +47,34 @@ struct MmShape {
   static constexpr int kAccCols = NT < 32 ? 32 : NT;       // TMEM columns per buffer
   static constexpr int kBufs = kSwap ? 4 : 2;
   static constexpr int kTmemCols = kAccCols * kBufs;
-  static constexpr int kStageBytes = kMmPBytes + NT * kMmBlock;
+  static constexpr int kStageBytes = kMmPBytes + kQRows * kMmBlock;
   static constexpr int kCtasPerSm = kSwap ? 2 : 1;
   // !kSwap: a patch per epilogue warp, through which the output leaves in
-  // 64- or 128-byte pieces of a row
-  static constexpr int kLine = NT == 256 ? 64 : 128;
+  // 32- or 128-byte pieces of a row
+  static constexpr int kLine = NT == 256 ? 32 : 128;
   static constexpr int kPatchBytes = kSwap ? 0 : kEpiWarps * 32 * kLine;
-  static constexpr int kStages = (kSwap ? 108 * 1024 : 225 * 1024 - kPatchBytes) / kStageBytes;
-  static constexpr int kSmem = kStages * kStageBytes + kPatchBytes + 1024;
+  // scales: per block the a scales of the tile's rows of a (padded to 128) and
+  // the b scales of its 128-row parts
+  static constexpr int kScaleFloats = 128 + 4;
+  static constexpr int kRoom = (kSwap ? 113 * 1024 : 227 * 1024) - 1024 - 1024 - kPatchBytes;
+  static constexpr int kFit = (kRoom - kBufs * kScaleFloats * 4) / (kStageBytes + kScaleFloats * 4);
+  static constexpr int kStages = kFit > kMmMaxStages ? kMmMaxStages : kFit;
+  static constexpr int kSlots = kStages + kBufs;               // see the scale warp
+  static constexpr int kSmem = kStages * kStageBytes + kPatchBytes + kSlots * kScaleFloats * 4 + 1024;
   // fp32 sums of the tile in the ring's memory, laid out like the output: rows
   // of kSumCols neighbouring columns of out, the pitch chosen so that neither
   // the writes nor the reads conflict
   static constexpr int kSumRows = kSwap ? NT : 128, kSumCols = kSwap ? 128 : NT;
   static constexpr int kPitch = kSumCols * 4 + (kSwap ? 0 : 16);
   static_assert(kSumRows * kPitch <= kStages * kStageBytes, "sums exceed the ring");
-  static_assert(kSmem + 1024 <= 227 * 1024, "shared memory");
+  static_assert(kSmem + 1024 <= (kSwap ? 113 : 227) * 1024, "shared memory");
   static_assert(kStages <= kMmMaxStages && kTmemCols <= 512 / kCtasPerSm, "ring or TMEM");
 };
 
-template <bool kSwap>
-struct alignas(16) MmSmem {
-  uint64_t full[kMmMaxStages], empty[kMmMaxStages], tfull[4], tempty[4];
-  float factor[kSwap ? 4 : 1][kSwap ? 2 : 1][kSwap ? 64 : 4];  // kSwap: per epilogue warp, the scales of a block's columns (two blocks)
+struct MmSmem {
+  uint64_t full[kMmMaxStages];   // the block's codes are in shared memory (of both CTAs of a pair)
+  uint64_t done[kMmMaxStages];   // the block's MMAs are done: the stage is free, its product is in TMEM
+  uint64_t tempty[4];            // the TMEM buffer has been read
   uint32_t tmem_base;
   int abort;
 };
@@ -78,6 +85,7 @@ __device__ __forceinline__ uint32_t cluster_rank() {
   return r;
 }
 __device__ __forceinline__ void cluster_sync() {
+  __syncwarp();
   asm volatile("barrier.cluster.arrive.release.aligned;\nbarrier.cluster.wait.acquire.aligned;\n" ::: "memory");
 }
 // The same shared-memory address in the cluster's CTA `rank`, and a load from it.
@@ -94,6 +102,48 @@ __device__ __forceinline__ float4 ld_cluster_f4(uint32_t addr) {
                : "memory");
   return v;
 }
+// ---- the CTA pair (cta_group::2): one MMA over both CTAs' shared memory and
+// TMEM, issued by the even rank
+__device__ __forceinline__ void pair_alloc(uint32_t dst_smem, uint32_t ncols) {
+  asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;\n" ::"r"(dst_smem), "r"(ncols)
+               : "memory");
+  asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;\n" ::: "memory");
+}
+__device__ __forceinline__ void pair_dealloc(uint32_t taddr, uint32_t ncols) {
+  asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;\n" ::"r"(taddr), "r"(ncols) : "memory");
+}
+__device__ __forceinline__ void pair_mma(uint32_t tmem_d, uint64_t adesc, uint64_t bdesc, uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
+      " tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], %1, %2, %3, p;\n}\n" ::"r"(tmem_d),
+      "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+// Arrive on the barrier at this address in both CTAs once every MMA issued so
+// far is done.
+__device__ __forceinline__ void pair_commit(uint32_t bar) {
+  asm volatile(
+      "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;\n" ::"r"(bar),
+      "h"((uint16_t)3)
+      : "memory");
+}
+// Arrive on a barrier of the pair's even CTA (an address from cluster_addr).
+// Relaxed: what it announces are TMEM reads and bulk copies that have
+// completed, ordered by tcgen05.wait / fence and by the copies' own barrier,
+// and no ordinary memory access (a release at cluster scope would wait for all
+// of the thread's: 1177 instead of 579 us at 8192 x 8192 x 7168).
+__device__ __forceinline__ void arrive_remote(uint32_t addr) {
+  asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];\n" ::"r"(addr) : "memory");
+}
+// One fp32 from global to shared memory (0 when !have), and an arrival on bar
+// once the thread's copies so far have landed (counted in its arrivals).
+__device__ __forceinline__ void copy_f32(uint32_t dst, const float* src, bool have) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;\n" ::"r"(dst), "l"(src), "r"(have ? 4 : 0) : "memory");
+}
+__device__ __forceinline__ void copies_arrive(uint32_t bar) {
+  asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];\n" ::"r"(bar) : "memory");
+}
+
 // d += a * b on two packed fp32 values.
 __device__ __forceinline__ void fma2(uint64_t& d, uint64_t a, uint64_t b) {
   asm("fma.rn.f32x2 %0, %1, %2, %0;\n" : "+l"(d) : "l"(a), "l"(b));
@@ -157,6 +207,12 @@ __device__ __forceinline__ uint4 lds_u4(uint32_t a) {
   return v;
 }
 
+__device__ __forceinline__ float lds_f32(uint32_t a) {
+  float v;
+  asm volatile("ld.shared.f32 %0, [%1];\n" : "=f"(v) : "r"(a) : "memory");
+  return v;
+}
+
 // 32 rows (one per lane) x kLine bytes of output from registers to out: through
 // the warp's patch (16-byte chunks swizzled by the row, so that neither the
 // row-wise writes nor the line-wise reads conflict), then whole lines of
@@ -165,7 +221,7 @@ template <typename T, int kLine>
 __device__ __forceinline__ void store_patch(uint32_t patch, const float* v, int lane, T* out, int64_t stride, int rows,
                                             int cols, bool vec) {
   constexpr int E = 16 / (int)sizeof(T), C = kLine / 16;
-  auto at = [&](int r, int j) { return patch + r * kLine + ((j ^ ((C == 8 ? r : r >> 1) & (C - 1))) * 16); };
+  auto at = [&](int r, int j) { return patch + r * kLine + ((j ^ ((C == 8 ? r : r >> 2) & (C - 1))) * 16); };
 #pragma unroll
   for (int j = 0; j < C; ++j) {
     T t[E];
@@ -248,29 +304,35 @@ __device__ __forceinline__ void add_sums(uint32_t base, int rank, int rows, int6
   }
 }
 
-template <int NT, bool kSwap, typename T>
-__global__ void __launch_bounds__(MmShape<NT, kSwap>::kThreads, MmShape<NT, kSwap>::kCtasPerSm)
+// kPair: a cluster of two CTAs works on a tile of 256 rows of P; each holds its
+// 128 rows of P and half of Q's rows, so a block costs an SM 32 KB of copies
+// instead of 48 KB.  The even CTA issues the MMAs for both.
+template <int NT, bool kSwap, bool kPair, typename T>
+__global__ void __launch_bounds__(MmShape<NT, kSwap, kPair>::kThreads, MmShape<NT, kSwap, kPair>::kCtasPerSm)
     mm_kernel(const __grid_constant__ CUtensorMap pmap, const __grid_constant__ CUtensorMap qmap,
               const MmArgs g, int split, int ptiles, int qtiles) {
-  using Sh = MmShape<NT, kSwap>;
+  using Sh = MmShape<NT, kSwap, kPair>;
+  static_assert(!kPair || !kSwap, "pairs take whole tiles");
   extern __shared__ __align__(16) uint8_t smem_raw[];
-  __shared__ MmSmem<kSwap> sm;
+  __shared__ MmSmem sm;
   const uint32_t base = (smem_u32(smem_raw) + 1023u) & ~1023u;
+  const uint32_t scales = base + Sh::kStages * Sh::kStageBytes + Sh::kPatchBytes;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int KB = (g.K + kMmBlock - 1) / kMmBlock;
-  const int rank = split > 1 ? (int)cluster_rank() : 0;
+  const int peer = kPair ? (int)cluster_rank() : 0;                      // this CTA in its pair
+  const int rank = !kPair && split > 1 ? (int)cluster_rank() : 0;
   const int kb0 = (int)((int64_t)rank * KB / split), kb1 = (int)((int64_t)(rank + 1) * KB / split);
   const int tiles = ptiles * qtiles;
-  const int first = blockIdx.x / split, step = gridDim.x / split;
+  const int ctas = kPair ? 2 : split;                                    // per tile
+  const int first = blockIdx.x / ctas, step = gridDim.x / ctas;
   if (threadIdx.x == 0) {
     for (int i = 0; i < Sh::kStages; ++i) {
-      tc5::mbar_init(smem_u32(&sm.full[i]), 1);
-      tc5::mbar_init(smem_u32(&sm.empty[i]), 1);
+      // the bulk copies, the scale warp's lanes and, in the even CTA of a pair,
+      // word of the odd one's
+      tc5::mbar_init(smem_u32(&sm.full[i]), 1 + 32 + (kPair && peer == 0 ? 1 : 0));
+      tc5::mbar_init(smem_u32(&sm.done[i]), 1);
     }
-    for (int i = 0; i < Sh::kBufs; ++i) {
-      tc5::mbar_init(smem_u32(&sm.tfull[i]), 1);
-      tc5::mbar_init(smem_u32(&sm.tempty[i]), Sh::kEpiWarps);
-    }
+    for (int i = 0; i < Sh::kBufs; ++i) tc5::mbar_init(smem_u32(&sm.tempty[i]), Sh::kEpiWarps * (kPair ? 2 : 1));
     sm.abort = 0;
     tc5::fence_mbar_init();
     tc5::prefetch_tmap(&pmap);
@@ -281,18 +343,23 @@ __global__ void __launch_bounds__(MmShape<NT, kSwap>::kThreads, MmShape<NT, kSwa
   // that kernel's end.
   pdl_wait();
   if (warp == 1) {
-    tc5::tmem_alloc(smem_u32(&sm.tmem_base), Sh::kTmemCols);
-    tc5::tmem_relinquish();
+    if constexpr (kPair) {
+      pair_alloc(smem_u32(&sm.tmem_base), Sh::kTmemCols);
+    } else {
+      tc5::tmem_alloc(smem_u32(&sm.tmem_base), Sh::kTmemCols);
+      tc5::tmem_relinquish();
+    }
   }
   tc5::fence_before_sync();
   __syncthreads();
+  if (kPair) cluster_sync();  // both CTAs' barriers and TMEM are ready
   tc5::fence_after_sync();
   const uint32_t tmem = sm.tmem_base;
   volatile int* abort = &sm.abort;
   pdl_trigger();
 
-  // tile t: its P and Q tile
-  auto p_of = [&](int t) { return t % ptiles; };
+  // tile t: its P tile (128 rows of it in this CTA) and Q tile
+  auto p_of = [&](int t) { return kPair ? t % ptiles * 2 + peer : t % ptiles; };
   auto q_of = [&](int t) { return t / ptiles; };
 
   if (warp < 4) {
@@ -301,21 +368,72 @@ __global__ void __launch_bounds__(MmShape<NT, kSwap>::kThreads, MmShape<NT, kSwa
       uint32_t ph = 0;
       for (int t = first; t < tiles && !*abort; t += step)
         for (int kb = kb0; kb < kb1; ++kb, ++n) {
-          if (n >= Sh::kStages && !tc5::mbar_wait(smem_u32(&sm.empty[st]), ph ^ 1u, abort)) goto loaded;
+          if (n >= Sh::kStages && !tc5::mbar_wait(smem_u32(&sm.done[st]), ph ^ 1u, abort)) goto loaded;
           const uint32_t bar = smem_u32(&sm.full[st]), dst = base + st * Sh::kStageBytes;
           tc5::mbar_expect_tx(bar, Sh::kStageBytes);
           tc5::tma_load_2d(dst, &pmap, kb * kMmBlock, p_of(t) * 128, bar);
-          tc5::tma_load_2d(dst + kMmPBytes, &qmap, kb * kMmBlock, q_of(t) * NT, bar);
+          tc5::tma_load_2d(dst + kMmPBytes, &qmap, kb * kMmBlock, q_of(t) * NT + peer * Sh::kQRows, bar);
           if (++st == Sh::kStages) st = 0, ph ^= 1u;
         }
     loaded:
-      // copies still in flight land before the block exits
+      // copies still in flight land before the block exits (of a pair that
+      // gave up, the even CTA's barrier may miss the other's word: the wait
+      // then runs out, long after the copies)
       for (int k = n > Sh::kStages ? n - Sh::kStages : 0; k < n; ++k)
         tc5::mbar_wait_drain(smem_u32(&sm.full[k % Sh::kStages]), (k / Sh::kStages) & 1);
-    } else if (warp == 1 && lane == 0) {
+    } else if (warp == 3) {
+      // the blocks' scales, as copies of their own: fetched by the epilogue's
+      // threads, each row's line by every warp, they took longer than the sums
+      // (16 warps x 32 lines per block).  The slot of block n was last read for
+      // block n - kSlots = n - kStages - kBufs; done(n - kStages) says that its
+      // MMAs were issued, for which block n - kSlots's TMEM buffer, and so its
+      // scales, had been read.
+      int st = 0, slot = 0, n = 0;
+      uint32_t ph = 0;
+      for (int t = first; t < tiles && !*abort; t += step) {
+        const int64_t m0 = kSwap ? (int64_t)q_of(t) * NT : (int64_t)p_of(t) * 128;
+        const int64_t nb = kSwap ? p_of(t) : (int64_t)q_of(t) * NT / 128;
+        constexpr int kRows = kSwap ? (NT < 32 ? 32 : NT) : 128, kParts = kSwap ? 1 : NT / 128;
+        const float* src[kRows / 32];
+        bool have[kRows / 32];
+#pragma unroll
+        for (int i = 0; i < kRows / 32; ++i) {
+          const int64_t m = m0 + i * 32 + lane;
+          have[i] = m < g.M;
+          src[i] = g.a_scale + (have[i] ? m * g.a_scale_stride : 0);
+        }
+        const bool have_b = lane < kParts && (nb + lane) * 128 < g.N;
+        const float* src_b = g.b_scale + (have_b ? (nb + lane) * g.b_scale_stride : 0);
+        for (int kb = kb0; kb < kb1; ++kb, ++n) {
+          if (n >= Sh::kStages && !tc5::mbar_wait(smem_u32(&sm.done[st]), ph ^ 1u, abort)) goto scaled;
+          const uint32_t dst = scales + slot * Sh::kScaleFloats * 4;
+#pragma unroll
+          for (int i = 0; i < kRows / 32; ++i) copy_f32(dst + (i * 32 + lane) * 4, src[i] + kb, have[i]);
+          if (lane < kParts) copy_f32(dst + (128 + lane) * 4, src_b + kb, have_b);
+          copies_arrive(smem_u32(&sm.full[st]));
+          if (++st == Sh::kStages) st = 0, ph ^= 1u;
+          if (++slot == Sh::kSlots) slot = 0;
+        }
+      }
+    scaled:
+      cp_async_commit();
+      cp_async_wait<0>();
+    } else if (kPair && peer == 1 && warp == 2 && lane == 0) {
+      // tells the even CTA that this CTA's half of a block has landed
+      int st = 0;
+      uint32_t ph = 0;
+      for (int t = first; t < tiles && !*abort; t += step)
+        for (int kb = kb0; kb < kb1; ++kb) {
+          const uint32_t bar = smem_u32(&sm.full[st]);
+          if (!tc5::mbar_wait(bar, ph, abort)) goto told;
+          arrive_remote(cluster_addr(bar, 0));
+          if (++st == Sh::kStages) st = 0, ph ^= 1u;
+        }
+    told:;
+    } else if (warp == 1 && lane == 0 && peer == 0) {
       int st = 0, buf = 0, n = 0;
       uint32_t ph = 0, bph = 0;
-      const uint32_t idesc = tc5::idesc_e4m3_f32(128, NT);
+      const uint32_t idesc = tc5::idesc_e4m3_f32(kPair ? 256 : 128, NT);
       for (int t = first; t < tiles && !*abort; t += step)
         for (int kb = kb0; kb < kb1; ++kb, ++n) {
           if (n >= Sh::kBufs && !tc5::mbar_wait(smem_u32(&sm.tempty[buf]), bph ^ 1u, abort)) goto issued;
@@ -324,56 +442,44 @@ __global__ void __launch_bounds__(MmShape<NT, kSwap>::kThreads, MmShape<NT, kSwa
           const uint64_t pd = tc5::sdesc_k_sw128(base + st * Sh::kStageBytes);
           const uint64_t qd = tc5::sdesc_k_sw128(base + st * Sh::kStageBytes + kMmPBytes);
 #pragma unroll
-          for (int i = 0; i < 4; ++i)
-            tc5::mma_e4m3(tmem + buf * Sh::kAccCols, pd + 2 * i, qd + 2 * i, idesc, i > 0);
-          tc5::mma_commit(smem_u32(&sm.empty[st]));
-          tc5::mma_commit(smem_u32(&sm.tfull[buf]));
+          for (int i = 0; i < 4; ++i) {
+            if constexpr (kPair)
+              pair_mma(tmem + buf * Sh::kAccCols, pd + 2 * i, qd + 2 * i, idesc, i > 0);
+            else
+              tc5::mma_e4m3(tmem + buf * Sh::kAccCols, pd + 2 * i, qd + 2 * i, idesc, i > 0);
+          }
+          // one commit frees the stage and hands the product to the epilogue
+          if constexpr (kPair)
+            pair_commit(smem_u32(&sm.done[st]));
+          else
+            tc5::mma_commit(smem_u32(&sm.done[st]));
           if (++st == Sh::kStages) st = 0, ph ^= 1u;
           if (++buf == Sh::kBufs) buf = 0, bph ^= 1u;
         }
     issued:
       // MMAs still in flight finish before TMEM is freed
-      for (int k = n > Sh::kBufs ? n - Sh::kBufs : 0; k < n; ++k)
-        tc5::mbar_wait_drain(smem_u32(&sm.tfull[k % Sh::kBufs]), (k / Sh::kBufs) & 1);
+      for (int k = n > Sh::kStages ? n - Sh::kStages : 0; k < n; ++k)
+        tc5::mbar_wait_drain(smem_u32(&sm.done[k % Sh::kStages]), (k / Sh::kStages) & 1);
     }
   } else {
     const int ew = warp - 4, quarter = ew & 3, group = ew >> 2;
     const int row = quarter * 32 + lane;                 // TMEM lane: row of the P tile
     const uint32_t tcol = tmem + ((uint32_t)(quarter * 32) << 16) + group * Sh::kCols;
-    int buf = 0;
-    uint32_t bph = 0;
+    int buf = 0, st = 0, slot = 0;
+    uint32_t ph = 0;
     for (int t = first; t < tiles && !*abort; t += step) {
       const int64_t p0 = (int64_t)p_of(t) * 128, q0 = (int64_t)q_of(t) * NT + group * Sh::kCols;
       uint64_t acc[Sh::kCols / 2];
 #pragma unroll
       for (int i = 0; i < Sh::kCols / 2; ++i) acc[i] = 0;
       bool ok = true;
-      // scales: !kSwap one factor per thread, kSwap one per column (lane l
-      // fetches columns l and l + 32, the warp shares them through shared
-      // memory); fetched one block ahead
-      constexpr int kFetch = kSwap ? (NT + 31) / 32 : 1;
-      float ahead[kFetch], ahead_b = 0.f;
-      auto fetch = [&](int kb) {
-        const int64_t nb = (kSwap ? p0 : q0) / 128;
-        ahead_b = nb * 128 < g.N ? __ldg(g.b_scale + nb * g.b_scale_stride + kb) : 0.f;
-#pragma unroll
-        for (int i = 0; i < kFetch; ++i) {
-          const int64_t m = kSwap ? q0 + i * 32 + lane : p0 + row;
-          ahead[i] = m < g.M && (!kSwap || i * 32 + lane < NT) ? __ldg(g.a_scale + m * g.a_scale_stride + kb) : 0.f;
-        }
-      };
-      fetch(kb0);
       for (int kb = kb0; kb < kb1; ++kb) {
-        const float f = ahead[0] * ahead_b;
-        float* factor = sm.factor[kSwap ? quarter : 0][kSwap ? kb & 1 : 0];
-        if (kSwap) {
-#pragma unroll
-          for (int i = 0; i < kFetch; ++i)
-            if (i * 32 + lane < NT) factor[i * 32 + lane] = ahead[i] * ahead_b;
-        }
-        if (kb + 1 < kb1) fetch(kb + 1);
-        if (kSwap) __syncwarp();
-        if (!tc5::mbar_wait(smem_u32(&sm.tfull[buf]), bph, abort)) { ok = false; break; }
+        if (!tc5::mbar_wait(smem_u32(&sm.done[st]), ph, abort)) { ok = false; break; }
+        const uint32_t sc = scales + slot * Sh::kScaleFloats * 4;
+        // !kSwap: one factor per thread; kSwap: the b scale for all, the a
+        // scales by column
+        const float sb = lds_f32(sc + (128 + (kSwap ? 0 : group * Sh::kCols / 128)) * 4);
+        const float f = kSwap ? sb : sb * lds_f32(sc + row * 4);
         tc5::fence_after_sync();
         const uint64_t f2 = pack2(f, f);
         constexpr int kChunk = Sh::kChunk, kParts = Sh::kCols / kChunk;
@@ -386,7 +492,12 @@ __global__ void __launch_bounds__(MmShape<NT, kSwap>::kThreads, MmShape<NT, kSwa
           if (x + 1 == kParts) {  // the buffer is read: the next block's MMAs may have it
             tc5::fence_before_sync();
             __syncwarp();
-            if (lane == 0) tc5::mbar_arrive(smem_u32(&sm.tempty[buf]));
+            if (lane == 0) {
+              if (kPair)
+                arrive_remote(cluster_addr(smem_u32(&sm.tempty[buf]), 0));
+              else
+                tc5::mbar_arrive(smem_u32(&sm.tempty[buf]));
+            }
           }
 #pragma unroll
           for (int i = 0; i < kChunk; i += 4) {
@@ -394,15 +505,17 @@ __global__ void __launch_bounds__(MmShape<NT, kSwap>::kThreads, MmShape<NT, kSwa
             const int at = (x * kChunk + i) / 2;
             uint64_t s01 = f2, s23 = f2;
             if (kSwap) {
-              const float4 s = *reinterpret_cast<const float4*>(factor + x * kChunk + i);
-              s01 = pack2(s.x, s.y);
-              s23 = pack2(s.z, s.w);
+              const uint4 s = lds_u4(sc + (x * kChunk + i) * 4);
+              s01 = pack2(__uint_as_float(s.x) * f, __uint_as_float(s.y) * f);
+              s23 = pack2(__uint_as_float(s.z) * f, __uint_as_float(s.w) * f);
             }
             fma2(acc[at], pack2(__uint_as_float(r[0]), __uint_as_float(r[1])), s01);
             fma2(acc[at + 1], pack2(__uint_as_float(r[2]), __uint_as_float(r[3])), s23);
           }
         }
-        if (++buf == Sh::kBufs) buf = 0, bph ^= 1u;
+        if (++buf == Sh::kBufs) buf = 0;
+        if (++slot == Sh::kSlots) slot = 0;
+        if (++st == Sh::kStages) st = 0, ph ^= 1u;
       }
       if (!ok) break;
       float v[Sh::kCols];
@@ -440,7 +553,6 @@ __global__ void __launch_bounds__(MmShape<NT, kSwap>::kThreads, MmShape<NT, kSwa
   if (kSwap || split > 1) {
     // one tile per cluster: its sums, added over the ranks in order, leave in
     // pieces of four neighbouring columns, an equal share from each rank
-    __syncwarp();
     if (split > 1)
       cluster_sync();
     else
@@ -456,16 +568,19 @@ __global__ void __launch_bounds__(MmShape<NT, kSwap>::kThreads, MmShape<NT, kSwa
       case 4: add_sums<Sh, T, 4>(base, rank, rows, left, out, g.out_stride, g.vec); break;
       default: add_sums<Sh, T, 8>(base, rank, rows, left, out, g.out_stride, g.vec); break;
     }
-    if (split > 1) {
-      __syncwarp();
-      cluster_sync();  // no CTA leaves while another reads its sums
-    }
+    if (split > 1) cluster_sync();  // no CTA leaves while another reads its sums
   }
   tc5::fence_before_sync();
   __syncthreads();
+  if (kPair) cluster_sync();  // the pair's MMAs and arrivals are over
   tc5::fence_after_sync();
   if (threadIdx.x == 0 && sm.abort && g.status) set_status(g.status, kStatusTimeout);
-  if (warp == 1) tc5::tmem_dealloc(tmem, Sh::kTmemCols);
+  if (warp == 1) {
+    if constexpr (kPair)
+      pair_dealloc(tmem, Sh::kTmemCols);
+    else
+      tc5::tmem_dealloc(tmem, Sh::kTmemCols);
+  }
 }
 
 bool make_mm_map(CUtensorMap* m, const void* ptr, uint64_t rows, uint64_t cols, uint64_t stride, uint32_t box_rows) {
@@ -480,29 +595,31 @@ bool make_mm_map(CUtensorMap* m, const void* ptr, uint64_t rows, uint64_t cols, 
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <int NT, bool kSwap, typename T>
+template <int NT, bool kSwap, bool kPair, typename T>
 int launch_shape(const MmArgs& g, int num_sms, cudaStream_t st, bool pdl) {
-  using Sh = MmShape<NT, kSwap>;
+  using Sh = MmShape<NT, kSwap, kPair>;
   CUtensorMap pmap, qmap;
   const bool ok = kSwap ? make_mm_map(&pmap, g.b, g.N, g.K, g.b_stride, 128) &&
                               make_mm_map(&qmap, g.a, g.M, g.K, g.a_stride, NT)
                         : make_mm_map(&pmap, g.a, g.M, g.K, g.a_stride, 128) &&
-                              make_mm_map(&qmap, g.b, g.N, g.K, g.b_stride, NT);
+                              make_mm_map(&qmap, g.b, g.N, g.K, g.b_stride, Sh::kQRows);
   if (!ok) return launch_fail("cuTensorMapEncodeTiled(a, b)", cudaSuccess);
-  auto kern = mm_kernel<NT, kSwap, T>;
+  auto kern = mm_kernel<NT, kSwap, kPair, T>;
   static PerDeviceOnce attr;
   if (const cudaError_t e = attr.run([&] { return allow_max_dynamic_smem(kern); }))
     return launch_fail("cudaFuncSetAttribute(mm_kernel)", e);
-  const int ptiles = (int)(((kSwap ? g.N : g.M) + 127) / 128), qtiles = (int)(((kSwap ? g.M : g.N) + NT - 1) / NT);
+  constexpr int kPTile = kPair ? 256 : 128;
+  const int ptiles = (int)(((int64_t)(kSwap ? g.N : g.M) + kPTile - 1) / kPTile), qtiles = (int)(((int64_t)(kSwap ? g.M : g.N) + NT - 1) / NT);
   const int64_t tiles = (int64_t)ptiles * qtiles;
   if (tiles > 0x7fffffff / 8) return launch_fail("too many tiles", cudaSuccess);
   const int slots = num_sms * Sh::kCtasPerSm;
   const int KB = (g.K + kMmBlock - 1) / kMmBlock;
   // a tile's blocks over the CTAs of a cluster while that still adds CTAs
   int split = 1;
-  while (split < 8 && tiles * split * 2 <= slots && KB >= split * 2 * 2) split *= 2;
+  while (!kPair && split < 8 && tiles * split * 2 <= slots && KB >= split * 2 * 2) split *= 2;
   // kSwap and split tiles leave through the ring's memory: one tile per cluster
-  const int64_t grid = kSwap || split > 1 ? tiles * split : (tiles < slots ? tiles : slots);
+  const int64_t grid = kPair ? 2 * (tiles < slots / 2 ? tiles : slots / 2)
+                       : kSwap || split > 1 ? tiles * split : (tiles < slots ? tiles : slots);
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)grid);
   cfg.blockDim = dim3(Sh::kThreads);
@@ -514,9 +631,9 @@ int launch_shape(const MmArgs& g, int num_sms, cudaStream_t st, bool pdl) {
     at[na].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     at[na++].val.programmaticStreamSerializationAllowed = 1;
   }
-  if (split > 1) {
+  if (kPair || split > 1) {
     at[na].id = cudaLaunchAttributeClusterDimension;
-    at[na].val.clusterDim.x = split;
+    at[na].val.clusterDim.x = kPair ? 2 : split;
     at[na].val.clusterDim.y = 1;
     at[na++].val.clusterDim.z = 1;
   }
@@ -528,12 +645,14 @@ int launch_shape(const MmArgs& g, int num_sms, cudaStream_t st, bool pdl) {
 
 template <typename T>
 int launch_out(const MmArgs& g, int num_sms, cudaStream_t st, bool pdl) {
-  if (g.M <= 16) return launch_shape<16, true, T>(g, num_sms, st, pdl);
-  if (g.M <= 32) return launch_shape<32, true, T>(g, num_sms, st, pdl);
-  if (g.M <= 64) return launch_shape<64, true, T>(g, num_sms, st, pdl);
-  // 256 columns per tile halve the reads of a, 128 keep more SMs busy
-  const int64_t tiles = (int64_t)((g.M + 127) / 128) * ((g.N + 255) / 256);
-  return tiles >= num_sms ? launch_shape<256, false, T>(g, num_sms, st, pdl) : launch_shape<128, false, T>(g, num_sms, st, pdl);
+  if (g.M <= 16) return launch_shape<16, true, false, T>(g, num_sms, st, pdl);
+  if (g.M <= 32) return launch_shape<32, true, false, T>(g, num_sms, st, pdl);
+  if (g.M <= 64) return launch_shape<64, true, false, T>(g, num_sms, st, pdl);
+  // pairs on 256 x 256 tiles halve the reads of both operands, 128 x 128 tiles
+  // keep more SMs busy
+  const int64_t pairs = (int64_t)((g.M + 255) / 256) * ((g.N + 255) / 256);
+  return pairs >= num_sms / 2 ? launch_shape<256, false, true, T>(g, num_sms, st, pdl)
+                              : launch_shape<128, false, false, T>(g, num_sms, st, pdl);
 }
 
 }  // namespace

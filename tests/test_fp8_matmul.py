@@ -137,7 +137,8 @@ SHAPES = [(1, 1, 1), (1, 128, 128), (1, 8192, 1536), (2, 130, 17), (3, 257, 129)
           (17, 129, 1000), (32, 4096, 512), (33, 300, 2048), (63, 576, 1280), (64, 2304, 1536), (65, 129, 300),
           (100, 77, 7168), (128, 128, 128), (129, 513, 384), (200, 4100, 1000), (331, 1100, 7000), (1000, 1111, 333),
           (1, 100000, 256), (2048, 2176, 512), (700, 300, 16384), (5, 40, 65536),
-          (2500, 2300, 700), (4000, 1290, 1)]
+          (2500, 2300, 700), (4000, 1290, 1), (2300, 2650, 1500),
+          (20000, 257, 300), (300, 20000, 130)]
 
 
 @pytest.mark.gpu
