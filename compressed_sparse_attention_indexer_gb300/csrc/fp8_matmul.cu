@@ -9,9 +9,10 @@
 // block's product back from TMEM and add it, times its scale, to fp32
 // registers, while the MMAs of the next block fill another buffer.
 //
-//   warp 0      producer: per block one TMA box of each operand into a ring
+//   warp 0      copies: per block one TMA box of each operand into a ring, and
+//               the block's scales into another
 //   warp 1      TMEM allocation; one thread issues four K = 32 MMAs per block
-//   warps 4..   epilogue: thread = TMEM lane (row of P), its columns of Q
+//   warps 2..   epilogue: thread = TMEM lane (row of P), its columns of Q
 //
 // The operand in the TMEM lanes (P, 128 rows per tile) and the one in its
 // columns (Q, NT rows per tile) are a and b, or with `kSwap` b and a: for a
@@ -35,19 +36,25 @@ constexpr int kMmBlock = 128;                 // codes per scale, bytes per stag
 constexpr int kMmPBytes = 128 * kMmBlock;     // P tile: 128 rows
 constexpr int kMmMaxStages = 12;
 
-template <int NT, bool kSwap, bool kPair>
+
+// One test of a barrier's phase, whose answer is used later.
+__device__ __forceinline__ uint32_t bar_ask(uint32_t bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile("{\n .reg .pred p;\n mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n selp.u32 %0, 1, 0, p;\n}\n" : "=r"(ok) : "r"(bar), "r"(parity) : "memory");
+  return ok;
+}
+template <int NT, bool kSwap>
 struct MmShape {
-  static constexpr int kQRows = kPair ? NT / 2 : NT;       // rows of the Q tile in this CTA's shared memory
   // 64 sums per epilogue thread at most; with 256 columns sixteen warps, four
   // per scheduler, hide each other's TMEM reads
   static constexpr int kEpiWarps = kSwap ? 4 : NT == 256 ? 16 : 8;
-  static constexpr int kThreads = 128 + 32 * kEpiWarps;
+  static constexpr int kThreads = 64 + 32 * kEpiWarps;
   static constexpr int kCols = NT / (kEpiWarps / 4);       // columns per epilogue thread
   static constexpr int kChunk = kSwap || NT == 256 ? 16 : 32;  // columns per TMEM read
   static constexpr int kAccCols = NT < 32 ? 32 : NT;       // TMEM columns per buffer
   static constexpr int kBufs = kSwap ? 4 : 2;
   static constexpr int kTmemCols = kAccCols * kBufs;
-  static constexpr int kStageBytes = kMmPBytes + kQRows * kMmBlock;
+  static constexpr int kStageBytes = kMmPBytes + NT * kMmBlock;
   static constexpr int kCtasPerSm = kSwap ? 2 : 1;
   // !kSwap: a patch per epilogue warp, through which the output leaves in
   // 32- or 128-byte pieces of a row
@@ -72,7 +79,7 @@ struct MmShape {
 };
 
 struct MmSmem {
-  uint64_t full[kMmMaxStages];   // the block's codes are in shared memory (of both CTAs of a pair)
+  uint64_t full[kMmMaxStages];   // the block's codes are in shared memory
   uint64_t done[kMmMaxStages];   // the block's MMAs are done: the stage is free, its product is in TMEM
   uint64_t tempty[4];            // the TMEM buffer has been read
   uint32_t tmem_base;
@@ -101,39 +108,6 @@ __device__ __forceinline__ float4 ld_cluster_f4(uint32_t addr) {
                : "r"(addr)
                : "memory");
   return v;
-}
-// ---- the CTA pair (cta_group::2): one MMA over both CTAs' shared memory and
-// TMEM, issued by the even rank
-__device__ __forceinline__ void pair_alloc(uint32_t dst_smem, uint32_t ncols) {
-  asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;\n" ::"r"(dst_smem), "r"(ncols)
-               : "memory");
-  asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;\n" ::: "memory");
-}
-__device__ __forceinline__ void pair_dealloc(uint32_t taddr, uint32_t ncols) {
-  asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;\n" ::"r"(taddr), "r"(ncols) : "memory");
-}
-__device__ __forceinline__ void pair_mma(uint32_t tmem_d, uint64_t adesc, uint64_t bdesc, uint32_t idesc, uint32_t accumulate) {
-  asm volatile(
-      "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
-      " tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], %1, %2, %3, p;\n}\n" ::"r"(tmem_d),
-      "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
-      : "memory");
-}
-// Arrive on the barrier at this address in both CTAs once every MMA issued so
-// far is done.
-__device__ __forceinline__ void pair_commit(uint32_t bar) {
-  asm volatile(
-      "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;\n" ::"r"(bar),
-      "h"((uint16_t)3)
-      : "memory");
-}
-// Arrive on a barrier of the pair's even CTA (an address from cluster_addr).
-// Relaxed: what it announces are TMEM reads and bulk copies that have
-// completed, ordered by tcgen05.wait / fence and by the copies' own barrier,
-// and no ordinary memory access (a release at cluster scope would wait for all
-// of the thread's: 1177 instead of 579 us at 8192 x 8192 x 7168).
-__device__ __forceinline__ void arrive_remote(uint32_t addr) {
-  asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];\n" ::"r"(addr) : "memory");
 }
 // One fp32 from global to shared memory (0 when !have), and an arrival on bar
 // once the thread's copies so far have landed (counted in its arrivals).
@@ -304,35 +278,27 @@ __device__ __forceinline__ void add_sums(uint32_t base, int rank, int rows, int6
   }
 }
 
-// kPair: a cluster of two CTAs works on a tile of 256 rows of P; each holds its
-// 128 rows of P and half of Q's rows, so a block costs an SM 32 KB of copies
-// instead of 48 KB.  The even CTA issues the MMAs for both.
-template <int NT, bool kSwap, bool kPair, typename T>
-__global__ void __launch_bounds__(MmShape<NT, kSwap, kPair>::kThreads, MmShape<NT, kSwap, kPair>::kCtasPerSm)
+template <int NT, bool kSwap, typename T>
+__global__ void __launch_bounds__(MmShape<NT, kSwap>::kThreads, MmShape<NT, kSwap>::kCtasPerSm)
     mm_kernel(const __grid_constant__ CUtensorMap pmap, const __grid_constant__ CUtensorMap qmap,
               const MmArgs g, int split, int ptiles, int qtiles) {
-  using Sh = MmShape<NT, kSwap, kPair>;
-  static_assert(!kPair || !kSwap, "pairs take whole tiles");
+  using Sh = MmShape<NT, kSwap>;
   extern __shared__ __align__(16) uint8_t smem_raw[];
   __shared__ MmSmem sm;
   const uint32_t base = (smem_u32(smem_raw) + 1023u) & ~1023u;
   const uint32_t scales = base + Sh::kStages * Sh::kStageBytes + Sh::kPatchBytes;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int KB = (g.K + kMmBlock - 1) / kMmBlock;
-  const int peer = kPair ? (int)cluster_rank() : 0;                      // this CTA in its pair
-  const int rank = !kPair && split > 1 ? (int)cluster_rank() : 0;
+  const int rank = split > 1 ? (int)cluster_rank() : 0;
   const int kb0 = (int)((int64_t)rank * KB / split), kb1 = (int)((int64_t)(rank + 1) * KB / split);
   const int tiles = ptiles * qtiles;
-  const int ctas = kPair ? 2 : split;                                    // per tile
-  const int first = blockIdx.x / ctas, step = gridDim.x / ctas;
+  const int first = blockIdx.x / split, step = gridDim.x / split;
   if (threadIdx.x == 0) {
     for (int i = 0; i < Sh::kStages; ++i) {
-      // the bulk copies, the scale warp's lanes and, in the even CTA of a pair,
-      // word of the odd one's
-      tc5::mbar_init(smem_u32(&sm.full[i]), 1 + 32 + (kPair && peer == 0 ? 1 : 0));
+      tc5::mbar_init(smem_u32(&sm.full[i]), 1 + 32);  // the bulk copies, the scales of 32 lanes
       tc5::mbar_init(smem_u32(&sm.done[i]), 1);
     }
-    for (int i = 0; i < Sh::kBufs; ++i) tc5::mbar_init(smem_u32(&sm.tempty[i]), Sh::kEpiWarps * (kPair ? 2 : 1));
+    for (int i = 0; i < Sh::kBufs; ++i) tc5::mbar_init(smem_u32(&sm.tempty[i]), Sh::kEpiWarps);
     sm.abort = 0;
     tc5::fence_mbar_init();
     tc5::prefetch_tmap(&pmap);
@@ -343,118 +309,93 @@ __global__ void __launch_bounds__(MmShape<NT, kSwap, kPair>::kThreads, MmShape<N
   // that kernel's end.
   pdl_wait();
   if (warp == 1) {
-    if constexpr (kPair) {
-      pair_alloc(smem_u32(&sm.tmem_base), Sh::kTmemCols);
-    } else {
-      tc5::tmem_alloc(smem_u32(&sm.tmem_base), Sh::kTmemCols);
-      tc5::tmem_relinquish();
-    }
+    tc5::tmem_alloc(smem_u32(&sm.tmem_base), Sh::kTmemCols);
+    tc5::tmem_relinquish();
   }
   tc5::fence_before_sync();
   __syncthreads();
-  if (kPair) cluster_sync();  // both CTAs' barriers and TMEM are ready
   tc5::fence_after_sync();
   const uint32_t tmem = sm.tmem_base;
   volatile int* abort = &sm.abort;
   pdl_trigger();
 
-  // tile t: its P tile (128 rows of it in this CTA) and Q tile
-  auto p_of = [&](int t) { return kPair ? t % ptiles * 2 + peer : t % ptiles; };
+  // tile t: its P and Q tile
+  auto p_of = [&](int t) { return t % ptiles; };
   auto q_of = [&](int t) { return t / ptiles; };
 
-  if (warp < 4) {
-    if (warp == 0 && lane == 0) {
-      int st = 0, n = 0;
-      uint32_t ph = 0;
-      for (int t = first; t < tiles && !*abort; t += step)
-        for (int kb = kb0; kb < kb1; ++kb, ++n) {
-          if (n >= Sh::kStages && !tc5::mbar_wait(smem_u32(&sm.done[st]), ph ^ 1u, abort)) goto loaded;
-          const uint32_t bar = smem_u32(&sm.full[st]), dst = base + st * Sh::kStageBytes;
+  if (warp == 0) {
+    // copies: lane 0 the codes (bulk), every lane the scales.  (Fetched by the
+    // epilogue's threads instead, each row's line by every warp, the scales
+    // took longer than the sums.)  Block n's scales go to slot n % kSlots, last
+    // read for block n - kStages - kBufs; done(n - kStages) says that its MMAs
+    // were issued, for which that block's TMEM buffer, and so its scales, had
+    // been read.
+    constexpr int kRows = kSwap ? (NT < 32 ? 32 : NT) : 128, kParts = kSwap ? 1 : NT / 128;
+    int st = 0, slot = 0, n = 0;
+    uint32_t ph = 0;
+    for (int t = first; t < tiles && !*abort; t += step) {
+      const int64_t m0 = kSwap ? (int64_t)q_of(t) * NT : (int64_t)p_of(t) * 128;
+      const int64_t nb = kSwap ? p_of(t) : (int64_t)q_of(t) * NT / 128;
+      const float* src[kRows / 32];
+      bool have[kRows / 32];
+#pragma unroll
+      for (int i = 0; i < kRows / 32; ++i) {
+        const int64_t m = m0 + i * 32 + lane;
+        have[i] = m < g.M;
+        src[i] = g.a_scale + (have[i] ? m * g.a_scale_stride : 0);
+      }
+      const bool have_b = lane < kParts && (nb + lane) * 128 < g.N;
+      const float* src_b = g.b_scale + (have_b ? (nb + lane) * g.b_scale_stride : 0);
+      for (int kb = kb0; kb < kb1; ++kb, ++n) {
+        if (n >= Sh::kStages && !tc5::mbar_wait(smem_u32(&sm.done[st]), ph ^ 1u, abort)) goto loaded;
+        const uint32_t bar = smem_u32(&sm.full[st]);
+        if (lane == 0) {
+          const uint32_t dst = base + st * Sh::kStageBytes;
           tc5::mbar_expect_tx(bar, Sh::kStageBytes);
           tc5::tma_load_2d(dst, &pmap, kb * kMmBlock, p_of(t) * 128, bar);
-          tc5::tma_load_2d(dst + kMmPBytes, &qmap, kb * kMmBlock, q_of(t) * NT + peer * Sh::kQRows, bar);
-          if (++st == Sh::kStages) st = 0, ph ^= 1u;
+          tc5::tma_load_2d(dst + kMmPBytes, &qmap, kb * kMmBlock, q_of(t) * NT, bar);
         }
-    loaded:
-      // copies still in flight land before the block exits (of a pair that
-      // gave up, the even CTA's barrier may miss the other's word: the wait
-      // then runs out, long after the copies)
-      for (int k = n > Sh::kStages ? n - Sh::kStages : 0; k < n; ++k)
-        tc5::mbar_wait_drain(smem_u32(&sm.full[k % Sh::kStages]), (k / Sh::kStages) & 1);
-    } else if (warp == 3) {
-      // the blocks' scales, as copies of their own: fetched by the epilogue's
-      // threads, each row's line by every warp, they took longer than the sums
-      // (16 warps x 32 lines per block).  The slot of block n was last read for
-      // block n - kSlots = n - kStages - kBufs; done(n - kStages) says that its
-      // MMAs were issued, for which block n - kSlots's TMEM buffer, and so its
-      // scales, had been read.
-      int st = 0, slot = 0, n = 0;
-      uint32_t ph = 0;
-      for (int t = first; t < tiles && !*abort; t += step) {
-        const int64_t m0 = kSwap ? (int64_t)q_of(t) * NT : (int64_t)p_of(t) * 128;
-        const int64_t nb = kSwap ? p_of(t) : (int64_t)q_of(t) * NT / 128;
-        constexpr int kRows = kSwap ? (NT < 32 ? 32 : NT) : 128, kParts = kSwap ? 1 : NT / 128;
-        const float* src[kRows / 32];
-        bool have[kRows / 32];
+        __syncwarp();
+        const uint32_t dst = scales + slot * Sh::kScaleFloats * 4;
 #pragma unroll
-        for (int i = 0; i < kRows / 32; ++i) {
-          const int64_t m = m0 + i * 32 + lane;
-          have[i] = m < g.M;
-          src[i] = g.a_scale + (have[i] ? m * g.a_scale_stride : 0);
-        }
-        const bool have_b = lane < kParts && (nb + lane) * 128 < g.N;
-        const float* src_b = g.b_scale + (have_b ? (nb + lane) * g.b_scale_stride : 0);
-        for (int kb = kb0; kb < kb1; ++kb, ++n) {
-          if (n >= Sh::kStages && !tc5::mbar_wait(smem_u32(&sm.done[st]), ph ^ 1u, abort)) goto scaled;
-          const uint32_t dst = scales + slot * Sh::kScaleFloats * 4;
-#pragma unroll
-          for (int i = 0; i < kRows / 32; ++i) copy_f32(dst + (i * 32 + lane) * 4, src[i] + kb, have[i]);
-          if (lane < kParts) copy_f32(dst + (128 + lane) * 4, src_b + kb, have_b);
-          copies_arrive(smem_u32(&sm.full[st]));
-          if (++st == Sh::kStages) st = 0, ph ^= 1u;
-          if (++slot == Sh::kSlots) slot = 0;
-        }
+        for (int i = 0; i < kRows / 32; ++i) copy_f32(dst + (i * 32 + lane) * 4, src[i] + kb, have[i]);
+        if (lane < kParts) copy_f32(dst + (128 + lane) * 4, src_b + kb, have_b);
+        copies_arrive(bar);
+        if (++st == Sh::kStages) st = 0, ph ^= 1u;
+        if (++slot == Sh::kSlots) slot = 0;
       }
-    scaled:
-      cp_async_commit();
-      cp_async_wait<0>();
-    } else if (kPair && peer == 1 && warp == 2 && lane == 0) {
-      // tells the even CTA that this CTA's half of a block has landed
-      int st = 0;
-      uint32_t ph = 0;
-      for (int t = first; t < tiles && !*abort; t += step)
-        for (int kb = kb0; kb < kb1; ++kb) {
-          const uint32_t bar = smem_u32(&sm.full[st]);
-          if (!tc5::mbar_wait(bar, ph, abort)) goto told;
-          arrive_remote(cluster_addr(bar, 0));
-          if (++st == Sh::kStages) st = 0, ph ^= 1u;
-        }
-    told:;
-    } else if (warp == 1 && lane == 0 && peer == 0) {
+    }
+  loaded:
+    // copies still in flight land before the block exits
+    cp_async_commit();
+    cp_async_wait<0>();
+    for (int k = n > Sh::kStages ? n - Sh::kStages : 0; k < n; ++k)
+      tc5::mbar_wait_drain(smem_u32(&sm.full[k % Sh::kStages]), (k / Sh::kStages) & 1);
+  } else if (warp == 1) {
+    if (lane == 0) {
       int st = 0, buf = 0, n = 0;
       uint32_t ph = 0, bph = 0;
-      const uint32_t idesc = tc5::idesc_e4m3_f32(kPair ? 256 : 128, NT);
+      const uint32_t idesc = tc5::idesc_e4m3_f32(128, NT);
+      uint32_t okf = 0, okt = 1;
       for (int t = first; t < tiles && !*abort; t += step)
         for (int kb = kb0; kb < kb1; ++kb, ++n) {
-          if (n >= Sh::kBufs && !tc5::mbar_wait(smem_u32(&sm.tempty[buf]), bph ^ 1u, abort)) goto issued;
-          if (!tc5::mbar_wait(smem_u32(&sm.full[st]), ph, abort)) goto issued;
+          if (!okf && !tc5::mbar_wait(smem_u32(&sm.full[st]), ph, abort)) goto issued;
+          if (!okt && !tc5::mbar_wait(smem_u32(&sm.tempty[buf]), bph ^ 1u, abort)) goto issued;
           tc5::fence_after_sync();
           const uint64_t pd = tc5::sdesc_k_sw128(base + st * Sh::kStageBytes);
           const uint64_t qd = tc5::sdesc_k_sw128(base + st * Sh::kStageBytes + kMmPBytes);
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            if constexpr (kPair)
-              pair_mma(tmem + buf * Sh::kAccCols, pd + 2 * i, qd + 2 * i, idesc, i > 0);
-            else
-              tc5::mma_e4m3(tmem + buf * Sh::kAccCols, pd + 2 * i, qd + 2 * i, idesc, i > 0);
-          }
-          // one commit frees the stage and hands the product to the epilogue
-          if constexpr (kPair)
-            pair_commit(smem_u32(&sm.done[st]));
-          else
-            tc5::mma_commit(smem_u32(&sm.done[st]));
+          const uint32_t d = tmem + buf * Sh::kAccCols, now = smem_u32(&sm.done[st]);
           if (++st == Sh::kStages) st = 0, ph ^= 1u;
           if (++buf == Sh::kBufs) buf = 0, bph ^= 1u;
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            tc5::mma_e4m3(d, pd + 2 * i, qd + 2 * i, idesc, i > 0);
+            if (i == 1) {  // asked here, the next block's barriers answer while the MMAs are issued
+              okf = bar_ask(smem_u32(&sm.full[st]), ph);
+              okt = n + 1 < Sh::kBufs ? 1u : bar_ask(smem_u32(&sm.tempty[buf]), bph ^ 1u);
+            }
+          }
+          tc5::mma_commit(now);  // frees the stage and hands the product to the epilogue
         }
     issued:
       // MMAs still in flight finish before TMEM is freed
@@ -462,7 +403,8 @@ __global__ void __launch_bounds__(MmShape<NT, kSwap, kPair>::kThreads, MmShape<N
         tc5::mbar_wait_drain(smem_u32(&sm.done[k % Sh::kStages]), (k / Sh::kStages) & 1);
     }
   } else {
-    const int ew = warp - 4, quarter = ew & 3, group = ew >> 2;
+    // a warp reads the TMEM lanes of its number mod 4
+    const int ew = warp - 2, quarter = warp & 3, group = ew >> 2;
     const int row = quarter * 32 + lane;                 // TMEM lane: row of the P tile
     const uint32_t tcol = tmem + ((uint32_t)(quarter * 32) << 16) + group * Sh::kCols;
     int buf = 0, st = 0, slot = 0;
@@ -476,32 +418,28 @@ __global__ void __launch_bounds__(MmShape<NT, kSwap, kPair>::kThreads, MmShape<N
       for (int kb = kb0; kb < kb1; ++kb) {
         if (!tc5::mbar_wait(smem_u32(&sm.done[st]), ph, abort)) { ok = false; break; }
         const uint32_t sc = scales + slot * Sh::kScaleFloats * 4;
+        tc5::fence_after_sync();
+        constexpr int kChunk = Sh::kChunk, kParts = Sh::kCols / kChunk;
+        const uint32_t t0 = tcol + buf * Sh::kAccCols;
+        uint32_t v[2][kChunk];
+        tmem_ask<kChunk>(t0, v[0]);
         // !kSwap: one factor per thread; kSwap: the b scale for all, the a
         // scales by column
         const float sb = lds_f32(sc + (128 + (kSwap ? 0 : group * Sh::kCols / 128)) * 4);
         const float f = kSwap ? sb : sb * lds_f32(sc + row * 4);
-        tc5::fence_after_sync();
         const uint64_t f2 = pack2(f, f);
-        constexpr int kChunk = Sh::kChunk, kParts = Sh::kCols / kChunk;
-        const uint32_t t0 = tcol + buf * Sh::kAccCols;
 #pragma unroll
         for (int x = 0; x < kParts; ++x) {
-          uint32_t v[kChunk];
-          tmem_ask<kChunk>(t0 + x * kChunk, v);
-          tmem_arrive<kChunk>(v);
+          tmem_arrive<kChunk>(v[x & 1]);
+          if (x + 1 < kParts) tmem_ask<kChunk>(t0 + (x + 1) * kChunk, v[(x + 1) & 1]);
           if (x + 1 == kParts) {  // the buffer is read: the next block's MMAs may have it
             tc5::fence_before_sync();
             __syncwarp();
-            if (lane == 0) {
-              if (kPair)
-                arrive_remote(cluster_addr(smem_u32(&sm.tempty[buf]), 0));
-              else
-                tc5::mbar_arrive(smem_u32(&sm.tempty[buf]));
-            }
+            if (lane == 0) tc5::mbar_arrive(smem_u32(&sm.tempty[buf]));
           }
 #pragma unroll
           for (int i = 0; i < kChunk; i += 4) {
-            const uint32_t* r = v + i;
+            const uint32_t* r = v[x & 1] + i;
             const int at = (x * kChunk + i) / 2;
             uint64_t s01 = f2, s23 = f2;
             if (kSwap) {
@@ -572,15 +510,9 @@ __global__ void __launch_bounds__(MmShape<NT, kSwap, kPair>::kThreads, MmShape<N
   }
   tc5::fence_before_sync();
   __syncthreads();
-  if (kPair) cluster_sync();  // the pair's MMAs and arrivals are over
   tc5::fence_after_sync();
   if (threadIdx.x == 0 && sm.abort && g.status) set_status(g.status, kStatusTimeout);
-  if (warp == 1) {
-    if constexpr (kPair)
-      pair_dealloc(tmem, Sh::kTmemCols);
-    else
-      tc5::tmem_dealloc(tmem, Sh::kTmemCols);
-  }
+  if (warp == 1) tc5::tmem_dealloc(tmem, Sh::kTmemCols);
 }
 
 bool make_mm_map(CUtensorMap* m, const void* ptr, uint64_t rows, uint64_t cols, uint64_t stride, uint32_t box_rows) {
@@ -595,31 +527,29 @@ bool make_mm_map(CUtensorMap* m, const void* ptr, uint64_t rows, uint64_t cols, 
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <int NT, bool kSwap, bool kPair, typename T>
+template <int NT, bool kSwap, typename T>
 int launch_shape(const MmArgs& g, int num_sms, cudaStream_t st, bool pdl) {
-  using Sh = MmShape<NT, kSwap, kPair>;
+  using Sh = MmShape<NT, kSwap>;
   CUtensorMap pmap, qmap;
   const bool ok = kSwap ? make_mm_map(&pmap, g.b, g.N, g.K, g.b_stride, 128) &&
                               make_mm_map(&qmap, g.a, g.M, g.K, g.a_stride, NT)
                         : make_mm_map(&pmap, g.a, g.M, g.K, g.a_stride, 128) &&
-                              make_mm_map(&qmap, g.b, g.N, g.K, g.b_stride, Sh::kQRows);
+                              make_mm_map(&qmap, g.b, g.N, g.K, g.b_stride, NT);
   if (!ok) return launch_fail("cuTensorMapEncodeTiled(a, b)", cudaSuccess);
-  auto kern = mm_kernel<NT, kSwap, kPair, T>;
+  auto kern = mm_kernel<NT, kSwap, T>;
   static PerDeviceOnce attr;
   if (const cudaError_t e = attr.run([&] { return allow_max_dynamic_smem(kern); }))
     return launch_fail("cudaFuncSetAttribute(mm_kernel)", e);
-  constexpr int kPTile = kPair ? 256 : 128;
-  const int ptiles = (int)(((int64_t)(kSwap ? g.N : g.M) + kPTile - 1) / kPTile), qtiles = (int)(((int64_t)(kSwap ? g.M : g.N) + NT - 1) / NT);
+  const int ptiles = (int)(((int64_t)(kSwap ? g.N : g.M) + 127) / 128), qtiles = (int)(((int64_t)(kSwap ? g.M : g.N) + NT - 1) / NT);
   const int64_t tiles = (int64_t)ptiles * qtiles;
   if (tiles > 0x7fffffff / 8) return launch_fail("too many tiles", cudaSuccess);
   const int slots = num_sms * Sh::kCtasPerSm;
   const int KB = (g.K + kMmBlock - 1) / kMmBlock;
   // a tile's blocks over the CTAs of a cluster while that still adds CTAs
   int split = 1;
-  while (!kPair && split < 8 && tiles * split * 2 <= slots && KB >= split * 2 * 2) split *= 2;
+  while (split < 8 && tiles * split * 2 <= slots && KB >= split * 2 * 2) split *= 2;
   // kSwap and split tiles leave through the ring's memory: one tile per cluster
-  const int64_t grid = kPair ? 2 * (tiles < slots / 2 ? tiles : slots / 2)
-                       : kSwap || split > 1 ? tiles * split : (tiles < slots ? tiles : slots);
+  const int64_t grid = kSwap || split > 1 ? tiles * split : (tiles < slots ? tiles : slots);
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)grid);
   cfg.blockDim = dim3(Sh::kThreads);
@@ -631,9 +561,9 @@ int launch_shape(const MmArgs& g, int num_sms, cudaStream_t st, bool pdl) {
     at[na].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     at[na++].val.programmaticStreamSerializationAllowed = 1;
   }
-  if (kPair || split > 1) {
+  if (split > 1) {
     at[na].id = cudaLaunchAttributeClusterDimension;
-    at[na].val.clusterDim.x = kPair ? 2 : split;
+    at[na].val.clusterDim.x = split;
     at[na].val.clusterDim.y = 1;
     at[na++].val.clusterDim.z = 1;
   }
@@ -645,14 +575,12 @@ int launch_shape(const MmArgs& g, int num_sms, cudaStream_t st, bool pdl) {
 
 template <typename T>
 int launch_out(const MmArgs& g, int num_sms, cudaStream_t st, bool pdl) {
-  if (g.M <= 16) return launch_shape<16, true, false, T>(g, num_sms, st, pdl);
-  if (g.M <= 32) return launch_shape<32, true, false, T>(g, num_sms, st, pdl);
-  if (g.M <= 64) return launch_shape<64, true, false, T>(g, num_sms, st, pdl);
-  // pairs on 256 x 256 tiles halve the reads of both operands, 128 x 128 tiles
-  // keep more SMs busy
-  const int64_t pairs = (int64_t)((g.M + 255) / 256) * ((g.N + 255) / 256);
-  return pairs >= num_sms / 2 ? launch_shape<256, false, true, T>(g, num_sms, st, pdl)
-                              : launch_shape<128, false, false, T>(g, num_sms, st, pdl);
+  if (g.M <= 16) return launch_shape<16, true, T>(g, num_sms, st, pdl);
+  if (g.M <= 32) return launch_shape<32, true, T>(g, num_sms, st, pdl);
+  if (g.M <= 64) return launch_shape<64, true, T>(g, num_sms, st, pdl);
+  // 256 columns per tile halve the reads of a, 128 keep more SMs busy
+  const int64_t tiles = (int64_t)((g.M + 127) / 128) * ((g.N + 255) / 256);
+  return tiles >= num_sms ? launch_shape<256, false, T>(g, num_sms, st, pdl) : launch_shape<128, false, T>(g, num_sms, st, pdl);
 }
 
 }  // namespace
