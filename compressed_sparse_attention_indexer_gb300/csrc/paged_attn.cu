@@ -10,11 +10,11 @@
 // stream of row copies.
 //
 // Split of the work.  A unit is (request, kv head, chunk of 16 MT query
-// rows); its cost is its number of 128-row tiles.  The units' tiles form one
+// rows); its cost is its number of tiles (128 or 256 rows).  The units' tiles form one
 // list, cut evenly over the CTAs (one per SM), so that a ragged batch or a
 // single long request fills the device alike; the lengths are read on the
 // device, so a captured graph follows them.  Within a tile each warp owns 16
-// rows: it copies them itself (16-byte cp.async into its own ring, several
+// or 32 rows: it copies them itself (16-byte cp.async into its own ring, several
 // tiles ahead, across unit boundaries), and keeps its own running maximum,
 // sum and output in registers: no barrier per tile.  At the end of a unit (or
 // of the CTA's share) the warps' states are joined through shared memory; a
@@ -24,7 +24,12 @@
 //
 // Scores, maxima, sums and O are fp32.  The weights are rounded to bf16 for
 // the PV product (the operand type: at most 2^-8 relative each, unbiased);
-// the sum l adds the unrounded ones, so lse is exact to fp32.
+// the sum l adds the unrounded ones, so lse is exact to fp32.  E4M3 codes are f16
+// values, so those pools take f16 products (a bf16 operand would cost three
+// more conversions per pair of codes: 765 instead of 548 us for 32 requests of
+// 16384 .. 32768 rows): a query row is scaled by a power of two to at most 2
+// (what then lies below 2^-14 is rounded to 2^-25 of the row's maximum), and the
+// weights include the V rows' scales.
 // Rows outside a query's range never reach its output: they are not loaded,
 // or their scores become -inf and, where another query of the same MMA sees
 // them, their V rows are masked out, so a NaN or infinity there stays there.
@@ -43,20 +48,25 @@ template <int D, int MT, bool kFp8>
 struct PaShape {
   static constexpr int kWarps = D == 256 ? 4 : 8;
   static constexpr int kThreads = 32 * kWarps;
-  static constexpr int kTile = 16 * kWarps;                      // rows per tile
-  static constexpr int kRows = 16 * MT;                          // query rows per unit
   static constexpr int kRowBytes = D * (kFp8 ? 1 : 2);
+  // rows a warp takes per tile: short rows take 32, so that the work per tile
+  // (maxima, look-ups) is spread over as many bytes
+  static constexpr int kPer = kRowBytes <= 128 ? 32 : 16;
+  static constexpr int kGroups = kPer / 16;
+  static constexpr int kTile = kPer * kWarps;                    // rows per tile
+  static constexpr int kRows = 16 * MT;                          // query rows per unit
   static constexpr int kChunks = kRowBytes / 16;                 // 16-byte chunks per row
-  static constexpr int kWarpStage = 2 * 16 * kRowBytes + (kFp8 ? 128 : 0);
+  static constexpr int kWarpStage = 2 * kPer * kRowBytes + (kFp8 ? 2 * kPer * 4 : 0);
+  static constexpr int kScaleBytes = kFp8 ? kPer * 16 : 0;       // per warp: the tile's scales as used
   static constexpr bool kQReg = MT == 1 && D <= 128;             // Q fragments in registers
-  static constexpr int kQBytes = kQReg ? 0 : kRows * D * 2;
+  static constexpr int kQBytes = kQReg ? 0 : kRows * D * 2 + (kFp8 ? kRows * 4 : 0);
   static constexpr int kSlots = kWarps / 2;
   static constexpr int kSlotFloats = kRows * D;
   static constexpr int kSlotBytes = kSlots * (kSlotFloats + 2 * kRows) * 4;
-  static constexpr int kRoom = (224 * 1024 - kQBytes - kSlotBytes) / (kWarps * kWarpStage);
+  static constexpr int kRoom = (224 * 1024 - kQBytes - kSlotBytes - kWarps * kScaleBytes) / (kWarps * kWarpStage);
   static constexpr int kStages = kRoom > 6 ? 6 : kRoom;
   static constexpr int kRing = kStages * kWarps * kWarpStage;
-  static constexpr int kSmem = kRing + kQBytes + kSlotBytes;
+  static constexpr int kSmem = kRing + kQBytes + kSlotBytes + kWarps * kScaleBytes;
   static_assert(kStages >= 2, "no room for two stages");
 };
 
@@ -73,23 +83,59 @@ __device__ __forceinline__ float fast_exp2(float x) {
   asm("ex2.approx.ftz.f32 %0, %1;\n" : "=f"(y) : "f"(x));
   return y;
 }
-// Two E4M3 codes (low byte first) to bf16x2, exactly.
-__device__ __forceinline__ uint32_t e4m3x2_to_bf16x2(uint32_t pair) {
+// Two E4M3 codes (low byte first) to f16x2: every E4M3 value is an f16 value.
+__device__ __forceinline__ uint32_t e4m3x2_to_f16x2(uint32_t pair) {
   uint32_t o;
-  asm("{\n .reg .b32 h2;\n .reg .b16 a, b, c;\n .reg .f32 fa, fb;\n cvt.u16.u32 c, %1;\n"
-      " cvt.rn.f16x2.e4m3x2 h2, c;\n mov.b32 {a, b}, h2;\n"
-      " cvt.f32.f16 fa, a;\n cvt.f32.f16 fb, b;\n cvt.rn.bf16x2.f32 %0, fb, fa;\n}\n"
-      : "=r"(o)
-      : "r"(pair));
+  asm("{\n .reg .b16 c;\n cvt.u16.u32 c, %1;\n cvt.rn.f16x2.e4m3x2 %0, c;\n}\n" : "=r"(o) : "r"(pair));
   return o;
+}
+// D += A(16x16 f16, row) * B(16x8 f16, col), fp32 accumulate.
+__device__ __forceinline__ void mma_f16_16816(float* d, const uint32_t* a, uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};\n"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+template <bool kFp8>
+__device__ __forceinline__ void mma16(float* d, const uint32_t* a, uint32_t b0, uint32_t b1) {
+  if (kFp8)
+    mma_f16_16816(d, a, b0, b1);
+  else
+    mma_bf16_16816(d, a, b0, b1);
+}
+__device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
+  const __half2 v = __floats2half2_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&v);
+}
+// The power of two in (max / 2, max], 1 for zero, subnormal and non-finite max.
+__device__ __forceinline__ float pow2_below(float max) {
+  const uint32_t e = __float_as_uint(max) >> 23;
+  return e >= 1 && e <= 253 ? __uint_as_float(e << 23) : 1.f;
+}
+// Two bf16 times inv (a power of two) as f16x2.
+__device__ __forceinline__ uint32_t bf16x2_to_f16x2(uint32_t v, float inv) {
+  return pack_f16x2(__uint_as_float(v << 16) * inv, __uint_as_float(v & 0xffff0000u) * inv);
+}
+__device__ __forceinline__ float fast_log2(float x) {
+  float y;
+  asm("lg2.approx.ftz.f32 %0, %1;\n" : "=f"(y) : "f"(x));
+  return y;
 }
 __device__ __forceinline__ void cp_async4(uint32_t dst, const void* src, int src_bytes) {
   asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;\n" ::"r"(dst), "l"(src), "r"(src_bytes) : "memory");
 }
 __device__ __forceinline__ float lds_f32(uint32_t a) {
   float v;
-  asm volatile("ld.shared.f32 %0, [%1];\n" : "=f"(v) : "r"(a));
+  asm volatile("ld.shared.f32 %0, [%1];\n" : "=f"(v) : "r"(a) : "memory");
   return v;
+}
+__device__ __forceinline__ float4 lds_f4(uint32_t a) {
+  float4 v;
+  asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];\n" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(a) : "memory");
+  return v;
+}
+__device__ __forceinline__ void sts_f4(uint32_t a, float x, float y, float z, float w) {
+  asm volatile("st.shared.v4.f32 [%0], {%1, %2, %3, %4};\n" ::"r"(a), "f"(x), "f"(y), "f"(z), "f"(w) : "memory");
 }
 __device__ __forceinline__ uint4 lds_u4(uint32_t a) {
   uint4 v;
@@ -144,7 +190,7 @@ template <int D, int MT, bool kFp8>
 __global__ void __launch_bounds__(PaShape<D, MT, kFp8>::kThreads, 1)
     paged_attn_kernel(const PagedArgs a, int chunks, float* __restrict__ part, PaJoin* __restrict__ joins) {
   using Sh = PaShape<D, MT, kFp8>;
-  constexpr int kTile = Sh::kTile;
+  constexpr int kTile = Sh::kTile, kPer = Sh::kPer, kGroups = Sh::kGroups;
   extern __shared__ __align__(128) uint8_t smem_raw[];
   __shared__ int scan_tmp[33];
   __shared__ int64_t start_at;
@@ -153,6 +199,7 @@ __global__ void __launch_bounds__(PaShape<D, MT, kFp8>::kThreads, 1)
   const uint32_t ring = smem_u32(smem_raw) + warp * (Sh::kStages * Sh::kWarpStage);
   const uint32_t qsm = smem_u32(smem_raw) + Sh::kRing;
   float* slots = reinterpret_cast<float*>(smem_raw + Sh::kRing + Sh::kQBytes);
+  const uint32_t rowsc = smem_u32(smem_raw) + Sh::kRing + Sh::kQBytes + Sh::kSlotBytes + warp * Sh::kScaleBytes;
   const int group = a.heads / a.kv_heads;
   const int qrows = a.S * group;                    // query rows per kv head
   const int units = a.kv_heads * chunks;
@@ -199,13 +246,13 @@ __global__ void __launch_bounds__(PaShape<D, MT, kFp8>::kThreads, 1)
   const int steps = (int)(hi - lo);
   int loaded = 0;
 
-  // ---- row copies: lane r < 16 looks up the pool row of the warp's row r,
+  // ---- row copies: lane r < kPer looks up the pool row of the warp's row r,
   // one tile ahead of the copies that use it (-1: nothing to read)
   int prow = -1;
   auto lookup = [&](const Cursor<kTile>& c) {
     int p = -1;
-    if (lane < 16) {
-      const int r = (c.sp.t0 + c.tile) * kTile + warp * 16 + lane;
+    if (lane < kPer) {
+      const int r = (c.sp.t0 + c.tile) * kTile + warp * kPer + lane;
       if (r >= c.sp.lo && r < c.sp.L) {
         const int64_t x = pool_row(a.table, a.block, a.table_stride, a.off, c.b, r);
         if (x >= 0 && x < a.rows) p = (int)x;
@@ -215,13 +262,13 @@ __global__ void __launch_bounds__(PaShape<D, MT, kFp8>::kThreads, 1)
     return p;
   };
   auto copy = [&](int stage) {
-    const uint32_t kdst = ring + stage * Sh::kWarpStage, vdst = kdst + 16 * Sh::kRowBytes;
+    const uint32_t kdst = ring + stage * Sh::kWarpStage, vdst = kdst + kPer * Sh::kRowBytes;
     const int h = ld.unit / chunks;
     constexpr int kSpan = Sh::kChunks > 32 ? 32 : Sh::kChunks;           // lanes per row and copy
-    constexpr int kPer = 32 / kSpan;                                     // rows per warp-wide copy
+    constexpr int kAtOnce = 32 / kSpan;                                  // rows per warp-wide copy
 #pragma unroll
-    for (int i = 0; i < 16 / kPer; ++i) {
-      const int row = i * kPer + lane / kSpan, ch = lane % kSpan;
+    for (int i = 0; i < kPer / kAtOnce; ++i) {
+      const int row = i * kAtOnce + lane / kSpan, ch = lane % kSpan;
       const int p = __shfl_sync(0xffffffffu, prow, row);
       const int64_t x = p < 0 ? 0 : p;
       const uint32_t at = row * Sh::kRowBytes + swizzle<kFp8>(row, ch) * 16;
@@ -231,10 +278,11 @@ __global__ void __launch_bounds__(PaShape<D, MT, kFp8>::kThreads, 1)
       cp_async16(kdst + at, ks, p < 0 ? 0 : 16);
       cp_async16(vdst + at, vs, p < 0 ? 0 : 16);
     }
-    if (kFp8) {  // lanes 0..15: K scales, 16..31: V scales
-      const int p = __shfl_sync(0xffffffffu, prow, lane & 15);
-      const float* s = (lane < 16 ? a.k_scale : a.v_scale) + (int64_t)(p < 0 ? 0 : p) * a.scale_stride + h;
-      cp_async4(kdst + 32 * Sh::kRowBytes + lane * 4, s, p < 0 ? 0 : 4);
+    if (kFp8) {  // the rows' K scales, then their V scales
+      const int64_t at = (int64_t)(prow < 0 ? 0 : prow) * a.scale_stride + h;
+      const uint32_t dst = kdst + 2 * kPer * Sh::kRowBytes + lane * 4;
+      cp_async4(dst, a.k_scale + at, prow < 0 ? 0 : 4);
+      cp_async4(dst + kPer * 4, a.v_scale + at, prow < 0 ? 0 : 4);
     }
   };
   auto load_step = [&] {
@@ -255,6 +303,7 @@ __global__ void __launch_bounds__(PaShape<D, MT, kFp8>::kThreads, 1)
   // ---- per-unit state
   const int g = lane >> 2, c = lane & 3;
   uint32_t qf[Sh::kQReg ? D / 16 : 1][4];
+  float qmul[MT][2];                               // E4M3: the power of two taken out of the thread's query rows
   float o[MT][D / 8][4], m[MT][2], l[MT][2];
   int pos[MT][2], sq[MT][2];                       // last visible row and token of the thread's query rows
   int seg_first = 0;                               // step at which the current piece started
@@ -303,29 +352,77 @@ __global__ void __launch_bounds__(PaShape<D, MT, kFp8>::kThreads, 1)
               qf[ks][2 + e] = in ? *reinterpret_cast<const uint32_t*>(q + ks * 16 + 8 + c * 2) : 0;
             }
           }
+          if constexpr (kFp8) {
+            float top = 0.f;
+#pragma unroll
+            for (int ks = 0; ks < D / 16; ++ks)
+#pragma unroll
+              for (int x = e; x < 4; x += 2)
+                top = fmaxf(top, fmaxf(fabsf(__uint_as_float(qf[ks][x] << 16)), fabsf(__uint_as_float(qf[ks][x] & 0xffff0000u))));
+            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+            const float two = pow2_below(top);
+            qmul[0][e] = two;
+#pragma unroll
+            for (int ks = 0; ks < D / 16; ++ks)
+#pragma unroll
+              for (int x = e; x < 4; x += 2) qf[ks][x] = bf16x2_to_f16x2(qf[ks][x], 1.f / two);
+          }
         }
       } else {
         for (int x = tid; x < Sh::kRows * (D / 8); x += Sh::kThreads) {
           const int r = x / (D / 8), ch = x % (D / 8);
           uint4 v = make_uint4(0, 0, 0, 0);
           if (row0 + r < qrows) v = *reinterpret_cast<const uint4*>(q_at(row0 + r) + ch * 8);
+          if constexpr (kFp8) {  // D = 128: a row is 16 neighbouring lanes
+            uint32_t* w = reinterpret_cast<uint32_t*>(&v);
+            float top = 0.f;
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+              top = fmaxf(top, fmaxf(fabsf(__uint_as_float(w[i] << 16)), fabsf(__uint_as_float(w[i] & 0xffff0000u))));
+#pragma unroll
+            for (int i = 8; i > 0; i >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, i));
+            const float two = pow2_below(top);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) w[i] = bf16x2_to_f16x2(w[i], 1.f / two);
+            if (ch == 0) *reinterpret_cast<float*>(smem_raw + Sh::kRing + Sh::kRows * D * 2 + r * 4) = two;
+          }
           *reinterpret_cast<uint4*>(smem_raw + Sh::kRing + r * D * 2 + ((ch ^ (r & 7)) * 16)) = v;
         }
         __syncthreads();
+        if constexpr (kFp8) {
+#pragma unroll
+          for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) qmul[mt][e] = lds_f32(qsm + Sh::kRows * D * 2 + (mt * 16 + g + 8 * e) * 4);
+        }
       }
     }
     load_step();
     cp_async_wait<Sh::kStages - 1>();
     __syncwarp();
-    const uint32_t kt = ring + (step % Sh::kStages) * Sh::kWarpStage, vt = kt + 16 * Sh::kRowBytes;
-    const int base = (cu.sp.t0 + cu.tile) * kTile + warp * 16;   // first row of the warp's 16
-    if (base < cu.sp.L && base + 15 >= cu.sp.lo) {
-      // ---- S = Q K^T: 16 MT query rows x 16 rows (two n = 8 tiles)
-      float s[MT][2][4];
+    const uint32_t kt = ring + (step % Sh::kStages) * Sh::kWarpStage, vt = kt + kPer * Sh::kRowBytes;
+    const int base = (cu.sp.t0 + cu.tile) * kTile + warp * kPer;   // first of the warp's rows
+    if (base < cu.sp.L && base + kPer - 1 >= cu.sp.lo) {
+      if constexpr (kFp8) {
+        // lane r: its row's scales as the scores and weights use them.  The
+        // weight of a V row is p |v_scale|, so v_scale goes into the exponent
+        // (lv) and the maximum is taken over both: the f16 weights then keep
+        // their precision whatever the scales.  The softmax's own sum takes
+        // the factor out again (1 / |v_scale|).  |v_scale| below 2^-100 counts
+        // as 2^-100 there, and the rest of it is kept in the sign factor.
+        const uint32_t src = kt + 2 * kPer * Sh::kRowBytes + lane * 4;
+        const float ks = lds_f32(src) * scale2, vs = lds_f32(src + kPer * 4);
+        const float lv = fast_log2(fmaxf(fabsf(vs), 7.8886091e-31f)), inv = fast_exp2(-lv);
+        sts_f4(rowsc + lane * 16, ks, vs == vs ? lv : vs, inv, vs * inv);
+        __syncwarp();
+      }
+      // ---- S = Q K^T: 16 MT query rows x kPer rows (n = 8 tiles)
+      float s[MT][2 * kGroups][4];
 #pragma unroll
       for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
-        for (int n = 0; n < 2; ++n) s[mt][n][0] = s[mt][n][1] = s[mt][n][2] = s[mt][n][3] = 0.f;
+        for (int n = 0; n < 2 * kGroups; ++n) s[mt][n][0] = s[mt][n][1] = s[mt][n][2] = s[mt][n][3] = 0.f;
       auto q_frag = [&](int mt, int ks, uint32_t* f) {
         if constexpr (Sh::kQReg) {
 #pragma unroll
@@ -349,80 +446,82 @@ __global__ void __launch_bounds__(PaShape<D, MT, kFp8>::kThreads, 1)
         // (q's fragments above take the same dims).
 #pragma unroll
         for (int j = 0; j < D / 64; ++j) {
-          uint32_t w[2][4];
+          uint32_t w[2 * kGroups][4];
 #pragma unroll
-          for (int n = 0; n < 2; ++n) {
+          for (int n = 0; n < 2 * kGroups; ++n) {
             const int r = n * 8 + g;
             const uint4 v = lds_u4(kt + r * Sh::kRowBytes + swizzle<true>(r, j * 4 + c) * 16);
             w[n][0] = v.x; w[n][1] = v.y; w[n][2] = v.z; w[n][3] = v.w;
           }
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
-            uint32_t b[2][2];
+            uint32_t f[MT][4];
 #pragma unroll
-            for (int n = 0; n < 2; ++n) {
-              b[n][0] = e4m3x2_to_bf16x2(w[n][i]);
-              b[n][1] = e4m3x2_to_bf16x2(w[n][i] >> 16);
-            }
+            for (int mt = 0; mt < MT; ++mt) q_frag(mt, j * 4 + i, f[mt]);
 #pragma unroll
-            for (int mt = 0; mt < MT; ++mt) {
-              uint32_t f[4];
-              q_frag(mt, j * 4 + i, f);
-              mma_bf16_16816(s[mt][0], f, b[0][0], b[0][1]);
-              mma_bf16_16816(s[mt][1], f, b[1][0], b[1][1]);
+            for (int n = 0; n < 2 * kGroups; ++n) {
+              const uint32_t b0 = e4m3x2_to_f16x2(w[n][i]), b1 = e4m3x2_to_f16x2(w[n][i] >> 16);
+#pragma unroll
+              for (int mt = 0; mt < MT; ++mt) mma16<true>(s[mt][n], f[mt], b0, b1);
             }
           }
         }
       } else {
 #pragma unroll
         for (int ks = 0; ks < D / 16; ++ks) {
-          const int r = ((lane >> 4) << 3) + (lane & 7), ch = ks * 2 + ((lane >> 3) & 1);
-          uint32_t b0, b1, b2, b3;
-          ldsm_x4(kt + r * Sh::kRowBytes + swizzle<false>(r, ch) * 16, b0, b1, b2, b3);
+          uint32_t f[MT][4];
 #pragma unroll
-          for (int mt = 0; mt < MT; ++mt) {
-            uint32_t f[4];
-            q_frag(mt, ks, f);
-            mma_bf16_16816(s[mt][0], f, b0, b1);
-            mma_bf16_16816(s[mt][1], f, b2, b3);
+          for (int mt = 0; mt < MT; ++mt) q_frag(mt, ks, f[mt]);
+#pragma unroll
+          for (int x = 0; x < kGroups; ++x) {
+            const int r = x * 16 + ((lane >> 4) << 3) + (lane & 7), ch = ks * 2 + ((lane >> 3) & 1);
+            uint32_t b0, b1, b2, b3;
+            ldsm_x4(kt + r * Sh::kRowBytes + swizzle<false>(r, ch) * 16, b0, b1, b2, b3);
+#pragma unroll
+            for (int mt = 0; mt < MT; ++mt) {
+              mma16<false>(s[mt][2 * x], f[mt], b0, b1);
+              mma16<false>(s[mt][2 * x + 1], f[mt], b2, b3);
+            }
           }
         }
       }
       // ---- scores in log2 units; rows outside a query's range weigh nothing
-      float ksc[2][2], vsc[2][2];
+      const int p_first = cu.sp.L - a.S;   // the first token's position
+      const bool edge = base < cu.sp.lo || base + kPer - 1 > p_first ||
+                        (a.win > 0 && base < cu.sp.L - a.win);  // some query does not see all the rows
+      uint32_t pf[MT][kGroups][4];
+      float inv[2 * kGroups][2], sgn[2 * kGroups][2];           // E4M3: 1 / |v_scale| and its sign
 #pragma unroll
-      for (int n = 0; n < 2; ++n)
+      for (int n = 0; n < 2 * kGroups; ++n)
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
-          ksc[n][e] = scale2;
-          vsc[n][e] = 1.f;
-          if (kFp8) {
-            const uint32_t sc = kt + 32 * Sh::kRowBytes + (n * 8 + c * 2 + e) * 4;
-            ksc[n][e] *= lds_f32(sc);
-            vsc[n][e] = lds_f32(sc + 64);
+          float ks = scale2, lv = 0.f;
+          inv[n][e] = sgn[n][e] = 1.f;
+          if constexpr (kFp8) {
+            const float4 t = lds_f4(rowsc + (n * 8 + c * 2 + e) * 16);
+            ks = t.x, lv = t.y, inv[n][e] = t.z, sgn[n][e] = t.w;
           }
+#pragma unroll
+          for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+            for (int y = 0; y < 2; ++y) {
+              float x = s[mt][n][2 * y + e];
+              x = kFp8 ? fmaf(x, ks * qmul[mt][y], lv) : x * ks;
+              if (edge) {
+                const int r = base + n * 8 + c * 2 + e, last = pos[mt][y];
+                if (r > last || (a.win > 0 && r <= last - a.win)) x = -INFINITY;
+              }
+              s[mt][n][2 * y + e] = x;
+            }
         }
-      const int p_first = cu.sp.L - a.S;   // the first token's position
-      const bool edge = base < cu.sp.lo || base + 15 > p_first ||
-                        (a.win > 0 && base < cu.sp.L - a.win);  // some query does not see all 16 rows
-      uint32_t pf[MT][4];
 #pragma unroll
       for (int mt = 0; mt < MT; ++mt) {
-#pragma unroll
-        for (int n = 0; n < 2; ++n)
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            float x = s[mt][n][i] * ksc[n][i & 1];
-            if (edge) {
-              const int r = base + n * 8 + c * 2 + (i & 1), last = pos[mt][i >> 1];
-              if (r > last || (a.win > 0 && r <= last - a.win)) x = -INFINITY;
-            }
-            s[mt][n][i] = x;
-          }
         float top[2];
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
-          float t = fmaxf(fmaxf(s[mt][0][2 * e], s[mt][0][2 * e + 1]), fmaxf(s[mt][1][2 * e], s[mt][1][2 * e + 1]));
+          float t = fmaxf(s[mt][0][2 * e], s[mt][0][2 * e + 1]);
+#pragma unroll
+          for (int n = 1; n < 2 * kGroups; ++n) t = fmaxf(t, fmaxf(s[mt][n][2 * e], s[mt][n][2 * e + 1]));
           t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, 1));
           top[e] = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, 2));
         }
@@ -442,43 +541,40 @@ __global__ void __launch_bounds__(PaShape<D, MT, kFp8>::kThreads, 1)
             }
           }
         }
-        float p[2][4];
 #pragma unroll
-        for (int n = 0; n < 2; ++n)
+        for (int x = 0; x < kGroups; ++x) {
+          float p[2][4];
+#pragma unroll
+          for (int n = 0; n < 2; ++n)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const float ref = m[mt][i >> 1] == -INFINITY ? 0.f : m[mt][i >> 1];
+              const float w = fast_exp2(s[mt][2 * x + n][i] - ref);
+              if (kFp8) {  // a row that weighs nothing stays at zero whatever its scale
+                l[mt][i >> 1] += w == 0.f ? 0.f : w * inv[2 * x + n][i & 1];
+                p[n][i] = w == 0.f ? 0.f : w * sgn[2 * x + n][i & 1];
+              } else {
+                l[mt][i >> 1] += w;
+                p[n][i] = w;
+              }
+            }
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
-            const float ref = m[mt][i >> 1] == -INFINITY ? 0.f : m[mt][i >> 1];
-            p[n][i] = fast_exp2(s[mt][n][i] - ref);
-            l[mt][i >> 1] += p[n][i];
-            // a row that weighs nothing stays at zero whatever its scale
-            if (kFp8) p[n][i] = p[n][i] == 0.f ? 0.f : p[n][i] * vsc[n][i & 1];
+            const float x0 = p[i >> 1][(i & 1) * 2], x1 = p[i >> 1][(i & 1) * 2 + 1];
+            pf[mt][x][i] = kFp8 ? pack_f16x2(x0, x1) : pack_bf16x2(x0, x1);
           }
-        pf[mt][0] = pack_bf16x2(p[0][0], p[0][1]);
-        pf[mt][1] = pack_bf16x2(p[0][2], p[0][3]);
-        pf[mt][2] = pack_bf16x2(p[1][0], p[1][1]);
-        pf[mt][3] = pack_bf16x2(p[1][2], p[1][3]);
+        }
       }
       // ---- O += P V.  Where tokens of one MMA see different rows (S > 1 at
       // an end of their ranges), one pass per token with its own V rows kept
       // and its own query rows added (a zero weight times a NaN is a NaN).
       const int passes = edge && a.S > 1 ? a.S : 1;
       for (int t = 0; t < passes; ++t) {
-        uint32_t keep[2] = {0xffffffffu, 0xffffffffu};
-        auto pv = [&](int mt, int j, uint32_t b0, uint32_t b1) {
-          if (passes == 1) {
-            mma_bf16_16816(o[mt][j], pf[mt], b0, b1);
-          } else {
-            float x[4] = {0.f, 0.f, 0.f, 0.f};
-            mma_bf16_16816(x, pf[mt], b0 & keep[0], b1 & keep[1]);
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-              if (sq[mt][i >> 1] == t) o[mt][j][i] += x[i];
-          }
-        };
+        uint32_t keep[2 * kGroups];
         if (passes > 1) {
           const int last = p_first + t;
 #pragma unroll
-          for (int n = 0; n < 2; ++n) {
+          for (int n = 0; n < 2 * kGroups; ++n) {
             keep[n] = 0;
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
@@ -487,37 +583,51 @@ __global__ void __launch_bounds__(PaShape<D, MT, kFp8>::kThreads, 1)
             }
           }
         }
-        if constexpr (kFp8) {
-          // n-tile j holds dims 16 n + j (n = 0..7): thread g takes codes 16 g .. 16 g + 15 of its four rows
-          uint32_t w[4][4];
+        auto pv = [&](int mt, int x, int j, uint32_t b0, uint32_t b1) {
+          if (passes == 1) {
+            mma16<kFp8>(o[mt][j], pf[mt][x], b0, b1);
+          } else {
+            float y[4] = {0.f, 0.f, 0.f, 0.f};
+            mma16<kFp8>(y, pf[mt][x], b0 & keep[2 * x], b1 & keep[2 * x + 1]);
 #pragma unroll
-          for (int x = 0; x < 4; ++x) {
-            const int r = (x >> 1) * 8 + c * 2 + (x & 1);
-            const uint4 v = lds_u4(vt + r * Sh::kRowBytes + swizzle<true>(r, g) * 16);
-            w[x][0] = v.x; w[x][1] = v.y; w[x][2] = v.z; w[x][3] = v.w;
+            for (int i = 0; i < 4; ++i)
+              if (sq[mt][i >> 1] == t) o[mt][j][i] += y[i];
           }
+        };
 #pragma unroll
-          for (int y = 0; y < 4; ++y) {
-            const uint32_t lo01 = __byte_perm(w[0][y], w[1][y], 0x5140), hi01 = __byte_perm(w[0][y], w[1][y], 0x7362);
-            const uint32_t lo23 = __byte_perm(w[2][y], w[3][y], 0x5140), hi23 = __byte_perm(w[2][y], w[3][y], 0x7362);
+        for (int x = 0; x < kGroups; ++x) {
+          if constexpr (kFp8) {
+            // n-tile j holds dims 16 n + j (n = 0..7): thread g takes codes 16 g .. 16 g + 15 of its four rows
+            uint32_t w[4][4];
 #pragma unroll
             for (int z = 0; z < 4; ++z) {
-              const uint32_t b0 = e4m3x2_to_bf16x2((z < 2 ? lo01 : hi01) >> (16 * (z & 1)));
-              const uint32_t b1 = e4m3x2_to_bf16x2((z < 2 ? lo23 : hi23) >> (16 * (z & 1)));
-#pragma unroll
-              for (int mt = 0; mt < MT; ++mt) pv(mt, y * 4 + z, b0, b1);
+              const int r = x * 16 + (z >> 1) * 8 + c * 2 + (z & 1);
+              const uint4 v = lds_u4(vt + r * Sh::kRowBytes + swizzle<true>(r, g) * 16);
+              w[z][0] = v.x; w[z][1] = v.y; w[z][2] = v.z; w[z][3] = v.w;
             }
-          }
-        } else {
 #pragma unroll
-          for (int dt = 0; dt < D / 16; ++dt) {
-            const int r = (((lane >> 3) & 1) << 3) + (lane & 7), ch = dt * 2 + (lane >> 4);
-            uint32_t b0, b1, b2, b3;
-            ldsm_x4_trans(vt + r * Sh::kRowBytes + swizzle<false>(r, ch) * 16, b0, b1, b2, b3);
+            for (int y = 0; y < 4; ++y) {
+              const uint32_t lo01 = __byte_perm(w[0][y], w[1][y], 0x5140), hi01 = __byte_perm(w[0][y], w[1][y], 0x7362);
+              const uint32_t lo23 = __byte_perm(w[2][y], w[3][y], 0x5140), hi23 = __byte_perm(w[2][y], w[3][y], 0x7362);
 #pragma unroll
-            for (int mt = 0; mt < MT; ++mt) {
-              pv(mt, dt * 2, b0, b1);
-              pv(mt, dt * 2 + 1, b2, b3);
+              for (int z = 0; z < 4; ++z) {
+                const uint32_t b0 = e4m3x2_to_f16x2((z < 2 ? lo01 : hi01) >> (16 * (z & 1)));
+                const uint32_t b1 = e4m3x2_to_f16x2((z < 2 ? lo23 : hi23) >> (16 * (z & 1)));
+#pragma unroll
+                for (int mt = 0; mt < MT; ++mt) pv(mt, x, y * 4 + z, b0, b1);
+              }
+            }
+          } else {
+#pragma unroll
+            for (int dt = 0; dt < D / 16; ++dt) {
+              const int r = x * 16 + (((lane >> 3) & 1) << 3) + (lane & 7), ch = dt * 2 + (lane >> 4);
+              uint32_t b0, b1, b2, b3;
+              ldsm_x4_trans(vt + r * Sh::kRowBytes + swizzle<false>(r, ch) * 16, b0, b1, b2, b3);
+#pragma unroll
+              for (int mt = 0; mt < MT; ++mt) {
+                pv(mt, x, dt * 2, b0, b1);
+                pv(mt, x, dt * 2 + 1, b2, b3);
+              }
             }
           }
         }
