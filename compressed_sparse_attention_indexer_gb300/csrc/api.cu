@@ -892,6 +892,9 @@ int csa_paged_attn(const csa_paged* a, void* stream) {
   if (!rc) rc = check_rows("k", a->k, a->k_stride, (int64_t)a->kv_heads * a->dim, fp8 ? 1 : 2);
   if (!rc) rc = check_rows("v", a->v, a->v_stride, (int64_t)a->kv_heads * a->dim, fp8 ? 1 : 2);
   if (rc) return rc;
+  if (a->k_stride >= (int64_t(1) << 31) / (fp8 ? 1 : 2) || a->v_stride >= (int64_t(1) << 31) / (fp8 ? 1 : 2) ||
+      a->q_stride >= (int64_t(1) << 40) || a->out_stride >= (int64_t(1) << 40))
+    return fail(CSA_ERR_UNSUPPORTED, "pool rows more than 2 GB apart");
   if (a->rows < 0 || a->rows > 0x7fffffff) return fail(CSA_ERR_INVALID_ARG, "rows outside [0, 2^31)");
   if (!a->ctx_len) return fail(CSA_ERR_INVALID_ARG, "ctx_len is NULL");
   if (fp8) {
@@ -919,7 +922,8 @@ int csa_paged_attn(const csa_paged* a, void* stream) {
   k.scale = a->softmax_scale > 0.f ? a->softmax_scale : (float)(1.0 / sqrt((double)a->dim));
   k.ctx_len = a->ctx_len;
   k.q = a->q; k.q_stride = a->q_stride;
-  k.k = a->k; k.v = a->v; k.k_stride = a->k_stride; k.v_stride = a->v_stride; k.rows = a->rows;
+  k.k = a->k; k.v = a->v; k.k_step = (uint32_t)(a->k_stride * (fp8 ? 1 : 2));
+  k.v_step = (uint32_t)(a->v_stride * (fp8 ? 1 : 2)); k.rows = a->rows;
   k.k_scale = a->k_scale; k.v_scale = a->v_scale; k.scale_stride = a->scale_stride;
   k.off = a->off; k.table = a->table; k.block = a->block; k.table_stride = a->table_stride;
   k.out = a->out; k.out_stride = a->out_stride; k.lse = a->lse; k.status = a->status;

@@ -399,13 +399,14 @@ struct MmArgs {
 };
 int launch_fp8_matmul(const MmArgs& g, int out_dtype, int num_sms, cudaStream_t st, bool pdl);
 // Dense attention over paged K / V pools (csa_paged_attn): the arguments of
-// csa_paged with checked pointers; strides in elements of the pool.
+// csa_paged with checked pointers.  k_step, v_step: bytes from one pool row to
+// the next (below 2^32); the other strides in elements.
 struct PagedArgs {
   int B, S, heads, kv_heads, dim, win, max_len;
   float scale;
   const int* ctx_len;
   const void* q; int64_t q_stride;
-  const void* k; const void* v; int64_t k_stride, v_stride, rows;
+  const void* k; const void* v; uint32_t k_step, v_step; int64_t rows;
   const float* k_scale; const float* v_scale; int64_t scale_stride;
   const int64_t* off;
   const int* table; int block, table_stride;

@@ -83,11 +83,11 @@ __device__ __forceinline__ float fast_exp2(float x) {
   asm("ex2.approx.ftz.f32 %0, %1;\n" : "=f"(y) : "f"(x));
   return y;
 }
-// Two E4M3 codes (low byte first) to f16x2: every E4M3 value is an f16 value.
-__device__ __forceinline__ uint32_t e4m3x2_to_f16x2(uint32_t pair) {
-  uint32_t o;
-  asm("{\n .reg .b16 c;\n cvt.u16.u32 c, %1;\n cvt.rn.f16x2.e4m3x2 %0, c;\n}\n" : "=r"(o) : "r"(pair));
-  return o;
+// Four E4M3 codes (low byte first) to two f16x2: every E4M3 value is an f16 value.
+__device__ __forceinline__ void e4m3x4_to_f16x2(uint32_t w, uint32_t& lo, uint32_t& hi) {
+  asm("{\n .reg .b16 a, b;\n mov.b32 {a, b}, %2;\n cvt.rn.f16x2.e4m3x2 %0, a;\n cvt.rn.f16x2.e4m3x2 %1, b;\n}\n"
+      : "=r"(lo), "=r"(hi)
+      : "r"(w));
 }
 // D += A(16x16 f16, row) * B(16x8 f16, col), fp32 accumulate.
 __device__ __forceinline__ void mma_f16_16816(float* d, const uint32_t* a, uint32_t b0, uint32_t b1) {
@@ -266,17 +266,17 @@ __global__ void __launch_bounds__(PaShape<D, MT, kFp8>::kThreads, 1)
     const int h = ld.unit / chunks;
     constexpr int kSpan = Sh::kChunks > 32 ? 32 : Sh::kChunks;           // lanes per row and copy
     constexpr int kAtOnce = 32 / kSpan;                                  // rows per warp-wide copy
+    const int ch = lane % kSpan, r0 = lane / kSpan;
+    const uint8_t* kb = static_cast<const uint8_t*>(a.k) + (h * Sh::kRowBytes + ch * 16);
+    const uint8_t* vb = static_cast<const uint8_t*>(a.v) + (h * Sh::kRowBytes + ch * 16);
 #pragma unroll
     for (int i = 0; i < kPer / kAtOnce; ++i) {
-      const int row = i * kAtOnce + lane / kSpan, ch = lane % kSpan;
+      const int row = i * kAtOnce + r0;
       const int p = __shfl_sync(0xffffffffu, prow, row);
-      const int64_t x = p < 0 ? 0 : p;
-      const uint32_t at = row * Sh::kRowBytes + swizzle<kFp8>(row, ch) * 16;
-      constexpr int es = kFp8 ? 1 : 2;
-      const uint8_t* ks = static_cast<const uint8_t*>(a.k) + (x * a.k_stride + h * D) * es + ch * 16;
-      const uint8_t* vs = static_cast<const uint8_t*>(a.v) + (x * a.v_stride + h * D) * es + ch * 16;
-      cp_async16(kdst + at, ks, p < 0 ? 0 : 16);
-      cp_async16(vdst + at, vs, p < 0 ? 0 : 16);
+      const uint32_t x = p < 0 ? 0u : (uint32_t)p, at = row * Sh::kRowBytes + swizzle<kFp8>(row, ch) * 16;
+      const int bytes = p < 0 ? 0 : 16;
+      cp_async16(kdst + at, kb + (uint64_t)x * (uint32_t)a.k_step, bytes);
+      cp_async16(vdst + at, vb + (uint64_t)x * (uint32_t)a.v_step, bytes);
     }
     if (kFp8) {  // the rows' K scales, then their V scales
       const int64_t at = (int64_t)(prow < 0 ? 0 : prow) * a.scale_stride + h;
@@ -414,7 +414,11 @@ __global__ void __launch_bounds__(PaShape<D, MT, kFp8>::kThreads, 1)
         const uint32_t src = kt + 2 * kPer * Sh::kRowBytes + lane * 4;
         const float ks = lds_f32(src) * scale2, vs = lds_f32(src + kPer * 4);
         const float lv = fast_log2(fmaxf(fabsf(vs), 7.8886091e-31f)), inv = fast_exp2(-lv);
-        sts_f4(rowsc + lane * 16, ks, vs == vs ? lv : vs, inv, vs * inv);
+        // a v_scale that is no number reaches whoever sees the row by its exponent alone
+        if (fabsf(vs) < INFINITY)
+          sts_f4(rowsc + lane * 16, ks, lv, inv, vs * inv);
+        else
+          sts_f4(rowsc + lane * 16, ks, __uint_as_float(0x7fffffffu), 1.f, 1.f);
         __syncwarp();
       }
       // ---- S = Q K^T: 16 MT query rows x kPer rows (n = 8 tiles)
@@ -460,7 +464,8 @@ __global__ void __launch_bounds__(PaShape<D, MT, kFp8>::kThreads, 1)
             for (int mt = 0; mt < MT; ++mt) q_frag(mt, j * 4 + i, f[mt]);
 #pragma unroll
             for (int n = 0; n < 2 * kGroups; ++n) {
-              const uint32_t b0 = e4m3x2_to_f16x2(w[n][i]), b1 = e4m3x2_to_f16x2(w[n][i] >> 16);
+              uint32_t b0, b1;
+              e4m3x4_to_f16x2(w[n][i], b0, b1);
 #pragma unroll
               for (int mt = 0; mt < MT; ++mt) mma16<true>(s[mt][n], f[mt], b0, b1);
             }
@@ -505,15 +510,21 @@ __global__ void __launch_bounds__(PaShape<D, MT, kFp8>::kThreads, 1)
           for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
             for (int y = 0; y < 2; ++y) {
-              float x = s[mt][n][2 * y + e];
-              x = kFp8 ? fmaf(x, ks * qmul[mt][y], lv) : x * ks;
-              if (edge) {
-                const int r = base + n * 8 + c * 2 + e, last = pos[mt][y];
-                if (r > last || (a.win > 0 && r <= last - a.win)) x = -INFINITY;
-              }
-              s[mt][n][2 * y + e] = x;
+              const float x = s[mt][n][2 * y + e];
+              s[mt][n][2 * y + e] = kFp8 ? fmaf(x, ks * qmul[mt][y], lv) : x * ks;
             }
         }
+      if (edge) {
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+          for (int n = 0; n < 2 * kGroups; ++n)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const int r = base + n * 8 + c * 2 + (i & 1), last = pos[mt][i >> 1];
+              if (r > last || (a.win > 0 && r <= last - a.win)) s[mt][n][i] = -INFINITY;
+            }
+      }
 #pragma unroll
       for (int mt = 0; mt < MT; ++mt) {
         float top[2];
@@ -550,13 +561,8 @@ __global__ void __launch_bounds__(PaShape<D, MT, kFp8>::kThreads, 1)
             for (int i = 0; i < 4; ++i) {
               const float ref = m[mt][i >> 1] == -INFINITY ? 0.f : m[mt][i >> 1];
               const float w = fast_exp2(s[mt][2 * x + n][i] - ref);
-              if (kFp8) {  // a row that weighs nothing stays at zero whatever its scale
-                l[mt][i >> 1] += w == 0.f ? 0.f : w * inv[2 * x + n][i & 1];
-                p[n][i] = w == 0.f ? 0.f : w * sgn[2 * x + n][i & 1];
-              } else {
-                l[mt][i >> 1] += w;
-                p[n][i] = w;
-              }
+              l[mt][i >> 1] += kFp8 ? w * inv[2 * x + n][i & 1] : w;
+              p[n][i] = kFp8 ? w * sgn[2 * x + n][i & 1] : w;
             }
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
@@ -565,35 +571,8 @@ __global__ void __launch_bounds__(PaShape<D, MT, kFp8>::kThreads, 1)
           }
         }
       }
-      // ---- O += P V.  Where tokens of one MMA see different rows (S > 1 at
-      // an end of their ranges), one pass per token with its own V rows kept
-      // and its own query rows added (a zero weight times a NaN is a NaN).
-      const int passes = edge && a.S > 1 ? a.S : 1;
-      for (int t = 0; t < passes; ++t) {
-        uint32_t keep[2 * kGroups];
-        if (passes > 1) {
-          const int last = p_first + t;
-#pragma unroll
-          for (int n = 0; n < 2 * kGroups; ++n) {
-            keep[n] = 0;
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-              const int r = base + n * 8 + c * 2 + e;
-              if (r <= last && (a.win == 0 || r > last - a.win)) keep[n] |= e ? 0xffff0000u : 0xffffu;
-            }
-          }
-        }
-        auto pv = [&](int mt, int x, int j, uint32_t b0, uint32_t b1) {
-          if (passes == 1) {
-            mma16<kFp8>(o[mt][j], pf[mt][x], b0, b1);
-          } else {
-            float y[4] = {0.f, 0.f, 0.f, 0.f};
-            mma16<kFp8>(y, pf[mt][x], b0 & keep[2 * x], b1 & keep[2 * x + 1]);
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-              if (sq[mt][i >> 1] == t) o[mt][j][i] += y[i];
-          }
-        };
+      // ---- O += P V
+      auto products = [&](auto&& pv) {
 #pragma unroll
         for (int x = 0; x < kGroups; ++x) {
           if constexpr (kFp8) {
@@ -607,14 +586,17 @@ __global__ void __launch_bounds__(PaShape<D, MT, kFp8>::kThreads, 1)
             }
 #pragma unroll
             for (int y = 0; y < 4; ++y) {
-              const uint32_t lo01 = __byte_perm(w[0][y], w[1][y], 0x5140), hi01 = __byte_perm(w[0][y], w[1][y], 0x7362);
-              const uint32_t lo23 = __byte_perm(w[2][y], w[3][y], 0x5140), hi23 = __byte_perm(w[2][y], w[3][y], 0x7362);
 #pragma unroll
-              for (int z = 0; z < 4; ++z) {
-                const uint32_t b0 = e4m3x2_to_f16x2((z < 2 ? lo01 : hi01) >> (16 * (z & 1)));
-                const uint32_t b1 = e4m3x2_to_f16x2((z < 2 ? lo23 : hi23) >> (16 * (z & 1)));
+              for (int z = 0; z < 4; z += 2) {  // dims 16 g + 4 y + z, + 1: rows interleaved pair by pair
+                const uint32_t sel = z ? 0x7362 : 0x5140;
+                uint32_t a0, a1, b0, b1;
+                e4m3x4_to_f16x2(__byte_perm(w[0][y], w[1][y], sel), a0, a1);
+                e4m3x4_to_f16x2(__byte_perm(w[2][y], w[3][y], sel), b0, b1);
 #pragma unroll
-                for (int mt = 0; mt < MT; ++mt) pv(mt, x, y * 4 + z, b0, b1);
+                for (int mt = 0; mt < MT; ++mt) {
+                  pv(mt, x, y * 4 + z, a0, b0);
+                  pv(mt, x, y * 4 + z + 1, a1, b1);
+                }
               }
             }
           } else {
@@ -630,6 +612,33 @@ __global__ void __launch_bounds__(PaShape<D, MT, kFp8>::kThreads, 1)
               }
             }
           }
+        }
+      };
+      if (!edge || a.S == 1) {
+        products([&](int mt, int x, int j, uint32_t b0, uint32_t b1) { mma16<kFp8>(o[mt][j], pf[mt][x], b0, b1); });
+      } else {
+        // tokens of one MMA see different rows here: one pass per token with its
+        // own V rows kept and its own query rows added (a zero weight times a
+        // NaN is a NaN)
+        for (int t = 0; t < a.S; ++t) {
+          const int last = p_first + t;
+          uint32_t keep[2 * kGroups];
+#pragma unroll
+          for (int n = 0; n < 2 * kGroups; ++n) {
+            keep[n] = 0;
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              const int r = base + n * 8 + c * 2 + e;
+              if (r <= last && (a.win == 0 || r > last - a.win)) keep[n] |= e ? 0xffff0000u : 0xffffu;
+            }
+          }
+          products([&](int mt, int x, int j, uint32_t b0, uint32_t b1) {
+            float y[4] = {0.f, 0.f, 0.f, 0.f};
+            mma16<kFp8>(y, pf[mt][x], b0 & keep[2 * x], b1 & keep[2 * x + 1]);
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+              if (sq[mt][i >> 1] == t) o[mt][j][i] += y[i];
+          });
         }
       }
     }
