@@ -10,10 +10,11 @@
 // stream of row copies.
 //
 // Split of the work.  A unit is (request, kv head, chunk of 16 MT query
-// rows); its cost is its number of tiles (128 or 256 rows).  The units' tiles form one
-// list, cut evenly over the CTAs (one per SM), so that a ragged batch or a
-// single long request fills the device alike; the lengths are read on the
-// device, so a captured graph follows them.  Within a tile each warp owns 16
+// rows); its cost is its number of tiles (128 or 256 rows) and one more for
+// its start and end.  The units' tiles form one list, cut evenly by cost over
+// the CTAs (one per SM), so that a ragged batch or a single long request fills
+// the device alike; the lengths are read on the device, so a captured graph
+// follows them.  Within a tile each warp owns 16
 // or 32 rows: it copies them itself (16-byte cp.async into its own ring, several
 // tiles ahead, across unit boundaries), and keeps its own running maximum,
 // sum and output in registers: no barrier per tile.  At the end of a unit (or
@@ -186,6 +187,12 @@ struct Cursor {
   }
 };
 
+// A cut of the list of tiles: before this tile of this unit.
+struct Cut {
+  int b, unit, tile;
+  int64_t first, at;   // the unit's start in the list of costs, the tiles before the cut
+};
+
 template <int D, int MT, bool kFp8>
 __global__ void __launch_bounds__(PaShape<D, MT, kFp8>::kThreads, 1)
     paged_attn_kernel(const PagedArgs a, int chunks, float* __restrict__ part, PaJoin* __restrict__ joins) {
@@ -193,8 +200,7 @@ __global__ void __launch_bounds__(PaShape<D, MT, kFp8>::kThreads, 1)
   constexpr int kTile = Sh::kTile, kPer = Sh::kPer, kGroups = Sh::kGroups;
   extern __shared__ __align__(128) uint8_t smem_raw[];
   __shared__ int scan_tmp[33];
-  __shared__ int64_t start_at;
-  __shared__ int start_b;
+  __shared__ Cut cut_sh[2];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const uint32_t ring = smem_u32(smem_raw) + warp * (Sh::kStages * Sh::kWarpStage);
   const uint32_t qsm = smem_u32(smem_raw) + Sh::kRing;
@@ -206,12 +212,13 @@ __global__ void __launch_bounds__(PaShape<D, MT, kFp8>::kThreads, 1)
   pdl_wait();
   pdl_trigger();
 
-  // ---- this CTA's share of the list
+  // ---- this CTA's share of the list: of the costs (a unit's tiles and one
+  // more for its start and end), with the cuts moved to the next whole tile
   int64_t total = 0;
   for (int b0 = 0; b0 < a.B; b0 += Sh::kThreads) {
     Span<kTile> sp;
     int n = 0, sum;
-    if (b0 + tid < a.B) sp.set(a, a.ctx_len[b0 + tid]), n = sp.tiles;
+    if (b0 + tid < a.B) sp.set(a, a.ctx_len[b0 + tid]), n = sp.tiles + 1;
     block_exclusive_scan(n, scan_tmp, &sum);
     total += sum;
   }
@@ -221,7 +228,7 @@ __global__ void __launch_bounds__(PaShape<D, MT, kFp8>::kThreads, 1)
     if (tid == 0) joins[blockIdx.x].count = 0;
     return;
   }
-  const int64_t lo = blockIdx.x * total / G, hi = (blockIdx.x + 1) * total / G;
+  const int64_t cut[2] = {blockIdx.x * total / G, (blockIdx.x + 1) * total / G};
   int64_t before = 0;
   for (int b0 = 0; b0 < a.B; b0 += Sh::kThreads) {
     Span<kTile> sp;
@@ -229,21 +236,38 @@ __global__ void __launch_bounds__(PaShape<D, MT, kFp8>::kThreads, 1)
     if (b0 + tid < a.B) {
       const int len = a.ctx_len[b0 + tid];
       sp.set(a, len);
-      n = sp.tiles;
+      n = sp.tiles + 1;
       if (blockIdx.x == 0 && a.status && (len < 0 || len > a.max_len)) set_status(a.status, kStatusBadIndex);
     }
     const int64_t p = (before + block_exclusive_scan(n, scan_tmp, &sum)) * units;
-    if (n > 0 && p <= lo && lo < p + (int64_t)n * units) start_b = b0 + tid, start_at = lo - p;
+#pragma unroll
+    for (int e = 0; e < 2; ++e)
+      // (the list's end belongs to its last request)
+      if (n > 0 && p <= cut[e] && (cut[e] < p + (int64_t)n * units || b0 + tid == a.B - 1)) {
+        const int64_t at = cut[e] - p;
+        const int unit = (int)(at / n), x = (int)(at - (int64_t)unit * n);
+        cut_sh[e].b = b0 + tid;
+        cut_sh[e].unit = unit;
+        cut_sh[e].tile = x > 0 ? x - 1 : 0;
+        cut_sh[e].first = p + (int64_t)unit * n;
+        // tiles before it in the whole list
+        cut_sh[e].at = p - (int64_t)(b0 + tid) * units + (int64_t)unit * sp.tiles + cut_sh[e].tile;
+      }
     before += sum;
   }
   __syncthreads();
+  const int steps = (int)(cut_sh[1].at - cut_sh[0].at);
+  if (steps == 0) {
+    if (tid == 0) joins[blockIdx.x].count = 0;
+    return;
+  }
   Cursor<kTile> ld;  // the loader's position, several tiles ahead of the products
-  ld.b = start_b;
+  ld.b = cut_sh[0].b;
   ld.sp.set(a, a.ctx_len[ld.b]);
-  ld.unit = (int)(start_at / ld.sp.tiles);
-  ld.tile = (int)(start_at - (int64_t)ld.unit * ld.sp.tiles);
+  ld.unit = cut_sh[0].unit;
+  ld.tile = cut_sh[0].tile;
+  int64_t unit_at = cut_sh[0].first;  // the current unit's place in the list of costs
   Cursor<kTile> cu = ld;
-  const int steps = (int)(hi - lo);
   int loaded = 0;
 
   // ---- row copies: lane r < kPer looks up the pool row of the warp's row r,
@@ -287,7 +311,7 @@ __global__ void __launch_bounds__(PaShape<D, MT, kFp8>::kThreads, 1)
   };
   auto load_step = [&] {
     if (loaded < steps) {
-      copy(loaded % Sh::kStages);
+      if (ld.sp.L > 0) copy(loaded % Sh::kStages);
       ++loaded;
       if (loaded < steps) {
         ld.next(a, units);
@@ -312,6 +336,23 @@ __global__ void __launch_bounds__(PaShape<D, MT, kFp8>::kThreads, 1)
 
   for (int step = 0; step < steps; ++step) {
     const int h = cu.unit / chunks, row0 = (cu.unit - h * chunks) * Sh::kRows;
+    if (cu.sp.L <= 0) {  // a padding request: nothing to read, nothing to join
+      load_step();
+      for (int x = tid; x < Sh::kRows * (D / 8); x += Sh::kThreads) {
+        const int i = row0 + x / (D / 8);
+        if (i < qrows) {
+          const int s = i / group, hd = h * group + i - s * group;
+          const int64_t tok = (int64_t)cu.b * a.S + s;
+          *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(a.out) + tok * a.out_stride + hd * D + x % (D / 8) * 8) =
+              make_uint4(0, 0, 0, 0);
+          if (a.lse && x % (D / 8) == 0) a.lse[tok * a.heads + hd] = -INFINITY;
+        }
+      }
+      if (tid == 0 && step + 1 == steps) joins[blockIdx.x].count = 0;
+      unit_at += cu.sp.tiles + 1;
+      cu.next(a, units);
+      continue;
+    }
     if (seg_new) {
       seg_new = false;
       seg_first = step;
@@ -742,12 +783,13 @@ __global__ void __launch_bounds__(PaShape<D, MT, kFp8>::kThreads, 1)
         j.b = cu.b;
         j.unit = cu.unit;
         if (!unit_end && cu.tile == step - seg_first) {
-          const int64_t last = lo + seg_first + cu.sp.tiles - 1;     // the unit's last tile in the list
+          const int64_t last = unit_at + cu.sp.tiles;     // the unit's last tile in the list of costs
           j.count = (int)(((last + 1) * G - 1) / total) - (int)blockIdx.x + 1;
         }
         joins[blockIdx.x] = j;
       }
       seg_new = true;
+      unit_at += cu.sp.tiles + 1;
     }
     cu.next(a, units);
   }
