@@ -47,9 +47,12 @@ constexpr float kRescaleAbove = 8.f;  // the reference maximum moves when exceed
 
 template <int D, int MT, bool kFp8>
 struct PaShape {
-  static constexpr int kWarps = D == 256 ? 4 : 8;
-  static constexpr int kThreads = 32 * kWarps;
   static constexpr int kRowBytes = D * (kFp8 ? 1 : 2);
+  // three warps per scheduler where registers allow it (64-dim heads: 71 us with
+  // 8 warps, 67 with 12; E4M3: 353 and 333 us, its Q fragments then in shared
+  // memory): the chain of a tile, QK to PV, is long and each warp does its own
+  static constexpr int kWarps = D == 256 ? 4 : kRowBytes <= 128 && MT == 1 ? 12 : 8;
+  static constexpr int kThreads = 32 * kWarps;
   // rows a warp takes per tile: short rows take 32, so that the work per tile
   // (maxima, look-ups) is spread over as many bytes
   static constexpr int kPer = kRowBytes <= 128 ? 32 : 16;
@@ -59,12 +62,12 @@ struct PaShape {
   static constexpr int kChunks = kRowBytes / 16;                 // 16-byte chunks per row
   static constexpr int kWarpStage = 2 * kPer * kRowBytes + (kFp8 ? 2 * kPer * 4 : 0);
   static constexpr int kScaleBytes = kFp8 ? kPer * 16 : 0;       // per warp: the tile's scales as used
-  static constexpr bool kQReg = MT == 1 && D <= 128;             // Q fragments in registers
+  static constexpr bool kQReg = MT == 1 && D <= 128 && !kFp8;    // Q fragments in registers
   static constexpr int kQBytes = kQReg ? 0 : kRows * D * 2 + (kFp8 ? kRows * 4 : 0);
-  static constexpr int kSlots = kWarps / 2;
+  static constexpr int kSlots = kWarps < 8 ? kWarps / 2 : kFp8 && MT == 1 ? 2 : 4;
   static constexpr int kSlotFloats = kRows * D;
   static constexpr int kSlotBytes = kSlots * (kSlotFloats + 2 * kRows) * 4;
-  static constexpr int kRoom = (224 * 1024 - kQBytes - kSlotBytes - kWarps * kScaleBytes) / (kWarps * kWarpStage);
+  static constexpr int kRoom = (226 * 1024 - kQBytes - kSlotBytes - kWarps * kScaleBytes) / (kWarps * kWarpStage);
   static constexpr int kStages = kRoom > 6 ? 6 : kRoom;
   static constexpr int kRing = kStages * kWarps * kWarpStage;
   static constexpr int kSmem = kRing + kQBytes + kSlotBytes + kWarps * kScaleBytes;
@@ -302,7 +305,7 @@ __global__ void __launch_bounds__(PaShape<D, MT, kFp8>::kThreads, 1)
       cp_async16(kdst + at, kb + (uint64_t)x * (uint32_t)a.k_step, bytes);
       cp_async16(vdst + at, vb + (uint64_t)x * (uint32_t)a.v_step, bytes);
     }
-    if (kFp8) {  // the rows' K scales, then their V scales
+    if (kFp8 && lane < kPer) {  // the rows' K scales, then their V scales
       const int64_t at = (int64_t)(prow < 0 ? 0 : prow) * a.scale_stride + h;
       const uint32_t dst = kdst + 2 * kPer * Sh::kRowBytes + lane * 4;
       cp_async4(dst, a.k_scale + at, prow < 0 ? 0 : 4);
@@ -383,31 +386,8 @@ __global__ void __launch_bounds__(PaShape<D, MT, kFp8>::kThreads, 1)
           const __nv_bfloat16* q = q_at(in ? i : 0);
 #pragma unroll
           for (int ks = 0; ks < D / 16; ++ks) {
-            if constexpr (kFp8) {  // the k order of the E4M3 fragments, see below
-              const uint2 v = in ? *reinterpret_cast<const uint2*>(q + (ks / 4) * 64 + c * 16 + (ks % 4) * 4)
-                                 : make_uint2(0, 0);
-              qf[ks][e] = v.x;
-              qf[ks][2 + e] = v.y;
-            } else {
-              qf[ks][e] = in ? *reinterpret_cast<const uint32_t*>(q + ks * 16 + c * 2) : 0;
-              qf[ks][2 + e] = in ? *reinterpret_cast<const uint32_t*>(q + ks * 16 + 8 + c * 2) : 0;
-            }
-          }
-          if constexpr (kFp8) {
-            float top = 0.f;
-#pragma unroll
-            for (int ks = 0; ks < D / 16; ++ks)
-#pragma unroll
-              for (int x = e; x < 4; x += 2)
-                top = fmaxf(top, fmaxf(fabsf(__uint_as_float(qf[ks][x] << 16)), fabsf(__uint_as_float(qf[ks][x] & 0xffff0000u))));
-            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
-            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
-            const float two = pow2_below(top);
-            qmul[0][e] = two;
-#pragma unroll
-            for (int ks = 0; ks < D / 16; ++ks)
-#pragma unroll
-              for (int x = e; x < 4; x += 2) qf[ks][x] = bf16x2_to_f16x2(qf[ks][x], 1.f / two);
+            qf[ks][e] = in ? *reinterpret_cast<const uint32_t*>(q + ks * 16 + c * 2) : 0;
+            qf[ks][2 + e] = in ? *reinterpret_cast<const uint32_t*>(q + ks * 16 + 8 + c * 2) : 0;
           }
         }
       } else {
@@ -452,14 +432,14 @@ __global__ void __launch_bounds__(PaShape<D, MT, kFp8>::kThreads, 1)
         // their precision whatever the scales.  The softmax's own sum takes
         // the factor out again (1 / |v_scale|).  |v_scale| below 2^-100 counts
         // as 2^-100 there, and the rest of it is kept in the sign factor.
-        const uint32_t src = kt + 2 * kPer * Sh::kRowBytes + lane * 4;
+        const uint32_t src = kt + 2 * kPer * Sh::kRowBytes + (lane % kPer) * 4;
         const float ks = lds_f32(src) * scale2, vs = lds_f32(src + kPer * 4);
         const float lv = fast_log2(fmaxf(fabsf(vs), 7.8886091e-31f)), inv = fast_exp2(-lv);
         // a v_scale that is no number reaches whoever sees the row by its exponent alone
         if (fabsf(vs) < INFINITY)
-          sts_f4(rowsc + lane * 16, ks, lv, inv, vs * inv);
+          sts_f4(rowsc + (lane % kPer) * 16, ks, lv, inv, vs * inv);
         else
-          sts_f4(rowsc + lane * 16, ks, __uint_as_float(0x7fffffffu), 1.f, 1.f);
+          sts_f4(rowsc + (lane % kPer) * 16, ks, __uint_as_float(0x7fffffffu), 1.f, 1.f);
         __syncwarp();
       }
       // ---- S = Q K^T: 16 MT query rows x kPer rows (n = 8 tiles)
@@ -713,24 +693,31 @@ __global__ void __launch_bounds__(PaShape<D, MT, kFp8>::kThreads, 1)
           }
       };
       __syncthreads();   // the slots' last readers are done
-      if (warp >= Sh::kSlots) put();
-      __syncthreads();
-      if (warp < Sh::kSlots) {
+      // kSlots warps at a time hand their state to the kSlots before them
 #pragma unroll
-        for (int mt = 0; mt < MT; ++mt)
+      for (int from = Sh::kWarps - Sh::kSlots; from > 0; from -= Sh::kSlots) {
+        if (warp >= from && warp < from + Sh::kSlots) put();
+        __syncthreads();
+        if (warp >= from - Sh::kSlots && warp < from) {
 #pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            const int r = mt * 16 + g + 8 * e;
-            const float m2 = sml[r], top = fmaxf(m[mt][e], m2), ref = top == -INFINITY ? 0.f : top;
-            const float f1 = fast_exp2(m[mt][e] - ref), f2 = fast_exp2(m2 - ref);
-            l[mt][e] = l[mt][e] * f1 + sml[Sh::kRows + r] * f2;
-            m[mt][e] = top;
+          for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
-            for (int j = 0; j < D / 8; ++j) {
-              o[mt][j][2 * e] = o[mt][j][2 * e] * f1 + so[r * D + dim_of(j, 0)] * f2;
-              o[mt][j][2 * e + 1] = o[mt][j][2 * e + 1] * f1 + so[r * D + dim_of(j, 1)] * f2;
+            for (int e = 0; e < 2; ++e) {
+              const int r = mt * 16 + g + 8 * e;
+              const float m2 = sml[r], top = fmaxf(m[mt][e], m2), ref = top == -INFINITY ? 0.f : top;
+              const float f1 = fast_exp2(m[mt][e] - ref), f2 = fast_exp2(m2 - ref);
+              l[mt][e] = l[mt][e] * f1 + sml[Sh::kRows + r] * f2;
+              m[mt][e] = top;
+#pragma unroll
+              for (int j = 0; j < D / 8; ++j) {
+                o[mt][j][2 * e] = o[mt][j][2 * e] * f1 + so[r * D + dim_of(j, 0)] * f2;
+                o[mt][j][2 * e + 1] = o[mt][j][2 * e + 1] * f1 + so[r * D + dim_of(j, 1)] * f2;
+              }
             }
-          }
+        }
+        if (from > Sh::kSlots) __syncthreads();
+      }
+      if (warp < Sh::kSlots) {
         __syncwarp();
         put();
       }
