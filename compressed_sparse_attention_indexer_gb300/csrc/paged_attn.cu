@@ -196,6 +196,12 @@ struct Cut {
   int64_t first, at;   // the unit's start in the list of costs, the tiles before the cut
 };
 
+// i * total / parts (a 32-bit division where that holds it).
+__device__ __forceinline__ int64_t split_at(int64_t total, int i, int parts) {
+  const int64_t x = total * i;
+  return x < (int64_t(1) << 32) ? (int64_t)((uint32_t)x / (uint32_t)parts) : x / parts;
+}
+
 template <int D, int MT, bool kFp8>
 __global__ void __launch_bounds__(PaShape<D, MT, kFp8>::kThreads, 1)
     paged_attn_kernel(const PagedArgs a, int chunks, float* __restrict__ part, PaJoin* __restrict__ joins) {
@@ -204,6 +210,9 @@ __global__ void __launch_bounds__(PaShape<D, MT, kFp8>::kThreads, 1)
   extern __shared__ __align__(128) uint8_t smem_raw[];
   __shared__ int scan_tmp[33];
   __shared__ Cut cut_sh[2];
+  // thread 0's alone, kept out of everyone's registers: the list's cost, and the
+  // current unit's place in it
+  __shared__ int64_t total_sh, unit_at;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const uint32_t ring = smem_u32(smem_raw) + warp * (Sh::kStages * Sh::kWarpStage);
   const uint32_t qsm = smem_u32(smem_raw) + Sh::kRing;
@@ -217,12 +226,14 @@ __global__ void __launch_bounds__(PaShape<D, MT, kFp8>::kThreads, 1)
 
   // ---- this CTA's share of the list: of the costs (a unit's tiles and one
   // more for its start and end), with the cuts moved to the next whole tile
+  const bool once = a.B <= Sh::kThreads;   // one request per thread: scanned once
+  Span<kTile> sp;
+  int n = 0, sum, ahead = 0, len = 0;
   int64_t total = 0;
   for (int b0 = 0; b0 < a.B; b0 += Sh::kThreads) {
-    Span<kTile> sp;
-    int n = 0, sum;
-    if (b0 + tid < a.B) sp.set(a, a.ctx_len[b0 + tid]), n = sp.tiles + 1;
-    block_exclusive_scan(n, scan_tmp, &sum);
+    n = 0;
+    if (b0 + tid < a.B) len = a.ctx_len[b0 + tid], sp.set(a, len), n = sp.tiles + 1;
+    ahead = block_exclusive_scan(n, scan_tmp, &sum);
     total += sum;
   }
   total *= units;
@@ -231,24 +242,24 @@ __global__ void __launch_bounds__(PaShape<D, MT, kFp8>::kThreads, 1)
     if (tid == 0) joins[blockIdx.x].count = 0;
     return;
   }
-  const int64_t cut[2] = {blockIdx.x * total / G, (blockIdx.x + 1) * total / G};
+  const int64_t cut[2] = {split_at(total, blockIdx.x, (int)G), split_at(total, blockIdx.x + 1, (int)G)};
   int64_t before = 0;
   for (int b0 = 0; b0 < a.B; b0 += Sh::kThreads) {
-    Span<kTile> sp;
-    int n = 0, sum;
-    if (b0 + tid < a.B) {
-      const int len = a.ctx_len[b0 + tid];
-      sp.set(a, len);
-      n = sp.tiles + 1;
-      if (blockIdx.x == 0 && a.status && (len < 0 || len > a.max_len)) set_status(a.status, kStatusBadIndex);
+    if (!once) {
+      n = 0;
+      if (b0 + tid < a.B) len = a.ctx_len[b0 + tid], sp.set(a, len), n = sp.tiles + 1;
+      ahead = block_exclusive_scan(n, scan_tmp, &sum);
     }
-    const int64_t p = (before + block_exclusive_scan(n, scan_tmp, &sum)) * units;
+    if (blockIdx.x == 0 && a.status && b0 + tid < a.B && (len < 0 || len > a.max_len))
+      set_status(a.status, kStatusBadIndex);
+    const int64_t p = (before + ahead) * units;
 #pragma unroll
     for (int e = 0; e < 2; ++e)
       // (the list's end belongs to its last request)
       if (n > 0 && p <= cut[e] && (cut[e] < p + (int64_t)n * units || b0 + tid == a.B - 1)) {
         const int64_t at = cut[e] - p;
-        const int unit = (int)(at / n), x = (int)(at - (int64_t)unit * n);
+        const int unit = at < (1u << 31) ? (int)((uint32_t)at / (uint32_t)n) : (int)(at / n);
+        const int x = (int)(at - (int64_t)unit * n);
         cut_sh[e].b = b0 + tid;
         cut_sh[e].unit = unit;
         cut_sh[e].tile = x > 0 ? x - 1 : 0;
@@ -269,7 +280,7 @@ __global__ void __launch_bounds__(PaShape<D, MT, kFp8>::kThreads, 1)
   ld.sp.set(a, a.ctx_len[ld.b]);
   ld.unit = cut_sh[0].unit;
   ld.tile = cut_sh[0].tile;
-  int64_t unit_at = cut_sh[0].first;  // the current unit's place in the list of costs
+  if (tid == 0) total_sh = total, unit_at = cut_sh[0].first;
   Cursor<kTile> cu = ld;
   int loaded = 0;
 
@@ -352,7 +363,7 @@ __global__ void __launch_bounds__(PaShape<D, MT, kFp8>::kThreads, 1)
         }
       }
       if (tid == 0 && step + 1 == steps) joins[blockIdx.x].count = 0;
-      unit_at += cu.sp.tiles + 1;
+      if (tid == 0) unit_at += cu.sp.tiles + 1;
       cu.next(a, units);
       continue;
     }
@@ -771,12 +782,13 @@ __global__ void __launch_bounds__(PaShape<D, MT, kFp8>::kThreads, 1)
         j.unit = cu.unit;
         if (!unit_end && cu.tile == step - seg_first) {
           const int64_t last = unit_at + cu.sp.tiles;     // the unit's last tile in the list of costs
-          j.count = (int)(((last + 1) * G - 1) / total) - (int)blockIdx.x + 1;
+          const int64_t G = total_sh < gridDim.x ? total_sh : gridDim.x;
+          j.count = (int)(((last + 1) * G - 1) / total_sh) - (int)blockIdx.x + 1;
         }
         joins[blockIdx.x] = j;
       }
       seg_new = true;
-      unit_at += cu.sp.tiles + 1;
+      if (tid == 0) unit_at += cu.sp.tiles + 1;
     }
     cu.next(a, units);
   }
