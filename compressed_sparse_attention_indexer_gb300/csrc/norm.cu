@@ -68,12 +68,13 @@ struct VecOf<__nv_bfloat16> {
   static __device__ __forceinline__ __nv_bfloat16 one(float v) { return __float2bfloat16_rn(v); }
 };
 
-// Vector v of a row of `width` elements; elements past the row read as zero
-// (the row may be the pool's last: nothing behind it is touched).
-template <typename T>
+// Vector v of a row of `width` elements.  kTail: the row's last vector may be
+// short; elements past the row then read as zero and are not written (the row
+// may be the last of its buffer: nothing behind it is touched).
+template <bool kTail, typename T>
 __device__ __forceinline__ uint4 load_vec(const T* row, int v, int width) {
   constexpr int E = VecOf<T>::E;
-  if ((v + 1) * E <= width) return __ldcs(reinterpret_cast<const uint4*>(row) + v);
+  if (!kTail || (v + 1) * E <= width) return __ldcs(reinterpret_cast<const uint4*>(row) + v);
   T t[E];
 #pragma unroll
   for (int i = 0; i < E; ++i) t[i] = v * E + i < width ? row[v * E + i] : T(0.f);
@@ -81,10 +82,10 @@ __device__ __forceinline__ uint4 load_vec(const T* row, int v, int width) {
   memcpy(&r, t, 16);
   return r;
 }
-template <typename T>
+template <bool kTail, typename T>
 __device__ __forceinline__ void store_vec(T* row, int v, int width, const float* f) {
   constexpr int E = VecOf<T>::E;
-  if ((v + 1) * E <= width) {
+  if (!kTail || (v + 1) * E <= width) {
     reinterpret_cast<uint4*>(row)[v] = VecOf<T>::pack(f);
     return;
   }
@@ -93,14 +94,13 @@ __device__ __forceinline__ void store_vec(T* row, int v, int width, const float*
     if (v * E + i < width) row[v * E + i] = VecOf<T>::one(f[i]);
 }
 // E codes of a row at vector v.
-template <int E>
-__device__ __forceinline__ void store_codes(uint8_t* row, int v, int width, const float* f, float inv) {
+template <bool kTail, int E>
+__device__ __forceinline__ void store_codes(uint8_t* row, int v, int width, const float* f, float mul) {
   uint16_t c[E / 2];
 #pragma unroll
   for (int i = 0; i < E / 2; ++i)
-    c[i] = __nv_cvt_float2_to_fp8x2(make_float2(f[2 * i] * inv, f[2 * i + 1] * inv), __NV_SATFINITE,
-                                    __NV_E4M3);
-  if ((v + 1) * E <= width) {
+    c[i] = __nv_cvt_float2_to_fp8x2(make_float2(f[2 * i] * mul, f[2 * i + 1] * mul), __NV_SATFINITE, __NV_E4M3);
+  if (!kTail || (v + 1) * E <= width) {
     if (E == 8)
       reinterpret_cast<uint2*>(row)[v] =
           make_uint2(c[0] | (uint32_t)c[1] << 16, c[E / 2 - 2] | (uint32_t)c[E / 2 - 1] << 16);
@@ -112,12 +112,22 @@ __device__ __forceinline__ void store_codes(uint8_t* row, int v, int width, cons
   for (int i = 0; i < E; ++i)
     if (v * E + i < width) row[v * E + i] = (uint8_t)(c[i / 2] >> (8 * (i & 1)));
 }
+__device__ __forceinline__ float rcp_approx(float x) {
+  float y;
+  asm("rcp.approx.f32 %0, %1;\n" : "=f"(y) : "f"(x));
+  return y;
+}
 
 // tpr threads per row (a divisor of 32, or the whole block); blockDim.x / tpr
 // rows per block and step, rows in a grid-stride loop.  The next row's
 // vectors are loaded before the current row is reduced.
-template <typename T, int VPT>
-__global__ void __launch_bounds__(kNormMaxThreads) norm_kernel(const NormArgs a, int tpr) {
+// Narrow rows are bound by instructions before bytes (131072 rows of 128: 239
+// per warp and step took 17.2 us), so: the weight multiplies s before the norm
+// is known and the norm's factor r > 0 goes into the scale
+// (max|y| = r max|s weight|, code = s weight * (r / scale)), and row pointers
+// advance by additions.
+template <typename T, int VPT, bool kTail>
+__global__ void __launch_bounds__(kNormMaxThreads, VPT <= 2 ? 2 : 1) norm_kernel(const NormArgs a, int tpr) {
   constexpr int E = VecOf<T>::E;
   // the next row in flight and the weight held, where registers allow it
   constexpr bool kAhead = VPT <= 4;
@@ -126,43 +136,51 @@ __global__ void __launch_bounds__(kNormMaxThreads) norm_kernel(const NormArgs a,
   const int t = threadIdx.x % tpr;
   const int rpb = blockDim.x / tpr;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int W = a.width;
+  const int W = a.width, vecs = (W + E - 1) / E;
   const float inv_width = 1.f / (float)W;
+  const int64_t step = (int64_t)gridDim.x * rpb;
+  int64_t row = (int64_t)blockIdx.x * rpb + threadIdx.x / tpr;
+  const T* xp = static_cast<const T*>(a.x) + row * a.x_stride;
+  const T* rp = static_cast<const T*>(a.residual) + (a.residual ? row * a.residual_stride : 0);
+  T* sp = static_cast<T*>(a.residual_out) + (a.residual ? row * a.residual_out_stride : 0);
+  T* op = static_cast<T*>(a.out) + (a.out ? row * a.out_stride : 0);
+  uint8_t* cp = a.codes + (a.codes ? row * a.codes_stride : 0);
+  float* fp = a.scale + (a.codes ? row * a.scale_stride : 0);
   pdl_wait();
   pdl_trigger();
-  int64_t row = (int64_t)blockIdx.x * rpb + threadIdx.x / tpr;
-  const int64_t step = (int64_t)gridDim.x * rpb;
   uint4 xr[VPT], rr[VPT], wr[VPT];
-  auto fetch = [&](int64_t r) {
-    if (r >= a.n) return;
+  auto fetch = [&](bool have) {
+    if (!have) return;
 #pragma unroll
     for (int i = 0; i < VPT; ++i) {
       const int v = i * tpr + t;
-      if (v * E < W) {
-        xr[i] = load_vec(static_cast<const T*>(a.x) + r * a.x_stride, v, W);
-        if (a.residual) rr[i] = load_vec(static_cast<const T*>(a.residual) + r * a.residual_stride, v, W);
+      if (v < vecs) {
+        xr[i] = load_vec<kTail>(xp, v, W);
+        if (a.residual) rr[i] = load_vec<kTail>(rp, v, W);
       }
     }
+    xp += step * a.x_stride;
+    if (a.residual) rp += step * a.residual_stride;
   };
-  if (kAhead) fetch(row);
+  if (kAhead) fetch(row < a.n);
   if (kAhead && a.weight) {
 #pragma unroll
     for (int i = 0; i < VPT; ++i) {
       const int v = i * tpr + t;
-      if (v * E < W) wr[i] = load_vec(static_cast<const T*>(a.weight), v, W);
+      if (v < vecs) wr[i] = load_vec<kTail>(static_cast<const T*>(a.weight), v, W);
     }
   }
   int buf = 0;
   // every thread of the block runs the same number of steps (barrier inside)
   for (int64_t first = (int64_t)blockIdx.x * rpb; first < a.n; first += step, row += step) {
     const bool live = row < a.n;
-    if (!kAhead) fetch(row);
+    if (!kAhead) fetch(live);
     float y[VPT][E];
     float sum = 0.f;
 #pragma unroll
     for (int i = 0; i < VPT; ++i) {
       const int v = i * tpr + t;
-      if (live && v * E < W) {
+      if (live && v < vecs) {
         VecOf<T>::unpack(xr[i], y[i]);
         if (a.residual) {
           float r[E];
@@ -177,17 +195,23 @@ __global__ void __launch_bounds__(kNormMaxThreads) norm_kernel(const NormArgs a,
 #pragma unroll
       for (int e = 0; e < E; ++e) sum = fmaf(y[i][e], y[i][e], sum);
     }
-    if (kAhead) fetch(row + step);
-    if (live && a.residual) {
+    if (kAhead) fetch(row + step < a.n);
+    if (a.residual) {
 #pragma unroll
       for (int i = 0; i < VPT; ++i) {
         const int v = i * tpr + t;
-        if (v * E < W) store_vec(static_cast<T*>(a.residual_out) + row * a.residual_out_stride, v, W, y[i]);
+        if (live && v < vecs) store_vec<kTail>(sp, v, W, y[i]);
       }
+      sp += step * a.residual_out_stride;
     }
+    float r = 1.f;
     if (a.norm) {
-      const int span = tpr < 32 ? tpr : 32;
-      for (int o = span >> 1; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+      if (tpr < 32) {
+        for (int o = tpr >> 1; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+      } else {
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+      }
       if (tpr > 32) {
         if (lane == 0) part[buf][warp] = sum;
         __syncthreads();
@@ -196,49 +220,62 @@ __global__ void __launch_bounds__(kNormMaxThreads) norm_kernel(const NormArgs a,
         for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
         buf ^= 1;  // the next step's sums go elsewhere: one barrier per row is enough
       }
-      const float r = rsqrtf(sum * inv_width + a.eps);
+      r = rsqrtf(sum * inv_width + a.eps);
+      if (a.weight) {
 #pragma unroll
-      for (int i = 0; i < VPT; ++i) {
-        if (a.weight && (i * tpr + t) * E < W) {
-          float w[E];
-          VecOf<T>::unpack(kAhead ? wr[i] : load_vec(static_cast<const T*>(a.weight), i * tpr + t, W), w);
+        for (int i = 0; i < VPT; ++i) {
+          const int v = i * tpr + t;
+          if (v < vecs) {
+            float w[E];
+            VecOf<T>::unpack(kAhead ? wr[i] : load_vec<kTail>(static_cast<const T*>(a.weight), v, W), w);
 #pragma unroll
-          for (int e = 0; e < E; ++e) y[i][e] = y[i][e] * r * w[e];
-        } else {
-#pragma unroll
-          for (int e = 0; e < E; ++e) y[i][e] *= r;
+            for (int e = 0; e < E; ++e) y[i][e] *= w[e];
+          }
         }
       }
     }
+    if (a.codes) {
 #pragma unroll
-    for (int i = 0; i < VPT; ++i) {
-      const int v = i * tpr + t;
-      const bool mine = live && v * E < W;
-      if (a.out && mine) store_vec(static_cast<T*>(a.out) + row * a.out_stride, v, W, y[i]);
-      if (a.codes) {
+      for (int i = 0; i < VPT; ++i) {
+        const int v = i * tpr + t;
         float m = 0.f;  // NaN elements leave the maximum alone and become NaN codes
 #pragma unroll
         for (int e = 0; e < E; ++e) m = fmaxf(m, fabsf(y[i][e]));
 #pragma unroll
         for (int o = kLanes >> 1; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-        const float scale = m > 0.f ? fmaxf(m / kE4m3Max, 1.17549435e-38f) : 1.f;
-        if (mine) {
-          store_codes<E>(a.codes + row * a.codes_stride, v, W, y[i], 1.f / scale);
-          if (t % kLanes == 0) a.scale[row * a.scale_stride + v / kLanes] = scale;
+        m *= r;
+        const float scale = m > 0.f ? fmaxf(m * (1.f / kE4m3Max), 1.17549435e-38f) : 1.f;
+        if (live && v < vecs) {
+          store_codes<kTail, E>(cp, v, W, y[i], r * rcp_approx(scale));
+          if (t % kLanes == 0) fp[v / kLanes] = scale;
         }
       }
+      cp += step * a.codes_stride;
+      fp += step * a.scale_stride;
+    }
+    if (a.out) {
+#pragma unroll
+      for (int i = 0; i < VPT; ++i) {
+        const int v = i * tpr + t;
+        if (live && v < vecs) {
+#pragma unroll
+          for (int e = 0; e < E; ++e) y[i][e] *= r;
+          store_vec<kTail>(op, v, W, y[i]);
+        }
+      }
+      op += step * a.out_stride;
     }
   }
 }
 
 // The grid is what fits the device at once (or the rows, when fewer): each
 // block then walks its rows with the next one in flight.
-template <typename T, int VPT>
-int launch_vpt(const NormArgs& a, int tpr, int threads, int num_sms, cudaStream_t st, bool pdl) {
+template <typename T, int VPT, bool kTail>
+int launch_kind(const NormArgs& a, int tpr, int threads, int num_sms, cudaStream_t st, bool pdl) {
   static std::atomic<int> per_sm[kNormMaxThreads / 32 + 1];  // resident blocks by block size (0: not asked yet)
   int r = per_sm[threads / 32].load(std::memory_order_relaxed);
   if (r == 0) {
-    const cudaError_t e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&r, norm_kernel<T, VPT>, threads, 0);
+    const cudaError_t e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&r, norm_kernel<T, VPT, kTail>, threads, 0);
     if (e != cudaSuccess) return launch_fail("cudaOccupancyMaxActiveBlocksPerMultiprocessor", e);
     if (r < 1) r = 1;
     per_sm[threads / 32].store(r, std::memory_order_relaxed);
@@ -246,7 +283,13 @@ int launch_vpt(const NormArgs& a, int tpr, int threads, int num_sms, cudaStream_
   const int64_t rpb = threads / tpr;
   int64_t blocks = (a.n + rpb - 1) / rpb;
   if (blocks > (int64_t)num_sms * r) blocks = (int64_t)num_sms * r;
-  return launch_kernel(norm_kernel<T, VPT>, dim3((unsigned)blocks), dim3(threads), 0, st, pdl, a, tpr);
+  return launch_kernel(norm_kernel<T, VPT, kTail>, dim3((unsigned)blocks), dim3(threads), 0, st, pdl, a, tpr);
+}
+
+template <typename T, int VPT>
+int launch_vpt(const NormArgs& a, int tpr, int threads, int num_sms, cudaStream_t st, bool pdl) {
+  return a.width % VecOf<T>::E == 0 ? launch_kind<T, VPT, false>(a, tpr, threads, num_sms, st, pdl)
+                                    : launch_kind<T, VPT, true>(a, tpr, threads, num_sms, st, pdl);
 }
 
 template <typename T>
@@ -259,9 +302,10 @@ int launch_t(const NormArgs& a, int num_sms, cudaStream_t st, bool pdl) {
     vpt = 1;
     threads = 256;
   } else {
-    // four vectors per thread keep enough loads in flight with many rows; a
-    // few rows take one vector per thread, which is the shorter latency
-    int per = a.n >= num_sms ? 4 : 1;
+    // as few vectors per thread as the block's size allows: the shortest chain
+    // per row (4097 x 1000 fp32: 7.3 us with one, 7.7 with two, 11.2 with four;
+    // 16384 x 7168: the same with two and four)
+    int per = 1;
     while (((vecs + per - 1) / per + 31) / 32 * 32 > kNormMaxThreads) ++per;
     tpr = ((vecs + per - 1) / per + 31) / 32 * 32;
     vpt = (vecs + tpr - 1) / tpr;
