@@ -118,8 +118,8 @@ __device__ __forceinline__ float rcp_approx(float x) {
   return y;
 }
 
-// tpr threads per row (a divisor of 32, or the whole block); blockDim.x / tpr
-// rows per block and step, rows in a grid-stride loop.  The next row's
+// tpr threads per row (a warp, or the whole block); blockDim.x / tpr rows per
+// block and step, rows in a grid-stride loop.  The next row's
 // vectors are loaded before the current row is reduced.
 // Narrow rows are bound by instructions before bytes (131072 rows of 128: 239
 // per warp and step took 17.2 us), so: the weight multiplies s before the norm
@@ -127,7 +127,7 @@ __device__ __forceinline__ float rcp_approx(float x) {
 // (max|y| = r max|s weight|, code = s weight * (r / scale)), and row pointers
 // advance by additions.
 template <typename T, int VPT, bool kTail>
-__global__ void __launch_bounds__(kNormMaxThreads, VPT <= 2 ? 2 : 1) norm_kernel(const NormArgs a, int tpr) {
+__global__ void __launch_bounds__(kNormMaxThreads, VPT == 1 ? 2 : 1) norm_kernel(const NormArgs a, int tpr) {
   constexpr int E = VecOf<T>::E;
   // the next row in flight and the weight held, where registers allow it
   constexpr bool kAhead = VPT <= 4;
@@ -206,12 +206,8 @@ __global__ void __launch_bounds__(kNormMaxThreads, VPT <= 2 ? 2 : 1) norm_kernel
     }
     float r = 1.f;
     if (a.norm) {
-      if (tpr < 32) {
-        for (int o = tpr >> 1; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-      } else {
 #pragma unroll
-        for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-      }
+      for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
       if (tpr > 32) {
         if (lane == 0) part[buf][warp] = sum;
         __syncthreads();
@@ -268,6 +264,127 @@ __global__ void __launch_bounds__(kNormMaxThreads, VPT <= 2 ? 2 : 1) norm_kernel
   }
 }
 
+// ---- rows of one block of codes (width <= 128: head rows, indexer keys) ----
+// Sixteen (bf16) or 32 (fp32) lanes per row and kNarrowRows rows per thread,
+// their chains interleaved: with a row per thread and step the kernel above
+// spends 199 instructions per warp and step, most of them not on elements
+// (131072 x 128 bf16 with codes: 15.5 us, this one 11.5;
+// two rows 13.0, one row 14.8).  Two elements per
+// multiply (f32x2); both reductions run together.
+constexpr int kNarrowRows = 4, kNarrowThreads = 256, kNarrowBlocks = 2;
+
+__device__ __forceinline__ uint64_t pack2(float lo, float hi) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};\n" : "=l"(r) : "f"(lo), "f"(hi));
+  return r;
+}
+__device__ __forceinline__ void mul2(float* d, float b0, float b1) {
+  uint64_t x = pack2(d[0], d[1]);
+  const uint64_t y = pack2(b0, b1);
+  asm("mul.rn.f32x2 %0, %0, %1;\n" : "+l"(x) : "l"(y));
+  asm("mov.b64 {%0, %1}, %2;\n" : "=f"(d[0]), "=f"(d[1]) : "l"(x));
+}
+
+template <typename T, bool kTail, bool kRes>
+__global__ void __launch_bounds__(kNarrowThreads, kNarrowBlocks) norm_narrow_kernel(const NormArgs a) {
+  constexpr int E = VecOf<T>::E, kLanes = kNormBlock / E, R = kNarrowRows;
+  constexpr int kSide = kNarrowThreads / kLanes;       // rows side by side in a block
+  const int t = threadIdx.x % kLanes, W = a.width;
+  const bool mine = t * E < W;
+  const float inv_width = 1.f / (float)W;
+  pdl_wait();
+  pdl_trigger();
+  float w[E];
+#pragma unroll
+  for (int e = 0; e < E; ++e) w[e] = 1.f;
+  if (a.weight && mine) VecOf<T>::unpack(load_vec<kTail>(static_cast<const T*>(a.weight), t, W), w);
+  const int64_t step = (int64_t)gridDim.x * (kSide * R);
+  uint4 xr[R], rr[kRes ? R : 1];
+  auto fetch = [&](int64_t at) {
+#pragma unroll
+    for (int j = 0; j < R; ++j) {
+      const int64_t row = at + j * kSide;
+      xr[j] = make_uint4(0, 0, 0, 0);
+      if (mine && row < a.n) {
+        xr[j] = load_vec<kTail>(static_cast<const T*>(a.x) + row * a.x_stride, t, W);
+        if constexpr (kRes) rr[j] = load_vec<kTail>(static_cast<const T*>(a.residual) + row * a.residual_stride, t, W);
+      }
+    }
+  };
+  int64_t block = (int64_t)blockIdx.x * (kSide * R);
+  int64_t first = block + threadIdx.x / kLanes;
+  fetch(first);
+  for (; block < a.n; block += step, first += step) {  // the whole block runs the same steps
+    float y[R][E], sum[R], top[R];
+#pragma unroll
+    for (int j = 0; j < R; ++j) {
+      const int64_t row = first + j * kSide;
+      VecOf<T>::unpack(xr[j], y[j]);
+      if constexpr (kRes) {
+        if (mine && row < a.n) {
+          float r[E];
+          VecOf<T>::unpack(rr[j], r);
+#pragma unroll
+          for (int e = 0; e < E; ++e) y[j][e] += r[e];
+          store_vec<kTail>(static_cast<T*>(a.residual_out) + row * a.residual_out_stride, t, W, y[j]);
+        }
+      }
+      if (j + 1 == R) fetch(first + step);
+      sum[j] = 0.f;
+      if (a.norm) {
+#pragma unroll
+        for (int e = 0; e < E; ++e) sum[j] = fmaf(y[j][e], y[j][e], sum[j]);
+      }
+      if (a.weight) {
+#pragma unroll
+        for (int e = 0; e < E; e += 2) mul2(y[j] + e, w[e], w[e + 1]);
+      }
+      top[j] = 0.f;  // NaN elements leave the maximum alone and become NaN codes
+#pragma unroll
+      for (int e = 0; e < E; ++e) top[j] = fmaxf(top[j], fabsf(y[j][e]));
+    }
+#pragma unroll
+    for (int o = kLanes >> 1; o > 0; o >>= 1)
+#pragma unroll
+      for (int j = 0; j < R; ++j) {
+        if (a.norm) sum[j] += __shfl_xor_sync(0xffffffffu, sum[j], o);
+        if (a.codes) top[j] = fmaxf(top[j], __shfl_xor_sync(0xffffffffu, top[j], o));
+      }
+#pragma unroll
+    for (int j = 0; j < R; ++j) {
+      const int64_t row = first + j * kSide;
+      const float r = a.norm ? rsqrtf(sum[j] * inv_width + a.eps) : 1.f;
+      if (!mine || row >= a.n) continue;
+      if (a.codes) {
+        const float m = top[j] * r;
+        const float scale = m > 0.f ? fmaxf(m * (1.f / kE4m3Max), 1.17549435e-38f) : 1.f;
+        const float mul = r * rcp_approx(scale);
+        float z[E];
+#pragma unroll
+        for (int e = 0; e < E; e += 2) {
+          z[e] = y[j][e], z[e + 1] = y[j][e + 1];
+          mul2(z + e, mul, mul);
+        }
+        store_codes<kTail, E>(a.codes + row * a.codes_stride, t, W, z, 1.f);
+        if (t == 0) a.scale[row * a.scale_stride] = scale;
+      }
+      if (a.out) {
+#pragma unroll
+        for (int e = 0; e < E; e += 2) mul2(y[j] + e, r, r);
+        store_vec<kTail>(static_cast<T*>(a.out) + row * a.out_stride, t, W, y[j]);
+      }
+    }
+  }
+}
+
+template <typename T, bool kTail, bool kRes>
+int launch_narrow(const NormArgs& a, int num_sms, cudaStream_t st, bool pdl) {
+  constexpr int kRowsPerBlock = kNarrowThreads / (kNormBlock / VecOf<T>::E) * kNarrowRows;
+  int64_t blocks = ((int64_t)a.n + kRowsPerBlock - 1) / kRowsPerBlock;
+  if (blocks > (int64_t)num_sms * kNarrowBlocks) blocks = (int64_t)num_sms * kNarrowBlocks;
+  return launch_kernel(norm_narrow_kernel<T, kTail, kRes>, dim3((unsigned)blocks), dim3(kNarrowThreads), 0, st, pdl, a);
+}
+
 // The grid is what fits the device at once (or the rows, when fewer): each
 // block then walks its rows with the next one in flight.
 template <typename T, int VPT, bool kTail>
@@ -297,15 +414,22 @@ int launch_t(const NormArgs& a, int num_sms, cudaStream_t st, bool pdl) {
   constexpr int E = VecOf<T>::E;
   const int vecs = (a.width + E - 1) / E;
   int tpr, vpt, threads;
-  if (vecs <= 32) {  // a row per half warp or warp
-    tpr = vecs <= kNormBlock / E ? kNormBlock / E : 32;
+  if (a.width <= kNormBlock)
+    return a.width % E == 0 ? (a.residual ? launch_narrow<T, false, true>(a, num_sms, st, pdl)
+                                          : launch_narrow<T, false, false>(a, num_sms, st, pdl))
+                            : (a.residual ? launch_narrow<T, true, true>(a, num_sms, st, pdl)
+                                          : launch_narrow<T, true, false>(a, num_sms, st, pdl));
+  if (vecs <= 32) {  // a row per warp
+    tpr = 32;
     vpt = 1;
     threads = 256;
   } else {
-    // as few vectors per thread as the block's size allows: the shortest chain
-    // per row (4097 x 1000 fp32: 7.3 us with one, 7.7 with two, 11.2 with four;
-    // 16384 x 7168: the same with two and four)
-    int per = 1;
+    // one vector per thread where the block's size allows it (4097 x 1000 fp32:
+    // 5.7 us with one, 11.2 with four; bf16 rows of 1000 .. 4096: within 5%
+    // either way); wider rows take four, so that several rows share an SM
+    // (7168: 152 us with four, 176 with two at 19456 rows, 12.9 and 13.4 at
+    // 1216), or, with fewer rows than SMs, as few as fit
+    int per = vecs <= kNormMaxThreads ? 1 : a.n >= num_sms ? 4 : 2;
     while (((vecs + per - 1) / per + 31) / 32 * 32 > kNormMaxThreads) ++per;
     tpr = ((vecs + per - 1) / per + 31) / 32 * 32;
     vpt = (vecs + tpr - 1) / tpr;
