@@ -206,20 +206,29 @@ __device__ __forceinline__ void store_patch(uint32_t patch, const float* v, int 
     sts_u4(at(lane, j), r);
   }
   __syncwarp();
+  if (vec && cols >= C * E) {
 #pragma unroll
-  for (int i = 0; i < C; ++i) {
-    const int r = i * (32 / C) + lane / C, j = lane % C;
-    const uint4 x = lds_u4(at(r, j));
-    if (r < rows) {
-      T* dst = out + r * stride + j * E;
-      if (vec && (j + 1) * E <= cols) {
-        *reinterpret_cast<uint4*>(dst) = x;
-      } else {
-        T t[E];
-        memcpy(t, &x, 16);
-#pragma unroll
-        for (int e = 0; e < E; ++e)
-          if (j * E + e < cols) dst[e] = t[e];
+    for (int i = 0; i < C; ++i) {
+      const int r = i * (32 / C) + lane / C, j = lane % C;
+      const uint4 x = lds_u4(at(r, j));
+      if (r < rows) *reinterpret_cast<uint4*>(out + r * stride + j * E) = x;
+    }
+  } else {
+    // rows off the 16-byte boundary, or fewer columns: neighbouring lanes store
+    // neighbouring elements
+    constexpr int kCols = C * E;
+#pragma unroll 4
+    for (int i = lane; i < 32 * kCols; i += 32) {
+      const int r = i / kCols, c = i % kCols;
+      const uint32_t src = at(r, c / E) + (c % E) * (uint32_t)sizeof(T);
+      if (r < rows && c < cols) {
+        if constexpr (sizeof(T) == 2) {
+          uint16_t x;
+          asm volatile("ld.shared.u16 %0, [%1];\n" : "=h"(x) : "r"(src) : "memory");
+          *reinterpret_cast<uint16_t*>(out + r * stride + c) = x;
+        } else {
+          *reinterpret_cast<float*>(out + r * stride + c) = lds_f32(src);
+        }
       }
     }
   }

@@ -95,11 +95,11 @@ __device__ __forceinline__ void store_vec(T* row, int v, int width, const float*
 }
 // E codes of a row at vector v.
 template <bool kTail, int E>
-__device__ __forceinline__ void store_codes(uint8_t* row, int v, int width, const float* f, float mul) {
+__device__ __forceinline__ void store_codes(uint8_t* row, int v, int width, const float* f) {
   uint16_t c[E / 2];
 #pragma unroll
   for (int i = 0; i < E / 2; ++i)
-    c[i] = __nv_cvt_float2_to_fp8x2(make_float2(f[2 * i] * mul, f[2 * i + 1] * mul), __NV_SATFINITE, __NV_E4M3);
+    c[i] = __nv_cvt_float2_to_fp8x2(make_float2(f[2 * i], f[2 * i + 1]), __NV_SATFINITE, __NV_E4M3);
   if (!kTail || (v + 1) * E <= width) {
     if (E == 8)
       reinterpret_cast<uint2*>(row)[v] =
@@ -116,6 +116,26 @@ __device__ __forceinline__ float rcp_approx(float x) {
   float y;
   asm("rcp.approx.f32 %0, %1;\n" : "=f"(y) : "f"(x));
   return y;
+}
+
+// The scale of a block whose largest magnitude is m.
+__device__ __forceinline__ float block_scale(float m) {
+  return m > 0.f ? fmaxf(m / kE4m3Max, 1.17549435e-38f) : 1.f;
+}
+// f / scale to within a rounding that almost never differs from the exact
+// one's: the product with the reciprocal, corrected by its residual (one step
+// of Newton's iteration for the quotient).  Rows quantised as they are have
+// many values next to a border of two codes' ranges, where a quotient that is
+// off in the last place takes the other code.  An infinite scale leaves 0, and
+// NaN for an infinite f.
+template <int E>
+__device__ __forceinline__ void divide(float* f, float scale) {
+  const float inv = rcp_approx(scale), d = scale < INFINITY ? scale : 0.f;
+#pragma unroll
+  for (int e = 0; e < E; ++e) {
+    const float q = f[e] * inv;
+    f[e] = fmaf(fmaf(-q, d, f[e]), inv, q);
+  }
 }
 
 // tpr threads per row (a warp, or the whole block); blockDim.x / tpr rows per
@@ -240,9 +260,19 @@ __global__ void __launch_bounds__(kNormMaxThreads, VPT == 1 ? 2 : 1) norm_kernel
 #pragma unroll
         for (int o = kLanes >> 1; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
         m *= r;
-        const float scale = m > 0.f ? fmaxf(m * (1.f / kE4m3Max), 1.17549435e-38f) : 1.f;
+        const float scale = block_scale(m);
         if (live && v < vecs) {
-          store_codes<kTail, E>(cp, v, W, y[i], r * rcp_approx(scale));
+          float z[E];
+#pragma unroll
+          for (int e = 0; e < E; ++e) z[e] = y[i][e];
+          if (a.norm) {
+            const float mul = r * rcp_approx(scale);
+#pragma unroll
+            for (int e = 0; e < E; ++e) z[e] *= mul;
+          } else {
+            divide<E>(z, scale);
+          }
+          store_codes<kTail, E>(cp, v, W, z);
           if (t % kLanes == 0) fp[v / kLanes] = scale;
         }
       }
@@ -285,7 +315,7 @@ __device__ __forceinline__ void mul2(float* d, float b0, float b1) {
   asm("mov.b64 {%0, %1}, %2;\n" : "=f"(d[0]), "=f"(d[1]) : "l"(x));
 }
 
-template <typename T, bool kTail, bool kRes>
+template <typename T, bool kTail, bool kRes, bool kNorm>
 __global__ void __launch_bounds__(kNarrowThreads, kNarrowBlocks) norm_narrow_kernel(const NormArgs a) {
   constexpr int E = VecOf<T>::E, kLanes = kNormBlock / E, R = kNarrowRows;
   constexpr int kSide = kNarrowThreads / kLanes;       // rows side by side in a block
@@ -297,7 +327,7 @@ __global__ void __launch_bounds__(kNarrowThreads, kNarrowBlocks) norm_narrow_ker
   float w[E];
 #pragma unroll
   for (int e = 0; e < E; ++e) w[e] = 1.f;
-  if (a.weight && mine) VecOf<T>::unpack(load_vec<kTail>(static_cast<const T*>(a.weight), t, W), w);
+  if (kNorm && a.weight && mine) VecOf<T>::unpack(load_vec<kTail>(static_cast<const T*>(a.weight), t, W), w);
   const int64_t step = (int64_t)gridDim.x * (kSide * R);
   uint4 xr[R], rr[kRes ? R : 1];
   auto fetch = [&](int64_t at) {
@@ -331,11 +361,11 @@ __global__ void __launch_bounds__(kNarrowThreads, kNarrowBlocks) norm_narrow_ker
       }
       if (j + 1 == R) fetch(first + step);
       sum[j] = 0.f;
-      if (a.norm) {
+      if (kNorm) {
 #pragma unroll
         for (int e = 0; e < E; ++e) sum[j] = fmaf(y[j][e], y[j][e], sum[j]);
       }
-      if (a.weight) {
+      if (kNorm && a.weight) {
 #pragma unroll
         for (int e = 0; e < E; e += 2) mul2(y[j] + e, w[e], w[e + 1]);
       }
@@ -347,25 +377,27 @@ __global__ void __launch_bounds__(kNarrowThreads, kNarrowBlocks) norm_narrow_ker
     for (int o = kLanes >> 1; o > 0; o >>= 1)
 #pragma unroll
       for (int j = 0; j < R; ++j) {
-        if (a.norm) sum[j] += __shfl_xor_sync(0xffffffffu, sum[j], o);
+        if (kNorm) sum[j] += __shfl_xor_sync(0xffffffffu, sum[j], o);
         if (a.codes) top[j] = fmaxf(top[j], __shfl_xor_sync(0xffffffffu, top[j], o));
       }
 #pragma unroll
     for (int j = 0; j < R; ++j) {
       const int64_t row = first + j * kSide;
-      const float r = a.norm ? rsqrtf(sum[j] * inv_width + a.eps) : 1.f;
+      const float r = kNorm ? rsqrtf(sum[j] * inv_width + a.eps) : 1.f;
       if (!mine || row >= a.n) continue;
       if (a.codes) {
-        const float m = top[j] * r;
-        const float scale = m > 0.f ? fmaxf(m * (1.f / kE4m3Max), 1.17549435e-38f) : 1.f;
-        const float mul = r * rcp_approx(scale);
+        const float scale = block_scale(top[j] * r);
         float z[E];
 #pragma unroll
-        for (int e = 0; e < E; e += 2) {
-          z[e] = y[j][e], z[e + 1] = y[j][e + 1];
-          mul2(z + e, mul, mul);
+        for (int e = 0; e < E; ++e) z[e] = y[j][e];
+        if (kNorm) {
+          const float mul = r * rcp_approx(scale);
+#pragma unroll
+          for (int e = 0; e < E; e += 2) mul2(z + e, mul, mul);
+        } else {
+          divide<E>(z, scale);
         }
-        store_codes<kTail, E>(a.codes + row * a.codes_stride, t, W, z, 1.f);
+        store_codes<kTail, E>(a.codes + row * a.codes_stride, t, W, z);
         if (t == 0) a.scale[row * a.scale_stride] = scale;
       }
       if (a.out) {
@@ -377,12 +409,21 @@ __global__ void __launch_bounds__(kNarrowThreads, kNarrowBlocks) norm_narrow_ker
   }
 }
 
-template <typename T, bool kTail, bool kRes>
-int launch_narrow(const NormArgs& a, int num_sms, cudaStream_t st, bool pdl) {
+template <typename T, bool kTail, bool kRes, bool kNorm>
+int launch_narrow_kind(const NormArgs& a, int num_sms, cudaStream_t st, bool pdl) {
   constexpr int kRowsPerBlock = kNarrowThreads / (kNormBlock / VecOf<T>::E) * kNarrowRows;
   int64_t blocks = ((int64_t)a.n + kRowsPerBlock - 1) / kRowsPerBlock;
   if (blocks > (int64_t)num_sms * kNarrowBlocks) blocks = (int64_t)num_sms * kNarrowBlocks;
-  return launch_kernel(norm_narrow_kernel<T, kTail, kRes>, dim3((unsigned)blocks), dim3(kNarrowThreads), 0, st, pdl, a);
+  return launch_kernel(norm_narrow_kernel<T, kTail, kRes, kNorm>, dim3((unsigned)blocks), dim3(kNarrowThreads), 0, st, pdl, a);
+}
+
+template <typename T, bool kTail>
+int launch_narrow(const NormArgs& a, int num_sms, cudaStream_t st, bool pdl) {
+  if (a.residual)
+    return a.norm ? launch_narrow_kind<T, kTail, true, true>(a, num_sms, st, pdl)
+                  : launch_narrow_kind<T, kTail, true, false>(a, num_sms, st, pdl);
+  return a.norm ? launch_narrow_kind<T, kTail, false, true>(a, num_sms, st, pdl)
+                : launch_narrow_kind<T, kTail, false, false>(a, num_sms, st, pdl);
 }
 
 // The grid is what fits the device at once (or the rows, when fewer): each
@@ -415,10 +456,7 @@ int launch_t(const NormArgs& a, int num_sms, cudaStream_t st, bool pdl) {
   const int vecs = (a.width + E - 1) / E;
   int tpr, vpt, threads;
   if (a.width <= kNormBlock)
-    return a.width % E == 0 ? (a.residual ? launch_narrow<T, false, true>(a, num_sms, st, pdl)
-                                          : launch_narrow<T, false, false>(a, num_sms, st, pdl))
-                            : (a.residual ? launch_narrow<T, true, true>(a, num_sms, st, pdl)
-                                          : launch_narrow<T, true, false>(a, num_sms, st, pdl));
+    return a.width % E == 0 ? launch_narrow<T, false>(a, num_sms, st, pdl) : launch_narrow<T, true>(a, num_sms, st, pdl);
   if (vecs <= 32) {  // a row per warp
     tpr = 32;
     vpt = 1;

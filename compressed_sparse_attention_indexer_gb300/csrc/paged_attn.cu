@@ -190,6 +190,88 @@ struct Cursor {
   }
 };
 
+// The products of a warp's weights with its V rows in shared memory (at vt):
+// pv(mt, x, j, b0, b1) for each 16-row group x and n-tile j, b0 / b1 the
+// fragment of V.
+template <int D, int MT, bool kFp8, typename F>
+__device__ __forceinline__ void v_products(uint32_t vt, int lane, F&& pv) {
+  using Sh = PaShape<D, MT, kFp8>;
+  constexpr int kGroups = Sh::kGroups;
+  const int g = lane >> 2, c = lane & 3;
+#pragma unroll
+  for (int x = 0; x < kGroups; ++x) {
+    if constexpr (kFp8) {
+      // n-tile j holds dims 16 n + j (n = 0..7): thread g takes codes 16 g .. 16 g + 15 of its four rows
+      uint32_t w[4][4];
+#pragma unroll
+      for (int z = 0; z < 4; ++z) {
+        const int r = x * 16 + (z >> 1) * 8 + c * 2 + (z & 1);
+        const uint4 v = lds_u4(vt + r * Sh::kRowBytes + swizzle<true>(r, g) * 16);
+        w[z][0] = v.x; w[z][1] = v.y; w[z][2] = v.z; w[z][3] = v.w;
+      }
+#pragma unroll
+      for (int y = 0; y < 4; ++y) {
+#pragma unroll
+        for (int z = 0; z < 4; z += 2) {  // dims 16 g + 4 y + z, + 1: rows interleaved pair by pair
+          const uint32_t sel = z ? 0x7362 : 0x5140;
+          uint32_t a0, a1, b0, b1;
+          e4m3x4_to_f16x2(__byte_perm(w[0][y], w[1][y], sel), a0, a1);
+          e4m3x4_to_f16x2(__byte_perm(w[2][y], w[3][y], sel), b0, b1);
+#pragma unroll
+          for (int mt = 0; mt < MT; ++mt) {
+            pv(mt, x, y * 4 + z, a0, b0);
+            pv(mt, x, y * 4 + z + 1, a1, b1);
+          }
+        }
+      }
+    } else {
+#pragma unroll
+      for (int dt = 0; dt < D / 16; ++dt) {
+        const int r = x * 16 + (((lane >> 3) & 1) << 3) + (lane & 7), ch = dt * 2 + (lane >> 4);
+        uint32_t b0, b1, b2, b3;
+        ldsm_x4_trans(vt + r * Sh::kRowBytes + swizzle<false>(r, ch) * 16, b0, b1, b2, b3);
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt) {
+          pv(mt, x, dt * 2, b0, b1);
+          pv(mt, x, dt * 2 + 1, b2, b3);
+        }
+      }
+    }
+  }
+}
+
+// O += P V where a V row that some token of the warp's tile does not see holds
+// a NaN or an infinity: a pass per token with its own rows kept and its own
+// query rows taken.  Out of line, on copies of o and pf: rare, and the common
+// path keeps its registers.
+template <int D, int MT, bool kFp8>
+__device__ __noinline__ void v_products_apart(float* o, const uint32_t* pf, const int* sq, uint32_t vt, int lane, int base,
+                                              int p_first, int S, int win) {
+  using Sh = PaShape<D, MT, kFp8>;
+  const int c = lane & 3;
+  for (int t = 0; t < S; ++t) {
+    const int last = p_first + t;
+    uint32_t keep[2 * Sh::kGroups];
+#pragma unroll
+    for (int n = 0; n < 2 * Sh::kGroups; ++n) {
+      keep[n] = 0;
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const int r = base + n * 8 + c * 2 + e;
+        if (r <= last && (win == 0 || r > last - win)) keep[n] |= e ? 0xffff0000u : 0xffffu;
+      }
+    }
+    v_products<D, MT, kFp8>(vt, lane, [&](int mt, int x, int j, uint32_t b0, uint32_t b1) {
+      float* d = o + (mt * (D / 8) + j) * 4;
+      float y[4] = {d[0], d[1], d[2], d[3]};
+      mma16<kFp8>(y, pf + (mt * Sh::kGroups + x) * 4, b0 & keep[2 * x], b1 & keep[2 * x + 1]);
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        if (sq[mt * 2 + (i >> 1)] == t) d[i] = y[i];
+    });
+  }
+}
+
 // A cut of the list of tiles: before this tile of this unit.
 struct Cut {
   int b, unit, tile;
@@ -343,7 +425,7 @@ __global__ void __launch_bounds__(PaShape<D, MT, kFp8>::kThreads, 1)
   uint32_t qf[Sh::kQReg ? D / 16 : 1][4];
   float qmul[MT][2];                               // E4M3: the power of two taken out of the thread's query rows
   float o[MT][D / 8][4], m[MT][2], l[MT][2];
-  int pos[MT][2], sq[MT][2];                       // last visible row and token of the thread's query rows
+  int pos[MT][2];                                  // last visible row of the thread's query rows
   int seg_first = 0;                               // step at which the current piece started
   bool seg_new = true;
   const float scale2 = a.scale * kLog2e;
@@ -380,7 +462,6 @@ __global__ void __launch_bounds__(PaShape<D, MT, kFp8>::kThreads, 1)
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
           const int i = row0 + mt * 16 + g + 8 * e;
-          sq[mt][e] = i < qrows ? i / group : a.S;
           pos[mt][e] = i < qrows ? cu.sp.L - a.S + i / group : -1;
           m[mt][e] = -INFINITY;
           l[mt][e] = 0.f;
@@ -604,74 +685,41 @@ __global__ void __launch_bounds__(PaShape<D, MT, kFp8>::kThreads, 1)
         }
       }
       // ---- O += P V
-      auto products = [&](auto&& pv) {
+      // Tokens of one MMA may see different rows here.  A zero weight takes a
+      // finite row's part out exactly; a NaN or infinity (looked for in the
+      // warp's V rows) takes the way apart.  Both give the same bits.
+      bool apart = edge && a.S > 1;
+      if (apart) {
+        bool bad = false;
+        for (int x = lane; x < kPer * Sh::kChunks; x += 32) {
+          const uint4 v = lds_u4(vt + x * 16);
+          const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
-        for (int x = 0; x < kGroups; ++x) {
-          if constexpr (kFp8) {
-            // n-tile j holds dims 16 n + j (n = 0..7): thread g takes codes 16 g .. 16 g + 15 of its four rows
-            uint32_t w[4][4];
-#pragma unroll
-            for (int z = 0; z < 4; ++z) {
-              const int r = x * 16 + (z >> 1) * 8 + c * 2 + (z & 1);
-              const uint4 v = lds_u4(vt + r * Sh::kRowBytes + swizzle<true>(r, g) * 16);
-              w[z][0] = v.x; w[z][1] = v.y; w[z][2] = v.z; w[z][3] = v.w;
-            }
-#pragma unroll
-            for (int y = 0; y < 4; ++y) {
-#pragma unroll
-              for (int z = 0; z < 4; z += 2) {  // dims 16 g + 4 y + z, + 1: rows interleaved pair by pair
-                const uint32_t sel = z ? 0x7362 : 0x5140;
-                uint32_t a0, a1, b0, b1;
-                e4m3x4_to_f16x2(__byte_perm(w[0][y], w[1][y], sel), a0, a1);
-                e4m3x4_to_f16x2(__byte_perm(w[2][y], w[3][y], sel), b0, b1);
-#pragma unroll
-                for (int mt = 0; mt < MT; ++mt) {
-                  pv(mt, x, y * 4 + z, a0, b0);
-                  pv(mt, x, y * 4 + z + 1, a1, b1);
-                }
-              }
-            }
-          } else {
-#pragma unroll
-            for (int dt = 0; dt < D / 16; ++dt) {
-              const int r = x * 16 + (((lane >> 3) & 1) << 3) + (lane & 7), ch = dt * 2 + (lane >> 4);
-              uint32_t b0, b1, b2, b3;
-              ldsm_x4_trans(vt + r * Sh::kRowBytes + swizzle<false>(r, ch) * 16, b0, b1, b2, b3);
-#pragma unroll
-              for (int mt = 0; mt < MT; ++mt) {
-                pv(mt, x, dt * 2, b0, b1);
-                pv(mt, x, dt * 2 + 1, b2, b3);
-              }
-            }
-          }
+          for (int i = 0; i < 4; ++i)
+            bad |= kFp8 ? (((w[i] & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u) != 0
+                        : (w[i] & 0x7f80u) == 0x7f80u || (w[i] & 0x7f800000u) == 0x7f800000u;
         }
-      };
-      if (!edge || a.S == 1) {
-        products([&](int mt, int x, int j, uint32_t b0, uint32_t b1) { mma16<kFp8>(o[mt][j], pf[mt][x], b0, b1); });
+        apart = __any_sync(0xffffffffu, bad);
+      }
+      if (!apart) {
+        v_products<D, MT, kFp8>(vt, lane, [&](int mt, int x, int j, uint32_t b0, uint32_t b1) {
+          mma16<kFp8>(o[mt][j], pf[mt][x], b0, b1);
+        });
       } else {
-        // tokens of one MMA see different rows here: one pass per token with its
-        // own V rows kept and its own query rows added (a zero weight times a
-        // NaN is a NaN)
-        for (int t = 0; t < a.S; ++t) {
-          const int last = p_first + t;
-          uint32_t keep[2 * kGroups];
+        float o2[MT][D / 8][4];
+        uint32_t pf2[MT][kGroups][4];
+        int sq2[MT][2];
+        memcpy(o2, o, sizeof o2);
+        memcpy(pf2, pf, sizeof pf2);
 #pragma unroll
-          for (int n = 0; n < 2 * kGroups; ++n) {
-            keep[n] = 0;
+        for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
-            for (int e = 0; e < 2; ++e) {
-              const int r = base + n * 8 + c * 2 + e;
-              if (r <= last && (a.win == 0 || r > last - a.win)) keep[n] |= e ? 0xffff0000u : 0xffffu;
-            }
+          for (int e = 0; e < 2; ++e) {
+            const int i = row0 + mt * 16 + g + 8 * e;
+            sq2[mt][e] = i < qrows ? i / group : a.S;
           }
-          products([&](int mt, int x, int j, uint32_t b0, uint32_t b1) {
-            float y[4] = {0.f, 0.f, 0.f, 0.f};
-            mma16<kFp8>(y, pf[mt][x], b0 & keep[2 * x], b1 & keep[2 * x + 1]);
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-              if (sq[mt][i >> 1] == t) o[mt][j][i] += y[i];
-          });
-        }
+        v_products_apart<D, MT, kFp8>(&o2[0][0][0], &pf2[0][0][0], &sq2[0][0], vt, lane, base, p_first, a.S, a.win);
+        memcpy(o, o2, sizeof o);
       }
     }
     __syncwarp();
@@ -862,6 +910,9 @@ int launch_shape(const PagedArgs& a, int num_sms, cudaStream_t st, bool pdl) {
   const int grid = tiles < num_sms ? (int)tiles : num_sms;
   const int r = launch_kernel(kern, dim3(grid), dim3(Sh::kThreads), Sh::kSmem, st, pdl, a, chunks, part, joins);
   if (r < 0) return r;
+  // a unit of one tile is never cut
+  const int span = a.win > 0 && a.win + a.S - 1 < a.max_len ? a.win + a.S - 1 + Sh::kTile - 1 : a.max_len;
+  if (span <= Sh::kTile) return r;
   const int rows = qrows < Sh::kRows ? qrows : Sh::kRows;
   const int r2 = launch_kernel(paged_join_kernel<D>, dim3(grid, rows), dim3(32 * kJoinWarps), 0, st, pdl, a, chunks,
                                (int)Sh::kRows, (const float*)part, (const PaJoin*)joins);
