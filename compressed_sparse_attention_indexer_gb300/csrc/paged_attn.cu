@@ -65,7 +65,11 @@ struct PaShape {
   static constexpr bool kQReg = MT == 1 && D <= 128 && !kFp8;    // Q fragments in registers
   static constexpr int kQBytes = kQReg ? 0 : kRows * D * 2 + (kFp8 ? kRows * 4 : 0);
   static constexpr int kSlots = kWarps < 8 ? kWarps / 2 : kFp8 && MT == 1 ? 2 : 4;
-  static constexpr int kSlotFloats = kRows * D;
+  // a slot: 16 MT rows of fp32 dims.  bf16: 8 floats of padding per row let the
+  // threads' 8-byte pieces of eight rows fall on different banks; E4M3 (16-byte
+  // pieces, see e4m3_piece) needs none
+  static constexpr int kPitch = D + (kFp8 ? 0 : 8);
+  static constexpr int kSlotFloats = kRows * kPitch;
   static constexpr int kSlotBytes = kSlots * (kSlotFloats + 2 * kRows) * 4;
   static constexpr int kRoom = (226 * 1024 - kQBytes - kSlotBytes - kWarps * kScaleBytes) / (kWarps * kWarpStage);
   static constexpr int kStages = kRoom > 6 ? 6 : kRoom;
@@ -160,6 +164,11 @@ template <bool kFp8>
 __device__ __forceinline__ int swizzle(int row, int ch) {
   return kFp8 ? ch ^ ((((row >> 1) & 3) << 1) ^ ((row & 1) << 2)) : ch ^ (row & 7);
 }
+
+// Where piece x (dims 32 c + 4 x .. + 3) of row r lies in its slot row: the
+// pieces of the four threads of a quad, and of neighbouring rows, fall on
+// different banks.
+__device__ __forceinline__ int e4m3_piece(int r, int c, int x) { return 32 * c + ((x ^ c ^ ((r & 1) << 2)) << 2); }
 
 // Tiles of a request (at least one, so that every unit is visited and
 // written): the rows any of its S queries sees are [lo, L).
@@ -736,7 +745,6 @@ __global__ void __launch_bounds__(PaShape<D, MT, kFp8>::kThreads, 1)
         }
       float* so = slots + (warp % Sh::kSlots) * Sh::kSlotFloats;
       float* sml = slots + Sh::kSlots * Sh::kSlotFloats + (warp % Sh::kSlots) * 2 * Sh::kRows;
-      auto dim_of = [&](int j, int e) { return kFp8 ? 32 * c + 16 * e + j : 8 * j + 2 * c + e; };
       auto put = [&] {
 #pragma unroll
         for (int mt = 0; mt < MT; ++mt)
@@ -744,17 +752,28 @@ __global__ void __launch_bounds__(PaShape<D, MT, kFp8>::kThreads, 1)
           for (int e = 0; e < 2; ++e) {
             const int r = mt * 16 + g + 8 * e;
             if (c == 0) sml[r] = m[mt][e], sml[Sh::kRows + r] = l[mt][e];
+            if constexpr (kFp8) {
 #pragma unroll
-            for (int j = 0; j < D / 8; ++j) {
-              so[r * D + dim_of(j, 0)] = o[mt][j][2 * e];
-              so[r * D + dim_of(j, 1)] = o[mt][j][2 * e + 1];
+              for (int x = 0; x < 8; ++x) {   // dims 32 c + 4 x .. + 3
+                const int j = (x & 3) * 4, k = 2 * e + (x >> 2);
+                *reinterpret_cast<float4*>(so + r * Sh::kPitch + e4m3_piece(r, c, x)) =
+                    make_float4(o[mt][j][k], o[mt][j + 1][k], o[mt][j + 2][k], o[mt][j + 3][k]);
+              }
+            } else {
+#pragma unroll
+              for (int j = 0; j < D / 8; ++j)
+                *reinterpret_cast<float2*>(so + r * Sh::kPitch + 8 * j + 2 * c) = make_float2(o[mt][j][2 * e], o[mt][j][2 * e + 1]);
             }
           }
       };
+      // warps that held rows in this piece (all of them if it had two tiles)
+      const int left = (cu.sp.L - (cu.sp.t0 + cu.tile) * kTile + kPer - 1) / kPer;
+      const int held = step > seg_first || left > Sh::kWarps ? Sh::kWarps : left;
       __syncthreads();   // the slots' last readers are done
       // kSlots warps at a time hand their state to the kSlots before them
 #pragma unroll
       for (int from = Sh::kWarps - Sh::kSlots; from > 0; from -= Sh::kSlots) {
+        if (from >= held) continue;
         if (warp >= from && warp < from + Sh::kSlots) put();
         __syncthreads();
         if (warp >= from - Sh::kSlots && warp < from) {
@@ -767,10 +786,23 @@ __global__ void __launch_bounds__(PaShape<D, MT, kFp8>::kThreads, 1)
               const float f1 = fast_exp2(m[mt][e] - ref), f2 = fast_exp2(m2 - ref);
               l[mt][e] = l[mt][e] * f1 + sml[Sh::kRows + r] * f2;
               m[mt][e] = top;
+              if constexpr (kFp8) {
 #pragma unroll
-              for (int j = 0; j < D / 8; ++j) {
-                o[mt][j][2 * e] = o[mt][j][2 * e] * f1 + so[r * D + dim_of(j, 0)] * f2;
-                o[mt][j][2 * e + 1] = o[mt][j][2 * e + 1] * f1 + so[r * D + dim_of(j, 1)] * f2;
+                for (int x = 0; x < 8; ++x) {
+                  const int j = (x & 3) * 4, k = 2 * e + (x >> 2);
+                  const float4 v = *reinterpret_cast<const float4*>(so + r * Sh::kPitch + e4m3_piece(r, c, x));
+                  o[mt][j][k] = o[mt][j][k] * f1 + v.x * f2;
+                  o[mt][j + 1][k] = o[mt][j + 1][k] * f1 + v.y * f2;
+                  o[mt][j + 2][k] = o[mt][j + 2][k] * f1 + v.z * f2;
+                  o[mt][j + 3][k] = o[mt][j + 3][k] * f1 + v.w * f2;
+                }
+              } else {
+#pragma unroll
+                for (int j = 0; j < D / 8; ++j) {
+                  const float2 v = *reinterpret_cast<const float2*>(so + r * Sh::kPitch + 8 * j + 2 * c);
+                  o[mt][j][2 * e] = o[mt][j][2 * e] * f1 + v.x * f2;
+                  o[mt][j][2 * e + 1] = o[mt][j][2 * e + 1] * f1 + v.y * f2;
+                }
               }
             }
         }
@@ -787,6 +819,7 @@ __global__ void __launch_bounds__(PaShape<D, MT, kFp8>::kThreads, 1)
       const int slot = seg_first == 0 ? 0 : 1;
       const int64_t pslot = (int64_t)blockIdx.x * 2 + slot;
       for (int r = warp; r < Sh::kRows && row0 + r < qrows; r += Sh::kWarps) {
+        const float* row_at = slots + r * Sh::kPitch + (kFp8 ? e4m3_piece(r, lane >> 3, lane & 7) : lane * (D / 32));
         float top = -INFINITY;
 #pragma unroll
         for (int x = 0; x < Sh::kSlots; ++x) top = fmaxf(top, ml[x * 2 * Sh::kRows + r]);
@@ -800,7 +833,7 @@ __global__ void __launch_bounds__(PaShape<D, MT, kFp8>::kThreads, 1)
           sum += ml[x * 2 * Sh::kRows + Sh::kRows + r] * f;
 #pragma unroll
           for (int i = 0; i < D / 32; ++i)
-            acc[i] += slots[x * Sh::kSlotFloats + r * D + lane * (D / 32) + i] * f;
+            acc[i] += row_at[x * Sh::kSlotFloats + i] * f;
         }
         if (whole) {
           const int i = row0 + r, s = i / group, hd = h * group + i - s * group;
