@@ -793,6 +793,7 @@ int csa_norm_rows(const csa_norm* a, void* stream) {
   if (a->n < 0 || a->width < 1) return fail(CSA_ERR_INVALID_ARG, "need n >= 0 and width >= 1");
   if (a->width > csa::norm_max_width(a->dtype))
     return fail(CSA_ERR_UNSUPPORTED, "width %d above %d", a->width, csa::norm_max_width(a->dtype));
+  if (a->n == 0) { g_err.clear(); return CSA_OK; }
   if (a->norm != 0 && a->norm != 1) return fail(CSA_ERR_INVALID_ARG, "norm must be 0 or 1");
   if (!(a->eps >= 0.f)) return fail(CSA_ERR_INVALID_ARG, "eps must be >= 0");
   if (!a->norm && a->weight) return fail(CSA_ERR_INVALID_ARG, "weight given with norm = 0");
@@ -800,7 +801,6 @@ int csa_norm_rows(const csa_norm* a, void* stream) {
     return fail(CSA_ERR_INVALID_ARG, "residual and residual_out go together");
   if (!a->codes != !a->scale) return fail(CSA_ERR_INVALID_ARG, "codes and scale go together");
   if (!a->out && !a->codes) return fail(CSA_ERR_INVALID_ARG, "neither out nor codes given");
-  if (a->n == 0) { g_err.clear(); return CSA_OK; }
   const int es = a->dtype == CSA_DTYPE_BF16 ? 2 : 4;
   int rc = check_rows("x", a->x, a->x_stride, a->width, es);
   if (!rc && a->residual) rc = check_rows("residual", a->residual, a->residual_stride, a->width, es);
@@ -837,6 +837,8 @@ int csa_fp8_matmul(const csa_fp8_mm* a, void* stream) {
   if (a->out_dtype != CSA_DTYPE_BF16 && a->out_dtype != CSA_DTYPE_F32)
     return fail(CSA_ERR_UNSUPPORTED, "out_dtype must be CSA_DTYPE_F32 or CSA_DTYPE_BF16");
   if (a->M < 0 || a->N < 0 || a->K < 1) return fail(CSA_ERR_INVALID_ARG, "need M >= 0, N >= 0 and K >= 1");
+  if (a->M > (1 << 30) || a->N > (1 << 30) || a->K > (1 << 30))
+    return fail(CSA_ERR_UNSUPPORTED, "M, N or K above 2^30");
   if (a->M == 0 || a->N == 0) { g_err.clear(); return CSA_OK; }
   int rc = check_rows("a", a->a, a->a_stride, a->K, 1);
   if (!rc) rc = check_rows("b", a->b, a->b_stride, a->K, 1);
@@ -918,7 +920,8 @@ int csa_paged_attn(const csa_paged* a, void* stream) {
                 (long long)csa::paged_attn_workspace(a->dim, sms));
   csa::PagedArgs k;
   k.B = a->B; k.S = a->S; k.heads = a->heads; k.kv_heads = a->kv_heads; k.dim = a->dim;
-  k.win = a->win; k.max_len = a->max_len;
+  k.win = a->win >= a->max_len ? 0 : a->win;  // a window over everything is none
+  k.max_len = a->max_len;
   k.scale = a->softmax_scale > 0.f ? a->softmax_scale : (float)(1.0 / sqrt((double)a->dim));
   k.ctx_len = a->ctx_len;
   k.q = a->q; k.q_stride = a->q_stride;

@@ -526,13 +526,16 @@ __global__ void __launch_bounds__(PaShape<D, MT, kFp8>::kThreads, 1)
     const uint32_t kt = ring + (step % Sh::kStages) * Sh::kWarpStage, vt = kt + kPer * Sh::kRowBytes;
     const int base = (cu.sp.t0 + cu.tile) * kTile + warp * kPer;   // first of the warp's rows
     if (base < cu.sp.L && base + kPer - 1 >= cu.sp.lo) {
+      bool wide = false;
       if constexpr (kFp8) {
         // lane r: its row's scales as the scores and weights use them.  The
         // weight of a V row is p |v_scale|, so v_scale goes into the exponent
         // (lv) and the maximum is taken over both: the f16 weights then keep
         // their precision whatever the scales.  The softmax's own sum takes
-        // the factor out again (1 / |v_scale|).  |v_scale| below 2^-100 counts
-        // as 2^-100 there, and the rest of it is kept in the sign factor.
+        // the factor out again (1 / |v_scale|), or, where a row's |lv| is so
+        // large that the weight may vanish while its part of the sum does not
+        // (`wide`), has an exponential of its own.  |v_scale| below 2^-100
+        // (zero) counts as 2^-100, the rest of it is kept in the sign factor.
         const uint32_t src = kt + 2 * kPer * Sh::kRowBytes + (lane % kPer) * 4;
         const float ks = lds_f32(src) * scale2, vs = lds_f32(src + kPer * 4);
         const float lv = fast_log2(fmaxf(fabsf(vs), 7.8886091e-31f)), inv = fast_exp2(-lv);
@@ -541,6 +544,7 @@ __global__ void __launch_bounds__(PaShape<D, MT, kFp8>::kThreads, 1)
           sts_f4(rowsc + (lane % kPer) * 16, ks, lv, inv, vs * inv);
         else
           sts_f4(rowsc + (lane % kPer) * 16, ks, __uint_as_float(0x7fffffffu), 1.f, 1.f);
+        wide = __any_sync(0xffffffffu, !(fabsf(lv) <= 40.f));
         __syncwarp();
       }
       // ---- S = Q K^T: 16 MT query rows x kPer rows (n = 8 tiles)
@@ -683,9 +687,20 @@ __global__ void __launch_bounds__(PaShape<D, MT, kFp8>::kThreads, 1)
             for (int i = 0; i < 4; ++i) {
               const float ref = m[mt][i >> 1] == -INFINITY ? 0.f : m[mt][i >> 1];
               const float w = fast_exp2(s[mt][2 * x + n][i] - ref);
-              l[mt][i >> 1] += kFp8 ? w * inv[2 * x + n][i & 1] : w;
+              if (!kFp8) l[mt][i >> 1] += w;
+              else if (!wide) l[mt][i >> 1] += w * inv[2 * x + n][i & 1];
               p[n][i] = kFp8 ? w * sgn[2 * x + n][i & 1] : w;
             }
+          if (kFp8 && wide) {
+#pragma unroll
+            for (int n = 0; n < 2; ++n)
+#pragma unroll
+              for (int i = 0; i < 4; ++i) {
+                const float ref = m[mt][i >> 1] == -INFINITY ? 0.f : m[mt][i >> 1];
+                const float lv = lds_f32(rowsc + ((2 * x + n) * 8 + c * 2 + (i & 1)) * 16 + 4), t = s[mt][2 * x + n][i];
+                l[mt][i >> 1] += t == -INFINITY ? 0.f : fast_exp2(t - lv - ref);
+              }
+          }
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
             const float x0 = p[i >> 1][(i & 1) * 2], x1 = p[i >> 1][(i & 1) * 2 + 1];

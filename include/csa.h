@@ -316,7 +316,7 @@ CSA_API int csa_norm_rows(const csa_norm *a, void *stream);
  * one may be shorter.  The sums are fp32, out is rounded once.  a_scale and
  * b_scale may be any fp32 numbers. */
 typedef struct {
-    int32_t M, N, K;          /* M = 0 or N = 0: a no-op; K >= 1                    */
+    int32_t M, N, K;          /* M = 0 or N = 0: a no-op; K >= 1; at most 2^30      */
     int32_t out_dtype;        /* CSA_DTYPE_BF16 or CSA_DTYPE_F32                    */
     const uint8_t *a; int64_t a_stride;                /* [M, K]                    */
     const float *a_scale; int64_t a_scale_stride;      /* [M, ceil(K / 128)]        */
@@ -330,7 +330,7 @@ typedef struct {
 /* Rows of a and b start on 16-byte boundaries (pointer and stride multiples of
  * 16); out needs the alignment of its element only, and nothing past N is
  * written; out must not overlap an input.  Returns CSA_ERR_INVALID_ARG or
- * CSA_ERR_UNSUPPORTED (out_dtype). */
+ * CSA_ERR_UNSUPPORTED (out_dtype, sizes). */
 CSA_API int csa_fp8_matmul(const csa_fp8_mm *a, void *stream);
 
 /* Dense causal attention of the S newest tokens of each request over all of
@@ -345,7 +345,8 @@ CSA_API int csa_fp8_matmul(const csa_fp8_mm *a, void *stream);
  * two halves of one pool.  Row r of request b is pool row off[b] + r, or
  * table[b * table_stride + r / block] * block + r % block with a block table,
  * as in csa_batch.  Scores, the softmax's maximum and sum, and the sum over
- * rows are fp32; the weights are rounded to bf16 for the product with v. */
+ * rows are fp32; the weights are rounded to bf16 for the product with v (E4M3
+ * pools: to f16, and q to 2^-25 of its row's largest element). */
 typedef struct {
     int32_t B, S;             /* requests (0: a no-op), new tokens per request      */
     int32_t heads, kv_heads;  /* heads a multiple of kv_heads                       */
@@ -377,8 +378,11 @@ typedef struct {
 } csa_paged;
 
 /* q, k, v and out start on 16-byte boundaries and their strides keep the rows
- * there.  Returns CSA_ERR_INVALID_ARG, CSA_ERR_UNSUPPORTED (dim, kv_dtype) or
- * CSA_ERR_WORKSPACE (workspace_bytes too small). */
+ * there; pool rows lie at most 2 GB apart.  |v_scale| is at most 2^100; one that is
+ * infinite or NaN makes out and lse NaN for the queries that see its row.  Returns
+ * CSA_ERR_INVALID_ARG, CSA_ERR_UNSUPPORTED (dim, kv_dtype, max_len above 2^30,
+ * S above 2^16, S * heads above 2^20) or CSA_ERR_WORKSPACE (workspace_bytes too
+ * small). */
 CSA_API int csa_paged_attn(const csa_paged *a, void *stream);
 
 /* Bytes of workspace csa_paged_attn needs on the current device for heads of

@@ -44,6 +44,9 @@ def test_empty_calls_are_no_ops(L):
     (dict(M=-1), csa.CSA_ERR_INVALID_ARG),
     (dict(N=-1), csa.CSA_ERR_INVALID_ARG),
     (dict(K=0), csa.CSA_ERR_INVALID_ARG),
+    (dict(M=(1 << 30) + 1), csa.CSA_ERR_UNSUPPORTED),
+    (dict(N=(1 << 31) - 1), csa.CSA_ERR_UNSUPPORTED),
+    (dict(K=(1 << 31) - 1), csa.CSA_ERR_UNSUPPORTED),
     (dict(out_dtype=csa.CSA_DTYPE_FP8_E4M3), csa.CSA_ERR_UNSUPPORTED),
     (dict(a=None), csa.CSA_ERR_INVALID_ARG),
     (dict(a=0x10008), csa.CSA_ERR_INVALID_ARG),
@@ -243,3 +246,31 @@ def test_repeats_bit_for_bit_on_another_stream_and_in_a_graph(m, n, k):
     graph.replay()
     torch.cuda.synchronize()
     assert torch.equal(other._out, first) and torch.equal(graphed._out, first) and torch.equal(op._out, first)
+
+
+@pytest.mark.gpu
+def test_empty_matrices():
+    _gpu()
+    b, sb = torch.zeros(200, 256, dtype=torch.uint8, device=DEV), torch.ones(2, 2, device=DEV)
+    a, sa = torch.zeros(3, 256, dtype=torch.uint8, device=DEV), torch.ones(3, 2, device=DEV)
+    assert csa.Fp8Matmul(a[:0], sa[:0], b, sb)().shape == (0, 200)
+    assert csa.Fp8Matmul(a, sa, b[:0], sb[:0])().shape == (3, 0)
+
+
+@pytest.mark.gpu
+def test_two_products_at_once_on_two_streams():
+    # kernels with tensor memory of their own beside each other, of different shapes
+    _gpu()
+    g = torch.Generator(device=DEV).manual_seed(1)
+    ops, firsts = [], []
+    for m, n, k in ((1, 8192, 1536), (60, 4096, 2048), (300, 1000, 2048), (2600, 2600, 512)):
+        a, b = _codes(m, k, g), _codes(n, k, g)
+        ops.append(csa.Fp8Matmul(a, _scales(m, k // 128, g), b, _scales(-(-n // 128), k // 128, g)))
+        firsts.append(ops[-1]().clone())
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in ops]
+    for _ in range(50):
+        for op, st in zip(ops, streams):
+            op(stream=st)
+    torch.cuda.synchronize()
+    assert all(torch.equal(op._out, f) for op, f in zip(ops, firsts))

@@ -77,6 +77,7 @@ def _call(L, **kw):
 
 def test_empty_call_is_a_no_op(L):
     assert _call(L, n=0) == csa.CSA_OK
+    assert _call(L, n=0, x=None, out=None, codes=None, scale=None) == csa.CSA_OK
 
 
 @pytest.mark.parametrize("kw,code", [
@@ -300,3 +301,31 @@ def test_width_128_makes_the_fp8_indexer_key_pool():
                                    values[off:off + vis])
         err = np.abs(out[b, :vis].cpu().numpy() - want)
         assert err.max() <= 2e-5 * np.abs(want).max()
+
+
+@pytest.mark.gpu
+def test_no_rows():
+    _gpu()
+    x = torch.zeros(0, 256, dtype=torch.bfloat16, device=DEV)
+    got = csa.NormRows(x, residual=x, out=True)()
+    assert got["out"].shape == (0, 256) and got["codes"].shape == (0, 256) and got["scale"].shape == (0, 2)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_codes_of_rows_as_they_are_are_the_nearest(dtype):
+    # norm = 0: the quotient y / scale decides the code; off a border by less than its own rounding it may take
+    # either neighbour, elsewhere it is the fp64 quotient's
+    _gpu()
+    x = _rows(3000, 384, dtype, 8)
+    got = csa.NormRows(x.to(DEV), norm=False)()
+    torch.cuda.synchronize()
+    z = x.double().view(3000, 3, 128) / got["scale"].cpu().double()[..., None]
+    want = z.float().to(torch.float8_e4m3fn).double()
+    code = got["codes"].cpu().double().view(3000, 3, 128)
+    off = code != want
+    # next to a border: half an E4M3 step from the code, to within 2^-22 of the value
+    _, e = torch.frexp(z.abs().clamp_min(2.0 ** -9))
+    half = torch.ldexp(torch.ones_like(z), (e - 1).clamp_min(-6) - 4)
+    assert (((z - want).abs() - half).abs()[off] <= 2.0 ** -22 * z.abs()[off]).all()
+    assert off.double().mean() < 1e-5

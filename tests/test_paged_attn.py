@@ -225,7 +225,7 @@ def test_several_tokens_and_windows(s, h, hk, d, fp8, win):
 
 @pytest.mark.gpu
 @pytest.mark.parametrize("d,fp8", [(64, False), (128, False), (256, False), (128, True)])
-@pytest.mark.parametrize("lens", [[20011], [1], [9000, 3, 1, 12001, 640], [77] * 300])
+@pytest.mark.parametrize("lens", [[20011], [1], [9000, 3, 1, 12001, 640], [77] * 300, [5, 0, 130] * 150])
 def test_long_requests_are_split_and_joined(lens, d, fp8):
     _gpu()
     _run(lens, 1, 4, 2, d, 128, fp8=fp8, seed=d)
@@ -398,3 +398,63 @@ def test_rows_past_32_bit_offsets():
     dense = torch.arange(5, dtype=torch.int32)[None]
     pad = torch.zeros(20, hk, d).double()
     _check(got, _exact(q, torch.cat([kk.double(), pad]), torch.cat([vv.double(), pad]), [n], dense, block, 0, d ** -0.5))
+
+
+@pytest.mark.gpu
+def test_a_window_over_everything_is_none_and_no_lse():
+    _gpu()
+    lens, h, hk, d, block = [3000, 40], 4, 2, 128, 64
+    pool, _, _ = _pool(lens, hk, d, block, 8)
+    q = torch.randn(2, 1, h, d, generator=torch.Generator().manual_seed(1)).bfloat16().to(DEV)
+    n = torch.tensor(lens, dtype=torch.int32, device=DEV)
+    args = (q, pool["k"], pool["v"], n)
+    kw = dict(table=pool["table"], block=block)
+    base = csa.PagedAttention(*args, **kw)()["out"].clone()
+    for win in (3008, 5000, (1 << 31) - 1):
+        got = csa.PagedAttention(*args, win=win, lse=False, **kw)()
+        assert list(got) == ["out"] and torch.equal(got["out"], base)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("fp8", [False, True])
+def test_many_tokens_of_one_request(fp8):
+    # a prompt's chunk: more query rows than one unit holds
+    _gpu()
+    _run([70, 64, 200], 64, 4, 2, 128, 16, fp8=fp8, seed=4)
+
+
+@pytest.mark.gpu
+def test_e4m3_scales_far_apart_zero_and_negative():
+    # the weights take the V rows' scales in: rows with scales from 1e-12 to 1e12, zero and negative ones
+    _gpu()
+    lens, h, hk, d, block = [700], 6, 2, 128, 64
+    pool, _, _ = _pool(lens, hk, d, block, 9, True)
+    rows = pool["v_scale"].shape[0]
+    g = torch.Generator().manual_seed(3)
+    f = 10.0 ** torch.randint(-12, 13, (rows, 1), generator=g).float()
+    f[::5] = 0.0
+    f[1::5] *= -1
+    pool["v_scale"] = (pool["v_scale"] * f.to(DEV)).contiguous()
+    q = (torch.randn(1, 1, h, d, generator=g) * 3).bfloat16()
+    got = csa.PagedAttention(q.to(DEV), pool["k"], pool["v"], torch.tensor(lens, dtype=torch.int32, device=DEV),
+                             table=pool["table"], block=block, k_scale=pool["k_scale"], v_scale=pool["v_scale"])()
+    torch.cuda.synchronize()
+    k, v = (pool[x].cpu().view(torch.float8_e4m3fn).double() * pool[x + "_scale"].cpu().double()[..., None] for x in "kv")
+    want = _exact(q, k, v, lens, pool["table"].cpu(), block, 0, d ** -0.5)
+    _check(got, want)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("scale", [1e-30, 1e30])
+def test_e4m3_queries_of_any_size(scale):
+    # a query row is scaled to f16's range by a power of two: rows far outside it, keys scaled back
+    _gpu()
+    lens, h, hk, d, block = [300, 20], 4, 2, 128, 64
+    pool, _, _ = _pool(lens, hk, d, block, 9, True)
+    pool["k_scale"] = (pool["k_scale"] / scale).contiguous()
+    q = (torch.randn(2, 1, h, d, generator=torch.Generator().manual_seed(5)) * scale).bfloat16()
+    got = csa.PagedAttention(q.to(DEV), pool["k"], pool["v"], torch.tensor(lens, dtype=torch.int32, device=DEV),
+                             table=pool["table"], block=block, k_scale=pool["k_scale"], v_scale=pool["v_scale"])()
+    torch.cuda.synchronize()
+    k, v = (pool[x].cpu().view(torch.float8_e4m3fn).double() * pool[x + "_scale"].cpu().double()[..., None] for x in "kv")
+    _check(got, _exact(q, k, v, lens, pool["table"].cpu(), block, 0, d ** -0.5))
