@@ -9,10 +9,11 @@
 // block's product back from TMEM and add it, times its scale, to fp32
 // registers, while the MMAs of the next block fill another buffer.
 //
-//   warp 0      copies: per block one TMA box of each operand into a ring, and
-//               the block's scales into another
-//   warp 1      TMEM allocation; one thread issues four K = 32 MMAs per block
-//   warps 2..   epilogue: thread = TMEM lane (row of P), its columns of Q
+//   warps 0, 2  copies: per block one TMA box of each operand into a ring, and
+//               the block's scales into another (kSwap: both by warp 0)
+//   warps 1, 3  TMEM allocation; one thread each issues four K = 32 MMAs per
+//               block, the blocks in turn (kSwap: warp 1 alone)
+//   the rest    epilogue: thread = TMEM lane (row of P), its columns of Q
 //
 // The operand in the TMEM lanes (P, 128 rows per tile) and the one in its
 // columns (Q, NT rows per tile) are a and b, or with `kSwap` b and a: for a
@@ -48,11 +49,13 @@ struct MmShape {
   // 64 sums per epilogue thread at most; with 256 columns sixteen warps, four
   // per scheduler, hide each other's TMEM reads
   static constexpr int kEpiWarps = kSwap ? 4 : NT == 256 ? 16 : 8;
-  static constexpr int kThreads = 64 + 32 * kEpiWarps;
+  static constexpr int kAux = kSwap ? 2 : 4;               // warps before the epilogue's
+  static constexpr int kIssuers = kSwap ? 1 : 2;
+  static constexpr int kThreads = 32 * (kAux + kEpiWarps);
   static constexpr int kCols = NT / (kEpiWarps / 4);       // columns per epilogue thread
   static constexpr int kChunk = kSwap || NT == 256 ? 16 : 32;  // columns per TMEM read
   static constexpr int kAccCols = NT < 32 ? 32 : NT;       // TMEM columns per buffer
-  static constexpr int kBufs = kSwap ? 4 : 2;
+  static constexpr int kBufs = kSwap || NT == 128 ? 4 : 2;
   static constexpr int kTmemCols = kAccCols * kBufs;
   static constexpr int kStageBytes = kMmPBytes + NT * kMmBlock;
   static constexpr int kCtasPerSm = kSwap ? 2 : 1;
@@ -332,9 +335,10 @@ __global__ void __launch_bounds__(MmShape<NT, kSwap>::kThreads, MmShape<NT, kSwa
   auto p_of = [&](int t) { return t % ptiles; };
   auto q_of = [&](int t) { return t / ptiles; };
 
-  if (warp == 0) {
-    // copies: lane 0 the codes (bulk), every lane the scales.  (Fetched by the
-    // epilogue's threads instead, each row's line by every warp, the scales
+  const bool codes_warp = warp == 0, scales_warp = warp == (kSwap ? 0 : 2);
+  if (codes_warp || scales_warp) {
+    // copies: the codes (lane 0, bulk) and the scales (every lane).  (Fetched by
+    // the epilogue's threads instead, each row's line by every warp, the scales
     // took longer than the sums.)  Block n's scales go to slot n % kSlots, last
     // read for block n - kStages - kBufs; done(n - kStages) says that its MMAs
     // were issued, for which that block's TMEM buffer, and so its scales, had
@@ -358,18 +362,20 @@ __global__ void __launch_bounds__(MmShape<NT, kSwap>::kThreads, MmShape<NT, kSwa
       for (int kb = kb0; kb < kb1; ++kb, ++n) {
         if (n >= Sh::kStages && !tc5::mbar_wait(smem_u32(&sm.done[st]), ph ^ 1u, abort)) goto loaded;
         const uint32_t bar = smem_u32(&sm.full[st]);
-        if (lane == 0) {
+        if (codes_warp && lane == 0) {
           const uint32_t dst = base + st * Sh::kStageBytes;
           tc5::mbar_expect_tx(bar, Sh::kStageBytes);
           tc5::tma_load_2d(dst, &pmap, kb * kMmBlock, p_of(t) * 128, bar);
           tc5::tma_load_2d(dst + kMmPBytes, &qmap, kb * kMmBlock, q_of(t) * NT, bar);
         }
         __syncwarp();
-        const uint32_t dst = scales + slot * Sh::kScaleFloats * 4;
+        if (scales_warp) {
+          const uint32_t dst = scales + slot * Sh::kScaleFloats * 4;
 #pragma unroll
-        for (int i = 0; i < kRows / 32; ++i) copy_f32(dst + (i * 32 + lane) * 4, src[i] + kb, have[i]);
-        if (lane < kParts) copy_f32(dst + (128 + lane) * 4, src_b + kb, have_b);
-        copies_arrive(bar);
+          for (int i = 0; i < kRows / 32; ++i) copy_f32(dst + (i * 32 + lane) * 4, src[i] + kb, have[i]);
+          if (lane < kParts) copy_f32(dst + (128 + lane) * 4, src_b + kb, have_b);
+          copies_arrive(bar);
+        }
         if (++st == Sh::kStages) st = 0, ph ^= 1u;
         if (++slot == Sh::kSlots) slot = 0;
       }
@@ -378,42 +384,46 @@ __global__ void __launch_bounds__(MmShape<NT, kSwap>::kThreads, MmShape<NT, kSwa
     // copies still in flight land before the block exits
     cp_async_commit();
     cp_async_wait<0>();
-    for (int k = n > Sh::kStages ? n - Sh::kStages : 0; k < n; ++k)
-      tc5::mbar_wait_drain(smem_u32(&sm.full[k % Sh::kStages]), (k / Sh::kStages) & 1);
-  } else if (warp == 1) {
-    if (lane == 0) {
-      int st = 0, buf = 0, n = 0;
-      uint32_t ph = 0, bph = 0;
-      const uint32_t idesc = tc5::idesc_e4m3_f32(128, NT);
-      uint32_t okf = 0, okt = 1;
-      for (int t = first; t < tiles && !*abort; t += step)
-        for (int kb = kb0; kb < kb1; ++kb, ++n) {
-          if (!okf && !tc5::mbar_wait(smem_u32(&sm.full[st]), ph, abort)) goto issued;
-          if (!okt && !tc5::mbar_wait(smem_u32(&sm.tempty[buf]), bph ^ 1u, abort)) goto issued;
-          tc5::fence_after_sync();
-          const uint64_t pd = tc5::sdesc_k_sw128(base + st * Sh::kStageBytes);
-          const uint64_t qd = tc5::sdesc_k_sw128(base + st * Sh::kStageBytes + kMmPBytes);
-          const uint32_t d = tmem + buf * Sh::kAccCols, now = smem_u32(&sm.done[st]);
-          if (++st == Sh::kStages) st = 0, ph ^= 1u;
-          if (++buf == Sh::kBufs) buf = 0, bph ^= 1u;
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            tc5::mma_e4m3(d, pd + 2 * i, qd + 2 * i, idesc, i > 0);
-            if (i == 1) {  // asked here, the next block's barriers answer while the MMAs are issued
-              okf = bar_ask(smem_u32(&sm.full[st]), ph);
-              okt = n + 1 < Sh::kBufs ? 1u : bar_ask(smem_u32(&sm.tempty[buf]), bph ^ 1u);
-            }
-          }
-          tc5::mma_commit(now);  // frees the stage and hands the product to the epilogue
-        }
-    issued:
-      // MMAs still in flight finish before TMEM is freed
+    if (codes_warp)
       for (int k = n > Sh::kStages ? n - Sh::kStages : 0; k < n; ++k)
-        tc5::mbar_wait_drain(smem_u32(&sm.done[k % Sh::kStages]), (k / Sh::kStages) & 1);
+        tc5::mbar_wait_drain(smem_u32(&sm.full[k % Sh::kStages]), (k / Sh::kStages) & 1);
+  } else if (warp < Sh::kAux) {
+    // MMA issuers, the blocks in turn: a block's chain in its thread (two
+    // barriers, four MMAs, a commit: 700 cycles measured) is longer than its
+    // MMAs (280 with 128 columns).  One issuer / two: 1024 x 4096 x 4096 26.9 /
+    // 23.9 us, 331 x 1100 x 7000 11.5 / 10.5.
+    if (lane == 0) {
+      constexpr int kBy = Sh::kIssuers;
+      const int which = warp == 1 ? 0 : 1, blocks = first < tiles ? ((tiles - 1 - first) / step + 1) * (kb1 - kb0) : 0;
+      const uint32_t idesc = tc5::idesc_e4m3_f32(128, NT);
+      int st = which, buf = which, n = which, last = -1;
+      uint32_t ph = 0, bph = 0, okf = 0, okt = 1;
+      for (; n < blocks && !*abort; n += kBy) {
+        if (!okf && !tc5::mbar_wait(smem_u32(&sm.full[st]), ph, abort)) break;
+        if (!okt && !tc5::mbar_wait(smem_u32(&sm.tempty[buf]), bph ^ 1u, abort)) break;
+        tc5::fence_after_sync();
+        const uint64_t pd = tc5::sdesc_k_sw128(base + st * Sh::kStageBytes);
+        const uint64_t qd = tc5::sdesc_k_sw128(base + st * Sh::kStageBytes + kMmPBytes);
+        const uint32_t d = tmem + buf * Sh::kAccCols, now = smem_u32(&sm.done[st]);
+        if ((st += kBy) >= Sh::kStages) st -= Sh::kStages, ph ^= 1u;
+        if ((buf += kBy) >= Sh::kBufs) buf -= Sh::kBufs, bph ^= 1u;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          tc5::mma_e4m3(d, pd + 2 * i, qd + 2 * i, idesc, i > 0);
+          if (i == 1) {  // asked here, the next block's barriers answer while the MMAs are issued
+            okf = bar_ask(smem_u32(&sm.full[st]), ph);
+            okt = n + kBy < Sh::kBufs ? 1u : bar_ask(smem_u32(&sm.tempty[buf]), bph ^ 1u);
+          }
+        }
+        tc5::mma_commit(now);  // frees the stage and hands the product to the epilogue
+        last = n;
+      }
+      // MMAs still in flight finish before TMEM is freed (this thread's complete in order)
+      if (last >= 0) tc5::mbar_wait_drain(smem_u32(&sm.done[last % Sh::kStages]), (last / Sh::kStages) & 1);
     }
   } else {
     // a warp reads the TMEM lanes of its number mod 4
-    const int ew = warp - 2, quarter = warp & 3, group = ew >> 2;
+    const int ew = warp - Sh::kAux, quarter = warp & 3, group = ew >> 2;
     const int row = quarter * 32 + lane;                 // TMEM lane: row of the P tile
     const uint32_t tcol = tmem + ((uint32_t)(quarter * 32) << 16) + group * Sh::kCols;
     int buf = 0, st = 0, slot = 0;
