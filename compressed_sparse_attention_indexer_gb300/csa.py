@@ -360,7 +360,8 @@ class NormRows(_Operator):
     object by default, `residual` itself for in place), weight [width] or None (ones).  norm=False:
     the rows as they are.  out / codes: which outputs to make, or the tensors to fill (codes uint8 or
     float8_e4m3fn [n, width], scale fp32 [n, ceil(width / 128)]).  Calling the object returns
-    {"residual", "out", "codes", "scale"} as far as they are made."""
+    {"residual", "out", "codes", "scale"} as far as they are made.  Where nothing is asked of the rows
+    (no norm, residual or codes, and no tensor to fill) out is x itself."""
 
     def __init__(self, x, weight=None, residual=None, norm: bool = True, eps: float = 1e-6, out=False,
                  codes=True, scale=None, residual_out=None):
@@ -380,8 +381,11 @@ class NormRows(_Operator):
         if weight is not None and (tuple(weight.shape) != (width,) or weight.dtype != x.dtype or
                                    not weight.is_contiguous()):
             _bad(f"weight must be contiguous {x.dtype} of shape ({width},)")
+        if weight is not None and not norm:
+            _bad("weight given with norm=False")
+        self._same = not norm and residual is None and codes is False and out is True
         if out is True:
-            out = _empty_rows(x, n, width, x.dtype)
+            out = x if self._same else _empty_rows(x, n, width, x.dtype)
         if codes is True:
             codes = _empty_rows(x, n, width, torch.uint8)
         out, codes = (None if t is False else t for t in (out, codes))
@@ -414,7 +418,8 @@ class NormRows(_Operator):
             self._out["codes"], self._out["scale"] = codes.view(torch.float8_e4m3fn), scale
 
     def __call__(self, stream=None) -> dict:
-        self._launch(stream)
+        if not self._same:
+            self._launch(stream)
         return self._out
 
 

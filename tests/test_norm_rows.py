@@ -122,6 +122,9 @@ def test_object_refusals(L):
         with pytest.raises(csa.CsaError):
             csa.NormRows(x, **kw)
     with pytest.raises(csa.CsaError):
+        csa.NormRows(x, weight=torch.ones(256, dtype=torch.bfloat16), norm=False)
+    assert csa.NormRows(x, norm=False, out=True, codes=False)()["out"] is x      # nothing is asked of the rows
+    with pytest.raises(csa.CsaError):
         csa.NormRows(x.half())
     with pytest.raises(csa.CsaError):
         csa.NormRows(torch.zeros(256, 4, dtype=torch.bfloat16).t())     # a row's elements apart
@@ -329,3 +332,14 @@ def test_codes_of_rows_as_they_are_are_the_nearest(dtype):
     half = torch.ldexp(torch.ones_like(z), (e - 1).clamp_min(-6) - 4)
     assert (((z - want).abs() - half).abs()[off] <= 2.0 ** -22 * z.abs()[off]).all()
     assert off.double().mean() < 1e-5
+
+
+@pytest.mark.gpu
+def test_rows_copied_as_they_are():
+    # nothing but a tensor to fill: a copy
+    _gpu()
+    x = torch.randn(50, 200, device=DEV)
+    out = torch.zeros(50, 208, device=DEV)
+    csa.NormRows(x, norm=False, out=out[:, :200], codes=False)()
+    torch.cuda.synchronize()
+    assert torch.equal(out[:, :200], x) and (out[:, 200:] == 0).all()
