@@ -16,13 +16,14 @@
 // reduced by shuffles alone, a longer one by one barrier.  Every reduction
 // has a fixed order.
 //
-// Measured (GB300): 16384 x 7168 bf16, residual, both outputs, in 167 us
-// (6.4 TB/s, 94% of the measured copy rate); 131072 x 128 to codes in 12.2 us
-// (4.2 TB/s: bound by instructions per row); 4097 x 1000 fp32 to codes in
-// 6.2 us; one row of 4096 in 3.0 us (a launch).
+// Measured (GB300): 16384 x 7168 bf16, residual, both outputs, in 166 us
+// (6.4 TB/s, 94% of the measured copy rate); 131072 x 128 to codes in 11.4 us
+// (4.5 TB/s: bound by instructions per row); 4097 x 1000 fp32 to codes in
+// 6.3 us; one row of 4096 in 3.0 us (a launch).
 #include <cuda_fp8.h>
 
 #include "csa_internal.cuh"
+#include "ptx.cuh"
 
 namespace csa {
 
@@ -32,6 +33,7 @@ constexpr float kE4m3Max = 448.f;
 constexpr int kNormMaxThreads = 512;
 constexpr int kNormMaxVec = 8;      // 16-byte vectors per thread at most
 constexpr int kNormBlock = 128;     // elements that share a scale
+constexpr int kNormDepth = 2;       // rows of the shared-memory ring
 
 template <typename T>
 struct VecOf;
@@ -123,9 +125,13 @@ __device__ __forceinline__ float rcp_approx(float x) {
   return y;
 }
 
-// The scale of a block whose largest magnitude is m.
+// The scale of a block whose largest magnitude is m.  The quotient is the
+// rounded one: the product with 1 / 448, corrected by its residual (an infinite
+// m stays).
 __device__ __forceinline__ float block_scale(float m) {
-  return m > 0.f ? fmaxf(m / kE4m3Max, 1.17549435e-38f) : 1.f;
+  constexpr float kInv = 1.f / kE4m3Max;
+  const float q = m * kInv;
+  return m > 0.f ? fmaxf(m < INFINITY ? fmaf(fmaf(-q, kE4m3Max, m), kInv, q) : m, 1.17549435e-38f) : 1.f;
 }
 // f / scale to within a rounding that almost never differs from the exact
 // one's: the product with the reciprocal, corrected by its residual (one step
@@ -143,20 +149,44 @@ __device__ __forceinline__ void divide(float* f, float scale) {
   }
 }
 
+__device__ __forceinline__ uint4 lds128(uint32_t a) {
+  uint4 r;
+  asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];\n" : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w) : "r"(a) : "memory");
+  return r;
+}
+__device__ __forceinline__ uint64_t pack2(float lo, float hi) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};\n" : "=l"(r) : "f"(lo), "f"(hi));
+  return r;
+}
+__device__ __forceinline__ void mul2(float* d, float b0, float b1) {
+  uint64_t x = pack2(d[0], d[1]);
+  const uint64_t y = pack2(b0, b1);
+  asm("mul.rn.f32x2 %0, %0, %1;\n" : "+l"(x) : "l"(y));
+  asm("mov.b64 {%0, %1}, %2;\n" : "=f"(d[0]), "=f"(d[1]) : "l"(x));
+}
+
 // tpr threads per row (a warp, or the whole block); blockDim.x / tpr rows per
-// block and step, rows in a grid-stride loop.  The next row's
-// vectors are loaded before the current row is reduced.
-// Narrow rows are bound by instructions before bytes (131072 rows of 128: 239
-// per warp and step took 17.2 us), so: the weight multiplies s before the norm
-// is known and the norm's factor r > 0 goes into the scale
-// (max|y| = r max|s weight|, code = s weight * (r / scale)), and row pointers
-// advance by additions.
-template <typename T, int VPT, bool kTail>
+// block and step, rows in a grid-stride loop.  A row's vectors are fetched
+// while the rows before it are worked on: into registers, or (kRing) by
+// cp.async into a ring of two rows in shared memory (four were no faster), where
+// a thread reads back only what it copied itself (no barrier) and a short last vector is
+// zero-filled by the copy.  The ring leaves registers to more vectors per
+// thread and a tail costs nothing to load; register loads carry a
+// streaming hint and do better where reads and writes are about equally
+// many (see launch_t for both sides).
+// Instructions bound it before bytes, so: the weight multiplies s before the
+// norm is known and the norm's factor r > 0 goes into the scale
+// (max|y| = r max|s weight|, code = s weight * (r / scale)), so that the
+// blocks' maxima are found while the row's sum crosses the barrier.
+template <typename T, int VPT, bool kTail, bool kRing>
 __global__ void __launch_bounds__(kNormMaxThreads, VPT == 1 ? 2 : 1) norm_kernel(const NormArgs a, int tpr) {
   constexpr int E = VecOf<T>::E;
-  // the next row in flight and the weight held, where registers allow it
+  // the next rows in flight and the weight held, where registers allow it
   constexpr bool kAhead = VPT <= 4;
+  static_assert(kAhead || !kRing, "the ring is for rows of up to four vectors per thread");
   constexpr int kLanes = kNormBlock / E;  // lanes that share a scale
+  extern __shared__ uint4 ring[];         // [slot][x, residual][vector][thread]
   __shared__ float part[2][32];
   const int t = threadIdx.x % tpr;
   const int rpb = blockDim.x / tpr;
@@ -165,51 +195,68 @@ __global__ void __launch_bounds__(kNormMaxThreads, VPT == 1 ? 2 : 1) norm_kernel
   const float inv_width = 1.f / (float)W;
   const int64_t step = (int64_t)gridDim.x * rpb;
   int64_t row = (int64_t)blockIdx.x * rpb + threadIdx.x / tpr;
-  const T* xp = static_cast<const T*>(a.x) + row * a.x_stride;
-  const T* rp = static_cast<const T*>(a.residual) + (a.residual ? row * a.residual_stride : 0);
-  T* sp = static_cast<T*>(a.residual_out) + (a.residual ? row * a.residual_out_stride : 0);
-  T* op = static_cast<T*>(a.out) + (a.out ? row * a.out_stride : 0);
-  uint8_t* cp = a.codes + (a.codes ? row * a.codes_stride : 0);
-  float* fp = a.scale + (a.codes ? row * a.scale_stride : 0);
+  const uint32_t vec_bytes = blockDim.x * 16, slot_bytes = (a.residual ? 2 : 1) * VPT * vec_bytes;
+  const uint32_t mine = smem_u32(ring) + threadIdx.x * 16;
+  uint32_t put = 0, get = 0;
+  uint4 xr[kRing ? 1 : VPT], rr[kRing ? 1 : VPT], wr[kAhead ? VPT : 1];
+  int64_t ahead = row;
   pdl_wait();
   pdl_trigger();
-  uint4 xr[VPT], rr[VPT], wr[VPT];
-  auto fetch = [&](bool have) {
-    if (!have) return;
+  auto fetch = [&]() {
+    if (ahead < a.n) {
+      const T* xp = static_cast<const T*>(a.x) + ahead * a.x_stride;
+      const T* rp = a.residual ? static_cast<const T*>(a.residual) + ahead * a.residual_stride : nullptr;
 #pragma unroll
-    for (int i = 0; i < VPT; ++i) {
-      const int v = i * tpr + t;
-      if (v < vecs) {
-        xr[i] = load_vec<kTail>(xp, v, W);
-        if (a.residual) rr[i] = load_vec<kTail>(rp, v, W);
+      for (int i = 0; i < VPT; ++i) {
+        const int v = i * tpr + t;
+        if (v >= vecs) continue;
+        if constexpr (kRing) {
+          const int bytes = kTail && (v + 1) * E > W ? (W - v * E) * (int)sizeof(T) : 16;
+          const uint32_t at = mine + put + i * vec_bytes;
+          cp_async16(at, xp + v * E, bytes);
+          if (a.residual) cp_async16(at + VPT * vec_bytes, rp + v * E, bytes);
+        } else {
+          xr[i] = load_vec<kTail>(xp, v, W);
+          if (a.residual) rr[i] = load_vec<kTail>(rp, v, W);
+        }
       }
     }
-    xp += step * a.x_stride;
-    if (a.residual) rp += step * a.residual_stride;
+    if constexpr (kRing) {
+      cp_async_commit();
+      put = put + slot_bytes == kNormDepth * slot_bytes ? 0 : put + slot_bytes;
+    }
+    ahead += step;
   };
-  if (kAhead) fetch(row < a.n);
+  if constexpr (kRing) {
+#pragma unroll
+    for (int i = 0; i < kNormDepth - 1; ++i) fetch();
+  } else if (kAhead) {
+    fetch();
+  }
   if (kAhead && a.weight) {
 #pragma unroll
     for (int i = 0; i < VPT; ++i) {
       const int v = i * tpr + t;
-      if (v < vecs) wr[i] = load_vec<kTail>(static_cast<const T*>(a.weight), v, W);
+      if (v < vecs) wr[kAhead ? i : 0] = load_vec<kTail>(static_cast<const T*>(a.weight), v, W);
     }
   }
   int buf = 0;
   // every thread of the block runs the same number of steps (barrier inside)
   for (int64_t first = (int64_t)blockIdx.x * rpb; first < a.n; first += step, row += step) {
     const bool live = row < a.n;
-    if (!kAhead) fetch(live);
+    if (kRing || !kAhead) fetch();
+    if constexpr (kRing) cp_async_wait<kNormDepth - 1>();
     float y[VPT][E];
     float sum = 0.f;
 #pragma unroll
     for (int i = 0; i < VPT; ++i) {
       const int v = i * tpr + t;
       if (live && v < vecs) {
-        VecOf<T>::unpack(xr[i], y[i]);
+        const uint32_t at = mine + get + i * vec_bytes;
+        VecOf<T>::unpack(kRing ? lds128(at) : xr[kRing ? 0 : i], y[i]);
         if (a.residual) {
           float r[E];
-          VecOf<T>::unpack(rr[i], r);
+          VecOf<T>::unpack(kRing ? lds128(at + VPT * vec_bytes) : rr[kRing ? 0 : i], r);
 #pragma unroll
           for (int e = 0; e < E; ++e) y[i][e] += r[e];
         }
@@ -220,21 +267,49 @@ __global__ void __launch_bounds__(kNormMaxThreads, VPT == 1 ? 2 : 1) norm_kernel
 #pragma unroll
       for (int e = 0; e < E; ++e) sum = fmaf(y[i][e], y[i][e], sum);
     }
-    if (kAhead) fetch(row + step < a.n);
+    if constexpr (kRing) get = get + slot_bytes == kNormDepth * slot_bytes ? 0 : get + slot_bytes;
+    else if (kAhead) fetch();
     if (a.residual) {
+      T* sp = static_cast<T*>(a.residual_out) + row * a.residual_out_stride;
 #pragma unroll
       for (int i = 0; i < VPT; ++i) {
         const int v = i * tpr + t;
         if (live && v < vecs) store_vec<kTail>(sp, v, W, y[i]);
       }
-      sp += step * a.residual_out_stride;
     }
-    float r = 1.f;
     if (a.norm) {
 #pragma unroll
       for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+      if (tpr > 32 && lane == 0) part[buf][warp] = sum;
+      if (a.weight) {
+#pragma unroll
+        for (int i = 0; i < VPT; ++i) {
+          const int v = i * tpr + t;
+          if (v < vecs) {
+            float w[E];
+            VecOf<T>::unpack(kAhead ? wr[kAhead ? i : 0] : load_vec<kTail>(static_cast<const T*>(a.weight), v, W), w);
+#pragma unroll
+            for (int e = 0; e < E; e += 2) mul2(y[i] + e, w[e], w[e + 1]);
+          }
+        }
+      }
+    }
+    float top[VPT];  // NaN elements leave the maximum alone and become NaN codes
+    if (a.codes) {
+#pragma unroll
+      for (int i = 0; i < VPT; ++i) {
+        top[i] = 0.f;
+#pragma unroll
+        for (int e = 0; e < E; ++e) top[i] = fmaxf(top[i], fabsf(y[i][e]));
+      }
+#pragma unroll
+      for (int o = kLanes >> 1; o > 0; o >>= 1)
+#pragma unroll
+        for (int i = 0; i < VPT; ++i) top[i] = fmaxf(top[i], __shfl_xor_sync(0xffffffffu, top[i], o));
+    }
+    float r = 1.f;
+    if (a.norm) {
       if (tpr > 32) {
-        if (lane == 0) part[buf][warp] = sum;
         __syncthreads();
         sum = lane < (int)(blockDim.x >> 5) ? part[buf][lane] : 0.f;
 #pragma unroll
@@ -242,30 +317,14 @@ __global__ void __launch_bounds__(kNormMaxThreads, VPT == 1 ? 2 : 1) norm_kernel
         buf ^= 1;  // the next step's sums go elsewhere: one barrier per row is enough
       }
       r = rsqrtf(sum * inv_width + a.eps);
-      if (a.weight) {
-#pragma unroll
-        for (int i = 0; i < VPT; ++i) {
-          const int v = i * tpr + t;
-          if (v < vecs) {
-            float w[E];
-            VecOf<T>::unpack(kAhead ? wr[i] : load_vec<kTail>(static_cast<const T*>(a.weight), v, W), w);
-#pragma unroll
-            for (int e = 0; e < E; ++e) y[i][e] *= w[e];
-          }
-        }
-      }
     }
     if (a.codes) {
+      uint8_t* cp = a.codes + row * a.codes_stride;
+      float* fp = a.scale + row * a.scale_stride;
 #pragma unroll
       for (int i = 0; i < VPT; ++i) {
         const int v = i * tpr + t;
-        float m = 0.f;  // NaN elements leave the maximum alone and become NaN codes
-#pragma unroll
-        for (int e = 0; e < E; ++e) m = fmaxf(m, fabsf(y[i][e]));
-#pragma unroll
-        for (int o = kLanes >> 1; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-        m *= r;
-        const float scale = block_scale(m);
+        const float scale = block_scale(top[i] * r);
         if (live && v < vecs) {
           float z[E];
 #pragma unroll
@@ -273,7 +332,7 @@ __global__ void __launch_bounds__(kNormMaxThreads, VPT == 1 ? 2 : 1) norm_kernel
           if (a.norm) {
             const float mul = r * rcp_approx(scale);
 #pragma unroll
-            for (int e = 0; e < E; ++e) z[e] *= mul;
+            for (int e = 0; e < E; e += 2) mul2(z + e, mul, mul);
           } else {
             divide<E>(z, scale);
           }
@@ -281,20 +340,18 @@ __global__ void __launch_bounds__(kNormMaxThreads, VPT == 1 ? 2 : 1) norm_kernel
           if (t % kLanes == 0) fp[v / kLanes] = scale;
         }
       }
-      cp += step * a.codes_stride;
-      fp += step * a.scale_stride;
     }
     if (a.out) {
+      T* op = static_cast<T*>(a.out) + row * a.out_stride;
 #pragma unroll
       for (int i = 0; i < VPT; ++i) {
         const int v = i * tpr + t;
         if (live && v < vecs) {
 #pragma unroll
-          for (int e = 0; e < E; ++e) y[i][e] *= r;
+          for (int e = 0; e < E; e += 2) mul2(y[i] + e, r, r);
           store_vec<kTail>(op, v, W, y[i]);
         }
       }
-      op += step * a.out_stride;
     }
   }
 }
@@ -307,18 +364,6 @@ __global__ void __launch_bounds__(kNormMaxThreads, VPT == 1 ? 2 : 1) norm_kernel
 // two rows 13.0, one row 14.8).  Two elements per
 // multiply (f32x2); both reductions run together.
 constexpr int kNarrowRows = 4, kNarrowThreads = 256, kNarrowBlocks = 2;
-
-__device__ __forceinline__ uint64_t pack2(float lo, float hi) {
-  uint64_t r;
-  asm("mov.b64 %0, {%1, %2};\n" : "=l"(r) : "f"(lo), "f"(hi));
-  return r;
-}
-__device__ __forceinline__ void mul2(float* d, float b0, float b1) {
-  uint64_t x = pack2(d[0], d[1]);
-  const uint64_t y = pack2(b0, b1);
-  asm("mul.rn.f32x2 %0, %0, %1;\n" : "+l"(x) : "l"(y));
-  asm("mov.b64 {%0, %1}, %2;\n" : "=f"(d[0]), "=f"(d[1]) : "l"(x));
-}
 
 template <typename T, bool kTail, bool kRes, bool kNorm>
 __global__ void __launch_bounds__(kNarrowThreads, kNarrowBlocks) norm_narrow_kernel(const NormArgs a) {
@@ -433,60 +478,94 @@ int launch_narrow(const NormArgs& a, int num_sms, cudaStream_t st, bool pdl) {
 
 // The grid is what fits the device at once (or the rows, when fewer): each
 // block then walks its rows with the next one in flight.
-template <typename T, int VPT, bool kTail>
+template <typename T, int VPT, bool kTail, bool kRing>
 int launch_kind(const NormArgs& a, int tpr, int threads, int num_sms, cudaStream_t st, bool pdl) {
-  static std::atomic<int> per_sm[kNormMaxThreads / 32 + 1];  // resident blocks by block size (0: not asked yet)
-  int r = per_sm[threads / 32].load(std::memory_order_relaxed);
+  auto kern = norm_kernel<T, VPT, kTail, kRing>;
+  const int depth = kRing ? kNormDepth : 0, res = a.residual ? 1 : 0;
+  const size_t slot = (size_t)VPT * threads * 16 * (1 + res);
+  if constexpr (kRing) {
+    static PerDeviceOnce attr;
+    if (const cudaError_t e = attr.run([&] { return allow_max_dynamic_smem(kern); }))
+      return launch_fail("cudaFuncSetAttribute(norm_kernel)", e);
+  }
+  static std::atomic<int> per_sm[2][kNormMaxThreads / 32 + 1];  // resident blocks by block size (0: not asked yet)
+  int r = per_sm[res][threads / 32].load(std::memory_order_relaxed);
   if (r == 0) {
-    const cudaError_t e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&r, norm_kernel<T, VPT, kTail>, threads, 0);
+    const cudaError_t e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&r, kern, threads, slot * depth);
     if (e != cudaSuccess) return launch_fail("cudaOccupancyMaxActiveBlocksPerMultiprocessor", e);
     if (r < 1) r = 1;
-    per_sm[threads / 32].store(r, std::memory_order_relaxed);
+    per_sm[res][threads / 32].store(r, std::memory_order_relaxed);
   }
   const int64_t rpb = threads / tpr;
   int64_t blocks = (a.n + rpb - 1) / rpb;
   if (blocks > (int64_t)num_sms * r) blocks = (int64_t)num_sms * r;
-  return launch_kernel(norm_kernel<T, VPT, kTail>, dim3((unsigned)blocks), dim3(threads), 0, st, pdl, a, tpr);
+  // no more slots than a block takes steps
+  const int64_t steps = (a.n + blocks * rpb - 1) / (blocks * rpb);
+  return launch_kernel(kern, dim3((unsigned)blocks), dim3(threads), slot * (size_t)(steps < depth ? steps : depth), st,
+                       pdl, a, tpr);
 }
 
 template <typename T, int VPT>
-int launch_vpt(const NormArgs& a, int tpr, int threads, int num_sms, cudaStream_t st, bool pdl) {
-  return a.width % VecOf<T>::E == 0 ? launch_kind<T, VPT, false>(a, tpr, threads, num_sms, st, pdl)
-                                    : launch_kind<T, VPT, true>(a, tpr, threads, num_sms, st, pdl);
+int launch_vpt(const NormArgs& a, bool ring, int tpr, int threads, int num_sms, cudaStream_t st, bool pdl) {
+  const bool tail = a.width % VecOf<T>::E != 0;
+  if constexpr (VPT <= 4) {
+    if (tail) return launch_kind<T, VPT, true, true>(a, tpr, threads, num_sms, st, pdl);
+    if constexpr (sizeof(T) == 2) {
+      if (!ring) return launch_kind<T, VPT, false, false>(a, tpr, threads, num_sms, st, pdl);
+    }
+    return launch_kind<T, VPT, false, true>(a, tpr, threads, num_sms, st, pdl);
+  } else {
+    return tail ? launch_kind<T, VPT, true, false>(a, tpr, threads, num_sms, st, pdl)
+                : launch_kind<T, VPT, false, false>(a, tpr, threads, num_sms, st, pdl);
+  }
 }
 
 template <typename T>
 int launch_t(const NormArgs& a, int num_sms, cudaStream_t st, bool pdl) {
   constexpr int E = VecOf<T>::E;
   const int vecs = (a.width + E - 1) / E;
-  int tpr, vpt, threads;
   if (a.width <= kNormBlock)
     return a.width % E == 0 ? launch_narrow<T, false>(a, num_sms, st, pdl) : launch_narrow<T, true>(a, num_sms, st, pdl);
-  if (vecs <= 32) {  // a row per warp
-    tpr = 32;
-    vpt = 1;
-    threads = 256;
-  } else {
-    // one vector per thread where the block's size allows it (4097 x 1000 fp32:
-    // 5.7 us with one, 11.2 with four; bf16 rows of 1000 .. 4096: within 5%
-    // either way); wider rows take four, so that several rows share an SM
-    // (7168: 152 us with four, 176 with two at 19456 rows, 12.9 and 13.4 at
-    // 1216), or, with fewer rows than SMs, as few as fit
-    int per = vecs <= kNormMaxThreads ? 1 : a.n >= num_sms ? 4 : 2;
-    while (((vecs + per - 1) / per + 31) / 32 * 32 > kNormMaxThreads) ++per;
-    tpr = ((vecs + per - 1) / per + 31) / 32 * 32;
-    vpt = (vecs + tpr - 1) / tpr;
-    threads = tpr;
+  // The ring, except for bf16 rows with a residual (1024 .. 4096 wide, both
+  // outputs: 59 us from registers at 82 MB per tensor, 65 .. 67 from the ring;
+  // without a residual codes take 31 us and not 38, out 28 and not 34; fp32
+  // 1000 x 24615 with a residual to codes 55 and not 64; a tail from registers
+  // 1.6 to 2.2 times as long).
+  const bool ring = a.width % E != 0 || !a.residual || E == 4;
+  auto threads_for = [&](int per) { return ((vecs + per - 1) / per + 31) / 32 * 32; };
+  // Vectors per thread.  Ring: two to four, the count that leaves the fewest
+  // threads idle (bf16 rows of 768: three 8.1 us, two 9.8 at 12000 rows); of
+  // equals two (1497 fp32: 10.8 us with two, 12.0 with four at 4097 rows) but
+  // four from 384 vectors on (bf16 4096: 37.5 and 41.5 us at 12000 rows).  One
+  // row per SM or fewer: one, for the latency.
+  // Registers: one where the block's size allows it, else four, so that several
+  // rows share an SM (7168: 152 us with four, 176 with two at 19456 rows), or,
+  // with fewer rows than SMs, as few as fit.
+  int per = 1;
+  if (vecs > 32) {
+    if (ring && a.n >= num_sms && vecs <= 4 * kNormMaxThreads) {
+      per = 2;
+      for (int p = 3; p <= 4; ++p) {
+        const int more = p * threads_for(p) - per * threads_for(per);
+        if (more < 0 || (more == 0 && vecs > 384) || threads_for(per) > kNormMaxThreads) per = p;
+      }
+    } else {
+      per = vecs <= kNormMaxThreads ? 1 : a.n >= num_sms ? 4 : 2;
+    }
+    while (threads_for(per) > kNormMaxThreads) ++per;
   }
+  // a row per warp: several warps to a block (33 vectors, 4097 rows: 2.9 us with
+  // four rows per block, 5.0 with one)
+  const int tpr = threads_for(per), threads = vecs <= 32 ? 256 : tpr == 32 ? 128 : tpr, vpt = (vecs + tpr - 1) / tpr;
   switch (vpt) {
-    case 1: return launch_vpt<T, 1>(a, tpr, threads, num_sms, st, pdl);
-    case 2: return launch_vpt<T, 2>(a, tpr, threads, num_sms, st, pdl);
-    case 3: return launch_vpt<T, 3>(a, tpr, threads, num_sms, st, pdl);
-    case 4: return launch_vpt<T, 4>(a, tpr, threads, num_sms, st, pdl);
-    case 5: return launch_vpt<T, 5>(a, tpr, threads, num_sms, st, pdl);
-    case 6: return launch_vpt<T, 6>(a, tpr, threads, num_sms, st, pdl);
-    case 7: return launch_vpt<T, 7>(a, tpr, threads, num_sms, st, pdl);
-    default: return launch_vpt<T, 8>(a, tpr, threads, num_sms, st, pdl);
+    case 1: return launch_vpt<T, 1>(a, ring, tpr, threads, num_sms, st, pdl);
+    case 2: return launch_vpt<T, 2>(a, ring, tpr, threads, num_sms, st, pdl);
+    case 3: return launch_vpt<T, 3>(a, ring, tpr, threads, num_sms, st, pdl);
+    case 4: return launch_vpt<T, 4>(a, ring, tpr, threads, num_sms, st, pdl);
+    case 5: return launch_vpt<T, 5>(a, ring, tpr, threads, num_sms, st, pdl);
+    case 6: return launch_vpt<T, 6>(a, ring, tpr, threads, num_sms, st, pdl);
+    case 7: return launch_vpt<T, 7>(a, ring, tpr, threads, num_sms, st, pdl);
+    default: return launch_vpt<T, 8>(a, ring, tpr, threads, num_sms, st, pdl);
   }
 }
 

@@ -343,3 +343,23 @@ def test_rows_copied_as_they_are():
     csa.NormRows(x, norm=False, out=out[:, :200], codes=False)()
     torch.cuda.synchronize()
     assert torch.equal(out[:, :200], x) and (out[:, 200:] == 0).all()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("width", [130, 257, 300, 761, 768, 1497, 2048, 4092, 6001])
+@pytest.mark.parametrize("residual", [False, True])
+def test_many_rows_per_block(width, dtype, residual):
+    # more rows than the device holds at once: the rows in flight wrap around; in place, rows' padding left alone
+    _gpu()
+    n = 9001 if width < 1000 else 3001
+    g = torch.Generator().manual_seed(width)
+    stride = -(-width // 16) * 16 + 16
+    x, res = (torch.randn(n, stride, generator=g).to(dtype) for _ in range(2))
+    weight = (1 + 0.1 * torch.randn(width, generator=g)).to(dtype)
+    xd, rd = x.to(DEV), res.to(DEV)
+    kw = dict(residual=rd[:, :width], residual_out=rd[:, :width]) if residual else {}
+    got = csa.NormRows(xd[:, :width], weight=weight.to(DEV), out=xd[:, :width], codes=True, **kw)()
+    torch.cuda.synchronize()
+    check(got, x[:, :width], res[:, :width] if residual else None, weight, True, 1e-6, f"{width} {dtype}")
+    assert torch.equal(xd[:, width:].cpu(), x[:, width:]) and torch.equal(rd[:, width:].cpu(), res[:, width:])
