@@ -324,10 +324,10 @@ def _row_stride(t, unit: int = 1) -> int:
     return int(t.stride(0)) if t.shape[0] > 1 else -(-int(t.shape[1]) // unit) * unit
 
 
-def _empty_rows(like, n: int, width: int, dtype):
-    """[n, width] whose rows start on 16-byte boundaries."""
+def _empty_rows(like, n: int, width: int, dtype, align: int = 16):
+    """[n, width] whose rows start on boundaries of `align` bytes."""
     import torch
-    unit = 16 // torch.empty(0, dtype=dtype).element_size()
+    unit = align // torch.empty(0, dtype=dtype).element_size()
     return torch.empty(n, -(-width // unit) * unit, dtype=dtype, device=like.device)[:, :width]
 
 
@@ -435,8 +435,9 @@ class Fp8Matmul(_Operator):
     """csa_fp8_matmul: out [M, N] = a [M, K] times b [N, K] transposed, both E4M3 codes (uint8 or
     float8_e4m3fn) with fp32 scales a_scale [M, ceil(K / 128)] and b_scale [ceil(N / 128), ceil(K / 128)].
 
-    out: the tensor to fill (bf16 or fp32), by default a buffer of the object in out_dtype.  status: an
-    int32 on the device that records a wait that gave up.  Calling the object returns out."""
+    out: the tensor to fill (bf16 or fp32), by default a buffer of the object in out_dtype whose rows
+    start on 32-byte boundaries (a view of a wider buffer where N * its size is no multiple of 32).
+    status: an int32 on the device that records a wait that gave up.  Calling the object returns out."""
 
     def __init__(self, a, a_scale, b, b_scale, out=None, out_dtype=None, status=None):
         import torch
@@ -450,7 +451,7 @@ class Fp8Matmul(_Operator):
         _rows2d("a_scale", a_scale, m, kb, torch.float32)
         _rows2d("b_scale", b_scale, -(-n // 128), kb, torch.float32)
         if out is None:
-            out = torch.empty(m, n, dtype=out_dtype or torch.bfloat16, device=a.device)
+            out = _empty_rows(a, m, n, out_dtype or torch.bfloat16, 32)
         elif out_dtype is not None and out.dtype != out_dtype:
             _bad(f"out is {out.dtype}, not {out_dtype}")
         _rows2d("out", out, m, n)

@@ -274,3 +274,22 @@ def test_two_products_at_once_on_two_streams():
             op(stream=st)
     torch.cuda.synchronize()
     assert all(torch.equal(op._out, f) for op, f in zip(ops, firsts))
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("m,n,k", [(5, 77, 300), (200, 333, 700), (700, 8191, 130), (3000, 2047, 16)])
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_rows_of_the_default_buffer_and_contiguous_ones(m, n, k, dtype):
+    # by default rows start on 32-byte boundaries (vector stores); a contiguous output of an odd
+    # number of columns is stored element by element: the same bits
+    _gpu()
+    gen = torch.Generator(device=DEV).manual_seed(m + n)
+    kb = -(-k // 128)
+    a, b = _codes(m, k, gen), _codes(n, k, gen)
+    sa, sb = torch.rand(m, kb, generator=gen, device=DEV), torch.rand(-(-n // 128), kb, generator=gen, device=DEV)
+    got = csa.Fp8Matmul(a, sa, b, sb, out_dtype=dtype)()
+    assert got.shape == (m, n) and got.stride(0) * got.element_size() % 32 == 0 and got.stride(1) == 1
+    flat = torch.full((m * n + 3,), 7.0, dtype=dtype, device=DEV)
+    csa.Fp8Matmul(a, sa, b, sb, out=flat[:m * n].view(m, n))()
+    torch.cuda.synchronize()
+    assert torch.equal(flat[:m * n].view(m, n), got) and (flat[m * n:] == 7).all()
