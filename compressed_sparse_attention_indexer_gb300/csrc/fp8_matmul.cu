@@ -26,7 +26,7 @@
 // Every mbarrier wait is bounded; one that gives up sets bit 1 of the status.
 //
 // Measured (GB300): 8192 x 8192 x 7168 in 452 us (2.13 PFLOP/s, 1785 MHz under
-// the power cap; 406 us in a burst), 1024 x 4096 x 4096 in 23.9 us, 64 x 36864 x
+// the power cap; 406 us in a burst), 1024 x 4096 x 4096 in 21.5 us, 64 x 36864 x
 // 1536 in 14.1 us (4.4 TB/s), 331 x 1100 x 7000 in 10.5 us, 1 x 8192 x 1536 in
 // 6.0 us.  What bounds large tiles: the two 256-column TMEM buffers, each held
 // for its MMAs (512 cycles) and its way through the epilogue; in variants that
@@ -607,9 +607,20 @@ int launch_out(const MmArgs& g, int num_sms, cudaStream_t st, bool pdl) {
   if (g.M <= 16) return launch_shape<16, true, T>(g, num_sms, st, pdl);
   if (g.M <= 32) return launch_shape<32, true, T>(g, num_sms, st, pdl);
   if (g.M <= 64) return launch_shape<64, true, T>(g, num_sms, st, pdl);
-  // 256 columns per tile halve the reads of a, 128 keep more SMs busy
-  const int64_t tiles = (int64_t)((g.M + 127) / 128) * ((g.N + 255) / 256);
-  return tiles >= num_sms ? launch_shape<256, false, T>(g, num_sms, st, pdl) : launch_shape<128, false, T>(g, num_sms, st, pdl);
+  // Columns per tile, by the SMs' turns that the tiles come to and what a tile
+  // takes: one of 128 columns 0.48 (few blocks, where the output bounds it) to
+  // 0.6 (many) of one of 256.  Measured (256 / 128): 8192 x 8192 x 1024 93 / 88 us,
+  // 5051 x 12681 x 1408 108 / 113, 2048 x 9728 x 4096 75 / 83, 2048 x 5120 x 4096
+  // 57 / 53, 2048 x 2432 x 4096 38 / 24, 1100 x 4000 x 8000 36 / 42,
+  // 128 x 20000 x 7168 35 / 44.  Where those of 128 fit in one turn they are
+  // taken: 331 x 1100 x 7000 13.1 / 10.5.
+  const int64_t rows = ((int64_t)g.M + 127) / 128;
+  auto turns = [&](int64_t tiles) { return (tiles + num_sms - 1) / num_sms; };
+  const int64_t blocks = (g.K + kMmBlock - 1) / kMmBlock;
+  const int64_t narrow = turns(rows * (((int64_t)g.N + 127) / 128)), wide = turns(rows * (((int64_t)g.N + 255) / 256));
+  return narrow > 1 && narrow * (240 + (blocks < 12 ? blocks : 12) + (blocks < 60 ? blocks : 60)) >= wide * 500
+             ? launch_shape<256, false, T>(g, num_sms, st, pdl)
+             : launch_shape<128, false, T>(g, num_sms, st, pdl);
 }
 
 }  // namespace

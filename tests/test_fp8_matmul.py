@@ -293,3 +293,19 @@ def test_rows_of_the_default_buffer_and_contiguous_ones(m, n, k, dtype):
     csa.Fp8Matmul(a, sa, b, sb, out=flat[:m * n].view(m, n))()
     torch.cuda.synchronize()
     assert torch.equal(flat[:m * n].view(m, n), got) and (flat[m * n:] == 7).all()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("m,n,k", [(1100, 4000, 1300), (1990, 4801, 2500), (130, 19900, 2100), (2200, 2321, 1700)])
+def test_tiles_in_one_turn_of_the_sms_and_in_several(m, n, k, dtype):
+    _gpu()
+    g = torch.Generator(device=DEV).manual_seed(m + n + k)
+    a, b = _codes(m, k, g), _codes(n, k, g)
+    kb = -(-k // 128)
+    sa, sb = _scales(m, kb, g), _scales(-(-n // 128), kb, g)
+    got = csa.Fp8Matmul(a, sa, b, sb, out=torch.empty(m, n, dtype=dtype, device=DEV))()
+    _check(got, a, sa, b, sb, (m, n, k))
+    padded = csa.Fp8Matmul(a, sa, b, sb, out_dtype=dtype)()
+    torch.cuda.synchronize()
+    assert torch.equal(got, padded)
