@@ -37,9 +37,9 @@
 //
 // Measured (GB300): 64 requests of 1024 .. 65536 rows, 32 / 4 heads of 128, bf16,
 // in 675 .. 700 us (6.7 .. 7.0 TB/s, the copy rate); 32 of 16384 .. 32768 rows,
-// 64 / 8 heads, E4M3, in 322 .. 340 us (4.9 TB/s: bound by issue, about 820
+// 64 / 8 heads, E4M3, in 310 .. 330 us (5 TB/s: bound by issue, about 820
 // instructions per 32 rows of 256 bytes); 48 x 4 tokens, 16 / 8 heads of 64, in
-// 64 us (4.8 TB/s); one request of 1023 rows in 8.7 us (launch, two rounds of
+// 64 us (4.8 TB/s); one request of 1023 rows in 8.2 us (launch, two rounds of
 // dependent loads, one tile, the join of the warps and of the CTAs).
 #include "csa_internal.cuh"
 #include "ptx.cuh"
@@ -317,6 +317,9 @@ __global__ void __launch_bounds__(PaShape<D, MT, kFp8>::kThreads, 1)
   float* slots = reinterpret_cast<float*>(smem_raw + Sh::kRing + Sh::kQBytes);
   const uint32_t rowsc = smem_u32(smem_raw) + Sh::kRing + Sh::kQBytes + Sh::kSlotBytes + warp * Sh::kScaleBytes;
   const int group = a.heads / a.kv_heads;
+  const float per_group = 1.f / (float)group;
+  // i / group for 0 <= i < S * heads <= 2^20 (off by less than half of 1 / group)
+  auto token_of = [&](int i) { return (int)(((float)i + 0.5f) * per_group); };
   const int qrows = a.S * group;                    // query rows per kv head
   const int units = a.kv_heads * chunks;
   pdl_wait();
@@ -399,7 +402,7 @@ __global__ void __launch_bounds__(PaShape<D, MT, kFp8>::kThreads, 1)
   };
   auto copy = [&](int stage) {
     const uint32_t kdst = ring + stage * Sh::kWarpStage, vdst = kdst + kPer * Sh::kRowBytes;
-    const int h = ld.unit / chunks;
+    const int h = chunks == 1 ? ld.unit : ld.unit / chunks;
     constexpr int kSpan = Sh::kChunks > 32 ? 32 : Sh::kChunks;           // lanes per row and copy
     constexpr int kAtOnce = 32 / kSpan;                                  // rows per warp-wide copy
     const int ch = lane % kSpan, r0 = lane / kSpan;
@@ -447,13 +450,13 @@ __global__ void __launch_bounds__(PaShape<D, MT, kFp8>::kThreads, 1)
   const float scale2 = a.scale * kLog2e;
 
   for (int step = 0; step < steps; ++step) {
-    const int h = cu.unit / chunks, row0 = (cu.unit - h * chunks) * Sh::kRows;
+    const int h = chunks == 1 ? cu.unit : cu.unit / chunks, row0 = (cu.unit - h * chunks) * Sh::kRows;
     if (cu.sp.L <= 0) {  // a padding request: nothing to read, nothing to join
       load_step();
       for (int x = tid; x < Sh::kRows * (D / 8); x += Sh::kThreads) {
         const int i = row0 + x / (D / 8);
         if (i < qrows) {
-          const int s = i / group, hd = h * group + i - s * group;
+          const int s = token_of(i), hd = h * group + i - s * group;
           const int64_t tok = (int64_t)cu.b * a.S + s;
           *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(a.out) + tok * a.out_stride + hd * D + x % (D / 8) * 8) =
               make_uint4(0, 0, 0, 0);
@@ -470,7 +473,7 @@ __global__ void __launch_bounds__(PaShape<D, MT, kFp8>::kThreads, 1)
       seg_first = step;
       const __nv_bfloat16* q0 = static_cast<const __nv_bfloat16*>(a.q) + (int64_t)cu.b * a.S * a.q_stride;
       auto q_at = [&](int i) {  // query row i of the unit's kv head: token i / group, head h * group + i % group
-        const int s = i / group;
+        const int s = token_of(i);
         return q0 + (int64_t)s * a.q_stride + (h * group + i - s * group) * D;
       };
 #pragma unroll
@@ -478,7 +481,7 @@ __global__ void __launch_bounds__(PaShape<D, MT, kFp8>::kThreads, 1)
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
           const int i = row0 + mt * 16 + g + 8 * e;
-          pos[mt][e] = i < qrows ? cu.sp.L - a.S + i / group : -1;
+          pos[mt][e] = i < qrows ? cu.sp.L - a.S + token_of(i) : -1;
           m[mt][e] = -INFINITY;
           l[mt][e] = 0.f;
         }
@@ -747,7 +750,7 @@ __global__ void __launch_bounds__(PaShape<D, MT, kFp8>::kThreads, 1)
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
             const int i = row0 + mt * 16 + g + 8 * e;
-            sq2[mt][e] = i < qrows ? i / group : a.S;
+            sq2[mt][e] = i < qrows ? token_of(i) : a.S;
           }
         v_products_apart<D, MT, kFp8>(&o2[0][0][0], &pf2[0][0][0], &sq2[0][0], vt, lane, base, p_first, a.S, a.win);
         memcpy(o, o2, sizeof o);
@@ -772,6 +775,7 @@ __global__ void __launch_bounds__(PaShape<D, MT, kFp8>::kThreads, 1)
         for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
+            if (row0 + mt * 16 + 8 * e >= qrows) continue;   // no query row in these eight
             const int r = mt * 16 + g + 8 * e;
             if (c == 0) sml[r] = m[mt][e], sml[Sh::kRows + r] = l[mt][e];
             if constexpr (kFp8) {
@@ -803,6 +807,7 @@ __global__ void __launch_bounds__(PaShape<D, MT, kFp8>::kThreads, 1)
           for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
+              if (row0 + mt * 16 + 8 * e >= qrows) continue;
               const int r = mt * 16 + g + 8 * e;
               const float m2 = sml[r], top = fmaxf(m[mt][e], m2), ref = top == -INFINITY ? 0.f : top;
               const float f1 = fast_exp2(m[mt][e] - ref), f2 = fast_exp2(m2 - ref);
@@ -858,7 +863,7 @@ __global__ void __launch_bounds__(PaShape<D, MT, kFp8>::kThreads, 1)
             acc[i] += row_at[x * Sh::kSlotFloats + i] * f;
         }
         if (whole) {
-          const int i = row0 + r, s = i / group, hd = h * group + i - s * group;
+          const int i = row0 + r, s = token_of(i), hd = h * group + i - s * group;
           const bool any = sum > 0.f || sum != sum;   // some row weighs (a NaN is passed on)
           const float inv = any ? 1.f / sum : 0.f;
           __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(a.out) + ((int64_t)cu.b * a.S + s) * a.out_stride + hd * D +
