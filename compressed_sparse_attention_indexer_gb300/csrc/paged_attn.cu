@@ -37,8 +37,9 @@
 //
 // Measured (GB300): 64 requests of 1024 .. 65536 rows, 32 / 4 heads of 128, bf16,
 // in 675 .. 700 us (6.7 .. 7.0 TB/s, the copy rate); 32 of 16384 .. 32768 rows,
-// 64 / 8 heads, E4M3, in 310 .. 330 us (5 TB/s: bound by issue, about 820
-// instructions per 32 rows of 256 bytes); 48 x 4 tokens, 16 / 8 heads of 64, in
+// 64 / 8 heads, E4M3, in 311 us (5.2 TB/s; about 820 instructions
+// per 32 rows of 256 bytes in three warps per scheduler, a long chain each: 43% of
+// the issue slots, HBM neither); 48 x 4 tokens, 16 / 8 heads of 64, in
 // 64 us (4.8 TB/s); one request of 1023 rows in 8.2 us (launch, two rounds of
 // dependent loads, one tile, the join of the warps and of the CTAs).
 #include "csa_internal.cuh"
@@ -144,9 +145,9 @@ __device__ __forceinline__ float lds_f32(uint32_t a) {
   asm volatile("ld.shared.f32 %0, [%1];\n" : "=f"(v) : "r"(a) : "memory");
   return v;
 }
-__device__ __forceinline__ float4 lds_f4(uint32_t a) {
-  float4 v;
-  asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];\n" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(a) : "memory");
+__device__ __forceinline__ float2 lds_f2(uint32_t a) {
+  float2 v;
+  asm volatile("ld.shared.v2.f32 {%0, %1}, [%2];\n" : "=f"(v.x), "=f"(v.y) : "r"(a) : "memory");
   return v;
 }
 __device__ __forceinline__ void sts_f4(uint32_t a, float x, float y, float z, float w) {
@@ -385,20 +386,34 @@ __global__ void __launch_bounds__(PaShape<D, MT, kFp8>::kThreads, 1)
   Cursor<kTile> cu = ld;
   int loaded = 0;
 
-  // ---- row copies: lane r < kPer looks up the pool row of the warp's row r,
-  // one tile ahead of the copies that use it (-1: nothing to read)
-  int prow = -1;
+  // ---- row copies: lane r < kPer looks up the pool row of the warp's row r one
+  // tile ahead of the copies that use it.  A table's entry stays as it was
+  // loaded until then, so that nothing waits for it earlier (E4M3: 329 us to 311).
+  int entry = -1, within = 0;
   auto lookup = [&](const Cursor<kTile>& c) {
-    int p = -1;
-    if (lane < kPer) {
-      const int r = (c.sp.t0 + c.tile) * kTile + warp * kPer + lane;
-      if (r >= c.sp.lo && r < c.sp.L) {
-        const int64_t x = pool_row(a.table, a.block, a.table_stride, a.off, c.b, r);
-        if (x >= 0 && x < a.rows) p = (int)x;
-        else if (a.status) set_status(a.status, kStatusBadIndex);
+    const int r = (c.sp.t0 + c.tile) * kTile + warp * kPer + lane;
+    within = -1;                                   // nothing to read
+    if (lane < kPer && r >= c.sp.lo && r < c.sp.L) {
+      if (a.table) {
+        const int k = (int)((uint32_t)r / (uint32_t)a.block);
+        within = r - k * a.block;
+        entry = -1;
+        if (k < a.table_stride) entry = a.table[(int64_t)c.b * a.table_stride + k];
+      } else {
+        const int64_t x = a.off[c.b] + r;
+        within = 0;
+        entry = x >= 0 && x < a.rows ? (int)x : -1;
       }
     }
-    return p;
+  };
+  int prow = -1;                                   // the pool row (-1: nothing to read)
+  auto resolve = [&] {
+    prow = -1;
+    if (within >= 0) {
+      const int64_t x = entry < 0 ? -1 : a.table ? (int64_t)entry * a.block + within : entry;
+      if (x >= 0 && x < a.rows) prow = (int)x;
+      else if (a.status) set_status(a.status, kStatusBadIndex);
+    }
   };
   auto copy = [&](int stage) {
     const uint32_t kdst = ring + stage * Sh::kWarpStage, vdst = kdst + kPer * Sh::kRowBytes;
@@ -426,16 +441,19 @@ __global__ void __launch_bounds__(PaShape<D, MT, kFp8>::kThreads, 1)
   };
   auto load_step = [&] {
     if (loaded < steps) {
-      if (ld.sp.L > 0) copy(loaded % Sh::kStages);
+      if (ld.sp.L > 0) {
+        resolve();
+        copy(loaded % Sh::kStages);
+      }
       ++loaded;
       if (loaded < steps) {
         ld.next(a, units);
-        prow = lookup(ld);
+        lookup(ld);
       }
     }
     cp_async_commit();
   };
-  prow = lookup(ld);
+  lookup(ld);
 #pragma unroll
   for (int i = 0; i < Sh::kStages - 1; ++i) load_step();
 
@@ -444,9 +462,7 @@ __global__ void __launch_bounds__(PaShape<D, MT, kFp8>::kThreads, 1)
   uint32_t qf[Sh::kQReg ? D / 16 : 1][4];
   float qmul[MT][2];                               // E4M3: the power of two taken out of the thread's query rows
   float o[MT][D / 8][4], m[MT][2], l[MT][2];
-  int pos[MT][2];                                  // last visible row of the thread's query rows
-  int seg_first = 0;                               // step at which the current piece started
-  bool seg_new = true;
+  int seg_first = 0;                               // step at which the current piece starts
   const float scale2 = a.scale * kLog2e;
 
   for (int step = 0; step < steps; ++step) {
@@ -466,11 +482,10 @@ __global__ void __launch_bounds__(PaShape<D, MT, kFp8>::kThreads, 1)
       if (tid == 0 && step + 1 == steps) joins[blockIdx.x].count = 0;
       if (tid == 0) unit_at += cu.sp.tiles + 1;
       cu.next(a, units);
+      seg_first = step + 1;
       continue;
     }
-    if (seg_new) {
-      seg_new = false;
-      seg_first = step;
+    if (step == seg_first) {
       const __nv_bfloat16* q0 = static_cast<const __nv_bfloat16*>(a.q) + (int64_t)cu.b * a.S * a.q_stride;
       auto q_at = [&](int i) {  // query row i of the unit's kv head: token i / group, head h * group + i % group
         const int s = token_of(i);
@@ -480,8 +495,6 @@ __global__ void __launch_bounds__(PaShape<D, MT, kFp8>::kThreads, 1)
       for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
-          const int i = row0 + mt * 16 + g + 8 * e;
-          pos[mt][e] = i < qrows ? cu.sp.L - a.S + token_of(i) : -1;
           m[mt][e] = -INFINITY;
           l[mt][e] = 0.f;
         }
@@ -631,16 +644,14 @@ __global__ void __launch_bounds__(PaShape<D, MT, kFp8>::kThreads, 1)
       const bool edge = base < cu.sp.lo || base + kPer - 1 > p_first ||
                         (a.win > 0 && base < cu.sp.L - a.win);  // some query does not see all the rows
       uint32_t pf[MT][kGroups][4];
-      float inv[2 * kGroups][2], sgn[2 * kGroups][2];           // E4M3: 1 / |v_scale| and its sign
 #pragma unroll
       for (int n = 0; n < 2 * kGroups; ++n)
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
           float ks = scale2, lv = 0.f;
-          inv[n][e] = sgn[n][e] = 1.f;
           if constexpr (kFp8) {
-            const float4 t = lds_f4(rowsc + (n * 8 + c * 2 + e) * 16);
-            ks = t.x, lv = t.y, inv[n][e] = t.z, sgn[n][e] = t.w;
+            const float2 t = lds_f2(rowsc + (n * 8 + c * 2 + e) * 16);
+            ks = t.x, lv = t.y;
           }
 #pragma unroll
           for (int mt = 0; mt < MT; ++mt)
@@ -652,14 +663,21 @@ __global__ void __launch_bounds__(PaShape<D, MT, kFp8>::kThreads, 1)
         }
       if (edge) {
 #pragma unroll
-        for (int mt = 0; mt < MT; ++mt)
+        for (int mt = 0; mt < MT; ++mt) {
+          int pos[2];                              // last visible row of the thread's query rows
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            const int i = row0 + mt * 16 + g + 8 * e;
+            pos[e] = i < qrows ? p_first + token_of(i) : -1;
+          }
 #pragma unroll
           for (int n = 0; n < 2 * kGroups; ++n)
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-              const int r = base + n * 8 + c * 2 + (i & 1), last = pos[mt][i >> 1];
+              const int r = base + n * 8 + c * 2 + (i & 1), last = pos[i >> 1];
               if (r > last || (a.win > 0 && r <= last - a.win)) s[mt][n][i] = -INFINITY;
             }
+        }
       }
 #pragma unroll
       for (int mt = 0; mt < MT; ++mt) {
@@ -694,12 +712,17 @@ __global__ void __launch_bounds__(PaShape<D, MT, kFp8>::kThreads, 1)
 #pragma unroll
           for (int n = 0; n < 2; ++n)
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              const float ref = m[mt][i >> 1] == -INFINITY ? 0.f : m[mt][i >> 1];
-              const float w = fast_exp2(s[mt][2 * x + n][i] - ref);
-              if (!kFp8) l[mt][i >> 1] += w;
-              else if (!wide) l[mt][i >> 1] += w * inv[2 * x + n][i & 1];
-              p[n][i] = kFp8 ? w * sgn[2 * x + n][i & 1] : w;
+            for (int e = 0; e < 2; ++e) {
+              float2 t = make_float2(1.f, 1.f);                 // E4M3: 1 / |v_scale| and its sign
+              if constexpr (kFp8) t = lds_f2(rowsc + ((2 * x + n) * 8 + c * 2 + e) * 16 + 8);
+#pragma unroll
+              for (int y = 0; y < 2; ++y) {
+                const float ref = m[mt][y] == -INFINITY ? 0.f : m[mt][y];
+                const float w = fast_exp2(s[mt][2 * x + n][2 * y + e] - ref);
+                if (!kFp8) l[mt][y] += w;
+                else if (!wide) l[mt][y] += w * t.x;
+                p[n][2 * y + e] = kFp8 ? w * t.y : w;
+              }
             }
           if (kFp8 && wide) {
 #pragma unroll
@@ -895,7 +918,7 @@ __global__ void __launch_bounds__(PaShape<D, MT, kFp8>::kThreads, 1)
         }
         joins[blockIdx.x] = j;
       }
-      seg_new = true;
+      seg_first = step + 1;
       if (tid == 0) unit_at += cu.sp.tiles + 1;
     }
     cu.next(a, units);
