@@ -360,8 +360,8 @@ class NormRows(_Operator):
     object by default, `residual` itself for in place), weight [width] or None (ones).  norm=False:
     the rows as they are.  out / codes: which outputs to make, or the tensors to fill (codes uint8 or
     float8_e4m3fn [n, width], scale fp32 [n, ceil(width / 128)]).  Calling the object returns
-    {"residual", "out", "codes", "scale"} as far as they are made.  Where nothing is asked of the rows
-    (no norm, residual or codes, and no tensor to fill) out is x itself."""
+    {"residual", "out", "codes", "scale"} as far as they are made.  out=True without the norm is no copy:
+    out is x itself, or with a residual the sum (the tensor under "residual")."""
 
     def __init__(self, x, weight=None, residual=None, norm: bool = True, eps: float = 1e-6, out=False,
                  codes=True, scale=None, residual_out=None):
@@ -383,9 +383,9 @@ class NormRows(_Operator):
             _bad(f"weight must be contiguous {x.dtype} of shape ({width},)")
         if weight is not None and not norm:
             _bad("weight given with norm=False")
-        self._same = not norm and residual is None and codes is False and out is True
+        given = out is True and not norm               # the rows asked for are there already
         if out is True:
-            out = x if self._same else _empty_rows(x, n, width, x.dtype)
+            out = _empty_rows(x, n, width, x.dtype) if norm else x if residual is None else residual_out
         if codes is True:
             codes = _empty_rows(x, n, width, torch.uint8)
         out, codes = (None if t is False else t for t in (out, codes))
@@ -403,7 +403,9 @@ class NormRows(_Operator):
         unit = 8 if dt == CSA_DTYPE_BF16 else 4
         st = CNorm(n=n, width=width, dtype=dt, norm=1 if norm else 0, eps=eps, x=_ptr(x), x_stride=_row_stride(x, unit),
                    weight=_ptr(weight))
-        for name, t, u in (("residual", residual, unit), ("residual_out", residual_out, unit), ("out", out, unit),
+        self._idle = given and residual is None and codes is None
+        written = out if not given or codes is None else None
+        for name, t, u in (("residual", residual, unit), ("residual_out", residual_out, unit), ("out", written, unit),
                            ("codes", codes, 16), ("scale", scale, 1)):
             if t is not None:
                 setattr(st, name, _ptr(t))
@@ -418,7 +420,7 @@ class NormRows(_Operator):
             self._out["codes"], self._out["scale"] = codes.view(torch.float8_e4m3fn), scale
 
     def __call__(self, stream=None) -> dict:
-        if not self._same:
+        if not self._idle:
             self._launch(stream)
         return self._out
 

@@ -826,7 +826,9 @@ int csa_norm_rows(const csa_norm* a, void* stream) {
   k.residual = a->residual; k.residual_stride = a->residual_stride;
   k.residual_out = a->residual_out; k.residual_out_stride = a->residual_out_stride;
   k.weight = a->weight;
-  k.out = a->out; k.out_stride = a->out_stride;
+  // without the norm residual_out holds out's values already
+  const bool same = !a->norm && a->residual && a->out == a->residual_out && a->out_stride == a->residual_out_stride;
+  k.out = same ? nullptr : a->out; k.out_stride = a->out_stride;
   k.codes = a->codes; k.codes_stride = a->codes_stride;
   k.scale = a->scale; k.scale_stride = a->scale_stride;
   return finish_free(csa::launch_norm(k, a->dtype, sms, static_cast<cudaStream_t>(stream), use_pdl()));

@@ -17,8 +17,8 @@
 // has a fixed order.
 //
 // Measured (GB300): 16384 x 7168 bf16, residual, both outputs, in 166 us
-// (6.4 TB/s, 94% of the measured copy rate); 131072 x 128 to codes in 11.4 us
-// (4.5 TB/s: bound by instructions per row); 4097 x 1000 fp32 to codes in
+// (6.4 TB/s, 94% of the measured copy rate); 131072 x 128 to codes in 11.5 us
+// (4.4 TB/s: bound by instructions per row); 4097 x 1000 fp32 to codes in
 // 6.3 us; one row of 4096 in 3.0 us (a launch).
 #include <cuda_fp8.h>
 
@@ -132,6 +132,13 @@ __device__ __forceinline__ float block_scale(float m) {
   constexpr float kInv = 1.f / kE4m3Max;
   const float q = m * kInv;
   return m > 0.f ? fmaxf(m < INFINITY ? fmaf(fmaf(-q, kE4m3Max, m), kInv, q) : m, 1.17549435e-38f) : 1.f;
+}
+// What turns s weight into codes: r / scale, rounded (the product with the
+// reciprocal, corrected by its residual; uncorrected it takes the other one of
+// two neighbouring codes a fifth more often).
+__device__ __forceinline__ float code_factor(float r, float scale) {
+  const float inv = rcp_approx(scale), q = r * inv;
+  return scale < INFINITY ? fmaf(fmaf(-q, scale, r), inv, q) : q;
 }
 // f / scale to within a rounding that almost never differs from the exact
 // one's: the product with the reciprocal, corrected by its residual (one step
@@ -330,7 +337,7 @@ __global__ void __launch_bounds__(kNormMaxThreads, VPT == 1 ? 2 : 1) norm_kernel
 #pragma unroll
           for (int e = 0; e < E; ++e) z[e] = y[i][e];
           if (a.norm) {
-            const float mul = r * rcp_approx(scale);
+            const float mul = code_factor(r, scale);
 #pragma unroll
             for (int e = 0; e < E; e += 2) mul2(z + e, mul, mul);
           } else {
@@ -441,7 +448,7 @@ __global__ void __launch_bounds__(kNarrowThreads, kNarrowBlocks) norm_narrow_ker
 #pragma unroll
         for (int e = 0; e < E; ++e) z[e] = y[j][e];
         if (kNorm) {
-          const float mul = r * rcp_approx(scale);
+          const float mul = code_factor(r, scale);
 #pragma unroll
           for (int e = 0; e < E; e += 2) mul2(z + e, mul, mul);
         } else {

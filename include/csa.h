@@ -293,7 +293,8 @@ typedef struct {
     void *residual_out; int64_t residual_out_stride;   /* given exactly when residual is; may be
                                                           residual itself (in place) */
     const void *weight;       /* [width], NULL = ones                              */
-    void *out; int64_t out_stride;                     /* [n, width] or NULL; may be x itself */
+    void *out; int64_t out_stride;                     /* [n, width] or NULL; may be x itself,
+                                                          or with norm = 0 residual_out */
     uint8_t *codes; int64_t codes_stride;              /* [n, width] E4M3 bytes or NULL */
     float *scale; int64_t scale_stride;                /* [n, ceil(width / 128)], given exactly
                                                           when codes is              */

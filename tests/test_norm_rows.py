@@ -363,3 +363,45 @@ def test_many_rows_per_block(width, dtype, residual):
     torch.cuda.synchronize()
     check(got, x[:, :width], res[:, :width] if residual else None, weight, True, 1e-6, f"{width} {dtype}")
     assert torch.equal(xd[:, width:].cpu(), x[:, width:]) and torch.equal(rd[:, width:].cpu(), res[:, width:])
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("width", [128, 200, 1003, 4096])
+def test_out_without_the_norm_is_the_sum(width, dtype):
+    # no second copy of the sum: "out" is the tensor under "residual" (codes or not); a tensor to fill is filled
+    _gpu()
+    g = torch.Generator().manual_seed(width)
+    pad = -(-width // 16) * 16
+    x, res = (torch.randn(70, pad, generator=g).to(dtype)[:, :width] for _ in range(2))
+    xd, rd = x.to(DEV), res.to(DEV)
+    xd, rd = (torch.nn.functional.pad(t, (0, pad - width))[:, :width] for t in (xd, rd))
+    own = torch.zeros(70, pad, dtype=dtype, device=DEV)[:, :width]
+    for codes in (False, True):
+        got = csa.NormRows(xd, residual=rd, norm=False, out=True, codes=codes)()
+        assert got["out"] is got["residual"]
+        filled = csa.NormRows(xd, residual=rd, norm=False, out=own, codes=codes)()
+        torch.cuda.synchronize()
+        check(got, x, res, None, False, 1e-6)
+        assert filled["out"] is own and torch.equal(own, got["out"])
+        same = csa.NormRows(xd, norm=False, out=True, codes=codes)()
+        assert same["out"] is xd
+        if codes:
+            check(same, x, None, None, False, 1e-6)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("width", [128, 512])
+@pytest.mark.parametrize("size", [1e-36, 1e-30, 1.0, 1e17])
+def test_codes_of_rows_near_the_ends_of_the_range(width, size):
+    # the scale's lower bound among them; the mean square stays inside fp32's range (eps carries the smallest
+    # rows, whose squares vanish)
+    _gpu()
+    g = torch.Generator().manual_seed(width)
+    x = torch.randn(40, width, generator=g) * size
+    x[3] = 0
+    x[4, :128] = 0
+    weight = (1 + 0.1 * torch.randn(width, generator=g))
+    got = csa.NormRows(x.to(DEV), weight=weight.to(DEV), eps=1e-6, out=True, codes=True)()
+    torch.cuda.synchronize()
+    check(got, x, None, weight, True, 1e-6, f"{width} {size}")
