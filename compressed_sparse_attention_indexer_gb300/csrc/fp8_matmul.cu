@@ -38,15 +38,12 @@
 #include <cudaTypedefs.h>
 
 #include "csa_internal.cuh"
+#include "mm_pipeline.h"
 #include "tc5.cuh"
 
 namespace csa {
 
 namespace {
-
-constexpr int kMmBlock = 128;                 // codes per scale, bytes per stage row
-constexpr int kMmPBytes = 128 * kMmBlock;     // P tile: 128 rows
-constexpr int kMmMaxStages = 12;
 
 // One test of a barrier's phase, whose answer is used later.
 __device__ __forceinline__ uint32_t bar_ask(uint32_t bar, uint32_t parity) {
@@ -54,43 +51,6 @@ __device__ __forceinline__ uint32_t bar_ask(uint32_t bar, uint32_t parity) {
   asm volatile("{\n .reg .pred p;\n mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n selp.u32 %0, 1, 0, p;\n}\n" : "=r"(ok) : "r"(bar), "r"(parity) : "memory");
   return ok;
 }
-template <int NT, bool kSwap>
-struct MmShape {
-  // 64 sums per epilogue thread at most; with 256 columns sixteen warps, four
-  // per scheduler, hide each other's TMEM reads
-  static constexpr int kEpiWarps = kSwap ? 4 : NT == 256 ? 16 : 8;
-  static constexpr int kAux = kSwap ? 2 : 4;               // warps before the epilogue's
-  static constexpr int kIssuers = kSwap ? 1 : 2;
-  static constexpr int kThreads = 32 * (kAux + kEpiWarps);
-  static constexpr int kCols = NT / (kEpiWarps / 4);       // columns per epilogue thread
-  static constexpr int kChunk = kSwap || NT == 256 ? 16 : 32;  // columns per TMEM read
-  static constexpr int kAccCols = NT < 32 ? 32 : NT;       // TMEM columns per buffer
-  static constexpr int kBufs = kSwap || NT == 128 ? 4 : 2;
-  static constexpr int kTmemCols = kAccCols * kBufs;
-  static constexpr int kStageBytes = kMmPBytes + NT * kMmBlock;
-  static constexpr int kCtasPerSm = kSwap ? 2 : 1;
-  // !kSwap: a patch per epilogue warp, through which the output leaves in
-  // 32- or 128-byte pieces of a row
-  static constexpr int kLine = NT == 256 ? 32 : 128;
-  static constexpr int kPatchBytes = kSwap ? 0 : kEpiWarps * 32 * kLine;
-  // scales: per block the a scales of the tile's rows of a (padded to 128) and
-  // the b scales of its 128-row parts
-  static constexpr int kScaleFloats = 128 + 4;
-  static constexpr int kRoom = (kSwap ? 113 * 1024 : 227 * 1024) - 1024 - 1024 - kPatchBytes;
-  static constexpr int kFit = (kRoom - kBufs * kScaleFloats * 4) / (kStageBytes + kScaleFloats * 4);
-  static constexpr int kStages = kFit > kMmMaxStages ? kMmMaxStages : kFit;
-  static constexpr int kSlots = kStages + kBufs;               // see the scale warp
-  static constexpr int kSmem = kStages * kStageBytes + kPatchBytes + kSlots * kScaleFloats * 4 + 1024;
-  // fp32 sums of the tile in the ring's memory, laid out like the output: rows
-  // of kSumCols neighbouring columns of out, the pitch chosen so that neither
-  // the writes nor the reads conflict
-  static constexpr int kSumRows = kSwap ? NT : 128, kSumCols = kSwap ? 128 : NT;
-  static constexpr int kPitch = kSumCols * 4 + (kSwap ? 0 : 16);
-  static_assert(kSumRows * kPitch <= kStages * kStageBytes, "sums exceed the ring");
-  static_assert(kSmem + 1024 <= (kSwap ? 113 : 227) * 1024, "shared memory");
-  static_assert(kStages <= kMmMaxStages && kTmemCols <= 512 / kCtasPerSm, "ring or TMEM");
-};
-
 struct MmSmem {
   uint64_t full[kMmMaxStages];   // the block's codes are in shared memory
   uint64_t done[kMmMaxStages];   // the block's MMAs are done: the stage is free, its product is in TMEM
@@ -404,29 +364,32 @@ __global__ void __launch_bounds__(MmShape<NT, kSwap>::kThreads, MmShape<NT, kSwa
     // 23.9 us, 331 x 1100 x 7000 11.5 / 10.5.
     if (lane == 0) {
       constexpr int kBy = Sh::kIssuers;
-      const int which = warp == 1 ? 0 : 1, blocks = first < tiles ? ((tiles - 1 - first) / step + 1) * (kb1 - kb0) : 0;
+      struct {
+        MmSmem& sm;
+        volatile int* abort;
+        __device__ __forceinline__ bool wait_stage(int i, uint32_t parity) { return tc5::mbar_wait(smem_u32(&sm.full[i]), parity, abort); }
+        __device__ __forceinline__ bool wait_buffer(int i, uint32_t parity) { return tc5::mbar_wait(smem_u32(&sm.tempty[i]), parity, abort); }
+        __device__ __forceinline__ uint32_t ask_stage(int i, uint32_t parity) { return bar_ask(smem_u32(&sm.full[i]), parity); }
+        __device__ __forceinline__ uint32_t ask_buffer(int i, uint32_t parity) { return bar_ask(smem_u32(&sm.tempty[i]), parity); }
+      } bars{sm, abort};
+      const int blocks = first < tiles ? ((tiles - 1 - first) / step + 1) * (kb1 - kb0) : 0;
       const uint32_t idesc = tc5::idesc_e4m3_f32(128, NT);
-      int st = which, buf = which, n = which, last = -1;
-      uint32_t ph = 0, bph = 0, okf = 0, okt = 1;
-      for (; n < blocks && !*abort; n += kBy) {
-        if (!okf && !tc5::mbar_wait(smem_u32(&sm.full[st]), ph, abort)) break;
-        if (!okt && !tc5::mbar_wait(smem_u32(&sm.tempty[buf]), bph ^ 1u, abort)) break;
+      MmIssue<Sh> is(kBy == 1 || warp == 1 ? 0 : 1);
+      int last = -1;
+      for (; is.n < blocks && !*abort;) {
+        if (!is.ready(bars)) break;
         tc5::fence_after_sync();
-        const uint64_t pd = tc5::sdesc_k_sw128(base + st * Sh::kStageBytes);
-        const uint64_t qd = tc5::sdesc_k_sw128(base + st * Sh::kStageBytes + kMmPBytes);
-        const uint32_t d = tmem + buf * Sh::kAccCols, now = smem_u32(&sm.done[st]);
-        if ((st += kBy) >= Sh::kStages) st -= Sh::kStages, ph ^= 1u;
-        if ((buf += kBy) >= Sh::kBufs) buf -= Sh::kBufs, bph ^= 1u;
+        const uint64_t pd = tc5::sdesc_k_sw128(base + is.st * Sh::kStageBytes);
+        const uint64_t qd = tc5::sdesc_k_sw128(base + is.st * Sh::kStageBytes + kMmPBytes);
+        const uint32_t d = tmem + is.buf * Sh::kAccCols, now = smem_u32(&sm.done[is.st]);
+        last = is.n;
+        is.next();
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           tc5::mma_e4m3(d, pd + 2 * i, qd + 2 * i, idesc, i > 0);
-          if (i == 1) {  // asked here, the next block's barriers answer while the MMAs are issued
-            okf = bar_ask(smem_u32(&sm.full[st]), ph);
-            okt = n + kBy < Sh::kBufs ? 1u : bar_ask(smem_u32(&sm.tempty[buf]), bph ^ 1u);
-          }
+          if (i == 1) is.ask(bars);  // asked here, the next block's barriers answer while the MMAs are issued
         }
         tc5::mma_commit(now);  // frees the stage and hands the product to the epilogue
-        last = n;
       }
       // MMAs still in flight finish before TMEM is freed (this thread's complete in order)
       if (last >= 0) tc5::mbar_wait_drain(smem_u32(&sm.done[last % Sh::kStages]), (last / Sh::kStages) & 1);
