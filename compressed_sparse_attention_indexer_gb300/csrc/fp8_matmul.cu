@@ -309,10 +309,8 @@ __global__ void __launch_bounds__(MmShape<NT, kSwap>::kThreads, MmShape<NT, kSwa
   if (codes_warp || scales_warp) {
     // copies: the codes (lane 0, bulk) and the scales (every lane).  (Fetched by
     // the epilogue's threads instead, each row's line by every warp, the scales
-    // took longer than the sums.)  Block n's scales go to slot n % kSlots, last
-    // read for block n - kStages - kBufs; done(n - kStages) says that its MMAs
-    // were issued, for which that block's TMEM buffer, and so its scales, had
-    // been read.
+    // took longer than the sums.)  Block n's scales go to slot n % kSlots: see
+    // MmShape for what orders the slot's reads before its next copy.
     constexpr int kRows = kSwap ? (NT < 32 ? 32 : NT) : 128, kParts = kSwap ? 1 : NT / 128;
     int st = 0, slot = 0, n = 0;
     uint32_t ph = 0;

@@ -40,9 +40,13 @@ struct MmShape {
   // the b scales of its 128-row parts
   static constexpr int kScaleFloats = 128 + 4;
   static constexpr int kRoom = (kSwap ? 113 * 1024 : 227 * 1024) - 1024 - 1024 - kPatchBytes;
-  static constexpr int kFit = (kRoom - kBufs * kScaleFloats * 4) / (kStageBytes + kScaleFloats * 4);
+  static constexpr int kFit = (kRoom - (kBufs + 1) * kScaleFloats * 4) / (kStageBytes + kScaleFloats * 4);
   static constexpr int kStages = kFit > kMmMaxStages ? kMmMaxStages : kFit;
-  static constexpr int kSlots = kStages + kBufs;               // see the scale warp
+  // Block n's scales lie in slot n % kSlots and may be read until block n + 1's
+  // buffer is given back (kSwap: the last chunk's after block n's own is).  The
+  // slot's next copy, block n + kSlots, follows done(n + kBufs + 1), whose MMAs
+  // waited for that buffer.
+  static constexpr int kSlots = kStages + kBufs + 1;
   static constexpr int kSmem = kStages * kStageBytes + kPatchBytes + kSlots * kScaleFloats * 4 + 1024;
   // fp32 sums of the tile in the ring's memory, laid out like the output: rows
   // of kSumCols neighbouring columns of out, the pitch chosen so that neither

@@ -1,7 +1,8 @@
 // Runs the product's pipeline (mm_pipeline.h) as a model in which every warp, every copy and every
 // MMA may be as late as it likes, with mbarriers that tell a phase by its parity alone, as the
-// hardware's do.  Arguments: how many random orders to run per shape, and which walk the issuers
-// take: "own" (the kernel's) or "stage-first", a mistake planted here to see that the model finds it.
+// hardware's do.  Arguments: how many random orders to run per shape, and which mistake is planted to
+// see that the model finds it: "none", "stage-first" (in the issuers' walk) or "one-slot-less" (in
+// the ring of the scales).
 // Prints a line per shape and returns the number of shapes that went wrong.
 #include <cstdio>
 #include <cstdlib>
@@ -46,17 +47,18 @@ struct Model {
   static constexpr int kEpi = 3;                      // epilogue warps (more change nothing)
   static constexpr int kCopiers = Sh::kIssuers == 1 ? 1 : 2;
   std::mt19937 rng;
-  int blocks;
+  int blocks, slots;
   const char* wrong = nullptr;
   Bar full[kMmMaxStages], done[kMmMaxStages], tempty[4];
   int holds[kMmMaxStages];                            // the block whose codes are in the stage, -1: in flux
   int product[4];                                     // the block whose product is in the buffer, -1: in flux
+  std::vector<int> scales;                            // the block whose scales the slot is for, from its copy's start
   struct Landing { int block; bool codes; };
   std::vector<Landing> flight;                        // copies asked for and not landed
   struct Copier { int n = 0; } copier[2];
   struct Issuer { Walk<Sh> is; std::deque<int> mmas; bool asked = true; explicit Issuer(int i) : is(i) {} };
   std::vector<Issuer> issuer;
-  struct Epilogue { int n = 0, step = 0; } epi[kEpi];
+  struct Epilogue { int n = 0; bool late = false; } epi[kEpi];
 
   // what an issuer sees of the barriers: a wait that is not over is a step not taken
   bool wait_stage(int i, uint32_t p) { return full[i].test(p); }
@@ -64,7 +66,7 @@ struct Model {
   uint32_t ask_stage(int i, uint32_t p) { return full[i].test(p); }
   uint32_t ask_buffer(int i, uint32_t p) { return tempty[i].test(p); }
 
-  Model(unsigned seed, int n) : rng(seed), blocks(n) {
+  Model(unsigned seed, int n, int ring) : rng(seed), blocks(n), slots(ring), scales(ring, -1) {
     for (Bar& b : full) b.init(2);                    // the codes and the scales
     for (Bar& b : tempty) b.init(kEpi);
     for (int i = 0; i < Sh::kIssuers; ++i) issuer.emplace_back(i);
@@ -84,7 +86,10 @@ struct Model {
       holds[st] = -1;
       flight.push_back({n, true});
     }
-    if (who == kCopiers - 1) flight.push_back({n, false});
+    if (who == kCopiers - 1) {
+      scales[n % slots] = n;
+      flight.push_back({n, false});
+    }
     ++copier[who].n;
   }
   void land() {
@@ -105,7 +110,7 @@ struct Model {
     if (i.is.n >= blocks || !i.is.ready(*this)) return;
     if (holds[i.is.st] != i.is.n) wrong = "MMAs on a stage that does not hold their block";
     for (const Epilogue& e : epi)
-      if (e.n <= i.is.n - Sh::kBufs) wrong = "MMAs into a buffer that has not been read";
+      if (e.n + e.late <= i.is.n - Sh::kBufs) wrong = "MMAs into a buffer that has not been read";
     i.mmas.push_back(i.is.n);
     product[i.is.buf] = -1;
     i.is.next();
@@ -122,10 +127,16 @@ struct Model {
   void read(int who) {
     Epilogue& e = epi[who];
     if (e.n >= blocks) return;
+    if (e.late) {                                     // scales may be read after the buffer is given back
+      if (scales[e.n % slots] != e.n) wrong = "scales read that are another block's";
+      e.late = false;
+      ++e.n;
+      return;
+    }
     if (!done[e.n % Sh::kStages].test(e.n / Sh::kStages & 1)) return;
     if (product[e.n % Sh::kBufs] != e.n) wrong = "a product read that is not its block's";
     tempty[e.n % Sh::kBufs].arrive();
-    ++e.n;
+    e.late = true;
   }
 
   const char* run() {
@@ -153,7 +164,7 @@ struct Model {
       for (int i = 0; i < kCopiers; ++i) copy(i);
       land();
       for (int i = 0; i < Sh::kIssuers; ++i) issue(i), finish(i);
-      for (int i = 0; i < kEpi; ++i) read(i);
+      for (int i = 0; i < kEpi; ++i) read(i), read(i);
     }
     for (const Epilogue& e : epi)
       if (!wrong && e.n != blocks) wrong = "a block that never came through";
@@ -162,30 +173,33 @@ struct Model {
 };
 
 template <class Sh, template <class> class Walk>
-int check(const char* name, int orders) {
+int check(const char* name, int orders, int less) {
   const char* wrong = nullptr;
   int at = -1;
   for (int i = 0; i < orders && !wrong; ++i) {
-    Model<Sh, Walk> m(1000003u * i + 17, 3 + i % 60);
+    Model<Sh, Walk> m(1000003u * i + 17, 3 + i % 60, Sh::kSlots - less);
     wrong = m.run();
     at = i;
   }
-  std::printf("%s: stages %d, buffers %d, issuers %d: %s", name, Sh::kStages, Sh::kBufs, Sh::kIssuers, wrong ? wrong : "ok");
+  std::printf("%s: stages %d, buffers %d, issuers %d, slots %d: %s", name, Sh::kStages, Sh::kBufs, Sh::kIssuers, Sh::kSlots - less,
+              wrong ? wrong : "ok");
   if (wrong) std::printf(" (order %d)", at);
   std::printf("\n");
   return wrong != nullptr;
 }
 
 template <template <class> class Walk>
-int all(int orders) {
-  return check<MmShape<16, true>, Walk>("16 swapped", orders) + check<MmShape<32, true>, Walk>("32 swapped", orders) +
-         check<MmShape<64, true>, Walk>("64 swapped", orders) + check<MmShape<128, false>, Walk>("128", orders) +
-         check<MmShape<256, false>, Walk>("256", orders);
+int all(int orders, int less) {
+  return check<MmShape<16, true>, Walk>("16 swapped", orders, less) + check<MmShape<32, true>, Walk>("32 swapped", orders, less) +
+         check<MmShape<64, true>, Walk>("64 swapped", orders, less) + check<MmShape<128, false>, Walk>("128", orders, less) +
+         check<MmShape<256, false>, Walk>("256", orders, less);
 }
 
 }  // namespace
 
 int main(int argc, char** argv) {
   const int orders = argc > 1 ? std::atoi(argv[1]) : 1000;
-  return argc > 2 && !std::strcmp(argv[2], "stage-first") ? all<StageFirst>(orders) : all<MmIssue>(orders);
+  const char* mistake = argc > 2 ? argv[2] : "none";
+  return !std::strcmp(mistake, "stage-first") ? all<StageFirst>(orders, 0)
+                                              : all<MmIssue>(orders, !std::strcmp(mistake, "one-slot-less"));
 }

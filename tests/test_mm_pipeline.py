@@ -33,3 +33,9 @@ def test_a_stage_waited_for_before_the_buffer_is_found(model):
     # MMAs on a stage whose codes have not landed
     r = model("800", "stage-first")
     assert r.returncode > 0 and "MMAs on a stage that does not hold their block" in r.stdout, r.stdout
+
+
+def test_a_ring_of_scales_that_comes_round_too_soon_is_found(model):
+    # the epilogue gives a buffer back before it reads the last of the block's scales
+    r = model("800", "one-slot-less")
+    assert r.returncode > 0 and "scales read that are another block's" in r.stdout, r.stdout
