@@ -279,10 +279,11 @@ CSA_API int csa_cache_writeback(const void *rows, int64_t rows_stride, const int
  *                 (the last block may be shorter), 1 where they are all zero
  *   codes = y / scale[t][j] to the nearest E4M3 value (ties to even)
  * With width 128 codes and scale are the FP8 indexer-key pool's row and row
- * scale (csa_config.idx_dtype).  s and its squares are summed in fp32 and must
- * stay in its range.  A NaN element does not count in max|y| and becomes the
- * NaN code; an infinite one makes its block's scale infinite, its code NaN and
- * the block's finite codes zero. */
+ * scale (csa_config.idx_dtype).  All of it is formed in fp32: s and the sum of its
+ * squares must stay in its range, for codes |s * weight| below 2^96, and where y / scale
+ * lies as close to the middle between two codes as its roundings, either may come out.
+ * A NaN element does not count in max|y| and becomes the NaN code; an infinite one makes
+ * its block's scale infinite, its code NaN and the block's finite codes zero. */
 typedef struct {
     int32_t n, width;         /* rows (0: a no-op), elements per row               */
     int32_t dtype;            /* CSA_DTYPE_BF16 or CSA_DTYPE_F32: x, residual, weight, out */

@@ -405,3 +405,38 @@ def test_codes_of_rows_near_the_ends_of_the_range(width, size):
     got = csa.NormRows(x.to(DEV), weight=weight.to(DEV), eps=1e-6, out=True, codes=True)()
     torch.cuda.synchronize()
     check(got, x, None, weight, True, 1e-6, f"{width} {size}")
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("width,residual", [(128, False), (100, True), (512, False), (512, True), (1003, False)])
+@pytest.mark.parametrize("size", [1e-36, 3e-37, 1e-37, 1e-39])
+def test_codes_of_tiny_blocks(width, residual, dtype, size):
+    # blocks so small that norm factor / scale is no fp32 number: whole rows, and one block of an ordinary row
+    # (where the scale is at its lower bound), zeros among their elements.  A value that is subnormal before the
+    # division is off by 2^-150 at most, which is 2^-24 of the smallest scale (2^-23 allowed)
+    _gpu()
+    g = torch.Generator().manual_seed(width)
+    unit = 16 // torch.empty(0, dtype=dtype).element_size()
+    x = torch.randn(60, -(-width // unit) * unit, generator=g)
+    x[:30] *= size
+    x[30:, :128] *= size
+    x[::7, 3::5] = 0
+    if width == 128 or width == 100:
+        x[30:, 0] = 0.1                                    # one block: an ordinary maximum over tiny elements
+    x = x.to(dtype)
+    res = torch.zeros_like(x) if residual else None
+    r = None if res is None else res.to(DEV)[:, :width]
+    got = csa.NormRows(x.to(DEV)[:, :width], torch.full((width,), 0.5, dtype=dtype, device=DEV), r, eps=1e-6)()
+    torch.cuda.synchronize()
+    s, y = reference(x[:, :width], None, torch.full((width,), 0.5, dtype=dtype), True, 1e-6)
+    code, scale = got["codes"].cpu().double(), got["scale"].cpu().double()
+    assert torch.isfinite(code).all()
+    for j in range(scale.shape[1]):
+        part = y[:, 128 * j:128 * j + 128]
+        most = part.abs().amax(1)
+        want = torch.where(most > 0, (most / 448).clamp_min(2.0 ** -126), torch.ones_like(most))
+        assert ((scale[:, j] - want).abs() <= (Y_TOL + 2.0 ** -23) * want).all()
+        z = part / scale[:, j:j + 1]
+        tol = torch.maximum(z.abs() * 2.0 ** -4, torch.full_like(z, 2.0 ** -10)) + 2.0 ** -17 * z.abs() + 2.0 ** -23
+        assert ((code[:, 128 * j:128 * j + 128] - z).abs() <= tol).all()
