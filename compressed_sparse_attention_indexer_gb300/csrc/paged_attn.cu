@@ -52,6 +52,12 @@ namespace {
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kRescaleAbove = 8.f;  // the reference maximum moves when exceeded by this (log2 units)
+// E4M3: the softmax's sum has exponentials of its own in tiles with a V scale outside
+// 2^-kNear .. 2^kNear, and after one above them, which may have raised the reference.
+// What the joint exponentials lose elsewhere is below 2^-(126 - 2 kNear) of the
+// largest term.
+constexpr float kNear = 24.f;
+constexpr float kMinScale = 3.2311743e-27f;  // 2^-88: smaller V scales count so in the exponent
 
 template <int D, int MT, bool kFp8>
 struct PaShape {
@@ -98,6 +104,20 @@ __device__ __forceinline__ float fast_exp2(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;\n" : "=f"(y) : "f"(x));
   return y;
+}
+// The same with results below 2^-126 kept.
+__device__ __forceinline__ float tiny_exp2(float x) {
+  float y;
+  asm("ex2.approx.f32 %0, %1;\n" : "=f"(y) : "f"(x));
+  return y;
+}
+// A softmax's sum l moved to a reference maximum d higher (d <= 0 is added to the
+// exponents).  E4M3: a reference holds a row's V scale, so two of them may lie as far
+// apart as the scales, and l, which does not, is as much larger: in two factors, of
+// which neither vanishes.
+__device__ __forceinline__ float move_sum(float l, float d) {
+  const float f = fast_exp2(0.5f * d);
+  return l * f * f;
 }
 // Four E4M3 codes (low byte first) to two f16x2: every E4M3 value is an f16 value.
 __device__ __forceinline__ void e4m3x4_to_f16x2(uint32_t w, uint32_t& lo, uint32_t& hi) {
@@ -312,6 +332,9 @@ __global__ void __launch_bounds__(PaShape<D, MT, kFp8>::kThreads, 1)
   // thread 0's alone, kept out of everyone's registers: the list's cost, and the
   // current unit's place in it
   __shared__ int64_t total_sh, unit_at;
+  // E4M3, a warp's: its piece has had a V scale above 2^kNear (in a register: 388 us
+  // instead of 320 for 32 requests of 16384 .. 32768 rows, spills)
+  __shared__ volatile int high_sh[Sh::kWarps];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const uint32_t ring = smem_u32(smem_raw) + warp * (Sh::kStages * Sh::kWarpStage);
   const uint32_t qsm = smem_u32(smem_raw) + Sh::kRing;
@@ -486,6 +509,7 @@ __global__ void __launch_bounds__(PaShape<D, MT, kFp8>::kThreads, 1)
       continue;
     }
     if (step == seg_first) {
+      if (kFp8 && lane == 0) high_sh[warp] = 0;
       const __nv_bfloat16* q0 = static_cast<const __nv_bfloat16*>(a.q) + (int64_t)cu.b * a.S * a.q_stride;
       auto q_at = [&](int i) {  // query row i of the unit's kv head: token i / group, head h * group + i % group
         const int s = token_of(i);
@@ -555,19 +579,20 @@ __global__ void __launch_bounds__(PaShape<D, MT, kFp8>::kThreads, 1)
         // weight of a V row is p |v_scale|, so v_scale goes into the exponent
         // (lv) and the maximum is taken over both: the f16 weights then keep
         // their precision whatever the scales.  The softmax's own sum takes
-        // the factor out again (1 / |v_scale|), or, where a row's |lv| is so
-        // large that the weight may vanish while its part of the sum does not
-        // (`wide`), has an exponential of its own.  |v_scale| below 2^-100
-        // (zero) counts as 2^-100, the rest of it is kept in the sign factor.
+        // the factor out again (1 / |v_scale|), or, where the weight may vanish
+        // while its part of the sum does not (`wide`: see kNear), has an
+        // exponential of its own.  |v_scale| below kMinScale (zero) counts as
+        // kMinScale, the rest of it is kept in the sign factor.
         const uint32_t src = kt + 2 * kPer * Sh::kRowBytes + (lane % kPer) * 4;
         const float ks = lds_f32(src) * scale2, vs = lds_f32(src + kPer * 4);
-        const float lv = fast_log2(fmaxf(fabsf(vs), 7.8886091e-31f)), inv = fast_exp2(-lv);
+        const float lv = fast_log2(fmaxf(fabsf(vs), kMinScale)), inv = fast_exp2(-lv);
         // a v_scale that is no number reaches whoever sees the row by its exponent alone
         if (fabsf(vs) < INFINITY)
           sts_f4(rowsc + (lane % kPer) * 16, ks, lv, inv, vs * inv);
         else
           sts_f4(rowsc + (lane % kPer) * 16, ks, __uint_as_float(0x7fffffffu), 1.f, 1.f);
-        wide = __any_sync(0xffffffffu, !(fabsf(lv) <= 40.f));
+        wide = __any_sync(0xffffffffu, !(fabsf(lv) <= kNear) || high_sh[warp] != 0);
+        if (lv > kNear) high_sh[warp] = 1;   // for the tiles to come
         __syncwarp();
       }
       // ---- S = Q K^T: 16 MT query rows x kPer rows (n = 8 tiles)
@@ -696,8 +721,8 @@ __global__ void __launch_bounds__(PaShape<D, MT, kFp8>::kThreads, 1)
           for (int e = 0; e < 2; ++e) {
             if (top[e] > m[mt][e] + kRescaleAbove) {
               const float f = fast_exp2(m[mt][e] - top[e]);
+              l[mt][e] = kFp8 ? move_sum(l[mt][e], m[mt][e] - top[e]) : l[mt][e] * f;
               m[mt][e] = top[e];
-              l[mt][e] *= f;
 #pragma unroll
               for (int j = 0; j < D / 8; ++j) {
                 o[mt][j][2 * e] *= f;
@@ -731,7 +756,7 @@ __global__ void __launch_bounds__(PaShape<D, MT, kFp8>::kThreads, 1)
               for (int i = 0; i < 4; ++i) {
                 const float ref = m[mt][i >> 1] == -INFINITY ? 0.f : m[mt][i >> 1];
                 const float lv = lds_f32(rowsc + ((2 * x + n) * 8 + c * 2 + (i & 1)) * 16 + 4), t = s[mt][2 * x + n][i];
-                l[mt][i >> 1] += t == -INFINITY ? 0.f : fast_exp2(t - lv - ref);
+                l[mt][i >> 1] += t == -INFINITY ? 0.f : tiny_exp2(t - lv - ref);
               }
           }
 #pragma unroll
@@ -834,7 +859,10 @@ __global__ void __launch_bounds__(PaShape<D, MT, kFp8>::kThreads, 1)
               const int r = mt * 16 + g + 8 * e;
               const float m2 = sml[r], top = fmaxf(m[mt][e], m2), ref = top == -INFINITY ? 0.f : top;
               const float f1 = fast_exp2(m[mt][e] - ref), f2 = fast_exp2(m2 - ref);
-              l[mt][e] = l[mt][e] * f1 + sml[Sh::kRows + r] * f2;
+              if (kFp8)
+                l[mt][e] = move_sum(l[mt][e], m[mt][e] - ref) + move_sum(sml[Sh::kRows + r], m2 - ref);
+              else
+                l[mt][e] = l[mt][e] * f1 + sml[Sh::kRows + r] * f2;
               m[mt][e] = top;
               if constexpr (kFp8) {
 #pragma unroll
@@ -879,8 +907,8 @@ __global__ void __launch_bounds__(PaShape<D, MT, kFp8>::kThreads, 1)
         for (int i = 0; i < D / 32; ++i) acc[i] = 0.f;
 #pragma unroll
         for (int x = 0; x < Sh::kSlots; ++x) {
-          const float f = fast_exp2(ml[x * 2 * Sh::kRows + r] - ref);
-          sum += ml[x * 2 * Sh::kRows + Sh::kRows + r] * f;
+          const float d = ml[x * 2 * Sh::kRows + r] - ref, f = fast_exp2(d), ls = ml[x * 2 * Sh::kRows + Sh::kRows + r];
+          sum += kFp8 ? move_sum(ls, d) : ls * f;
 #pragma unroll
           for (int i = 0; i < D / 32; ++i)
             acc[i] += row_at[x * Sh::kSlotFloats + i] * f;
@@ -928,7 +956,7 @@ __global__ void __launch_bounds__(PaShape<D, MT, kFp8>::kThreads, 1)
 // Joins the pieces of the units cut between CTAs: block (x, y) does query row
 // y of the unit that starts in CTA x, its warps a part of the pieces each.
 constexpr int kJoinWarps = 8;
-template <int D>
+template <int D, bool kFp8>
 __global__ void __launch_bounds__(32 * kJoinWarps)
     paged_join_kernel(const PagedArgs a, int chunks, int rows, const float* __restrict__ part,
                       const PaJoin* __restrict__ joins) {
@@ -949,7 +977,7 @@ __global__ void __launch_bounds__(32 * kJoinWarps)
     const float m2 = src[D], l2 = src[D + 1];
     const float top = fmaxf(m, m2), ref = top == -INFINITY ? 0.f : top;
     const float f1 = fast_exp2(m - ref), f2 = fast_exp2(m2 - ref);
-    l = l * f1 + l2 * f2;
+    l = kFp8 ? move_sum(l, m - ref) + move_sum(l2, m2 - ref) : l * f1 + l2 * f2;
     m = top;
 #pragma unroll
     for (int x = 0; x < D / 32; ++x) acc[x] = acc[x] * f1 + src[lane + 32 * x] * f2;
@@ -964,7 +992,10 @@ __global__ void __launch_bounds__(32 * kJoinWarps)
   const float ref = top == -INFINITY ? 0.f : top;
   float sum = 0.f, f[kJoinWarps];
 #pragma unroll
-  for (int w = 0; w < kJoinWarps; ++w) f[w] = fast_exp2(sm_m[w] - ref), sum += sm_l[w] * f[w];
+  for (int w = 0; w < kJoinWarps; ++w) {
+    f[w] = fast_exp2(sm_m[w] - ref);
+    sum += kFp8 ? move_sum(sm_l[w], sm_m[w] - ref) : sm_l[w] * f[w];
+  }
   const bool any = sum > 0.f || sum != sum;
   const int s = i / group, hd = h * group + i - s * group;
   const int64_t tok = (int64_t)j.b * a.S + s;
@@ -997,7 +1028,7 @@ int launch_shape(const PagedArgs& a, int num_sms, cudaStream_t st, bool pdl) {
   const int span = a.win > 0 && a.win + a.S - 1 < a.max_len ? a.win + a.S - 1 + Sh::kTile - 1 : a.max_len;
   if (span <= Sh::kTile) return r;
   const int rows = qrows < Sh::kRows ? qrows : Sh::kRows;
-  const int r2 = launch_kernel(paged_join_kernel<D>, dim3(grid, rows), dim3(32 * kJoinWarps), 0, st, pdl, a, chunks,
+  const int r2 = launch_kernel(paged_join_kernel<D, kFp8>, dim3(grid, rows), dim3(32 * kJoinWarps), 0, st, pdl, a, chunks,
                                (int)Sh::kRows, (const float*)part, (const PaJoin*)joins);
   return r2 < 0 ? r2 : r + r2;
 }

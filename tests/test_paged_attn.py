@@ -458,3 +458,43 @@ def test_e4m3_queries_of_any_size(scale):
     torch.cuda.synchronize()
     k, v = (pool[x].cpu().view(torch.float8_e4m3fn).double() * pool[x + "_scale"].cpu().double()[..., None] for x in "kv")
     _check(got, _exact(q, k, v, lens, pool["table"].cpu(), block, 0, d ** -0.5))
+
+
+def _by_row(lens, h, hk, factor, seed, win=0):
+    """A run over E4M3 pools whose V scales take the factor of their row in the request (a tensor)."""
+    d, block = 128, 64
+    pool, _, _ = _pool(lens, hk, d, block, seed, True)
+    for i, n in enumerate(lens):
+        r = torch.arange(n)
+        rows = (pool["table"][i].cpu().long()[r // block] * block + r % block).to(DEV)
+        pool["v_scale"][rows] *= factor[:n, None].to(DEV)
+    q = torch.randn(len(lens), 1, h, d, generator=torch.Generator().manual_seed(seed + 1)).bfloat16()
+    got = csa.PagedAttention(q.to(DEV), pool["k"], pool["v"], torch.tensor(lens, dtype=torch.int32, device=DEV), win=win,
+                             table=pool["table"], block=block, k_scale=pool["k_scale"], v_scale=pool["v_scale"])()
+    torch.cuda.synchronize()
+    k, v = (pool[x].cpu().view(torch.float8_e4m3fn).double() * pool[x + "_scale"].cpu().double()[..., None] for x in "kv")
+    _check(got, _exact(q, k, v, lens, pool["table"].cpu(), block, win, d ** -0.5))
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("h", [6, 64])
+@pytest.mark.parametrize("few,many", [(0.0, 2.0 ** 40), (0.0, 2.0 ** 100), (2.0 ** -40, 2.0 ** 95), (2.0 ** -29, 2.0 ** 100)])
+@pytest.mark.parametrize("run", [32, 768, 5000])
+@pytest.mark.parametrize("first", [0, 1])
+def test_e4m3_scales_far_apart_between_warps_tiles_and_ctas(run, few, many, h, first):
+    # rows of tiny or zero V scales beside rows of huge ones, in runs that a warp, a tile or a CTA has to itself, in
+    # both orders: the softmax's sum keeps the part of either, whatever the V scales
+    _gpu()
+    r = torch.arange(10000)
+    _by_row([10000, 1500], h, 2, torch.where((r // run + first) % 2 == 0, few, many).float(), run)
+
+
+@pytest.mark.gpu
+def test_e4m3_one_huge_scale_among_ordinary_ones():
+    # a single row raises the reference: the rows after it, ordinary by themselves, stay in the sum
+    _gpu()
+    for at in (0, 40, 399):
+        for rest in (1.0, 2.0 ** -30):
+            f = torch.full((3000,), rest)
+            f[at] = 2.0 ** 100
+            _by_row([3000, 500], 6, 2, f, at)
