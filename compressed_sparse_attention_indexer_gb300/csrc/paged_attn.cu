@@ -30,7 +30,8 @@
 // more conversions per pair of codes: 765 instead of 548 us at the time for 32
 // requests of 16384 .. 32768 rows): a query row is scaled by a power of two to at most 2
 // (what then lies below 2^-14 is rounded to 2^-25 of the row's maximum), and the
-// weights include the V rows' scales.
+// weights include the V rows' scales (small ones are rounded to 2^-32 of the largest,
+// see kWeightTop).
 // Rows outside a query's range never reach its output: they are not loaded,
 // or their scores become -inf and, where another query of the same MMA sees
 // them, a NaN or infinity among their V rows is masked out (v_products_apart).
@@ -52,6 +53,11 @@ namespace {
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kRescaleAbove = 8.f;  // the reference maximum moves when exceeded by this (log2 units)
+// E4M3: the reference is set this far below the maximum, so that the f16 weights use
+// f16's range: up to 2^15, and off by at most 2^-25, 2^-32 of the largest, where they
+// are small.  (At the maximum itself rows below 2^-25 of it would vanish from the
+// output, however many, while the sum counts them.)
+constexpr float kWeightTop = 7.f;
 // E4M3: the softmax's sum has exponentials of its own in tiles with a V scale outside
 // 2^-kNear .. 2^kNear, and after one above them, which may have raised the reference.
 // What the joint exponentials lose elsewhere is below 2^-(126 - 2 kNear) of the
@@ -715,14 +721,16 @@ __global__ void __launch_bounds__(PaShape<D, MT, kFp8>::kThreads, 1)
           t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, 1));
           top[e] = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, 2));
         }
-        const bool grow = top[0] > m[mt][0] + kRescaleAbove || top[1] > m[mt][1] + kRescaleAbove;
+        // how far the maximum may be above the reference, and where a new reference is
+        constexpr float kAbove = kRescaleAbove + (kFp8 ? kWeightTop : 0.f), kBelow = kFp8 ? kWeightTop : 0.f;
+        const bool grow = top[0] > m[mt][0] + kAbove || top[1] > m[mt][1] + kAbove;
         if (__any_sync(0xffffffffu, grow)) {
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
-            if (top[e] > m[mt][e] + kRescaleAbove) {
-              const float f = fast_exp2(m[mt][e] - top[e]);
-              l[mt][e] = kFp8 ? move_sum(l[mt][e], m[mt][e] - top[e]) : l[mt][e] * f;
-              m[mt][e] = top[e];
+            if (top[e] > m[mt][e] + kAbove) {
+              const float to = top[e] - kBelow, f = fast_exp2(m[mt][e] - to);
+              l[mt][e] = kFp8 ? move_sum(l[mt][e], m[mt][e] - to) : l[mt][e] * f;
+              m[mt][e] = to;
 #pragma unroll
               for (int j = 0; j < D / 8; ++j) {
                 o[mt][j][2 * e] *= f;

@@ -498,3 +498,41 @@ def test_e4m3_one_huge_scale_among_ordinary_ones():
             f = torch.full((3000,), rest)
             f[at] = 2.0 ** 100
             _by_row([3000, 500], 6, 2, f, at)
+
+
+@pytest.mark.gpu
+def test_e4m3_many_rows_far_below_a_peak():
+    # a peak in every warp's first rows, whose V rows are zeros, and 2^23 rows that weigh 2^-25.25 of it: together 1.7 %
+    # of the output's weight.  A weight is an f16 number; one below 2^-25 of the largest must not vanish from the
+    # output while the softmax's sum counts it.  (Pages are shared: one page of tail rows, read over and over.)
+    _gpu()
+    hk, d, block, pages = 8, 128, 1024, 1 << 13
+    b = max(1, torch.cuda.get_device_properties(0).multi_processor_count // hk)
+    n = (pages + 1) * block
+    k = torch.zeros(2 * block, hk, d, dtype=torch.uint8, device=DEV)
+    k[0:384:32, :, 0] = 0x38                                 # 1.0
+    v = torch.randn(1, hk, d, generator=torch.Generator().manual_seed(1)).to(torch.float8_e4m3fn).view(torch.uint8)
+    v = v.to(DEV).expand(2 * block, hk, d).contiguous()
+    v[0:384:32] = 0
+    one = torch.ones(2 * block, hk, device=DEV)
+    q = torch.zeros(b, 1, hk, d, dtype=torch.bfloat16, device=DEV)
+    q[..., 0] = 1.0
+    scale = 25.25 * math.log(2)
+    table = torch.ones(b, pages + 1, dtype=torch.int32, device=DEV)
+    table[:, 0] = 0
+    got = csa.PagedAttention(q, k, v, torch.full((b,), n, dtype=torch.int32, device=DEV), table=table, block=block,
+                             k_scale=one, v_scale=one, scale=scale)()
+    torch.cuda.synchronize()
+    tail = (n - 12) * 2.0 ** -25.25
+    row = v[1].view(torch.float8_e4m3fn).double().cpu()
+    want = (row * tail / (12 + tail)).expand(b, 1, hk, d)
+    # A thread adds the weights of a quarter of its warp's rows, one after the other, to an fp32 sum: n / 48 terms with
+    # twelve warps, each addition off by 2^-24 of the sum at most, so the sum is within `most` of its value, lse too,
+    # and the output by that part of itself more than the rounded weights make it
+    most = n / 48 * 2.0 ** -24
+    assert ((got["lse"].cpu().double() - scale - math.log(12 + tail)).abs() <= most + LSE_TOL).all()
+    big = row.abs().amax(1)[:, None]
+    assert ((got["out"].cpu().double() - want).abs() <= 1.01 * U * (big + want.abs()) + 1.01 * most * want.abs()).all()
+    # and the tail is there (its weights, 2^-18.25 in f16, are off by 2^-6.75 of themselves at most): without it the
+    # output is zero
+    assert ((got["out"].cpu().double() - want).abs() <= 0.1 * want.abs() + 1e-4).all()
