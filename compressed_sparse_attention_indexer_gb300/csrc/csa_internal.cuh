@@ -415,6 +415,7 @@ struct PagedArgs {
   int* status;
   void* workspace;
 };
+constexpr int kPagedMaxLen = 1 << 30;   // csa_paged.max_len at most
 size_t paged_attn_workspace(int dim, int num_sms);
 int launch_paged_attn(const PagedArgs& a, bool fp8, int num_sms, cudaStream_t st, bool pdl);
 int norm_max_width(int dtype);

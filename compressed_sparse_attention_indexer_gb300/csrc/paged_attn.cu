@@ -43,6 +43,8 @@
 // the issue slots, HBM neither); 48 x 4 tokens, 16 / 8 heads of 64, in
 // 64 us (4.8 TB/s); one request of 1023 rows in 8.2 us (launch, two rounds of
 // dependent loads, one tile, the join of the warps and of the CTAs).
+#include <limits>
+
 #include "csa_internal.cuh"
 #include "ptx.cuh"
 
@@ -64,6 +66,8 @@ constexpr float kWeightTop = 7.f;
 // largest term.
 constexpr float kNear = 24.f;
 constexpr float kMinScale = 3.2311743e-27f;  // 2^-88: smaller V scales count so in the exponent
+
+using PaCost = uint32_t;  // of the units of one kv head and chunk of as many requests as a block has threads
 
 template <int D, int MT, bool kFp8>
 struct PaShape {
@@ -96,6 +100,8 @@ struct PaShape {
   static constexpr int kRing = kStages * kWarps * kWarpStage;
   static constexpr int kSmem = kRing + kQBytes + kSlotBytes + kWarps * kScaleBytes;
   static_assert(kStages >= 2, "no room for two stages");
+  // the costs of a block's scan (a request per thread) add up in 32 bits
+  static_assert((uint64_t)kThreads * (kPagedMaxLen / kTile + 2) <= std::numeric_limits<PaCost>::max(), "sum of costs");
 };
 
 // What a CTA leaves for the join of the unit that starts in it and goes on in
@@ -333,7 +339,7 @@ __global__ void __launch_bounds__(PaShape<D, MT, kFp8>::kThreads, 1)
   using Sh = PaShape<D, MT, kFp8>;
   constexpr int kTile = Sh::kTile, kPer = Sh::kPer, kGroups = Sh::kGroups;
   extern __shared__ __align__(128) uint8_t smem_raw[];
-  __shared__ int scan_tmp[33];
+  __shared__ PaCost scan_tmp[33];
   __shared__ Cut cut_sh[2];
   // thread 0's alone, kept out of everyone's registers: the list's cost, and the
   // current unit's place in it
@@ -359,7 +365,8 @@ __global__ void __launch_bounds__(PaShape<D, MT, kFp8>::kThreads, 1)
   // more for its start and end), with the cuts moved to the next whole tile
   const bool once = a.B <= Sh::kThreads;   // one request per thread: scanned once
   Span<kTile> sp;
-  int n = 0, sum, ahead = 0, len = 0;
+  PaCost n = 0, sum, ahead = 0;
+  int len = 0;
   int64_t total = 0;
   for (int b0 = 0; b0 < a.B; b0 += Sh::kThreads) {
     n = 0;
@@ -383,13 +390,13 @@ __global__ void __launch_bounds__(PaShape<D, MT, kFp8>::kThreads, 1)
     }
     if (blockIdx.x == 0 && a.status && b0 + tid < a.B && (len < 0 || len > a.max_len))
       set_status(a.status, kStatusBadIndex);
-    const int64_t p = (before + ahead) * units;
+    const int64_t p = (before + (int64_t)ahead) * units;
 #pragma unroll
     for (int e = 0; e < 2; ++e)
       // (the list's end belongs to its last request)
       if (n > 0 && p <= cut[e] && (cut[e] < p + (int64_t)n * units || b0 + tid == a.B - 1)) {
         const int64_t at = cut[e] - p;
-        const int unit = at < (1u << 31) ? (int)((uint32_t)at / (uint32_t)n) : (int)(at / n);
+        const int unit = at < (1u << 31) ? (int)((uint32_t)at / n) : (int)(at / n);
         const int x = (int)(at - (int64_t)unit * n);
         cut_sh[e].b = b0 + tid;
         cut_sh[e].unit = unit;

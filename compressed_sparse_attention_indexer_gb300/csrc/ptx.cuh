@@ -76,34 +76,35 @@ __device__ __forceinline__ void named_barrier_sync(int id, int count) {
   asm volatile("bar.sync %0, %1;\n" ::"r"(id), "r"(count) : "memory");
 }
 
-// Block-wide exclusive scan of one int per thread (blockDim.x a multiple of
-// 32, <= 1024).  `warp_tmp` holds >= 33 ints of shared memory.  Returns the
+// Block-wide exclusive scan of one integer per thread (blockDim.x a multiple of
+// 32, <= 1024).  `warp_tmp` holds >= 33 of them in shared memory.  Returns the
 // exclusive prefix; *total receives the block sum.  Contains __syncthreads.
-__device__ __forceinline__ int block_exclusive_scan(int v, int* warp_tmp, int* total) {
+template <typename T>
+__device__ __forceinline__ T block_exclusive_scan(T v, T* warp_tmp, T* total) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int nwarps = blockDim.x >> 5;
-  int x = v;
+  T x = v;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
-    int y = __shfl_up_sync(0xffffffffu, x, o);
+    T y = __shfl_up_sync(0xffffffffu, x, o);
     if (lane >= o) x += y;
   }
   if (lane == 31) warp_tmp[warp] = x;
   __syncthreads();
   if (warp == 0) {
-    int t = lane < nwarps ? warp_tmp[lane] : 0;
+    T t = lane < nwarps ? warp_tmp[lane] : 0;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-      int y = __shfl_up_sync(0xffffffffu, t, o);
+      T y = __shfl_up_sync(0xffffffffu, t, o);
       if (lane >= o) t += y;
     }
     if (lane < nwarps) warp_tmp[lane] = t;  // inclusive warp prefix
     if (lane == 31) warp_tmp[32] = t;
   }
   __syncthreads();
-  int base = warp > 0 ? warp_tmp[warp - 1] : 0;
+  T base = warp > 0 ? warp_tmp[warp - 1] : 0;
   *total = warp_tmp[32];
-  int r = base + x - v;
+  T r = base + x - v;
   __syncthreads();
   return r;
 }
