@@ -315,8 +315,9 @@ CSA_API int csa_norm_rows(const csa_norm *a, void *stream);
  * a [M, K] (activations, as csa_norm_rows writes them: a scale per row and 128
  * elements), b [N, K] (weights, one row per output element: a scale per 128
  * rows and 128 elements), block kb = elements 128 kb .. 128 kb + 127, the last
- * one may be shorter.  The sums are fp32, out is rounded once.  a_scale and
- * b_scale may be any fp32 numbers. */
+ * one may be shorter.  The sums are fp32, out is rounded once.  A block's two scales
+ * are multiplied first: a_scale and b_scale may be any fp32 numbers whose product is
+ * zero or between 2^-126 and 2^128 in size. */
 typedef struct {
     int32_t M, N, K;          /* M = 0 or N = 0: a no-op; K >= 1; at most 2^30      */
     int32_t out_dtype;        /* CSA_DTYPE_BF16 or CSA_DTYPE_F32                    */

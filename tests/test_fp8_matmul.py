@@ -309,3 +309,23 @@ def test_tiles_in_one_turn_of_the_sms_and_in_several(m, n, k, dtype):
     padded = csa.Fp8Matmul(a, sa, b, sb, out_dtype=dtype)()
     torch.cuda.synchronize()
     assert torch.equal(got, padded)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("m", [3, 40, 200])
+@pytest.mark.parametrize("ea,eb", [(-63, -63), (-100, -26), (-26, -100), (60, 40), (100, 0), (-20, 120)])
+def test_scales_at_the_ends_of_the_range(m, ea, eb):
+    # the product of a block's two scales at the lowest normal number, and so large that the sums (up to
+    # 448^2 x 1024 < 2^28) just stay numbers.  At the low end a block's sum is about 2^13 and its bound above 2^-130,
+    # far above fp32's last place there (2^-149)
+    _gpu()
+    n, k = 300, 1024
+    g = torch.Generator(device=DEV).manual_seed(m)
+    a, b = _codes(m, k, g), _codes(n, k, g)
+    sign = lambda *s: torch.randint(0, 2, s, generator=g, device=DEV).float() * 2 - 1
+    sa, sb = sign(m, 8) * 2.0 ** ea, sign(3, 8) * 2.0 ** eb
+    sa[:, 2], sb[1, 3] = 0, 0
+    got = csa.Fp8Matmul(a, sa, b, sb, out_dtype=torch.float32)()
+    torch.cuda.synchronize()
+    assert torch.isfinite(got).all()
+    _check(got, a, sa, b, sb, (m, ea, eb))
