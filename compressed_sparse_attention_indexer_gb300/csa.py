@@ -309,6 +309,13 @@ def _bad(msg: str):
     raise CsaError(CSA_ERR_INVALID_ARG, msg)
 
 
+def _int32(**sizes):
+    """Refuses sizes that the C structs' 32-bit fields would silently cut."""
+    for name, v in sizes.items():
+        if not -2 ** 31 <= int(v) < 2 ** 31:
+            raise CsaError(CSA_ERR_UNSUPPORTED, f"{name} = {v} does not fit 32 bits")
+
+
 def _rows2d(name: str, t, n: int, width: int, dtype=None):
     """A matrix [n, width] whose rows are contiguous (any row stride)."""
     if t.dim() != 2 or tuple(t.shape) != (n, width):
@@ -370,6 +377,7 @@ class NormRows(_Operator):
         if x.dim() != 2:
             _bad("x must have two dimensions")
         n, width = (int(v) for v in x.shape)
+        _int32(n=n, width=width)
         _rows2d("x", x, n, width)
         if residual is not None:
             _rows2d("residual", residual, n, width, x.dtype)
@@ -447,6 +455,7 @@ class Fp8Matmul(_Operator):
             if t.dim() != 2 or str(t.dtype) not in _E4M3_DTYPES:
                 _bad(f"{name} must be a matrix of uint8 or float8_e4m3fn")
         (m, k), n = (int(v) for v in a.shape), int(b.shape[0])
+        _int32(M=m, N=n, K=k)
         kb = -(-k // 128)
         _rows2d("a", a, m, k)
         _rows2d("b", b, n, k)
@@ -494,6 +503,7 @@ class PagedAttention(_Operator):
             _bad("q must be [B, S, heads, dim] and k, v [rows, kv_heads, dim]")
         b, s, heads, dim = (int(x) for x in q.shape)
         rows, kv_heads = int(k.shape[0]), int(k.shape[1])
+        _int32(B=b, S=s, heads=heads, kv_heads=kv_heads, dim=dim, win=win, block=block)
         if out is None:
             out = torch.empty(b, s, heads, dim, dtype=q.dtype, device=q.device)
         strides = []
@@ -536,6 +546,7 @@ class PagedAttention(_Operator):
                 _bad(f"off must be contiguous int64 of shape ({b},)")
             if max_len is None:
                 _bad("max_len is needed with off")
+        _int32(max_len=max_len, table_stride=0 if table is None else table.shape[1])
         if lse is True:
             lse = torch.empty(b, s, heads, dtype=torch.float32, device=q.device)
         elif lse is False:

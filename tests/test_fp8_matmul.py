@@ -329,3 +329,13 @@ def test_scales_at_the_ends_of_the_range(m, ea, eb):
     torch.cuda.synchronize()
     assert torch.isfinite(got).all()
     _check(got, a, sa, b, sb, (m, ea, eb))
+
+
+def test_sizes_that_do_not_fit_32_bits_are_refused():
+    # (the C struct's fields have 32 bits: 2^32 + 16 rows would arrive as 16)
+    big = 2 ** 32 + 128
+    t = lambda *s, d=torch.uint8: torch.empty(s, dtype=d, device="meta")
+    for m, n, k in ((big, 128, 128), (128, big, 128), (128, 128, big)):
+        kb = -(-k // 128)
+        with pytest.raises(csa.CsaError, match="32 bits"):
+            csa.Fp8Matmul(t(m, k), t(m, kb, d=torch.float32), t(n, k), t(-(-n // 128), kb, d=torch.float32))

@@ -440,3 +440,10 @@ def test_codes_of_tiny_blocks(width, residual, dtype, size):
         z = part / scale[:, j:j + 1]
         tol = torch.maximum(z.abs() * 2.0 ** -4, torch.full_like(z, 2.0 ** -10)) + 2.0 ** -17 * z.abs() + 2.0 ** -23
         assert ((code[:, 128 * j:128 * j + 128] - z).abs() <= tol).all()
+
+
+def test_sizes_that_do_not_fit_32_bits_are_refused():
+    # (the C struct's fields have 32 bits: 2^32 + 4 rows would arrive as 4)
+    for shape in ((2 ** 32 + 4, 256), (4, 2 ** 32 + 256)):
+        with pytest.raises(csa.CsaError, match="32 bits"):
+            csa.NormRows(torch.empty(shape, dtype=torch.bfloat16, device="meta"))

@@ -536,3 +536,20 @@ def test_e4m3_many_rows_far_below_a_peak():
     # and the tail is there (its weights, 2^-18.25 in f16, are off by 2^-6.75 of themselves at most): without it the
     # output is zero
     assert ((got["out"].cpu().double() - want).abs() <= 0.1 * want.abs() + 1e-4).all()
+
+
+def test_sizes_that_do_not_fit_32_bits_are_refused():
+    # (the C struct's fields have 32 bits: 2^32 + 64 would arrive as 64)
+    q = torch.zeros(1, 1, 4, 128, dtype=torch.bfloat16)
+    k = torch.zeros(64, 2, 128, dtype=torch.bfloat16)
+    n, t = torch.zeros(1, dtype=torch.int32), torch.zeros(1, 1, dtype=torch.int32)
+    for kw in (dict(table=t, block=2 ** 32 + 64, max_len=64), dict(table=t, block=64, win=2 ** 32 + 1),
+               dict(table=t, block=64, max_len=2 ** 32 + 64),
+               dict(table=torch.zeros(1, 1 << 20, dtype=torch.int32), block=4096)):    # what the table holds: 2^32
+        with pytest.raises(csa.CsaError, match="32 bits"):
+            csa.PagedAttention(q, k, k, n, **kw)
+    b = 2 ** 32 + 1
+    many = [torch.empty(s, dtype=d, device="meta") for s, d in (((b, 1, 4, 128), torch.bfloat16), ((64, 2, 128), torch.bfloat16),
+                                                                ((b,), torch.int32), ((b, 1), torch.int32))]
+    with pytest.raises(csa.CsaError, match="32 bits"):
+        csa.PagedAttention(many[0], many[1], many[1], many[2], table=many[3], block=64)
