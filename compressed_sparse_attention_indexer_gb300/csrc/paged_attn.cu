@@ -158,7 +158,7 @@ __device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
 // The power of two in (max / 2, max], 1 for zero, subnormal and non-finite max.
 __device__ __forceinline__ float pow2_below(float max) {
   const uint32_t e = __float_as_uint(max) >> 23;
-  return e >= 1 && e <= 253 ? __uint_as_float(e << 23) : 1.f;
+  return e >= 1 && e <= 254 ? __uint_as_float(e << 23) : 1.f;
 }
 // Two bf16 times inv (a power of two) as f16x2.
 __device__ __forceinline__ uint32_t bf16x2_to_f16x2(uint32_t v, float inv) {

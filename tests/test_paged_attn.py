@@ -553,3 +553,23 @@ def test_sizes_that_do_not_fit_32_bits_are_refused():
                                                                 ((b,), torch.int32), ((b, 1), torch.int32))]
     with pytest.raises(csa.CsaError, match="32 bits"):
         csa.PagedAttention(many[0], many[1], many[1], many[2], table=many[3], block=64)
+
+
+@pytest.mark.gpu
+def test_e4m3_queries_at_the_end_of_the_range():
+    # |q| from 2^127 on: the power of two taken out of the row is 2^127
+    _gpu()
+    n, h, hk, d, block = 200, 4, 2, 128, 64
+    g = torch.Generator().manual_seed(5)
+    k = torch.randn(256, hk, d, generator=g) * 2.0 ** -6
+    k, v = (t.to(torch.float8_e4m3fn) for t in (k, torch.randn(256, hk, d, generator=g)))
+    ks, vs = torch.full((256, hk), 2.0 ** -115), torch.ones(256, hk)
+    q = torch.zeros(1, 1, h, d)
+    q[..., 0] = torch.tensor([1.8e38, 2.5e38, -3e38, 3.38e38])
+    q = q.bfloat16()
+    table = torch.arange(4, dtype=torch.int32)[None]
+    got = csa.PagedAttention(q.to(DEV), k.view(torch.uint8).to(DEV), v.view(torch.uint8).to(DEV),
+                             torch.tensor([n], dtype=torch.int32, device=DEV), table=table.to(DEV), block=block,
+                             k_scale=ks.to(DEV), v_scale=vs.to(DEV))()
+    torch.cuda.synchronize()
+    _check(got, _exact(q, k.double() * 2.0 ** -115, v.double(), [n], table, block, 0, d ** -0.5))
