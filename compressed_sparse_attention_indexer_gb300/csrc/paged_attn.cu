@@ -290,15 +290,17 @@ __device__ __forceinline__ void v_products(uint32_t vt, int lane, F&& pv) {
 }
 
 // O += P V where a V row that some token of the warp's tile does not see holds
-// a NaN or an infinity: a pass per token with its own rows kept and its own
-// query rows taken.  Out of line, on copies of o and pf: rare, and the common
-// path keeps its registers.
+// a NaN or an infinity: a pass per token that the product's query rows may
+// be of (sq, ascending; S: no query row) with its own rows kept and its own query rows taken.
+// Out of line, on copies of o and pf: rare, and the common path keeps its registers.
 template <int D, int MT, bool kFp8>
 __device__ __noinline__ void v_products_apart(float* o, const uint32_t* pf, const int* sq, uint32_t vt, int lane, int base,
                                               int p_first, int S, int win) {
   using Sh = PaShape<D, MT, kFp8>;
   const int c = lane & 3;
-  for (int t = 0; t < S; ++t) {
+  int t = __shfl_sync(0xffffffffu, sq[0], 0);
+  if (S > t + 16 * MT) S = t + 16 * MT;
+  for (; t < S; ++t) {
     const int last = p_first + t;
     uint32_t keep[2 * Sh::kGroups];
 #pragma unroll
@@ -335,7 +337,7 @@ __device__ __forceinline__ int64_t split_at(int64_t total, int i, int parts) {
 
 template <int D, int MT, bool kFp8>
 __global__ void __launch_bounds__(PaShape<D, MT, kFp8>::kThreads, 1)
-    paged_attn_kernel(const PagedArgs a, int chunks, float* __restrict__ part, PaJoin* __restrict__ joins) {
+    paged_attn_kernel(const PagedArgs a, int chunks, int units, float* __restrict__ part, PaJoin* __restrict__ joins) {
   using Sh = PaShape<D, MT, kFp8>;
   constexpr int kTile = Sh::kTile, kPer = Sh::kPer, kGroups = Sh::kGroups;
   extern __shared__ __align__(128) uint8_t smem_raw[];
@@ -357,7 +359,6 @@ __global__ void __launch_bounds__(PaShape<D, MT, kFp8>::kThreads, 1)
   // i / group for 0 <= i < S * heads <= 2^20 (off by less than half of 1 / group)
   auto token_of = [&](int i) { return (int)(((float)i + 0.5f) * per_group); };
   const int qrows = a.S * group;                    // query rows per kv head
-  const int units = a.kv_heads * chunks;
   pdl_wait();
   pdl_trigger();
 
@@ -1037,7 +1038,7 @@ int launch_shape(const PagedArgs& a, int num_sms, cudaStream_t st, bool pdl) {
   // at most the tiles that the bound on the lengths allows
   const int64_t tiles = (int64_t)a.B * a.kv_heads * chunks * ((a.max_len + Sh::kTile - 1) / Sh::kTile + 1);
   const int grid = tiles < num_sms ? (int)tiles : num_sms;
-  const int r = launch_kernel(kern, dim3(grid), dim3(Sh::kThreads), Sh::kSmem, st, pdl, a, chunks, part, joins);
+  const int r = launch_kernel(kern, dim3(grid), dim3(Sh::kThreads), Sh::kSmem, st, pdl, a, chunks, a.kv_heads * chunks, part, joins);
   if (r < 0) return r;
   // a unit of one tile is never cut
   const int span = a.win > 0 && a.win + a.S - 1 < a.max_len ? a.win + a.S - 1 + Sh::kTile - 1 : a.max_len;

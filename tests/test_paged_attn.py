@@ -573,3 +573,35 @@ def test_e4m3_queries_at_the_end_of_the_range():
                              k_scale=ks.to(DEV), v_scale=vs.to(DEV))()
     torch.cuda.synchronize()
     _check(got, _exact(q, k.double() * 2.0 ** -115, v.double(), [n], table, block, 0, d ** -0.5))
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("fp8", [False, True])
+def test_nan_rows_in_a_long_chunk_cost_passes_for_the_tokens_of_one_product_only(fp8):
+    # a NaN among the V rows of a tile that tokens see in part: a pass for each token whose queries are in the product
+    # (32 at most, some 32 times a tile's time), not for each of the chunk's 4096
+    _gpu()
+    s, h, d, block = 4096, 2, 128, 64
+    pool, _, _ = _pool([s], 2, d, block, 12, fp8)
+    q = torch.randn(1, s, h, d, generator=torch.Generator().manual_seed(1)).bfloat16().to(DEV)
+    n = torch.tensor([s], dtype=torch.int32, device=DEV)
+    op = csa.PagedAttention(q, pool["k"], pool["v"], n, table=pool["table"], block=block, k_scale=pool.get("k_scale"),
+                            v_scale=pool.get("v_scale"))
+
+    def timed():
+        t0, t1 = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
+        t0.record()
+        op()
+        t1.record()
+        torch.cuda.synchronize()
+        return t0.elapsed_time(t1)
+
+    timed()
+    clean, base = {x: t.clone() for x, t in op().items()}, max(timed(), timed())
+    for r in range(s - 64, s, 16):                       # one in each 16 rows at the end: most tokens do not see them
+        row = int(pool["table"][0, r // block]) * block + r % block
+        pool["v"].view(torch.uint8 if fp8 else torch.int16)[row] = 0x7F if fp8 else 0x7FC0
+    got, took = op(), timed()
+    assert torch.equal(got["out"][:, :s - 64], clean["out"][:, :s - 64]) and torch.equal(got["lse"], clean["lse"])
+    assert torch.isnan(got["out"][:, s - 64:]).all()
+    assert took <= 60 * base + 1, (took, base)
