@@ -887,6 +887,8 @@ int csa_paged_attn(const csa_paged* a, void* stream) {
   if (a->B < 0 || a->S < 1) return fail(CSA_ERR_INVALID_ARG, "need B >= 0 and S >= 1");
   if (a->heads < 1 || a->kv_heads < 1 || a->heads % a->kv_heads != 0)
     return fail(CSA_ERR_INVALID_ARG, "heads must be a positive multiple of kv_heads");
+  if (isnan(a->softmax_scale) || a->softmax_scale == INFINITY)
+    return fail(CSA_ERR_INVALID_ARG, "softmax_scale must be a finite number (<= 0: 1 / sqrt(dim))");
   if (a->win < 0 || a->max_len < 0) return fail(CSA_ERR_INVALID_ARG, "need win >= 0 and max_len >= 0");
   if (a->max_len > csa::kPagedMaxLen || a->S > (1 << 16) || (int64_t)a->S * a->heads > (1 << 20))
     return fail(CSA_ERR_UNSUPPORTED, "max_len above 2^30, S above 2^16 or S * heads above 2^20");

@@ -605,3 +605,10 @@ def test_nan_rows_in_a_long_chunk_cost_passes_for_the_tokens_of_one_product_only
     assert torch.equal(got["out"][:, :s - 64], clean["out"][:, :s - 64]) and torch.equal(got["lse"], clean["lse"])
     assert torch.isnan(got["out"][:, s - 64:]).all()
     assert took <= 60 * base + 1, (took, base)
+
+
+@pytest.mark.parametrize("scale", [float("nan"), float("inf")])
+def test_a_softmax_scale_that_is_no_number_is_refused(L, scale):
+    # (a NaN would be taken for "not given", 1 / sqrt(dim))
+    assert _call(L, softmax_scale=scale) == csa.CSA_ERR_INVALID_ARG
+    assert "softmax_scale" in csa.last_error()
