@@ -555,6 +555,8 @@ class PagedAttention(_Operator):
                                 not lse.is_contiguous()):
             _bad(f"lse must be contiguous float32 of shape ({b}, {s}, {heads})")
         _status_word(status)
+        if workspace is not None and not workspace.is_contiguous():
+            _bad("workspace must be contiguous")
         if workspace is None and q.is_cuda:
             with torch.cuda.device(q.device):
                 workspace = torch.empty(paged_attn_workspace(dim), dtype=torch.uint8, device=q.device)

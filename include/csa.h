@@ -382,7 +382,8 @@ typedef struct {
 } csa_paged;
 
 /* q, k, v and out start on 16-byte boundaries and their strides keep the rows
- * there; pool rows lie at most 2 GB apart.  |v_scale| is at most 2^100; one that is
+ * there; pool rows lie at most 2 GB apart; out, lse and the workspace must not
+ * overlap an input.  |v_scale| is at most 2^100; one that is
  * infinite or NaN makes out and lse NaN for the queries that see its row.  Returns
  * CSA_ERR_INVALID_ARG, CSA_ERR_UNSUPPORTED (dim, kv_dtype, max_len above 2^30,
  * S above 2^16, S * heads above 2^20) or CSA_ERR_WORKSPACE (workspace_bytes too

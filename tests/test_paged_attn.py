@@ -612,3 +612,13 @@ def test_a_softmax_scale_that_is_no_number_is_refused(L, scale):
     # (a NaN would be taken for "not given", 1 / sqrt(dim))
     assert _call(L, softmax_scale=scale) == csa.CSA_ERR_INVALID_ARG
     assert "softmax_scale" in csa.last_error()
+
+
+def test_a_workspace_that_is_no_plain_memory_is_refused():
+    # its size is taken from its elements: with gaps or repeated ones that is not the memory behind it
+    q, k = torch.zeros(1, 1, 4, 128, dtype=torch.bfloat16), torch.zeros(64, 2, 128, dtype=torch.bfloat16)
+    n, t = torch.zeros(1, dtype=torch.int32), torch.zeros(1, 1, dtype=torch.int32)
+    for ws in (torch.empty(1, dtype=torch.uint8).expand(1 << 24), torch.empty(1 << 12, dtype=torch.uint8)[::2]):
+        with pytest.raises(csa.CsaError, match="workspace"):
+            csa.PagedAttention(q, k, k, n, table=t, block=64, workspace=ws)
+    csa.PagedAttention(q, k, k, n, table=t, block=64, workspace=torch.empty(1 << 12, dtype=torch.uint8))
