@@ -25,16 +25,16 @@
 // so that few tiles still keep every SM loading; no workspace, no atomics.
 // Every mbarrier wait is bounded; one that gives up sets bit 1 of the status.
 //
-// Measured (GB300): 8192 x 8192 x 7168 in 452 us (2.13 PFLOP/s, 1785 MHz under
-// the power cap; 406 us in a burst), 1024 x 4096 x 4096 in 21.5 us, 64 x 36864 x
-// 1536 in 14.1 us (4.4 TB/s), 331 x 1100 x 7000 in 10.5 us, 1 x 8192 x 1536 in
-// 6.0 us.  What bounds large tiles: the two 256-column TMEM buffers, each held
-// for its MMAs (512 cycles) and its way through the epilogue; in variants that
-// left work out, 385 us without the TMEM reads, 405 without the copies, 371
-// without either (one issuing thread).  CTA pairs (256 x 256 tiles, half the
-// copies per SM) came to 470 us: the longer way to the other CTA and back per
-// buffer costs more than the copies saved.  Small products: launch, the first
-// stage's latency (0.8 us) and the output's way out (1.2 us) beside the stream.
+// Measured (GB300): 8192 x 8192 x 7168 in 456 .. 464 us (2.1 PFLOP/s, 1785 MHz under
+// the power cap), 1024 x 4096 x 4096 in 22.8 us, 64 x 36864 x 1536 in 14.1 us
+// (4.4 TB/s), 331 x 1100 x 7000 in 10.3 us, 1 x 8192 x 1536 in 5.8 us.  What bounds
+// large tiles: about 1030 cycles per block of 256 columns and 740 of 128, of which
+// the MMAs take about 290 per 128 columns; the other 450 are not explained.  It is
+// not the copies or the epilogue for the larger part: with one issuing thread 406 us
+// in a burst, 385 without the TMEM reads, 405 without the copies, 371 without
+// either.  CTA pairs (256 x 256 tiles, half the copies per SM) came to 470 us.
+// Small products: launch, the first stage's latency (0.8 us) and the output's way
+// out (1.2 us) beside the stream.
 #include <cudaTypedefs.h>
 
 #include "csa_internal.cuh"
@@ -358,8 +358,8 @@ __global__ void __launch_bounds__(MmShape<NT, kSwap>::kThreads, MmShape<NT, kSwa
   } else if (warp < Sh::kAux) {
     // MMA issuers, the blocks in turn: a block's chain in its thread (two
     // barriers, four MMAs, a commit: 700 cycles measured) is longer than its
-    // MMAs (280 with 128 columns).  One issuer / two: 1024 x 4096 x 4096 26.9 /
-    // 23.9 us, 331 x 1100 x 7000 11.5 / 10.5.
+    // MMAs (280 with 128 columns).  One issuer / two, when the second came:
+    // 1024 x 4096 x 4096 26.9 / 23.9 us, 331 x 1100 x 7000 11.5 / 10.5.
     if (lane == 0) {
       constexpr int kBy = Sh::kIssuers;
       struct {

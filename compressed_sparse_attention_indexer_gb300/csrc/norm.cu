@@ -17,9 +17,11 @@
 // has a fixed order.
 //
 // Measured (GB300): 16384 x 7168 bf16, residual, both outputs, in 166 us
-// (6.4 TB/s, 94% of the measured copy rate); 131072 x 128 to codes in 11.5 us
-// (4.4 TB/s: bound by instructions per row); 4097 x 1000 fp32 to codes in
-// 6.3 us; one row of 4096 in 3.0 us (a launch).
+// (6.4 TB/s, 94% of the measured copy rate); 131072 x 128 to codes in 11.8 us
+// (4.3 TB/s: bound by instructions per row); 4097 x 1000 fp32 to codes in
+// 6.3 us; one row of 4096 in 2.9 us (a launch).  Wide rows to codes without a
+// residual are bound by each row's dependent chain, not by HBM: 10000 x 4096 bf16
+// 32 us (3.8 TB/s), 80023 x 761 bf16 50 us, 24615 x 1497 fp32 53 us.
 #include <cuda_fp8.h>
 
 #include "csa_internal.cuh"
@@ -373,7 +375,7 @@ __global__ void __launch_bounds__(kNormMaxThreads, VPT == 1 ? 2 : 1) norm_kernel
 // Sixteen (bf16) or 32 (fp32) lanes per row and kNarrowRows rows per thread,
 // their chains interleaved: with a row per thread and step the kernel above
 // spends 199 instructions per warp and step, most of them not on elements
-// (131072 x 128 bf16 with codes: 15.5 us, this one 11.5;
+// (131072 x 128 bf16 with codes: 15.5 us, this one 11.5 at the time, 11.8 now;
 // two rows 13.0, one row 14.8).  Two elements per
 // multiply (f32x2); both reductions run together.
 constexpr int kNarrowRows = 4, kNarrowThreads = 256, kNarrowBlocks = 2;

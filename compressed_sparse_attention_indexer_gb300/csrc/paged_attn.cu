@@ -37,12 +37,16 @@
 // them, a NaN or infinity among their V rows is masked out (v_products_apart).
 //
 // Measured (GB300): 64 requests of 1024 .. 65536 rows, 32 / 4 heads of 128, bf16,
-// in 675 .. 700 us (6.7 .. 7.0 TB/s, the copy rate); 32 of 16384 .. 32768 rows,
-// 64 / 8 heads, E4M3, in 311 us (5.2 TB/s; about 820 instructions
+// in 685 us (6.9 TB/s, the copy rate); 32 of 16384 .. 32768 rows,
+// 64 / 8 heads, E4M3, in 315 us (5.2 TB/s; about 820 instructions
 // per 32 rows of 256 bytes in three warps per scheduler, a long chain each: 43% of
 // the issue slots, HBM neither); 48 x 4 tokens, 16 / 8 heads of 64, in
-// 64 us (4.8 TB/s); one request of 1023 rows in 8.2 us (launch, two rounds of
-// dependent loads, one tile, the join of the warps and of the CTAs).
+// 63 us (4.9 TB/s); one request of 1023 rows in 8.1 us (launch, two rounds of
+// dependent loads, one tile, the join of the warps and of the CTAs); 32 of 4096 ..
+// 16384 rows, 16 / 4 heads of 256, in 203 us (6.1 TB/s).  Far from their floors: a
+// prompt (4096 tokens of 4096 rows, 32 / 8 heads: 1963 us against 73; every chunk of
+// query rows streams all rows, windows or not) and many short units (64 tokens with a
+// window of 128 rows: 20 us against 5).
 #include <limits>
 
 #include "csa_internal.cuh"
