@@ -24,7 +24,7 @@ EXPORTS = ("csa_decode_create", "csa_decode_destroy", "csa_indexer_topk", "csa_s
            "csa_get_status", "csa_last_error", "csa_last_launch_count", "csa_abi_version",
            "csa_profile_enable", "csa_profile_read", "csa_indexer_topk_static", "csa_cache_writeback",
            "csa_debug_set_wait_polls", "csa_norm_rows", "csa_fp8_matmul",
-           "csa_paged_attn", "csa_paged_attn_workspace")
+           "csa_paged_attn", "csa_paged_attn_workspace", "csa_qk_rope", "csa_kv_append")
 STAGES = ("plan", "indexer", "topk", "attention")
 
 
@@ -84,6 +84,26 @@ class CPaged(ctypes.Structure):
         ("out", _P), ("out_stride", _I64), ("lse", _P), ("status", _P), ("workspace", _P), ("workspace_bytes", _I64)]
 
 
+class CRope(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in ("n", "q_heads", "k_heads", "dim", "dtype", "norm")] + [
+        ("eps", ctypes.c_float), ("rope_dim", ctypes.c_int32), ("rope_at", ctypes.c_int32), ("halves", ctypes.c_int32),
+        ("base", ctypes.c_float), ("freq", _P), ("pos", _P), ("q", _P), ("q_stride", _I64), ("q_weight", _P),
+        ("q_out", _P), ("q_out_stride", _I64), ("k", _P), ("k_stride", _I64), ("k_weight", _P), ("k_out", _P),
+        ("k_out_stride", _I64)]
+
+
+class CAppend(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in
+                ("B", "S", "q_heads", "kv_heads", "dim", "dtype", "kv_dtype", "norm")] + [
+        ("eps", ctypes.c_float), ("rope_dim", ctypes.c_int32), ("rope_at", ctypes.c_int32), ("halves", ctypes.c_int32),
+        ("base", ctypes.c_float), ("freq", _P), ("pos", _P), ("ctx_len", _P), ("count", _P), ("slot", _P), ("off", _P),
+        ("table", _P), ("block", ctypes.c_int32), ("table_stride", ctypes.c_int32), ("rows", _I64),
+        ("q", _P), ("q_stride", _I64), ("q_weight", _P), ("q_out", _P), ("q_out_stride", _I64),
+        ("k", _P), ("k_stride", _I64), ("k_weight", _P), ("v", _P), ("v_stride", _I64),
+        ("k_pool", _P), ("k_pool_stride", _I64), ("v_pool", _P), ("v_pool_stride", _I64),
+        ("k_scale", _P), ("v_scale", _P), ("scale_stride", _I64), ("status", _P)]
+
+
 _lib = None
 _lock = threading.Lock()
 
@@ -128,13 +148,15 @@ def lib(path: str | None = None):
             L.csa_norm_rows.argtypes = [ctypes.POINTER(CNorm), vp]
             L.csa_fp8_matmul.argtypes = [ctypes.POINTER(CFp8Mm), vp]
             L.csa_paged_attn.argtypes = [ctypes.POINTER(CPaged), vp]
+            L.csa_qk_rope.argtypes = [ctypes.POINTER(CRope), vp]
+            L.csa_kv_append.argtypes = [ctypes.POINTER(CAppend), vp]
             L.csa_paged_attn_workspace.argtypes = [i32]
             L.csa_paged_attn_workspace.restype = ctypes.c_int64
             for name in ("csa_decode_create", "csa_indexer_topk", "csa_sparse_attn", "csa_decode_step",
                          "csa_indexer_scores", "csa_topk_select", "csa_check_batch", "csa_get_status",
                          "csa_profile_enable", "csa_profile_read", "csa_indexer_topk_static",
                          "csa_cache_writeback", "csa_debug_set_wait_polls", "csa_norm_rows",
-                         "csa_fp8_matmul", "csa_paged_attn"):
+                         "csa_fp8_matmul", "csa_paged_attn", "csa_qk_rope", "csa_kv_append"):
                 getattr(L, name).restype = ctypes.c_int
             _lib = L
     return _lib
@@ -574,6 +596,196 @@ class PagedAttention(_Operator):
         self._bind(lib().csa_paged_attn, st, (q, k, v, ctx_len, table, off, k_scale, v_scale, out, lse, status,
                                               workspace))
         self._out = {"out": out} if lse is None else {"out": out, "lse": lse}
+
+    def __call__(self, stream=None) -> dict:
+        self._launch(stream)
+        return self._out
+
+
+def _tokens(name: str, t, lead, heads: int, dim: int, dtype):
+    """Heads of tokens [*lead, heads, dim]: a token's heads together, the tokens evenly spaced.
+    Returns the elements from one token to the next."""
+    shape = (*lead, heads, dim)
+    if tuple(t.shape) != shape or t.dtype != dtype:
+        _bad(f"{name} must be {dtype} of shape {shape}, got {t.dtype} {tuple(t.shape)}")
+    if (dim > 1 and t.stride(-1) != 1) or (heads > 1 and t.stride(-2) != dim):
+        _bad(f"{name}: a token's heads must be contiguous")
+    step, width = None, 1
+    for size, stride in zip(reversed(lead), reversed(t.stride()[:len(lead)])):
+        if size == 1:
+            continue
+        if step is None:
+            step = stride
+        elif stride != width * step:
+            _bad(f"{name}: the tokens must be evenly spaced")
+        width *= size
+    return heads * dim if step is None else int(step)
+
+
+def _head_weight(name: str, weight, like, dim: int, norm: bool):
+    if weight is not None and not norm:
+        _bad(f"{name} given with norm=False")
+    if weight is not None and (tuple(weight.shape) != (dim,) or weight.dtype != like.dtype or not weight.is_contiguous()):
+        _bad(f"{name} must be contiguous {like.dtype} of shape ({dim},)")
+
+
+def _flat(name: str, t, dtype, shape):
+    if t is not None and (t.dtype != dtype or tuple(t.shape) not in (shape if isinstance(shape, list) else [shape]) or
+                          not t.is_contiguous()):
+        _bad(f"{name} must be contiguous {dtype} of shape {shape}, got {t.dtype} {tuple(t.shape)}")
+
+
+class QkRope(_Operator):
+    """csa_qk_rope: each query and key head normed (norm=True: RMS over its dims, times q_weight / k_weight [dim],
+    None: ones) and rotated by its token's position.
+
+    q [n, q_heads, dim] and / or k [n, k_heads, dim], bf16 or fp32 (or [B, S, heads, dim], the tokens evenly
+    spaced), pos [n] (or [B, S]) int32.  rope_dim dims from rope_at on are rotated (None: all of them; 0: none),
+    as pairs (2i, 2i + 1) or with halves=True (i, i + rope_dim / 2), by pos * base^(-2i / rope_dim) or pos * freq[i]
+    (fp32 [rope_dim / 2]).  q_out, k_out: buffers of the object by default, the input itself for in place.
+    Calling the object returns {"q", "k"} as far as they are given."""
+
+    def __init__(self, q=None, k=None, pos=None, q_weight=None, k_weight=None, norm: bool = False, eps: float = 1e-6,
+                 rope_dim: int | None = None, rope_at: int = 0, halves: bool = False, base: float = 10000.0, freq=None,
+                 q_out=None, k_out=None):
+        import torch
+        x = k if q is None else q
+        if x is None or x.dim() < 3:
+            _bad("give q or k, [n, heads, dim] or [B, S, heads, dim]")
+        lead, dim, dt = tuple(int(v) for v in x.shape[:-2]), int(x.shape[-1]), _dtype_code(x)
+        rope_dim = dim - rope_at if rope_dim is None else rope_dim
+        n = 1
+        for v in lead:
+            n *= v
+        _int32(n=n, dim=dim, rope_dim=rope_dim, rope_at=rope_at)
+        st = CRope(n=n, dim=dim, dtype=dt, norm=1 if norm else 0, eps=eps, rope_dim=rope_dim, rope_at=rope_at,
+                   halves=1 if halves else 0, base=base, freq=_ptr(freq), pos=_ptr(pos))
+        if pos is None and rope_dim > 0:
+            _bad("pos is needed for the rotation")
+        _flat("pos", pos, torch.int32, [lead, (n,)])
+        _flat("freq", freq, torch.float32, (rope_dim // 2,))
+        self._out = {}
+        for name, t, w, out in (("q", q, q_weight, q_out), ("k", k, k_weight, k_out)):
+            if t is None:
+                if w is not None or out is not None:
+                    _bad(f"{name}_weight or {name}_out given without {name}")
+                continue
+            heads = int(t.shape[-2]) if t.dim() >= 2 else 0
+            _int32(heads=heads)
+            stride = _tokens(name, t, lead, heads, dim, x.dtype)
+            _head_weight(name + "_weight", w, x, dim, norm)
+            if out is None:
+                out = torch.empty(t.shape, dtype=t.dtype, device=t.device)
+            setattr(st, name + "_heads", heads)
+            setattr(st, name, _ptr(t))
+            setattr(st, name + "_stride", stride)
+            setattr(st, name + "_weight", _ptr(w))
+            setattr(st, name + "_out", _ptr(out))
+            setattr(st, name + "_out_stride", _tokens(name + "_out", out, lead, heads, dim, x.dtype))
+            self._out[name] = out
+        self._bind(lib().csa_qk_rope, st, (q, k, pos, q_weight, k_weight, freq, *self._out.values()))
+
+    def __call__(self, stream=None) -> dict:
+        self._launch(stream)
+        return self._out
+
+
+class KvAppend(_Operator):
+    """csa_kv_append: the keys (normed and rotated as QkRope does it) and values of new tokens into the pools of a
+    cache, their queries normed and rotated beside them.
+
+    k, v [B, S, kv_heads, dim] bf16 or fp32 (v None: keys only); k_pool, v_pool [rows, kv_heads, dim] in the same
+    type, or E4M3 codes (uint8 or float8_e4m3fn) with k_scale, v_scale fp32 [rows, kv_heads].  The tokens' rows: through
+    ctx_len [B] int32 (the new tokens included) with table [B, blocks] int32 and block, or with off [B] int64; or by
+    slot int64 [B * S] (negative: padding).  count [B] int32: the real tokens of each request, the first of its S
+    (None: all S).  pos int32 [B * S]: positions, by default the tokens' rows in their request.  q [B, S, q_heads, dim]
+    with q_out (a buffer of the object by default; padding tokens' rows are left as they are), weights, norm and rotation
+    as in QkRope.  status: an int32 on the device that records bad rows.  Calling the object returns the pools and
+    what else it writes: {"k", "v", "k_scale", "v_scale", "q"} as far as they are given."""
+
+    def __init__(self, k, v, k_pool, v_pool, k_scale=None, v_scale=None, ctx_len=None, count=None, table=None,
+                 block: int = 0, off=None, slot=None, pos=None, q=None, q_out=None, q_weight=None, k_weight=None,
+                 norm: bool = False, eps: float = 1e-6, rope_dim: int | None = None, rope_at: int = 0,
+                 halves: bool = False, base: float = 10000.0, freq=None, status=None):
+        import torch
+        if k.dim() != 4 or k_pool.dim() != 3:
+            _bad("k, v must be [B, S, kv_heads, dim] and the pools [rows, kv_heads, dim]")
+        b, s, heads, dim = (int(x) for x in k.shape)
+        rows, dt = int(k_pool.shape[0]), _dtype_code(k)
+        rope_dim = dim - rope_at if rope_dim is None else rope_dim
+        _int32(B=b, S=s, kv_heads=heads, dim=dim, rope_dim=rope_dim, rope_at=rope_at, block=block)
+        fp8 = str(k_pool.dtype) in _E4M3_DTYPES
+        st = CAppend(B=b, S=s, kv_heads=heads, dim=dim, dtype=dt, kv_dtype=CSA_DTYPE_FP8_E4M3 if fp8 else dt,
+                     norm=1 if norm else 0, eps=eps, rope_dim=rope_dim, rope_at=rope_at, halves=1 if halves else 0,
+                     base=base, freq=_ptr(freq), pos=_ptr(pos), ctx_len=_ptr(ctx_len), count=_ptr(count),
+                     slot=_ptr(slot), off=_ptr(off), table=_ptr(table), block=block, rows=rows, status=_ptr(status))
+        if (v is None) != (v_pool is None):
+            _bad("v and v_pool go together")
+        self._out = {}
+        for name, t, pool, scale in (("k", k, k_pool, k_scale), ("v", v, v_pool, v_scale)):
+            if t is None:
+                if scale is not None:
+                    _bad(f"{name}_scale given without {name}")
+                continue
+            setattr(st, name, _ptr(t))
+            setattr(st, name + "_stride", _tokens(name, t, (b, s), heads, dim, k.dtype))
+            if tuple(pool.shape) != (rows, heads, dim) or (str(pool.dtype) not in _E4M3_DTYPES if fp8
+                                                           else pool.dtype != k.dtype):
+                _bad(f"{name}_pool must be {k.dtype} or E4M3 codes, both alike, of shape ({rows}, {heads}, {dim})")
+            if (dim > 1 and pool.stride(2) != 1) or (heads > 1 and pool.stride(1) != dim):
+                _bad(f"{name}_pool: the heads of a row must be contiguous")
+            setattr(st, name + "_pool", _ptr(pool))
+            setattr(st, name + "_pool_stride", int(pool.stride(0)) if rows > 1 else -(-heads * dim // 16) * 16)
+            if fp8:
+                if scale is None:
+                    _bad(f"{name}_scale is needed with E4M3 codes")
+                _rows2d(name + "_scale", scale, rows, heads, torch.float32)
+                step = int(scale.stride(0)) if rows > 1 else heads
+                if name == "v" and st.scale_stride != step:
+                    _bad("k_scale and v_scale must have the same row stride")
+                st.scale_stride = step
+                setattr(st, name + "_scale", _ptr(scale))
+                self._out[name + "_scale"] = scale
+            elif scale is not None:
+                _bad("scales given with a pool that is not of E4M3 codes")
+            self._out[name] = pool.view(torch.float8_e4m3fn) if fp8 else pool
+            w = k_weight if name == "k" else None
+            _head_weight("k_weight", w, k, dim, norm)
+        st.k_weight = _ptr(k_weight)
+        if q is not None:
+            if q.dim() != 4:
+                _bad("q must be [B, S, q_heads, dim]")
+            q_heads = int(q.shape[2])
+            _int32(q_heads=q_heads)
+            if q_out is None:
+                q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+            _head_weight("q_weight", q_weight, k, dim, norm)
+            st.q_heads, st.q, st.q_weight, st.q_out = q_heads, _ptr(q), _ptr(q_weight), _ptr(q_out)
+            st.q_stride = _tokens("q", q, (b, s), q_heads, dim, k.dtype)
+            st.q_out_stride = _tokens("q_out", q_out, (b, s), q_heads, dim, k.dtype)
+            self._out["q"] = q_out
+        elif q_out is not None or q_weight is not None:
+            _bad("q_out or q_weight given without q")
+        if (table is not None) + (off is not None) + (slot is not None) != 1:
+            _bad("give one of table (with block), off and slot")
+        if slot is None and ctx_len is None:
+            _bad("ctx_len is needed without slot")
+        if rope_dim > 0 and pos is None and ctx_len is None:
+            _bad("pos or ctx_len is needed for the rotation")
+        if table is not None:
+            if table.dtype != torch.int32 or table.dim() != 2 or table.shape[0] != b or not table.is_contiguous():
+                _bad(f"table must be contiguous int32 of shape ({b}, blocks)")
+            _int32(table_stride=table.shape[1])
+            st.table_stride = int(table.shape[1])
+        _flat("ctx_len", ctx_len, torch.int32, (b,))
+        _flat("count", count, torch.int32, (b,))
+        _flat("off", off, torch.int64, (b,))
+        _flat("slot", slot, torch.int64, [(b * s,), (b, s)])
+        _flat("pos", pos, torch.int32, [(b * s,), (b, s)])
+        _flat("freq", freq, torch.float32, (rope_dim // 2,))
+        _status_word(status)
+        self._bind(lib().csa_kv_append, st, (k, v, k_pool, v_pool, k_scale, v_scale, ctx_len, count, table, off, slot, pos,
+                                             q, q_out, q_weight, k_weight, freq, status))
 
     def __call__(self, stream=None) -> dict:
         self._launch(stream)

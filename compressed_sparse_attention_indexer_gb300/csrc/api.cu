@@ -938,6 +938,149 @@ int csa_paged_attn(const csa_paged* a, void* stream) {
   return finish_free(csa::launch_paged_attn(k, fp8, sms, static_cast<cudaStream_t>(stream), use_pdl()));
 }
 
+namespace {
+
+// What csa_qk_rope and csa_kv_append share: the heads' shape, norm and angles.
+struct HeadShape {
+  int dim, dtype, norm, rope_dim, rope_at, halves;
+  float eps, base;
+  const float* freq;
+  int64_t heads;
+};
+int check_heads(const HeadShape& s) {
+  if (s.dtype != CSA_DTYPE_BF16 && s.dtype != CSA_DTYPE_F32)
+    return fail(CSA_ERR_UNSUPPORTED, "dtype must be CSA_DTYPE_F32 or CSA_DTYPE_BF16");
+  if (s.dim < 1 || s.rope_dim < 0 || s.rope_at < 0) return fail(CSA_ERR_INVALID_ARG, "negative sizes");
+  if (s.dim % 8 != 0 || s.dim > csa::kHeadMaxDim)
+    return fail(CSA_ERR_UNSUPPORTED, "dim must be a multiple of 8 up to %d", csa::kHeadMaxDim);
+  if (s.rope_dim % 2 != 0 || (int64_t)s.rope_at + s.rope_dim > s.dim)
+    return fail(CSA_ERR_INVALID_ARG, "the rotated dims must be even in number and lie within the head");
+  if (s.rope_dim > csa::kRopeMaxDim) return fail(CSA_ERR_UNSUPPORTED, "rope_dim above %d", csa::kRopeMaxDim);
+  if (s.norm != 0 && s.norm != 1) return fail(CSA_ERR_INVALID_ARG, "norm must be 0 or 1");
+  if (s.halves != 0 && s.halves != 1) return fail(CSA_ERR_INVALID_ARG, "halves must be 0 or 1");
+  if (s.norm && !(s.eps >= 0.f)) return fail(CSA_ERR_INVALID_ARG, "eps must be >= 0");
+  if (s.rope_dim > 0 && !s.freq && !(s.base >= 1.f && s.base < INFINITY))
+    return fail(CSA_ERR_INVALID_ARG, "base must be a finite number >= 1");
+  if (s.heads > 4096) return fail(CSA_ERR_UNSUPPORTED, "more than 4096 heads");
+  return CSA_OK;
+}
+// One kind of heads: `name`s of [tokens, heads, dim], their weight.
+int check_tokens(const char* name, const void* p, int64_t stride, int64_t heads, const HeadShape& s, const void* weight) {
+  const int rc = check_rows(name, p, stride, heads * s.dim, s.dtype == CSA_DTYPE_BF16 ? 2 : 4);
+  if (rc) return rc;
+  if (weight && !s.norm) return fail(CSA_ERR_INVALID_ARG, "%s_weight given with norm = 0", name);
+  if (!aligned16(weight)) return fail(CSA_ERR_INVALID_ARG, "%s_weight is not 16-byte aligned", name);
+  return CSA_OK;
+}
+struct Aligned { const void* p; int align; const char* n; };
+int check_aligned(const Aligned* x, int n) {
+  for (int i = 0; i < n; ++i)
+    if (reinterpret_cast<uintptr_t>(x[i].p) % x[i].align != 0)
+      return fail(CSA_ERR_INVALID_ARG, "%s is not %d-byte aligned", x[i].n, x[i].align);
+  return CSA_OK;
+}
+
+}  // namespace
+
+int csa_qk_rope(const csa_rope* a, void* stream) {
+  if (!a) return fail(CSA_ERR_INVALID_ARG, "args is NULL");
+  if (a->n < 0 || a->q_heads < 0 || a->k_heads < 0 || (a->q_heads == 0 && a->k_heads == 0))
+    return fail(CSA_ERR_INVALID_ARG, "need n >= 0 and query or key heads");
+  const HeadShape s = {a->dim, a->dtype, a->norm, a->rope_dim, a->rope_at, a->halves, a->eps, a->base, a->freq,
+                       (int64_t)a->q_heads + a->k_heads};
+  int rc = check_heads(s);
+  if (rc) return rc;
+  if (a->n == 0) { g_err.clear(); return CSA_OK; }
+  const int es = a->dtype == CSA_DTYPE_BF16 ? 2 : 4;
+  if (a->q_heads > 0) {
+    rc = check_tokens("q", a->q, a->q_stride, a->q_heads, s, a->q_weight);
+    if (!rc) rc = check_rows("q_out", a->q_out, a->q_out_stride, (int64_t)a->q_heads * a->dim, es);
+  }
+  if (!rc && a->k_heads > 0) {
+    rc = check_tokens("k", a->k, a->k_stride, a->k_heads, s, a->k_weight);
+    if (!rc) rc = check_rows("k_out", a->k_out, a->k_out_stride, (int64_t)a->k_heads * a->dim, es);
+  }
+  if (rc) return rc;
+  if (a->rope_dim > 0 && !a->pos) return fail(CSA_ERR_INVALID_ARG, "pos is NULL");
+  const Aligned al[] = {{a->pos, 4, "pos"}, {a->freq, 4, "freq"}};
+  rc = check_aligned(al, 2);
+  if (rc) return rc;
+  int sms = 0;
+  rc = device_sms(&sms);
+  if (rc) return rc;
+  csa::HeadArgs k = {};
+  k.n = a->n; k.S = 1; k.dim = a->dim; k.R = a->rope_dim; k.at = a->rope_at; k.halves = a->halves;
+  k.norm = a->norm; k.eps = a->eps;
+  k.heads[0] = a->q_heads; k.heads[1] = a->k_heads;
+  k.src[0] = a->q; k.src_stride[0] = a->q_stride; k.src[1] = a->k; k.src_stride[1] = a->k_stride;
+  k.weight[0] = a->q_weight; k.weight[1] = a->k_weight;
+  k.dst[0] = a->q_out; k.dst_stride[0] = a->q_out_stride; k.dst[1] = a->k_out; k.dst_stride[1] = a->k_out_stride;
+  k.pos = a->pos; k.freq = a->freq;
+  return finish_free(csa::launch_heads(k, a->dtype, false, a->base, sms, static_cast<cudaStream_t>(stream), use_pdl()));
+}
+
+int csa_kv_append(const csa_append* a, void* stream) {
+  if (!a) return fail(CSA_ERR_INVALID_ARG, "args is NULL");
+  if (a->kv_dtype != 0 && a->kv_dtype != a->dtype && a->kv_dtype != CSA_DTYPE_FP8_E4M3)
+    return fail(CSA_ERR_UNSUPPORTED, "kv_dtype must be dtype or CSA_DTYPE_FP8_E4M3");
+  const bool fp8 = a->kv_dtype == CSA_DTYPE_FP8_E4M3;
+  if (a->B < 0 || a->S < 1 || a->q_heads < 0 || a->kv_heads < 1)
+    return fail(CSA_ERR_INVALID_ARG, "need B >= 0, S >= 1, q_heads >= 0 and kv_heads >= 1");
+  const HeadShape s = {a->dim, a->dtype, a->norm, a->rope_dim, a->rope_at, a->halves, a->eps, a->base, a->freq,
+                       (int64_t)a->q_heads + a->kv_heads};
+  int rc = check_heads(s);
+  if (rc) return rc;
+  if (a->B == 0) { g_err.clear(); return CSA_OK; }
+  const int es = a->dtype == CSA_DTYPE_BF16 ? 2 : 4, pe = fp8 ? 1 : es;
+  const int64_t width = (int64_t)a->kv_heads * a->dim;
+  if (a->q_heads > 0) {
+    rc = check_tokens("q", a->q, a->q_stride, a->q_heads, s, a->q_weight);
+    if (!rc) rc = check_rows("q_out", a->q_out, a->q_out_stride, (int64_t)a->q_heads * a->dim, es);
+  }
+  if (!rc) rc = check_tokens("k", a->k, a->k_stride, a->kv_heads, s, a->k_weight);
+  if (!rc) rc = check_rows("k_pool", a->k_pool, a->k_pool_stride, width, pe);
+  if (!rc && !a->v != !a->v_pool) rc = fail(CSA_ERR_INVALID_ARG, "v and v_pool go together");
+  if (!rc && a->v) rc = check_rows("v", a->v, a->v_stride, width, es);
+  if (!rc && a->v) rc = check_rows("v_pool", a->v_pool, a->v_pool_stride, width, pe);
+  if (rc) return rc;
+  if (fp8) {
+    if (!a->k_scale || (a->v && !a->v_scale)) return fail(CSA_ERR_INVALID_ARG, "E4M3 pools need k_scale and v_scale");
+    if (a->scale_stride < a->kv_heads) return fail(CSA_ERR_INVALID_ARG, "scale_stride below kv_heads");
+  }
+  if (a->rows < 0) return fail(CSA_ERR_INVALID_ARG, "rows < 0");
+  if (!a->slot) {
+    if (!a->ctx_len) return fail(CSA_ERR_INVALID_ARG, "ctx_len is NULL without slot");
+    if (!a->table && !a->off) return fail(CSA_ERR_INVALID_ARG, "none of slot, table and off given");
+    if (a->table && (a->block < 1 || a->table_stride < 1))
+      return fail(CSA_ERR_INVALID_ARG, "block and table_stride must be >= 1 with a table");
+  } else if (a->table || a->off) {
+    return fail(CSA_ERR_INVALID_ARG, "slot given with table or off");
+  }
+  if (a->rope_dim > 0 && !a->pos && !a->ctx_len) return fail(CSA_ERR_INVALID_ARG, "neither pos nor ctx_len given");
+  const Aligned al[] = {{a->pos, 4, "pos"}, {a->freq, 4, "freq"}, {a->ctx_len, 4, "ctx_len"}, {a->count, 4, "count"},
+                        {a->slot, 8, "slot"}, {a->off, 8, "off"}, {a->table, 4, "table"}, {a->k_scale, 4, "k_scale"},
+                        {a->v_scale, 4, "v_scale"}, {a->status, 4, "status"}};
+  rc = check_aligned(al, (int)(sizeof(al) / sizeof(al[0])));
+  if (rc) return rc;
+  int sms = 0;
+  rc = device_sms(&sms);
+  if (rc) return rc;
+  csa::HeadArgs k = {};
+  k.n = (int64_t)a->B * a->S; k.S = a->S; k.dim = a->dim; k.R = a->rope_dim; k.at = a->rope_at; k.halves = a->halves;
+  k.norm = a->norm; k.eps = a->eps; k.append = 1;
+  k.heads[0] = a->q_heads; k.heads[1] = a->kv_heads; k.heads[2] = a->v ? a->kv_heads : 0;
+  k.src[0] = a->q; k.src_stride[0] = a->q_stride; k.src[1] = a->k; k.src_stride[1] = a->k_stride;
+  k.src[2] = a->v; k.src_stride[2] = a->v_stride;
+  k.weight[0] = a->q_weight; k.weight[1] = a->k_weight;
+  k.dst[0] = a->q_out; k.dst_stride[0] = a->q_out_stride; k.dst[1] = a->k_pool; k.dst_stride[1] = a->k_pool_stride;
+  k.dst[2] = a->v_pool; k.dst_stride[2] = a->v_pool_stride;
+  k.scale[0] = a->k_scale; k.scale[1] = a->v_scale; k.scale_stride = a->scale_stride;
+  k.pos = a->pos; k.ctx_len = a->ctx_len; k.count = a->count; k.slot = a->slot; k.off = a->off;
+  k.table = a->table; k.block = a->block; k.table_stride = a->table_stride; k.rows = a->rows; k.status = a->status;
+  k.freq = a->freq;
+  return finish_free(csa::launch_heads(k, a->dtype, fp8, a->base, sms, static_cast<cudaStream_t>(stream), use_pdl()));
+}
+
 int csa_debug_set_wait_polls(csa_handle* h, int32_t polls) {
   if (!h) return fail(CSA_ERR_INVALID_ARG, "handle is NULL");
   h->dc.wait_polls = polls < 0 ? -1 : polls;

@@ -418,6 +418,29 @@ struct PagedArgs {
 constexpr int kPagedMaxLen = 1 << 30;   // csa_paged.max_len at most
 size_t paged_attn_workspace(int dim, int num_sms);
 int launch_paged_attn(const PagedArgs& a, bool fp8, int num_sms, cudaStream_t st, bool pdl);
+// Heads of new tokens: norm, rotation and the place they go to (csa_qk_rope,
+// csa_kv_append) with checked arguments.  Kinds 0, 1, 2 are queries, keys and
+// values; strides in elements, from one token or pool row to the next.
+// append = 0: keys go to row t of dst[1], like the queries.
+struct HeadArgs {
+  int64_t n;                                 // tokens
+  int S, dim, R, at, halves, norm, append;
+  float eps;
+  int heads[3];
+  const void* src[3]; int64_t src_stride[3];
+  const void* weight[2];
+  void* dst[3]; int64_t dst_stride[3];
+  float* scale[2]; int64_t scale_stride;     // of E4M3 keys and values
+  const int* pos; const int* ctx_len; const int* count;
+  const int64_t* slot; const int64_t* off;
+  const int* table; int block, table_stride;
+  int64_t rows;
+  int* status;
+  const float* freq;
+};
+constexpr int kRopeMaxDim = 256;             // rotated dims at most
+constexpr int kHeadMaxDim = 1024;
+int launch_heads(const HeadArgs& a, int dtype, bool fp8, double base, int num_sms, cudaStream_t st, bool pdl);
 int norm_max_width(int dtype);
 int launch_norm(const NormArgs& a, int dtype, int num_sms, cudaStream_t st, bool pdl);
 // early: this library's own kernel of the same call runs right before (the

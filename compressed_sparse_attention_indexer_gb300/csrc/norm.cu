@@ -26,56 +26,16 @@
 
 #include "csa_internal.cuh"
 #include "ptx.cuh"
+#include "rows.cuh"
 
 namespace csa {
 
 namespace {
 
-constexpr float kE4m3Max = 448.f;
 constexpr int kNormMaxThreads = 512;
 constexpr int kNormMaxVec = 8;      // 16-byte vectors per thread at most
 constexpr int kNormBlock = 128;     // elements that share a scale
 constexpr int kNormDepth = 2;       // rows of the shared-memory ring
-
-template <typename T>
-struct VecOf;
-template <>
-struct VecOf<float> {
-  static constexpr int E = 4;
-  static __device__ __forceinline__ void unpack(const uint4& r, float* f) {
-    f[0] = __uint_as_float(r.x);
-    f[1] = __uint_as_float(r.y);
-    f[2] = __uint_as_float(r.z);
-    f[3] = __uint_as_float(r.w);
-  }
-  static __device__ __forceinline__ uint4 pack(const float* f) {
-    return make_uint4(__float_as_uint(f[0]), __float_as_uint(f[1]), __float_as_uint(f[2]),
-                      __float_as_uint(f[3]));
-  }
-  static __device__ __forceinline__ float one(float v) { return v; }
-};
-template <>
-struct VecOf<__nv_bfloat16> {
-  static constexpr int E = 8;
-  static __device__ __forceinline__ void unpack(const uint4& r, float* f) {
-    const uint32_t w[4] = {r.x, r.y, r.z, r.w};
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      f[2 * i] = __uint_as_float(w[i] << 16);
-      f[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
-    }
-  }
-  static __device__ __forceinline__ uint4 pack(const float* f) {
-    uint32_t w[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const __nv_bfloat162 v = __floats2bfloat162_rn(f[2 * i], f[2 * i + 1]);
-      w[i] = *reinterpret_cast<const uint32_t*>(&v);
-    }
-    return make_uint4(w[0], w[1], w[2], w[3]);
-  }
-  static __device__ __forceinline__ __nv_bfloat16 one(float v) { return __float2bfloat16_rn(v); }
-};
 
 // Vector v of a row of `width` elements.  kTail: the row's last vector may be
 // short; elements past the row then read as zero and are not written (the row
@@ -121,20 +81,6 @@ __device__ __forceinline__ void store_codes(uint8_t* row, int v, int width, cons
   for (int i = 0; i < E; ++i)
     if (v * E + i < width) row[v * E + i] = (uint8_t)(c[i / 2] >> (8 * (i & 1)));
 }
-__device__ __forceinline__ float rcp_approx(float x) {
-  float y;
-  asm("rcp.approx.f32 %0, %1;\n" : "=f"(y) : "f"(x));
-  return y;
-}
-
-// The scale of a block whose largest magnitude is m.  The quotient is the
-// rounded one: the product with 1 / 448, corrected by its residual (an infinite
-// m stays).
-__device__ __forceinline__ float block_scale(float m) {
-  constexpr float kInv = 1.f / kE4m3Max;
-  const float q = m * kInv;
-  return m > 0.f ? fmaxf(m < INFINITY ? fmaf(fmaf(-q, kE4m3Max, m), kInv, q) : m, 1.17549435e-38f) : 1.f;
-}
 // r / scale is up to 448 / max|s weight|, which for blocks below 1.3e-36 is no
 // fp32 number.  So s weight is taken times kLift and r by 1 / kLift, both exactly:
 // from max|s weight| = 2^-149 on 448 / (kLift max|s weight|) is one.  (A branch
@@ -148,22 +94,6 @@ __device__ __forceinline__ float code_factor(float r, float scale) {
   const float inv = rcp_approx(scale), q = r * inv;
   return scale < INFINITY ? fmaf(fmaf(-q, scale, r), inv, q) : q;
 }
-// f / scale to within a rounding that almost never differs from the exact
-// one's: the product with the reciprocal, corrected by its residual (one step
-// of Newton's iteration for the quotient).  Rows quantised as they are have
-// many values next to a border of two codes' ranges, where a quotient that is
-// off in the last place takes the other code.  An infinite scale leaves 0, and
-// NaN for an infinite f.
-template <int E>
-__device__ __forceinline__ void divide(float* f, float scale) {
-  const float inv = rcp_approx(scale), d = scale < INFINITY ? scale : 0.f;
-#pragma unroll
-  for (int e = 0; e < E; ++e) {
-    const float q = f[e] * inv;
-    f[e] = fmaf(fmaf(-q, d, f[e]), inv, q);
-  }
-}
-
 __device__ __forceinline__ uint4 lds128(uint32_t a) {
   uint4 r;
   asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];\n" : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w) : "r"(a) : "memory");

@@ -394,6 +394,91 @@ CSA_API int csa_paged_attn(const csa_paged *a, void *stream);
  * `dim` elements, whatever the batch; 0 when the device cannot be asked. */
 CSA_API int64_t csa_paged_attn_workspace(int32_t dim);
 
+/* ---- new and drafted tokens of a dense layer: heads, cache rows, trees ---- */
+
+/* Norms of queries and keys for each head with the position rotation in the
+ * same pass.  Token t < n, each of its heads x of `dim` elements:
+ *   y = x * (sum_i x_i^2 / dim + eps)^(-1/2) * weight    (norm = 0: y = x)
+ *   (y_a, y_b) -> (y_a cos - y_b sin, y_a sin + y_b cos)
+ * for the rope_dim / 2 pairs of the dims rope_at .. rope_at + rope_dim - 1, by the
+ * angle pos[t] * base^(-2i / rope_dim), or pos[t] * freq[i].  Pair i is dims
+ * (2i, 2i + 1) of the rotated ones, as the CSA rows have them, or with halves = 1
+ * (i, i + rope_dim / 2).  All of it is formed in fp32 and rounded once; the angles
+ * are reduced exactly (base's: to 2^-53 of |pos theta|; freq's: of the fp32 numbers
+ * given), so positions may be any 32-bit number.  The sum of a head's squares must
+ * stay in fp32's range. */
+typedef struct {
+    int32_t n;                /* tokens (0: a no-op)                                */
+    int32_t q_heads, k_heads; /* per token; either may be 0, not both               */
+    int32_t dim;              /* of a head: a multiple of 8, at most 1024           */
+    int32_t dtype;            /* CSA_DTYPE_BF16 or CSA_DTYPE_F32: q, k, weights, outputs */
+    int32_t norm;             /* 1: RMS norm of each head; 0: none (weights must be NULL) */
+    float eps;                /* >= 0                                               */
+    int32_t rope_dim, rope_at; /* even, at most 256, rope_at + rope_dim <= dim; 0: no rotation */
+    int32_t halves;
+    float base;               /* >= 1, finite                                       */
+    const float *freq;        /* [rope_dim / 2] angles per position, or NULL: from base */
+    const int32_t *pos;       /* [n]; may be NULL with rope_dim = 0                 */
+    const void *q; int64_t q_stride;          /* [n, q_heads, dim]; q_stride elements from one
+                                                 token to the next, a token's heads together */
+    const void *q_weight;     /* [dim], NULL = ones                                 */
+    void *q_out; int64_t q_out_stride;        /* may be q itself (in place)         */
+    const void *k; int64_t k_stride;          /* [n, k_heads, dim]                  */
+    const void *k_weight;
+    void *k_out; int64_t k_out_stride;        /* may be k itself                    */
+} csa_rope;
+
+/* Tokens, weights and outputs start on 16-byte boundaries (pointers and strides *
+ * element size multiples of 16).  An output in place has its input's pointer and
+ * stride; any other overlap is undefined.  Returns CSA_ERR_INVALID_ARG or
+ * CSA_ERR_UNSUPPORTED (dtype, dim, rope_dim, more than 4096 heads). */
+CSA_API int csa_qk_rope(const csa_rope *a, void *stream);
+
+/* New tokens' keys (normed and rotated as csa_qk_rope does it) and values into
+ * the pools of a cache, their queries beside them.  Request b has n_b = count[b]
+ * new tokens (S without count), the first n_b of its S; token s becomes row
+ *   r = L_b - n_b + s
+ * of its cache, which is pool row off[b] + r, or through the block table as in
+ * csa_batch, or slot[b * S + s] where slots are given.  Its position is pos[b * S + s],
+ * without pos r.  A token with s >= n_b, r < 0 or a negative slot is padding: nothing
+ * of it is written, q_out's row neither.
+ * Pool rows hold kv_heads x dim elements, head g at g * dim: in dtype, or as E4M3
+ * codes with scale = max(max|y| / 448, 2^-126) per row and head (1 where all are zero),
+ * codes = y / scale to the nearest E4M3 value; what csa_paged_attn, csa_tree_attn and,
+ * with one head of 128, the FP8 indexer keys read.  Rows that are not new keep what
+ * they hold.  v may be NULL (rows that serve as both, indexer keys).
+ * Slots are expected to be free of collisions, as csa_cache_writeback expects them. */
+typedef struct {
+    int32_t B, S;             /* requests (0: a no-op), tokens per request          */
+    int32_t q_heads, kv_heads; /* q_heads 0: no queries                             */
+    int32_t dim, dtype;       /* as in csa_rope; dtype of q, k, v, weights, q_out   */
+    int32_t kv_dtype;         /* of the pools: 0 = dtype, or CSA_DTYPE_FP8_E4M3     */
+    int32_t norm; float eps;  /* of query and key heads                             */
+    int32_t rope_dim, rope_at, halves; float base; const float *freq;
+    const int32_t *pos;       /* [B * S] or NULL (then ctx_len is needed, but with rope_dim = 0) */
+    const int32_t *ctx_len;   /* [B] L_b, including the new tokens; may be NULL with slot */
+    const int32_t *count;     /* [B] n_b in [0, S], or NULL                         */
+    const int64_t *slot;      /* [B * S] pool rows, or NULL                         */
+    const int64_t *off;       /* [B], without slot and table                        */
+    const int32_t *table; int32_t block, table_stride;  /* [B * table_stride], or NULL */
+    int64_t rows;             /* of each pool                                       */
+    const void *q; int64_t q_stride; const void *q_weight; void *q_out; int64_t q_out_stride;
+    const void *k; int64_t k_stride; const void *k_weight;
+    const void *v; int64_t v_stride;
+    void *k_pool; int64_t k_pool_stride;                /* elements from one row to the next */
+    void *v_pool; int64_t v_pool_stride;                /* given exactly when v is  */
+    float *k_scale, *v_scale; int64_t scale_stride;     /* [rows, kv_heads], E4M3 only */
+    int32_t *status;          /* NULL or a device int32: bit 0 (value 1) is set by a count
+                                 outside [0, S], a negative length (their tokens are padding)
+                                 or a row that is unmapped or outside the pools (its key
+                                 and value are skipped)                             */
+} csa_append;
+
+/* Alignment as csa_qk_rope; rows of the pools start on 16-byte boundaries too.
+ * Returns CSA_ERR_INVALID_ARG or CSA_ERR_UNSUPPORTED (types, dim, rope_dim, more than
+ * 4096 heads). */
+CSA_API int csa_kv_append(const csa_append *a, void *stream);
+
 /* Host-side checks of a batch against a config, exactly those every entry
  * point runs before launching (null / misaligned pointers, strides, sizes
  * against the maxima, ctx_len_host values).  Touches no device memory and
