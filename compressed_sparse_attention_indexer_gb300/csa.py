@@ -24,7 +24,8 @@ EXPORTS = ("csa_decode_create", "csa_decode_destroy", "csa_indexer_topk", "csa_s
            "csa_get_status", "csa_last_error", "csa_last_launch_count", "csa_abi_version",
            "csa_profile_enable", "csa_profile_read", "csa_indexer_topk_static", "csa_cache_writeback",
            "csa_debug_set_wait_polls", "csa_norm_rows", "csa_fp8_matmul",
-           "csa_paged_attn", "csa_paged_attn_workspace", "csa_qk_rope", "csa_kv_append")
+           "csa_paged_attn", "csa_paged_attn_workspace", "csa_qk_rope", "csa_kv_append",
+           "csa_tree_attn", "csa_tree_attn_workspace")
 STAGES = ("plan", "indexer", "topk", "attention")
 
 
@@ -82,6 +83,10 @@ class CPaged(ctypes.Structure):
         ("ctx_len", _P), ("q", _P), ("q_stride", _I64), ("k", _P), ("v", _P), ("k_stride", _I64), ("v_stride", _I64),
         ("rows", _I64), ("k_scale", _P), ("v_scale", _P), ("scale_stride", _I64), ("off", _P), ("table", _P),
         ("out", _P), ("out_stride", _I64), ("lse", _P), ("status", _P), ("workspace", _P), ("workspace_bytes", _I64)]
+
+
+class CTree(ctypes.Structure):
+    _fields_ = [("base", CPaged), ("tree", _P), ("count", _P), ("pos", _P)]
 
 
 class CRope(ctypes.Structure):
@@ -150,13 +155,17 @@ def lib(path: str | None = None):
             L.csa_paged_attn.argtypes = [ctypes.POINTER(CPaged), vp]
             L.csa_qk_rope.argtypes = [ctypes.POINTER(CRope), vp]
             L.csa_kv_append.argtypes = [ctypes.POINTER(CAppend), vp]
+            L.csa_tree_attn.argtypes = [ctypes.POINTER(CTree), vp]
+            L.csa_tree_attn_workspace.argtypes = [i32]
+            L.csa_tree_attn_workspace.restype = ctypes.c_int64
             L.csa_paged_attn_workspace.argtypes = [i32]
             L.csa_paged_attn_workspace.restype = ctypes.c_int64
             for name in ("csa_decode_create", "csa_indexer_topk", "csa_sparse_attn", "csa_decode_step",
                          "csa_indexer_scores", "csa_topk_select", "csa_check_batch", "csa_get_status",
                          "csa_profile_enable", "csa_profile_read", "csa_indexer_topk_static",
                          "csa_cache_writeback", "csa_debug_set_wait_polls", "csa_norm_rows",
-                         "csa_fp8_matmul", "csa_paged_attn", "csa_qk_rope", "csa_kv_append"):
+                         "csa_fp8_matmul", "csa_paged_attn", "csa_qk_rope", "csa_kv_append",
+                         "csa_tree_attn"):
                 getattr(L, name).restype = ctypes.c_int
             _lib = L
     return _lib
@@ -520,6 +529,13 @@ class PagedAttention(_Operator):
     def __init__(self, q, k, v, ctx_len, table=None, block: int = 0, off=None, k_scale=None, v_scale=None,
                  win: int = 0, scale: float = 0.0, max_len: int | None = None, out=None, lse=True, status=None,
                  workspace=None):
+        st, tensors, self._out = self._paged(q, k, v, ctx_len, table, block, off, k_scale, v_scale, win, scale, max_len, out,
+                                             lse, status, workspace, paged_attn_workspace)
+        self._bind(lib().csa_paged_attn, st, tensors)
+
+    def _paged(self, q, k, v, ctx_len, table, block, off, k_scale, v_scale, win, scale, max_len, out, lse, status, workspace,
+               workspace_bytes):
+        """The C struct, the tensors it points at and what the call returns."""
         import torch
         if q.dim() != 4 or k.dim() != 3:
             _bad("q must be [B, S, heads, dim] and k, v [rows, kv_heads, dim]")
@@ -581,7 +597,7 @@ class PagedAttention(_Operator):
             _bad("workspace must be contiguous")
         if workspace is None and q.is_cuda:
             with torch.cuda.device(q.device):
-                workspace = torch.empty(paged_attn_workspace(dim), dtype=torch.uint8, device=q.device)
+                workspace = torch.empty(workspace_bytes(dim), dtype=torch.uint8, device=q.device)
         st = CPaged(B=b, S=s, heads=heads, kv_heads=kv_heads, dim=dim,
                     kv_dtype=CSA_DTYPE_FP8_E4M3 if fp8 else CSA_DTYPE_BF16, win=win, max_len=max_len,
                     softmax_scale=scale, block=block, table_stride=0 if table is None else int(table.shape[1]),
@@ -593,13 +609,59 @@ class PagedAttention(_Operator):
                     off=_ptr(off), table=_ptr(table), out=_ptr(out), out_stride=strides[1], lse=_ptr(lse),
                     status=_ptr(status), workspace=_ptr(workspace),
                     workspace_bytes=0 if workspace is None else workspace.numel() * workspace.element_size())
-        self._bind(lib().csa_paged_attn, st, (q, k, v, ctx_len, table, off, k_scale, v_scale, out, lse, status,
-                                              workspace))
-        self._out = {"out": out} if lse is None else {"out": out, "lse": lse}
+        return st, (q, k, v, ctx_len, table, off, k_scale, v_scale, out, lse, status, workspace), \
+            {"out": out} if lse is None else {"out": out, "lse": lse}
 
     def __call__(self, stream=None) -> dict:
         self._launch(stream)
         return self._out
+
+
+def tree_attn_workspace(dim: int) -> int:
+    """Bytes of workspace csa_tree_attn needs on the current device (dim: 64, 128 or 256)."""
+    return int(lib().csa_tree_attn_workspace(int(dim)))
+
+
+def tree_masks(parent):
+    """The masks csa_tree_attn takes, int64 [B, S, ceil(S / 64)], of trees given by each draft's parent: parent [B, S],
+    an earlier draft of the request, or negative for a draft that follows the context's last token."""
+    import torch
+    if parent.dim() != 2 or parent.dtype not in (torch.int32, torch.int64):
+        _bad("parent must be int32 or int64 of shape (B, S)")
+    b, s = parent.shape
+    if bool((parent >= torch.arange(s, device=parent.device)).any()):
+        _bad("a draft's parent must come before it")
+    masks = torch.zeros(b, s, -(-s // 64), dtype=torch.int64, device=parent.device)
+    at = torch.arange(b, device=parent.device)
+    for t in range(s):
+        p = parent[:, t].long()
+        masks[:, t] = torch.where((p >= 0)[:, None], masks[at, p.clamp_min(0)], 0)
+        masks[:, t, t // 64] |= -2 ** 63 if t % 64 == 63 else 1 << (t % 64)
+    return masks
+
+
+class TreeAttention(PagedAttention):
+    """csa_tree_attn: attention of a tree of S drafted tokens per request over its cache.
+
+    tree [B, S, ceil(S / 64)] int64: bit t % 64 of word t / 64 set where a draft sees draft t, itself included
+    (tree_masks makes them of parents).  count [B] int32: the real drafts of each request, the first of its S (None:
+    all S); they lie in the last rows of its context.  pos [B, S] int32: the drafts' positions, needed with a window.
+    workspace: at least tree_attn_workspace(dim) bytes.  The rest is as in PagedAttention."""
+
+    def __init__(self, q, k, v, ctx_len, tree, count=None, pos=None, table=None, block: int = 0, off=None, k_scale=None,
+                 v_scale=None, win: int = 0, scale: float = 0.0, max_len: int | None = None, out=None, lse=True,
+                 status=None, workspace=None):
+        import torch
+        base, tensors, self._out = self._paged(q, k, v, ctx_len, table, block, off, k_scale, v_scale, win, scale, max_len,
+                                               out, lse, status, workspace, tree_attn_workspace)
+        b, s = int(q.shape[0]), int(q.shape[1])
+        _flat("tree", tree, torch.int64, (b, s, -(-s // 64)))
+        _flat("count", count, torch.int32, (b,))
+        _flat("pos", pos, torch.int32, [(b, s), (b * s,)])
+        if win > 0 and pos is None:
+            _bad("pos is needed with a window")
+        st = CTree(base=base, tree=_ptr(tree), count=_ptr(count), pos=_ptr(pos))
+        self._bind(lib().csa_tree_attn, st, (*tensors, tree, count, pos))
 
 
 def _tokens(name: str, t, lead, heads: int, dim: int, dtype):

@@ -877,8 +877,10 @@ int64_t csa_paged_attn_workspace(int32_t dim) {
   return (int64_t)csa::paged_attn_workspace(dim, sms);
 }
 
-int csa_paged_attn(const csa_paged* a, void* stream) {
-  if (!a) return fail(CSA_ERR_INVALID_ARG, "args is NULL");
+namespace {
+
+// csa_paged_attn's checks and launch; tree: csa_tree_attn's own arguments, whose base a is.
+int run_paged(const csa_paged* a, const csa_tree* tree, void* stream) {
   if (a->kv_dtype != 0 && a->kv_dtype != CSA_DTYPE_BF16 && a->kv_dtype != CSA_DTYPE_FP8_E4M3)
     return fail(CSA_ERR_UNSUPPORTED, "kv_dtype must be CSA_DTYPE_BF16 or CSA_DTYPE_FP8_E4M3");
   const bool fp8 = a->kv_dtype == CSA_DTYPE_FP8_E4M3;
@@ -892,6 +894,7 @@ int csa_paged_attn(const csa_paged* a, void* stream) {
   if (a->win < 0 || a->max_len < 0) return fail(CSA_ERR_INVALID_ARG, "need win >= 0 and max_len >= 0");
   if (a->max_len > csa::kPagedMaxLen || a->S > (1 << 16) || (int64_t)a->S * a->heads > (1 << 20))
     return fail(CSA_ERR_UNSUPPORTED, "max_len above 2^30, S above 2^16 or S * heads above 2^20");
+  if (tree && a->S > csa::kTreeMaxDrafts) return fail(CSA_ERR_UNSUPPORTED, "S above %d", csa::kTreeMaxDrafts);
   if (a->B == 0) { g_err.clear(); return CSA_OK; }
   int rc = check_rows("q", a->q, a->q_stride, (int64_t)a->heads * a->dim, 2);
   if (!rc) rc = check_rows("out", a->out, a->out_stride, (int64_t)a->heads * a->dim, 2);
@@ -916,13 +919,21 @@ int csa_paged_attn(const csa_paged* a, void* stream) {
   for (const P& x : ptrs)
     if (reinterpret_cast<uintptr_t>(x.p) % x.align != 0)
       return fail(CSA_ERR_INVALID_ARG, "%s is not %d-byte aligned", x.n, x.align);
+  if (tree) {
+    if (!tree->tree) return fail(CSA_ERR_INVALID_ARG, "tree is NULL");
+    if (a->win > 0 && !tree->pos) return fail(CSA_ERR_INVALID_ARG, "pos is NULL with a window");
+    const P more[] = {{tree->tree, 8, "tree"}, {tree->count, 4, "count"}, {tree->pos, 4, "pos"}};
+    for (const P& x : more)
+      if (reinterpret_cast<uintptr_t>(x.p) % x.align != 0)
+        return fail(CSA_ERR_INVALID_ARG, "%s is not %d-byte aligned", x.n, x.align);
+  }
   int sms = 0;
   rc = device_sms(&sms);
   if (rc) return rc;
-  if (!a->workspace || a->workspace_bytes < (int64_t)csa::paged_attn_workspace(a->dim, sms))
-    return fail(CSA_ERR_WORKSPACE, "workspace of %lld bytes, need %lld", (long long)a->workspace_bytes,
-                (long long)csa::paged_attn_workspace(a->dim, sms));
-  csa::PagedArgs k;
+  const int64_t need = (int64_t)(tree ? csa::tree_attn_workspace(a->dim, sms) : csa::paged_attn_workspace(a->dim, sms));
+  if (!a->workspace || a->workspace_bytes < need)
+    return fail(CSA_ERR_WORKSPACE, "workspace of %lld bytes, need %lld", (long long)a->workspace_bytes, (long long)need);
+  csa::PagedArgs k = {};
   k.B = a->B; k.S = a->S; k.heads = a->heads; k.kv_heads = a->kv_heads; k.dim = a->dim;
   k.win = a->win >= a->max_len ? 0 : a->win;  // a window over everything is none
   k.max_len = a->max_len;
@@ -935,7 +946,31 @@ int csa_paged_attn(const csa_paged* a, void* stream) {
   k.off = a->off; k.table = a->table; k.block = a->block; k.table_stride = a->table_stride;
   k.out = a->out; k.out_stride = a->out_stride; k.lse = a->lse; k.status = a->status;
   k.workspace = a->workspace;
+  if (tree) {
+    k.tree = reinterpret_cast<const unsigned long long*>(tree->tree);
+    k.words = (a->S + 63) / 64;
+    k.count = tree->count;
+    k.tpos = tree->pos;
+  }
   return finish_free(csa::launch_paged_attn(k, fp8, sms, static_cast<cudaStream_t>(stream), use_pdl()));
+}
+
+}  // namespace
+
+int csa_paged_attn(const csa_paged* a, void* stream) {
+  if (!a) return fail(CSA_ERR_INVALID_ARG, "args is NULL");
+  return run_paged(a, nullptr, stream);
+}
+
+int64_t csa_tree_attn_workspace(int32_t dim) {
+  int sms = 0;
+  if (device_sms(&sms) != CSA_OK) return 0;
+  return (int64_t)csa::tree_attn_workspace(dim, sms);
+}
+
+int csa_tree_attn(const csa_tree* a, void* stream) {
+  if (!a) return fail(CSA_ERR_INVALID_ARG, "args is NULL");
+  return run_paged(&a->base, a, stream);
 }
 
 namespace {

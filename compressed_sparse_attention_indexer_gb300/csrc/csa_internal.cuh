@@ -414,9 +414,14 @@ struct PagedArgs {
   float* lse;
   int* status;
   void* workspace;
+  // trees of drafts (csa_tree_attn): NULL for the plain causal attention
+  const unsigned long long* tree; int words;
+  const int* count; const int* tpos;
 };
 constexpr int kPagedMaxLen = 1 << 30;   // csa_paged.max_len at most
+constexpr int kTreeMaxDrafts = 1024;    // csa_tree: drafts per request at most
 size_t paged_attn_workspace(int dim, int num_sms);
+size_t tree_attn_workspace(int dim, int num_sms);
 int launch_paged_attn(const PagedArgs& a, bool fp8, int num_sms, cudaStream_t st, bool pdl);
 // Heads of new tokens: norm, rotation and the place they go to (csa_qk_rope,
 // csa_kv_append) with checked arguments.  Kinds 0, 1, 2 are queries, keys and

@@ -3,6 +3,8 @@
 // with a scale per row and head, optional sliding window.
 //   pos = L - S + s;  rows max(0, pos - win + 1) .. pos (win = 0: 0 .. pos)
 //   out[s][h] = sum_r softmax_r(scale q[s][h] . k[r]) v[r],  lse = ln sum_r exp(.)
+// and the same of a tree of drafted tokens (kTree), each of which sees the rows
+// before the drafts and those drafts that its bit mask names.
 //
 // HBM bound: a K / V row is read once and serves every query row of its group
 // (S * heads / kv_heads, folded into the M = 16 rows of the warp MMA), so the
@@ -216,12 +218,19 @@ __device__ __forceinline__ int e4m3_piece(int r, int c, int x) { return 32 * c +
 
 // Tiles of a request (at least one, so that every unit is visited and
 // written): the rows any of its S queries sees are [lo, L).
-template <int kTile>
+// A tree's request has n of them, and none with a bad count.
+template <int kTile, bool kTree>
 struct Span {
-  int L, lo, t0, tiles;
-  __device__ __forceinline__ void set(const PagedArgs& a, int len) {
+  int L, lo, t0, tiles, n;
+  __device__ __forceinline__ void set(const PagedArgs& a, int b) {
+    const int len = a.ctx_len[b];
     L = len < 0 || len > a.max_len ? 0 : len;  // a bad length reads nothing
-    const int p0 = L - a.S;
+    n = a.S;
+    if (kTree && a.count) {
+      n = a.count[b];
+      if (n <= 0 || n > a.S) L = 0;
+    }
+    const int p0 = L - n;
     lo = a.win > 0 && p0 - a.win + 1 > 0 ? p0 - a.win + 1 : 0;
     t0 = lo / kTile;
     tiles = (L + kTile - 1) / kTile - t0;
@@ -230,18 +239,30 @@ struct Span {
 };
 
 // Position in the list of tiles: request b, unit (kv head, chunk), tile.
-template <int kTile>
+template <int kTile, bool kTree>
 struct Cursor {
   int b, unit, tile;
-  Span<kTile> sp;
+  Span<kTile, kTree> sp;
   __device__ __forceinline__ void next(const PagedArgs& a, int units) {
     if (++tile < sp.tiles) return;
     tile = 0;
     if (++unit < units) return;
     unit = 0;
-    if (++b < a.B) sp.set(a, a.ctx_len[b]);
+    if (++b < a.B) sp.set(a, b);
   }
 };
+
+// Whether draft s of request b sees draft t of its tree.
+__device__ __forceinline__ bool tree_sees(const PagedArgs& a, int b, int s, int t) {
+  return (a.tree[((int64_t)b * a.S + s) * a.words + (t >> 6)] >> (t & 63)) & 1;
+}
+// The last rows of the window before draft s of request b: rows up to this one are outside it
+// (p: the request's first draft's row, n: its drafts).
+__device__ __forceinline__ int tree_outside(const PagedArgs& a, int b, int s, int p, int n) {
+  if (a.win == 0) return -1;
+  const int at = a.tpos[(int64_t)b * a.S + s];
+  return min(max(at, p), p + n - 1) - a.win;
+}
 
 // The products of a warp's weights with its V rows in shared memory (at vt):
 // pv(mt, x, j, b0, b1) for each 16-row group x and n-tile j, b0 / b1 the
@@ -297,15 +318,15 @@ __device__ __forceinline__ void v_products(uint32_t vt, int lane, F&& pv) {
 // a NaN or an infinity: a pass per token that the product's query rows may
 // be of (sq, ascending; S: no query row) with its own rows kept and its own query rows taken.
 // Out of line, on copies of o and pf: rare, and the common path keeps its registers.
-template <int D, int MT, bool kFp8>
+template <int D, int MT, bool kFp8, bool kTree>
 __device__ __noinline__ void v_products_apart(float* o, const uint32_t* pf, const int* sq, uint32_t vt, int lane, int base,
-                                              int p_first, int S, int win) {
+                                              int p_first, int S, int win, const PagedArgs& a, int b) {
   using Sh = PaShape<D, MT, kFp8>;
   const int c = lane & 3;
   int t = __shfl_sync(0xffffffffu, sq[0], 0);
   if (S > t + 16 * MT) S = t + 16 * MT;
   for (; t < S; ++t) {
-    const int last = p_first + t;
+    const int last = p_first + t, out = kTree ? tree_outside(a, b, t, p_first, S) : 0;
     uint32_t keep[2 * Sh::kGroups];
 #pragma unroll
     for (int n = 0; n < 2 * Sh::kGroups; ++n) {
@@ -313,7 +334,9 @@ __device__ __noinline__ void v_products_apart(float* o, const uint32_t* pf, cons
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
         const int r = base + n * 8 + c * 2 + e;
-        if (r <= last && (win == 0 || r > last - win)) keep[n] |= e ? 0xffff0000u : 0xffffu;
+        const bool sees = kTree ? (r < p_first ? r > out : r < p_first + S && tree_sees(a, b, t, r - p_first))
+                                : r <= last && (win == 0 || r > last - win);
+        if (sees) keep[n] |= e ? 0xffff0000u : 0xffffu;
       }
     }
     v_products<D, MT, kFp8>(vt, lane, [&](int mt, int x, int j, uint32_t b0, uint32_t b1) {
@@ -339,7 +362,7 @@ __device__ __forceinline__ int64_t split_at(int64_t total, int i, int parts) {
   return x < (int64_t(1) << 32) ? (int64_t)((uint32_t)x / (uint32_t)parts) : x / parts;
 }
 
-template <int D, int MT, bool kFp8>
+template <int D, int MT, bool kFp8, bool kTree>
 __global__ void __launch_bounds__(PaShape<D, MT, kFp8>::kThreads, 1)
     paged_attn_kernel(const PagedArgs a, int chunks, int units, float* __restrict__ part, PaJoin* __restrict__ joins) {
   using Sh = PaShape<D, MT, kFp8>;
@@ -369,13 +392,13 @@ __global__ void __launch_bounds__(PaShape<D, MT, kFp8>::kThreads, 1)
   // ---- this CTA's share of the list: of the costs (a unit's tiles and one
   // more for its start and end), with the cuts moved to the next whole tile
   const bool once = a.B <= Sh::kThreads;   // one request per thread: scanned once
-  Span<kTile> sp;
+  Span<kTile, kTree> sp;
   PaCost n = 0, sum, ahead = 0;
   int len = 0;
   int64_t total = 0;
   for (int b0 = 0; b0 < a.B; b0 += Sh::kThreads) {
     n = 0;
-    if (b0 + tid < a.B) len = a.ctx_len[b0 + tid], sp.set(a, len), n = sp.tiles + 1;
+    if (b0 + tid < a.B) len = a.ctx_len[b0 + tid], sp.set(a, b0 + tid), n = sp.tiles + 1;
     ahead = block_exclusive_scan(n, scan_tmp, &sum);
     total += sum;
   }
@@ -390,10 +413,11 @@ __global__ void __launch_bounds__(PaShape<D, MT, kFp8>::kThreads, 1)
   for (int b0 = 0; b0 < a.B; b0 += Sh::kThreads) {
     if (!once) {
       n = 0;
-      if (b0 + tid < a.B) len = a.ctx_len[b0 + tid], sp.set(a, len), n = sp.tiles + 1;
+      if (b0 + tid < a.B) len = a.ctx_len[b0 + tid], sp.set(a, b0 + tid), n = sp.tiles + 1;
       ahead = block_exclusive_scan(n, scan_tmp, &sum);
     }
-    if (blockIdx.x == 0 && a.status && b0 + tid < a.B && (len < 0 || len > a.max_len))
+    if (blockIdx.x == 0 && a.status && b0 + tid < a.B &&
+        (len < 0 || len > a.max_len || (kTree && a.count && (sp.n < 0 || sp.n > a.S))))
       set_status(a.status, kStatusBadIndex);
     const int64_t p = (before + (int64_t)ahead) * units;
 #pragma unroll
@@ -418,20 +442,20 @@ __global__ void __launch_bounds__(PaShape<D, MT, kFp8>::kThreads, 1)
     if (tid == 0) joins[blockIdx.x].count = 0;
     return;
   }
-  Cursor<kTile> ld;  // the loader's position, several tiles ahead of the products
+  Cursor<kTile, kTree> ld;  // the loader's position, several tiles ahead of the products
   ld.b = cut_sh[0].b;
-  ld.sp.set(a, a.ctx_len[ld.b]);
+  ld.sp.set(a, ld.b);
   ld.unit = cut_sh[0].unit;
   ld.tile = cut_sh[0].tile;
   if (tid == 0) total_sh = total, unit_at = cut_sh[0].first;
-  Cursor<kTile> cu = ld;
+  Cursor<kTile, kTree> cu = ld;
   int loaded = 0;
 
   // ---- row copies: lane r < kPer looks up the pool row of the warp's row r one
   // tile ahead of the copies that use it.  A table's entry stays as it was
   // loaded until then, so that nothing waits for it earlier (E4M3: 329 us to 311).
   int entry = -1, within = 0;
-  auto lookup = [&](const Cursor<kTile>& c) {
+  auto lookup = [&](const Cursor<kTile, kTree>& c) {
     const int r = (c.sp.t0 + c.tile) * kTile + warp * kPer + lane;
     within = -1;                                   // nothing to read
     if (lane < kPer && r >= c.sp.lo && r < c.sp.L) {
@@ -683,8 +707,8 @@ __global__ void __launch_bounds__(PaShape<D, MT, kFp8>::kThreads, 1)
         }
       }
       // ---- scores in log2 units; rows outside a query's range weigh nothing
-      const int p_first = cu.sp.L - a.S;   // the first token's position
-      const bool edge = base < cu.sp.lo || base + kPer - 1 > p_first ||
+      const int p_first = cu.sp.L - (kTree ? cu.sp.n : a.S);   // the first token's position
+      const bool edge = base < cu.sp.lo || base + kPer - 1 > p_first - (kTree ? 1 : 0) ||
                         (a.win > 0 && base < cu.sp.L - a.win);  // some query does not see all the rows
       uint32_t pf[MT][kGroups][4];
 #pragma unroll
@@ -712,6 +736,25 @@ __global__ void __launch_bounds__(PaShape<D, MT, kFp8>::kThreads, 1)
           for (int e = 0; e < 2; ++e) {
             const int i = row0 + mt * 16 + g + 8 * e;
             pos[e] = i < qrows ? p_first + token_of(i) : -1;
+          }
+          if constexpr (kTree) {
+            int token[2], out[2];
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              const int i = row0 + mt * 16 + g + 8 * e;
+              token[e] = i < qrows ? token_of(i) : cu.sp.n;
+              out[e] = token[e] < cu.sp.n ? tree_outside(a, cu.b, token[e], p_first, cu.sp.n) : cu.sp.L;
+            }
+#pragma unroll
+            for (int n = 0; n < 2 * kGroups; ++n)
+#pragma unroll
+              for (int i = 0; i < 4; ++i) {
+                const int r = base + n * 8 + c * 2 + (i & 1), s1 = token[i >> 1];
+                const bool sees = r < p_first ? r > out[i >> 1]
+                                              : r < cu.sp.L && s1 < cu.sp.n && tree_sees(a, cu.b, s1, r - p_first);
+                if (!sees) s[mt][n][i] = -INFINITY;
+              }
+            continue;
           }
 #pragma unroll
           for (int n = 0; n < 2 * kGroups; ++n)
@@ -820,7 +863,8 @@ __global__ void __launch_bounds__(PaShape<D, MT, kFp8>::kThreads, 1)
             const int i = row0 + mt * 16 + g + 8 * e;
             sq2[mt][e] = i < qrows ? token_of(i) : a.S;
           }
-        v_products_apart<D, MT, kFp8>(&o2[0][0][0], &pf2[0][0][0], &sq2[0][0], vt, lane, base, p_first, a.S, a.win);
+        v_products_apart<D, MT, kFp8, kTree>(&o2[0][0][0], &pf2[0][0][0], &sq2[0][0], vt, lane, base, p_first,
+                                             kTree ? cu.sp.n : a.S, a.win, a, cu.b);
         memcpy(o, o2, sizeof o);
       }
     }
@@ -935,13 +979,14 @@ __global__ void __launch_bounds__(PaShape<D, MT, kFp8>::kThreads, 1)
         }
         if (whole) {
           const int i = row0 + r, s = token_of(i), hd = h * group + i - s * group;
-          const bool any = sum > 0.f || sum != sum;   // some row weighs (a NaN is passed on)
+          // some row weighs (a NaN is passed on)
+          const bool any = (sum > 0.f || sum != sum) && (!kTree || s < cu.sp.n);
           const float inv = any ? 1.f / sum : 0.f;
           __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(a.out) + ((int64_t)cu.b * a.S + s) * a.out_stride + hd * D +
                                lane * (D / 32);
 #pragma unroll
           for (int x = 0; x < D / 32; x += 2)
-            *reinterpret_cast<uint32_t*>(dst + x) = pack_bf16x2(acc[x] * inv, acc[x + 1] * inv);
+            *reinterpret_cast<uint32_t*>(dst + x) = kTree && !any ? 0u : pack_bf16x2(acc[x] * inv, acc[x + 1] * inv);
           if (a.lse && lane == 0)
             a.lse[((int64_t)cu.b * a.S + s) * a.heads + hd] = any ? (top + log2f(sum)) * kLn2 : -INFINITY;
         } else {
@@ -976,7 +1021,7 @@ __global__ void __launch_bounds__(PaShape<D, MT, kFp8>::kThreads, 1)
 // Joins the pieces of the units cut between CTAs: block (x, y) does query row
 // y of the unit that starts in CTA x, its warps a part of the pieces each.
 constexpr int kJoinWarps = 8;
-template <int D, bool kFp8>
+template <int D, bool kFp8, bool kTree>
 __global__ void __launch_bounds__(32 * kJoinWarps)
     paged_join_kernel(const PagedArgs a, int chunks, int rows, const float* __restrict__ part,
                       const PaJoin* __restrict__ joins) {
@@ -1016,8 +1061,8 @@ __global__ void __launch_bounds__(32 * kJoinWarps)
     f[w] = fast_exp2(sm_m[w] - ref);
     sum += kFp8 ? move_sum(sm_l[w], sm_m[w] - ref) : sm_l[w] * f[w];
   }
-  const bool any = sum > 0.f || sum != sum;
   const int s = i / group, hd = h * group + i - s * group;
+  const bool any = (sum > 0.f || sum != sum) && (!kTree || !a.count || s < a.count[j.b]);
   const int64_t tok = (int64_t)j.b * a.S + s;
   if (threadIdx.x < D) {
     const int d = threadIdx.x;
@@ -1029,10 +1074,10 @@ __global__ void __launch_bounds__(32 * kJoinWarps)
   if (a.lse && threadIdx.x == 0) a.lse[tok * a.heads + hd] = any ? (top + log2f(sum)) * kLn2 : -INFINITY;
 }
 
-template <int D, int MT, bool kFp8>
+template <int D, int MT, bool kFp8, bool kTree>
 int launch_shape(const PagedArgs& a, int num_sms, cudaStream_t st, bool pdl) {
   using Sh = PaShape<D, MT, kFp8>;
-  auto kern = paged_attn_kernel<D, MT, kFp8>;
+  auto kern = paged_attn_kernel<D, MT, kFp8, kTree>;
   static PerDeviceOnce attr;
   if (const cudaError_t e = attr.run([&] { return allow_max_dynamic_smem(kern); }))
     return launch_fail("cudaFuncSetAttribute(paged_attn_kernel)", e);
@@ -1048,7 +1093,7 @@ int launch_shape(const PagedArgs& a, int num_sms, cudaStream_t st, bool pdl) {
   const int span = a.win > 0 && a.win + a.S - 1 < a.max_len ? a.win + a.S - 1 + Sh::kTile - 1 : a.max_len;
   if (span <= Sh::kTile) return r;
   const int rows = qrows < Sh::kRows ? qrows : Sh::kRows;
-  const int r2 = launch_kernel(paged_join_kernel<D, kFp8>, dim3(grid, rows), dim3(32 * kJoinWarps), 0, st, pdl, a, chunks,
+  const int r2 = launch_kernel(paged_join_kernel<D, kFp8, kTree>, dim3(grid, rows), dim3(32 * kJoinWarps), 0, st, pdl, a, chunks,
                                (int)Sh::kRows, (const float*)part, (const PaJoin*)joins);
   return r2 < 0 ? r2 : r + r2;
 }
@@ -1060,14 +1105,25 @@ size_t paged_attn_workspace(int dim, int num_sms) {
   return (size_t)num_sms * (2 * 32 * (dim + 2) * sizeof(float) + sizeof(PaJoin));
 }
 
-int launch_paged_attn(const PagedArgs& a, bool fp8, int num_sms, cudaStream_t st, bool pdl) {
+size_t tree_attn_workspace(int dim, int num_sms) { return paged_attn_workspace(dim, num_sms); }
+
+template <bool kTree>
+static int launch_warps(const PagedArgs& a, bool fp8, int num_sms, cudaStream_t st, bool pdl) {
   const bool two = a.S * (a.heads / a.kv_heads) > 16;
-  if (fp8) return two ? launch_shape<128, 2, true>(a, num_sms, st, pdl) : launch_shape<128, 1, true>(a, num_sms, st, pdl);
+  if (fp8)
+    return two ? launch_shape<128, 2, true, kTree>(a, num_sms, st, pdl) : launch_shape<128, 1, true, kTree>(a, num_sms, st, pdl);
   switch (a.dim) {
-    case 64: return two ? launch_shape<64, 2, false>(a, num_sms, st, pdl) : launch_shape<64, 1, false>(a, num_sms, st, pdl);
-    case 128: return two ? launch_shape<128, 2, false>(a, num_sms, st, pdl) : launch_shape<128, 1, false>(a, num_sms, st, pdl);
-    default: return launch_shape<256, 1, false>(a, num_sms, st, pdl);
+    case 64:
+      return two ? launch_shape<64, 2, false, kTree>(a, num_sms, st, pdl) : launch_shape<64, 1, false, kTree>(a, num_sms, st, pdl);
+    case 128:
+      return two ? launch_shape<128, 2, false, kTree>(a, num_sms, st, pdl)
+                 : launch_shape<128, 1, false, kTree>(a, num_sms, st, pdl);
+    default: return launch_shape<256, 1, false, kTree>(a, num_sms, st, pdl);
   }
+}
+
+int launch_paged_attn(const PagedArgs& a, bool fp8, int num_sms, cudaStream_t st, bool pdl) {
+  return a.tree ? launch_warps<true>(a, fp8, num_sms, st, pdl) : launch_warps<false>(a, fp8, num_sms, st, pdl);
 }
 
 }  // namespace csa

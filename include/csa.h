@@ -479,6 +479,33 @@ typedef struct {
  * 4096 heads). */
 CSA_API int csa_kv_append(const csa_append *a, void *stream);
 
+/* Attention of a tree of drafted tokens over a cache: csa_paged_attn for S drafts per
+ * request that are not one chain.  Request b has n_b = count[b] drafts (S without
+ * count), its first n_b queries; they lie in the last n_b rows of its cache, draft t in
+ * row L_b - n_b + t.  Draft s sees every row r < L_b - n_b before them, with a window
+ * those with r > p - win only, p = pos[b * S + s] (taken to the nearest of L_b - n_b ..
+ * L_b - 1), and of the drafts' rows those whose bit is set in its mask: draft t is bit
+ * t % 64 of word t / 64 of tree[b * S + s], its own bit included.  Bits from n_b on are
+ * not read.  out and lse of queries that see no row, or that are not among the n_b, are
+ * zeros and -inf.  Everything else is as in csa_paged: base.win is the window, base.S
+ * the drafts per request (at most 1024), and the sums, roundings, refusals and the
+ * workspace are its own. */
+typedef struct {
+    csa_paged base;
+    const uint64_t *tree;     /* [B, S, ceil(S / 64)]                               */
+    const int32_t *count;     /* [B] in [0, S], or NULL; outside sets bit 0 of *status and
+                                 counts as 0                                        */
+    const int32_t *pos;       /* [B * S], needed with a window                      */
+} csa_tree;
+
+/* As csa_paged_attn; base.workspace holds csa_tree_attn_workspace() bytes.
+ * CSA_ERR_UNSUPPORTED for S above 1024 too. */
+CSA_API int csa_tree_attn(const csa_tree *a, void *stream);
+
+/* Bytes of workspace csa_tree_attn needs on the current device for heads of `dim`
+ * elements, whatever the batch; 0 when the device cannot be asked. */
+CSA_API int64_t csa_tree_attn_workspace(int32_t dim);
+
 /* Host-side checks of a batch against a config, exactly those every entry
  * point runs before launching (null / misaligned pointers, strides, sizes
  * against the maxima, ctx_len_host values).  Touches no device memory and
