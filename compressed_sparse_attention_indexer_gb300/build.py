@@ -19,7 +19,7 @@ BUILD = os.path.join(HERE, "_build", platform.machine())
 LIB_PATH = os.path.join(HERE, "_build", f"libcsa_{platform.machine()}.so")
 SOURCES = ["api.cu", "plan.cu", "indexer.cu", "indexer_tc5.cu", "topk.cu", "attention.cu", "attention_tc5.cu",
            "writeback.cu", "norm.cu",
-           "fp8_matmul.cu", "paged_attn.cu", "rope.cu"]
+           "fp8_matmul.cu", "paged_attn.cu", "rope.cu", "tree_attn.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-Xcompiler", "-fvisibility=hidden",
          "--expt-relaxed-constexpr"]

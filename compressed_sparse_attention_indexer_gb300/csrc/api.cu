@@ -952,7 +952,8 @@ int run_paged(const csa_paged* a, const csa_tree* tree, void* stream) {
     k.count = tree->count;
     k.tpos = tree->pos;
   }
-  return finish_free(csa::launch_paged_attn(k, fp8, sms, static_cast<cudaStream_t>(stream), use_pdl()));
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  return finish_free(tree ? csa::launch_tree_attn(k, fp8, sms, st, use_pdl()) : csa::launch_paged_attn(k, fp8, sms, st, use_pdl()));
 }
 
 }  // namespace

@@ -423,6 +423,7 @@ constexpr int kTreeMaxDrafts = 1024;    // csa_tree: drafts per request at most
 size_t paged_attn_workspace(int dim, int num_sms);
 size_t tree_attn_workspace(int dim, int num_sms);
 int launch_paged_attn(const PagedArgs& a, bool fp8, int num_sms, cudaStream_t st, bool pdl);
+int launch_tree_attn(const PagedArgs& a, bool fp8, int num_sms, cudaStream_t st, bool pdl);
 // Heads of new tokens: norm, rotation and the place they go to (csa_qk_rope,
 // csa_kv_append) with checked arguments.  Kinds 0, 1, 2 are queries, keys and
 // values; strides in elements, from one token or pool row to the next.

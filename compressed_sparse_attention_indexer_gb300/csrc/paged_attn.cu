@@ -49,17 +49,14 @@
 // prompt (4096 tokens of 4096 rows, 32 / 8 heads: 1963 us against 73; every chunk of
 // query rows streams all rows, windows or not) and many short units (64 tokens with a
 // window of 128 rows: 20 us against 5).
-#include <limits>
-
 #include "csa_internal.cuh"
+#include "paged.cuh"
 #include "ptx.cuh"
 
 namespace csa {
 
 namespace {
 
-constexpr float kLog2e = 1.4426950408889634f;
-constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kRescaleAbove = 8.f;  // the reference maximum moves when exceeded by this (log2 units)
 // E4M3: the reference is set this far below the maximum, so that the f16 weights use
 // f16's range: up to 2^15, and off by at most 2^-25, 2^-32 of the largest, where they
@@ -72,8 +69,6 @@ constexpr float kWeightTop = 7.f;
 // largest term.
 constexpr float kNear = 24.f;
 constexpr float kMinScale = 3.2311743e-27f;  // 2^-88: smaller V scales count so in the exponent
-
-using PaCost = uint32_t;  // of the units of one kv head and chunk of as many requests as a block has threads
 
 template <int D, int MT, bool kFp8>
 struct PaShape {
@@ -110,19 +105,6 @@ struct PaShape {
   static_assert((uint64_t)kThreads * (kPagedMaxLen / kTile + 2) <= std::numeric_limits<PaCost>::max(), "sum of costs");
 };
 
-// What a CTA leaves for the join of the unit that starts in it and goes on in
-// the next CTAs (count = 0: none).
-struct PaJoin {
-  int count;         // CTAs that hold a piece
-  int slot;          // the first piece's slot in this CTA (0 or 1)
-  int b, unit;
-};
-
-__device__ __forceinline__ float fast_exp2(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;\n" : "=f"(y) : "f"(x));
-  return y;
-}
 // The same with results below 2^-126 kept.
 __device__ __forceinline__ float tiny_exp2(float x) {
   float y;
@@ -136,12 +118,6 @@ __device__ __forceinline__ float tiny_exp2(float x) {
 __device__ __forceinline__ float move_sum(float l, float d) {
   const float f = fast_exp2(0.5f * d);
   return l * f * f;
-}
-// Four E4M3 codes (low byte first) to two f16x2: every E4M3 value is an f16 value.
-__device__ __forceinline__ void e4m3x4_to_f16x2(uint32_t w, uint32_t& lo, uint32_t& hi) {
-  asm("{\n .reg .b16 a, b;\n mov.b32 {a, b}, %2;\n cvt.rn.f16x2.e4m3x2 %0, a;\n cvt.rn.f16x2.e4m3x2 %1, b;\n}\n"
-      : "=r"(lo), "=r"(hi)
-      : "r"(w));
 }
 // D += A(16x16 f16, row) * B(16x8 f16, col), fp32 accumulate.
 __device__ __forceinline__ void mma_f16_16816(float* d, const uint32_t* a, uint32_t b0, uint32_t b1) {
@@ -174,9 +150,6 @@ __device__ __forceinline__ float fast_log2(float x) {
   float y;
   asm("lg2.approx.ftz.f32 %0, %1;\n" : "=f"(y) : "f"(x));
   return y;
-}
-__device__ __forceinline__ void cp_async4(uint32_t dst, const void* src, int src_bytes) {
-  asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;\n" ::"r"(dst), "l"(src), "r"(src_bytes) : "memory");
 }
 __device__ __forceinline__ float lds_f32(uint32_t a) {
   float v;
@@ -215,54 +188,6 @@ __device__ __forceinline__ int swizzle(int row, int ch) {
 // pieces of the four threads of a quad, and of neighbouring rows, fall on
 // different banks.
 __device__ __forceinline__ int e4m3_piece(int r, int c, int x) { return 32 * c + ((x ^ c ^ ((r & 1) << 2)) << 2); }
-
-// Tiles of a request (at least one, so that every unit is visited and
-// written): the rows any of its S queries sees are [lo, L).
-// A tree's request has n of them, and none with a bad count.
-template <int kTile, bool kTree>
-struct Span {
-  int L, lo, t0, tiles, n;
-  __device__ __forceinline__ void set(const PagedArgs& a, int b) {
-    const int len = a.ctx_len[b];
-    L = len < 0 || len > a.max_len ? 0 : len;  // a bad length reads nothing
-    n = a.S;
-    if (kTree && a.count) {
-      n = a.count[b];
-      if (n <= 0 || n > a.S) L = 0;
-    }
-    const int p0 = L - n;
-    lo = a.win > 0 && p0 - a.win + 1 > 0 ? p0 - a.win + 1 : 0;
-    t0 = lo / kTile;
-    tiles = (L + kTile - 1) / kTile - t0;
-    if (tiles < 1) tiles = 1;
-  }
-};
-
-// Position in the list of tiles: request b, unit (kv head, chunk), tile.
-template <int kTile, bool kTree>
-struct Cursor {
-  int b, unit, tile;
-  Span<kTile, kTree> sp;
-  __device__ __forceinline__ void next(const PagedArgs& a, int units) {
-    if (++tile < sp.tiles) return;
-    tile = 0;
-    if (++unit < units) return;
-    unit = 0;
-    if (++b < a.B) sp.set(a, b);
-  }
-};
-
-// Whether draft s of request b sees draft t of its tree.
-__device__ __forceinline__ bool tree_sees(const PagedArgs& a, int b, int s, int t) {
-  return (a.tree[((int64_t)b * a.S + s) * a.words + (t >> 6)] >> (t & 63)) & 1;
-}
-// The last rows of the window before draft s of request b: rows up to this one are outside it
-// (p: the request's first draft's row, n: its drafts).
-__device__ __forceinline__ int tree_outside(const PagedArgs& a, int b, int s, int p, int n) {
-  if (a.win == 0) return -1;
-  const int at = a.tpos[(int64_t)b * a.S + s];
-  return min(max(at, p), p + n - 1) - a.win;
-}
 
 // The products of a warp's weights with its V rows in shared memory (at vt):
 // pv(mt, x, j, b0, b1) for each 16-row group x and n-tile j, b0 / b1 the
@@ -350,18 +275,6 @@ __device__ __noinline__ void v_products_apart(float* o, const uint32_t* pf, cons
   }
 }
 
-// A cut of the list of tiles: before this tile of this unit.
-struct Cut {
-  int b, unit, tile;
-  int64_t first, at;   // the unit's start in the list of costs, the tiles before the cut
-};
-
-// i * total / parts (a 32-bit division where that holds it).
-__device__ __forceinline__ int64_t split_at(int64_t total, int i, int parts) {
-  const int64_t x = total * i;
-  return x < (int64_t(1) << 32) ? (int64_t)((uint32_t)x / (uint32_t)parts) : x / parts;
-}
-
 template <int D, int MT, bool kFp8, bool kTree>
 __global__ void __launch_bounds__(PaShape<D, MT, kFp8>::kThreads, 1)
     paged_attn_kernel(const PagedArgs a, int chunks, int units, float* __restrict__ part, PaJoin* __restrict__ joins) {
@@ -391,52 +304,11 @@ __global__ void __launch_bounds__(PaShape<D, MT, kFp8>::kThreads, 1)
 
   // ---- this CTA's share of the list: of the costs (a unit's tiles and one
   // more for its start and end), with the cuts moved to the next whole tile
-  const bool once = a.B <= Sh::kThreads;   // one request per thread: scanned once
-  Span<kTile, kTree> sp;
-  PaCost n = 0, sum, ahead = 0;
-  int len = 0;
-  int64_t total = 0;
-  for (int b0 = 0; b0 < a.B; b0 += Sh::kThreads) {
-    n = 0;
-    if (b0 + tid < a.B) len = a.ctx_len[b0 + tid], sp.set(a, b0 + tid), n = sp.tiles + 1;
-    ahead = block_exclusive_scan(n, scan_tmp, &sum);
-    total += sum;
-  }
-  total *= units;
-  const int64_t G = total < gridDim.x ? total : gridDim.x;
-  if (blockIdx.x >= G) {
+  int64_t total, G;
+  if (!paged_cuts<kTile, kTree, Sh::kThreads, 1>(a, units, scan_tmp, cut_sh, total, G)) {
     if (tid == 0) joins[blockIdx.x].count = 0;
     return;
   }
-  const int64_t cut[2] = {split_at(total, blockIdx.x, (int)G), split_at(total, blockIdx.x + 1, (int)G)};
-  int64_t before = 0;
-  for (int b0 = 0; b0 < a.B; b0 += Sh::kThreads) {
-    if (!once) {
-      n = 0;
-      if (b0 + tid < a.B) len = a.ctx_len[b0 + tid], sp.set(a, b0 + tid), n = sp.tiles + 1;
-      ahead = block_exclusive_scan(n, scan_tmp, &sum);
-    }
-    if (blockIdx.x == 0 && a.status && b0 + tid < a.B &&
-        (len < 0 || len > a.max_len || (kTree && a.count && (sp.n < 0 || sp.n > a.S))))
-      set_status(a.status, kStatusBadIndex);
-    const int64_t p = (before + (int64_t)ahead) * units;
-#pragma unroll
-    for (int e = 0; e < 2; ++e)
-      // (the list's end belongs to its last request)
-      if (n > 0 && p <= cut[e] && (cut[e] < p + (int64_t)n * units || b0 + tid == a.B - 1)) {
-        const int64_t at = cut[e] - p;
-        const int unit = at < (1u << 31) ? (int)((uint32_t)at / n) : (int)(at / n);
-        const int x = (int)(at - (int64_t)unit * n);
-        cut_sh[e].b = b0 + tid;
-        cut_sh[e].unit = unit;
-        cut_sh[e].tile = x > 0 ? x - 1 : 0;
-        cut_sh[e].first = p + (int64_t)unit * n;
-        // tiles before it in the whole list
-        cut_sh[e].at = p - (int64_t)(b0 + tid) * units + (int64_t)unit * sp.tiles + cut_sh[e].tile;
-      }
-    before += sum;
-  }
-  __syncthreads();
   const int steps = (int)(cut_sh[1].at - cut_sh[0].at);
   if (steps == 0) {
     if (tid == 0) joins[blockIdx.x].count = 0;
@@ -1104,8 +976,6 @@ int launch_shape(const PagedArgs& a, int num_sms, cudaStream_t st, bool pdl) {
 size_t paged_attn_workspace(int dim, int num_sms) {
   return (size_t)num_sms * (2 * 32 * (dim + 2) * sizeof(float) + sizeof(PaJoin));
 }
-
-size_t tree_attn_workspace(int dim, int num_sms) { return paged_attn_workspace(dim, num_sms); }
 
 template <bool kTree>
 static int launch_warps(const PagedArgs& a, bool fp8, int num_sms, cudaStream_t st, bool pdl) {

@@ -1,0 +1,883 @@
+// Attention of trees of drafted tokens over paged K / V pools on the fifth-
+// generation tensor cores, for requests whose drafts and heads make more query
+// rows per kv head than the warps' MMA takes at once (csa_tree_attn; see
+// launch_tree_attn for the rule).
+//   out[s][h] = sum_r softmax_r(scale q[s][h] . k[r]) v[r],  lse = ln sum_r exp(.)
+// over the rows before the drafts (the window's) and the drafts in s's mask.
+//
+// A K / V row pair serves all S * heads / kv_heads query rows of its kv head: up
+// to about 290 of them the rows' bytes bound it, above that the products (and
+// their exponentials).  So 128 query rows make the M of a product, and up to 256
+// share a tile of 128 K / V rows.
+//
+// One CTA per SM takes an even share of the list of tiles (paged_cuts).  Two
+// slots of tensor memory hold 128 x 128 scores each, over which their bf16 weights
+// are written, and 128 x D of output.  kRows = 256: a slot is a half of the query
+// rows, both take every tile.  kRows = 128: the slots take tiles in turn and are
+// joined at a piece's end.  Either way one slot's products run under the other's
+// softmax:
+//   warps 0-3, 4-7   softmax of slot 0 and 1: a thread per query row, its 128 scores
+//                    in registers, so that maxima and sums need no exchange; the
+//                    reference maximum moves only when exceeded by 2^8 (the output is
+//                    then rescaled in place);
+//   warps 8-11       gather the rows by 16-byte cp.async into a ring of 128-byte
+//                    swizzled stages (K and V alike: V is read as an MN-major
+//                    operand), several ahead, across units.  E4M3 codes land beside
+//                    the ring and are converted by the thread that copied them;
+//   warp 12          issues the MMAs: S = Q K^T, O += P V (P from tensor memory);
+//   warps 13-15      the unit's query rows.
+//
+// Masks.  A tile that some draft does not see whole (the window's first rows,
+// the drafts') is an edge tile: each thread builds the 128 bits of its row and
+// takes masked scores as -inf, whatever they hold.  V rows with a NaN or an
+// infinity there are zeroed in shared memory and added by hand, to the drafts
+// that see them (add_apart).
+//
+// Scores, maxima, sums and output are fp32; the weights are rounded to bf16 for
+// the product with V, E4M3 ones after they took V's scale (bf16 has the range of
+// fp32, so no scale makes them vanish).
+#include "csa_internal.cuh"
+#include "paged.cuh"
+#include "ptx.cuh"
+#include "tc5.cuh"
+
+namespace csa {
+
+namespace {
+
+constexpr int kTtThreads = 512;
+constexpr int kLoadWarp = 8, kLoadWarps = 4, kMmaWarp = 12, kQWarp = 13, kQThreads = 96;
+constexpr int kRegsSoftmax = 184, kRegsOthers = 72;   // of the launch's 128 per thread
+constexpr int kTile = 128;                 // K / V rows per tile
+constexpr int kExtra = 2;                  // a unit's start and end, in tiles
+constexpr int kSub = kTile * 128;          // 128 rows x 64 dims bf16
+constexpr float kGrow = 8.f;               // the reference maximum moves when exceeded by this (log2 units)
+constexpr int kScaleTiles = 8;             // tiles whose E4M3 scales are held
+constexpr int kScaleBytes = kTile * 2 * 4; // K's and V's of a tile
+
+struct TtSmem {
+  uint64_t full[8], empty[8];              // stages of the ring
+  uint64_t s_full[2], p_full[2], o_full[2];
+  uint64_t q_full, q_empty, sc_full[kScaleTiles], pair, done;
+  uint32_t tmem;
+  int abort;
+  PaCost scan[33];
+  Cut cut[2];
+  uint32_t bad[8][4];                      // per stage: V rows with a NaN or an infinity
+  float ml[2][2][128];                     // per slot: maxima and sums, for the join of two slots
+};
+
+template <int D, int kRows, bool kFp8>
+struct TtShape {
+  static constexpr int kSubs = D / 64;
+  static constexpr int kStage = kSubs * kSub;
+  static constexpr int kQBytes = kRows / 128 * kStage;
+  static constexpr int kRawDepth = kFp8 ? 3 : 1;   // chunks of codes beside the ring
+  static constexpr int kRaw = kFp8 ? kTile * D : 0;
+  static constexpr int kScales = kFp8 ? kScaleTiles * kScaleBytes : 0;
+  static constexpr int kRoom = (227 * 1024 - (int)sizeof(TtSmem) - kQBytes - kRawDepth * kRaw - kScales) / kStage;
+  static constexpr int kStages = kRoom > 8 ? 8 : kRoom;
+  static constexpr int kDepth = kFp8 ? kRawDepth - 1 : kStages - 2;   // chunks in flight behind the newest
+  static constexpr int kSmem = kQBytes + kStages * kStage + kRawDepth * kRaw + kScales + (int)sizeof(TtSmem);
+  static_assert(kStages >= 3 && kDepth >= 1, "ring");
+  // a tile's scales stay until its weights are made: the loaders are at most
+  // (kRawDepth + kStages + 1) / 2 + 1 tiles ahead of that (see the scales' ring)
+  static_assert(!kFp8 || (kRawDepth + kStages + 1) / 2 + 1 < kScaleTiles, "scales");
+};
+
+// One piece: consecutive tiles of a unit that this CTA takes.
+struct Piece {
+  Span<kTile, true> sp;
+  int b, unit, tile, nt;
+  bool whole, first;                       // all of the unit's tiles; from the unit's first on
+};
+struct Walk {
+  Cursor<kTile, true> cu;
+  int left;
+  __device__ __forceinline__ void init(const PagedArgs& a, const Cut* cut) {
+    cu.b = cut[0].b;
+    cu.sp.set(a, cu.b);
+    cu.unit = cut[0].unit;
+    cu.tile = cut[0].tile;
+    left = (int)(cut[1].at - cut[0].at);
+  }
+  __device__ __forceinline__ bool next(const PagedArgs& a, int units, Piece& p) {
+    if (left == 0) return false;
+    p.sp = cu.sp;
+    p.b = cu.b;
+    p.unit = cu.unit;
+    p.tile = cu.tile;
+    p.nt = min(cu.sp.tiles - cu.tile, left);
+    p.first = cu.tile == 0;
+    p.whole = p.nt == cu.sp.tiles;
+    left -= p.nt;
+    cu.tile += p.nt - 1;
+    if (left > 0) cu.next(a, units);
+    return true;
+  }
+};
+
+// Whether some draft sees only a part of tile t's rows.
+__device__ __forceinline__ bool edge_tile(const PagedArgs& a, const Span<kTile, true>& sp, int t) {
+  const int base = (sp.t0 + t) * kTile;
+  return base < sp.lo || base + kTile > sp.L - sp.n || (a.win > 0 && base < sp.L - a.win);
+}
+
+// 32 rows' bits from row c0 on, for a draft: rows up to `out` are outside its window,
+// the drafts start at row p and are n, `bits` are its mask's 32-bit words.
+__device__ __forceinline__ uint32_t seen32(int c0, int out, int p, int n, const uint32_t* bits, int words32) {
+  auto ones = [](int lo, int hi) -> uint32_t {   // bits lo .. hi - 1, either end anywhere
+    lo = max(lo, 0);
+    hi = min(hi, 32);
+    return hi <= lo ? 0u : (hi == 32 ? 0xffffffffu : (1u << hi) - 1u) & ~((1u << lo) - 1u);
+  };
+  uint32_t v = ones(out + 1 - c0, p - c0);
+  const int t = c0 - p;                          // draft at the first bit
+  if (t > -32 && t < n) {
+    uint32_t w;
+    if (t < 0) {
+      w = bits[0] << -t;
+    } else {
+      const int i = t >> 5;
+      w = __funnelshift_r(bits[i], i + 1 < words32 ? bits[i + 1] : 0u, t & 31);
+    }
+    v |= w & ones(-t, n - t);
+  }
+  return v;
+}
+
+__device__ __forceinline__ uint64_t sdesc_mn_sw128(uint32_t saddr, uint32_t lbo) {
+  return tc5::sdesc_k_sw128(saddr) - ((uint64_t)1u << 16) + ((uint64_t)((lbo >> 4) & 0x3FFFu) << 16);
+}
+__device__ __forceinline__ bool not_finite(uint32_t bf16_bits) { return (bf16_bits & 0x7f80u) == 0x7f80u; }
+
+// A wait that a whole warp makes: true when every lane saw the phase.
+__device__ __forceinline__ bool warp_wait(uint64_t& bar, uint32_t parity, volatile int* abort) {
+  return __all_sync(0xffffffffu, tc5::mbar_wait_backoff(smem_u32(&bar), parity, abort, 64));
+}
+template <int N>
+__device__ __forceinline__ void setmaxnreg_inc() {
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;\n" ::"n"(N));
+}
+template <int N>
+__device__ __forceinline__ void setmaxnreg_dec() {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;\n" ::"n"(N));
+}
+
+// The part of an edge tile's V rows that was zeroed: rows `bad` (four words), added to
+// the output of the threads whose row sees them.  Rare, out of line.
+template <int D, bool kFp8>
+__device__ __noinline__ void add_apart(const PagedArgs& a, int b, int h, int base, const uint32_t* bad, const uint32_t* seen,
+                                       uint32_t p_at, uint32_t o_at) {
+#pragma unroll 1
+  for (int r = 0; r < kTile; ++r) {
+    if (!((bad[r >> 5] >> (r & 31)) & 1)) continue;
+    const int64_t row = pool_row(a.table, a.block, a.table_stride, a.off, b, base + r);
+    if (row < 0 || row >= a.rows) continue;
+    uint32_t w;
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x1.b32 {%0}, [%1];\n tcgen05.wait::ld.sync.aligned;\n" : "=r"(w) : "r"(p_at + (r >> 1)) : "memory");
+    const float p = __uint_as_float(r & 1 ? w & 0xffff0000u : w << 16);
+    const bool mine = (seen[r >> 5] >> (r & 31)) & 1;
+    const uint8_t* v = static_cast<const uint8_t*>(a.v) + (uint64_t)row * a.v_step + (size_t)h * D * (kFp8 ? 1 : 2);
+#pragma unroll 1
+    for (int c = 0; c < D; c += 32) {
+      float o[32];
+      tc5::tmem_ld32(o_at + c, o);
+#pragma unroll
+      for (int i = 0; i < 32; ++i) {
+        float x;
+        bool apart;
+        if (kFp8) {
+          apart = (v[c + i] & 0x7f) == 0x7f;
+          x = __uint_as_float(0x7fffffffu);
+        } else {
+          const uint32_t u = reinterpret_cast<const uint16_t*>(v)[c + i];
+          apart = not_finite(u);
+          x = __uint_as_float(u << 16);
+        }
+        if (apart && mine) o[i] += p * x;
+      }
+      tc5::tmem_st32(o_at + c, o);
+      tc5::tmem_wait_st();
+    }
+  }
+}
+
+template <int D, int kRows, bool kFp8>
+__global__ void __launch_bounds__(kTtThreads, 1)
+    tree_kernel(const __grid_constant__ PagedArgs a, int chunks, int units, float* __restrict__ part, PaJoin* __restrict__ joins) {
+  using Sh = TtShape<D, kRows, kFp8>;
+  constexpr int ST = Sh::kStages;
+  constexpr bool kPair = kRows == 128;     // the slots share the query rows
+  // (no static shared memory: the dynamic part starts on a 1024-byte boundary)
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  TtSmem& sm = *reinterpret_cast<TtSmem*>(smem_raw + Sh::kSmem - sizeof(TtSmem));
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const uint32_t qsm = smem_u32(smem_raw);
+  const uint32_t ring = qsm + Sh::kQBytes, raw = ring + ST * Sh::kStage, scales = raw + Sh::kRawDepth * Sh::kRaw;
+  volatile int* abort = &sm.abort;
+  const int group = a.heads / a.kv_heads, qrows = a.S * group;
+  pdl_wait();
+  pdl_trigger();
+
+  int64_t total, G;
+  const bool share = paged_cuts<kTile, true, kTtThreads / 2, kExtra>(a, units, sm.scan, sm.cut, total, G);
+  if (tid == 0) joins[blockIdx.x].count = 0;
+  if (!share || sm.cut[1].at == sm.cut[0].at) return;
+  if (tid == 0) {
+    const Cut& c0 = sm.cut[0];
+    const Cut& c1 = sm.cut[1];
+    const bool same = c0.b == c1.b && c0.unit == c1.unit;
+    if (c1.tile > 0 && (!same || c0.tile == 0)) {
+      // a unit starts here and goes on in the next CTAs
+      Span<kTile, true> sp;
+      sp.set(a, c1.b);
+      const int64_t last = c1.first + sp.tiles + kExtra - 1;   // its last place in the list of costs
+      PaJoin j;
+      j.count = (int)(((last + 1) * G - 1) / total) - (int)blockIdx.x + 1;
+      j.slot = same ? 0 : 1;
+      j.b = c1.b;
+      j.unit = c1.unit;
+      joins[blockIdx.x] = j;
+    }
+    sm.abort = 0;
+    for (int i = 0; i < 8; ++i) {
+      tc5::mbar_init(smem_u32(&sm.full[i]), kLoadWarps);
+      tc5::mbar_init(smem_u32(&sm.empty[i]), 1);
+    }
+    for (int i = 0; i < kScaleTiles; ++i) tc5::mbar_init(smem_u32(&sm.sc_full[i]), kLoadWarps);
+    for (int i = 0; i < 2; ++i) {
+      tc5::mbar_init(smem_u32(&sm.s_full[i]), 1);
+      tc5::mbar_init(smem_u32(&sm.p_full[i]), 4);
+      tc5::mbar_init(smem_u32(&sm.o_full[i]), 1);
+    }
+    tc5::mbar_init(smem_u32(&sm.q_full), kQThreads / 32);
+    tc5::mbar_init(smem_u32(&sm.q_empty), 1);
+    tc5::mbar_init(smem_u32(&sm.pair), 256);
+    tc5::mbar_init(smem_u32(&sm.done), 1);
+    tc5::fence_mbar_init();
+  }
+  if (warp == kMmaWarp) {
+    tc5::tmem_alloc(smem_u32(&sm.tmem), 512);
+    tc5::tmem_relinquish();
+  }
+  tc5::fence_before_sync();
+  __syncthreads();
+  tc5::fence_after_sync();
+  const uint32_t tmem = sm.tmem;
+  // i / group for 0 <= i < S * heads <= 2^20
+  const float per_group = 1.f / (float)group;
+  auto token_of = [&](int i) { return (int)(((float)i + 0.5f) * per_group); };
+
+  if (warp < kLoadWarp) {
+    setmaxnreg_inc<kRegsSoftmax>();
+    // ------------------------------------------------------------ softmax
+    const int slot = warp >> 2, t = tid & 127;
+    const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
+    const uint32_t s_at = tmem + lanes + slot * 128, o_at = tmem + lanes + 256 + slot * 128;
+    const float scale2 = a.scale * kLog2e;
+    const int words32 = 2 * a.words;
+    uint32_t n_s = 0, n_o = 0, n_pair = 0;     // phases of s_full, o_full and pair
+    int jj = 0, seen_pieces = 0;                // tiles of the CTA before this piece
+    Walk walk;
+    walk.init(a, sm.cut);
+    Piece pc;
+    bool ok = true;
+    while (ok && walk.next(a, units, pc)) {
+      const int h = chunks == 1 ? pc.unit : pc.unit / chunks, row0 = (pc.unit - h * chunks) * kRows;
+      const int i = row0 + (kPair ? 0 : slot * 128) + t;
+      const int s = i < qrows ? token_of(i) : 0, hd = h * group + i - s * group;
+      const int64_t tok = (int64_t)pc.b * a.S + s;
+      __nv_bfloat16* out = static_cast<__nv_bfloat16*>(a.out) + tok * a.out_stride + hd * D;
+      const int at_piece = seen_pieces++;
+      if (pc.sp.L <= 0) {                      // a padding request
+        if (i < qrows && !(kPair && slot == 1)) {
+          for (int c = 0; c < D; c += 8) *reinterpret_cast<uint4*>(out + c) = make_uint4(0, 0, 0, 0);
+          if (a.lse) a.lse[tok * a.heads + hd] = -INFINITY;
+        }
+        continue;
+      }
+      const int p_first = pc.sp.L - pc.sp.n;
+      const bool real = i < qrows && s < pc.sp.n;
+      const bool busy = kPair ? pc.nt > slot : row0 + slot * 128 < qrows;   // the slot has tiles in this piece
+      float m = -INFINITY, l = 0.f;
+      if (busy) {
+        const int outside = real ? tree_outside(a, pc.b, s, p_first, pc.sp.n) : 0;
+        const uint32_t* bits = reinterpret_cast<const uint32_t*>(a.tree + tok * a.words);
+        {
+          float z[32];
+#pragma unroll
+          for (int x = 0; x < 32; ++x) z[x] = 0.f;
+#pragma unroll
+          for (int c = 0; c < D; c += 32) tc5::tmem_st32(o_at + c, z);
+        }
+        for (int j = kPair ? slot : 0; j < pc.nt; j += kPair ? 2 : 1) {
+          const int base = (pc.sp.t0 + pc.tile + j) * kTile;
+          const bool edge = edge_tile(a, pc.sp, pc.tile + j);
+          ok = warp_wait(sm.s_full[slot], n_s & 1, abort);
+          ++n_s;
+          if (!ok) break;
+          tc5::fence_after_sync();
+          float x[128];
+          tc5::tmem_ld32x2(s_at, x, x + 32);
+          tc5::tmem_ld32x2(s_at + 64, x + 64, x + 96);
+          uint32_t sc = 0;
+          if (kFp8) {
+            const int at = jj + j;
+            ok = warp_wait(sm.sc_full[at % kScaleTiles], (at / kScaleTiles) & 1, abort);
+            if (!ok) break;
+            sc = scales + (at % kScaleTiles) * kScaleBytes;
+#pragma unroll
+            for (int c = 0; c < 128; c += 4) {
+              float4 k;
+              asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];\n" : "=f"(k.x), "=f"(k.y), "=f"(k.z), "=f"(k.w) : "r"(sc + c * 4));
+              x[c] *= k.x, x[c + 1] *= k.y, x[c + 2] *= k.z, x[c + 3] *= k.w;
+            }
+          }
+          uint32_t seen[4];
+          if (edge) {
+#pragma unroll
+            for (int w = 0; w < 4; ++w) seen[w] = real ? seen32(base + 32 * w, outside, p_first, pc.sp.n, bits, words32) : 0u;
+#pragma unroll
+            for (int c = 0; c < 128; ++c)
+              if (!((seen[c >> 5] >> (c & 31)) & 1)) x[c] = -INFINITY;
+          }
+          float top[4] = {x[0], x[1], x[2], x[3]};
+#pragma unroll
+          for (int c = 4; c < 128; ++c) top[c & 3] = fmaxf(top[c & 3], x[c]);
+          const float mul = kFp8 ? 1.f : scale2;
+          const float most = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])) * mul;
+          const bool grow = most > m + kGrow;
+          if (__any_sync(0xffffffffu, grow && m > -INFINITY)) {
+            const float f = grow ? exp2f(m - most) : 1.f;
+            l *= f;
+#pragma unroll 1
+            for (int c = 0; c < D; c += 32) {
+              float o[32];
+              tc5::tmem_ld32(o_at + c, o);
+#pragma unroll
+              for (int e = 0; e < 32; ++e) o[e] *= f;
+              tc5::tmem_st32(o_at + c, o);
+            }
+          }
+          if (grow) m = most;
+          const float ref = m == -INFINITY ? 0.f : m;
+          float sum[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+          for (int half = 0; half < 2; ++half) {
+            float pk[32];
+#pragma unroll
+            for (int c = 0; c < 64; c += 4) {
+              float4 v = make_float4(1.f, 1.f, 1.f, 1.f);
+              if (kFp8)
+                asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];\n" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+                             : "r"(sc + kTile * 4 + (half * 64 + c) * 4));
+              float p[4];
+#pragma unroll
+              for (int e = 0; e < 4; ++e) {
+                p[e] = fast_exp2(fmaf(x[half * 64 + c + e], mul, -ref));
+                sum[e] += p[e];
+              }
+              if (kFp8) p[0] *= v.x, p[1] *= v.y, p[2] *= v.z, p[3] *= v.w;
+              pk[c / 2] = __uint_as_float(pack_bf16x2(p[0], p[1]));
+              pk[c / 2 + 1] = __uint_as_float(pack_bf16x2(p[2], p[3]));
+            }
+            tc5::tmem_st32(s_at + 32 * half, pk);
+          }
+          l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+          tc5::tmem_wait_st();
+          if (edge) {
+            const int n = 2 * (jj + j) + 1;     // V's stage of the ring
+            ok = warp_wait(sm.full[n % ST], (n / ST) & 1, abort);
+            if (!ok) break;
+            uint32_t bad[4];
+#pragma unroll
+            for (int w = 0; w < 4; ++w) bad[w] = *(volatile uint32_t*)&sm.bad[n % ST][w];
+            if (bad[0] | bad[1] | bad[2] | bad[3]) add_apart<D, kFp8>(a, pc.b, h, base, bad, seen, s_at, o_at);
+          }
+          tc5::fence_before_sync();
+          __syncwarp();
+          if (lane == 0) tc5::mbar_arrive(smem_u32(&sm.p_full[slot]));
+        }
+        if (ok) {
+          ok = warp_wait(sm.o_full[slot], n_o & 1, abort);
+          ++n_o;
+          tc5::fence_after_sync();
+        }
+      }
+      jj += pc.nt;
+      if (kPair) {
+        // the two slots' states of a query row are joined: either warpgroup takes
+        // half of the dims
+        sm.ml[slot][0][t] = m;
+        sm.ml[slot][1][t] = l;
+        tc5::fence_before_sync();
+        ok = __all_sync(0xffffffffu, tc5::bar_bounded(smem_u32(&sm.pair), n_pair, abort)) && ok;
+        tc5::fence_after_sync();
+        if (!ok) break;
+        const float m0 = sm.ml[0][0][t], m1 = sm.ml[1][0][t];
+        const float top = fmaxf(m0, m1), ref = top == -INFINITY ? 0.f : top;
+        const float f0 = exp2f(m0 - ref), f1 = exp2f(m1 - ref);
+        l = sm.ml[0][1][t] * f0 + (pc.nt > 1 ? sm.ml[1][1][t] * f1 : 0.f);
+        m = top;
+        const bool any = real && (l > 0.f || l != l);
+        const float inv = any ? 1.f / l : 0.f;
+        const int64_t pslot = (int64_t)blockIdx.x * 2 + (at_piece == 0 ? 0 : 1);
+        float* dst = part + (pslot * kRows + (t & ~31)) * (D + 2) + lane;
+#pragma unroll 1
+        for (int c = slot * (D / 2); c < (slot + 1) * (D / 2); c += 32) {
+          float o[32];
+          tc5::tmem_ld32(tmem + lanes + 256 + c, o);
+          if (pc.nt > 1) {
+            float o1[32];
+            tc5::tmem_ld32(tmem + lanes + 384 + c, o1);
+#pragma unroll
+            for (int e = 0; e < 32; ++e) o[e] = o[e] * f0 + o1[e] * f1;
+          }
+          if (i < qrows) {
+            if (pc.whole) {
+#pragma unroll
+              for (int e = 0; e < 32; e += 8) {
+                uint32_t w[4];
+#pragma unroll
+                for (int x = 0; x < 4; ++x) w[x] = any ? pack_bf16x2(o[e + 2 * x] * inv, o[e + 2 * x + 1] * inv) : 0u;
+                *reinterpret_cast<uint4*>(out + c + e) = make_uint4(w[0], w[1], w[2], w[3]);
+              }
+            } else {
+#pragma unroll
+              for (int e = 0; e < 32; ++e) dst[(c + e) * 32] = o[e];
+            }
+          }
+        }
+        if (i < qrows && slot == 0) {
+          if (!pc.whole) dst[D * 32] = m, dst[(D + 1) * 32] = l;
+          else if (a.lse) a.lse[tok * a.heads + hd] = any ? (m + log2f(l)) * kLn2 : -INFINITY;
+        }
+        // neither slot is written again before both were read
+        tc5::fence_before_sync();
+        ok = __all_sync(0xffffffffu, tc5::bar_bounded(smem_u32(&sm.pair), n_pair, abort));
+        tc5::fence_after_sync();
+      } else if (busy && ok) {
+        const bool any = real && (l > 0.f || l != l);
+        const float inv = any ? 1.f / l : 0.f;
+        const int64_t pslot = (int64_t)blockIdx.x * 2 + (at_piece == 0 ? 0 : 1);
+        float* dst = part + (pslot * kRows + slot * 128 + (t & ~31)) * (D + 2) + lane;
+#pragma unroll 1
+        for (int c = 0; c < D; c += 32) {
+          float o[32];
+          tc5::tmem_ld32(o_at + c, o);
+          if (i < qrows) {
+            if (pc.whole) {
+#pragma unroll
+              for (int e = 0; e < 32; e += 8) {
+                uint32_t w[4];
+#pragma unroll
+                for (int x = 0; x < 4; ++x) w[x] = any ? pack_bf16x2(o[e + 2 * x] * inv, o[e + 2 * x + 1] * inv) : 0u;
+                *reinterpret_cast<uint4*>(out + c + e) = make_uint4(w[0], w[1], w[2], w[3]);
+              }
+            } else {
+#pragma unroll
+              for (int e = 0; e < 32; ++e) dst[(c + e) * 32] = o[e];
+            }
+          }
+        }
+        if (i < qrows) {
+          if (!pc.whole) dst[D * 32] = m, dst[(D + 1) * 32] = l;
+          else if (a.lse) a.lse[tok * a.heads + hd] = any ? (m + log2f(l)) * kLn2 : -INFINITY;
+        }
+      }
+    }
+  } else {
+    setmaxnreg_dec<kRegsOthers>();
+    if (warp < kMmaWarp) {
+      // ---------------------------------------------------------- row loaders
+      const int w = warp - kLoadWarp;
+      constexpr int kRowBytes = D * (kFp8 ? 1 : 2), kSpan = kRowBytes / 16, kAtOnce = 32 / kSpan, kIter = 32 / kAtOnce;
+      const int ch = lane % kSpan, r0 = lane / kSpan;
+      const int steps = (int)(sm.cut[1].at - sm.cut[0].at);
+      Cursor<kTile, true> ld;                  // the tile being copied
+      ld.b = sm.cut[0].b;
+      ld.sp.set(a, ld.b);
+      ld.unit = sm.cut[0].unit;
+      ld.tile = sm.cut[0].tile;
+      Cursor<kTile, true> sg = ld;             // the tile whose chunks are handed on
+      // lane: its row of the warp's 32, looked up one tile ahead
+      int entry = -1, within = -1, prow = -1;
+      auto lookup = [&](const Cursor<kTile, true>& c) {
+        const int r = (c.sp.t0 + c.tile) * kTile + w * 32 + lane;
+        within = -1;
+        if (r >= c.sp.lo && r < c.sp.L) {
+          if (a.table) {
+            const int k = (int)((uint32_t)r / (uint32_t)a.block);
+            within = r - k * a.block;
+            entry = -1;
+            if (k < a.table_stride) entry = a.table[(int64_t)c.b * a.table_stride + k];
+          } else {
+            const int64_t x = a.off[c.b] + r;
+            within = 0;
+            entry = x >= 0 && x < a.rows ? (int)x : -1;
+          }
+        }
+      };
+      auto resolve = [&] {
+        prow = -1;
+        if (within >= 0) {
+          const int64_t x = entry < 0 ? -1 : a.table ? (int64_t)entry * a.block + within : entry;
+          if (x >= 0 && x < a.rows) prow = (int)x;
+          else if (a.status) set_status(a.status, kStatusBadIndex);
+        }
+      };
+      // where this thread's piece i of a chunk lies in a stage
+      auto place = [&](int i) {
+        const int row = w * 32 + i * kAtOnce + r0;
+        const int c0 = kFp8 ? 2 * ch : ch;
+        return (uint32_t)((c0 >> 3) * kSub + row * 128 + (((c0 & 7) ^ (row & 7)) << 4));
+      };
+      uint32_t n_iss = 0, n_sig = 0;           // chunks (a tile's K, then its V) copied, handed on
+      bool ok = true;
+      auto hand_on = [&] {
+        while (sg.sp.L <= 0) sg.next(a, units);
+        const uint32_t st = n_sig % ST, stage = ring + st * Sh::kStage;
+        const int kv = n_sig & 1;
+        uint32_t bad = 0;
+        const bool look = kv && edge_tile(a, sg.sp, sg.tile);
+        if (kFp8) {
+          if (n_sig >= ST) ok = warp_wait(sm.empty[st], (n_sig / ST - 1) & 1, abort);
+          if (!ok) return;
+          const uint32_t from = raw + (n_sig % Sh::kRawDepth) * Sh::kRaw + (w * kIter * 32 + lane) * 16;
+#pragma unroll 2
+          for (int i = 0; i < kIter; ++i) {
+            uint32_t c[4], u[8];
+            asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];\n" : "=r"(c[0]), "=r"(c[1]), "=r"(c[2]), "=r"(c[3]) : "r"(from + i * 512) : "memory");
+            if (look) {
+              uint32_t any = 0;
+#pragma unroll
+              for (int x = 0; x < 4; ++x) any |= ((c[x] & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u;
+              if (any) {
+                bad |= 1u << (i * kAtOnce + r0);
+#pragma unroll
+                for (int x = 0; x < 4; ++x) {
+                  const uint32_t nan = (((c[x] & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u) >> 7;   // 1 in a NaN's byte
+                  c[x] &= ~(nan * 0xffu);
+                }
+              }
+            }
+#pragma unroll
+            for (int x = 0; x < 4; ++x) {
+              uint32_t lo, hi;
+              e4m3x4_to_f16x2(c[x], lo, hi);
+              const float2 f0 = __half22float2(*reinterpret_cast<const __half2*>(&lo));
+              const float2 f1 = __half22float2(*reinterpret_cast<const __half2*>(&hi));
+              u[2 * x] = pack_bf16x2(f0.x, f0.y);
+              u[2 * x + 1] = pack_bf16x2(f1.x, f1.y);
+            }
+            const uint32_t at = stage + place(i);
+            asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};\n" ::"r"(at), "r"(u[0]), "r"(u[1]), "r"(u[2]), "r"(u[3]) : "memory");
+            asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};\n" ::"r"(at ^ 16u), "r"(u[4]), "r"(u[5]), "r"(u[6]), "r"(u[7]) : "memory");
+          }
+          if (kv == 0) {
+            // the row's scales as the scores and weights take them; a V scale that is no
+            // number reaches whoever sees the row by its score
+            const uint32_t at = scales + ((n_sig / 2) % kScaleTiles) * kScaleBytes + (w * 32 + lane) * 4;
+            float ks, vs;
+            asm volatile("ld.shared.f32 %0, [%1];\n" : "=f"(ks) : "r"(at) : "memory");
+            asm volatile("ld.shared.f32 %0, [%1];\n" : "=f"(vs) : "r"(at + kTile * 4) : "memory");
+            const bool number = fabsf(vs) < INFINITY;
+            ks = number ? ks * (a.scale * kLog2e) : __uint_as_float(0x7fffffffu);
+            asm volatile("st.shared.f32 [%0], %1;\n" ::"r"(at), "f"(ks) : "memory");
+            asm volatile("st.shared.f32 [%0], %1;\n" ::"r"(at + kTile * 4), "f"(number ? vs : 1.f) : "memory");
+          }
+        } else if (look) {
+#pragma unroll 1
+          for (int i = 0; i < kIter; ++i) {
+            uint32_t c[4];
+            const uint32_t at = stage + place(i);
+            asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];\n" : "=r"(c[0]), "=r"(c[1]), "=r"(c[2]), "=r"(c[3]) : "r"(at) : "memory");
+            bool any = false;
+#pragma unroll
+            for (int x = 0; x < 4; ++x) any |= not_finite(c[x]) || not_finite(c[x] >> 16);
+            if (any) {
+              bad |= 1u << (i * kAtOnce + r0);
+#pragma unroll
+              for (int x = 0; x < 4; ++x)
+                c[x] &= (not_finite(c[x]) ? 0u : 0xffffu) | (not_finite(c[x] >> 16) ? 0u : 0xffff0000u);
+              asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};\n" ::"r"(at), "r"(c[0]), "r"(c[1]), "r"(c[2]), "r"(c[3]) : "memory");
+            }
+          }
+        }
+        if (look) {
+          bad = __reduce_or_sync(0xffffffffu, bad);
+          if (lane == 0) *(volatile uint32_t*)&sm.bad[st][w] = bad;
+        }
+        tc5::fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) {
+          tc5::mbar_arrive(smem_u32(&sm.full[st]));
+          if (kFp8 && kv == 0) tc5::mbar_arrive(smem_u32(&sm.sc_full[(n_sig / 2) % kScaleTiles]));
+        }
+        ++n_sig;
+        if (kv) sg.next(a, units);
+      };
+      lookup(ld);
+      for (int step = 0; ok && step < steps; ++step) {
+        if (ld.sp.L > 0) {
+          resolve();
+          const int h = chunks == 1 ? ld.unit : ld.unit / chunks;
+#pragma unroll 1
+          for (int kv = 0; kv < 2; ++kv) {
+            uint32_t to;
+            if (kFp8) {
+              to = raw + (n_iss % Sh::kRawDepth) * Sh::kRaw + (w * kIter * 32 + lane) * 16;
+              if (kv == 0) {
+                const int64_t at = (int64_t)(prow < 0 ? 0 : prow) * a.scale_stride + h;
+                const uint32_t dst = scales + ((n_iss / 2) % kScaleTiles) * kScaleBytes + (w * 32 + lane) * 4;
+                cp_async4(dst, a.k_scale + at, prow < 0 ? 0 : 4);
+                cp_async4(dst + kTile * 4, a.v_scale + at, prow < 0 ? 0 : 4);
+              }
+            } else {
+              const uint32_t st = n_iss % ST;
+              if (n_iss >= ST) ok = warp_wait(sm.empty[st], (n_iss / ST - 1) & 1, abort);
+              if (!ok) break;
+              to = ring + st * Sh::kStage;
+            }
+            const uint8_t* src = static_cast<const uint8_t*>(kv ? a.v : a.k) + (h * kRowBytes + ch * 16);
+            const uint32_t pitch = kv ? a.v_step : a.k_step;
+#pragma unroll
+            for (int i = 0; i < kIter; ++i) {
+              const int p = __shfl_sync(0xffffffffu, prow, i * kAtOnce + r0);
+              cp_async16(kFp8 ? to + i * 512 : to + place(i), src + (uint64_t)(p < 0 ? 0u : (uint32_t)p) * pitch, p < 0 ? 0 : 16);
+            }
+            cp_async_commit();
+            ++n_iss;
+            if (n_iss - n_sig > Sh::kDepth) {
+              cp_async_wait<Sh::kDepth>();
+              hand_on();
+            }
+          }
+        }
+        if (step + 1 < steps) {
+          ld.next(a, units);
+          lookup(ld);
+        }
+      }
+      cp_async_wait<0>();
+      while (ok && n_sig < n_iss) hand_on();
+    } else if (warp == kMmaWarp) {
+      // ---------------------------------------------------------- MMA issue
+      if (lane == 0) {
+        const uint32_t idesc_s = tc5::idesc_bf16_f32(128, kTile);
+        const uint32_t idesc_o = tc5::idesc_bf16_f32(128, D) | (1u << 16);   // B MN-major
+        const uint64_t dq = tc5::sdesc_k_sw128(qsm), dk = tc5::sdesc_k_sw128(ring), dv = sdesc_mn_sw128(ring, kSub);
+        uint32_t n_p[2] = {0, 0}, n_q = 0, n0 = 0;   // phases; the piece's first chunk
+        bool ok = true;
+        auto wait = [&](uint64_t& bar, uint32_t parity) {
+          if (ok) ok = tc5::mbar_wait(smem_u32(&bar), parity, abort);
+          tc5::fence_after_sync();
+        };
+        auto landed = [&](uint32_t n) { wait(sm.full[n % ST], (n / ST) & 1); };
+        auto release = [&](uint32_t n) { tc5::mma_commit(smem_u32(&sm.empty[n % ST])); };
+        auto qk = [&](int slot, uint32_t n) {
+          const uint64_t q = dq + ((kPair ? 0 : slot * Sh::kStage) >> 4), k = dk + (((n % ST) * Sh::kStage) >> 4);
+#pragma unroll
+          for (int x = 0; x < D / 16; ++x)
+            tc5::mma_bf16(tmem + slot * 128, q + (((x >> 2) * kSub + (x & 3) * 32) >> 4),
+                          k + (((x >> 2) * kSub + (x & 3) * 32) >> 4), idesc_s, x > 0);
+        };
+        auto pv = [&](int slot, uint32_t n) {
+          const uint64_t v = dv + (((n % ST) * Sh::kStage) >> 4);
+#pragma unroll
+          for (int x = 0; x < kTile / 16; ++x)
+            tc5::mma_bf16_ta(tmem + 256 + slot * 128, tmem + slot * 128 + 8 * x, v + ((x * 2048) >> 4), idesc_o, 1u);
+        };
+        Walk walk;
+        walk.init(a, sm.cut);
+        Piece pc;
+        while (ok && walk.next(a, units, pc)) {
+          if (pc.sp.L <= 0) continue;
+          const int h = chunks == 1 ? pc.unit : pc.unit / chunks, row0 = (pc.unit - h * chunks) * kRows;
+          const bool two = kPair ? pc.nt > 1 : row0 + 128 < qrows;
+          wait(sm.q_full, n_q & 1);
+          ++n_q;
+          if (kPair) {
+#pragma unroll 1
+            for (int j = -2; ok && j < pc.nt; ++j) {
+              const int slot = j & 1;
+              if (j >= 0) {
+                wait(sm.p_full[slot], n_p[slot] & 1);
+                ++n_p[slot];
+                landed(n0 + 2 * j + 1);
+                if (!ok) break;
+                pv(slot, n0 + 2 * j + 1);
+                release(n0 + 2 * j + 1);
+              }
+              if (j + 2 < pc.nt) {
+                landed(n0 + 2 * (j + 2));
+                if (!ok) break;
+                qk(slot, n0 + 2 * (j + 2));
+                release(n0 + 2 * (j + 2));
+                tc5::mma_commit(smem_u32(&sm.s_full[slot]));
+                if (j + 3 == pc.nt) tc5::mma_commit(smem_u32(&sm.q_empty));
+              } else if (j >= 0) {
+                tc5::mma_commit(smem_u32(&sm.o_full[slot]));
+              }
+            }
+          } else {
+#pragma unroll 1
+            for (int j = -1; ok && j < pc.nt; ++j) {
+#pragma unroll 1
+              for (int slot = 0; slot < (two ? 2 : 1); ++slot) {
+                const bool end = slot == (two ? 1 : 0);
+                if (j >= 0) {
+                  wait(sm.p_full[slot], n_p[slot] & 1);
+                  ++n_p[slot];
+                  if (slot == 0) landed(n0 + 2 * j + 1);
+                  if (!ok) break;
+                  pv(slot, n0 + 2 * j + 1);
+                  if (end) release(n0 + 2 * j + 1);
+                }
+                if (j + 1 < pc.nt) {
+                  if (slot == 0) landed(n0 + 2 * (j + 1));
+                  if (!ok) break;
+                  qk(slot, n0 + 2 * (j + 1));
+                  if (end) release(n0 + 2 * (j + 1));
+                  tc5::mma_commit(smem_u32(&sm.s_full[slot]));
+                  if (end && j + 2 == pc.nt) tc5::mma_commit(smem_u32(&sm.q_empty));
+                } else {
+                  tc5::mma_commit(smem_u32(&sm.o_full[slot]));
+                }
+              }
+            }
+          }
+          n0 += 2 * pc.nt;
+        }
+        tc5::mma_commit(smem_u32(&sm.done));
+        tc5::mbar_wait_drain(smem_u32(&sm.done), 0);
+      }
+      __syncwarp();
+    } else {
+      // ---------------------------------------------------------- the units' query rows
+      uint32_t n_q = 0;
+      bool ok = true;
+      Walk walk;
+      walk.init(a, sm.cut);
+      Piece pc;
+      while (ok && walk.next(a, units, pc)) {
+        if (pc.sp.L <= 0) continue;
+        const int h = chunks == 1 ? pc.unit : pc.unit / chunks, row0 = (pc.unit - h * chunks) * kRows;
+        if (n_q > 0) ok = warp_wait(sm.q_empty, (n_q - 1) & 1, abort);
+        if (!ok) break;
+        const __nv_bfloat16* q0 = static_cast<const __nv_bfloat16*>(a.q) + (int64_t)pc.b * a.S * a.q_stride;
+#pragma unroll 4
+        for (int x = tid - kQWarp * 32; x < kRows * (D / 8); x += kQThreads) {
+          const int r = x / (D / 8), c = x % (D / 8), i = row0 + r;
+          const int s = i < qrows ? token_of(i) : 0;
+          const __nv_bfloat16* src = q0 + (int64_t)s * a.q_stride + (h * group + i - s * group) * D + c * 8;
+          const uint32_t dst = qsm + (r >> 7) * Sh::kStage + (c >> 3) * kSub + (r & 127) * 128 + (((c & 7) ^ (r & 7)) << 4);
+          cp_async16(dst, i < qrows ? src : q0, i < qrows ? 16 : 0);
+        }
+        cp_async_commit();
+        cp_async_wait<0>();
+        tc5::fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) tc5::mbar_arrive(smem_u32(&sm.q_full));
+        ++n_q;
+      }
+    }
+  }
+  cp_async_wait<0>();
+  tc5::fence_before_sync();
+  __syncthreads();
+  tc5::fence_after_sync();
+  if (warp == kMmaWarp) tc5::tmem_dealloc(tmem, 512);
+  if (tid == 0 && sm.abort && a.status) set_status(a.status, kStatusTimeout);
+}
+
+// Joins the pieces of the units cut between CTAs: block (x, y) does query rows
+// 32 y .. of the unit that starts in CTA x, a thread a row and D / 8 dims.
+template <int D>
+__global__ void __launch_bounds__(256)
+    tree_join_kernel(const PagedArgs a, int chunks, int rows, const float* __restrict__ part, const PaJoin* __restrict__ joins) {
+  pdl_wait();
+  pdl_trigger();
+  const PaJoin j = joins[blockIdx.x];
+  if (j.count == 0) return;
+  const int lane = threadIdx.x & 31, c0 = (threadIdx.x >> 5) * (D / 8);
+  const int group = a.heads / a.kv_heads, h = j.unit / chunks, r0 = blockIdx.y * 32;
+  const int i = (j.unit - h * chunks) * rows + r0 + lane;
+  if (i >= a.S * group) return;
+  float m = -INFINITY, l = 0.f, acc[D / 8];
+#pragma unroll
+  for (int x = 0; x < D / 8; ++x) acc[x] = 0.f;
+  for (int p = 0; p < j.count; ++p) {
+    const int64_t slot = p == 0 ? (int64_t)blockIdx.x * 2 + j.slot : (int64_t)(blockIdx.x + p) * 2;
+    const float* src = part + (slot * rows + r0) * (D + 2) + lane;
+    const float m2 = src[D * 32], l2 = src[(D + 1) * 32];
+    const float top = fmaxf(m, m2), ref = top == -INFINITY ? 0.f : top;
+    const float f1 = exp2f(m - ref), f2 = exp2f(m2 - ref);
+    l = l * f1 + l2 * f2;
+    m = top;
+#pragma unroll
+    for (int x = 0; x < D / 8; ++x) acc[x] = acc[x] * f1 + src[(c0 + x) * 32] * f2;
+  }
+  const int s = i / group, hd = h * group + i - s * group;
+  const int64_t tok = (int64_t)j.b * a.S + s;
+  const bool any = (l > 0.f || l != l) && (!a.count || s < a.count[j.b]);
+  const float inv = any ? 1.f / l : 0.f;
+  __nv_bfloat16* out = static_cast<__nv_bfloat16*>(a.out) + tok * a.out_stride + hd * D + c0;
+#pragma unroll
+  for (int x = 0; x < D / 8; x += 8) {
+    uint32_t w[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) w[e] = any ? pack_bf16x2(acc[x + 2 * e] * inv, acc[x + 2 * e + 1] * inv) : 0u;
+    *reinterpret_cast<uint4*>(out + x) = make_uint4(w[0], w[1], w[2], w[3]);
+  }
+  if (a.lse && c0 == 0) a.lse[tok * a.heads + hd] = any ? (m + log2f(l)) * kLn2 : -INFINITY;
+}
+
+template <int D, int kRows, bool kFp8>
+int launch_rows(const PagedArgs& a, int num_sms, cudaStream_t st, bool pdl) {
+  using Sh = TtShape<D, kRows, kFp8>;
+  auto kern = tree_kernel<D, kRows, kFp8>;
+  static PerDeviceOnce attr;
+  if (const cudaError_t e = attr.run([&] {
+        // the warpgroups' shares of the registers must add up to what the launch brings
+        cudaFuncAttributes fa;
+        const cudaError_t q = cudaFuncGetAttributes(&fa, kern);
+        if (q != cudaSuccess) return q;
+        if (fa.numRegs * kTtThreads < kTtThreads / 2 * (kRegsSoftmax + kRegsOthers)) return cudaErrorLaunchOutOfResources;
+        return allow_max_dynamic_smem(kern);
+      }))
+    return launch_fail("cudaFuncSetAttribute(tree_kernel)", e);
+  const int qrows = a.S * (a.heads / a.kv_heads), chunks = (qrows + kRows - 1) / kRows;
+  float* part = static_cast<float*>(a.workspace);
+  PaJoin* joins = reinterpret_cast<PaJoin*>(part + (size_t)num_sms * 2 * kRows * (D + 2));
+  const int64_t tiles = (int64_t)a.B * a.kv_heads * chunks * ((a.max_len + kTile - 1) / kTile + kExtra);
+  const int grid = tiles < num_sms ? (int)tiles : num_sms;
+  const int r = launch_kernel(kern, dim3(grid), dim3(kTtThreads), Sh::kSmem, st, pdl, a, chunks, a.kv_heads * chunks, part, joins);
+  if (r < 0) return r;
+  const int most = qrows < kRows ? qrows : kRows;
+  const int r2 = launch_kernel(tree_join_kernel<D>, dim3(grid, (most + 31) / 32), dim3(256), 0, st, pdl, a, chunks, kRows,
+                               (const float*)part, (const PaJoin*)joins);
+  return r2 < 0 ? r2 : r + r2;
+}
+
+}  // namespace
+
+// Partials of two pieces per CTA of up to 256 query rows, and the join list (the warps'
+// kernel needs less).
+size_t tree_attn_workspace(int dim, int num_sms) {
+  const size_t wide = dim == 256 ? 0 : (size_t)num_sms * (2 * 256 * (dim + 2) * sizeof(float) + sizeof(PaJoin));
+  const size_t warps = paged_attn_workspace(dim, num_sms);
+  return wide > warps ? wide : warps;
+}
+
+int launch_tree_attn(const PagedArgs& a, bool fp8, int num_sms, cudaStream_t st, bool pdl) {
+  const int qrows = a.S * (a.heads / a.kv_heads);
+  if (a.dim == 256 || qrows <= 32) return launch_paged_attn(a, fp8, num_sms, st, pdl);
+  const bool two = qrows > 128;
+  if (fp8) return two ? launch_rows<128, 256, true>(a, num_sms, st, pdl) : launch_rows<128, 128, true>(a, num_sms, st, pdl);
+  if (a.dim == 64) return two ? launch_rows<64, 256, false>(a, num_sms, st, pdl) : launch_rows<64, 128, false>(a, num_sms, st, pdl);
+  return two ? launch_rows<128, 256, false>(a, num_sms, st, pdl) : launch_rows<128, 128, false>(a, num_sms, st, pdl);
+}
+
+}  // namespace csa
