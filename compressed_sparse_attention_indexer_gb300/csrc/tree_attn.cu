@@ -20,12 +20,16 @@
 //                    in registers, so that maxima and sums need no exchange; the
 //                    reference maximum moves only when exceeded by 2^8 (the output is
 //                    then rescaled in place);
-//   warps 8-11       gather the rows by 16-byte cp.async into a ring of 128-byte
-//                    swizzled stages (K and V alike: V is read as an MN-major
-//                    operand), several ahead, across units.  E4M3 codes land beside
-//                    the ring and are converted by the thread that copied them;
+//   warp 13          copies the rows by TMA into a ring of 128-byte swizzled stages
+//                    (K and V alike: V is read as an MN-major operand), several ahead,
+//                    across units.  A copy takes the rows of a tile that surely lie in
+//                    one page, gcd(block, 128) of them.  (Four warps of 16-byte
+//                    cp.async took 1900 cycles for a chunk of 32 KB, TMA gathers of four
+//                    rows 80 cycles each: 1699 and 2527 us for 64 x 16 drafts.)
+//   warps 8-11       E4M3: convert the codes, which land beside the ring; bf16: look
+//                    through V's rows in edge tiles;
 //   warp 12          issues the MMAs: S = Q K^T, O += P V (P from tensor memory);
-//   warps 13-15      the unit's query rows.
+//   warps 14, 15     the unit's query rows.
 //
 // Masks.  A tile that some draft does not see whole (the window's first rows,
 // the drafts') is an edge tile: each thread builds the 128 bits of its row and
@@ -36,6 +40,8 @@
 // Scores, maxima, sums and output are fp32; the weights are rounded to bf16 for
 // the product with V, E4M3 ones after they took V's scale (bf16 has the range of
 // fp32, so no scale makes them vanish).
+#include <cudaTypedefs.h>
+
 #include "csa_internal.cuh"
 #include "paged.cuh"
 #include "ptx.cuh"
@@ -46,7 +52,7 @@ namespace csa {
 namespace {
 
 constexpr int kTtThreads = 512;
-constexpr int kLoadWarp = 8, kLoadWarps = 4, kMmaWarp = 12, kQWarp = 13, kQThreads = 96;
+constexpr int kRowWarp = 8, kRowWarps = 4, kMmaWarp = 12, kLoadWarp = 13, kQWarp = 14, kQThreads = 64;
 constexpr int kRegsSoftmax = 184, kRegsOthers = 72;   // of the launch's 128 per thread
 constexpr int kTile = 128;                 // K / V rows per tile
 constexpr int kExtra = 2;                  // a unit's start and end, in tiles
@@ -57,6 +63,8 @@ constexpr int kScaleBytes = kTile * 2 * 4; // K's and V's of a tile
 
 struct TtSmem {
   uint64_t full[8], empty[8];              // stages of the ring
+  uint64_t land[8];                        // bf16 V of an edge tile, before it was looked through
+  uint64_t raw_full[3], raw_empty[3];      // chunks of E4M3 codes
   uint64_t s_full[2], p_full[2], o_full[2];
   uint64_t q_full, q_empty, sc_full[kScaleTiles], pair, done;
   uint32_t tmem;
@@ -64,6 +72,7 @@ struct TtSmem {
   PaCost scan[33];
   Cut cut[2];
   uint32_t bad[8][4];                      // per stage: V rows with a NaN or an infinity
+  int looked[8];                           // warps that have looked through it, modulo 4
   float ml[2][2][128];                     // per slot: maxima and sums, for the join of two slots
 };
 
@@ -77,12 +86,11 @@ struct TtShape {
   static constexpr int kScales = kFp8 ? kScaleTiles * kScaleBytes : 0;
   static constexpr int kRoom = (227 * 1024 - (int)sizeof(TtSmem) - kQBytes - kRawDepth * kRaw - kScales) / kStage;
   static constexpr int kStages = kRoom > 8 ? 8 : kRoom;
-  static constexpr int kDepth = kFp8 ? kRawDepth - 1 : kStages - 2;   // chunks in flight behind the newest
   static constexpr int kSmem = kQBytes + kStages * kStage + kRawDepth * kRaw + kScales + (int)sizeof(TtSmem);
-  static_assert(kStages >= 3 && kDepth >= 1, "ring");
-  // a tile's scales stay until its weights are made: the loaders are at most
-  // (kRawDepth + kStages + 1) / 2 + 1 tiles ahead of that (see the scales' ring)
-  static_assert(!kFp8 || (kRawDepth + kStages + 1) / 2 + 1 < kScaleTiles, "scales");
+  static_assert(kStages >= 3, "ring");
+  // a tile's scales stay until its weights are made: its V then waits in the ring, so
+  // that the tile being written is at most kStages / 2 + 1 tiles ahead
+  static_assert(kStages / 2 + 1 < kScaleTiles, "scales");
 };
 
 // One piece: consecutive tiles of a unit that this CTA takes.
@@ -123,14 +131,21 @@ __device__ __forceinline__ bool edge_tile(const PagedArgs& a, const Span<kTile, 
   return base < sp.lo || base + kTile > sp.L - sp.n || (a.win > 0 && base < sp.L - a.win);
 }
 
+// Bits lo .. hi - 1, either end anywhere.
+__device__ __forceinline__ uint32_t ones(int lo, int hi) {
+  lo = max(lo, 0);
+  hi = min(hi, 32);
+  return hi <= lo ? 0u : (hi == 32 ? 0xffffffffu : (1u << hi) - 1u) & ~((1u << lo) - 1u);
+}
+// Rows 32 w .. of tile t that belong to the span.
+__device__ __forceinline__ uint32_t span_rows(const Span<kTile, true>& sp, int t, int w) {
+  const int r0 = (sp.t0 + t) * kTile + 32 * w;
+  return ones(sp.lo - r0, sp.L - r0);
+}
+
 // 32 rows' bits from row c0 on, for a draft: rows up to `out` are outside its window,
 // the drafts start at row p and are n, `bits` are its mask's 32-bit words.
 __device__ __forceinline__ uint32_t seen32(int c0, int out, int p, int n, const uint32_t* bits, int words32) {
-  auto ones = [](int lo, int hi) -> uint32_t {   // bits lo .. hi - 1, either end anywhere
-    lo = max(lo, 0);
-    hi = min(hi, 32);
-    return hi <= lo ? 0u : (hi == 32 ? 0xffffffffu : (1u << hi) - 1u) & ~((1u << lo) - 1u);
-  };
   uint32_t v = ones(out + 1 - c0, p - c0);
   const int t = c0 - p;                          // draft at the first bit
   if (t > -32 && t < n) {
@@ -164,6 +179,47 @@ __device__ __forceinline__ void setmaxnreg_dec() {
   asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;\n" ::"n"(N));
 }
 
+// The places in the pool of kN segments of `seg` rows of a tile (each within a page), looked
+// up ahead of their use.
+template <int kN>
+struct Places {
+  int entry[kN], within[kN];
+  int first, last;                         // the span's rows among the tile's, [first, last)
+  __device__ __forceinline__ void lookup(const PagedArgs& a, const Cursor<kTile, true>& c, int at, int seg, int n) {
+    const int base = (c.sp.t0 + c.tile) * kTile;
+    first = max(c.sp.lo - base, 0);
+    last = min(c.sp.L - base, kTile);
+#pragma unroll
+    for (int i = 0; i < kN; ++i) {
+      const int r = (at + i) * seg;
+      within[i] = entry[i] = -1;
+      if (i < n && r < last && r + seg > first) {
+        if (a.table) {
+          const int k = (int)((uint32_t)(base + r) / (uint32_t)a.block);
+          within[i] = base + r - k * a.block;
+          if (k < a.table_stride) entry[i] = a.table[(int64_t)c.b * a.table_stride + k];
+        } else {
+          within[i] = 0;
+          // rows outside the pool may be a part of the segment: its start is kept near the pool
+          const int64_t x = a.off[c.b] + base + r;
+          entry[i] = (int)(x < -kTile ? -kTile : x > a.rows ? a.rows : x);
+        }
+      }
+    }
+  }
+  // Pool row of segment i, `none` where it has no row to read; false when some of its rows
+  // in the span are unmapped or outside the pool.
+  __device__ __forceinline__ bool resolve(const PagedArgs& a, int i, int at, int seg, int none, int& row) const {
+    row = none;
+    if (within[i] < 0) return true;
+    if (a.table && entry[i] < 0) return false;
+    const int64_t x = a.table ? (int64_t)entry[i] * a.block + within[i] : entry[i];
+    const int r = (at + i) * seg;
+    if (x < a.rows) row = (int)x;
+    return x + max(first - r, 0) >= 0 && x + min(last - r, seg) <= a.rows;
+  }
+};
+
 // The part of an edge tile's V rows that was zeroed: rows `bad` (four words), added to
 // the output of the threads whose row sees them.  Rare, out of line.
 template <int D, bool kFp8>
@@ -172,12 +228,13 @@ __device__ __noinline__ void add_apart(const PagedArgs& a, int b, int h, int bas
 #pragma unroll 1
   for (int r = 0; r < kTile; ++r) {
     if (!((bad[r >> 5] >> (r & 31)) & 1)) continue;
+    const bool mine = (seen[r >> 5] >> (r & 31)) & 1;
+    if (!__any_sync(0xffffffffu, mine)) continue;
     const int64_t row = pool_row(a.table, a.block, a.table_stride, a.off, b, base + r);
     if (row < 0 || row >= a.rows) continue;
     uint32_t w;
     asm volatile("tcgen05.ld.sync.aligned.32x32b.x1.b32 {%0}, [%1];\n tcgen05.wait::ld.sync.aligned;\n" : "=r"(w) : "r"(p_at + (r >> 1)) : "memory");
     const float p = __uint_as_float(r & 1 ? w & 0xffff0000u : w << 16);
-    const bool mine = (seen[r >> 5] >> (r & 31)) & 1;
     const uint8_t* v = static_cast<const uint8_t*>(a.v) + (uint64_t)row * a.v_step + (size_t)h * D * (kFp8 ? 1 : 2);
 #pragma unroll 1
     for (int c = 0; c < D; c += 32) {
@@ -205,7 +262,8 @@ __device__ __noinline__ void add_apart(const PagedArgs& a, int b, int h, int bas
 
 template <int D, int kRows, bool kFp8>
 __global__ void __launch_bounds__(kTtThreads, 1)
-    tree_kernel(const __grid_constant__ PagedArgs a, int chunks, int units, float* __restrict__ part, PaJoin* __restrict__ joins) {
+    tree_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap,
+                const __grid_constant__ PagedArgs a, int seg, int chunks, int units, float* __restrict__ part, PaJoin* __restrict__ joins) {
   using Sh = TtShape<D, kRows, kFp8>;
   constexpr int ST = Sh::kStages;
   constexpr bool kPair = kRows == 128;     // the slots share the query rows
@@ -242,10 +300,16 @@ __global__ void __launch_bounds__(kTtThreads, 1)
     }
     sm.abort = 0;
     for (int i = 0; i < 8; ++i) {
-      tc5::mbar_init(smem_u32(&sm.full[i]), kLoadWarps);
+      tc5::mbar_init(smem_u32(&sm.full[i]), kFp8 ? kRowWarps : 1);
       tc5::mbar_init(smem_u32(&sm.empty[i]), 1);
+      tc5::mbar_init(smem_u32(&sm.land[i]), 1);
+      sm.looked[i] = 0;
     }
-    for (int i = 0; i < kScaleTiles; ++i) tc5::mbar_init(smem_u32(&sm.sc_full[i]), kLoadWarps);
+    for (int i = 0; i < 3; ++i) {
+      tc5::mbar_init(smem_u32(&sm.raw_full[i]), 1);
+      tc5::mbar_init(smem_u32(&sm.raw_empty[i]), kRowWarps);
+    }
+    for (int i = 0; i < kScaleTiles; ++i) tc5::mbar_init(smem_u32(&sm.sc_full[i]), kRowWarps);
     for (int i = 0; i < 2; ++i) {
       tc5::mbar_init(smem_u32(&sm.s_full[i]), 1);
       tc5::mbar_init(smem_u32(&sm.p_full[i]), 4);
@@ -269,7 +333,7 @@ __global__ void __launch_bounds__(kTtThreads, 1)
   const float per_group = 1.f / (float)group;
   auto token_of = [&](int i) { return (int)(((float)i + 0.5f) * per_group); };
 
-  if (warp < kLoadWarp) {
+  if (warp < kRowWarp) {
     setmaxnreg_inc<kRegsSoftmax>();
     // ------------------------------------------------------------ softmax
     const int slot = warp >> 2, t = tid & 127;
@@ -490,269 +554,348 @@ __global__ void __launch_bounds__(kTtThreads, 1)
   } else {
     setmaxnreg_dec<kRegsOthers>();
     if (warp < kMmaWarp) {
-      // ---------------------------------------------------------- row loaders
-      const int w = warp - kLoadWarp;
+      // ---------------------------------------------------------- converters, or V's readers
+      const int w = warp - kRowWarp;
       constexpr int kRowBytes = D * (kFp8 ? 1 : 2), kSpan = kRowBytes / 16, kAtOnce = 32 / kSpan, kIter = 32 / kAtOnce;
       const int ch = lane % kSpan, r0 = lane / kSpan;
-      const int steps = (int)(sm.cut[1].at - sm.cut[0].at);
-      Cursor<kTile, true> ld;                  // the tile being copied
-      ld.b = sm.cut[0].b;
-      ld.sp.set(a, ld.b);
-      ld.unit = sm.cut[0].unit;
-      ld.tile = sm.cut[0].tile;
-      Cursor<kTile, true> sg = ld;             // the tile whose chunks are handed on
-      // lane: its row of the warp's 32, looked up one tile ahead
-      int entry = -1, within = -1, prow = -1;
-      auto lookup = [&](const Cursor<kTile, true>& c) {
-        const int r = (c.sp.t0 + c.tile) * kTile + w * 32 + lane;
-        within = -1;
-        if (r >= c.sp.lo && r < c.sp.L) {
-          if (a.table) {
-            const int k = (int)((uint32_t)r / (uint32_t)a.block);
-            within = r - k * a.block;
-            entry = -1;
-            if (k < a.table_stride) entry = a.table[(int64_t)c.b * a.table_stride + k];
-          } else {
-            const int64_t x = a.off[c.b] + r;
-            within = 0;
-            entry = x >= 0 && x < a.rows ? (int)x : -1;
-          }
-        }
-      };
-      auto resolve = [&] {
-        prow = -1;
-        if (within >= 0) {
-          const int64_t x = entry < 0 ? -1 : a.table ? (int64_t)entry * a.block + within : entry;
-          if (x >= 0 && x < a.rows) prow = (int)x;
-          else if (a.status) set_status(a.status, kStatusBadIndex);
-        }
-      };
+      int steps = (int)(sm.cut[1].at - sm.cut[0].at);
+      Cursor<kTile, true> cu;
+      cu.b = sm.cut[0].b;
+      cu.sp.set(a, cu.b);
+      cu.unit = sm.cut[0].unit;
+      cu.tile = sm.cut[0].tile;
       // where this thread's piece i of a chunk lies in a stage
       auto place = [&](int i) {
         const int row = w * 32 + i * kAtOnce + r0;
         const int c0 = kFp8 ? 2 * ch : ch;
         return (uint32_t)((c0 >> 3) * kSub + row * 128 + (((c0 & 7) ^ (row & 7)) << 4));
       };
-      uint32_t n_iss = 0, n_sig = 0;           // chunks (a tile's K, then its V) copied, handed on
+      uint32_t n = 0, parity = 0;              // chunks; bit st: phase of land[st]
       bool ok = true;
-      auto hand_on = [&] {
-        while (sg.sp.L <= 0) sg.next(a, units);
-        const uint32_t st = n_sig % ST, stage = ring + st * Sh::kStage;
-        const int kv = n_sig & 1;
-        uint32_t bad = 0;
-        const bool look = kv && edge_tile(a, sg.sp, sg.tile);
-        if (kFp8) {
-          if (n_sig >= ST) ok = warp_wait(sm.empty[st], (n_sig / ST - 1) & 1, abort);
-          if (!ok) return;
-          const uint32_t from = raw + (n_sig % Sh::kRawDepth) * Sh::kRaw + (w * kIter * 32 + lane) * 16;
+      if constexpr (kFp8) {
+        // the lane's row of the tile: its scales are fetched a tile ahead, its place two
+        Cursor<kTile, true> at = cu;
+        int left = steps;
+        Places<1> rows;
+        float ks = 0.f, vs = 0.f;
+        auto ahead = [&] {                     // `at` to the next tile with rows, its place looked up
+          while (left > 0 && at.sp.L <= 0) {
+            if (--left > 0) at.next(a, units);
+          }
+          rows.within[0] = -1;
+          if (left > 0) rows.lookup(a, at, w * 32 + lane, 1, 1);
+        };
+        auto fetch = [&] {
+          int row;
+          if (!rows.resolve(a, 0, w * 32 + lane, 1, -1, row)) row = -1;
+          const int h = chunks == 1 ? at.unit : at.unit / chunks;
+          ks = vs = 0.f;
+          if (row >= 0) ks = a.k_scale[(int64_t)row * a.scale_stride + h], vs = a.v_scale[(int64_t)row * a.scale_stride + h];
+          if (left > 0 && --left > 0) at.next(a, units);
+        };
+        ahead();
+        fetch();
+        ahead();
+        for (; ok && steps > 0; --steps) {
+          if (cu.sp.L > 0) {
+#pragma unroll 1
+            for (int kv = 0; kv < 2; ++kv, ++n) {
+              const uint32_t st = n % ST, stage = ring + st * Sh::kStage, slot = n % Sh::kRawDepth;
+              const bool look = kv && edge_tile(a, cu.sp, cu.tile);
+              uint32_t bad = 0;
+              ok = warp_wait(sm.raw_full[slot], (n / Sh::kRawDepth) & 1, abort);
+              if (ok && n >= ST) ok = warp_wait(sm.empty[st], (n / ST - 1) & 1, abort);
+              if (!ok) break;
+              const uint32_t from = raw + slot * Sh::kRaw + (w * kIter * 32 + lane) * 16;
 #pragma unroll 2
-          for (int i = 0; i < kIter; ++i) {
-            uint32_t c[4], u[8];
-            asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];\n" : "=r"(c[0]), "=r"(c[1]), "=r"(c[2]), "=r"(c[3]) : "r"(from + i * 512) : "memory");
-            if (look) {
-              uint32_t any = 0;
+              for (int i = 0; i < kIter; ++i) {
+                uint32_t c[4], u[8];
+                asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];\n" : "=r"(c[0]), "=r"(c[1]), "=r"(c[2]), "=r"(c[3]) : "r"(from + i * 512) : "memory");
+                if (look) {
+                  uint32_t any = 0;
 #pragma unroll
-              for (int x = 0; x < 4; ++x) any |= ((c[x] & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u;
-              if (any) {
-                bad |= 1u << (i * kAtOnce + r0);
+                  for (int x = 0; x < 4; ++x) any |= ((c[x] & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u;
+                  if (any) {
+                    bad |= 1u << (i * kAtOnce + r0);
+#pragma unroll
+                    for (int x = 0; x < 4; ++x) {
+                      const uint32_t nan = (((c[x] & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u) >> 7;   // 1 in a NaN's byte
+                      c[x] &= ~(nan * 0xffu);
+                    }
+                  }
+                }
 #pragma unroll
                 for (int x = 0; x < 4; ++x) {
-                  const uint32_t nan = (((c[x] & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u) >> 7;   // 1 in a NaN's byte
-                  c[x] &= ~(nan * 0xffu);
+                  uint32_t lo, hi;
+                  e4m3x4_to_f16x2(c[x], lo, hi);
+                  const float2 f0 = __half22float2(*reinterpret_cast<const __half2*>(&lo));
+                  const float2 f1 = __half22float2(*reinterpret_cast<const __half2*>(&hi));
+                  u[2 * x] = pack_bf16x2(f0.x, f0.y);
+                  u[2 * x + 1] = pack_bf16x2(f1.x, f1.y);
+                }
+                const uint32_t to = stage + place(i);
+                asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};\n" ::"r"(to), "r"(u[0]), "r"(u[1]), "r"(u[2]), "r"(u[3]) : "memory");
+                asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};\n" ::"r"(to ^ 16u), "r"(u[4]), "r"(u[5]), "r"(u[6]), "r"(u[7]) : "memory");
+              }
+              if (kv == 0) {
+                // the row's scales as the scores and weights take them; a V scale that is no
+                // number reaches whoever sees the row by its score
+                const uint32_t to = scales + ((n / 2) % kScaleTiles) * kScaleBytes + (w * 32 + lane) * 4;
+                const bool number = fabsf(vs) < INFINITY;
+                asm volatile("st.shared.f32 [%0], %1;\n" ::"r"(to), "f"(number ? ks * (a.scale * kLog2e) : __uint_as_float(0x7fffffffu)) : "memory");
+                asm volatile("st.shared.f32 [%0], %1;\n" ::"r"(to + kTile * 4), "f"(number ? vs : 1.f) : "memory");
+              }
+              if (look) {
+                bad = __reduce_or_sync(0xffffffffu, bad) & span_rows(cu.sp, cu.tile, w);
+                if (lane == 0) *(volatile uint32_t*)&sm.bad[st][w] = bad;
+              }
+              tc5::fence_proxy_async_smem();
+              __syncwarp();
+              if (lane == 0) {
+                tc5::mbar_arrive(smem_u32(&sm.full[st]));
+                tc5::mbar_arrive(smem_u32(&sm.raw_empty[slot]));
+                if (kv == 0) tc5::mbar_arrive(smem_u32(&sm.sc_full[(n / 2) % kScaleTiles]));
+              }
+              if (kv == 0) {
+                fetch();
+                ahead();
+              }
+            }
+          }
+          if (steps > 1) cu.next(a, units);
+        }
+      } else {
+        for (; ok && steps > 0; --steps) {
+          if (cu.sp.L > 0) {
+            if (edge_tile(a, cu.sp, cu.tile)) {
+              const uint32_t st = (n + 1) % ST, stage = ring + st * Sh::kStage;
+              ok = warp_wait(sm.land[st], (parity >> st) & 1, abort);
+              parity ^= 1u << st;
+              if (!ok) break;
+              uint32_t bad = 0;
+#pragma unroll 4
+              for (int i = 0; i < kIter; ++i) {
+                uint32_t c[4];
+                const uint32_t at = stage + place(i);
+                asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];\n" : "=r"(c[0]), "=r"(c[1]), "=r"(c[2]), "=r"(c[3]) : "r"(at) : "memory");
+                bool any = false;
+#pragma unroll
+                for (int x = 0; x < 4; ++x) any |= not_finite(c[x]) || not_finite(c[x] >> 16);
+                if (any) {
+                  bad |= 1u << (i * kAtOnce + r0);
+#pragma unroll
+                  for (int x = 0; x < 4; ++x)
+                    c[x] &= (not_finite(c[x]) ? 0u : 0xffffu) | (not_finite(c[x] >> 16) ? 0u : 0xffff0000u);
+                  asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};\n" ::"r"(at), "r"(c[0]), "r"(c[1]), "r"(c[2]), "r"(c[3]) : "memory");
+                }
+              }
+              bad = __reduce_or_sync(0xffffffffu, bad) & span_rows(cu.sp, cu.tile, w);
+              if (lane == 0) *(volatile uint32_t*)&sm.bad[st][w] = bad;
+              tc5::fence_proxy_async_smem();
+              __syncwarp();
+              if (lane == 0) {
+                __threadfence_block();
+                if ((atomicAdd(&sm.looked[st], 1) & 3) == 3) {   // the last of the four
+                  __threadfence_block();
+                  tc5::mbar_arrive(smem_u32(&sm.full[st]));
                 }
               }
             }
-#pragma unroll
-            for (int x = 0; x < 4; ++x) {
-              uint32_t lo, hi;
-              e4m3x4_to_f16x2(c[x], lo, hi);
-              const float2 f0 = __half22float2(*reinterpret_cast<const __half2*>(&lo));
-              const float2 f1 = __half22float2(*reinterpret_cast<const __half2*>(&hi));
-              u[2 * x] = pack_bf16x2(f0.x, f0.y);
-              u[2 * x + 1] = pack_bf16x2(f1.x, f1.y);
-            }
-            const uint32_t at = stage + place(i);
-            asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};\n" ::"r"(at), "r"(u[0]), "r"(u[1]), "r"(u[2]), "r"(u[3]) : "memory");
-            asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};\n" ::"r"(at ^ 16u), "r"(u[4]), "r"(u[5]), "r"(u[6]), "r"(u[7]) : "memory");
+            n += 2;
           }
-          if (kv == 0) {
-            // the row's scales as the scores and weights take them; a V scale that is no
-            // number reaches whoever sees the row by its score
-            const uint32_t at = scales + ((n_sig / 2) % kScaleTiles) * kScaleBytes + (w * 32 + lane) * 4;
-            float ks, vs;
-            asm volatile("ld.shared.f32 %0, [%1];\n" : "=f"(ks) : "r"(at) : "memory");
-            asm volatile("ld.shared.f32 %0, [%1];\n" : "=f"(vs) : "r"(at + kTile * 4) : "memory");
-            const bool number = fabsf(vs) < INFINITY;
-            ks = number ? ks * (a.scale * kLog2e) : __uint_as_float(0x7fffffffu);
-            asm volatile("st.shared.f32 [%0], %1;\n" ::"r"(at), "f"(ks) : "memory");
-            asm volatile("st.shared.f32 [%0], %1;\n" ::"r"(at + kTile * 4), "f"(number ? vs : 1.f) : "memory");
-          }
-        } else if (look) {
-#pragma unroll 1
-          for (int i = 0; i < kIter; ++i) {
-            uint32_t c[4];
-            const uint32_t at = stage + place(i);
-            asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];\n" : "=r"(c[0]), "=r"(c[1]), "=r"(c[2]), "=r"(c[3]) : "r"(at) : "memory");
-            bool any = false;
-#pragma unroll
-            for (int x = 0; x < 4; ++x) any |= not_finite(c[x]) || not_finite(c[x] >> 16);
-            if (any) {
-              bad |= 1u << (i * kAtOnce + r0);
-#pragma unroll
-              for (int x = 0; x < 4; ++x)
-                c[x] &= (not_finite(c[x]) ? 0u : 0xffffu) | (not_finite(c[x] >> 16) ? 0u : 0xffff0000u);
-              asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};\n" ::"r"(at), "r"(c[0]), "r"(c[1]), "r"(c[2]), "r"(c[3]) : "memory");
-            }
-          }
+          if (steps > 1) cu.next(a, units);
         }
-        if (look) {
-          bad = __reduce_or_sync(0xffffffffu, bad);
-          if (lane == 0) *(volatile uint32_t*)&sm.bad[st][w] = bad;
-        }
-        tc5::fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0) {
-          tc5::mbar_arrive(smem_u32(&sm.full[st]));
-          if (kFp8 && kv == 0) tc5::mbar_arrive(smem_u32(&sm.sc_full[(n_sig / 2) % kScaleTiles]));
-        }
-        ++n_sig;
-        if (kv) sg.next(a, units);
-      };
-      lookup(ld);
+      }
+    } else if (warp == kLoadWarp) {
+      // ---------------------------------------------------------- row loader
+      // lane: `per` segments of the tile from per * lane on, looked up one tile ahead
+      const int steps = (int)(sm.cut[1].at - sm.cut[0].at);
+      Cursor<kTile, true> ld;
+      ld.b = sm.cut[0].b;
+      ld.sp.set(a, ld.b);
+      ld.unit = sm.cut[0].unit;
+      ld.tile = sm.cut[0].tile;
+      if (lane == 0) {
+        tc5::prefetch_tmap(&kmap);
+        tc5::prefetch_tmap(&vmap);
+      }
+      const int segs = kTile / seg, per = (segs + 31) / 32, mine = lane * per < segs ? per : 0, none = a.rows > 0 ? (int)a.rows : 1;
+      Places<4> rows;
+      uint32_t n = 0;
+      bool ok = true;
+      rows.lookup(a, ld, per * lane, seg, mine);
       for (int step = 0; ok && step < steps; ++step) {
         if (ld.sp.L > 0) {
-          resolve();
+          int row[4];                            // a row behind the pool reads as zeros
+          bool all = true;
+#pragma unroll
+          for (int i = 0; i < 4; ++i) all &= rows.resolve(a, i, per * lane, seg, none, row[i]);
+          if (!all && a.status) set_status(a.status, kStatusBadIndex);
           const int h = chunks == 1 ? ld.unit : ld.unit / chunks;
 #pragma unroll 1
-          for (int kv = 0; kv < 2; ++kv) {
-            uint32_t to;
+          for (int kv = 0; kv < 2; ++kv, ++n) {
+            const uint32_t st = n % ST, slot = n % Sh::kRawDepth;
+            uint64_t* bar;
             if (kFp8) {
-              to = raw + (n_iss % Sh::kRawDepth) * Sh::kRaw + (w * kIter * 32 + lane) * 16;
-              if (kv == 0) {
-                const int64_t at = (int64_t)(prow < 0 ? 0 : prow) * a.scale_stride + h;
-                const uint32_t dst = scales + ((n_iss / 2) % kScaleTiles) * kScaleBytes + (w * 32 + lane) * 4;
-                cp_async4(dst, a.k_scale + at, prow < 0 ? 0 : 4);
-                cp_async4(dst + kTile * 4, a.v_scale + at, prow < 0 ? 0 : 4);
-              }
+              if (n >= (uint32_t)Sh::kRawDepth) ok = warp_wait(sm.raw_empty[slot], (n / Sh::kRawDepth - 1) & 1, abort);
+              bar = &sm.raw_full[slot];
             } else {
-              const uint32_t st = n_iss % ST;
-              if (n_iss >= ST) ok = warp_wait(sm.empty[st], (n_iss / ST - 1) & 1, abort);
-              if (!ok) break;
-              to = ring + st * Sh::kStage;
+              if (n >= ST) ok = warp_wait(sm.empty[st], (n / ST - 1) & 1, abort);
+              bar = kv && edge_tile(a, ld.sp, ld.tile) ? &sm.land[st] : &sm.full[st];
             }
-            const uint8_t* src = static_cast<const uint8_t*>(kv ? a.v : a.k) + (h * kRowBytes + ch * 16);
-            const uint32_t pitch = kv ? a.v_step : a.k_step;
+            if (!ok) break;
+            if (lane == 0) tc5::mbar_expect_tx(smem_u32(bar), kFp8 ? Sh::kRaw : Sh::kStage);
+            __syncwarp();
 #pragma unroll
-            for (int i = 0; i < kIter; ++i) {
-              const int p = __shfl_sync(0xffffffffu, prow, i * kAtOnce + r0);
-              cp_async16(kFp8 ? to + i * 512 : to + place(i), src + (uint64_t)(p < 0 ? 0u : (uint32_t)p) * pitch, p < 0 ? 0 : 16);
-            }
-            cp_async_commit();
-            ++n_iss;
-            if (n_iss - n_sig > Sh::kDepth) {
-              cp_async_wait<Sh::kDepth>();
-              hand_on();
+            for (int i = 0; i < 4; ++i) {
+              if (i >= mine) continue;
+              const uint32_t to = (kFp8 ? raw + slot * Sh::kRaw : ring + st * Sh::kStage) + (per * lane + i) * seg * 128;
+#pragma unroll
+              for (int x = 0; x < (kFp8 ? 1 : Sh::kSubs); ++x)
+                tc5::tma_load_2d(to + x * kSub, kv ? &vmap : &kmap, h * D + 64 * x, row[i], smem_u32(bar));
             }
           }
         }
         if (step + 1 < steps) {
           ld.next(a, units);
-          lookup(ld);
+          rows.lookup(a, ld, per * lane, seg, mine);
         }
       }
-      cp_async_wait<0>();
-      while (ok && n_sig < n_iss) hand_on();
+      // the copies in flight land before the block ends (they have, unless a wait gave up)
+      constexpr uint32_t kInFlight = kFp8 ? Sh::kRawDepth : ST;
+      for (uint32_t m = n > kInFlight ? n - kInFlight : 0; m < n; ++m)
+        if (!tc5::mbar_wait_drain(smem_u32(kFp8 ? &sm.raw_full[m % kInFlight] : &sm.full[m % kInFlight]), (m / kInFlight) & 1)) break;
     } else if (warp == kMmaWarp) {
       // ---------------------------------------------------------- MMA issue
-      if (lane == 0) {
-        const uint32_t idesc_s = tc5::idesc_bf16_f32(128, kTile);
-        const uint32_t idesc_o = tc5::idesc_bf16_f32(128, D) | (1u << 16);   // B MN-major
-        const uint64_t dq = tc5::sdesc_k_sw128(qsm), dk = tc5::sdesc_k_sw128(ring), dv = sdesc_mn_sw128(ring, kSub);
-        uint32_t n_p[2] = {0, 0}, n_q = 0, n0 = 0;   // phases; the piece's first chunk
-        bool ok = true;
-        auto wait = [&](uint64_t& bar, uint32_t parity) {
-          if (ok) ok = tc5::mbar_wait(smem_u32(&bar), parity, abort);
-          tc5::fence_after_sync();
-        };
-        auto landed = [&](uint32_t n) { wait(sm.full[n % ST], (n / ST) & 1); };
-        auto release = [&](uint32_t n) { tc5::mma_commit(smem_u32(&sm.empty[n % ST])); };
-        auto qk = [&](int slot, uint32_t n) {
-          const uint64_t q = dq + ((kPair ? 0 : slot * Sh::kStage) >> 4), k = dk + (((n % ST) * Sh::kStage) >> 4);
+      // The warp runs as one (waits, ring places: the same in every lane), a lane issues.
+      // Places in the ring are counted up, not divided out: the chain from a softmax's end
+      // to its slot's next products is on everyone's way.
+      const bool one = lane == 0;
+      constexpr uint32_t idesc_s = tc5::idesc_bf16_f32(128, kTile);
+      constexpr uint32_t idesc_o = tc5::idesc_bf16_f32(128, D) | (1u << 16);   // B MN-major
+      const uint64_t dq = tc5::sdesc_k_sw128(qsm), dk = tc5::sdesc_k_sw128(ring), dv = sdesc_mn_sw128(ring, kSub);
+      uint32_t kst = 0, kph = 0, vst = 1, vph = 0;   // the next K and V: stage and phase
+      uint32_t pph0 = 0, pph1 = 0, qph = 0;
+      bool ok = true;
+      auto wait = [&](uint64_t& bar, uint32_t parity) {
+        uint32_t i = 0;
+        while (ok && !tc5::mbar_try_wait(smem_u32(&bar), parity)) {
+          if ((++i & 63u) == 0 && (*abort || i >= tc5::kWaitPolls)) {
+            *abort = 1;
+            ok = false;
+          }
+        }
+        ok = __all_sync(0xffffffffu, ok);
+        tc5::fence_after_sync();
+      };
+      auto commit = [&](uint64_t& bar) {
+        if (one) tc5::mma_commit(smem_u32(&bar));
+      };
+      auto next_k = [&] {
+        kst += 2;
+        if (kst >= ST) kst -= ST, kph ^= 1;
+      };
+      auto next_v = [&] {
+        vst += 2;
+        if (vst >= ST) vst -= ST, vph ^= 1;
+      };
+      auto qk = [&](int slot) {
+        if (one) {
+          const uint64_t q = dq + ((kPair ? 0 : slot * Sh::kStage) >> 4), k = dk + ((kst * Sh::kStage) >> 4);
 #pragma unroll
           for (int x = 0; x < D / 16; ++x)
             tc5::mma_bf16(tmem + slot * 128, q + (((x >> 2) * kSub + (x & 3) * 32) >> 4),
                           k + (((x >> 2) * kSub + (x & 3) * 32) >> 4), idesc_s, x > 0);
-        };
-        auto pv = [&](int slot, uint32_t n) {
-          const uint64_t v = dv + (((n % ST) * Sh::kStage) >> 4);
+        }
+      };
+      auto pv = [&](int slot) {
+        if (one) {
+          const uint64_t v = dv + ((vst * Sh::kStage) >> 4);
 #pragma unroll
           for (int x = 0; x < kTile / 16; ++x)
             tc5::mma_bf16_ta(tmem + 256 + slot * 128, tmem + slot * 128 + 8 * x, v + ((x * 2048) >> 4), idesc_o, 1u);
+        }
+      };
+      auto weights = [&](int slot) {
+        uint32_t& ph = slot ? pph1 : pph0;
+        wait(sm.p_full[slot], ph);
+        ph ^= 1;
+      };
+      Walk walk;
+      walk.init(a, sm.cut);
+      Piece pc;
+      while (ok && walk.next(a, units, pc)) {
+        if (pc.sp.L <= 0) continue;
+        const int h = chunks == 1 ? pc.unit : pc.unit / chunks, row0 = (pc.unit - h * chunks) * kRows;
+        const bool two = kPair ? pc.nt > 1 : row0 + 128 < qrows;
+        wait(sm.q_full, qph);
+        qph ^= 1;
+        // step j: slot's weights of tile j, then its scores of the next tile it takes
+        auto pair_step = [&](int j, int slot) {
+          if (j >= 0 && ok) {
+            wait(sm.full[vst], vph);
+            weights(slot);
+            if (!ok) return;
+            pv(slot);
+            commit(sm.empty[vst]);
+            next_v();
+          }
+          if (j + 2 < pc.nt) {
+            wait(sm.full[kst], kph);
+            if (!ok) return;
+            qk(slot);
+            commit(sm.s_full[slot]);
+            commit(sm.empty[kst]);
+            if (j + 3 == pc.nt) commit(sm.q_empty);
+            next_k();
+          } else if (j >= 0) {
+            commit(sm.o_full[slot]);
+          }
         };
-        Walk walk;
-        walk.init(a, sm.cut);
-        Piece pc;
-        while (ok && walk.next(a, units, pc)) {
-          if (pc.sp.L <= 0) continue;
-          const int h = chunks == 1 ? pc.unit : pc.unit / chunks, row0 = (pc.unit - h * chunks) * kRows;
-          const bool two = kPair ? pc.nt > 1 : row0 + 128 < qrows;
-          wait(sm.q_full, n_q & 1);
-          ++n_q;
-          if (kPair) {
-#pragma unroll 1
-            for (int j = -2; ok && j < pc.nt; ++j) {
-              const int slot = j & 1;
-              if (j >= 0) {
-                wait(sm.p_full[slot], n_p[slot] & 1);
-                ++n_p[slot];
-                landed(n0 + 2 * j + 1);
-                if (!ok) break;
-                pv(slot, n0 + 2 * j + 1);
-                release(n0 + 2 * j + 1);
-              }
-              if (j + 2 < pc.nt) {
-                landed(n0 + 2 * (j + 2));
-                if (!ok) break;
-                qk(slot, n0 + 2 * (j + 2));
-                release(n0 + 2 * (j + 2));
-                tc5::mma_commit(smem_u32(&sm.s_full[slot]));
-                if (j + 3 == pc.nt) tc5::mma_commit(smem_u32(&sm.q_empty));
-              } else if (j >= 0) {
-                tc5::mma_commit(smem_u32(&sm.o_full[slot]));
-              }
-            }
-          } else {
-#pragma unroll 1
-            for (int j = -1; ok && j < pc.nt; ++j) {
-#pragma unroll 1
-              for (int slot = 0; slot < (two ? 2 : 1); ++slot) {
-                const bool end = slot == (two ? 1 : 0);
-                if (j >= 0) {
-                  wait(sm.p_full[slot], n_p[slot] & 1);
-                  ++n_p[slot];
-                  if (slot == 0) landed(n0 + 2 * j + 1);
-                  if (!ok) break;
-                  pv(slot, n0 + 2 * j + 1);
-                  if (end) release(n0 + 2 * j + 1);
-                }
-                if (j + 1 < pc.nt) {
-                  if (slot == 0) landed(n0 + 2 * (j + 1));
-                  if (!ok) break;
-                  qk(slot, n0 + 2 * (j + 1));
-                  if (end) release(n0 + 2 * (j + 1));
-                  tc5::mma_commit(smem_u32(&sm.s_full[slot]));
-                  if (end && j + 2 == pc.nt) tc5::mma_commit(smem_u32(&sm.q_empty));
-                } else {
-                  tc5::mma_commit(smem_u32(&sm.o_full[slot]));
-                }
-              }
+        auto step = [&](int j, int slot, bool end) {
+          if (j >= 0) {
+            if (slot == 0) wait(sm.full[vst], vph);
+            weights(slot);
+            if (!ok) return;
+            pv(slot);
+            if (end) {
+              commit(sm.empty[vst]);
+              next_v();
             }
           }
-          n0 += 2 * pc.nt;
+          if (j + 1 < pc.nt) {
+            if (slot == 0) wait(sm.full[kst], kph);
+            if (!ok) return;
+            qk(slot);
+            commit(sm.s_full[slot]);
+            if (end) {
+              commit(sm.empty[kst]);
+              if (j + 2 == pc.nt) commit(sm.q_empty);
+              next_k();
+            }
+          } else {
+            commit(sm.o_full[slot]);
+          }
+        };
+        if (kPair) {
+#pragma unroll 1
+          for (int j = -2; ok && j < pc.nt; j += 2) {
+            pair_step(j, 0);
+            if (ok && j + 1 < pc.nt) pair_step(j + 1, 1);
+          }
+        } else if (two) {
+#pragma unroll 1
+          for (int j = -1; ok && j < pc.nt; ++j) {
+            step(j, 0, false);
+            if (ok) step(j, 1, true);
+          }
+        } else {
+#pragma unroll 1
+          for (int j = -1; ok && j < pc.nt; ++j) step(j, 0, true);
         }
-        tc5::mma_commit(smem_u32(&sm.done));
-        tc5::mbar_wait_drain(smem_u32(&sm.done), 0);
       }
+      commit(sm.done);
+      tc5::mbar_wait_drain(smem_u32(&sm.done), 0);
       __syncwarp();
     } else {
       // ---------------------------------------------------------- the units' query rows
@@ -834,6 +977,21 @@ __global__ void __launch_bounds__(256)
   if (a.lse && c0 == 0) a.lse[tok * a.heads + hd] = any ? (m + log2f(l)) * kLn2 : -INFINITY;
 }
 
+// The pool's rows, `width` elements each, copied `seg` rows of 128 bytes at a time.
+bool make_pool_map(CUtensorMap* m, const void* ptr, int64_t rows, uint64_t width, uint64_t step, bool fp8, int dim, int seg) {
+  auto fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(tensor_map_encoder());
+  if (!fn) return false;
+  cuuint64_t dims[2] = {(cuuint64_t)width, (cuuint64_t)(rows > 0 ? rows : 1)};
+  cuuint64_t strides[1] = {step};
+  cuuint32_t box[2] = {fp8 ? 128u : 64u, (cuuint32_t)seg};
+  cuuint32_t estr[2] = {1, 1};
+  return fn(m, fp8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(ptr), dims, strides,
+            box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, fp8 ? CU_TENSOR_MAP_SWIZZLE_NONE : CU_TENSOR_MAP_SWIZZLE_128B,
+            // a head's row is 256 bytes of a bf16 pool of 128 dims, 128 otherwise
+            !fp8 && dim == 128 ? CU_TENSOR_MAP_L2_PROMOTION_L2_256B : CU_TENSOR_MAP_L2_PROMOTION_L2_128B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 template <int D, int kRows, bool kFp8>
 int launch_rows(const PagedArgs& a, int num_sms, cudaStream_t st, bool pdl) {
   using Sh = TtShape<D, kRows, kFp8>;
@@ -848,12 +1006,18 @@ int launch_rows(const PagedArgs& a, int num_sms, cudaStream_t st, bool pdl) {
         return allow_max_dynamic_smem(kern);
       }))
     return launch_fail("cudaFuncSetAttribute(tree_kernel)", e);
+  int seg = kTile;                               // rows of a copy: a power of two that divides a page
+  while (a.table && a.block % seg != 0) seg /= 2;
+  CUtensorMap kmap, vmap;
+  if (!make_pool_map(&kmap, a.k, a.rows, (uint64_t)a.kv_heads * D, a.k_step, kFp8, D, seg) ||
+      !make_pool_map(&vmap, a.v, a.rows, (uint64_t)a.kv_heads * D, a.v_step, kFp8, D, seg))
+    return launch_fail("cuTensorMapEncodeTiled(K / V pools)", cudaErrorInvalidValue);
   const int qrows = a.S * (a.heads / a.kv_heads), chunks = (qrows + kRows - 1) / kRows;
   float* part = static_cast<float*>(a.workspace);
   PaJoin* joins = reinterpret_cast<PaJoin*>(part + (size_t)num_sms * 2 * kRows * (D + 2));
   const int64_t tiles = (int64_t)a.B * a.kv_heads * chunks * ((a.max_len + kTile - 1) / kTile + kExtra);
   const int grid = tiles < num_sms ? (int)tiles : num_sms;
-  const int r = launch_kernel(kern, dim3(grid), dim3(kTtThreads), Sh::kSmem, st, pdl, a, chunks, a.kv_heads * chunks, part, joins);
+  const int r = launch_kernel(kern, dim3(grid), dim3(kTtThreads), Sh::kSmem, st, pdl, kmap, vmap, a, seg, chunks, a.kv_heads * chunks, part, joins);
   if (r < 0) return r;
   const int most = qrows < kRows ? qrows : kRows;
   const int r2 = launch_kernel(tree_join_kernel<D>, dim3(grid, (most + 31) / 32), dim3(256), 0, st, pdl, a, chunks, kRows,
