@@ -28,8 +28,11 @@
 //                    rows 80 cycles each: 1699 and 2527 us for 64 x 16 drafts.)
 //   warps 8-11       E4M3: convert the codes, which land beside the ring; bf16: look
 //                    through V's rows in edge tiles;
-//   warp 12          issues the MMAs: S = Q K^T, O += P V (P from tensor memory);
-//   warps 14, 15     the unit's query rows.
+//   warps 12, 14     issue the MMAs of slot 0 and 1: S = Q K^T, O += P V (P from tensor
+//                    memory).  An issue waits for the pipe, so one warp for both slots
+//                    left the pipe idle over its waits (4700 cycles for two slots'
+//                    tile, of which 1900 are products);
+//   warp 15          the unit's query rows.
 //
 // Masks.  A tile that some draft does not see whole (the window's first rows,
 // the drafts') is an edge tile: each thread builds the 128 bits of its row and
@@ -52,7 +55,7 @@ namespace csa {
 namespace {
 
 constexpr int kTtThreads = 512;
-constexpr int kRowWarp = 8, kRowWarps = 4, kMmaWarp = 12, kLoadWarp = 13, kQWarp = 14, kQThreads = 64;
+constexpr int kRowWarp = 8, kRowWarps = 4, kMmaWarp = 12, kMmaWarp2 = 14, kLoadWarp = 13;
 constexpr int kRegsSoftmax = 184, kRegsOthers = 72;   // of the launch's 128 per thread
 constexpr int kTile = 128;                 // K / V rows per tile
 constexpr int kExtra = 2;                  // a unit's start and end, in tiles
@@ -66,7 +69,7 @@ struct TtSmem {
   uint64_t land[8];                        // bf16 V of an edge tile, before it was looked through
   uint64_t raw_full[3], raw_empty[3];      // chunks of E4M3 codes
   uint64_t s_full[2], p_full[2], o_full[2];
-  uint64_t q_full, q_empty, sc_full[kScaleTiles], pair, done;
+  uint64_t q_full, q_empty, sc_full[kScaleTiles], pair, done[2];
   uint32_t tmem;
   int abort;
   PaCost scan[33];
@@ -301,7 +304,7 @@ __global__ void __launch_bounds__(kTtThreads, 1)
     sm.abort = 0;
     for (int i = 0; i < 8; ++i) {
       tc5::mbar_init(smem_u32(&sm.full[i]), kFp8 ? kRowWarps : 1);
-      tc5::mbar_init(smem_u32(&sm.empty[i]), 1);
+      tc5::mbar_init(smem_u32(&sm.empty[i]), kPair ? 1 : 2);   // the slots that read a stage
       tc5::mbar_init(smem_u32(&sm.land[i]), 1);
       sm.looked[i] = 0;
     }
@@ -315,10 +318,10 @@ __global__ void __launch_bounds__(kTtThreads, 1)
       tc5::mbar_init(smem_u32(&sm.p_full[i]), 4);
       tc5::mbar_init(smem_u32(&sm.o_full[i]), 1);
     }
-    tc5::mbar_init(smem_u32(&sm.q_full), kQThreads / 32);
-    tc5::mbar_init(smem_u32(&sm.q_empty), 1);
+    tc5::mbar_init(smem_u32(&sm.q_full), 1);
+    tc5::mbar_init(smem_u32(&sm.q_empty), 2);
     tc5::mbar_init(smem_u32(&sm.pair), 256);
-    tc5::mbar_init(smem_u32(&sm.done), 1);
+    for (int i = 0; i < 2; ++i) tc5::mbar_init(smem_u32(&sm.done[i]), 1);
     tc5::fence_mbar_init();
   }
   if (warp == kMmaWarp) {
@@ -765,17 +768,19 @@ __global__ void __launch_bounds__(kTtThreads, 1)
       constexpr uint32_t kInFlight = kFp8 ? Sh::kRawDepth : ST;
       for (uint32_t m = n > kInFlight ? n - kInFlight : 0; m < n; ++m)
         if (!tc5::mbar_wait_drain(smem_u32(kFp8 ? &sm.raw_full[m % kInFlight] : &sm.full[m % kInFlight]), (m / kInFlight) & 1)) break;
-    } else if (warp == kMmaWarp) {
+    } else if (warp == kMmaWarp || warp == kMmaWarp2) {
       // ---------------------------------------------------------- MMA issue
       // The warp runs as one (waits, ring places: the same in every lane), a lane issues.
       // Places in the ring are counted up, not divided out: the chain from a softmax's end
       // to its slot's next products is on everyone's way.
       const bool one = lane == 0;
+      const int slot = warp == kMmaWarp ? 0 : 1;
       constexpr uint32_t idesc_s = tc5::idesc_bf16_f32(128, kTile);
       constexpr uint32_t idesc_o = tc5::idesc_bf16_f32(128, D) | (1u << 16);   // B MN-major
-      const uint64_t dq = tc5::sdesc_k_sw128(qsm), dk = tc5::sdesc_k_sw128(ring), dv = sdesc_mn_sw128(ring, kSub);
-      uint32_t kst = 0, kph = 0, vst = 1, vph = 0;   // the next K and V: stage and phase
-      uint32_t pph0 = 0, pph1 = 0, qph = 0;
+      const uint64_t dq = tc5::sdesc_k_sw128(qsm + (kPair ? 0 : slot * Sh::kStage));
+      const uint64_t dk = tc5::sdesc_k_sw128(ring), dv = sdesc_mn_sw128(ring, kSub);
+      const uint32_t s_at = tmem + slot * 128, o_at = tmem + 256 + slot * 128;
+      uint32_t n0 = 0, pph = 0, qph = 0;       // the piece's first chunk; phases
       bool ok = true;
       auto wait = [&](uint64_t& bar, uint32_t parity) {
         uint32_t i = 0;
@@ -788,114 +793,81 @@ __global__ void __launch_bounds__(kTtThreads, 1)
         ok = __all_sync(0xffffffffu, ok);
         tc5::fence_after_sync();
       };
-      auto commit = [&](uint64_t& bar) {
-        if (one) tc5::mma_commit(smem_u32(&bar));
-      };
-      auto next_k = [&] {
-        kst += 2;
-        if (kst >= ST) kst -= ST, kph ^= 1;
-      };
-      auto next_v = [&] {
-        vst += 2;
-        if (vst >= ST) vst -= ST, vph ^= 1;
-      };
-      auto qk = [&](int slot) {
-        if (one) {
-          const uint64_t q = dq + ((kPair ? 0 : slot * Sh::kStage) >> 4), k = dk + ((kst * Sh::kStage) >> 4);
-#pragma unroll
-          for (int x = 0; x < D / 16; ++x)
-            tc5::mma_bf16(tmem + slot * 128, q + (((x >> 2) * kSub + (x & 3) * 32) >> 4),
-                          k + (((x >> 2) * kSub + (x & 3) * 32) >> 4), idesc_s, x > 0);
+      // a chunk's place in the ring, moved on by kStep chunks at a time
+      struct Place {
+        uint32_t st, ph;
+        __device__ __forceinline__ void set(uint32_t n) { st = n % ST, ph = (n / ST) & 1; }
+        __device__ __forceinline__ void move(uint32_t by) {
+          st += by;
+          while (st >= ST) st -= ST, ph ^= 1;
         }
       };
-      auto pv = [&](int slot) {
-        if (one) {
-          const uint64_t v = dv + ((vst * Sh::kStage) >> 4);
-#pragma unroll
-          for (int x = 0; x < kTile / 16; ++x)
-            tc5::mma_bf16_ta(tmem + 256 + slot * 128, tmem + slot * 128 + 8 * x, v + ((x * 2048) >> 4), idesc_o, 1u);
-        }
-      };
-      auto weights = [&](int slot) {
-        uint32_t& ph = slot ? pph1 : pph0;
-        wait(sm.p_full[slot], ph);
-        ph ^= 1;
-      };
+      constexpr uint32_t kStep = kPair ? 4 : 2;  // from one tile of the slot to its next
       Walk walk;
       walk.init(a, sm.cut);
       Piece pc;
       while (ok && walk.next(a, units, pc)) {
         if (pc.sp.L <= 0) continue;
         const int h = chunks == 1 ? pc.unit : pc.unit / chunks, row0 = (pc.unit - h * chunks) * kRows;
-        const bool two = kPair ? pc.nt > 1 : row0 + 128 < qrows;
-        wait(sm.q_full, qph);
-        qph ^= 1;
-        // step j: slot's weights of tile j, then its scores of the next tile it takes
-        auto pair_step = [&](int j, int slot) {
-          if (j >= 0 && ok) {
-            wait(sm.full[vst], vph);
-            weights(slot);
-            if (!ok) return;
-            pv(slot);
-            commit(sm.empty[vst]);
-            next_v();
-          }
-          if (j + 2 < pc.nt) {
-            wait(sm.full[kst], kph);
-            if (!ok) return;
-            qk(slot);
-            commit(sm.s_full[slot]);
-            commit(sm.empty[kst]);
-            if (j + 3 == pc.nt) commit(sm.q_empty);
-            next_k();
-          } else if (j >= 0) {
-            commit(sm.o_full[slot]);
-          }
-        };
-        auto step = [&](int j, int slot, bool end) {
-          if (j >= 0) {
-            if (slot == 0) wait(sm.full[vst], vph);
-            weights(slot);
-            if (!ok) return;
-            pv(slot);
-            if (end) {
-              commit(sm.empty[vst]);
-              next_v();
+        const bool busy = kPair ? pc.nt > slot : row0 + slot * 128 < qrows;
+        if (!busy) {
+          // no rows or tiles for this slot: what it would have read is given back
+          if (!kPair) {
+            Place c;
+            c.set(n0);
+#pragma unroll 1
+            for (int i = 0; ok && i < 2 * pc.nt; ++i, c.move(1)) {
+              wait(sm.full[c.st], c.ph);
+              if (ok && one) tc5::mbar_arrive(smem_u32(&sm.empty[c.st]));
             }
           }
-          if (j + 1 < pc.nt) {
-            if (slot == 0) wait(sm.full[kst], kph);
-            if (!ok) return;
-            qk(slot);
-            commit(sm.s_full[slot]);
-            if (end) {
-              commit(sm.empty[kst]);
-              if (j + 2 == pc.nt) commit(sm.q_empty);
-              next_k();
-            }
-          } else {
-            commit(sm.o_full[slot]);
-          }
-        };
-        if (kPair) {
-#pragma unroll 1
-          for (int j = -2; ok && j < pc.nt; j += 2) {
-            pair_step(j, 0);
-            if (ok && j + 1 < pc.nt) pair_step(j + 1, 1);
-          }
-        } else if (two) {
-#pragma unroll 1
-          for (int j = -1; ok && j < pc.nt; ++j) {
-            step(j, 0, false);
-            if (ok) step(j, 1, true);
-          }
+          wait(sm.q_full, qph);
+          if (ok && one) tc5::mbar_arrive(smem_u32(&sm.q_empty));
         } else {
+          Place k, v;
+          k.set(n0 + (kPair ? 2 * slot : 0));
+          v.set(n0 + (kPair ? 2 * slot : 0) + 1);
+          wait(sm.q_full, qph);
+          // tile j's scores, then with its weights the output, and the next tile's scores
+          const int first = kPair ? slot : 0, step = kPair ? 2 : 1;
 #pragma unroll 1
-          for (int j = -1; ok && j < pc.nt; ++j) step(j, 0, true);
+          for (int j = first - step; j < pc.nt; j += step) {
+            if (j >= first) {
+              wait(sm.full[v.st], v.ph);
+              wait(sm.p_full[slot], pph);
+              pph ^= 1;
+              if (!ok) break;
+              if (one) {
+                const uint64_t d = dv + ((v.st * Sh::kStage) >> 4);
+#pragma unroll
+                for (int x = 0; x < kTile / 16; ++x) tc5::mma_bf16_ta(o_at, s_at + 8 * x, d + ((x * 2048) >> 4), idesc_o, 1u);
+                tc5::mma_commit(smem_u32(&sm.empty[v.st]));
+                if (j + step >= pc.nt) tc5::mma_commit(smem_u32(&sm.o_full[slot]));
+              }
+              v.move(kStep);
+            }
+            if (j + step < pc.nt) {
+              wait(sm.full[k.st], k.ph);
+              if (!ok) break;
+              if (one) {
+                const uint64_t d = dk + ((k.st * Sh::kStage) >> 4);
+#pragma unroll
+                for (int x = 0; x < D / 16; ++x)
+                  tc5::mma_bf16(s_at, dq + (((x >> 2) * kSub + (x & 3) * 32) >> 4), d + (((x >> 2) * kSub + (x & 3) * 32) >> 4),
+                                idesc_s, x > 0);
+                tc5::mma_commit(smem_u32(&sm.s_full[slot]));
+                tc5::mma_commit(smem_u32(&sm.empty[k.st]));
+                if (j + 2 * step >= pc.nt) tc5::mma_commit(smem_u32(&sm.q_empty));
+              }
+              k.move(kStep);
+            }
+          }
         }
+        qph ^= 1;
+        n0 += 2 * pc.nt;
       }
-      commit(sm.done);
-      tc5::mbar_wait_drain(smem_u32(&sm.done), 0);
+      if (one) tc5::mma_commit(smem_u32(&sm.done[slot]));
+      tc5::mbar_wait_drain(smem_u32(&sm.done[slot]), 0);
       __syncwarp();
     } else {
       // ---------------------------------------------------------- the units' query rows
@@ -910,8 +882,8 @@ __global__ void __launch_bounds__(kTtThreads, 1)
         if (n_q > 0) ok = warp_wait(sm.q_empty, (n_q - 1) & 1, abort);
         if (!ok) break;
         const __nv_bfloat16* q0 = static_cast<const __nv_bfloat16*>(a.q) + (int64_t)pc.b * a.S * a.q_stride;
-#pragma unroll 4
-        for (int x = tid - kQWarp * 32; x < kRows * (D / 8); x += kQThreads) {
+#pragma unroll 8
+        for (int x = lane; x < kRows * (D / 8); x += 32) {
           const int r = x / (D / 8), c = x % (D / 8), i = row0 + r;
           const int s = i < qrows ? token_of(i) : 0;
           const __nv_bfloat16* src = q0 + (int64_t)s * a.q_stride + (h * group + i - s * group) * D + c * 8;
