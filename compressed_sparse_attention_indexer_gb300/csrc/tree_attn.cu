@@ -169,6 +169,13 @@ __device__ __forceinline__ uint64_t sdesc_mn_sw128(uint32_t saddr, uint32_t lbo)
 }
 __device__ __forceinline__ bool not_finite(uint32_t bf16_bits) { return (bf16_bits & 0x7f80u) == 0x7f80u; }
 
+// One lane of a warp that runs as one: the same lane every time.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}\n" : "=r"(p));
+  return p != 0;
+}
+
 // A wait that a whole warp makes: true when every lane saw the phase.
 __device__ __forceinline__ bool warp_wait(uint64_t& bar, uint32_t parity, volatile int* abort) {
   return __all_sync(0xffffffffu, tc5::mbar_wait_backoff(smem_u32(&bar), parity, abort, 64));
@@ -773,8 +780,7 @@ __global__ void __launch_bounds__(kTtThreads, 1)
       // The warp runs as one (waits, ring places: the same in every lane), a lane issues.
       // Places in the ring are counted up, not divided out: the chain from a softmax's end
       // to its slot's next products is on everyone's way.
-      const bool one = lane == 0;
-      const int slot = warp == kMmaWarp ? 0 : 1;
+      const int slot = __shfl_sync(0xffffffffu, warp, 0) == kMmaWarp ? 0 : 1;
       constexpr uint32_t idesc_s = tc5::idesc_bf16_f32(128, kTile);
       constexpr uint32_t idesc_o = tc5::idesc_bf16_f32(128, D) | (1u << 16);   // B MN-major
       const uint64_t dq = tc5::sdesc_k_sw128(qsm + (kPair ? 0 : slot * Sh::kStage));
@@ -818,11 +824,11 @@ __global__ void __launch_bounds__(kTtThreads, 1)
 #pragma unroll 1
             for (int i = 0; ok && i < 2 * pc.nt; ++i, c.move(1)) {
               wait(sm.full[c.st], c.ph);
-              if (ok && one) tc5::mbar_arrive(smem_u32(&sm.empty[c.st]));
+              if (ok && elect_one()) tc5::mbar_arrive(smem_u32(&sm.empty[c.st]));
             }
           }
           wait(sm.q_full, qph);
-          if (ok && one) tc5::mbar_arrive(smem_u32(&sm.q_empty));
+          if (ok && elect_one()) tc5::mbar_arrive(smem_u32(&sm.q_empty));
         } else {
           Place k, v;
           k.set(n0 + (kPair ? 2 * slot : 0));
@@ -837,7 +843,7 @@ __global__ void __launch_bounds__(kTtThreads, 1)
               wait(sm.p_full[slot], pph);
               pph ^= 1;
               if (!ok) break;
-              if (one) {
+              if (elect_one()) {
                 const uint64_t d = dv + ((v.st * Sh::kStage) >> 4);
 #pragma unroll
                 for (int x = 0; x < kTile / 16; ++x) tc5::mma_bf16_ta(o_at, s_at + 8 * x, d + ((x * 2048) >> 4), idesc_o, 1u);
@@ -849,7 +855,7 @@ __global__ void __launch_bounds__(kTtThreads, 1)
             if (j + step < pc.nt) {
               wait(sm.full[k.st], k.ph);
               if (!ok) break;
-              if (one) {
+              if (elect_one()) {
                 const uint64_t d = dk + ((k.st * Sh::kStage) >> 4);
 #pragma unroll
                 for (int x = 0; x < D / 16; ++x)
@@ -866,7 +872,7 @@ __global__ void __launch_bounds__(kTtThreads, 1)
         qph ^= 1;
         n0 += 2 * pc.nt;
       }
-      if (one) tc5::mma_commit(smem_u32(&sm.done[slot]));
+      if (elect_one()) tc5::mma_commit(smem_u32(&sm.done[slot]));
       tc5::mbar_wait_drain(smem_u32(&sm.done[slot]), 0);
       __syncwarp();
     } else {
