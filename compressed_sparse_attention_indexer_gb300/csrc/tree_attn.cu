@@ -90,7 +90,7 @@ struct TtShape {
   static constexpr int kRoom = (227 * 1024 - (int)sizeof(TtSmem) - kQBytes - kRawDepth * kRaw - kScales) / kStage;
   static constexpr int kStages = kRoom > 8 ? 8 : kRoom;
   static constexpr int kSmem = kQBytes + kStages * kStage + kRawDepth * kRaw + kScales + (int)sizeof(TtSmem);
-  static_assert(kStages >= 3, "ring");
+  static_assert(kStages >= (kRows == 128 ? 4 : 3), "a batch holds its K beside two tiles' V");
   // a tile's scales stay until its weights are made: its V then waits in the ring, so
   // that the tile being written is at most kStages / 2 + 1 tiles ahead
   static_assert(kStages / 2 + 1 < kScaleTiles, "scales");
@@ -189,44 +189,38 @@ __device__ __forceinline__ void setmaxnreg_dec() {
   asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;\n" ::"n"(N));
 }
 
-// The places in the pool of kN segments of `seg` rows of a tile (each within a page), looked
-// up ahead of their use.
-template <int kN>
-struct Places {
-  int entry[kN], within[kN];
-  int first, last;                         // the span's rows among the tile's, [first, last)
-  __device__ __forceinline__ void lookup(const PagedArgs& a, const Cursor<kTile, true>& c, int at, int seg, int n) {
-    const int base = (c.sp.t0 + c.tile) * kTile;
-    first = max(c.sp.lo - base, 0);
-    last = min(c.sp.L - base, kTile);
-#pragma unroll
-    for (int i = 0; i < kN; ++i) {
-      const int r = (at + i) * seg;
-      within[i] = entry[i] = -1;
-      if (i < n && r < last && r + seg > first) {
-        if (a.table) {
-          const int k = (int)((uint32_t)(base + r) / (uint32_t)a.block);
-          within[i] = base + r - k * a.block;
-          if (k < a.table_stride) entry[i] = a.table[(int64_t)c.b * a.table_stride + k];
-        } else {
-          within[i] = 0;
-          // rows outside the pool may be a part of the segment: its start is kept near the pool
-          const int64_t x = a.off[c.b] + base + r;
-          entry[i] = (int)(x < -kTile ? -kTile : x > a.rows ? a.rows : x);
-        }
-      }
+// The place in the pool of `seg` rows of a tile, rows r .. of it, which lie in one page:
+// looked up ahead of its use.
+struct Spot {
+  int entry, within;
+  int first, last;                         // the span's rows among the segment's, [first, last)
+  __device__ __forceinline__ void none() { within = -1; }
+  __device__ __forceinline__ void lookup(const PagedArgs& a, const Span<kTile, true>& sp, int b, int tile, int r, int seg) {
+    const int at = (sp.t0 + tile) * kTile + r;
+    first = max(sp.lo - at, 0);
+    last = min(sp.L - at, seg);
+    within = entry = -1;
+    if (first >= last) return;
+    if (a.table) {
+      const int k = (int)((uint32_t)at / (uint32_t)a.block);
+      within = at - k * a.block;
+      if (k < a.table_stride) entry = a.table[(int64_t)b * a.table_stride + k];
+    } else {
+      within = 0;
+      // rows outside the pool may be a part of the segment: its start is kept near the pool
+      const int64_t x = a.off[b] + at;
+      entry = (int)(x < -kTile ? -kTile : x > a.rows ? a.rows : x);
     }
   }
-  // Pool row of segment i, `none` where it has no row to read; false when some of its rows
-  // in the span are unmapped or outside the pool.
-  __device__ __forceinline__ bool resolve(const PagedArgs& a, int i, int at, int seg, int none, int& row) const {
+  // Its pool row, `none` where it has no row to read; false when some of its rows in the
+  // span are unmapped or outside the pool.
+  __device__ __forceinline__ bool resolve(const PagedArgs& a, int none, int& row) const {
     row = none;
-    if (within[i] < 0) return true;
-    if (a.table && entry[i] < 0) return false;
-    const int64_t x = a.table ? (int64_t)entry[i] * a.block + within[i] : entry[i];
-    const int r = (at + i) * seg;
+    if (within < 0) return true;
+    if (a.table && entry < 0) return false;
+    const int64_t x = a.table ? (int64_t)entry * a.block + within : entry;
     if (x < a.rows) row = (int)x;
-    return x + max(first - r, 0) >= 0 && x + min(last - r, seg) <= a.rows;
+    return x + first >= 0 && x + last <= a.rows;
   }
 };
 
@@ -586,18 +580,18 @@ __global__ void __launch_bounds__(kTtThreads, 1)
         // the lane's row of the tile: its scales are fetched a tile ahead, its place two
         Cursor<kTile, true> at = cu;
         int left = steps;
-        Places<1> rows;
+        Spot spot;
         float ks = 0.f, vs = 0.f;
         auto ahead = [&] {                     // `at` to the next tile with rows, its place looked up
           while (left > 0 && at.sp.L <= 0) {
             if (--left > 0) at.next(a, units);
           }
-          rows.within[0] = -1;
-          if (left > 0) rows.lookup(a, at, w * 32 + lane, 1, 1);
+          spot.none();
+          if (left > 0) spot.lookup(a, at.sp, at.b, at.tile, w * 32 + lane, 1);
         };
         auto fetch = [&] {
           int row;
-          if (!rows.resolve(a, 0, w * 32 + lane, 1, -1, row)) row = -1;
+          if (!spot.resolve(a, -1, row)) row = -1;
           const int h = chunks == 1 ? at.unit : at.unit / chunks;
           ks = vs = 0.f;
           if (row >= 0) ks = a.k_scale[(int64_t)row * a.scale_stride + h], vs = a.v_scale[(int64_t)row * a.scale_stride + h];
@@ -718,61 +712,83 @@ __global__ void __launch_bounds__(kTtThreads, 1)
       }
     } else if (warp == kLoadWarp) {
       // ---------------------------------------------------------- row loader
-      // lane: `per` segments of the tile from per * lane on, looked up one tile ahead
-      const int steps = (int)(sm.cut[1].at - sm.cut[0].at);
-      Cursor<kTile, true> ld;
-      ld.b = sm.cut[0].b;
-      ld.sp.set(a, ld.b);
-      ld.unit = sm.cut[0].unit;
-      ld.tile = sm.cut[0].tile;
+      // Segments of several tiles are looked up at once, a lane each (four at most, where
+      // a tile has more than 32), and a block of tiles ahead of their copies: looked up
+      // tile by tile, the table's latency was on everyone's way (4000 cycles a tile).
+      const int segs = kTile / seg, per = (segs + 31) / 32, ahead = per > 1 ? 1 : 32 / segs;   // tiles of a block
+      const int none = a.rows > 0 ? (int)a.rows : 1;   // a row behind the pool reads as zeros
       if (lane == 0) {
         tc5::prefetch_tmap(&kmap);
         tc5::prefetch_tmap(&vmap);
       }
-      const int segs = kTile / seg, per = (segs + 31) / 32, mine = lane * per < segs ? per : 0, none = a.rows > 0 ? (int)a.rows : 1;
-      Places<4> rows;
-      uint32_t n = 0;
-      bool ok = true;
-      rows.lookup(a, ld, per * lane, seg, mine);
-      for (int step = 0; ok && step < steps; ++step) {
-        if (ld.sp.L > 0) {
-          int row[4];                            // a row behind the pool reads as zeros
-          bool all = true;
-#pragma unroll
-          for (int i = 0; i < 4; ++i) all &= rows.resolve(a, i, per * lane, seg, none, row[i]);
-          if (!all && a.status) set_status(a.status, kStatusBadIndex);
-          const int h = chunks == 1 ? ld.unit : ld.unit / chunks;
-#pragma unroll 1
-          for (int kv = 0; kv < 2; ++kv, ++n) {
-            const uint32_t st = n % ST, slot = n % Sh::kRawDepth;
-            uint64_t* bar;
-            if (kFp8) {
-              if (n >= (uint32_t)Sh::kRawDepth) ok = warp_wait(sm.raw_empty[slot], (n / Sh::kRawDepth - 1) & 1, abort);
-              bar = &sm.raw_full[slot];
-            } else {
-              if (n >= ST) ok = warp_wait(sm.empty[st], (n / ST - 1) & 1, abort);
-              bar = kv && edge_tile(a, ld.sp, ld.tile) ? &sm.land[st] : &sm.full[st];
-            }
-            if (!ok) break;
-            if (lane == 0) tc5::mbar_expect_tx(smem_u32(bar), kFp8 ? Sh::kRaw : Sh::kStage);
-            __syncwarp();
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              if (i >= mine) continue;
-              const uint32_t to = (kFp8 ? raw + slot * Sh::kRaw : ring + st * Sh::kStage) + (per * lane + i) * seg * 128;
-#pragma unroll
-              for (int x = 0; x < (kFp8 ? 1 : Sh::kSubs); ++x)
-                tc5::tma_load_2d(to + x * kSub, kv ? &vmap : &kmap, h * D + 64 * x, row[i], smem_u32(bar));
-            }
-          }
+      Walk walk;
+      walk.init(a, sm.cut);
+      Piece next;                              // the block looked up: the first tiles of what is left of a piece
+      bool more = false;
+      Spot spot[4];
+      auto look = [&] {
+        while ((more = walk.next(a, units, next)) && next.sp.L <= 0) {
         }
-        if (step + 1 < steps) {
-          ld.next(a, units);
-          rows.lookup(a, ld, per * lane, seg, mine);
+      };
+      auto lookup = [&] {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          spot[i].none();
+          const int x = lane * per + i;         // segment of the block
+          if (i < per && more && x < segs * min(ahead, next.nt))
+            spot[i].lookup(a, next.sp, next.b, next.tile + x / segs, x % segs * seg, seg);
+        }
+      };
+      uint32_t n = 0, st = 0, ph = 1;          // chunks; place in the ring, its phase before
+      constexpr uint32_t kInFlight = kFp8 ? Sh::kRawDepth : ST;
+      bool ok = true;
+      look();
+      lookup();
+      while (ok && more) {
+        const Piece now = next;
+        const int nt = min(ahead, now.nt), h = chunks == 1 ? now.unit : now.unit / chunks;
+        int row[4];
+        bool all = true;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) all &= spot[i].resolve(a, none, row[i]);
+        if (!all && a.status) set_status(a.status, kStatusBadIndex);
+        next.tile += nt;
+        next.nt -= nt;
+        if (next.nt == 0) look();
+        lookup();
+#pragma unroll 1
+        for (int t = 0; ok && t < nt; ++t) {
+          const bool edge = !kFp8 && edge_tile(a, now.sp, now.tile + t);
+#pragma unroll 1
+          for (int kv = 0; kv < 2; ++kv) {
+            if (n >= kInFlight) ok = warp_wait(kFp8 ? sm.raw_empty[st] : sm.empty[st], ph, abort);
+            if (!ok) break;
+            const uint32_t bar = smem_u32(kFp8 ? &sm.raw_full[st] : kv && edge ? &sm.land[st] : &sm.full[st]);
+            const uint32_t to = kFp8 ? raw + st * Sh::kRaw : ring + st * Sh::kStage;
+            const CUtensorMap* map = kv ? &vmap : &kmap;
+            if (lane == 0) tc5::mbar_expect_tx(bar, kFp8 ? Sh::kRaw : Sh::kStage);
+            __syncwarp();
+            constexpr int kCopies = kFp8 ? 1 : Sh::kSubs;   // of a segment
+            if (per == 1) {
+#pragma unroll 1
+              for (int x0 = 0; x0 < segs * kCopies; x0 += 32) {
+                const int x = x0 + lane, s = x / kCopies, c = x % kCopies;
+                const int r = __shfl_sync(0xffffffffu, row[0], (t * segs + s) & 31);
+                if (x < segs * kCopies) tc5::tma_load_2d(to + s * seg * 128 + c * kSub, map, h * D + 64 * c, r, bar);
+              }
+            } else {
+#pragma unroll
+              for (int i = 0; i < 4; ++i)
+#pragma unroll
+                for (int c = 0; c < kCopies; ++c)
+                  if (i < per) tc5::tma_load_2d(to + (lane * per + i) * seg * 128 + c * kSub, map, h * D + 64 * c, row[i], bar);
+            }
+            ++n;
+            if (++st == kInFlight) st = 0, ph ^= 1;
+          }
         }
       }
       // the copies in flight land before the block ends (they have, unless a wait gave up)
-      constexpr uint32_t kInFlight = kFp8 ? Sh::kRawDepth : ST;
       for (uint32_t m = n > kInFlight ? n - kInFlight : 0; m < n; ++m)
         if (!tc5::mbar_wait_drain(smem_u32(kFp8 ? &sm.raw_full[m % kInFlight] : &sm.full[m % kInFlight]), (m / kInFlight) & 1)) break;
     } else if (warp == kMmaWarp || warp == kMmaWarp2) {
@@ -834,28 +850,26 @@ __global__ void __launch_bounds__(kTtThreads, 1)
           k.set(n0 + (kPair ? 2 * slot : 0));
           v.set(n0 + (kPair ? 2 * slot : 0) + 1);
           wait(sm.q_full, qph);
-          // tile j's scores, then with its weights the output, and the next tile's scores
+          // a batch: with tile j's weights the output, then the scores of the slot's next
+          // tile, 16 MMAs without anything between them
           const int first = kPair ? slot : 0, step = kPair ? 2 : 1;
 #pragma unroll 1
           for (int j = first - step; j < pc.nt; j += step) {
-            if (j >= first) {
+            const bool out = j >= first, in = j + step < pc.nt;
+            if (in) wait(sm.full[k.st], k.ph);
+            if (out) {
               wait(sm.full[v.st], v.ph);
               wait(sm.p_full[slot], pph);
               pph ^= 1;
-              if (!ok) break;
-              if (elect_one()) {
+            }
+            if (!ok) break;
+            if (elect_one()) {
+              if (out) {
                 const uint64_t d = dv + ((v.st * Sh::kStage) >> 4);
 #pragma unroll
                 for (int x = 0; x < kTile / 16; ++x) tc5::mma_bf16_ta(o_at, s_at + 8 * x, d + ((x * 2048) >> 4), idesc_o, 1u);
-                tc5::mma_commit(smem_u32(&sm.empty[v.st]));
-                if (j + step >= pc.nt) tc5::mma_commit(smem_u32(&sm.o_full[slot]));
               }
-              v.move(kStep);
-            }
-            if (j + step < pc.nt) {
-              wait(sm.full[k.st], k.ph);
-              if (!ok) break;
-              if (elect_one()) {
+              if (in) {
                 const uint64_t d = dk + ((k.st * Sh::kStage) >> 4);
 #pragma unroll
                 for (int x = 0; x < D / 16; ++x)
@@ -864,9 +878,13 @@ __global__ void __launch_bounds__(kTtThreads, 1)
                 tc5::mma_commit(smem_u32(&sm.s_full[slot]));
                 tc5::mma_commit(smem_u32(&sm.empty[k.st]));
                 if (j + 2 * step >= pc.nt) tc5::mma_commit(smem_u32(&sm.q_empty));
+              } else {
+                tc5::mma_commit(smem_u32(&sm.o_full[slot]));
               }
-              k.move(kStep);
+              if (out) tc5::mma_commit(smem_u32(&sm.empty[v.st]));
             }
+            if (in) k.move(kStep);
+            if (out) v.move(kStep);
           }
         }
         qph ^= 1;
