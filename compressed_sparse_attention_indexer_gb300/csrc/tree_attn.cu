@@ -906,13 +906,19 @@ __global__ void __launch_bounds__(kTtThreads, 1)
         if (n_q > 0) ok = warp_wait(sm.q_empty, (n_q - 1) & 1, abort);
         if (!ok) break;
         const __nv_bfloat16* q0 = static_cast<const __nv_bfloat16*>(a.q) + (int64_t)pc.b * a.S * a.q_stride;
-#pragma unroll 8
-        for (int x = lane; x < kRows * (D / 8); x += 32) {
-          const int r = x / (D / 8), c = x % (D / 8), i = row0 + r;
-          const int s = i < qrows ? token_of(i) : 0;
-          const __nv_bfloat16* src = q0 + (int64_t)s * a.q_stride + (h * group + i - s * group) * D + c * 8;
-          const uint32_t dst = qsm + (r >> 7) * Sh::kStage + (c >> 3) * kSub + (r & 127) * 128 + (((c & 7) ^ (r & 7)) << 4);
-          cp_async16(dst, i < qrows ? src : q0, i < qrows ? 16 : 0);
+        // a lane copies one 16-byte column of every kAt-th row; token and head are counted up
+        constexpr int kAt = 32 / (D / 8);
+        const int c = lane % (D / 8);
+        int r = lane / (D / 8), s = token_of(row0 + r), g = row0 + r - s * group;
+        uint32_t dst = qsm + (c >> 3) * kSub + r * 128;
+#pragma unroll 4
+        for (; r < kRows; r += kAt, dst += kAt * 128) {
+          if (r == 128 + lane / (D / 8)) dst += Sh::kStage - kSub;   // the second slot's rows
+          const bool in = row0 + r < qrows;
+          const __nv_bfloat16* src = q0 + (int64_t)(in ? s : 0) * a.q_stride + ((in ? h * group + g : 0) * D + c * 8);
+          cp_async16(dst + (((c & 7) ^ (r & 7)) << 4), src, in ? 16 : 0);
+          g += kAt;
+          while (g >= group) g -= group, ++s;
         }
         cp_async_commit();
         cp_async_wait<0>();

@@ -210,6 +210,17 @@ def test_long_requests_are_split_and_joined(lens, s, h, hk, d, fp8):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("s,h,hk,d,fp8", [(16, 16, 2, 128, False), (33, 2, 2, 64, False), (40, 4, 2, 128, True), (64, 8, 2, 128, False),
+                                          (21, 28, 4, 128, True), (37, 14, 2, 64, False)])
+@pytest.mark.parametrize("block", [64, 24, 2])
+def test_many_tiles_per_block_of_threads(s, h, hk, d, fp8, block):
+    # every CTA takes several tiles of one request after another, and several requests
+    _gpu()
+    lens = [2200 - 61 * i for i in range(30)] + [130] * 10
+    _run(lens, s, h, hk, d, block, fp8=fp8, seed=s, counts=[s if i % 3 else max(1, s // 2) for i in range(40)])
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("s,h,hk,d,fp8", SHAPES)
 def test_masks_that_leave_rows_empty_or_full(s, h, hk, d, fp8):
     # no bits, every bit (those of drafts behind the count too), and only another draft's
