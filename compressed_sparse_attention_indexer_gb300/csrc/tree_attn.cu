@@ -176,6 +176,29 @@ __device__ __forceinline__ bool elect_one() {
   return p != 0;
 }
 
+// Two fp32 operations in one instruction.
+__device__ __forceinline__ uint64_t f2(float lo, float hi) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};\n" : "=l"(r) : "f"(lo), "f"(hi));
+  return r;
+}
+__device__ __forceinline__ void f2_out(uint64_t v, float& lo, float& hi) { asm("mov.b64 {%0, %1}, %2;\n" : "=f"(lo), "=f"(hi) : "l"(v)); }
+__device__ __forceinline__ uint64_t f2_mul(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("mul.rn.f32x2 %0, %1, %2;\n" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ uint64_t f2_add(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;\n" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ uint64_t f2_fma(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;\n" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+
 // A wait that a whole warp makes: true when every lane saw the phase.
 __device__ __forceinline__ bool warp_wait(uint64_t& bar, uint32_t parity, volatile int* abort) {
   return __all_sync(0xffffffffu, tc5::mbar_wait_backoff(smem_u32(&bar), parity, abort, 64));
@@ -389,17 +412,17 @@ __global__ void __launch_bounds__(kTtThreads, 1)
           float x[128];
           tc5::tmem_ld32x2(s_at, x, x + 32);
           tc5::tmem_ld32x2(s_at + 64, x + 64, x + 96);
-          uint32_t sc = 0;
+          const float4* sc = nullptr;            // the tile's scales: K's, then V's
           if (kFp8) {
             const int at = jj + j;
             ok = warp_wait(sm.sc_full[at % kScaleTiles], (at / kScaleTiles) & 1, abort);
             if (!ok) break;
-            sc = scales + (at % kScaleTiles) * kScaleBytes;
+            sc = reinterpret_cast<const float4*>(smem_raw + (scales - qsm) + (at % kScaleTiles) * kScaleBytes);
 #pragma unroll
             for (int c = 0; c < 128; c += 4) {
-              float4 k;
-              asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];\n" : "=f"(k.x), "=f"(k.y), "=f"(k.z), "=f"(k.w) : "r"(sc + c * 4));
-              x[c] *= k.x, x[c + 1] *= k.y, x[c + 2] *= k.z, x[c + 3] *= k.w;
+              const float4 k = sc[c / 4];
+              f2_out(f2_mul(f2(x[c], x[c + 1]), f2(k.x, k.y)), x[c], x[c + 1]);
+              f2_out(f2_mul(f2(x[c + 2], x[c + 3]), f2(k.z, k.w)), x[c + 2], x[c + 3]);
             }
           }
           uint32_t seen[4];
@@ -430,29 +453,33 @@ __global__ void __launch_bounds__(kTtThreads, 1)
           }
           if (grow) m = most;
           const float ref = m == -INFINITY ? 0.f : m;
-          float sum[4] = {0.f, 0.f, 0.f, 0.f};
+          uint64_t sum[2] = {0, 0};
+          const uint64_t mul2 = f2(mul, mul), ref2 = f2(-ref, -ref);
 #pragma unroll
           for (int half = 0; half < 2; ++half) {
             float pk[32];
 #pragma unroll
             for (int c = 0; c < 64; c += 4) {
               float4 v = make_float4(1.f, 1.f, 1.f, 1.f);
-              if (kFp8)
-                asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];\n" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
-                             : "r"(sc + kTile * 4 + (half * 64 + c) * 4));
-              float p[4];
+              if (kFp8) v = sc[kTile / 4 + half * 16 + c / 4];
 #pragma unroll
-              for (int e = 0; e < 4; ++e) {
-                p[e] = fast_exp2(fmaf(x[half * 64 + c + e], mul, -ref));
-                sum[e] += p[e];
+              for (int e = 0; e < 2; ++e) {
+                float p0, p1;
+                f2_out(f2_fma(f2(x[half * 64 + c + 2 * e], x[half * 64 + c + 2 * e + 1]), mul2, ref2), p0, p1);
+                p0 = fast_exp2(p0), p1 = fast_exp2(p1);
+                uint64_t p = f2(p0, p1);
+                sum[e] = f2_add(sum[e], p);
+                if (kFp8) f2_out(f2_mul(p, e ? f2(v.z, v.w) : f2(v.x, v.y)), p0, p1);
+                pk[c / 2 + e] = __uint_as_float(pack_bf16x2(p0, p1));
               }
-              if (kFp8) p[0] *= v.x, p[1] *= v.y, p[2] *= v.z, p[3] *= v.w;
-              pk[c / 2] = __uint_as_float(pack_bf16x2(p[0], p[1]));
-              pk[c / 2 + 1] = __uint_as_float(pack_bf16x2(p[2], p[3]));
             }
             tc5::tmem_st32(s_at + 32 * half, pk);
           }
-          l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+          {
+            float s0, s1;
+            f2_out(f2_add(sum[0], sum[1]), s0, s1);
+            l += s0 + s1;
+          }
           tc5::tmem_wait_st();
           if (edge) {
             const int n = 2 * (jj + j) + 1;     // V's stage of the ring
@@ -611,35 +638,45 @@ __global__ void __launch_bounds__(kTtThreads, 1)
               if (ok && n >= ST) ok = warp_wait(sm.empty[st], (n / ST - 1) & 1, abort);
               if (!ok) break;
               const uint32_t from = raw + slot * Sh::kRaw + (w * kIter * 32 + lane) * 16;
-#pragma unroll 2
-              for (int i = 0; i < kIter; ++i) {
-                uint32_t c[4], u[8];
-                asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];\n" : "=r"(c[0]), "=r"(c[1]), "=r"(c[2]), "=r"(c[3]) : "r"(from + i * 512) : "memory");
+              // four pieces at a time, so that their loads and conversions overlap
+#pragma unroll 1
+              for (int i0 = 0; i0 < kIter; i0 += 4) {
+                uint32_t c[4][4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                  asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];\n" : "=r"(c[i][0]), "=r"(c[i][1]), "=r"(c[i][2]), "=r"(c[i][3]) : "r"(from + (i0 + i) * 512) : "memory");
                 if (look) {
-                  uint32_t any = 0;
 #pragma unroll
-                  for (int x = 0; x < 4; ++x) any |= ((c[x] & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u;
-                  if (any) {
-                    bad |= 1u << (i * kAtOnce + r0);
+                  for (int i = 0; i < 4; ++i) {
+                    uint32_t any = 0;
 #pragma unroll
-                    for (int x = 0; x < 4; ++x) {
-                      const uint32_t nan = (((c[x] & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u) >> 7;   // 1 in a NaN's byte
-                      c[x] &= ~(nan * 0xffu);
+                    for (int x = 0; x < 4; ++x) any |= ((c[i][x] & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u;
+                    if (any) {
+                      bad |= 1u << ((i0 + i) * kAtOnce + r0);
+#pragma unroll
+                      for (int x = 0; x < 4; ++x) {
+                        const uint32_t nan = (((c[i][x] & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u) >> 7;   // 1 in a NaN's byte
+                        c[i][x] &= ~(nan * 0xffu);
+                      }
                     }
                   }
                 }
 #pragma unroll
-                for (int x = 0; x < 4; ++x) {
-                  uint32_t lo, hi;
-                  e4m3x4_to_f16x2(c[x], lo, hi);
-                  const float2 f0 = __half22float2(*reinterpret_cast<const __half2*>(&lo));
-                  const float2 f1 = __half22float2(*reinterpret_cast<const __half2*>(&hi));
-                  u[2 * x] = pack_bf16x2(f0.x, f0.y);
-                  u[2 * x + 1] = pack_bf16x2(f1.x, f1.y);
+                for (int i = 0; i < 4; ++i) {
+                  uint32_t u[8];
+#pragma unroll
+                  for (int x = 0; x < 4; ++x) {
+                    uint32_t lo, hi;
+                    e4m3x4_to_f16x2(c[i][x], lo, hi);
+                    const float2 f0 = __half22float2(*reinterpret_cast<const __half2*>(&lo));
+                    const float2 f1 = __half22float2(*reinterpret_cast<const __half2*>(&hi));
+                    u[2 * x] = pack_bf16x2(f0.x, f0.y);
+                    u[2 * x + 1] = pack_bf16x2(f1.x, f1.y);
+                  }
+                  const uint32_t to = stage + place(i0 + i);
+                  asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};\n" ::"r"(to), "r"(u[0]), "r"(u[1]), "r"(u[2]), "r"(u[3]) : "memory");
+                  asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};\n" ::"r"(to ^ 16u), "r"(u[4]), "r"(u[5]), "r"(u[6]), "r"(u[7]) : "memory");
                 }
-                const uint32_t to = stage + place(i);
-                asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};\n" ::"r"(to), "r"(u[0]), "r"(u[1]), "r"(u[2]), "r"(u[3]) : "memory");
-                asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};\n" ::"r"(to ^ 16u), "r"(u[4]), "r"(u[5]), "r"(u[6]), "r"(u[7]) : "memory");
               }
               if (kv == 0) {
                 // the row's scales as the scores and weights take them; a V scale that is no
