@@ -673,9 +673,18 @@ __global__ void __launch_bounds__(kTtThreads, 1)
                     u[2 * x] = pack_bf16x2(f0.x, f0.y);
                     u[2 * x + 1] = pack_bf16x2(f1.x, f1.y);
                   }
+                  // (the lanes of a row's second half begin with the other piece: the eight
+                  // lanes of a row then write to eight different places of 16 bytes)
                   const uint32_t to = stage + place(i0 + i);
-                  asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};\n" ::"r"(to), "r"(u[0]), "r"(u[1]), "r"(u[2]), "r"(u[3]) : "memory");
-                  asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};\n" ::"r"(to ^ 16u), "r"(u[4]), "r"(u[5]), "r"(u[6]), "r"(u[7]) : "memory");
+                  const bool swap = ch >= 4;
+                  const uint32_t first = swap ? to ^ 16u : to;
+#pragma unroll
+                  for (int x = 0; x < 4; ++x) {
+                    const uint32_t lo = u[x], hi = u[4 + x];
+                    u[x] = swap ? hi : lo, u[4 + x] = swap ? lo : hi;
+                  }
+                  asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};\n" ::"r"(first), "r"(u[0]), "r"(u[1]), "r"(u[2]), "r"(u[3]) : "memory");
+                  asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};\n" ::"r"(first ^ 16u), "r"(u[4]), "r"(u[5]), "r"(u[6]), "r"(u[7]) : "memory");
                 }
               }
               if (kv == 0) {
@@ -825,7 +834,10 @@ __global__ void __launch_bounds__(kTtThreads, 1)
           }
         }
       }
-      // the copies in flight land before the block ends (they have, unless a wait gave up)
+      // the copies in flight land before the block ends (they have, unless a wait gave up:
+      // then nothing is known of the barriers, and their time is waited for)
+      if (*abort)
+        for (int i = 0; i < 100; ++i) __nanosleep(1000);
       for (uint32_t m = n > kInFlight ? n - kInFlight : 0; m < n; ++m)
         if (!tc5::mbar_wait_drain(smem_u32(kFp8 ? &sm.raw_full[m % kInFlight] : &sm.full[m % kInFlight]), (m / kInFlight) & 1)) break;
     } else if (warp == kMmaWarp || warp == kMmaWarp2) {
@@ -862,6 +874,14 @@ __global__ void __launch_bounds__(kTtThreads, 1)
         }
       };
       constexpr uint32_t kStep = kPair ? 4 : 2;  // from one tile of the slot to its next
+      // Every chunk's phase is seen, in order, the other slot's too: a wait for a stage's
+      // phase while the one before has not come would take the phase two before for it.
+      Place seen;
+      seen.set(0);
+      uint32_t n_seen = 0;
+      auto see = [&](uint32_t n) {             // chunks up to n have landed
+        for (; ok && n_seen <= n; ++n_seen, seen.move(1)) wait(sm.full[seen.st], seen.ph);
+      };
       Walk walk;
       walk.init(a, sm.cut);
       Piece pc;
@@ -871,14 +891,11 @@ __global__ void __launch_bounds__(kTtThreads, 1)
         const bool busy = kPair ? pc.nt > slot : row0 + slot * 128 < qrows;
         if (!busy) {
           // no rows or tiles for this slot: what it would have read is given back
-          if (!kPair) {
-            Place c;
-            c.set(n0);
 #pragma unroll 1
-            for (int i = 0; ok && i < 2 * pc.nt; ++i, c.move(1)) {
-              wait(sm.full[c.st], c.ph);
-              if (ok && elect_one()) tc5::mbar_arrive(smem_u32(&sm.empty[c.st]));
-            }
+          for (int i = 0; ok && i < 2 * pc.nt; ++i) {
+            const uint32_t st = seen.st;
+            see(n0 + i);
+            if (!kPair && ok && elect_one()) tc5::mbar_arrive(smem_u32(&sm.empty[st]));
           }
           wait(sm.q_full, qph);
           if (ok && elect_one()) tc5::mbar_arrive(smem_u32(&sm.q_empty));
@@ -893,9 +910,8 @@ __global__ void __launch_bounds__(kTtThreads, 1)
 #pragma unroll 1
           for (int j = first - step; j < pc.nt; j += step) {
             const bool out = j >= first, in = j + step < pc.nt;
-            if (in) wait(sm.full[k.st], k.ph);
+            see(in ? n0 + 2 * (j + step) : n0 + 2 * j + 1);   // (K of the next tile comes after V of this one)
             if (out) {
-              wait(sm.full[v.st], v.ph);
               wait(sm.p_full[slot], pph);
               pph ^= 1;
             }
@@ -923,6 +939,7 @@ __global__ void __launch_bounds__(kTtThreads, 1)
             if (in) k.move(kStep);
             if (out) v.move(kStep);
           }
+          see(n0 + 2 * pc.nt - 1);
         }
         qph ^= 1;
         n0 += 2 * pc.nt;
