@@ -17,7 +17,7 @@
 // power of two up to a warp) hold a head as pairs of 8-element units, the two
 // units that a rotation by halves pairs with one another in one lane, so that
 // the rotation needs no exchange (kPaired); regions that do not fall on whole
-// units take the partner's elements from memory a second time.
+// units exchange their elements through shared memory.
 #include "csa_internal.cuh"
 #include "ptx.cuh"
 #include "rows.cuh"
@@ -28,9 +28,17 @@ namespace {
 
 constexpr int kThreads = 128;
 constexpr int kUnit = 8;              // elements a lane loads together
+constexpr int kJobs = 8;              // heads per lane of a block, where there are enough
 
 struct Turns {
   uint64_t t[kRopeMaxDim / 2];        // theta_i / (2 pi) in units of 2^-64 turns
+};
+
+// How the blocks share the work: kind k's start at block start[k]; a block has tb[k] tokens
+// and per[k] of their heads, one of splits[k] parts.
+struct Plan {
+  int start[4];
+  int tb[3], splits[3], per[3];
 };
 
 // theta / (2 pi) as a fraction of 2^-64 turns.
@@ -38,6 +46,19 @@ __device__ __forceinline__ uint64_t turn_of(float theta) {
   double t = (double)theta * 0.15915494309189535;
   t -= rint(t);
   return (uint64_t)(int64_t)(t * 18446744073709551616.0);
+}
+
+// Cosine and sine of phase 2^-32 turns: the quarter turn nearest, and the rest of at most an
+// eighth (|x| <= pi / 4) by the Taylor series of either, cut off below 1e-9.
+__device__ __forceinline__ void cos_sin(uint32_t phase, float& cn, float& sn) {
+  const uint32_t quarter = (phase + 0x20000000u) >> 30;
+  const float x = (float)(int)(phase - (quarter << 30)) * 1.4629180792671596e-9f;   // 2 pi / 2^32
+  const float y = x * x;
+  const float s = fmaf(x * y, fmaf(y, fmaf(y, fmaf(y, 1.f / 362880.f, -1.f / 5040.f), 1.f / 120.f), -1.f / 6.f), x);
+  const float c = fmaf(y, fmaf(y, fmaf(y, fmaf(y, fmaf(y, -1.f / 3628800.f, 1.f / 40320.f), -1.f / 720.f), 1.f / 24.f), -0.5f), 1.f);
+  const float a = quarter & 1 ? s : c, b = quarter & 1 ? c : s;
+  cn = __uint_as_float(__float_as_uint(a) ^ ((quarter + 1) & 2) << 30);
+  sn = __uint_as_float(__float_as_uint(b) ^ (quarter & 2) << 30);
 }
 
 template <typename T>
@@ -58,22 +79,42 @@ struct Unit {
   }
 };
 
-__device__ __forceinline__ float to_f32(float v) { return v; }
-__device__ __forceinline__ float to_f32(__nv_bfloat16 v) { return __bfloat162float(v); }
+// Two fp32 products in one instruction.
+__device__ __forceinline__ void mul2(float* d, float b0, float b1) {
+  asm("{\n .reg .b64 x, y;\n mov.b64 x, {%0, %1};\n mov.b64 y, {%2, %3};\n mul.rn.f32x2 x, x, y;\n mov.b64 {%0, %1}, x;\n}\n"
+      : "+f"(d[0]), "+f"(d[1])
+      : "f"(b0), "f"(b1));
+}
+__device__ __forceinline__ void fma2(float* d, const float* a, const float* b) {   // d += a b
+  asm("{\n .reg .b64 x, y, z;\n mov.b64 x, {%0, %1};\n mov.b64 y, {%2, %3};\n mov.b64 z, {%4, %5};\n fma.rn.f32x2 x, y, z, x;\n"
+      " mov.b64 {%0, %1}, x;\n}\n"
+      : "+f"(d[0]), "+f"(d[1])
+      : "f"(a[0]), "f"(a[1]), "f"(b[0]), "f"(b[1]));
+}
 
-// kTasks pairs of units per lane.  Tokens blockIdx.x * tb .. + tb - 1, their
-// heads in order (queries, keys, values), nsub heads at a time.
+// A block does heads of one kind (queries, keys or values) of some tokens (see Plan),
+// nsub heads at a time, kTasks pairs of units per lane.  The kind is the block's, so
+// that its norm, rotation and destination are branches of the whole block and the weight
+// stays in registers.  (All kinds in one block, one after the other: 64 x 65 heads of
+// 576 dims in 13 us instead of 5.)
 template <typename T, int kTasks, bool kPaired, bool kFp8>
 __global__ void __launch_bounds__(kThreads)
-    heads_kernel(const HeadArgs a, const __grid_constant__ Turns turns, int lanes, int tb) {
-  extern __shared__ float2 cs_sh[];                 // [tb][R / 2] (cos, sin)
+    heads_kernel(const HeadArgs a, const __grid_constant__ Turns turns, const __grid_constant__ Plan plan, int lanes) {
+  extern __shared__ float4 cs_sh[];                 // cosines and sines, see place_of
   __shared__ int64_t row_sh[kThreads];              // pool row; -1: padding, -2: no such row
   __shared__ int pos_sh[kThreads];
+  __shared__ uint64_t turn_sh[kRopeMaxDim / 2];
   const int tid = threadIdx.x, sub = tid / lanes, nsub = kThreads / lanes, lane = tid % lanes;
-  const int H = a.heads[0] + a.heads[1] + a.heads[2], half = a.R / 2;
-  const int64_t first = (int64_t)blockIdx.x * tb;
+  const int half = a.R / 2;
+  const int kind = (int)blockIdx.x >= plan.start[2] ? 2 : (int)blockIdx.x >= plan.start[1] ? 1 : 0;
+  const int tb = plan.tb[kind], splits = plan.splits[kind], block = blockIdx.x - plan.start[kind];
+  const int64_t first = (int64_t)(block / splits) * tb;
+  const int head0 = block % splits * plan.per[kind];
+  const int heads = min(plan.per[kind], a.heads[kind] - head0);
+  if (heads <= 0) return;                           // the last split may be empty
   const int here = a.n - first < tb ? (int)(a.n - first) : tb;   // tokens of this block
   const int units = a.dim / kUnit, turned = kPaired ? a.R / (2 * kUnit) : 0, start = a.at / kUnit;
+  const bool norm = a.norm && kind != 2, rotate = half > 0 && kind != 2, quantised = kFp8 && kind != 0;
   pdl_wait();
   pdl_trigger();
 
@@ -92,31 +133,40 @@ __global__ void __launch_bounds__(kThreads)
       }
     }
   }
-  // job: token `tok` of the block, head h of its H
-  auto kind_of = [&](int h) { return h < a.heads[0] ? 0 : h < a.heads[0] + a.heads[1] ? 1 : 2; };
-  auto head_in = [&](int h, int kind) { return kind == 0 ? h : kind == 1 ? h - a.heads[0] : h - a.heads[0] - a.heads[1]; };
-  auto source = [&](int tok, int h) {
-    const int kind = kind_of(h);
-    return static_cast<const T*>(a.src[kind]) + (first + tok) * a.src_stride[kind] + head_in(h, kind) * a.dim;
-  };
+  // job: token `tok` of the block, head h of its heads
+  const T* src0 = static_cast<const T*>(a.src[kind]) + first * a.src_stride[kind] + head0 * a.dim;
+  const int64_t src_stride = a.src_stride[kind];
   Unit<T> next[kTasks][2];
   auto fetch = [&](int tok, int h) {
     if (tok >= here) return;
-    const T* src = source(tok, h);
+    const T* src = src0 + tok * src_stride + h * a.dim;
 #pragma unroll
     for (int i = 0; i < kTasks; ++i)
 #pragma unroll
       for (int e = 0; e < 2; ++e)
         if (ua[i][e] >= 0) next[i][e].load(src + ua[i][e] * kUnit);
   };
-  auto advance = [&](int& tok, int& h) {
-    h += nsub;
-    while (h >= H) h -= H, ++tok;
-  };
-  int tok = 0, h = sub;
-  while (h >= H) h -= H, ++tok;
+  const int dtok = nsub / heads, dh = nsub - dtok * heads;
+  int tok = sub / heads, h = sub - tok * heads;
   fetch(tok, h);
+  const T* weight = norm ? static_cast<const T*>(a.weight[kind]) : nullptr;
+  float w[kTasks][2][kUnit];
+#pragma unroll
+  for (int i = 0; i < kTasks; ++i)
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+#pragma unroll
+      for (int x = 0; x < kUnit; ++x) w[i][e][x] = 1.f;
+      if (weight && ua[i][e] >= 0) {
+        Unit<T> u;
+        u.load(weight + ua[i][e] * kUnit);
+        u.unpack(w[i][e]);
+      }
+    }
 
+  // (lanes of a warp read different ones: not from the launch's constants each time)
+  if (rotate)
+    for (int i = tid; i < half; i += kThreads) turn_sh[i] = a.freq ? turn_of(a.freq[i]) : turns.t[i];
   // ---- where the tokens go and their angles
   for (int x = tid; x < here; x += kThreads) {
     const int64_t t = first + x;
@@ -164,18 +214,39 @@ __global__ void __launch_bounds__(kThreads)
     pos_sh[x] = pos;
   }
   __syncthreads();
-  for (int x = tid; x < here * half; x += kThreads) {
-    const int k = x / half, i = x - k * half;
-    const uint64_t turn = a.freq ? turn_of(a.freq[i]) : turns.t[i];
-    const uint64_t phase = turn * (uint64_t)(int64_t)pos_sh[k];
-    float sn, cn;
-    sincospif((float)(int)(phase >> 32) * 0x1p-31f, &sn, &cn);
-    cs_sh[x] = make_float2(cn, sn);
+  // Cosine and sine of pair i of a token, in fours (cos, cos, sin, sin of two neighbouring
+  // pairs) that the lanes of a head read side by side: 8 pairs of a lane's two units by
+  // halves, 4 of either unit else.
+  float* cs = reinterpret_cast<float*>(cs_sh);
+  const int wide = a.halves ? turned : 2 * turned;   // lanes or units
+  auto place_of = [&](int i) {
+    if (!kPaired) return 2 * i;
+    const int p = a.halves ? i / kUnit : i / (kUnit / 2), x = a.halves ? i % kUnit : i % (kUnit / 2);
+    return ((x >> 1) * wide + p) * 4 + (x & 1);
+  };
+  if (rotate) {
+    int k = tid / half, i = tid - k * half;
+    const int dk = kThreads / half, di = kThreads - dk * half;
+    for (; k < here; k += dk, i += di) {
+      if (i >= half) {
+        i -= half;
+        if (++k >= here) break;
+      }
+      // the upper half of turn * pos modulo 2^64
+      const uint64_t turn = turn_sh[i];
+      const uint32_t lo = (uint32_t)turn, pos = (uint32_t)pos_sh[k];
+      const uint32_t phase = __umulhi(lo, pos) + (uint32_t)(turn >> 32) * pos - ((int)pos < 0 ? lo : 0u);
+      float sn, cn;
+      cos_sin(phase, cn, sn);
+      float* to = cs + k * a.R + place_of(i);
+      to[0] = cn;
+      to[kPaired ? 2 : 1] = sn;
+    }
+    __syncthreads();
   }
-  __syncthreads();
 
   const float inv_dim = 1.f / (float)a.dim;
-  const int steps = (here * H + nsub - 1) / nsub;   // the same for every thread (shuffles inside)
+  const int steps = (here * heads + nsub - 1) / nsub;   // the same for every thread (shuffles inside)
   for (int step = 0; step < steps; ++step) {
     const bool in = tok < here;
     float f[kTasks][2][kUnit];
@@ -191,68 +262,48 @@ __global__ void __launch_bounds__(kThreads)
         }
       }
     const int tok0 = tok, h0 = h;
-    advance(tok, h);
+    tok += dtok;
+    h += dh;
+    if (h >= heads) h -= heads, ++tok;
     fetch(tok, h);
-    const int kind = kind_of(h0), head = head_in(h0, kind);
     const int64_t row = in ? row_sh[tok0] : -1;
-    float r = 1.f;
-    if (a.norm) {
-      float sum = 0.f;
+    if (norm) {
+      float sum[2] = {0.f, 0.f};
 #pragma unroll
       for (int i = 0; i < kTasks; ++i)
 #pragma unroll
         for (int e = 0; e < 2; ++e)
 #pragma unroll
-          for (int x = 0; x < kUnit; ++x) sum = fmaf(f[i][e][x], f[i][e][x], sum);
-      for (int o = lanes / 2; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-      r = rsqrtf(fmaf(sum, inv_dim, a.eps));
+          for (int x = 0; x < kUnit; x += 2) fma2(sum, f[i][e] + x, f[i][e] + x);
+      float all = sum[0] + sum[1];
+      for (int o = lanes / 2; o > 0; o >>= 1) all += __shfl_xor_sync(0xffffffffu, all, o);
+      const float r = rsqrtf(fmaf(all, inv_dim, a.eps));
+#pragma unroll
+      for (int i = 0; i < kTasks; ++i)
+#pragma unroll
+        for (int e = 0; e < 2; ++e)
+#pragma unroll
+          for (int x = 0; x < kUnit; x += 2) {
+            float rw[2] = {r, r};
+            mul2(rw, w[i][e][x], w[i][e][x + 1]);
+            mul2(f[i][e] + x, rw[0], rw[1]);
+          }
     }
-    if (in && kind != 2) {
-      const T* weight = static_cast<const T*>(a.weight[kind]);
-      if (a.norm) {
+    if constexpr (!kPaired) {
+      // pairs that do not fall on whole units: the partner's element through shared memory
+      if (rotate) {
+        float* y = cs + tb * a.R + sub * a.R;
+        const float* c = cs + tok0 * a.R;
 #pragma unroll
         for (int i = 0; i < kTasks; ++i)
 #pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            if (ua[i][e] < 0) continue;
-            float w[kUnit];
-            if (weight) {
-              Unit<T> u;
-              u.load(weight + ua[i][e] * kUnit);
-              u.unpack(w);
-            }
-#pragma unroll
-            for (int x = 0; x < kUnit; ++x) f[i][e][x] *= weight ? r * w[x] : r;
-          }
-      }
-      const float2* cs = cs_sh + tok0 * half;
-      if constexpr (kPaired) {
-#pragma unroll
-        for (int i = 0; i < kTasks; ++i) {
-          const int p = lane + i * lanes;
-          if (p >= turned) continue;
-          if (a.halves) {
+          for (int e = 0; e < 2; ++e)
 #pragma unroll
             for (int x = 0; x < kUnit; ++x) {
-              const float2 c = cs[p * kUnit + x];
-              const float u = f[i][0][x], v = f[i][1][x];
-              f[i][0][x] = u * c.x - v * c.y;
-              f[i][1][x] = u * c.y + v * c.x;
+              const int d = ua[i][e] * kUnit + x - a.at;
+              if (ua[i][e] >= 0 && d >= 0 && d < a.R) y[d] = f[i][e][x];
             }
-          } else {
-#pragma unroll
-            for (int e = 0; e < 2; ++e)
-#pragma unroll
-              for (int x = 0; x < kUnit; x += 2) {
-                const float2 c = cs[((p + e * turned) * kUnit + x) / 2];
-                const float u = f[i][e][x], v = f[i][e][x + 1];
-                f[i][e][x] = u * c.x - v * c.y;
-                f[i][e][x + 1] = u * c.y + v * c.x;
-              }
-          }
-        }
-      } else if (half > 0) {
-        const T* src = source(tok0, h0);
+        __syncwarp();
 #pragma unroll
         for (int i = 0; i < kTasks; ++i)
 #pragma unroll
@@ -260,21 +311,54 @@ __global__ void __launch_bounds__(kThreads)
 #pragma unroll
             for (int x = 0; x < kUnit; ++x) {
               const int d = ua[i][e] * kUnit + x - a.at;       // within the rotated dims
-              if (ua[i][e] < 0 || d < 0 || d >= a.R) continue;
+              if (!in || ua[i][e] < 0 || d < 0 || d >= a.R) continue;
               const bool second = a.halves ? d >= half : d & 1;
               const int k = a.halves ? (second ? d - half : d) : d >> 1;
-              const int other = a.at + (a.halves ? (second ? d - half : d + half) : d ^ 1);
-              float o = to_f32(src[other]);
-              if (a.norm) o *= weight ? r * to_f32(weight[other]) : r;
-              const float2 c = cs[k];
-              f[i][e][x] = second ? fmaf(f[i][e][x], c.x, o * c.y) : fmaf(f[i][e][x], c.x, -(o * c.y));
+              const float o = y[a.halves ? (second ? d - half : d + half) : d ^ 1] * c[2 * k + 1];
+              f[i][e][x] = fmaf(f[i][e][x], c[2 * k], second ? o : -o);
             }
       }
     }
+    if constexpr (kPaired) {
+      if (rotate && in) {
+        const float4* c4 = cs_sh + tok0 * (a.R / 4);
+#pragma unroll
+        for (int i = 0; i < kTasks; ++i) {
+          const int p = lane + i * lanes;
+          if (p >= turned) continue;
+          if (a.halves) {
+#pragma unroll
+            for (int x = 0; x < kUnit; x += 2) {
+              const float4 c = c4[(x >> 1) * wide + p];
+              float* u = f[i][0] + x;
+              float* v = f[i][1] + x;
+              const float cn[2] = {c.x, c.y}, sn[2] = {c.z, c.w}, u0 = u[0], u1 = u[1];
+              u[0] = fmaf(u[0], c.x, -(v[0] * c.z));
+              u[1] = fmaf(u[1], c.y, -(v[1] * c.w));
+              const float was[2] = {u0, u1};
+              mul2(v, cn[0], cn[1]);
+              fma2(v, was, sn);
+            }
+          } else {
+#pragma unroll
+            for (int e = 0; e < 2; ++e)
+#pragma unroll
+              for (int x = 0; x < kUnit; x += 4) {
+                const float4 c = c4[(x >> 2) * wide + p + e * turned];
+                float* u = f[i][e] + x;
+                const float a0 = u[0], a1 = u[2];
+                u[0] = fmaf(u[0], c.x, -(u[1] * c.z));
+                u[1] = fmaf(u[1], c.x, a0 * c.z);
+                u[2] = fmaf(u[2], c.y, -(u[3] * c.w));
+                u[3] = fmaf(u[3], c.y, a1 * c.w);
+              }
+          }
+        }
+      }
+    }
     __syncwarp();   // a head's lanes have read what an output in place overwrites
-    const bool quantised = kFp8 && kind != 0;
     float scale = 1.f;
-    if (kFp8) {
+    if (quantised) {
       float most = 0.f;
 #pragma unroll
       for (int i = 0; i < kTasks; ++i)
@@ -287,33 +371,33 @@ __global__ void __launch_bounds__(kThreads)
     }
     if (row == -1 || (row < 0 && kind != 0)) continue;   // padding; no such row
     const int64_t to = kind == 0 || !a.append ? first + tok0 : row;
-    if (quantised && lane == 0) a.scale[kind - 1][to * a.scale_stride + head] = scale;
+    if (quantised && lane == 0) a.scale[kind - 1][to * a.scale_stride + head0 + h0] = scale;
+    const int64_t at = to * a.dst_stride[kind] + (head0 + h0) * a.dim;
 #pragma unroll
     for (int i = 0; i < kTasks; ++i)
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
         if (ua[i][e] < 0) continue;
-        const int64_t at = to * a.dst_stride[kind] + head * a.dim + ua[i][e] * kUnit;
         if (quantised) {
           divide<kUnit>(f[i][e], scale);
           uint32_t c[kUnit / 2];
 #pragma unroll
           for (int x = 0; x < kUnit / 2; ++x)
             c[x] = __nv_cvt_float2_to_fp8x2(make_float2(f[i][e][2 * x], f[i][e][2 * x + 1]), __NV_SATFINITE, __NV_E4M3);
-          *reinterpret_cast<uint2*>(static_cast<uint8_t*>(a.dst[kind]) + at) = make_uint2(c[0] | c[1] << 16, c[2] | c[3] << 16);
+          *reinterpret_cast<uint2*>(static_cast<uint8_t*>(a.dst[kind]) + at + ua[i][e] * kUnit) = make_uint2(c[0] | c[1] << 16, c[2] | c[3] << 16);
         } else {
-          Unit<T>::store(static_cast<T*>(a.dst[kind]) + at, f[i][e]);
+          Unit<T>::store(static_cast<T*>(a.dst[kind]) + at + ua[i][e] * kUnit, f[i][e]);
         }
       }
   }
 }
 
 template <typename T, int kTasks, bool kPaired>
-int launch_shape(const HeadArgs& a, const Turns& turns, int lanes, int tb, bool fp8, cudaStream_t st, bool pdl) {
-  const int64_t blocks = (a.n + tb - 1) / tb;
-  const size_t smem = (size_t)tb * (a.R / 2) * sizeof(float2);
+int launch_shape(const HeadArgs& a, const Turns& turns, const Plan& plan, int lanes, bool fp8, cudaStream_t st, bool pdl) {
+  const int tb = plan.tb[0] > plan.tb[1] ? plan.tb[0] : plan.tb[1];
+  const size_t smem = (size_t)(tb + (kPaired ? 0 : kThreads / lanes)) * a.R * sizeof(float);
   return launch_kernel(fp8 ? heads_kernel<T, kTasks, kPaired, true> : heads_kernel<T, kTasks, kPaired, false>,
-                       dim3((unsigned)blocks), dim3(kThreads), smem, st, pdl, a, turns, lanes, tb);
+                       dim3((unsigned)plan.start[3]), dim3(kThreads), smem, st, pdl, a, turns, plan, lanes);
 }
 
 }  // namespace
@@ -332,21 +416,40 @@ int launch_heads(const HeadArgs& a, int dtype, bool fp8, double base, int num_sm
   int lanes = 1;
   while (lanes < tasks && lanes < 32) lanes *= 2;
   const int per = (tasks + lanes - 1) / lanes;   // 1, or 2 for heads of more than 64 units
-  const int H = a.heads[0] + a.heads[1] + a.heads[2];
-  // tokens per block: a few heads per lane, fewer where there are not enough tokens for the SMs
-  const int nsub = kThreads / lanes;
-  int64_t tb = (4 * nsub + H - 1) / H;
-  const int64_t spread = (a.n + 4 * num_sms - 1) / (4 * num_sms);
-  if (tb > spread) tb = spread;
-  const int room = a.R > 0 ? 16384 / (a.R / 2 * (int)sizeof(float2)) : kThreads;
-  if (tb > room) tb = room;
-  if (tb > kThreads) tb = kThreads;
-  while ((a.n + tb - 1) / tb > 0x7fffffff) ++tb;
+  const int nsub = kThreads / lanes, kinds = (a.heads[0] > 0) + (a.heads[1] > 0) + (a.heads[2] > 0);
+  const int64_t want = 8 * (int64_t)num_sms;     // blocks at least, if there is work for them
+  Plan plan;
+  int64_t start = 0;
+  for (int k = 0; k < 3; ++k) {
+    plan.start[k] = (int)start;
+    plan.tb[k] = 0;
+    if (a.heads[k] == 0) continue;
+    const int H = a.heads[k], jobs = (H + nsub - 1) / nsub;   // turns of the block per token, at most
+    // some jobs per lane, fewer tokens where there are not enough of them for the SMs, and then
+    // the heads of a token in several blocks
+    int64_t tb = (kJobs * nsub + H - 1) / H;
+    const int64_t spread = (a.n * kinds + want - 1) / want;
+    if (tb > spread) tb = spread;
+    const int room = a.R > 0 && k != 2 ? 16384 / (a.R * (int)sizeof(float)) : kThreads;
+    if (tb > room) tb = room;
+    if (tb > kThreads) tb = kThreads;
+    int64_t splits = tb > 1 ? 1 : want / (a.n * kinds);
+    if (splits > jobs) splits = jobs;            // a job per lane at least
+    if (splits < 1) splits = 1;
+    plan.tb[k] = (int)tb;
+    plan.splits[k] = (int)splits;
+    plan.per[k] = (H + (int)splits - 1) / (int)splits;
+    start += (a.n + tb - 1) / tb * splits;
+    if (start > 0x7fffffff) return launch_fail("too many blocks", cudaErrorInvalidConfiguration);
+  }
+  plan.start[3] = (int)start;
+  if (a.heads[2] == 0) plan.start[2] = plan.start[3];
+  if (a.heads[1] == 0) plan.start[1] = plan.start[2];
 #define CSA_HEADS(T)                                                                                          \
-  (per == 1 ? paired ? launch_shape<T, 1, true>(a, turns, lanes, (int)tb, fp8, st, pdl)                       \
-                     : launch_shape<T, 1, false>(a, turns, lanes, (int)tb, fp8, st, pdl)                      \
-            : paired ? launch_shape<T, 2, true>(a, turns, lanes, (int)tb, fp8, st, pdl)                       \
-                     : launch_shape<T, 2, false>(a, turns, lanes, (int)tb, fp8, st, pdl))
+  (per == 1 ? paired ? launch_shape<T, 1, true>(a, turns, plan, lanes, fp8, st, pdl)                       \
+                     : launch_shape<T, 1, false>(a, turns, plan, lanes, fp8, st, pdl)                      \
+            : paired ? launch_shape<T, 2, true>(a, turns, plan, lanes, fp8, st, pdl)                       \
+                     : launch_shape<T, 2, false>(a, turns, plan, lanes, fp8, st, pdl))
   return dtype == CSA_DTYPE_BF16 ? CSA_HEADS(__nv_bfloat16) : CSA_HEADS(float);
 #undef CSA_HEADS
 }
