@@ -225,22 +225,30 @@ __global__ void __launch_bounds__(kThreads)
     return ((x >> 1) * wide + p) * 4 + (x & 1);
   };
   if (rotate) {
-    int k = tid / half, i = tid - k * half;
-    const int dk = kThreads / half, di = kThreads - dk * half;
-    for (; k < here; k += dk, i += di) {
-      if (i >= half) {
-        i -= half;
-        if (++k >= here) break;
-      }
+    auto angle = [&](uint64_t turn, int k, float* to) {
       // the upper half of turn * pos modulo 2^64
-      const uint64_t turn = turn_sh[i];
       const uint32_t lo = (uint32_t)turn, pos = (uint32_t)pos_sh[k];
       const uint32_t phase = __umulhi(lo, pos) + (uint32_t)(turn >> 32) * pos - ((int)pos < 0 ? lo : 0u);
       float sn, cn;
       cos_sin(phase, cn, sn);
-      float* to = cs + k * a.R + place_of(i);
       to[0] = cn;
       to[kPaired ? 2 : 1] = sn;
+    };
+    int k = tid / half, i = tid - k * half;
+    const int dk = kThreads / half, di = kThreads - dk * half;
+    if (di == 0) {                               // a thread has the same pair of every token
+      const uint64_t turn = turn_sh[i];
+      float* to = cs + k * a.R + place_of(i);
+#pragma unroll 2
+      for (; k < here; k += dk, to += dk * a.R) angle(turn, k, to);
+    } else {
+      for (; k < here; k += dk, i += di) {
+        if (i >= half) {
+          i -= half;
+          if (++k >= here) break;
+        }
+        angle(turn_sh[i], k, cs + k * a.R + place_of(i));
+      }
     }
     __syncthreads();
   }
@@ -379,7 +387,16 @@ __global__ void __launch_bounds__(kThreads)
       for (int e = 0; e < 2; ++e) {
         if (ua[i][e] < 0) continue;
         if (quantised) {
-          divide<kUnit>(f[i][e], scale);
+          // the quotients as divide() forms them, two at a time
+          const float inv = rcp_approx(scale), d = scale < INFINITY ? scale : 0.f, inv2[2] = {inv, inv};
+#pragma unroll
+          for (int x = 0; x < kUnit; x += 2) {
+            float q[2] = {f[i][e][x], f[i][e][x + 1]};
+            mul2(q, inv, inv);
+            const float rest[2] = {fmaf(-q[0], d, f[i][e][x]), fmaf(-q[1], d, f[i][e][x + 1])};
+            fma2(q, rest, inv2);
+            f[i][e][x] = q[0], f[i][e][x + 1] = q[1];
+          }
           uint32_t c[kUnit / 2];
 #pragma unroll
           for (int x = 0; x < kUnit / 2; ++x)
