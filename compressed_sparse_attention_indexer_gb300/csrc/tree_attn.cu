@@ -49,6 +49,7 @@
 #include "paged.cuh"
 #include "ptx.cuh"
 #include "tc5.cuh"
+#include "tree_pipeline.h"
 
 namespace csa {
 
@@ -88,9 +89,9 @@ struct TtShape {
   static constexpr int kRaw = kFp8 ? kTile * D : 0;
   static constexpr int kScales = kFp8 ? kScaleTiles * kScaleBytes : 0;
   static constexpr int kRoom = (227 * 1024 - (int)sizeof(TtSmem) - kQBytes - kRawDepth * kRaw - kScales) / kStage;
-  static constexpr int kStages = kRoom > 8 ? 8 : kRoom;
+  static constexpr int kStages = kRoom > 8 ? 8 : kRows == 128 ? kRoom / 2 * 2 : kRoom;
   static constexpr int kSmem = kQBytes + kStages * kStage + kRawDepth * kRaw + kScales + (int)sizeof(TtSmem);
-  static_assert(kStages >= (kRows == 128 ? 4 : 3), "a batch holds its K beside two tiles' V");
+  static_assert(kRows == 128 ? kStages % 2 == 0 && kStages >= 4 : kStages >= 3, "a batch's V and K");
   // a tile's scales stay until its weights are made: its V then waits in the ring, so
   // that the tile being written is at most kStages / 2 + 1 tiles ahead
   static_assert(kStages / 2 + 1 < kScaleTiles, "scales");
@@ -168,6 +169,13 @@ __device__ __forceinline__ uint64_t sdesc_mn_sw128(uint32_t saddr, uint32_t lbo)
   return tc5::sdesc_k_sw128(saddr) - ((uint64_t)1u << 16) + ((uint64_t)((lbo >> 4) & 0x3FFFu) << 16);
 }
 __device__ __forceinline__ bool not_finite(uint32_t bf16_bits) { return (bf16_bits & 0x7f80u) == 0x7f80u; }
+
+__device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap* map, int x, int y, int z, uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];\n" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(bar)
+      : "memory");
+}
 
 // One lane of a warp that runs as one: the same lane every time.
 __device__ __forceinline__ bool elect_one() {
@@ -289,11 +297,12 @@ __device__ __noinline__ void add_apart(const PagedArgs& a, int b, int h, int bas
 
 template <int D, int kRows, bool kFp8>
 __global__ void __launch_bounds__(kTtThreads, 1)
-    tree_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap,
-                const __grid_constant__ PagedArgs a, int seg, int chunks, int units, float* __restrict__ part, PaJoin* __restrict__ joins) {
+    tree_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__ CUtensorMap kmap,
+                const __grid_constant__ CUtensorMap vmap, const __grid_constant__ PagedArgs a, int rs, int seg, int chunks, int units, float* __restrict__ part, PaJoin* __restrict__ joins) {
   using Sh = TtShape<D, kRows, kFp8>;
   constexpr int ST = Sh::kStages;
-  constexpr bool kPair = kRows == 128;     // the slots share the query rows
+  constexpr bool kPair = kRows == 128;     // the slots share the query rows and take tiles in turn
+  using Ring = TreeRing<kPair, ST>;
   // (no static shared memory: the dynamic part starts on a 1024-byte boundary)
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   TtSmem& sm = *reinterpret_cast<TtSmem*>(smem_raw + Sh::kSmem - sizeof(TtSmem));
@@ -302,6 +311,7 @@ __global__ void __launch_bounds__(kTtThreads, 1)
   const uint32_t ring = qsm + Sh::kQBytes, raw = ring + ST * Sh::kStage, scales = raw + Sh::kRawDepth * Sh::kRaw;
   volatile int* abort = &sm.abort;
   const int group = a.heads / a.kv_heads, qrows = a.S * group;
+  const int unit_rows = kPair ? rs : 2 * rs;     // query rows of a unit, rs of them in a slot
   pdl_wait();
   pdl_trigger();
 
@@ -369,14 +379,16 @@ __global__ void __launch_bounds__(kTtThreads, 1)
     const float scale2 = a.scale * kLog2e;
     const int words32 = 2 * a.words;
     uint32_t n_s = 0, n_o = 0, n_pair = 0;     // phases of s_full, o_full and pair
-    int jj = 0, seen_pieces = 0;                // tiles of the CTA before this piece
+    int jj = 0, seen_pieces = 0;                // tiles and pieces of the CTA before this piece
+    Ring places;
+    places.start();
     Walk walk;
     walk.init(a, sm.cut);
     Piece pc;
     bool ok = true;
     while (ok && walk.next(a, units, pc)) {
-      const int h = chunks == 1 ? pc.unit : pc.unit / chunks, row0 = (pc.unit - h * chunks) * kRows;
-      const int i = row0 + (kPair ? 0 : slot * 128) + t;
+      const int h = chunks == 1 ? pc.unit : pc.unit / chunks, row0 = (pc.unit - h * chunks) * unit_rows;
+      const int i = t < rs ? row0 + (kPair ? 0 : slot * rs) + t : qrows;   // (qrows: no row)
       const int s = i < qrows ? token_of(i) : 0, hd = h * group + i - s * group;
       const int64_t tok = (int64_t)pc.b * a.S + s;
       __nv_bfloat16* out = static_cast<__nv_bfloat16*>(a.out) + tok * a.out_stride + hd * D;
@@ -390,7 +402,7 @@ __global__ void __launch_bounds__(kTtThreads, 1)
       }
       const int p_first = pc.sp.L - pc.sp.n;
       const bool real = i < qrows && s < pc.sp.n;
-      const bool busy = kPair ? pc.nt > slot : row0 + slot * 128 < qrows;   // the slot has tiles in this piece
+      const bool busy = kPair ? pc.nt > slot : row0 + slot * rs < qrows;   // the slot has tiles in this piece
       float m = -INFINITY, l = 0.f;
       if (busy) {
         const int outside = real ? tree_outside(a, pc.b, s, p_first, pc.sp.n) : 0;
@@ -482,12 +494,12 @@ __global__ void __launch_bounds__(kTtThreads, 1)
           }
           tc5::tmem_wait_st();
           if (edge) {
-            const int n = 2 * (jj + j) + 1;     // V's stage of the ring
-            ok = warp_wait(sm.full[n % ST], (n / ST) & 1, abort);
+            const typename Ring::Place v = places.at(j, true);
+            ok = warp_wait(sm.full[v.st], v.ph, abort);
             if (!ok) break;
             uint32_t bad[4];
 #pragma unroll
-            for (int w = 0; w < 4; ++w) bad[w] = *(volatile uint32_t*)&sm.bad[n % ST][w];
+            for (int w = 0; w < 4; ++w) bad[w] = *(volatile uint32_t*)&sm.bad[v.st][w];
             if (bad[0] | bad[1] | bad[2] | bad[3]) add_apart<D, kFp8>(a, pc.b, h, base, bad, seen, s_at, o_at);
           }
           tc5::fence_before_sync();
@@ -501,6 +513,7 @@ __global__ void __launch_bounds__(kTtThreads, 1)
         }
       }
       jj += pc.nt;
+      places.after(pc.nt);
       if (kPair) {
         // the two slots' states of a query row are joined: either warpgroup takes
         // half of the dims
@@ -589,53 +602,62 @@ __global__ void __launch_bounds__(kTtThreads, 1)
       const int w = warp - kRowWarp;
       constexpr int kRowBytes = D * (kFp8 ? 1 : 2), kSpan = kRowBytes / 16, kAtOnce = 32 / kSpan, kIter = 32 / kAtOnce;
       const int ch = lane % kSpan, r0 = lane / kSpan;
-      int steps = (int)(sm.cut[1].at - sm.cut[0].at);
-      Cursor<kTile, true> cu;
-      cu.b = sm.cut[0].b;
-      cu.sp.set(a, cu.b);
-      cu.unit = sm.cut[0].unit;
-      cu.tile = sm.cut[0].tile;
       // where this thread's piece i of a chunk lies in a stage
       auto place = [&](int i) {
         const int row = w * 32 + i * kAtOnce + r0;
         const int c0 = kFp8 ? 2 * ch : ch;
         return (uint32_t)((c0 >> 3) * kSub + row * 128 + (((c0 & 7) ^ (row & 7)) << 4));
       };
-      uint32_t n = 0, parity = 0;              // chunks; bit st: phase of land[st]
+      uint32_t parity = 0;                     // bit st: phase of land[st]
       bool ok = true;
+      Walk walk;
+      walk.init(a, sm.cut);
+      Piece pc;
+      Ring places;
+      places.start();
       if constexpr (kFp8) {
         // the lane's row of the tile: its scales are fetched a tile ahead, its place two
-        Cursor<kTile, true> at = cu;
-        int left = steps;
+        Walk at;
+        at.init(a, sm.cut);
+        Piece pa;
+        pa.nt = 0;
+        int ja = 0;                            // the tile looked up next, of piece pa (nt < 0: none is left)
         Spot spot;
         float ks = 0.f, vs = 0.f;
-        auto ahead = [&] {                     // `at` to the next tile with rows, its place looked up
-          while (left > 0 && at.sp.L <= 0) {
-            if (--left > 0) at.next(a, units);
+        auto ahead = [&] {
+          while (ja == pa.nt) {
+            ja = 0;
+            if (!at.next(a, units, pa)) pa.nt = -1;
+            else if (pa.sp.L <= 0) pa.nt = 0;
           }
           spot.none();
-          if (left > 0) spot.lookup(a, at.sp, at.b, at.tile, w * 32 + lane, 1);
+          if (pa.nt > 0) spot.lookup(a, pa.sp, pa.b, pa.tile + ja, w * 32 + lane, 1);
         };
         auto fetch = [&] {
           int row;
           if (!spot.resolve(a, -1, row)) row = -1;
-          const int h = chunks == 1 ? at.unit : at.unit / chunks;
+          const int h = chunks == 1 ? pa.unit : pa.unit / chunks;
           ks = vs = 0.f;
           if (row >= 0) ks = a.k_scale[(int64_t)row * a.scale_stride + h], vs = a.v_scale[(int64_t)row * a.scale_stride + h];
-          if (left > 0 && --left > 0) at.next(a, units);
+          if (pa.nt > 0) ++ja;
         };
         ahead();
         fetch();
         ahead();
-        for (; ok && steps > 0; --steps) {
-          if (cu.sp.L > 0) {
+        uint32_t n = 0, tiles = 0;             // chunks, tiles before the piece
+        while (ok && walk.next(a, units, pc)) {
+          if (pc.sp.L <= 0) continue;
 #pragma unroll 1
-            for (int kv = 0; kv < 2; ++kv, ++n) {
-              const uint32_t st = n % ST, stage = ring + st * Sh::kStage, slot = n % Sh::kRawDepth;
-              const bool look = kv && edge_tile(a, cu.sp, cu.tile);
+          for (int x = 0; x < 2 * pc.nt; ++x, ++n) {
+            {
+              bool kv;
+              const int j = Ring::tile_of(x, pc.nt, kv);
+              const typename Ring::Place at_ring = places.at(j, kv);
+              const uint32_t st = at_ring.st, stage = ring + st * Sh::kStage, slot = n % Sh::kRawDepth, tile = tiles + j;
+              const bool look = kv && edge_tile(a, pc.sp, pc.tile + j);
               uint32_t bad = 0;
               ok = warp_wait(sm.raw_full[slot], (n / Sh::kRawDepth) & 1, abort);
-              if (ok && n >= ST) ok = warp_wait(sm.empty[st], (n / ST - 1) & 1, abort);
+              if (ok && at_ring.c >= Ring::kPer) ok = warp_wait(sm.empty[st], at_ring.ph ^ 1, abort);
               if (!ok) break;
               const uint32_t from = raw + slot * Sh::kRaw + (w * kIter * 32 + lane) * 16;
               // four pieces at a time, so that their loads and conversions overlap
@@ -687,16 +709,16 @@ __global__ void __launch_bounds__(kTtThreads, 1)
                   asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};\n" ::"r"(first ^ 16u), "r"(u[4]), "r"(u[5]), "r"(u[6]), "r"(u[7]) : "memory");
                 }
               }
-              if (kv == 0) {
+              if (!kv) {
                 // the row's scales as the scores and weights take them; a V scale that is no
                 // number reaches whoever sees the row by its score
-                const uint32_t to = scales + ((n / 2) % kScaleTiles) * kScaleBytes + (w * 32 + lane) * 4;
+                const uint32_t to = scales + (tile % kScaleTiles) * kScaleBytes + (w * 32 + lane) * 4;
                 const bool number = fabsf(vs) < INFINITY;
                 asm volatile("st.shared.f32 [%0], %1;\n" ::"r"(to), "f"(number ? ks * (a.scale * kLog2e) : __uint_as_float(0x7fffffffu)) : "memory");
                 asm volatile("st.shared.f32 [%0], %1;\n" ::"r"(to + kTile * 4), "f"(number ? vs : 1.f) : "memory");
               }
               if (look) {
-                bad = __reduce_or_sync(0xffffffffu, bad) & span_rows(cu.sp, cu.tile, w);
+                bad = __reduce_or_sync(0xffffffffu, bad) & span_rows(pc.sp, pc.tile + j, w);
                 if (lane == 0) *(volatile uint32_t*)&sm.bad[st][w] = bad;
               }
               tc5::fence_proxy_async_smem();
@@ -704,21 +726,24 @@ __global__ void __launch_bounds__(kTtThreads, 1)
               if (lane == 0) {
                 tc5::mbar_arrive(smem_u32(&sm.full[st]));
                 tc5::mbar_arrive(smem_u32(&sm.raw_empty[slot]));
-                if (kv == 0) tc5::mbar_arrive(smem_u32(&sm.sc_full[(n / 2) % kScaleTiles]));
+                if (!kv) tc5::mbar_arrive(smem_u32(&sm.sc_full[tile % kScaleTiles]));
               }
-              if (kv == 0) {
+              if (!kv) {
                 fetch();
                 ahead();
               }
             }
           }
-          if (steps > 1) cu.next(a, units);
+          tiles += pc.nt;
+          places.after(pc.nt);
         }
       } else {
-        for (; ok && steps > 0; --steps) {
-          if (cu.sp.L > 0) {
-            if (edge_tile(a, cu.sp, cu.tile)) {
-              const uint32_t st = (n + 1) % ST, stage = ring + st * Sh::kStage;
+        while (ok && walk.next(a, units, pc)) {
+          if (pc.sp.L <= 0) continue;
+#pragma unroll 1
+          for (int j = 0; j < pc.nt; ++j) {
+            if (edge_tile(a, pc.sp, pc.tile + j)) {
+              const uint32_t st = places.at(j, true).st, stage = ring + st * Sh::kStage;
               ok = warp_wait(sm.land[st], (parity >> st) & 1, abort);
               parity ^= 1u << st;
               if (!ok) break;
@@ -739,7 +764,7 @@ __global__ void __launch_bounds__(kTtThreads, 1)
                   asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};\n" ::"r"(at), "r"(c[0]), "r"(c[1]), "r"(c[2]), "r"(c[3]) : "memory");
                 }
               }
-              bad = __reduce_or_sync(0xffffffffu, bad) & span_rows(cu.sp, cu.tile, w);
+              bad = __reduce_or_sync(0xffffffffu, bad) & span_rows(pc.sp, pc.tile + j, w);
               if (lane == 0) *(volatile uint32_t*)&sm.bad[st][w] = bad;
               tc5::fence_proxy_async_smem();
               __syncwarp();
@@ -751,9 +776,8 @@ __global__ void __launch_bounds__(kTtThreads, 1)
                 }
               }
             }
-            n += 2;
           }
-          if (steps > 1) cu.next(a, units);
+          places.after(pc.nt);
         }
       }
     } else if (warp == kLoadWarp) {
@@ -772,6 +796,9 @@ __global__ void __launch_bounds__(kTtThreads, 1)
       Piece next;                              // the block looked up: the first tiles of what is left of a piece
       bool more = false;
       Spot spot[4];
+      int row[4] = {none, none, none, none}, before[2][4] = {{none, none, none, none}, {none, none, none, none}};
+      int j0 = 0, m = 0, nt_piece = 0;         // the block's first tile, the next chunk, the tiles of the piece
+      bool fresh = true;
       auto look = [&] {
         while ((more = walk.next(a, units, next)) && next.sp.L <= 0) {
         }
@@ -785,31 +812,51 @@ __global__ void __launch_bounds__(kTtThreads, 1)
             spot[i].lookup(a, next.sp, next.b, next.tile + x / segs, x % segs * seg, seg);
         }
       };
-      uint32_t n = 0, st = 0, ph = 1;          // chunks; place in the ring, its phase before
-      constexpr uint32_t kInFlight = kFp8 ? Sh::kRawDepth : ST;
+      uint32_t n = 0;                          // chunks
+      Ring places;
+      places.start();
       bool ok = true;
       look();
       lookup();
       while (ok && more) {
         const Piece now = next;
         const int nt = min(ahead, now.nt), h = chunks == 1 ? now.unit : now.unit / chunks;
-        int row[4];
         bool all = true;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) all &= spot[i].resolve(a, none, row[i]);
+        for (int i = 0; i < 4; ++i) {
+          before[1][i] = before[0][i];
+          before[0][i] = row[i];
+          all &= spot[i].resolve(a, none, row[i]);
+        }
         if (!all && a.status) set_status(a.status, kStatusBadIndex);
+        if (fresh) {
+          places.after(nt_piece);
+          j0 = 0, m = 0, nt_piece = now.nt;
+        }
         next.tile += nt;
         next.nt -= nt;
-        if (next.nt == 0) look();
+        fresh = next.nt == 0;
+        if (fresh) look();
         lookup();
+        // the piece's chunks up to the block's last K (its last block: all)
+        const int last = j0 + nt == nt_piece ? 2 * nt_piece : Ring::upto_k(j0 + nt);
 #pragma unroll 1
-        for (int t = 0; ok && t < nt; ++t) {
-          const bool edge = !kFp8 && edge_tile(a, now.sp, now.tile + t);
-#pragma unroll 1
-          for (int kv = 0; kv < 2; ++kv) {
-            if (n >= kInFlight) ok = warp_wait(kFp8 ? sm.raw_empty[st] : sm.empty[st], ph, abort);
+        for (; ok && m < last; ++m) {
+          bool kv;
+          const int j = Ring::tile_of(m, nt_piece, kv);
+          const bool edge = !kFp8 && kv && edge_tile(a, now.sp, now.tile + j - j0);
+          {
+            // the tile's block: this one, or up to two before it
+            const int back = j >= j0 ? 0 : (j0 - j + ahead - 1) / ahead, t = j - j0 + back * ahead;
+            int at[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) at[i] = back == 0 ? row[i] : back == 1 ? before[0][i] : before[1][i];
+            const typename Ring::Place at_ring = places.at(j, kv);
+            const uint32_t st = kFp8 ? n % Sh::kRawDepth : at_ring.st;
+            if (kFp8 ? n >= (uint32_t)Sh::kRawDepth : at_ring.c >= (uint32_t)Ring::kPer)
+              ok = warp_wait(kFp8 ? sm.raw_empty[st] : sm.empty[st], kFp8 ? (n / Sh::kRawDepth - 1) & 1 : at_ring.ph ^ 1, abort);
             if (!ok) break;
-            const uint32_t bar = smem_u32(kFp8 ? &sm.raw_full[st] : kv && edge ? &sm.land[st] : &sm.full[st]);
+            const uint32_t bar = smem_u32(kFp8 ? &sm.raw_full[st] : edge ? &sm.land[st] : &sm.full[st]);
             const uint32_t to = kFp8 ? raw + st * Sh::kRaw : ring + st * Sh::kStage;
             const CUtensorMap* map = kv ? &vmap : &kmap;
             if (lane == 0) tc5::mbar_expect_tx(bar, kFp8 ? Sh::kRaw : Sh::kStage);
@@ -819,7 +866,7 @@ __global__ void __launch_bounds__(kTtThreads, 1)
 #pragma unroll 1
               for (int x0 = 0; x0 < segs * kCopies; x0 += 32) {
                 const int x = x0 + lane, s = x / kCopies, c = x % kCopies;
-                const int r = __shfl_sync(0xffffffffu, row[0], (t * segs + s) & 31);
+                const int r = __shfl_sync(0xffffffffu, at[0], (t * segs + s) & 31);
                 if (x < segs * kCopies) tc5::tma_load_2d(to + s * seg * 128 + c * kSub, map, h * D + 64 * c, r, bar);
               }
             } else {
@@ -827,19 +874,16 @@ __global__ void __launch_bounds__(kTtThreads, 1)
               for (int i = 0; i < 4; ++i)
 #pragma unroll
                 for (int c = 0; c < kCopies; ++c)
-                  if (i < per) tc5::tma_load_2d(to + (lane * per + i) * seg * 128 + c * kSub, map, h * D + 64 * c, row[i], bar);
+                  if (i < per) tc5::tma_load_2d(to + (lane * per + i) * seg * 128 + c * kSub, map, h * D + 64 * c, at[i], bar);
             }
             ++n;
-            if (++st == kInFlight) st = 0, ph ^= 1;
           }
         }
+        j0 += nt;
       }
-      // the copies in flight land before the block ends (they have, unless a wait gave up:
-      // then nothing is known of the barriers, and their time is waited for)
+      // the copies have landed when the block ends, unless a wait gave up: their time is waited for
       if (*abort)
         for (int i = 0; i < 100; ++i) __nanosleep(1000);
-      for (uint32_t m = n > kInFlight ? n - kInFlight : 0; m < n; ++m)
-        if (!tc5::mbar_wait_drain(smem_u32(kFp8 ? &sm.raw_full[m % kInFlight] : &sm.full[m % kInFlight]), (m / kInFlight) & 1)) break;
     } else if (warp == kMmaWarp || warp == kMmaWarp2) {
       // ---------------------------------------------------------- MMA issue
       // The warp runs as one (waits, ring places: the same in every lane), a lane issues.
@@ -851,7 +895,7 @@ __global__ void __launch_bounds__(kTtThreads, 1)
       const uint64_t dq = tc5::sdesc_k_sw128(qsm + (kPair ? 0 : slot * Sh::kStage));
       const uint64_t dk = tc5::sdesc_k_sw128(ring), dv = sdesc_mn_sw128(ring, kSub);
       const uint32_t s_at = tmem + slot * 128, o_at = tmem + 256 + slot * 128;
-      uint32_t n0 = 0, pph = 0, qph = 0;       // the piece's first chunk; phases
+      uint32_t pph = 0, qph = 0;               // phases
       bool ok = true;
       auto wait = [&](uint64_t& bar, uint32_t parity) {
         uint32_t i = 0;
@@ -864,45 +908,43 @@ __global__ void __launch_bounds__(kTtThreads, 1)
         ok = __all_sync(0xffffffffu, ok);
         tc5::fence_after_sync();
       };
-      // a chunk's place in the ring, moved on by kStep chunks at a time
-      struct Place {
+      Ring places;
+      places.start();
+      // a slot's K or V, moved on to its next tile's
+      struct Next {
         uint32_t st, ph;
-        __device__ __forceinline__ void set(uint32_t n) { st = n % ST, ph = (n / ST) & 1; }
-        __device__ __forceinline__ void move(uint32_t by) {
-          st += by;
-          while (st >= ST) st -= ST, ph ^= 1;
+        __device__ __forceinline__ void set(const typename Ring::Place& p, int slot) { st = p.st - (kPair ? slot * Ring::kPer : 0), ph = p.ph; }
+        __device__ __forceinline__ void move() {
+          st += 2;
+          if (st >= Ring::kPer) st -= Ring::kPer, ph ^= 1;
         }
       };
-      constexpr uint32_t kStep = kPair ? 4 : 2;  // from one tile of the slot to its next
-      // Every chunk's phase is seen, in order, the other slot's too: a wait for a stage's
-      // phase while the one before has not come would take the phase two before for it.
-      Place seen;
-      seen.set(0);
-      uint32_t n_seen = 0;
-      auto see = [&](uint32_t n) {             // chunks up to n have landed
-        for (; ok && n_seen <= n; ++n_seen, seen.move(1)) wait(sm.full[seen.st], seen.ph);
-      };
+      uint64_t* const full = sm.full + (kPair ? slot * Ring::kPer : 0);
+      uint64_t* const empty = sm.empty + (kPair ? slot * Ring::kPer : 0);
+      const uint32_t stages = kPair ? slot * Ring::kPer * Sh::kStage : 0;   // the slot's ring
       Walk walk;
       walk.init(a, sm.cut);
       Piece pc;
       while (ok && walk.next(a, units, pc)) {
         if (pc.sp.L <= 0) continue;
-        const int h = chunks == 1 ? pc.unit : pc.unit / chunks, row0 = (pc.unit - h * chunks) * kRows;
-        const bool busy = kPair ? pc.nt > slot : row0 + slot * 128 < qrows;
+        const int h = chunks == 1 ? pc.unit : pc.unit / chunks, row0 = (pc.unit - h * chunks) * unit_rows;
+        const bool busy = kPair ? pc.nt > slot : row0 + slot * rs < qrows;
         if (!busy) {
           // no rows or tiles for this slot: what it would have read is given back
+          if (!kPair) {
 #pragma unroll 1
-          for (int i = 0; ok && i < 2 * pc.nt; ++i) {
-            const uint32_t st = seen.st;
-            see(n0 + i);
-            if (!kPair && ok && elect_one()) tc5::mbar_arrive(smem_u32(&sm.empty[st]));
+            for (int i = 0; ok && i < 2 * pc.nt; ++i) {
+              const typename Ring::Place c = places.at(i >> 1, i & 1);
+              wait(full[c.st], c.ph);
+              if (ok && elect_one()) tc5::mbar_arrive(smem_u32(&empty[c.st]));
+            }
           }
           wait(sm.q_full, qph);
           if (ok && elect_one()) tc5::mbar_arrive(smem_u32(&sm.q_empty));
         } else {
-          Place k, v;
-          k.set(n0 + (kPair ? 2 * slot : 0));
-          v.set(n0 + (kPair ? 2 * slot : 0) + 1);
+          Next k, v;
+          k.set(places.at(kPair ? slot : 0, false), slot);
+          v.set(places.at(kPair ? slot : 0, true), slot);
           wait(sm.q_full, qph);
           // a batch: with tile j's weights the output, then the scores of the slot's next
           // tile, 16 MMAs without anything between them
@@ -910,39 +952,39 @@ __global__ void __launch_bounds__(kTtThreads, 1)
 #pragma unroll 1
           for (int j = first - step; j < pc.nt; j += step) {
             const bool out = j >= first, in = j + step < pc.nt;
-            see(in ? n0 + 2 * (j + step) : n0 + 2 * j + 1);   // (K of the next tile comes after V of this one)
+            if (in) wait(full[k.st], k.ph);
             if (out) {
+              wait(full[v.st], v.ph);
               wait(sm.p_full[slot], pph);
               pph ^= 1;
             }
             if (!ok) break;
             if (elect_one()) {
               if (out) {
-                const uint64_t d = dv + ((v.st * Sh::kStage) >> 4);
+                const uint64_t d = dv + ((stages + v.st * Sh::kStage) >> 4);
 #pragma unroll
                 for (int x = 0; x < kTile / 16; ++x) tc5::mma_bf16_ta(o_at, s_at + 8 * x, d + ((x * 2048) >> 4), idesc_o, 1u);
               }
               if (in) {
-                const uint64_t d = dk + ((k.st * Sh::kStage) >> 4);
+                const uint64_t d = dk + ((stages + k.st * Sh::kStage) >> 4);
 #pragma unroll
                 for (int x = 0; x < D / 16; ++x)
                   tc5::mma_bf16(s_at, dq + (((x >> 2) * kSub + (x & 3) * 32) >> 4), d + (((x >> 2) * kSub + (x & 3) * 32) >> 4),
                                 idesc_s, x > 0);
                 tc5::mma_commit(smem_u32(&sm.s_full[slot]));
-                tc5::mma_commit(smem_u32(&sm.empty[k.st]));
+                tc5::mma_commit(smem_u32(&empty[k.st]));
                 if (j + 2 * step >= pc.nt) tc5::mma_commit(smem_u32(&sm.q_empty));
               } else {
                 tc5::mma_commit(smem_u32(&sm.o_full[slot]));
               }
-              if (out) tc5::mma_commit(smem_u32(&sm.empty[v.st]));
+              if (out) tc5::mma_commit(smem_u32(&empty[v.st]));
             }
-            if (in) k.move(kStep);
-            if (out) v.move(kStep);
+            if (in) k.move();
+            if (out) v.move();
           }
-          see(n0 + 2 * pc.nt - 1);
         }
         qph ^= 1;
-        n0 += 2 * pc.nt;
+        places.after(pc.nt);
       }
       if (elect_one()) tc5::mma_commit(smem_u32(&sm.done[slot]));
       tc5::mbar_wait_drain(smem_u32(&sm.done[slot]), 0);
@@ -951,39 +993,29 @@ __global__ void __launch_bounds__(kTtThreads, 1)
       // ---------------------------------------------------------- the units' query rows
       uint32_t n_q = 0;
       bool ok = true;
+      if (lane == 0) tc5::prefetch_tmap(&qmap);
       Walk walk;
       walk.init(a, sm.cut);
       Piece pc;
       while (ok && walk.next(a, units, pc)) {
         if (pc.sp.L <= 0) continue;
-        const int h = chunks == 1 ? pc.unit : pc.unit / chunks, row0 = (pc.unit - h * chunks) * kRows;
+        const int h = chunks == 1 ? pc.unit : pc.unit / chunks, row0 = (pc.unit - h * chunks) * unit_rows;
         if (n_q > 0) ok = warp_wait(sm.q_empty, (n_q - 1) & 1, abort);
         if (!ok) break;
-        const __nv_bfloat16* q0 = static_cast<const __nv_bfloat16*>(a.q) + (int64_t)pc.b * a.S * a.q_stride;
-        // a lane copies one 16-byte column of every kAt-th row; token and head are counted up
-        constexpr int kAt = 32 / (D / 8);
-        const int c = lane % (D / 8);
-        int r = lane / (D / 8), s = token_of(row0 + r), g = row0 + r - s * group;
-        uint32_t dst = qsm + (c >> 3) * kSub + r * 128;
-#pragma unroll 4
-        for (; r < kRows; r += kAt, dst += kAt * 128) {
-          if (r == 128 + lane / (D / 8)) dst += Sh::kStage - kSub;   // the second slot's rows
-          const bool in = row0 + r < qrows;
-          const __nv_bfloat16* src = q0 + (int64_t)(in ? s : 0) * a.q_stride + ((in ? h * group + g : 0) * D + c * 8);
-          cp_async16(dst + (((c & 7) ^ (r & 7)) << 4), src, in ? 16 : 0);
-          g += kAt;
-          while (g >= group) g -= group, ++s;
+        // whole tokens' heads: 128 / group tokens to a slot
+        const int slots = !kPair && row0 + rs < qrows ? 2 : 1, tokens = rs / group;
+        if (lane == 0) {
+          tc5::mbar_expect_tx(smem_u32(&sm.q_full), slots * Sh::kSubs * rs * 128);
+          for (int x = 0; x < slots * Sh::kSubs; ++x)
+            tma_load_3d(qsm + x * kSub, &qmap, 64 * (x % Sh::kSubs), h * group, pc.b * a.S + row0 / group + x / Sh::kSubs * tokens,
+                        smem_u32(&sm.q_full));
         }
-        cp_async_commit();
-        cp_async_wait<0>();
-        tc5::fence_proxy_async_smem();
         __syncwarp();
-        if (lane == 0) tc5::mbar_arrive(smem_u32(&sm.q_full));
         ++n_q;
       }
+      if (n_q > 0) tc5::mbar_wait_drain(smem_u32(&sm.q_full), (n_q - 1) & 1);   // landed before the block ends
     }
   }
-  cp_async_wait<0>();
   tc5::fence_before_sync();
   __syncthreads();
   tc5::fence_after_sync();
@@ -995,15 +1027,15 @@ __global__ void __launch_bounds__(kTtThreads, 1)
 // 32 y .. of the unit that starts in CTA x, a thread a row and D / 8 dims.
 template <int D>
 __global__ void __launch_bounds__(256)
-    tree_join_kernel(const PagedArgs a, int chunks, int rows, const float* __restrict__ part, const PaJoin* __restrict__ joins) {
+    tree_join_kernel(const PagedArgs a, int rs, int chunks, int rows, const float* __restrict__ part, const PaJoin* __restrict__ joins) {
   pdl_wait();
   pdl_trigger();
   const PaJoin j = joins[blockIdx.x];
   if (j.count == 0) return;
   const int lane = threadIdx.x & 31, c0 = (threadIdx.x >> 5) * (D / 8);
   const int group = a.heads / a.kv_heads, h = j.unit / chunks, r0 = blockIdx.y * 32;
-  const int i = (j.unit - h * chunks) * rows + r0 + lane;
-  if (i >= a.S * group) return;
+  const int t = (r0 & 127) + lane, i = ((j.unit - h * chunks) * (rows / 128) + (r0 >> 7)) * rs + t;
+  if (t >= rs || i >= a.S * group) return;
   float m = -INFINITY, l = 0.f, acc[D / 8];
 #pragma unroll
   for (int x = 0; x < D / 8; ++x) acc[x] = 0.f;
@@ -1048,6 +1080,18 @@ bool make_pool_map(CUtensorMap* m, const void* ptr, int64_t rows, uint64_t width
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// The queries by token, head and 64 dims; a copy takes `group` heads of `tokens` tokens.
+bool make_query_map(CUtensorMap* m, const PagedArgs& a, int group, int tokens) {
+  auto fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(tensor_map_encoder());
+  if (!fn) return false;
+  cuuint64_t dims[3] = {(cuuint64_t)a.dim, (cuuint64_t)a.heads, (cuuint64_t)a.B * a.S};
+  cuuint64_t strides[2] = {(cuuint64_t)a.dim * 2, (cuuint64_t)a.q_stride * 2};
+  cuuint32_t box[3] = {64, (cuuint32_t)group, (cuuint32_t)tokens};
+  cuuint32_t estr[3] = {1, 1, 1};
+  return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(a.q), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+            CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_128B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 template <int D, int kRows, bool kFp8>
 int launch_rows(const PagedArgs& a, int num_sms, cudaStream_t st, bool pdl) {
   using Sh = TtShape<D, kRows, kFp8>;
@@ -1068,15 +1112,18 @@ int launch_rows(const PagedArgs& a, int num_sms, cudaStream_t st, bool pdl) {
   if (!make_pool_map(&kmap, a.k, a.rows, (uint64_t)a.kv_heads * D, a.k_step, kFp8, D, seg) ||
       !make_pool_map(&vmap, a.v, a.rows, (uint64_t)a.kv_heads * D, a.v_step, kFp8, D, seg))
     return launch_fail("cuTensorMapEncodeTiled(K / V pools)", cudaErrorInvalidValue);
-  const int qrows = a.S * (a.heads / a.kv_heads), chunks = (qrows + kRows - 1) / kRows;
+  const int group = a.heads / a.kv_heads, qrows = a.S * group, rs = 128 / group * group;
+  const int unit_rows = kRows / 128 * rs, chunks = (qrows + unit_rows - 1) / unit_rows;
+  CUtensorMap qmap;
+  if (!make_query_map(&qmap, a, group, rs / group)) return launch_fail("cuTensorMapEncodeTiled(q)", cudaErrorInvalidValue);
   float* part = static_cast<float*>(a.workspace);
   PaJoin* joins = reinterpret_cast<PaJoin*>(part + (size_t)num_sms * 2 * kRows * (D + 2));
   const int64_t tiles = (int64_t)a.B * a.kv_heads * chunks * ((a.max_len + kTile - 1) / kTile + kExtra);
   const int grid = tiles < num_sms ? (int)tiles : num_sms;
-  const int r = launch_kernel(kern, dim3(grid), dim3(kTtThreads), Sh::kSmem, st, pdl, kmap, vmap, a, seg, chunks, a.kv_heads * chunks, part, joins);
+  const int r = launch_kernel(kern, dim3(grid), dim3(kTtThreads), Sh::kSmem, st, pdl, qmap, kmap, vmap, a, rs, seg, chunks, a.kv_heads * chunks, part, joins);
   if (r < 0) return r;
-  const int most = qrows < kRows ? qrows : kRows;
-  const int r2 = launch_kernel(tree_join_kernel<D>, dim3(grid, (most + 31) / 32), dim3(256), 0, st, pdl, a, chunks, kRows,
+  const int most = qrows < rs ? qrows : kRows;
+  const int r2 = launch_kernel(tree_join_kernel<D>, dim3(grid, (most + 31) / 32), dim3(256), 0, st, pdl, a, rs, chunks, kRows,
                                (const float*)part, (const PaJoin*)joins);
   return r2 < 0 ? r2 : r + r2;
 }
@@ -1093,8 +1140,10 @@ size_t tree_attn_workspace(int dim, int num_sms) {
 
 int launch_tree_attn(const PagedArgs& a, bool fp8, int num_sms, cudaStream_t st, bool pdl) {
   const int qrows = a.S * (a.heads / a.kv_heads);
-  if (a.dim == 256 || qrows <= 32) return launch_paged_attn(a, fp8, num_sms, st, pdl);
-  const bool two = qrows > 128;
+  const int group = a.heads / a.kv_heads;
+  // a slot takes whole tokens' heads; a token coordinate is an int
+  if (a.dim == 256 || qrows <= 32 || group > 128 || (int64_t)a.B * a.S > 0x7fffffff) return launch_paged_attn(a, fp8, num_sms, st, pdl);
+  const bool two = qrows > 128 / group * group;
   if (fp8) return two ? launch_rows<128, 256, true>(a, num_sms, st, pdl) : launch_rows<128, 128, true>(a, num_sms, st, pdl);
   if (a.dim == 64) return two ? launch_rows<64, 256, false>(a, num_sms, st, pdl) : launch_rows<64, 128, false>(a, num_sms, st, pdl);
   return two ? launch_rows<128, 256, false>(a, num_sms, st, pdl) : launch_rows<128, 128, false>(a, num_sms, st, pdl);
