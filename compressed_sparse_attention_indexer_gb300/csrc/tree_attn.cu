@@ -57,7 +57,12 @@ namespace {
 
 constexpr int kTtThreads = 512;
 constexpr int kRowWarp = 8, kRowWarps = 4, kMmaWarp = 12, kMmaWarp2 = 14, kLoadWarp = 13;
-constexpr int kRegsSoftmax = 184, kRegsOthers = 72;   // of the launch's 128 per thread
+// Registers of the softmax's threads and of the others, 2 x 128 together: E4M3's converters
+// want more (56: 195 us instead of 165 for 8 x 64 drafts over 8192 .. 16384 rows, 32 / 4 heads; bf16 101 with 56, 103 with 72).
+template <bool kFp8>
+constexpr int kRegsSoftmax = kFp8 ? 184 : 200;
+template <bool kFp8>
+constexpr int kRegsOthers = 256 - kRegsSoftmax<kFp8>;
 constexpr int kTile = 128;                 // K / V rows per tile
 constexpr int kExtra = 2;                  // a unit's start and end, in tiles
 constexpr int kSub = kTile * 128;          // 128 rows x 64 dims bf16
@@ -371,7 +376,7 @@ __global__ void __launch_bounds__(kTtThreads, 1)
   auto token_of = [&](int i) { return (int)(((float)i + 0.5f) * per_group); };
 
   if (warp < kRowWarp) {
-    setmaxnreg_inc<kRegsSoftmax>();
+    setmaxnreg_inc<kRegsSoftmax<kFp8>>();
     // ------------------------------------------------------------ softmax
     const int slot = warp >> 2, t = tid & 127;
     const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
@@ -494,7 +499,9 @@ __global__ void __launch_bounds__(kTtThreads, 1)
           }
           tc5::tmem_wait_st();
           if (edge) {
-            const typename Ring::Place v = places.at(j, true);
+            Ring now = places;
+            if (!kPair) now.base[0] = 2 * jj;    // (one register less to keep)
+            const typename Ring::Place v = now.at(j, true);
             ok = warp_wait(sm.full[v.st], v.ph, abort);
             if (!ok) break;
             uint32_t bad[4];
@@ -513,7 +520,7 @@ __global__ void __launch_bounds__(kTtThreads, 1)
         }
       }
       jj += pc.nt;
-      places.after(pc.nt);
+      if (kPair) places.after(pc.nt);
       if (kPair) {
         // the two slots' states of a query row are joined: either warpgroup takes
         // half of the dims
@@ -596,7 +603,7 @@ __global__ void __launch_bounds__(kTtThreads, 1)
       }
     }
   } else {
-    setmaxnreg_dec<kRegsOthers>();
+    setmaxnreg_dec<kRegsOthers<kFp8>>();
     if (warp < kMmaWarp) {
       // ---------------------------------------------------------- converters, or V's readers
       const int w = warp - kRowWarp;
@@ -608,57 +615,55 @@ __global__ void __launch_bounds__(kTtThreads, 1)
         const int c0 = kFp8 ? 2 * ch : ch;
         return (uint32_t)((c0 >> 3) * kSub + row * 128 + (((c0 & 7) ^ (row & 7)) << 4));
       };
-      uint32_t parity = 0;                     // bit st: phase of land[st]
       bool ok = true;
-      Walk walk;
-      walk.init(a, sm.cut);
-      Piece pc;
-      Ring places;
-      places.start();
       if constexpr (kFp8) {
         // the lane's row of the tile: its scales are fetched a tile ahead, its place two
-        Walk at;
-        at.init(a, sm.cut);
-        Piece pa;
-        pa.nt = 0;
-        int ja = 0;                            // the tile looked up next, of piece pa (nt < 0: none is left)
+        Cursor<kTile, true> at;
+        int left;
+        {
+          Walk walk;
+          walk.init(a, sm.cut);
+          at = walk.cu;
+          left = walk.left;
+        }
         Spot spot;
+        // of the tile looked up and of the one fetched: there is one, some draft does not see
+        // it whole, the span's rows of the warp's
+        bool some_ahead = false, edge_ahead = false, some = false, edge = false;
+        uint32_t rows_ahead = 0, rows = 0;
         float ks = 0.f, vs = 0.f;
-        auto ahead = [&] {
-          while (ja == pa.nt) {
-            ja = 0;
-            if (!at.next(a, units, pa)) pa.nt = -1;
-            else if (pa.sp.L <= 0) pa.nt = 0;
+        auto ahead = [&] {                     // `at` to the next tile with rows, its place looked up
+          while (left > 0 && at.sp.L <= 0) {
+            if (--left > 0) at.next(a, units);
           }
           spot.none();
-          if (pa.nt > 0) spot.lookup(a, pa.sp, pa.b, pa.tile + ja, w * 32 + lane, 1);
+          some_ahead = left > 0;
+          if (left > 0) {
+            spot.lookup(a, at.sp, at.b, at.tile, w * 32 + lane, 1);
+            edge_ahead = edge_tile(a, at.sp, at.tile);
+            rows_ahead = span_rows(at.sp, at.tile, w);
+          }
         };
         auto fetch = [&] {
+          some = some_ahead, edge = edge_ahead, rows = rows_ahead;
           int row;
           if (!spot.resolve(a, -1, row)) row = -1;
-          const int h = chunks == 1 ? pa.unit : pa.unit / chunks;
+          const int h = chunks == 1 ? at.unit : at.unit / chunks;
           ks = vs = 0.f;
           if (row >= 0) ks = a.k_scale[(int64_t)row * a.scale_stride + h], vs = a.v_scale[(int64_t)row * a.scale_stride + h];
-          if (pa.nt > 0) ++ja;
+          if (left > 0 && --left > 0) at.next(a, units);
         };
         ahead();
         fetch();
         ahead();
-        uint32_t n = 0, tiles = 0;             // chunks, tiles before the piece
-        while (ok && walk.next(a, units, pc)) {
-          if (pc.sp.L <= 0) continue;
-#pragma unroll 1
-          for (int x = 0; x < 2 * pc.nt; ++x, ++n) {
-            {
-              bool kv;
-              const int j = Ring::tile_of(x, pc.nt, kv);
-              const typename Ring::Place at_ring = places.at(j, kv);
-              const uint32_t st = at_ring.st, stage = ring + st * Sh::kStage, slot = n % Sh::kRawDepth, tile = tiles + j;
-              const bool look = kv && edge_tile(a, pc.sp, pc.tile + j);
+        uint32_t n = 0;                        // chunks
+        // chunk n to its stage: K or V (look: an edge tile's V, with the span's rows) of the CTA's `tile`
+        auto convert = [&](uint32_t st, bool wait_empty, uint32_t parity, bool kv, uint32_t tile, bool look, uint32_t mask) {
+              const uint32_t stage = ring + st * Sh::kStage, slot = n % Sh::kRawDepth;
               uint32_t bad = 0;
               ok = warp_wait(sm.raw_full[slot], (n / Sh::kRawDepth) & 1, abort);
-              if (ok && at_ring.c >= Ring::kPer) ok = warp_wait(sm.empty[st], at_ring.ph ^ 1, abort);
-              if (!ok) break;
+              if (ok && wait_empty) ok = warp_wait(sm.empty[st], parity, abort);
+              if (!ok) return;
               const uint32_t from = raw + slot * Sh::kRaw + (w * kIter * 32 + lane) * 16;
               // four pieces at a time, so that their loads and conversions overlap
 #pragma unroll 1
@@ -718,7 +723,7 @@ __global__ void __launch_bounds__(kTtThreads, 1)
                 asm volatile("st.shared.f32 [%0], %1;\n" ::"r"(to + kTile * 4), "f"(number ? vs : 1.f) : "memory");
               }
               if (look) {
-                bad = __reduce_or_sync(0xffffffffu, bad) & span_rows(pc.sp, pc.tile + j, w);
+                bad = __reduce_or_sync(0xffffffffu, bad) & mask;
                 if (lane == 0) *(volatile uint32_t*)&sm.bad[st][w] = bad;
               }
               tc5::fence_proxy_async_smem();
@@ -728,16 +733,56 @@ __global__ void __launch_bounds__(kTtThreads, 1)
                 tc5::mbar_arrive(smem_u32(&sm.raw_empty[slot]));
                 if (!kv) tc5::mbar_arrive(smem_u32(&sm.sc_full[tile % kScaleTiles]));
               }
+              ++n;
+        };
+        if constexpr (kPair) {
+          Walk walk;
+          walk.init(a, sm.cut);
+          Piece pc;
+          Ring places;
+          places.start();
+          uint32_t tiles = 0;                  // before the piece
+          while (ok && walk.next(a, units, pc)) {
+            if (pc.sp.L <= 0) continue;
+#pragma unroll 1
+            for (int x = 0; ok && x < 2 * pc.nt; ++x) {
+              bool kv;
+              const int j = Ring::tile_of(x, pc.nt, kv);
+              const typename Ring::Place to = places.at(j, kv);
+              convert(to.st, to.c >= Ring::kPer, to.ph ^ 1, kv, tiles + j, kv && edge_tile(a, pc.sp, pc.tile + j),
+                      span_rows(pc.sp, pc.tile + j, w));
+              if (!kv) {
+                fetch();
+                ahead();
+              }
+            }
+            tiles += pc.nt;
+            places.after(pc.nt);
+          }
+        } else {
+          // (K and V of tile after tile: pieces do not matter, which leaves registers)
+          uint32_t st = 0, ph = 1;
+          for (uint32_t tile = 0; ok && some; ++tile) {
+            const bool edge_now = edge;
+            const uint32_t rows_now = rows;
+#pragma unroll 1
+            for (int kv = 0; ok && kv < 2; ++kv) {
+              convert(st, n >= ST, ph, kv, tile, kv && edge_now, rows_now);
+              if (++st == ST) st = 0, ph ^= 1;
               if (!kv) {
                 fetch();
                 ahead();
               }
             }
           }
-          tiles += pc.nt;
-          places.after(pc.nt);
         }
       } else {
+        uint32_t parity = 0;                   // bit st: phase of land[st]
+        Walk walk;
+        walk.init(a, sm.cut);
+        Piece pc;
+        Ring places;
+        places.start();
         while (ok && walk.next(a, units, pc)) {
           if (pc.sp.L <= 0) continue;
 #pragma unroll 1
@@ -839,7 +884,7 @@ __global__ void __launch_bounds__(kTtThreads, 1)
         if (fresh) look();
         lookup();
         // the piece's chunks up to the block's last K (its last block: all)
-        const int last = j0 + nt == nt_piece ? 2 * nt_piece : Ring::upto_k(j0 + nt);
+        const int last = !kPair ? 2 * (j0 + nt) : j0 + nt == nt_piece ? 2 * nt_piece : Ring::upto_k(j0 + nt);
 #pragma unroll 1
         for (; ok && m < last; ++m) {
           bool kv;
@@ -850,7 +895,7 @@ __global__ void __launch_bounds__(kTtThreads, 1)
             const int back = j >= j0 ? 0 : (j0 - j + ahead - 1) / ahead, t = j - j0 + back * ahead;
             int at[4];
 #pragma unroll
-            for (int i = 0; i < 4; ++i) at[i] = back == 0 ? row[i] : back == 1 ? before[0][i] : before[1][i];
+            for (int i = 0; i < 4; ++i) at[i] = !kPair ? row[i] : back == 0 ? row[i] : back == 1 ? before[0][i] : before[1][i];
             const typename Ring::Place at_ring = places.at(j, kv);
             const uint32_t st = kFp8 ? n % Sh::kRawDepth : at_ring.st;
             if (kFp8 ? n >= (uint32_t)Sh::kRawDepth : at_ring.c >= (uint32_t)Ring::kPer)
@@ -1102,7 +1147,7 @@ int launch_rows(const PagedArgs& a, int num_sms, cudaStream_t st, bool pdl) {
         cudaFuncAttributes fa;
         const cudaError_t q = cudaFuncGetAttributes(&fa, kern);
         if (q != cudaSuccess) return q;
-        if (fa.numRegs * kTtThreads < kTtThreads / 2 * (kRegsSoftmax + kRegsOthers)) return cudaErrorLaunchOutOfResources;
+        if (fa.numRegs * kTtThreads < kTtThreads / 2 * (kRegsSoftmax<kFp8> + kRegsOthers<kFp8>)) return cudaErrorLaunchOutOfResources;
         return allow_max_dynamic_smem(kern);
       }))
     return launch_fail("cudaFuncSetAttribute(tree_kernel)", e);
