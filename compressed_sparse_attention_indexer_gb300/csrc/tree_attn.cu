@@ -841,9 +841,9 @@ __global__ void __launch_bounds__(kTtThreads, 1)
       Piece next;                              // the block looked up: the first tiles of what is left of a piece
       bool more = false;
       Spot spot[4];
-      int row[4] = {none, none, none, none}, before[2][4] = {{none, none, none, none}, {none, none, none, none}};
-      int j0 = 0, m = 0, nt_piece = 0;         // the block's first tile, the next chunk, the tiles of the piece
-      bool fresh = true;
+      // pool rows of the block's segments, and of the block's before (V follows its K by a tile
+      // where slots take turns)
+      int row[4] = {none, none, none, none}, before[4];
       auto look = [&] {
         while ((more = walk.next(a, units, next)) && next.sp.L <= 0) {
         }
@@ -857,74 +857,79 @@ __global__ void __launch_bounds__(kTtThreads, 1)
             spot[i].lookup(a, next.sp, next.b, next.tile + x / segs, x % segs * seg, seg);
         }
       };
-      uint32_t n = 0;                          // chunks
-      Ring places;
-      places.start();
+      // the places in the rings, or of E4M3 codes beside them: counted up
+      uint32_t st[2] = {0, 0}, ph[2] = {1, 1};  // stage within the ring, its phase before
+      bool wait_for[2] = {false, false};        // the ring has come round
+      constexpr uint32_t kPlaces = kFp8 ? Sh::kRawDepth : Ring::kPer;
       bool ok = true;
+      constexpr int kCopies = kFp8 ? 1 : Sh::kSubs;   // of a segment
+      const int copies = segs * kCopies;
+      const uint32_t to_lane = lane / kCopies * seg * 128 + lane % kCopies * kSub;
+      // tile t of the block (was: of the block before): its K or V, into the slot's ring
+      auto copy = [&](int t, bool was, bool v, int slot, int h, bool edge) {
+        const int ring_of = kPair && !kFp8 ? slot : 0;
+        const uint32_t s0 = ring_of ? st[1] : st[0], p0 = ring_of ? ph[1] : ph[0];
+        const uint32_t at = kFp8 ? s0 : s0 + (kPair ? slot * Ring::kPer : 0);
+        if (ring_of ? wait_for[1] : wait_for[0]) ok = warp_wait(kFp8 ? sm.raw_empty[at] : sm.empty[at], p0, abort);
+        if (!ok) return;
+        const uint32_t bar = smem_u32(kFp8 ? &sm.raw_full[at] : edge ? &sm.land[at] : &sm.full[at]);
+        const uint32_t to = kFp8 ? raw + at * Sh::kRaw : ring + at * Sh::kStage;
+        const CUtensorMap* map = v ? &vmap : &kmap;
+        if (lane == 0) tc5::mbar_expect_tx(bar, kFp8 ? Sh::kRaw : Sh::kStage);
+        __syncwarp();
+        if (per == 1) {
+          const int mine = was ? before[0] : row[0];
+          const int r = __shfl_sync(0xffffffffu, mine, (t * segs + lane / kCopies) & 31);
+          if (lane < copies) tc5::tma_load_2d(to + to_lane, map, h * D + 64 * (lane % kCopies), r, bar);
+          if (copies > 32) {                     // 32 segments in two copies
+            const int r2 = __shfl_sync(0xffffffffu, mine, 32 / kCopies + lane / kCopies);
+            tc5::tma_load_2d(to + to_lane + 32 / kCopies * seg * 128, map, h * D + 64 * (lane % kCopies), r2, bar);
+          }
+        } else {
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+#pragma unroll
+            for (int c = 0; c < kCopies; ++c)
+              if (i < per) tc5::tma_load_2d(to + (lane * per + i) * seg * 128 + c * kSub, map, h * D + 64 * c, was ? before[i] : row[i], bar);
+        }
+        const bool round = s0 + 1 == kPlaces;
+        if (ring_of) {
+          st[1] = round ? 0 : s0 + 1, ph[1] ^= round, wait_for[1] |= round;
+        } else {
+          st[0] = round ? 0 : s0 + 1, ph[0] ^= round, wait_for[0] |= round;
+        }
+      };
       look();
       lookup();
+      bool fresh = true;
+      int j = 0;                                 // the block's first tile in its piece
       while (ok && more) {
-        const Piece now = next;
-        const int nt = min(ahead, now.nt), h = chunks == 1 ? now.unit : now.unit / chunks;
+        const Span<kTile, true> sp = next.sp;
+        const int nt = min(ahead, next.nt), h = chunks == 1 ? next.unit : next.unit / chunks, tile0 = next.tile;
         bool all = true;
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          before[1][i] = before[0][i];
-          before[0][i] = row[i];
+          before[i] = row[i];
           all &= spot[i].resolve(a, none, row[i]);
         }
         if (!all && a.status) set_status(a.status, kStatusBadIndex);
-        if (fresh) {
-          places.after(nt_piece);
-          j0 = 0, m = 0, nt_piece = now.nt;
-        }
+        if (fresh) j = 0;
         next.tile += nt;
         next.nt -= nt;
-        fresh = next.nt == 0;
+        fresh = next.nt == 0;                    // the piece's last block
         if (fresh) look();
         lookup();
-        // the piece's chunks up to the block's last K (its last block: all)
-        const int last = !kPair ? 2 * (j0 + nt) : j0 + nt == nt_piece ? 2 * nt_piece : Ring::upto_k(j0 + nt);
 #pragma unroll 1
-        for (; ok && m < last; ++m) {
-          bool kv;
-          const int j = Ring::tile_of(m, nt_piece, kv);
-          const bool edge = !kFp8 && kv && edge_tile(a, now.sp, now.tile + j - j0);
-          {
-            // the tile's block: this one, or up to two before it
-            const int back = j >= j0 ? 0 : (j0 - j + ahead - 1) / ahead, t = j - j0 + back * ahead;
-            int at[4];
-#pragma unroll
-            for (int i = 0; i < 4; ++i) at[i] = !kPair ? row[i] : back == 0 ? row[i] : back == 1 ? before[0][i] : before[1][i];
-            const typename Ring::Place at_ring = places.at(j, kv);
-            const uint32_t st = kFp8 ? n % Sh::kRawDepth : at_ring.st;
-            if (kFp8 ? n >= (uint32_t)Sh::kRawDepth : at_ring.c >= (uint32_t)Ring::kPer)
-              ok = warp_wait(kFp8 ? sm.raw_empty[st] : sm.empty[st], kFp8 ? (n / Sh::kRawDepth - 1) & 1 : at_ring.ph ^ 1, abort);
-            if (!ok) break;
-            const uint32_t bar = smem_u32(kFp8 ? &sm.raw_full[st] : edge ? &sm.land[st] : &sm.full[st]);
-            const uint32_t to = kFp8 ? raw + st * Sh::kRaw : ring + st * Sh::kStage;
-            const CUtensorMap* map = kv ? &vmap : &kmap;
-            if (lane == 0) tc5::mbar_expect_tx(bar, kFp8 ? Sh::kRaw : Sh::kStage);
-            __syncwarp();
-            constexpr int kCopies = kFp8 ? 1 : Sh::kSubs;   // of a segment
-            if (per == 1) {
-#pragma unroll 1
-              for (int x0 = 0; x0 < segs * kCopies; x0 += 32) {
-                const int x = x0 + lane, s = x / kCopies, c = x % kCopies;
-                const int r = __shfl_sync(0xffffffffu, at[0], (t * segs + s) & 31);
-                if (x < segs * kCopies) tc5::tma_load_2d(to + s * seg * 128 + c * kSub, map, h * D + 64 * c, r, bar);
-              }
-            } else {
-#pragma unroll
-              for (int i = 0; i < 4; ++i)
-#pragma unroll
-                for (int c = 0; c < kCopies; ++c)
-                  if (i < per) tc5::tma_load_2d(to + (lane * per + i) * seg * 128 + c * kSub, map, h * D + 64 * c, at[i], bar);
-            }
-            ++n;
+        for (int t = 0; ok && t < nt; ++t, ++j) {
+          copy(t, false, false, j & 1, h, false);
+          if (!ok) break;
+          if (kPair) {                           // K0 K1 V0 K2 V1 ..: see TreeRing
+            if (j > 0) copy(t > 0 ? t - 1 : ahead - 1, t == 0, true, (j - 1) & 1, h, !kFp8 && edge_tile(a, sp, tile0 + t - 1));
+            if (ok && fresh && t + 1 == nt) copy(t, false, true, j & 1, h, !kFp8 && edge_tile(a, sp, tile0 + t));
+          } else {
+            copy(t, false, true, 0, h, !kFp8 && edge_tile(a, sp, tile0 + t));
           }
         }
-        j0 += nt;
       }
       // the copies have landed when the block ends, unless a wait gave up: their time is waited for
       if (*abort)
