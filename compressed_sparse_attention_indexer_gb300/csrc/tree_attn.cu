@@ -1,7 +1,7 @@
 // Attention of trees of drafted tokens over paged K / V pools on the fifth-
-// generation tensor cores, for requests whose drafts and heads make more query
-// rows per kv head than the warps' MMA takes at once (csa_tree_attn; see
-// launch_tree_attn for the rule).
+// generation tensor cores, for drafts and heads that make more query rows per kv
+// head than the warps' MMA takes at once, over enough requests or long ones
+// (csa_tree_attn; see launch_tree_attn for the rule).
 //   out[s][h] = sum_r softmax_r(scale q[s][h] . k[r]) v[r],  lse = ln sum_r exp(.)
 // over the rows before the drafts (the window's) and the drafts in s's mask.
 //
@@ -12,10 +12,11 @@
 //
 // One CTA per SM takes an even share of the list of tiles (paged_cuts).  Two
 // slots of tensor memory hold 128 x 128 scores each, over which their bf16 weights
-// are written, and 128 x D of output.  kRows = 256: a slot is a half of the query
-// rows, both take every tile.  kRows = 128: the slots take tiles in turn and are
-// joined at a piece's end.  Either way one slot's products run under the other's
-// softmax:
+// are written, and 128 x D of output.  A slot is a half of the query rows, both take
+// every tile, and one slot's products run under the other's softmax (with 128 query
+// rows or fewer the second slot passes the tiles on; slots that took tiles in turn
+// there were no faster: 768 and 776 us for 64 x 16 drafts, 67 and 66 for windows of
+// small heads).
 //   warps 0-3, 4-7   softmax of slot 0 and 1: a thread per query row, its 128 scores
 //                    in registers, so that maxima and sums need no exchange; the
 //                    reference maximum moves only when exceeded by 2^8 (the output is
@@ -49,7 +50,6 @@
 #include "paged.cuh"
 #include "ptx.cuh"
 #include "tc5.cuh"
-#include "tree_pipeline.h"
 
 namespace csa {
 
@@ -63,6 +63,7 @@ template <bool kFp8>
 constexpr int kRegsSoftmax = kFp8 ? 184 : 200;
 template <bool kFp8>
 constexpr int kRegsOthers = 256 - kRegsSoftmax<kFp8>;
+constexpr int kRows = 256;                 // query rows of a unit, two slots of 128
 constexpr int kTile = 128;                 // K / V rows per tile
 constexpr int kExtra = 2;                  // a unit's start and end, in tiles
 constexpr int kSub = kTile * 128;          // 128 rows x 64 dims bf16
@@ -75,17 +76,16 @@ struct TtSmem {
   uint64_t land[8];                        // bf16 V of an edge tile, before it was looked through
   uint64_t raw_full[3], raw_empty[3];      // chunks of E4M3 codes
   uint64_t s_full[2], p_full[2], o_full[2];
-  uint64_t q_full, q_empty, sc_full[kScaleTiles], pair, done[2];
+  uint64_t q_full, q_empty, sc_full[kScaleTiles], done[2];
   uint32_t tmem;
   int abort;
   PaCost scan[33];
   Cut cut[2];
   uint32_t bad[8][4];                      // per stage: V rows with a NaN or an infinity
   int looked[8];                           // warps that have looked through it, modulo 4
-  float ml[2][2][128];                     // per slot: maxima and sums, for the join of two slots
 };
 
-template <int D, int kRows, bool kFp8>
+template <int D, bool kFp8>
 struct TtShape {
   static constexpr int kSubs = D / 64;
   static constexpr int kStage = kSubs * kSub;
@@ -94,9 +94,9 @@ struct TtShape {
   static constexpr int kRaw = kFp8 ? kTile * D : 0;
   static constexpr int kScales = kFp8 ? kScaleTiles * kScaleBytes : 0;
   static constexpr int kRoom = (227 * 1024 - (int)sizeof(TtSmem) - kQBytes - kRawDepth * kRaw - kScales) / kStage;
-  static constexpr int kStages = kRoom > 8 ? 8 : kRows == 128 ? kRoom / 2 * 2 : kRoom;
+  static constexpr int kStages = kRoom > 8 ? 8 : kRoom;
   static constexpr int kSmem = kQBytes + kStages * kStage + kRawDepth * kRaw + kScales + (int)sizeof(TtSmem);
-  static_assert(kRows == 128 ? kStages % 2 == 0 && kStages >= 4 : kStages >= 3, "a batch's V and K");
+  static_assert(kStages >= 3, "a batch's V and K");
   // a tile's scales stay until its weights are made: its V then waits in the ring, so
   // that the tile being written is at most kStages / 2 + 1 tiles ahead
   static_assert(kStages / 2 + 1 < kScaleTiles, "scales");
@@ -300,14 +300,12 @@ __device__ __noinline__ void add_apart(const PagedArgs& a, int b, int h, int bas
   }
 }
 
-template <int D, int kRows, bool kFp8>
+template <int D, bool kFp8>
 __global__ void __launch_bounds__(kTtThreads, 1)
     tree_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__ CUtensorMap kmap,
                 const __grid_constant__ CUtensorMap vmap, const __grid_constant__ PagedArgs a, int rs, int seg, int chunks, int units, float* __restrict__ part, PaJoin* __restrict__ joins) {
-  using Sh = TtShape<D, kRows, kFp8>;
+  using Sh = TtShape<D, kFp8>;
   constexpr int ST = Sh::kStages;
-  constexpr bool kPair = kRows == 128;     // the slots share the query rows and take tiles in turn
-  using Ring = TreeRing<kPair, ST>;
   // (no static shared memory: the dynamic part starts on a 1024-byte boundary)
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   TtSmem& sm = *reinterpret_cast<TtSmem*>(smem_raw + Sh::kSmem - sizeof(TtSmem));
@@ -316,7 +314,7 @@ __global__ void __launch_bounds__(kTtThreads, 1)
   const uint32_t ring = qsm + Sh::kQBytes, raw = ring + ST * Sh::kStage, scales = raw + Sh::kRawDepth * Sh::kRaw;
   volatile int* abort = &sm.abort;
   const int group = a.heads / a.kv_heads, qrows = a.S * group;
-  const int unit_rows = kPair ? rs : 2 * rs;     // query rows of a unit, rs of them in a slot
+  const int unit_rows = 2 * rs;            // query rows of a unit, rs of them in a slot
   pdl_wait();
   pdl_trigger();
 
@@ -343,7 +341,7 @@ __global__ void __launch_bounds__(kTtThreads, 1)
     sm.abort = 0;
     for (int i = 0; i < 8; ++i) {
       tc5::mbar_init(smem_u32(&sm.full[i]), kFp8 ? kRowWarps : 1);
-      tc5::mbar_init(smem_u32(&sm.empty[i]), kPair ? 1 : 2);   // the slots that read a stage
+      tc5::mbar_init(smem_u32(&sm.empty[i]), 2);   // the slots
       tc5::mbar_init(smem_u32(&sm.land[i]), 1);
       sm.looked[i] = 0;
     }
@@ -359,7 +357,6 @@ __global__ void __launch_bounds__(kTtThreads, 1)
     }
     tc5::mbar_init(smem_u32(&sm.q_full), 1);
     tc5::mbar_init(smem_u32(&sm.q_empty), 2);
-    tc5::mbar_init(smem_u32(&sm.pair), 256);
     for (int i = 0; i < 2; ++i) tc5::mbar_init(smem_u32(&sm.done[i]), 1);
     tc5::fence_mbar_init();
   }
@@ -383,23 +380,21 @@ __global__ void __launch_bounds__(kTtThreads, 1)
     const uint32_t s_at = tmem + lanes + slot * 128, o_at = tmem + lanes + 256 + slot * 128;
     const float scale2 = a.scale * kLog2e;
     const int words32 = 2 * a.words;
-    uint32_t n_s = 0, n_o = 0, n_pair = 0;     // phases of s_full, o_full and pair
+    uint32_t n_s = 0, n_o = 0;                  // phases of s_full and o_full
     int jj = 0, seen_pieces = 0;                // tiles and pieces of the CTA before this piece
-    Ring places;
-    places.start();
     Walk walk;
     walk.init(a, sm.cut);
     Piece pc;
     bool ok = true;
     while (ok && walk.next(a, units, pc)) {
       const int h = chunks == 1 ? pc.unit : pc.unit / chunks, row0 = (pc.unit - h * chunks) * unit_rows;
-      const int i = t < rs ? row0 + (kPair ? 0 : slot * rs) + t : qrows;   // (qrows: no row)
+      const int i = t < rs ? row0 + slot * rs + t : qrows;   // (qrows: no row)
       const int s = i < qrows ? token_of(i) : 0, hd = h * group + i - s * group;
       const int64_t tok = (int64_t)pc.b * a.S + s;
       __nv_bfloat16* out = static_cast<__nv_bfloat16*>(a.out) + tok * a.out_stride + hd * D;
       const int at_piece = seen_pieces++;
       if (pc.sp.L <= 0) {                      // a padding request
-        if (i < qrows && !(kPair && slot == 1)) {
+        if (i < qrows) {
           for (int c = 0; c < D; c += 8) *reinterpret_cast<uint4*>(out + c) = make_uint4(0, 0, 0, 0);
           if (a.lse) a.lse[tok * a.heads + hd] = -INFINITY;
         }
@@ -407,7 +402,7 @@ __global__ void __launch_bounds__(kTtThreads, 1)
       }
       const int p_first = pc.sp.L - pc.sp.n;
       const bool real = i < qrows && s < pc.sp.n;
-      const bool busy = kPair ? pc.nt > slot : row0 + slot * rs < qrows;   // the slot has tiles in this piece
+      const bool busy = row0 + slot * rs < qrows;   // the slot has rows
       float m = -INFINITY, l = 0.f;
       if (busy) {
         const int outside = real ? tree_outside(a, pc.b, s, p_first, pc.sp.n) : 0;
@@ -419,7 +414,7 @@ __global__ void __launch_bounds__(kTtThreads, 1)
 #pragma unroll
           for (int c = 0; c < D; c += 32) tc5::tmem_st32(o_at + c, z);
         }
-        for (int j = kPair ? slot : 0; j < pc.nt; j += kPair ? 2 : 1) {
+        for (int j = 0; j < pc.nt; ++j) {
           const int base = (pc.sp.t0 + pc.tile + j) * kTile;
           const bool edge = edge_tile(a, pc.sp, pc.tile + j);
           ok = warp_wait(sm.s_full[slot], n_s & 1, abort);
@@ -499,14 +494,12 @@ __global__ void __launch_bounds__(kTtThreads, 1)
           }
           tc5::tmem_wait_st();
           if (edge) {
-            Ring now = places;
-            if (!kPair) now.base[0] = 2 * jj;    // (one register less to keep)
-            const typename Ring::Place v = now.at(j, true);
-            ok = warp_wait(sm.full[v.st], v.ph, abort);
+            const uint32_t v = 2 * (jj + j) + 1, st = v % ST;   // V's place in the ring
+            ok = warp_wait(sm.full[st], (v / ST) & 1, abort);
             if (!ok) break;
             uint32_t bad[4];
 #pragma unroll
-            for (int w = 0; w < 4; ++w) bad[w] = *(volatile uint32_t*)&sm.bad[v.st][w];
+            for (int w = 0; w < 4; ++w) bad[w] = *(volatile uint32_t*)&sm.bad[st][w];
             if (bad[0] | bad[1] | bad[2] | bad[3]) add_apart<D, kFp8>(a, pc.b, h, base, bad, seen, s_at, o_at);
           }
           tc5::fence_before_sync();
@@ -520,59 +513,7 @@ __global__ void __launch_bounds__(kTtThreads, 1)
         }
       }
       jj += pc.nt;
-      if (kPair) places.after(pc.nt);
-      if (kPair) {
-        // the two slots' states of a query row are joined: either warpgroup takes
-        // half of the dims
-        sm.ml[slot][0][t] = m;
-        sm.ml[slot][1][t] = l;
-        tc5::fence_before_sync();
-        ok = __all_sync(0xffffffffu, tc5::bar_bounded(smem_u32(&sm.pair), n_pair, abort)) && ok;
-        tc5::fence_after_sync();
-        if (!ok) break;
-        const float m0 = sm.ml[0][0][t], m1 = sm.ml[1][0][t];
-        const float top = fmaxf(m0, m1), ref = top == -INFINITY ? 0.f : top;
-        const float f0 = exp2f(m0 - ref), f1 = exp2f(m1 - ref);
-        l = sm.ml[0][1][t] * f0 + (pc.nt > 1 ? sm.ml[1][1][t] * f1 : 0.f);
-        m = top;
-        const bool any = real && (l > 0.f || l != l);
-        const float inv = any ? 1.f / l : 0.f;
-        const int64_t pslot = (int64_t)blockIdx.x * 2 + (at_piece == 0 ? 0 : 1);
-        float* dst = part + (pslot * kRows + (t & ~31)) * (D + 2) + lane;
-#pragma unroll 1
-        for (int c = slot * (D / 2); c < (slot + 1) * (D / 2); c += 32) {
-          float o[32];
-          tc5::tmem_ld32(tmem + lanes + 256 + c, o);
-          if (pc.nt > 1) {
-            float o1[32];
-            tc5::tmem_ld32(tmem + lanes + 384 + c, o1);
-#pragma unroll
-            for (int e = 0; e < 32; ++e) o[e] = o[e] * f0 + o1[e] * f1;
-          }
-          if (i < qrows) {
-            if (pc.whole) {
-#pragma unroll
-              for (int e = 0; e < 32; e += 8) {
-                uint32_t w[4];
-#pragma unroll
-                for (int x = 0; x < 4; ++x) w[x] = any ? pack_bf16x2(o[e + 2 * x] * inv, o[e + 2 * x + 1] * inv) : 0u;
-                *reinterpret_cast<uint4*>(out + c + e) = make_uint4(w[0], w[1], w[2], w[3]);
-              }
-            } else {
-#pragma unroll
-              for (int e = 0; e < 32; ++e) dst[(c + e) * 32] = o[e];
-            }
-          }
-        }
-        if (i < qrows && slot == 0) {
-          if (!pc.whole) dst[D * 32] = m, dst[(D + 1) * 32] = l;
-          else if (a.lse) a.lse[tok * a.heads + hd] = any ? (m + log2f(l)) * kLn2 : -INFINITY;
-        }
-        // neither slot is written again before both were read
-        tc5::fence_before_sync();
-        ok = __all_sync(0xffffffffu, tc5::bar_bounded(smem_u32(&sm.pair), n_pair, abort));
-        tc5::fence_after_sync();
-      } else if (busy && ok) {
+      if (busy && ok) {
         const bool any = real && (l > 0.f || l != l);
         const float inv = any ? 1.f / l : 0.f;
         const int64_t pslot = (int64_t)blockIdx.x * 2 + (at_piece == 0 ? 0 : 1);
@@ -607,16 +548,15 @@ __global__ void __launch_bounds__(kTtThreads, 1)
     if (warp < kMmaWarp) {
       // ---------------------------------------------------------- converters, or V's readers
       const int w = warp - kRowWarp;
-      constexpr int kRowBytes = D * (kFp8 ? 1 : 2), kSpan = kRowBytes / 16, kAtOnce = 32 / kSpan, kIter = 32 / kAtOnce;
-      const int ch = lane % kSpan, r0 = lane / kSpan;
-      // where this thread's piece i of a chunk lies in a stage
-      auto place = [&](int i) {
-        const int row = w * 32 + i * kAtOnce + r0;
-        const int c0 = kFp8 ? 2 * ch : ch;
-        return (uint32_t)((c0 >> 3) * kSub + row * 128 + (((c0 & 7) ^ (row & 7)) << 4));
-      };
       bool ok = true;
       if constexpr (kFp8) {
+        constexpr int kSpan = D / 16, kAtOnce = 32 / kSpan, kIter = 32 / kAtOnce;   // 16 codes of a row each
+        const int ch = lane % kSpan, r0 = lane / kSpan;
+        // where this thread's piece i of a chunk lies in a stage
+        auto place = [&](int i) {
+          const int row = w * 32 + i * kAtOnce + r0, c0 = 2 * ch;
+          return (uint32_t)((c0 >> 3) * kSub + row * 128 + (((c0 & 7) ^ (row & 7)) << 4));
+        };
         // the lane's row of the tile: its scales are fetched a tile ahead, its place two
         Cursor<kTile, true> at;
         int left;
@@ -735,60 +675,39 @@ __global__ void __launch_bounds__(kTtThreads, 1)
               }
               ++n;
         };
-        if constexpr (kPair) {
-          Walk walk;
-          walk.init(a, sm.cut);
-          Piece pc;
-          Ring places;
-          places.start();
-          uint32_t tiles = 0;                  // before the piece
-          while (ok && walk.next(a, units, pc)) {
-            if (pc.sp.L <= 0) continue;
+        // (K and V of tile after tile: pieces do not matter, which leaves registers)
+        uint32_t st = 0, ph = 1;
+        for (uint32_t tile = 0; ok && some; ++tile) {
+          const bool edge_now = edge;
+          const uint32_t rows_now = rows;
 #pragma unroll 1
-            for (int x = 0; ok && x < 2 * pc.nt; ++x) {
-              bool kv;
-              const int j = Ring::tile_of(x, pc.nt, kv);
-              const typename Ring::Place to = places.at(j, kv);
-              convert(to.st, to.c >= Ring::kPer, to.ph ^ 1, kv, tiles + j, kv && edge_tile(a, pc.sp, pc.tile + j),
-                      span_rows(pc.sp, pc.tile + j, w));
-              if (!kv) {
-                fetch();
-                ahead();
-              }
-            }
-            tiles += pc.nt;
-            places.after(pc.nt);
-          }
-        } else {
-          // (K and V of tile after tile: pieces do not matter, which leaves registers)
-          uint32_t st = 0, ph = 1;
-          for (uint32_t tile = 0; ok && some; ++tile) {
-            const bool edge_now = edge;
-            const uint32_t rows_now = rows;
-#pragma unroll 1
-            for (int kv = 0; ok && kv < 2; ++kv) {
-              convert(st, n >= ST, ph, kv, tile, kv && edge_now, rows_now);
-              if (++st == ST) st = 0, ph ^= 1;
-              if (!kv) {
-                fetch();
-                ahead();
-              }
+          for (int kv = 0; ok && kv < 2; ++kv) {
+            convert(st, n >= ST, ph, kv, tile, kv && edge_now, rows_now);
+            if (++st == ST) st = 0, ph ^= 1;
+            if (!kv) {
+              fetch();
+              ahead();
             }
           }
         }
       } else {
-        uint32_t parity = 0;                   // bit st: phase of land[st]
+        constexpr int kSpan = D / 8, kAtOnce = 32 / kSpan, kIter = 32 / kAtOnce;   // 16 bytes of a row each
+        const int ch = lane % kSpan, r0 = lane / kSpan;
+        // where this thread's piece i of a chunk lies in a stage
+        auto place = [&](int i) {
+          const int row = w * 32 + i * kAtOnce + r0;
+          return (uint32_t)((ch >> 3) * kSub + row * 128 + (((ch & 7) ^ (row & 7)) << 4));
+        };
+        uint32_t parity = 0, jj = 0;           // bit st: phase of land[st]; tiles before the piece
         Walk walk;
         walk.init(a, sm.cut);
         Piece pc;
-        Ring places;
-        places.start();
         while (ok && walk.next(a, units, pc)) {
           if (pc.sp.L <= 0) continue;
 #pragma unroll 1
           for (int j = 0; j < pc.nt; ++j) {
             if (edge_tile(a, pc.sp, pc.tile + j)) {
-              const uint32_t st = places.at(j, true).st, stage = ring + st * Sh::kStage;
+              const uint32_t st = (2 * (jj + j) + 1) % ST, stage = ring + st * Sh::kStage;
               ok = warp_wait(sm.land[st], (parity >> st) & 1, abort);
               parity ^= 1u << st;
               if (!ok) break;
@@ -822,7 +741,7 @@ __global__ void __launch_bounds__(kTtThreads, 1)
               }
             }
           }
-          places.after(pc.nt);
+          jj += pc.nt;
         }
       }
     } else if (warp == kLoadWarp) {
@@ -841,9 +760,7 @@ __global__ void __launch_bounds__(kTtThreads, 1)
       Piece next;                              // the block looked up: the first tiles of what is left of a piece
       bool more = false;
       Spot spot[4];
-      // pool rows of the block's segments, and of the block's before (V follows its K by a tile
-      // where slots take turns)
-      int row[4] = {none, none, none, none}, before[4];
+      int row[4] = {none, none, none, none};   // pool rows of the block's segments
       auto look = [&] {
         while ((more = walk.next(a, units, next)) && next.sp.L <= 0) {
         }
@@ -857,20 +774,17 @@ __global__ void __launch_bounds__(kTtThreads, 1)
             spot[i].lookup(a, next.sp, next.b, next.tile + x / segs, x % segs * seg, seg);
         }
       };
-      // the places in the rings, or of E4M3 codes beside them: counted up
-      uint32_t st[2] = {0, 0}, ph[2] = {1, 1};  // stage within the ring, its phase before
-      bool wait_for[2] = {false, false};        // the ring has come round
-      constexpr uint32_t kPlaces = kFp8 ? Sh::kRawDepth : Ring::kPer;
+      // the place in the ring, or of E4M3 codes beside it: counted up
+      uint32_t at = 0, ph = 1;                 // its phase before
+      bool again = false;                      // the ring has come round
+      constexpr uint32_t kPlaces = kFp8 ? Sh::kRawDepth : ST;
       bool ok = true;
       constexpr int kCopies = kFp8 ? 1 : Sh::kSubs;   // of a segment
       const int copies = segs * kCopies;
       const uint32_t to_lane = lane / kCopies * seg * 128 + lane % kCopies * kSub;
-      // tile t of the block (was: of the block before): its K or V, into the slot's ring
-      auto copy = [&](int t, bool was, bool v, int slot, int h, bool edge) {
-        const int ring_of = kPair && !kFp8 ? slot : 0;
-        const uint32_t s0 = ring_of ? st[1] : st[0], p0 = ring_of ? ph[1] : ph[0];
-        const uint32_t at = kFp8 ? s0 : s0 + (kPair ? slot * Ring::kPer : 0);
-        if (ring_of ? wait_for[1] : wait_for[0]) ok = warp_wait(kFp8 ? sm.raw_empty[at] : sm.empty[at], p0, abort);
+      // tile t of the block: its K or V
+      auto copy = [&](int t, bool v, int h, bool edge) {
+        if (again) ok = warp_wait(kFp8 ? sm.raw_empty[at] : sm.empty[at], ph, abort);
         if (!ok) return;
         const uint32_t bar = smem_u32(kFp8 ? &sm.raw_full[at] : edge ? &sm.land[at] : &sm.full[at]);
         const uint32_t to = kFp8 ? raw + at * Sh::kRaw : ring + at * Sh::kStage;
@@ -878,11 +792,10 @@ __global__ void __launch_bounds__(kTtThreads, 1)
         if (lane == 0) tc5::mbar_expect_tx(bar, kFp8 ? Sh::kRaw : Sh::kStage);
         __syncwarp();
         if (per == 1) {
-          const int mine = was ? before[0] : row[0];
-          const int r = __shfl_sync(0xffffffffu, mine, (t * segs + lane / kCopies) & 31);
+          const int r = __shfl_sync(0xffffffffu, row[0], (t * segs + lane / kCopies) & 31);
           if (lane < copies) tc5::tma_load_2d(to + to_lane, map, h * D + 64 * (lane % kCopies), r, bar);
           if (copies > 32) {                     // 32 segments in two copies
-            const int r2 = __shfl_sync(0xffffffffu, mine, 32 / kCopies + lane / kCopies);
+            const int r2 = __shfl_sync(0xffffffffu, row[0], 32 / kCopies + lane / kCopies);
             tc5::tma_load_2d(to + to_lane + 32 / kCopies * seg * 128, map, h * D + 64 * (lane % kCopies), r2, bar);
           }
         } else {
@@ -890,45 +803,29 @@ __global__ void __launch_bounds__(kTtThreads, 1)
           for (int i = 0; i < 4; ++i)
 #pragma unroll
             for (int c = 0; c < kCopies; ++c)
-              if (i < per) tc5::tma_load_2d(to + (lane * per + i) * seg * 128 + c * kSub, map, h * D + 64 * c, was ? before[i] : row[i], bar);
+              if (i < per) tc5::tma_load_2d(to + (lane * per + i) * seg * 128 + c * kSub, map, h * D + 64 * c, row[i], bar);
         }
-        const bool round = s0 + 1 == kPlaces;
-        if (ring_of) {
-          st[1] = round ? 0 : s0 + 1, ph[1] ^= round, wait_for[1] |= round;
-        } else {
-          st[0] = round ? 0 : s0 + 1, ph[0] ^= round, wait_for[0] |= round;
-        }
+        if (++at == kPlaces) at = 0, ph ^= 1, again = true;
       };
       look();
       lookup();
-      bool fresh = true;
-      int j = 0;                                 // the block's first tile in its piece
       while (ok && more) {
         const Span<kTile, true> sp = next.sp;
         const int nt = min(ahead, next.nt), h = chunks == 1 ? next.unit : next.unit / chunks, tile0 = next.tile;
         bool all = true;
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          before[i] = row[i];
           all &= spot[i].resolve(a, none, row[i]);
         }
         if (!all && a.status) set_status(a.status, kStatusBadIndex);
-        if (fresh) j = 0;
         next.tile += nt;
         next.nt -= nt;
-        fresh = next.nt == 0;                    // the piece's last block
-        if (fresh) look();
+        if (next.nt == 0) look();
         lookup();
 #pragma unroll 1
-        for (int t = 0; ok && t < nt; ++t, ++j) {
-          copy(t, false, false, j & 1, h, false);
-          if (!ok) break;
-          if (kPair) {                           // K0 K1 V0 K2 V1 ..: see TreeRing
-            if (j > 0) copy(t > 0 ? t - 1 : ahead - 1, t == 0, true, (j - 1) & 1, h, !kFp8 && edge_tile(a, sp, tile0 + t - 1));
-            if (ok && fresh && t + 1 == nt) copy(t, false, true, j & 1, h, !kFp8 && edge_tile(a, sp, tile0 + t));
-          } else {
-            copy(t, false, true, 0, h, !kFp8 && edge_tile(a, sp, tile0 + t));
-          }
+        for (int t = 0; ok && t < nt; ++t) {
+          copy(t, false, h, false);
+          if (ok) copy(t, true, h, !kFp8 && edge_tile(a, sp, tile0 + t));
         }
       }
       // the copies have landed when the block ends, unless a wait gave up: their time is waited for
@@ -942,7 +839,7 @@ __global__ void __launch_bounds__(kTtThreads, 1)
       const int slot = __shfl_sync(0xffffffffu, warp, 0) == kMmaWarp ? 0 : 1;
       constexpr uint32_t idesc_s = tc5::idesc_bf16_f32(128, kTile);
       constexpr uint32_t idesc_o = tc5::idesc_bf16_f32(128, D) | (1u << 16);   // B MN-major
-      const uint64_t dq = tc5::sdesc_k_sw128(qsm + (kPair ? 0 : slot * Sh::kStage));
+      const uint64_t dq = tc5::sdesc_k_sw128(qsm + slot * Sh::kStage);
       const uint64_t dk = tc5::sdesc_k_sw128(ring), dv = sdesc_mn_sw128(ring, kSub);
       const uint32_t s_at = tmem + slot * 128, o_at = tmem + 256 + slot * 128;
       uint32_t pph = 0, qph = 0;               // phases
@@ -958,83 +855,76 @@ __global__ void __launch_bounds__(kTtThreads, 1)
         ok = __all_sync(0xffffffffu, ok);
         tc5::fence_after_sync();
       };
-      Ring places;
-      places.start();
-      // a slot's K or V, moved on to its next tile's
+      // K or V in the ring, moved on to its next tile's
       struct Next {
         uint32_t st, ph;
-        __device__ __forceinline__ void set(const typename Ring::Place& p, int slot) { st = p.st - (kPair ? slot * Ring::kPer : 0), ph = p.ph; }
-        __device__ __forceinline__ void move() {
-          st += 2;
-          if (st >= Ring::kPer) st -= Ring::kPer, ph ^= 1;
+        __device__ __forceinline__ void set(uint32_t place) { st = place % ST, ph = (place / ST) & 1; }
+        __device__ __forceinline__ void move(uint32_t by = 2) {
+          st += by;
+          if (st >= ST) st -= ST, ph ^= 1;
         }
       };
-      uint64_t* const full = sm.full + (kPair ? slot * Ring::kPer : 0);
-      uint64_t* const empty = sm.empty + (kPair ? slot * Ring::kPer : 0);
-      const uint32_t stages = kPair ? slot * Ring::kPer * Sh::kStage : 0;   // the slot's ring
+      uint32_t jj = 0;                         // tiles before the piece
       Walk walk;
       walk.init(a, sm.cut);
       Piece pc;
       while (ok && walk.next(a, units, pc)) {
         if (pc.sp.L <= 0) continue;
         const int h = chunks == 1 ? pc.unit : pc.unit / chunks, row0 = (pc.unit - h * chunks) * unit_rows;
-        const bool busy = kPair ? pc.nt > slot : row0 + slot * rs < qrows;
-        if (!busy) {
-          // no rows or tiles for this slot: what it would have read is given back
-          if (!kPair) {
+        if (row0 + slot * rs >= qrows) {
+          // no rows for this slot: what it would have read is given back
+          Next c;
+          c.set(2 * jj);
 #pragma unroll 1
-            for (int i = 0; ok && i < 2 * pc.nt; ++i) {
-              const typename Ring::Place c = places.at(i >> 1, i & 1);
-              wait(full[c.st], c.ph);
-              if (ok && elect_one()) tc5::mbar_arrive(smem_u32(&empty[c.st]));
-            }
+          for (int i = 0; ok && i < 2 * pc.nt; ++i, c.move(1)) {
+            wait(sm.full[c.st], c.ph);
+            if (ok && elect_one()) tc5::mbar_arrive(smem_u32(&sm.empty[c.st]));
           }
           wait(sm.q_full, qph);
           if (ok && elect_one()) tc5::mbar_arrive(smem_u32(&sm.q_empty));
         } else {
           Next k, v;
-          k.set(places.at(kPair ? slot : 0, false), slot);
-          v.set(places.at(kPair ? slot : 0, true), slot);
+          k.set(2 * jj);
+          v.set(2 * jj + 1);
           wait(sm.q_full, qph);
           // a batch: with tile j's weights the output, then the scores of the slot's next
           // tile, 16 MMAs without anything between them
-          const int first = kPair ? slot : 0, step = kPair ? 2 : 1;
 #pragma unroll 1
-          for (int j = first - step; j < pc.nt; j += step) {
-            const bool out = j >= first, in = j + step < pc.nt;
-            if (in) wait(full[k.st], k.ph);
+          for (int j = -1; j < pc.nt; ++j) {
+            const bool out = j >= 0, in = j + 1 < pc.nt;
+            if (in) wait(sm.full[k.st], k.ph);
             if (out) {
-              wait(full[v.st], v.ph);
+              wait(sm.full[v.st], v.ph);
               wait(sm.p_full[slot], pph);
               pph ^= 1;
             }
             if (!ok) break;
             if (elect_one()) {
               if (out) {
-                const uint64_t d = dv + ((stages + v.st * Sh::kStage) >> 4);
+                const uint64_t d = dv + ((v.st * Sh::kStage) >> 4);
 #pragma unroll
                 for (int x = 0; x < kTile / 16; ++x) tc5::mma_bf16_ta(o_at, s_at + 8 * x, d + ((x * 2048) >> 4), idesc_o, 1u);
               }
               if (in) {
-                const uint64_t d = dk + ((stages + k.st * Sh::kStage) >> 4);
+                const uint64_t d = dk + ((k.st * Sh::kStage) >> 4);
 #pragma unroll
                 for (int x = 0; x < D / 16; ++x)
                   tc5::mma_bf16(s_at, dq + (((x >> 2) * kSub + (x & 3) * 32) >> 4), d + (((x >> 2) * kSub + (x & 3) * 32) >> 4),
                                 idesc_s, x > 0);
                 tc5::mma_commit(smem_u32(&sm.s_full[slot]));
-                tc5::mma_commit(smem_u32(&empty[k.st]));
-                if (j + 2 * step >= pc.nt) tc5::mma_commit(smem_u32(&sm.q_empty));
+                tc5::mma_commit(smem_u32(&sm.empty[k.st]));
+                if (j + 2 >= pc.nt) tc5::mma_commit(smem_u32(&sm.q_empty));
               } else {
                 tc5::mma_commit(smem_u32(&sm.o_full[slot]));
               }
-              if (out) tc5::mma_commit(smem_u32(&empty[v.st]));
+              if (out) tc5::mma_commit(smem_u32(&sm.empty[v.st]));
             }
             if (in) k.move();
             if (out) v.move();
           }
         }
         qph ^= 1;
-        places.after(pc.nt);
+        jj += pc.nt;
       }
       if (elect_one()) tc5::mma_commit(smem_u32(&sm.done[slot]));
       tc5::mbar_wait_drain(smem_u32(&sm.done[slot]), 0);
@@ -1053,7 +943,7 @@ __global__ void __launch_bounds__(kTtThreads, 1)
         if (n_q > 0) ok = warp_wait(sm.q_empty, (n_q - 1) & 1, abort);
         if (!ok) break;
         // whole tokens' heads: 128 / group tokens to a slot
-        const int slots = !kPair && row0 + rs < qrows ? 2 : 1, tokens = rs / group;
+        const int slots = row0 + rs < qrows ? 2 : 1, tokens = rs / group;
         if (lane == 0) {
           tc5::mbar_expect_tx(smem_u32(&sm.q_full), slots * Sh::kSubs * rs * 128);
           for (int x = 0; x < slots * Sh::kSubs; ++x)
@@ -1073,45 +963,69 @@ __global__ void __launch_bounds__(kTtThreads, 1)
   if (tid == 0 && sm.abort && a.status) set_status(a.status, kStatusTimeout);
 }
 
-// Joins the pieces of the units cut between CTAs: block (x, y) does query rows
-// 32 y .. of the unit that starts in CTA x, a thread a row and D / 8 dims.
+// Joins the pieces of the units cut between CTAs: block (x, y, z) does query rows
+// 32 y .. of the unit that starts in CTA x and dims 64 z .., a thread a row and eight dims.
+// The largest of the pieces' maxima first, then their sums: a piece's loads wait for
+// nothing of the piece before, four pieces' are under way (a running maximum took 1 us a
+// piece: 52 us for a request of 8000 rows in 38 pieces).
+constexpr int kJoinThreads = 256;
 template <int D>
-__global__ void __launch_bounds__(256)
-    tree_join_kernel(const PagedArgs a, int rs, int chunks, int rows, const float* __restrict__ part, const PaJoin* __restrict__ joins) {
+__global__ void __launch_bounds__(kJoinThreads)
+    tree_join_kernel(const PagedArgs a, int rs, int chunks, const float* __restrict__ part, const PaJoin* __restrict__ joins) {
+  constexpr int kDims = 8;
   pdl_wait();
   pdl_trigger();
   const PaJoin j = joins[blockIdx.x];
   if (j.count == 0) return;
-  const int lane = threadIdx.x & 31, c0 = (threadIdx.x >> 5) * (D / 8);
+  const int lane = threadIdx.x & 31, c0 = blockIdx.z * 64 + (threadIdx.x >> 5) * kDims;
   const int group = a.heads / a.kv_heads, h = j.unit / chunks, r0 = blockIdx.y * 32;
-  const int t = (r0 & 127) + lane, i = ((j.unit - h * chunks) * (rows / 128) + (r0 >> 7)) * rs + t;
+  const int t = (r0 & 127) + lane, i = ((j.unit - h * chunks) * (kRows / 128) + (r0 >> 7)) * rs + t;
   if (t >= rs || i >= a.S * group) return;
-  float m = -INFINITY, l = 0.f, acc[D / 8];
-#pragma unroll
-  for (int x = 0; x < D / 8; ++x) acc[x] = 0.f;
-  for (int p = 0; p < j.count; ++p) {
+  // piece p: the first is what its CTA has last (or alone), the others what theirs have first
+  auto piece = [&](int p) {
     const int64_t slot = p == 0 ? (int64_t)blockIdx.x * 2 + j.slot : (int64_t)(blockIdx.x + p) * 2;
-    const float* src = part + (slot * rows + r0) * (D + 2) + lane;
-    const float m2 = src[D * 32], l2 = src[(D + 1) * 32];
-    const float top = fmaxf(m, m2), ref = top == -INFINITY ? 0.f : top;
-    const float f1 = exp2f(m - ref), f2 = exp2f(m2 - ref);
-    l = l * f1 + l2 * f2;
-    m = top;
+    return part + (slot * kRows + r0) * (D + 2) + lane;
+  };
+  float m = -INFINITY;
+  for (int p0 = 0; p0 < j.count; p0 += 8) {
+    float v[8];
 #pragma unroll
-    for (int x = 0; x < D / 8; ++x) acc[x] = acc[x] * f1 + src[(c0 + x) * 32] * f2;
+    for (int p = 0; p < 8; ++p) v[p] = p0 + p < j.count ? piece(p0 + p)[D * 32] : -INFINITY;
+#pragma unroll
+    for (int p = 0; p < 8; ++p) m = fmaxf(m, v[p]);
+  }
+  const float ref = m == -INFINITY ? 0.f : m;
+  float l = 0.f, acc[kDims];
+#pragma unroll
+  for (int x = 0; x < kDims; ++x) acc[x] = 0.f;
+  for (int p0 = 0; p0 < j.count; p0 += 4) {
+    float v[4][kDims + 2];
+#pragma unroll
+    for (int p = 0; p < 4; ++p) {
+      const float* src = piece(min(p0 + p, j.count - 1));
+#pragma unroll
+      for (int x = 0; x < kDims; ++x) v[p][x] = src[(c0 + x) * 32];
+      v[p][kDims] = src[D * 32];
+      v[p][kDims + 1] = src[(D + 1) * 32];
+    }
+#pragma unroll
+    for (int p = 0; p < 4; ++p) {
+      if (p0 + p >= j.count) break;
+      const float f = exp2f(v[p][kDims] - ref);
+      l += v[p][kDims + 1] * f;
+#pragma unroll
+      for (int x = 0; x < kDims; ++x) acc[x] += v[p][x] * f;
+    }
   }
   const int s = i / group, hd = h * group + i - s * group;
   const int64_t tok = (int64_t)j.b * a.S + s;
   const bool any = (l > 0.f || l != l) && (!a.count || s < a.count[j.b]);
   const float inv = any ? 1.f / l : 0.f;
   __nv_bfloat16* out = static_cast<__nv_bfloat16*>(a.out) + tok * a.out_stride + hd * D + c0;
+  uint32_t w[4];
 #pragma unroll
-  for (int x = 0; x < D / 8; x += 8) {
-    uint32_t w[4];
-#pragma unroll
-    for (int e = 0; e < 4; ++e) w[e] = any ? pack_bf16x2(acc[x + 2 * e] * inv, acc[x + 2 * e + 1] * inv) : 0u;
-    *reinterpret_cast<uint4*>(out + x) = make_uint4(w[0], w[1], w[2], w[3]);
-  }
+  for (int e = 0; e < 4; ++e) w[e] = any ? pack_bf16x2(acc[2 * e] * inv, acc[2 * e + 1] * inv) : 0u;
+  *reinterpret_cast<uint4*>(out) = make_uint4(w[0], w[1], w[2], w[3]);
   if (a.lse && c0 == 0) a.lse[tok * a.heads + hd] = any ? (m + log2f(l)) * kLn2 : -INFINITY;
 }
 
@@ -1142,10 +1056,10 @@ bool make_query_map(CUtensorMap* m, const PagedArgs& a, int group, int tokens) {
             CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_128B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <int D, int kRows, bool kFp8>
+template <int D, bool kFp8>
 int launch_rows(const PagedArgs& a, int num_sms, cudaStream_t st, bool pdl) {
-  using Sh = TtShape<D, kRows, kFp8>;
-  auto kern = tree_kernel<D, kRows, kFp8>;
+  using Sh = TtShape<D, kFp8>;
+  auto kern = tree_kernel<D, kFp8>;
   static PerDeviceOnce attr;
   if (const cudaError_t e = attr.run([&] {
         // the warpgroups' shares of the registers must add up to what the launch brings
@@ -1163,7 +1077,7 @@ int launch_rows(const PagedArgs& a, int num_sms, cudaStream_t st, bool pdl) {
       !make_pool_map(&vmap, a.v, a.rows, (uint64_t)a.kv_heads * D, a.v_step, kFp8, D, seg))
     return launch_fail("cuTensorMapEncodeTiled(K / V pools)", cudaErrorInvalidValue);
   const int group = a.heads / a.kv_heads, qrows = a.S * group, rs = 128 / group * group;
-  const int unit_rows = kRows / 128 * rs, chunks = (qrows + unit_rows - 1) / unit_rows;
+  const int unit_rows = 2 * rs, chunks = (qrows + unit_rows - 1) / unit_rows;
   CUtensorMap qmap;
   if (!make_query_map(&qmap, a, group, rs / group)) return launch_fail("cuTensorMapEncodeTiled(q)", cudaErrorInvalidValue);
   float* part = static_cast<float*>(a.workspace);
@@ -1173,7 +1087,7 @@ int launch_rows(const PagedArgs& a, int num_sms, cudaStream_t st, bool pdl) {
   const int r = launch_kernel(kern, dim3(grid), dim3(kTtThreads), Sh::kSmem, st, pdl, qmap, kmap, vmap, a, rs, seg, chunks, a.kv_heads * chunks, part, joins);
   if (r < 0) return r;
   const int most = qrows < rs ? qrows : kRows;
-  const int r2 = launch_kernel(tree_join_kernel<D>, dim3(grid, (most + 31) / 32), dim3(256), 0, st, pdl, a, rs, chunks, kRows,
+  const int r2 = launch_kernel(tree_join_kernel<D>, dim3(grid, (most + 31) / 32, D / 64), dim3(kJoinThreads), 0, st, pdl, a, rs, chunks,
                                (const float*)part, (const PaJoin*)joins);
   return r2 < 0 ? r2 : r + r2;
 }
@@ -1189,14 +1103,28 @@ size_t tree_attn_workspace(int dim, int num_sms) {
 }
 
 int launch_tree_attn(const PagedArgs& a, bool fp8, int num_sms, cudaStream_t st, bool pdl) {
-  const int qrows = a.S * (a.heads / a.kv_heads);
-  const int group = a.heads / a.kv_heads;
+  const int group = a.heads / a.kv_heads, qrows = a.S * group;
   // a slot takes whole tokens' heads; a token coordinate is an int
-  if (a.dim == 256 || qrows <= 32 || group > 128 || (int64_t)a.B * a.S > 0x7fffffff) return launch_paged_attn(a, fp8, num_sms, st, pdl);
-  const bool two = qrows > 128 / group * group;
-  if (fp8) return two ? launch_rows<128, 256, true>(a, num_sms, st, pdl) : launch_rows<128, 128, true>(a, num_sms, st, pdl);
-  if (a.dim == 64) return two ? launch_rows<64, 256, false>(a, num_sms, st, pdl) : launch_rows<64, 128, false>(a, num_sms, st, pdl);
-  return two ? launch_rows<128, 256, false>(a, num_sms, st, pdl) : launch_rows<128, 128, false>(a, num_sms, st, pdl);
+  if (a.dim == 256 || group > 128 || (int64_t)a.B * a.S > 0x7fffffff) return launch_paged_attn(a, fp8, num_sms, st, pdl);
+  // The warps' kernel reads the rows again for every 32 query rows, this one for 256; a
+  // pass over a tile takes about as long there as here (E4M3: half as long, the codes
+  // need not be converted for it), but joining a request's pieces takes it longer here,
+  // 0.4 us a piece, and few requests make many.  Measured, warps / here, us, 128 dims:
+  //   query rows                 32         48 (64)    128         256
+  //   1 x 4000, 4 kv heads                  18 / 28    22 / 29     29 / 32
+  //   1 x 16000                             27 / 35    39 / 37     63 / 42
+  //   4 x 1000                              18 / 19    24 / 20     33 / 24
+  //   4 x 4000                              28 / 23    41 / 25     68 / 29
+  //   32 x 8192 .. 16384        160 / 151  313 / 152  613 / 155
+  //   E4M3, 4 x 4000                        28 / 30    42 / 32     69 / 37
+  //   E4M3, 32 x 8192 .. 16384  158 / 322  301 / 323  575 / 324
+  const int rs = 128 / group * group;
+  const int64_t chunks = (qrows + 2 * rs - 1) / (2 * rs), more = (qrows + 31) / 32 - (fp8 ? 2 : 1) * chunks;
+  const int64_t span = a.win > 0 && (int64_t)a.win + a.S < a.max_len ? (int64_t)a.win + a.S : a.max_len;
+  const double units = (double)a.B * a.kv_heads, tiles = units * ((span + kTile - 1) / kTile);
+  if (more <= 0 || more * units * fmax(1., tiles / num_sms) < 30.) return launch_paged_attn(a, fp8, num_sms, st, pdl);
+  if (fp8) return launch_rows<128, true>(a, num_sms, st, pdl);
+  return a.dim == 64 ? launch_rows<64, false>(a, num_sms, st, pdl) : launch_rows<128, false>(a, num_sms, st, pdl);
 }
 
 }  // namespace csa

@@ -152,16 +152,21 @@ def _run(lens, s, h, hk, d, block, win=0, fp8=False, seed=0, counts=None, masks=
     pos = ((torch.tensor(lens) - m)[:, None] + (sees.sum(2) - 1)).int()
     status = torch.zeros(1, dtype=torch.int32, device=DEV)
     dev = lambda t: t.to(DEV)
-    op = csa.TreeAttention(dev(q), pool.pop("k"), pool.pop("v"), torch.tensor(lens, dtype=torch.int32, device=DEV), dev(masks),
-                           count=None if counts is None else dev(m.int()), pos=dev(pos) if win else None, win=win,
-                           status=status, **pool, **kw)
-    got = op()
-    torch.cuda.synchronize()
-    assert int(status.item()) == 0
     want = _exact(q, k, v, lens, counts, sees, pos, pool["table"].cpu(), block, win, d ** -0.5)
-    _check(got, want, (lens, s, h, hk, d, block, win, fp8))
+    kk, vv = pool.pop("k"), pool.pop("v")
+    for max_len in LONGEST:
+        op = csa.TreeAttention(dev(q), kk, vv, torch.tensor(lens, dtype=torch.int32, device=DEV), dev(masks),
+                               count=None if counts is None else dev(m.int()), pos=dev(pos) if win else None, win=win,
+                               status=status, max_len=max_len, **pool, **kw)
+        got = op()
+        torch.cuda.synchronize()
+        assert int(status.item()) == 0
+        _check(got, want, (lens, s, h, hk, d, block, win, fp8, max_len))
     return op, want
 
+
+# The bound on the lengths goes into the choice of the kernel: few and short requests, and what might be long ones.
+LONGEST = (None, 1 << 20)
 
 SHAPES = [  # drafts, heads, kv heads, dim, E4M3
     (1, 8, 8, 64, False), (5, 8, 8, 64, False), (8, 8, 2, 128, False), (3, 4, 1, 256, False), (7, 14, 2, 128, True),
@@ -243,7 +248,8 @@ def test_flat_and_peaked_weights(s, h, hk, d, fp8, qstd):
 
 @pytest.mark.gpu
 @pytest.mark.parametrize("s,h,hk,d,fp8", [(8, 8, 2, 128, False), (64, 4, 1, 128, False), (8, 8, 2, 128, True), (64, 8, 2, 128, True)])
-def test_a_chain_is_the_causal_attention(s, h, hk, d, fp8):
+@pytest.mark.parametrize("max_len", LONGEST)
+def test_a_chain_is_the_causal_attention(s, h, hk, d, fp8, max_len):
     _gpu()
     lens = [s, 300, 1111]
     pool, _, _ = _pool(lens, hk, d, 64, 4, fp8)
@@ -251,7 +257,7 @@ def test_a_chain_is_the_causal_attention(s, h, hk, d, fp8):
     n = torch.tensor(lens, dtype=torch.int32, device=DEV)
     k, v = pool.pop("k"), pool.pop("v")
     chain = csa.tree_masks((torch.arange(s) - 1).repeat(3, 1)).to(DEV)
-    got = csa.TreeAttention(q, k, v, n, chain, **pool)()
+    got = csa.TreeAttention(q, k, v, n, chain, max_len=max_len, **pool)()
     ref = csa.PagedAttention(q, k, v, n, **pool)()
     torch.cuda.synchronize()
     big = 6.0   # normal values
@@ -260,9 +266,11 @@ def test_a_chain_is_the_causal_attention(s, h, hk, d, fp8):
 
 @pytest.mark.gpu
 @pytest.mark.parametrize("s,h,hk,d,fp8", [(6, 8, 2, 128, False), (64, 4, 2, 128, False), (6, 8, 2, 128, True), (64, 8, 2, 128, True),
-                                          (40, 4, 1, 64, False), (12, 8, 1, 256, False)])
+                                          (40, 4, 1, 64, False), (12, 8, 1, 256, False), (64, 8, 2, 128, False),
+                                          (80, 8, 2, 64, False)])
 @pytest.mark.parametrize("what", ["nan", "inf", "key"])
-def test_nan_in_a_row_reaches_only_the_drafts_that_see_it(s, h, hk, d, fp8, what):
+@pytest.mark.parametrize("max_len", LONGEST)
+def test_nan_in_a_row_reaches_only_the_drafts_that_see_it(s, h, hk, d, fp8, what, max_len):
     """Drafts' rows (seen by their descendants) and a row at the window's edge hold NaN or infinity: the others' outputs
     do not change by a bit."""
     _gpu()
@@ -274,7 +282,7 @@ def test_nan_in_a_row_reaches_only_the_drafts_that_see_it(s, h, hk, d, fp8, what
     sees = _sees(masks, s)
     pos = ((torch.tensor(lens) - s)[:, None] + sees.sum(2) - 1).int()
     op = csa.TreeAttention(q, pool["k"], pool["v"], n, masks.to(DEV), pos=pos.to(DEV), win=win, table=pool["table"], block=block,
-                           k_scale=pool.get("k_scale"), v_scale=pool.get("v_scale"))
+                           k_scale=pool.get("k_scale"), v_scale=pool.get("v_scale"), max_len=max_len)
     clean = {x: t.clone() for x, t in op().items()}
     torch.cuda.synchronize()
     touched = torch.zeros(3, s, dtype=torch.bool)
@@ -315,7 +323,8 @@ def test_nan_in_a_row_reaches_only_the_drafts_that_see_it(s, h, hk, d, fp8, what
 
 @pytest.mark.gpu
 @pytest.mark.parametrize("s,h,hk,d,fp8", [(6, 8, 2, 128, False), (64, 4, 2, 128, False), (64, 8, 2, 128, True)])
-def test_bad_lengths_counts_and_pages(s, h, hk, d, fp8):
+@pytest.mark.parametrize("long", [False, True])
+def test_bad_lengths_counts_and_pages(s, h, hk, d, fp8, long):
     _gpu()
     lens, block = [100 + s, 300 + s, 200 + s, 50 + s], 16
     pool, k, v = _pool(lens, hk, d, block, 5, fp8)
@@ -323,12 +332,13 @@ def test_bad_lengths_counts_and_pages(s, h, hk, d, fp8):
     masks = _tree(4, s, 5)
     sees = _sees(masks, s)
     status = torch.zeros(1, dtype=torch.int32, device=DEV)
+    max_len = LONGEST[1] if long else 300 + s
 
     def run(n, c, table):
         status.zero_()
         i32 = lambda x: torch.tensor(x, dtype=torch.int32, device=DEV)
         got = csa.TreeAttention(q.to(DEV), pool["k"], pool["v"], i32(n), masks.to(DEV), count=i32(c), table=table, block=block,
-                                k_scale=pool.get("k_scale"), v_scale=pool.get("v_scale"), status=status, max_len=300 + s)()
+                                k_scale=pool.get("k_scale"), v_scale=pool.get("v_scale"), status=status, max_len=max_len)()
         torch.cuda.synchronize()
         return got, int(status.item())
 
@@ -336,7 +346,7 @@ def test_bad_lengths_counts_and_pages(s, h, hk, d, fp8):
         return _exact(q, kk, vv, n, c, sees, None, pool["table"].cpu(), block, 0, d ** -0.5)
 
     c = [s] * 4
-    got, st = run([100 + s, 301 + s, -1, 50 + s], c, pool["table"])
+    got, st = run([100 + s, max_len + 1, -1, 50 + s], c, pool["table"])
     assert st == 1
     _check(got, exact([100 + s, 0, 0, 50 + s], c))
     got, st = run(lens, [s + 1, -1, s, 0], pool["table"])
@@ -355,8 +365,8 @@ def test_bad_lengths_counts_and_pages(s, h, hk, d, fp8):
 
 
 @pytest.mark.gpu
-@pytest.mark.parametrize("s,h,hk", [(5, 8, 2), (64, 8, 2)])
-def test_offsets_strides_and_outside_columns(s, h, hk):
+@pytest.mark.parametrize("s,h,hk,max_len", [(5, 8, 2, 600), (64, 8, 2, 600), (64, 8, 2, 1 << 20)])
+def test_offsets_strides_and_outside_columns(s, h, hk, max_len):
     _gpu()
     lens, d = [200, 64 + s, 517], 128
     g = torch.Generator().manual_seed(3)
@@ -369,7 +379,7 @@ def test_offsets_strides_and_outside_columns(s, h, hk):
     outw = torch.full((3, s, h + 4, d), 7.0, dtype=torch.bfloat16, device=DEV)
     masks = _tree(3, s, 6)
     got = csa.TreeAttention(wide[:, :, 2:2 + h], pool[:, :hk], pool[:, hk:2 * hk],
-                            torch.tensor(lens, dtype=torch.int32, device=DEV), masks.to(DEV), off=off.to(DEV), max_len=600,
+                            torch.tensor(lens, dtype=torch.int32, device=DEV), masks.to(DEV), off=off.to(DEV), max_len=max_len,
                             out=outw[:, :, 4:], scale=0.05)()
     torch.cuda.synchronize()
     table = torch.arange(900 + s, dtype=torch.int32)[None] + off[:, None].int()
@@ -380,8 +390,8 @@ def test_offsets_strides_and_outside_columns(s, h, hk):
 
 
 @pytest.mark.gpu
-@pytest.mark.parametrize("s,h,hk", [(4, 4, 2), (48, 4, 2)])
-def test_rows_far_into_a_large_pool(s, h, hk):
+@pytest.mark.parametrize("s,h,hk,max_len", [(4, 4, 2, None), (48, 4, 2, 1 << 20)])
+def test_rows_far_into_a_large_pool(s, h, hk, max_len):
     """Rows beyond 2^32 bytes and 2^31 elements of the pool."""
     _gpu()
     d, block, rows = 128, 64, 64 * 140000
@@ -396,7 +406,7 @@ def test_rows_far_into_a_large_pool(s, h, hk):
     q = torch.randn(2, s, h, d, generator=g).bfloat16()
     masks = _tree(2, s, 6)
     got = csa.TreeAttention(q.to(DEV), k, v, torch.tensor(lens, dtype=torch.int32, device=DEV), masks.to(DEV),
-                            table=table.to(DEV), block=block)()
+                            table=table.to(DEV), block=block, max_len=max_len)()
     torch.cuda.synchronize()
     local = torch.arange(10, dtype=torch.int32).view(2, 5)
     _check(got, _exact(q, ck.double(), cv.double(), lens, None, _sees(masks, s), None, local, block, 0, d ** -0.5))
@@ -404,7 +414,8 @@ def test_rows_far_into_a_large_pool(s, h, hk):
 
 @pytest.mark.gpu
 @pytest.mark.parametrize("s,h,hk,d,fp8", [(8, 8, 2, 128, False), (64, 8, 2, 128, False), (64, 8, 2, 128, True)])
-def test_captured_replays_follow_the_device_and_repeat_exactly(s, h, hk, d, fp8):
+@pytest.mark.parametrize("max_len", LONGEST)
+def test_captured_replays_follow_the_device_and_repeat_exactly(s, h, hk, d, fp8, max_len):
     _gpu()
     lens = [700, 300, 2000, 64 + s]
     pool, k, v = _pool(lens, hk, d, 64, 8, fp8)
@@ -414,7 +425,7 @@ def test_captured_replays_follow_the_device_and_repeat_exactly(s, h, hk, d, fp8)
     c = torch.full((4,), s, dtype=torch.int32, device=DEV)
     dm = masks.to(DEV)
     kk, vv = pool.pop("k"), pool.pop("v")
-    op = csa.TreeAttention(q.to(DEV), kk, vv, n, dm, count=c, **pool)
+    op = csa.TreeAttention(q.to(DEV), kk, vv, n, dm, count=c, max_len=max_len, **pool)
     st = torch.cuda.Stream()
     st.wait_stream(torch.cuda.current_stream())
     g = torch.cuda.CUDAGraph()
