@@ -404,7 +404,7 @@ CSA_API int64_t csa_paged_attn_workspace(int32_t dim);
  * angle pos[t] * base^(-2i / rope_dim), or pos[t] * freq[i].  Pair i is dims
  * (2i, 2i + 1) of the rotated ones, as the CSA rows have them, or with halves = 1
  * (i, i + rope_dim / 2).  All of it is formed in fp32 and rounded once; the angles
- * are reduced exactly (base's: to 2^-53 of |pos theta|; freq's: of the fp32 numbers
+ * are reduced exactly (base's: to 2^-46 of |pos theta|; freq's: of the fp32 numbers
  * given), so positions may be any 32-bit number.  The sum of a head's squares must
  * stay in fp32's range. */
 typedef struct {
@@ -488,8 +488,11 @@ CSA_API int csa_kv_append(const csa_append *a, void *stream);
  * t % 64 of word t / 64 of tree[b * S + s], its own bit included.  Bits from n_b on are
  * not read.  out and lse of queries that see no row, or that are not among the n_b, are
  * zeros and -inf.  Everything else is as in csa_paged: base.win is the window, base.S
- * the drafts per request (at most 1024), and the sums, roundings, refusals and the
- * workspace are its own. */
+ * the drafts per request (at most 1024), and sums, refusals and the workspace are its
+ * own.  The weights are rounded to bf16 for the product with v; E4M3: with the row's
+ * v_scale to f16 as there, or to bf16 (the sizes decide, max_len among them).  Bit 1
+ * (value 2) of *status is set where a wait on the device gave up (out is then
+ * undefined). */
 typedef struct {
     csa_paged base;
     const uint64_t *tree;     /* [B, S, ceil(S / 64)]                               */
