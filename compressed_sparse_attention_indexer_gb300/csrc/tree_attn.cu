@@ -152,22 +152,22 @@ __device__ __forceinline__ uint32_t span_rows(const Span<kTile, true>& sp, int t
   return ones(sp.lo - r0, sp.L - r0);
 }
 
-// 32 rows' bits from row c0 on, for a draft: rows up to `out` are outside its window,
-// the drafts start at row p and are n, `bits` are its mask's 32-bit words.
-__device__ __forceinline__ uint32_t seen32(int c0, int out, int p, int n, const uint32_t* bits, int words32) {
-  uint32_t v = ones(out + 1 - c0, p - c0);
-  const int t = c0 - p;                          // draft at the first bit
-  if (t > -32 && t < n) {
-    uint32_t w;
-    if (t < 0) {
-      w = bits[0] << -t;
-    } else {
-      const int i = t >> 5;
-      w = __funnelshift_r(bits[i], i + 1 < words32 ? bits[i + 1] : 0u, t & 31);
-    }
-    v |= w & ones(-t, n - t);
+// The bits of a tile's rows, from row c0 on, for a draft: rows up to `out` are outside its
+// window, the drafts start at row p and are n, `bits` are its mask's 32-bit words (their
+// loads go out together).
+__device__ __forceinline__ void seen_rows(uint32_t* seen, int c0, int out, int p, int n, const uint32_t* bits, int words32) {
+  const int t0 = c0 - p, i0 = t0 >> 5;           // draft at the first bit, its word: rounded down
+  uint32_t w[5] = {0, 0, 0, 0, 0};
+  if (t0 > -kTile) {
+#pragma unroll
+    for (int k = 0; k < 5; ++k)
+      if (i0 + k >= 0 && i0 + k < words32) w[k] = bits[i0 + k];
   }
-  return v;
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    const int c = c0 + 32 * k, t = t0 + 32 * k;
+    seen[k] = ones(out + 1 - c, p - c) | (__funnelshift_r(w[k], w[k + 1], t0 & 31) & ones(-t, n - t));
+  }
 }
 
 __device__ __forceinline__ uint64_t sdesc_mn_sw128(uint32_t saddr, uint32_t lbo) {
@@ -442,8 +442,11 @@ __global__ void __launch_bounds__(kTtThreads, 1)
           }
           uint32_t seen[4];
           if (edge) {
-#pragma unroll
-            for (int w = 0; w < 4; ++w) seen[w] = real ? seen32(base + 32 * w, outside, p_first, pc.sp.n, bits, words32) : 0u;
+            if (real) {
+              seen_rows(seen, base, outside, p_first, pc.sp.n, bits, words32);
+            } else {
+              seen[0] = seen[1] = seen[2] = seen[3] = 0u;
+            }
 #pragma unroll
             for (int c = 0; c < 128; ++c)
               if (!((seen[c >> 5] >> (c & 31)) & 1)) x[c] = -INFINITY;
@@ -556,7 +559,7 @@ __global__ void __launch_bounds__(kTtThreads, 1)
         // A lane takes 8 codes of a row at a time, 16 lanes a row: the 16 bytes that they
         // make go to eight different places of 16 bytes in either quarter of the warp.  (16
         // codes a lane, halves exchanged so that theirs do: 541 us instead of 512 for 16 x 64
-        // drafts; four rows at a time instead of eight 518, all sixteen without a loop more.)
+        // drafts; four loads at a time instead of eight 518.)
         const int e = lane & 15, hi = lane >> 4;
         uint32_t to[4];                        // of the warp's rows 2 i + hi, i < 4; then 1024 bytes on
 #pragma unroll
