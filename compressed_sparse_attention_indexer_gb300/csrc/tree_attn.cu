@@ -16,7 +16,7 @@
 // every tile, and one slot's products run under the other's softmax (with 128 query
 // rows or fewer the second slot passes the tiles on; slots that took tiles in turn
 // there were no faster: 768 and 776 us for 64 x 16 drafts, 67 and 66 for windows of
-// small heads).
+// small heads, at the time).
 //   warps 0-3, 4-7   softmax of slot 0 and 1: a thread per query row, its 128 scores
 //                    in registers, so that maxima and sums need no exchange; the
 //                    reference maximum moves only when exceeded by 2^8 (the output is
@@ -41,6 +41,12 @@
 // infinity there are zeroed in shared memory and added by hand, to the drafts
 // that see them (add_apart).
 //
+// Measured: 64 x 16 drafts over 1024 .. 65536 bf16 rows, 32 / 4 heads of 128, 761 us
+// (6.2 TB/s: HBM); 8 x 64 drafts over 8192 .. 16384, 95 us (1000 TFLOP/s: softmax and
+// products in turn); 16 x 64 drafts over E4M3 rows, 64 / 8 heads, 503 us (780 TFLOP/s:
+// softmax and conversion share the issue slots and the instruction cache); 48 x 21 drafts
+// with a window of 1000, 16 / 8 heads of 64, 56 us (starts of units).
+//
 // Scores, maxima, sums and output are fp32; the weights are rounded to bf16 for
 // the product with V, E4M3 ones after they took V's scale (bf16 has the range of
 // fp32, so no scale makes them vanish).
@@ -58,7 +64,8 @@ namespace {
 constexpr int kTtThreads = 512;
 constexpr int kRowWarp = 8, kRowWarps = 4, kMmaWarp = 12, kMmaWarp2 = 14, kLoadWarp = 13;
 // Registers of the softmax's threads and of the others, 2 x 128 together: E4M3's converters
-// want more (56: 195 us instead of 165 for 8 x 64 drafts over 8192 .. 16384 rows, 32 / 4 heads; bf16 101 with 56, 103 with 72).
+// want more (8 x 64 drafts over 8192 .. 16384 rows, 32 / 4 heads: 146 us with 72, 158 with 64, 167 with 80;
+// bf16 97 with 56, 95 with 48 but 64 x 16 drafts 772 instead of 760).
 template <bool kFp8>
 constexpr int kRegsSoftmax = kFp8 ? 184 : 200;
 template <bool kFp8>
@@ -1101,19 +1108,21 @@ int launch_tree_attn(const PagedArgs& a, bool fp8, int num_sms, cudaStream_t st,
   // a slot takes whole tokens' heads; the coordinates of tokens and rows are ints
   if (a.dim == 256 || group > 128 || (int64_t)a.B * a.S > 0x7fffffff || a.rows > 0x7fffffff) return launch_paged_attn(a, fp8, num_sms, st, pdl);
   // The warps' kernel reads the rows again for every 32 query rows, this one for 256; a
-  // pass over a tile takes about as long there as here (E4M3: half as long, the codes
+  // pass over a tile takes about as long there as here (E4M3: 1 / 1.75 of it, the codes
   // need not be converted for it), but joining a request's pieces takes it longer here,
   // 0.4 us a piece, and few requests make many.  Measured, warps / here, us, 128 dims:
-  //   query rows                 32         48 (64)    128         256
-  //   1 x 4000, 4 kv heads                  18 / 28    22 / 29     29 / 32
-  //   1 x 16000                             27 / 35    39 / 37     63 / 42
-  //   4 x 1000                              18 / 19    24 / 20     33 / 24
-  //   4 x 4000                              28 / 23    41 / 25     68 / 29
-  //   32 x 8192 .. 16384        160 / 151  313 / 152  613 / 155
-  //   E4M3, 4 x 4000                        28 / 30    42 / 32     69 / 37
-  //   E4M3, 32 x 8192 .. 16384  158 / 322  301 / 323  575 / 324
+  //   query rows                 32         64         128        256
+  //   1 x 4000, 4 kv heads       15 / 26    18 / 27    22 / 28    29 / 31
+  //   1 x 16000                  22 / 34    27 / 35    39 / 36    63 / 40
+  //   4 x 1000                   16 / 18    18 / 18    24 / 20    33 / 23
+  //   4 x 4000                   21 / 23    29 / 23    41 / 24    68 / 29
+  //   32 x 8192 .. 16384        160 / 150  319 / 152  614 / 157  1202 / 187
+  //   E4M3, 1 x 16000            23 / 39    29 / 40    39 / 41    62 / 45
+  //   E4M3, 4 x 4000             22 / 28    28 / 28    42 / 29    69 / 34
+  //   E4M3, 32 x 8192 .. 16384  157 / 257  301 / 256  576 / 256  1124 / 279
   const int rs = 128 / group * group;
-  const int64_t chunks = (qrows + 2 * rs - 1) / (2 * rs), more = (qrows + 31) / 32 - (fp8 ? 2 : 1) * chunks;
+  const int passes = (qrows + 31) / 32, chunks = (qrows + 2 * rs - 1) / (2 * rs);
+  const double more = passes - (fp8 ? 1.75 : 1.) * chunks;
   const int64_t span = a.win > 0 && (int64_t)a.win + a.S < a.max_len ? (int64_t)a.win + a.S : a.max_len;
   const double units = (double)a.B * a.kv_heads, tiles = units * ((span + kTile - 1) / kTile);
   if (more <= 0 || more * units * fmax(1., tiles / num_sms) < 30.) return launch_paged_attn(a, fp8, num_sms, st, pdl);

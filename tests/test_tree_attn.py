@@ -443,3 +443,36 @@ def test_captured_replays_follow_the_device_and_repeat_exactly(s, h, hk, d, fp8,
         g.replay()
         torch.cuda.synchronize()
         assert all(torch.equal(first[x], op._out[x]) for x in first)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("lens,s,h,hk,d,fp8", [([1500, 1024, 1023], 1024, 2, 1, 64, False), ([1300], 1023, 4, 4, 128, True),
+                                               ([700, 90], 3, 128, 1, 128, False), ([700, 90], 2, 127, 1, 64, False),
+                                               ([300, 90], 2, 130, 1, 128, False), ([300, 90], 5, 77, 1, 128, True)])
+def test_the_most_drafts_and_heads_per_row(lens, s, h, hk, d, fp8):
+    _gpu()
+    _run(lens, s, h, hk, d, 64, fp8=fp8, seed=s + h, counts=[min(s, n) for n in lens])
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("fp8", [False, True])
+def test_two_calls_at_once(fp8):
+    """Calls on two streams with workspaces of their own, many times over each other: as each alone."""
+    _gpu()
+    ops, alone, streams = [], [], [torch.cuda.Stream(), torch.cuda.Stream()]
+    for i, (s, h, hk) in enumerate(((64, 8, 2), (16, 32, 4))):
+        lens = [2000 - 300 * i, 700, 64 + s, 1200]
+        pool, _, _ = _pool(lens, hk, 128, 64, 20 + i, fp8)
+        q = torch.randn(4, s, h, 128, generator=torch.Generator().manual_seed(i)).bfloat16().to(DEV)
+        n = torch.tensor(lens, dtype=torch.int32, device=DEV)
+        op = csa.TreeAttention(q, pool.pop("k"), pool.pop("v"), n, _tree(4, s, i).to(DEV), max_len=1 << 20, **pool)
+        alone.append({x: t.clone() for x, t in op().items()})
+        ops.append(op)
+    torch.cuda.synchronize()
+    for _ in range(20):
+        for op, st in zip(ops, streams):
+            with torch.cuda.stream(st):
+                op()
+    torch.cuda.synchronize()
+    for op, want in zip(ops, alone):
+        assert all(torch.equal(op._out[x], want[x]) for x in want)
