@@ -476,3 +476,29 @@ def test_two_calls_at_once(fp8):
     torch.cuda.synchronize()
     for op, want in zip(ops, alone):
         assert all(torch.equal(op._out[x], want[x]) for x in want)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("max_len", LONGEST)
+@pytest.mark.parametrize("scale", [2.0 ** 80, 2.0 ** -80])
+@pytest.mark.parametrize("s,h,hk", [(64, 8, 2), (5, 8, 2)])
+def test_scales_of_any_size(s, h, hk, scale, max_len):
+    """E4M3 rows whose V scales are all huge or small (flat weights add up), or a few huge among ordinary ones."""
+    _gpu()
+    lens, block = [3000, s + 100, 700], 64
+    pool, k, v = _pool(lens, hk, 128, block, 31, True)
+    q = (torch.randn(3, s, h, 128, generator=torch.Generator().manual_seed(1)) * 0.1).bfloat16()
+    masks = _tree(3, s, 2)
+    n = torch.tensor(lens, dtype=torch.int32, device=DEV)
+    kk, vv = pool.pop("k"), pool.pop("v")
+    base = pool.pop("v_scale")
+    for mix in (False, True):
+        rows = torch.zeros(base.shape[0], dtype=torch.bool)
+        rows[::7 if mix else 1] = True
+        factor = torch.where(rows, scale, 1.0).double()
+        op = csa.TreeAttention(q.to(DEV), kk, vv, n, masks.to(DEV), max_len=max_len,
+                               v_scale=base * factor.float().to(DEV)[:, None], **pool)
+        got = op()
+        torch.cuda.synchronize()
+        want = _exact(q, k, v * factor[:, None, None], lens, None, _sees(masks, s), None, pool["table"].cpu(), block, 0, 128 ** -0.5)
+        _check(got, want, (s, scale, mix, max_len))
