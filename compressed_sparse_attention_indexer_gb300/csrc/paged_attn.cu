@@ -68,7 +68,11 @@ constexpr float kWeightTop = 7.f;
 // What the joint exponentials lose elsewhere is below 2^-(126 - 2 kNear) of the
 // largest term.
 constexpr float kNear = 24.f;
-constexpr float kMinScale = 3.2311743e-27f;  // 2^-88: smaller V scales count so in the exponent
+// Exponents count V scales down to kMinScale, 2^-126.  Next to it a sum's terms, up to
+// 2^15 / |v_scale|, pass fp32's range: from a term above 2^kFarTerm on a sum is kept 2^kFar
+// smaller, as a negative number, until its reference is far enough up again.
+constexpr float kMinScale = 1.1754944e-38f;
+constexpr float kFarTerm = 104.f, kFar = 64.f, kFarBy = 18446744073709551616.f;
 
 template <int D, int MT, bool kFp8>
 struct PaShape {
@@ -119,6 +123,28 @@ __device__ __forceinline__ float move_sum(float l, float d) {
   const float f = fast_exp2(0.5f * d);
   return l * f * f;
 }
+// Sums that are 2^kFar smaller where they are negative (see kFar): moved, added, the factor
+// that is left of one, its logarithm.
+__device__ __forceinline__ float far_move(float l, float d) {
+  const bool far = l < 0.f && (d < -kFar || l > -1.f);
+  return move_sum(far ? -l : l, far ? d + kFar : d);
+}
+struct FarSum {
+  float near = 0.f, far = 0.f;
+  __device__ __forceinline__ void add(float l) {
+    near += l < 0.f ? 0.f : l;   // (a NaN is passed on)
+    far -= l < 0.f ? l : 0.f;
+  }
+  __device__ __forceinline__ float sum() const { return far > 0.f ? -(far + near * (1.f / kFarBy)) : near; }
+};
+__device__ __forceinline__ float far_add(float a, float b) {
+  FarSum x;
+  x.add(a);
+  x.add(b);
+  return x.sum();
+}
+__device__ __forceinline__ float far_rest(float l) { return l < 0.f ? 1.f / kFarBy : 1.f; }
+__device__ __forceinline__ float far_log2(float l) { return log2f(fabsf(l)) + (l < 0.f ? kFar : 0.f); }
 // D += A(16x16 f16, row) * B(16x8 f16, col), fp32 accumulate.
 __device__ __forceinline__ void mma_f16_16816(float* d, const uint32_t* a, uint32_t b0, uint32_t b1) {
   asm volatile(
@@ -287,7 +313,7 @@ __global__ void __launch_bounds__(PaShape<D, MT, kFp8>::kThreads, 1)
   // current unit's place in it
   __shared__ int64_t total_sh, unit_at;
   // E4M3, a warp's: its piece has had a V scale above 2^kNear (in a register: 388 us
-  // instead of 320 for 32 requests of 16384 .. 32768 rows, spills)
+  // instead of 320 for 32 requests of 16384 .. 32768 rows, spills) or a sum below zero
   __shared__ volatile int high_sh[Sh::kWarps];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const uint32_t ring = smem_u32(smem_raw) + warp * (Sh::kStages * Sh::kWarpStage);
@@ -495,8 +521,8 @@ __global__ void __launch_bounds__(PaShape<D, MT, kFp8>::kThreads, 1)
         // their precision whatever the scales.  The softmax's own sum takes
         // the factor out again (1 / |v_scale|), or, where the weight may vanish
         // while its part of the sum does not (`wide`: see kNear), has an
-        // exponential of its own.  |v_scale| below kMinScale (zero) counts as
-        // kMinScale, the rest of it is kept in the sign factor.
+        // exponential of its own.  |v_scale| below kMinScale (zero) counts as kMinScale, the
+        // rest of it is kept in the sign factor.
         const uint32_t src = kt + 2 * kPer * Sh::kRowBytes + (lane % kPer) * 4;
         const float ks = lds_f32(src) * scale2, vs = lds_f32(src + kPer * 4);
         const float lv = fast_log2(fmaxf(fabsf(vs), kMinScale)), inv = fast_exp2(-lv);
@@ -656,7 +682,7 @@ __global__ void __launch_bounds__(PaShape<D, MT, kFp8>::kThreads, 1)
           for (int e = 0; e < 2; ++e) {
             if (top[e] > m[mt][e] + kAbove) {
               const float to = top[e] - kBelow, f = fast_exp2(m[mt][e] - to);
-              l[mt][e] = kFp8 ? move_sum(l[mt][e], m[mt][e] - to) : l[mt][e] * f;
+              l[mt][e] = kFp8 ? far_move(l[mt][e], m[mt][e] - to) : l[mt][e] * f;
               m[mt][e] = to;
 #pragma unroll
               for (int j = 0; j < D / 8; ++j) {
@@ -664,6 +690,26 @@ __global__ void __launch_bounds__(PaShape<D, MT, kFp8>::kThreads, 1)
                 o[mt][j][2 * e + 1] *= f;
               }
             }
+          }
+        }
+        if (kFp8 && wide) {
+#pragma unroll
+          for (int y = 0; y < 2; ++y) {
+            const float ref = m[mt][y] == -INFINITY ? 0.f : m[mt][y];
+            float e[4 * kGroups], most = -INFINITY, sum = l[mt][y];
+#pragma unroll
+            for (int x = 0; x < 4 * kGroups; ++x) {
+              const float lv = lds_f32(rowsc + ((x >> 1) * 8 + c * 2 + (x & 1)) * 16 + 4), t = s[mt][x >> 1][2 * y + (x & 1)];
+              e[x] = t == -INFINITY ? t : t - lv - ref;
+              most = fmaxf(most, e[x]);
+            }
+            if (most > kFarTerm && !(sum < 0.f)) sum = -fmaxf(sum * (1.f / kFarBy), kMinScale);   // (see kFar)
+            const float off = sum < 0.f ? kFar : 0.f;
+            if (off > 0.f) high_sh[warp] = 1;
+            float to = fabsf(sum);
+#pragma unroll
+            for (int x = 0; x < 4 * kGroups; ++x) to += tiny_exp2(e[x] - off);
+            l[mt][y] = off > 0.f ? -to : to;
           }
         }
 #pragma unroll
@@ -684,16 +730,6 @@ __global__ void __launch_bounds__(PaShape<D, MT, kFp8>::kThreads, 1)
                 p[n][2 * y + e] = kFp8 ? w * t.y : w;
               }
             }
-          if (kFp8 && wide) {
-#pragma unroll
-            for (int n = 0; n < 2; ++n)
-#pragma unroll
-              for (int i = 0; i < 4; ++i) {
-                const float ref = m[mt][i >> 1] == -INFINITY ? 0.f : m[mt][i >> 1];
-                const float lv = lds_f32(rowsc + ((2 * x + n) * 8 + c * 2 + (i & 1)) * 16 + 4), t = s[mt][2 * x + n][i];
-                l[mt][i >> 1] += t == -INFINITY ? 0.f : tiny_exp2(t - lv - ref);
-              }
-          }
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
             const float x0 = p[i >> 1][(i & 1) * 2], x1 = p[i >> 1][(i & 1) * 2 + 1];
@@ -749,8 +785,11 @@ __global__ void __launch_bounds__(PaShape<D, MT, kFp8>::kThreads, 1)
       for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
-          l[mt][e] += __shfl_xor_sync(0xffffffffu, l[mt][e], 1);
-          l[mt][e] += __shfl_xor_sync(0xffffffffu, l[mt][e], 2);
+#pragma unroll
+          for (int x = 1; x <= 2; ++x) {
+            const float other = __shfl_xor_sync(0xffffffffu, l[mt][e], x);
+            l[mt][e] = kFp8 ? far_add(l[mt][e], other) : l[mt][e] + other;
+          }
         }
       float* so = slots + (warp % Sh::kSlots) * Sh::kSlotFloats;
       float* sml = slots + Sh::kSlots * Sh::kSlotFloats + (warp % Sh::kSlots) * 2 * Sh::kRows;
@@ -796,7 +835,7 @@ __global__ void __launch_bounds__(PaShape<D, MT, kFp8>::kThreads, 1)
               const float m2 = sml[r], top = fmaxf(m[mt][e], m2), ref = top == -INFINITY ? 0.f : top;
               const float f1 = fast_exp2(m[mt][e] - ref), f2 = fast_exp2(m2 - ref);
               if (kFp8)
-                l[mt][e] = move_sum(l[mt][e], m[mt][e] - ref) + move_sum(sml[Sh::kRows + r], m2 - ref);
+                l[mt][e] = far_add(far_move(l[mt][e], m[mt][e] - ref), far_move(sml[Sh::kRows + r], m2 - ref));
               else
                 l[mt][e] = l[mt][e] * f1 + sml[Sh::kRows + r] * f2;
               m[mt][e] = top;
@@ -839,28 +878,34 @@ __global__ void __launch_bounds__(PaShape<D, MT, kFp8>::kThreads, 1)
         for (int x = 0; x < Sh::kSlots; ++x) top = fmaxf(top, ml[x * 2 * Sh::kRows + r]);
         const float ref = top == -INFINITY ? 0.f : top;
         float sum = 0.f, acc[D / 32];
+        FarSum sums;
 #pragma unroll
         for (int i = 0; i < D / 32; ++i) acc[i] = 0.f;
 #pragma unroll
         for (int x = 0; x < Sh::kSlots; ++x) {
           const float d = ml[x * 2 * Sh::kRows + r] - ref, f = fast_exp2(d), ls = ml[x * 2 * Sh::kRows + Sh::kRows + r];
-          sum += kFp8 ? move_sum(ls, d) : ls * f;
+          if (kFp8)
+            sums.add(far_move(ls, d));
+          else
+            sum += ls * f;
 #pragma unroll
           for (int i = 0; i < D / 32; ++i)
             acc[i] += row_at[x * Sh::kSlotFloats + i] * f;
         }
+        if (kFp8) sum = sums.sum();
         if (whole) {
           const int i = row0 + r, s = token_of(i), hd = h * group + i - s * group;
           // some row weighs (a NaN is passed on)
-          const bool any = (sum > 0.f || sum != sum) && (!kTree || s < cu.sp.n);
-          const float inv = any ? 1.f / sum : 0.f;
+          const bool any = sum != 0.f && (!kTree || s < cu.sp.n);
+          const float inv = any ? 1.f / (kFp8 ? fabsf(sum) : sum) : 0.f, rest = kFp8 ? far_rest(sum) : 1.f;
           __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(a.out) + ((int64_t)cu.b * a.S + s) * a.out_stride + hd * D +
                                lane * (D / 32);
 #pragma unroll
           for (int x = 0; x < D / 32; x += 2)
-            *reinterpret_cast<uint32_t*>(dst + x) = kTree && !any ? 0u : pack_bf16x2(acc[x] * inv, acc[x + 1] * inv);
+            *reinterpret_cast<uint32_t*>(dst + x) = kTree && !any ? 0u : pack_bf16x2(acc[x] * inv * rest, acc[x + 1] * inv * rest);
           if (a.lse && lane == 0)
-            a.lse[((int64_t)cu.b * a.S + s) * a.heads + hd] = any ? (top + log2f(sum)) * kLn2 : -INFINITY;
+            a.lse[((int64_t)cu.b * a.S + s) * a.heads + hd] =
+                any ? (top + (kFp8 ? far_log2(sum) : log2f(sum))) * kLn2 : -INFINITY;
         } else {
           float* dst = part + (pslot * Sh::kRows + r) * (D + 2);
 #pragma unroll
@@ -914,7 +959,7 @@ __global__ void __launch_bounds__(32 * kJoinWarps)
     const float m2 = src[D], l2 = src[D + 1];
     const float top = fmaxf(m, m2), ref = top == -INFINITY ? 0.f : top;
     const float f1 = fast_exp2(m - ref), f2 = fast_exp2(m2 - ref);
-    l = kFp8 ? move_sum(l, m - ref) + move_sum(l2, m2 - ref) : l * f1 + l2 * f2;
+    l = kFp8 ? far_add(far_move(l, m - ref), far_move(l2, m2 - ref)) : l * f1 + l2 * f2;
     m = top;
 #pragma unroll
     for (int x = 0; x < D / 32; ++x) acc[x] = acc[x] * f1 + src[lane + 32 * x] * f2;
@@ -928,22 +973,27 @@ __global__ void __launch_bounds__(32 * kJoinWarps)
   for (int w = 0; w < kJoinWarps; ++w) top = fmaxf(top, sm_m[w]);
   const float ref = top == -INFINITY ? 0.f : top;
   float sum = 0.f, f[kJoinWarps];
+  FarSum sums;
 #pragma unroll
   for (int w = 0; w < kJoinWarps; ++w) {
     f[w] = fast_exp2(sm_m[w] - ref);
-    sum += kFp8 ? move_sum(sm_l[w], sm_m[w] - ref) : sm_l[w] * f[w];
+    if (kFp8)
+      sums.add(far_move(sm_l[w], sm_m[w] - ref));
+    else
+      sum += sm_l[w] * f[w];
   }
+  if (kFp8) sum = sums.sum();
   const int s = i / group, hd = h * group + i - s * group;
-  const bool any = (sum > 0.f || sum != sum) && (!kTree || !a.count || s < a.count[j.b]);
+  const bool any = sum != 0.f && (!kTree || !a.count || s < a.count[j.b]);
   const int64_t tok = (int64_t)j.b * a.S + s;
   if (threadIdx.x < D) {
     const int d = threadIdx.x;
     float v = 0.f;
 #pragma unroll
     for (int w = 0; w < kJoinWarps; ++w) v += sm_o[w][d] * f[w];
-    static_cast<__nv_bfloat16*>(a.out)[tok * a.out_stride + hd * D + d] = __float2bfloat16_rn(any ? v / sum : 0.f);
+    static_cast<__nv_bfloat16*>(a.out)[tok * a.out_stride + hd * D + d] = __float2bfloat16_rn(any ? v / (kFp8 ? fabsf(sum) : sum) * (kFp8 ? far_rest(sum) : 1.f) : 0.f);
   }
-  if (a.lse && threadIdx.x == 0) a.lse[tok * a.heads + hd] = any ? (top + log2f(sum)) * kLn2 : -INFINITY;
+  if (a.lse && threadIdx.x == 0) a.lse[tok * a.heads + hd] = any ? (top + (kFp8 ? far_log2(sum) : log2f(sum))) * kLn2 : -INFINITY;
 }
 
 template <int D, int MT, bool kFp8, bool kTree>

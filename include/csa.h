@@ -349,8 +349,8 @@ CSA_API int csa_fp8_matmul(const csa_fp8_mm *a, void *stream);
  * table[b * table_stride + r / block] * block + r % block with a block table,
  * as in csa_batch.  Scores, the softmax's maximum and sum, and the sum over
  * rows are fp32; the weights are rounded to bf16 for the product with v (E4M3
- * pools: weights with the row's v_scale to f16, and to 2^-32 of the largest, and q to
- * 2^-25 of its row's largest element). */
+ * pools: weights with the row's v_scale, of any size, to f16, and to 2^-32 of the largest,
+ * which a row of zeros may have, and q to 2^-25 of its row's largest element). */
 typedef struct {
     int32_t B, S;             /* requests (0: a no-op), new tokens per request      */
     int32_t heads, kv_heads;  /* heads a multiple of kv_heads                       */
