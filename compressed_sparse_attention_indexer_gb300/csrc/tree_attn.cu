@@ -48,8 +48,11 @@
 // with a window of 1000, 16 / 8 heads of 64, 56 us (starts of units).
 //
 // Scores, maxima, sums and output are fp32; the weights are rounded to bf16 for
-// the product with V, E4M3 ones after they took V's scale (bf16 has the range of
-// fp32, so no scale makes them vanish).
+// the product with V, E4M3 ones after they took V's scale: scales of a request may
+// lie any factor apart (a row of zeros has 1), which bf16's range holds without an
+// exponent per row, and f16's, as the warps' kernel has them, would not.  bf16 ends
+// as low as fp32 does, so that E4M3 weights are lifted (kLift) for scales next to
+// 2^-126.
 #include <cudaTypedefs.h>
 
 #include "csa_internal.cuh"
@@ -75,6 +78,14 @@ constexpr int kTile = 128;                 // K / V rows per tile
 constexpr int kExtra = 2;                  // a unit's start and end, in tiles
 constexpr int kSub = kTile * 128;          // 128 rows x 64 dims bf16
 constexpr float kGrow = 8.f;               // the reference maximum moves when exceeded by this (log2 units)
+// E4M3: V's scales are taken 2^lift larger (and the output back), so that weights with one of
+// 2^-126 are normal bf16 numbers down to 2^-lift of the largest, and off by 2^-(lift + 8) of it
+// below that.  Weights of up to 2^8 times codes of up to 2^9 and scales of up to 2^80 over L rows
+// stay in fp32 for lift <= 30 - log2 L.  (A lift that ended with the first tile of larger
+// scales, known from its converters: 579 us instead of 503 for 16 x 64 drafts.)
+constexpr int kLift = 16;
+__device__ __forceinline__ int lift_of(int L) { return min(kLift, __clz(L - 1) - 2); }
+__device__ __forceinline__ float pow2(int e) { return __int_as_float((127 + e) << 23); }
 constexpr int kScaleTiles = 8;             // tiles whose E4M3 scales are held
 constexpr int kScaleBytes = kTile * 2 * 4; // K's and V's of a tile
 
@@ -528,7 +539,7 @@ __global__ void __launch_bounds__(kTtThreads, 1)
       jj += pc.nt;
       if (busy && ok) {
         const bool any = real && (l > 0.f || l != l);
-        const float inv = any ? 1.f / l : 0.f;
+        const float down = kFp8 ? pow2(-lift_of(pc.sp.L)) : 1.f, inv = any ? 1.f / l * down : 0.f;
         const int64_t pslot = (int64_t)blockIdx.x * 2 + (at_piece == 0 ? 0 : 1);
         float* dst = part + (pslot * kRows + slot * 128 + (t & ~31)) * (D + 2) + lane;
 #pragma unroll 1
@@ -546,7 +557,7 @@ __global__ void __launch_bounds__(kTtThreads, 1)
               }
             } else {
 #pragma unroll
-              for (int e = 0; e < 32; ++e) dst[(c + e) * 32] = o[e];
+              for (int e = 0; e < 32; ++e) dst[(c + e) * 32] = kFp8 ? o[e] * down : o[e];
             }
           }
         }
@@ -586,7 +597,7 @@ __global__ void __launch_bounds__(kTtThreads, 1)
         // it whole, the span's rows of the warp's
         bool some_ahead = false, edge_ahead = false, some = false, edge = false;
         uint32_t rows_ahead = 0, rows = 0;
-        float ks = 0.f, vs = 0.f;
+        float ks = 0.f, vs = 0.f, up = 1.f;
         auto ahead = [&] {                     // `at` to the next tile with rows, its place looked up
           while (left > 0 && at.sp.L <= 0) {
             if (--left > 0) at.next(a, units);
@@ -605,6 +616,7 @@ __global__ void __launch_bounds__(kTtThreads, 1)
           if (!spot.resolve(a, -1, row)) row = -1;
           const int h = chunks == 1 ? at.unit : at.unit / chunks;
           ks = vs = 0.f;
+          up = pow2(lift_of(at.sp.L));
           if (row >= 0) ks = a.k_scale[(int64_t)row * a.scale_stride + h], vs = a.v_scale[(int64_t)row * a.scale_stride + h];
           if (left > 0 && --left > 0) at.next(a, units);
         };
@@ -658,7 +670,7 @@ __global__ void __launch_bounds__(kTtThreads, 1)
                 const uint32_t to = scales + (tile % kScaleTiles) * kScaleBytes + (w * 32 + lane) * 4;
                 const bool number = fabsf(vs) < INFINITY;
                 asm volatile("st.shared.f32 [%0], %1;\n" ::"r"(to), "f"(number ? ks * (a.scale * kLog2e) : __uint_as_float(0x7fffffffu)) : "memory");
-                asm volatile("st.shared.f32 [%0], %1;\n" ::"r"(to + kTile * 4), "f"(number ? vs : 1.f) : "memory");
+                asm volatile("st.shared.f32 [%0], %1;\n" ::"r"(to + kTile * 4), "f"(number ? vs * up : 1.f) : "memory");
               }
               if (look) {
                 bad = __reduce_or_sync(0xffffffffu, bad) & mask;

@@ -491,9 +491,9 @@ CSA_API int csa_kv_append(const csa_append *a, void *stream);
  * the drafts per request (at most 1024), and sums, refusals and the workspace are its
  * own.  The weights are rounded to bf16 for the product with v; E4M3: with the row's
  * v_scale to f16 as there, or to bf16 (the sizes decide, max_len among them), for which
- * |v_scale| is at most 2^80 (weights of up to 2^8 over 2^30 rows stay in fp32).  Bit 1
- * (value 2) of *status is set where a wait on the device gave up (out is then
- * undefined). */
+ * |v_scale| is at most 2^80 (weights of up to 2^8 over 2^30 rows stay in fp32) and loses
+ * bits below 2^-126.  Bit 1 (value 2) of *status is set where a wait on the device gave up
+ * (out is then undefined). */
 typedef struct {
     csa_paged base;
     const uint64_t *tree;     /* [B, S, ceil(S / 64)]                               */

@@ -61,7 +61,7 @@ def check(got, want, unit=1.0, warps=False):
 
 
 # drafts, heads, kv heads, the bound on the lengths: few query rows and short requests go to the warps' kernel
-SHAPES = [(5, 8, 2, None), (16, 8, 1, None)]
+SHAPES = [(5, 8, 2, None), (16, 8, 1, None), (16, 8, 1, 1 << 20), (64, 8, 2, 1 << 20)]
 
 
 def _rows(lens, s, h, hk, seed, qstd):
