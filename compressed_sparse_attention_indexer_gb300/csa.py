@@ -622,20 +622,32 @@ def tree_attn_workspace(dim: int) -> int:
     return int(lib().csa_tree_attn_workspace(int(dim)))
 
 
-def tree_masks(parent):
+def tree_masks(parent, win: int = 0):
     """The masks csa_tree_attn takes, int64 [B, S, ceil(S / 64)], of trees given by each draft's parent: parent [B, S],
-    an earlier draft of the request, or negative for a draft that follows the context's last token."""
+    an earlier draft of the request, or negative for a draft that follows the context's last token.  win: the sliding
+    window (0: none), which the attention applies to the rows before the drafts alone: ancestors `win` and more
+    tokens back are left out."""
     import torch
     if parent.dim() != 2 or parent.dtype not in (torch.int32, torch.int64):
         _bad("parent must be int32 or int64 of shape (B, S)")
+    if win < 0:
+        _bad("win must be >= 0")
     b, s = parent.shape
     if bool((parent >= torch.arange(s, device=parent.device)).any()):
         _bad("a draft's parent must come before it")
     masks = torch.zeros(b, s, -(-s // 64), dtype=torch.int64, device=parent.device)
+    depth = torch.zeros(b, s, dtype=torch.int64, device=parent.device)
     at = torch.arange(b, device=parent.device)
     for t in range(s):
         p = parent[:, t].long()
-        masks[:, t] = torch.where((p >= 0)[:, None], masks[at, p.clamp_min(0)], 0)
+        seen = torch.where((p >= 0)[:, None], masks[at, p.clamp_min(0)], 0)
+        depth[:, t] = torch.where(p >= 0, depth[at, p.clamp_min(0)] + 1, 0)
+        if win > 0 and t > 0:
+            near = torch.zeros(b, masks.shape[2] * 64, dtype=torch.int64, device=parent.device)
+            near[:, :t] = depth[:, :t] > depth[:, t:t + 1] - win
+            bits = near.view(b, -1, 64) << torch.arange(64, device=parent.device)
+            seen = seen & bits.sum(2)
+        masks[:, t] = seen
         masks[:, t, t // 64] |= -2 ** 63 if t % 64 == 63 else 1 << (t % 64)
     return masks
 
@@ -644,8 +656,9 @@ class TreeAttention(PagedAttention):
     """csa_tree_attn: attention of a tree of S drafted tokens per request over its cache.
 
     tree [B, S, ceil(S / 64)] int64: bit t % 64 of word t / 64 set where a draft sees draft t, itself included
-    (tree_masks makes them of parents).  count [B] int32: the real drafts of each request, the first of its S (None:
-    all S); they lie in the last rows of its context.  pos [B, S] int32: the drafts' positions, needed with a window.
+    (tree_masks makes them of parents; with a window give it that too: here it hides rows before the drafts only).
+    count [B] int32: the real drafts of each request, the first of its S (None: all S); they lie in the last rows of
+    its context.  pos [B, S] int32: the drafts' positions, needed with a window.
     workspace: at least tree_attn_workspace(dim) bytes.  The rest is as in PagedAttention."""
 
     def __init__(self, q, k, v, ctx_len, tree, count=None, pos=None, table=None, block: int = 0, off=None, k_scale=None,

@@ -485,8 +485,9 @@ CSA_API int csa_kv_append(const csa_append *a, void *stream);
  * row L_b - n_b + t.  Draft s sees every row r < L_b - n_b before them, with a window
  * those with r > p - win only, p = pos[b * S + s] (taken to the nearest of L_b - n_b ..
  * L_b - 1), and of the drafts' rows those whose bit is set in its mask: draft t is bit
- * t % 64 of word t / 64 of tree[b * S + s], its own bit included.  Bits from n_b on are
- * not read.  out and lse of queries that see no row, or that are not among the n_b, are
+ * t % 64 of word t / 64 of tree[b * S + s], its own bit included (a window does not
+ * reach among the drafts: a mask leaves out the ancestors that it hides).  Bits from n_b
+ * on are not read.  out and lse of queries that see no row, or that are not among the n_b, are
  * zeros and -inf.  Everything else is as in csa_paged: base.win is the window, base.S
  * the drafts per request (at most 1024), and sums, refusals and the workspace are its
  * own.  The weights are rounded to bf16 for the product with v; E4M3: with the row's
