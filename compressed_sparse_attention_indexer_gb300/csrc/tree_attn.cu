@@ -59,6 +59,7 @@
 #include "paged.cuh"
 #include "ptx.cuh"
 #include "tc5.cuh"
+#include "tree_pipeline.h"
 
 namespace csa {
 
@@ -86,7 +87,7 @@ constexpr float kGrow = 8.f;               // the reference maximum moves when e
 constexpr int kLift = 16;
 __device__ __forceinline__ int lift_of(int L) { return min(kLift, __clz(L - 1) - 2); }
 __device__ __forceinline__ float pow2(int e) { return __int_as_float((127 + e) << 23); }
-constexpr int kScaleTiles = 8;             // tiles whose E4M3 scales are held
+constexpr int kScaleTiles = kTreeScales;
 constexpr int kScaleBytes = kTile * 2 * 4; // K's and V's of a tile
 
 struct TtSmem {
@@ -108,15 +109,13 @@ struct TtShape {
   static constexpr int kSubs = D / 64;
   static constexpr int kStage = kSubs * kSub;
   static constexpr int kQBytes = kRows / 128 * kStage;
-  static constexpr int kRawDepth = kFp8 ? 3 : 1;   // chunks of codes beside the ring
+  static constexpr int kRawDepth = kFp8 ? kTreeRaw : 1;   // chunks of codes beside the ring
   static constexpr int kRaw = kFp8 ? kTile * D : 0;
   static constexpr int kScales = kFp8 ? kScaleTiles * kScaleBytes : 0;
-  static constexpr int kRoom = (227 * 1024 - (int)sizeof(TtSmem) - kQBytes - kRawDepth * kRaw - kScales) / kStage;
-  static constexpr int kStages = kRoom > 8 ? 8 : kRoom;
+  static constexpr int kStages = tree_stages(D, kFp8);
   static constexpr int kSmem = kQBytes + kStages * kStage + kRawDepth * kRaw + kScales + (int)sizeof(TtSmem);
-  static_assert(kStages >= 3, "a batch's V and K");
-  // a tile's scales stay until its weights are made: its V then waits in the ring, so
-  // that the tile being written is at most kStages / 2 + 1 tiles ahead
+  static_assert(kSmem <= 227 * 1024, "shared memory");
+  static_assert(kStages >= 3 && kStages <= 8, "a batch's V and K; barriers");
   static_assert(kStages / 2 + 1 < kScaleTiles, "scales");
 };
 
@@ -518,8 +517,10 @@ __global__ void __launch_bounds__(kTtThreads, 1)
           }
           tc5::tmem_wait_st();
           if (edge) {
-            const uint32_t v = 2 * (jj + j) + 1, st = v % ST;   // V's place in the ring
-            ok = warp_wait(sm.full[st], (v / ST) & 1, abort);
+            TreePlace<ST> v;
+            v.set(2 * (jj + j) + 1);
+            const uint32_t st = v.st;
+            ok = warp_wait(sm.full[st], v.ph, abort);
             if (!ok) break;
             uint32_t bad[4];
 #pragma unroll
@@ -686,14 +687,15 @@ __global__ void __launch_bounds__(kTtThreads, 1)
               ++n;
         };
         // (K and V of tile after tile: pieces do not matter, which leaves registers)
-        uint32_t st = 0, ph = 1;
+        TreePlace<ST> to_ring;
+        to_ring.ph = 1;                        // (of the phase before)
         for (uint32_t tile = 0; ok && some; ++tile) {
           const bool edge_now = edge;
           const uint32_t rows_now = rows;
 #pragma unroll 1
           for (int kv = 0; ok && kv < 2; ++kv) {
-            convert(st, n >= ST, ph, kv, tile, kv && edge_now, rows_now);
-            if (++st == ST) st = 0, ph ^= 1;
+            convert(to_ring.st, n >= ST, to_ring.ph, kv, tile, kv && edge_now, rows_now);
+            to_ring.move(1);
             if (!kv) {
               fetch();
               ahead();
@@ -790,16 +792,15 @@ __global__ void __launch_bounds__(kTtThreads, 1)
         }
       };
       // the place in the ring, or of E4M3 codes beside it: counted up
-      uint32_t at = 0, ph = 1;                 // its phase before
-      bool again = false;                      // the ring has come round
-      constexpr uint32_t kPlaces = kFp8 ? Sh::kRawDepth : ST;
+      TreeFeed<kFp8 ? Sh::kRawDepth : ST> feed;
       bool ok = true;
       constexpr int kCopies = kFp8 ? 1 : Sh::kSubs;   // of a segment
       const int copies = segs * kCopies;
       const uint32_t to_lane = lane / kCopies * seg * 128 + lane % kCopies * kSub;
       // tile t of the block: its K or V
       auto copy = [&](int t, bool v, int h, bool edge) {
-        if (again) ok = warp_wait(kFp8 ? sm.raw_empty[at] : sm.empty[at], ph, abort);
+        const uint32_t at = feed.at;
+        if (feed.again) ok = warp_wait(kFp8 ? sm.raw_empty[at] : sm.empty[at], feed.ph, abort);
         if (!ok) return;
         const uint32_t bar = smem_u32(kFp8 ? &sm.raw_full[at] : edge ? &sm.land[at] : &sm.full[at]);
         const uint32_t to = kFp8 ? raw + at * Sh::kRaw : ring + at * Sh::kStage;
@@ -820,7 +821,7 @@ __global__ void __launch_bounds__(kTtThreads, 1)
             for (int c = 0; c < kCopies; ++c)
               tc5::tma_load_2d(to + (lane * per + i) * seg * 128 + c * kSub, map, h * D + 64 * c, row[i], bar);
         }
-        if (++at == kPlaces) at = 0, ph ^= 1, again = true;
+        feed.next();
       };
       look();
       lookup();
@@ -868,15 +869,6 @@ __global__ void __launch_bounds__(kTtThreads, 1)
         ok = __all_sync(0xffffffffu, ok);
         tc5::fence_after_sync();
       };
-      // K or V in the ring, moved on to its next tile's
-      struct Next {
-        uint32_t st, ph;
-        __device__ __forceinline__ void set(uint32_t place) { st = place % ST, ph = (place / ST) & 1; }
-        __device__ __forceinline__ void move(uint32_t by = 2) {
-          st += by;
-          if (st >= ST) st -= ST, ph ^= 1;
-        }
-      };
       uint32_t jj = 0;                         // tiles before the piece
       Walk walk;
       walk.init(a, sm.cut);
@@ -886,7 +878,7 @@ __global__ void __launch_bounds__(kTtThreads, 1)
         const int h = chunks == 1 ? pc.unit : pc.unit / chunks, row0 = (pc.unit - h * chunks) * unit_rows;
         if (row0 + slot * rs >= qrows) {
           // no rows for this slot: what it would have read is given back
-          Next c;
+          TreePlace<ST> c;
           c.set(2 * jj);
 #pragma unroll 1
           for (int i = 0; ok && i < 2 * pc.nt; ++i, c.move(1)) {
@@ -896,7 +888,7 @@ __global__ void __launch_bounds__(kTtThreads, 1)
           wait(sm.q_full, qph);
           if (ok && elect_one()) tc5::mbar_arrive(smem_u32(&sm.q_empty));
         } else {
-          Next k, v;
+          TreePlace<ST> k, v;                  // moved on to the next tile's
           k.set(2 * jj);
           v.set(2 * jj + 1);
           wait(sm.q_full, qph);
@@ -932,8 +924,8 @@ __global__ void __launch_bounds__(kTtThreads, 1)
               }
               if (out) tc5::mma_commit(smem_u32(&sm.empty[v.st]));
             }
-            if (in) k.move();
-            if (out) v.move();
+            if (in) k.move(2);
+            if (out) v.move(2);
           }
         }
         qph ^= 1;
