@@ -821,7 +821,7 @@ __global__ void __launch_bounds__(kTtThreads, 1)
             for (int c = 0; c < kCopies; ++c)
               tc5::tma_load_2d(to + (lane * per + i) * seg * 128 + c * kSub, map, h * D + 64 * c, row[i], bar);
         }
-        feed.next();
+        feed.next(edge);
       };
       look();
       lookup();
@@ -842,9 +842,15 @@ __global__ void __launch_bounds__(kTtThreads, 1)
           for (int v = 0; ok && v < 2; ++v) copy(t, v, h, v && !kFp8 && edge_tile(a, sp, tile0 + t));
         }
       }
-      // the copies have landed when the block ends, unless a wait gave up: their time is waited for
-      if (*abort)
-        for (int i = 0; i < 100; ++i) __nanosleep(1000);
+      // the copies land before the block ends, whoever gave up meanwhile
+      bool landed = true;
+#pragma unroll 1
+      for (uint32_t i = 0; landed && i < (kFp8 ? Sh::kRawDepth : ST); ++i) {
+        bool other;
+        uint32_t parity;
+        if (feed.last(i, other, parity))
+          landed = tc5::mbar_wait_drain(smem_u32(kFp8 ? &sm.raw_full[i] : other ? &sm.land[i] : &sm.full[i]), parity);
+      }
     } else if (warp == kMmaWarp || warp == kMmaWarp2) {
       // ---------------------------------------------------------- MMA issue
       // The warp runs as one (waits, ring places: the same in every lane), a lane issues.

@@ -37,13 +37,24 @@ struct TreePlace {
   }
 };
 
-// The loader's way through its N places (the ring's, or the codes').
+// The loader's way through its N places (the ring's, or the codes').  A chunk lands on the
+// place's barrier, or (`other`) on a second one that it has.
 template <int N>
 struct TreeFeed {
-  uint32_t at = 0, ph = 1;   // the place, the parity of its empty barrier's phase before
-  bool again = false;        // a chunk has been there
-  CSA_TREE_FN void next() {
+  uint32_t at = 0, ph = 1;            // the place, the parity of its empty barrier's phase before
+  bool again = false;                 // a chunk has been there
+  uint32_t others = 0, turns = 0;     // bit i: place i's last chunk was the other barrier's; that one's phases, modulo 2
+  CSA_TREE_FN void next(bool other) {
+    others = other ? others | 1u << at : others & ~(1u << at);
+    turns ^= other ? 1u << at : 0u;
     if (++at == N) at = 0, ph ^= 1, again = true;
+  }
+  // The barrier and the parity of the phase in which place i's last chunk lands; false
+  // when it had none.  The chunks before have landed, or the place would not have been free.
+  CSA_TREE_FN bool last(uint32_t i, bool& other, uint32_t& parity) const {
+    other = (others >> i) & 1;
+    parity = other ? ((turns >> i) & 1) ^ 1 : i < at ? ph ^ 1 : ph;
+    return again || i < at;
   }
 };
 

@@ -1,6 +1,7 @@
 """The order of csa_tree_attn's tcgen05 kernel on the host: the kernel's own ring (csrc/tree_pipeline.h), compiled by the
 host compiler into a model with mbarriers that tell a phase by its parity alone, run under random orders in which
-every warp, copy and product may be late: every one reads the chunk it means, and every order ends."""
+every warp, copy and product may be late, and waits may give up: every one reads the chunk it means, every order ends, and
+nothing lands behind its block's end."""
 import os
 import shutil
 import subprocess
@@ -31,6 +32,7 @@ def test_every_order_gives_each_product_its_own_chunk_and_ends(model):
 @pytest.mark.parametrize("mistake,found", [
     ("unseen", "a product with a V that is not its tile's"),          # a slot that gives back a phase it has not seen
     ("one-slot", "warps that wait for one another"),                  # two phases where one is meant: the same parity
+    ("no-drain", "a copy or a product behind its block's end"),       # a loader that leaves before its copies have landed
     ("unlooked", "a V's rows apart that are another chunk's"),
     ("few-scales", "scales that are another tile's"),
 ])

@@ -1,8 +1,9 @@
 // Runs the ring of csa_tree_attn's tcgen05 kernel (tree_pipeline.h) as a model in which every warp, every copy
 // and every product may be as late as it likes, with mbarriers that tell a phase by its parity alone, as the
 // hardware's do.  The warps are the kernel's, wait for wait: the loader, E4M3's converters or bf16's readers of V,
-// the queries' warp, two MMA warps, two slots' softmax warps.  Arguments: how many random orders to run per shape, and
-// which mistake is planted to see that the model finds it ("none" for none, see main).
+// the queries' warp, two MMA warps, two slots' softmax warps.  In half of the orders a wait gives up at some point, as
+// one that ran out does, and the others' after it: nothing may be under way when the last warp is gone.  Arguments:
+// how many random orders to run per shape, and which mistake is planted to see that the model finds it (see main).
 // Prints a line per shape and returns the number of shapes that went wrong.
 #include <coroutine>
 #include <cstdio>
@@ -45,21 +46,31 @@ struct Warp {
     void return_void() {}
     void unhandled_exception() { std::terminate(); }
     std::function<bool()> until;               // what it waits for; empty: it may go on
+    bool may_give_up = false, seen = true;
   };
   std::coroutine_handle<promise_type> h;
   bool done() const { return h.done(); }
-  bool step() {
-    if (h.done() || (h.promise().until && !h.promise().until())) return false;
-    h.promise().until = nullptr;
+  // give_up: whether a wait that is not over gives up
+  bool step(bool give_up) {
+    if (h.done()) return false;
+    promise_type& p = h.promise();
+    p.seen = !p.until || p.until();
+    if (!p.seen && !(give_up && p.may_give_up)) return false;
+    p.until = nullptr;
     h.resume();
     return true;
   }
 };
 struct Until {
   std::function<bool()> f;
+  bool may_give_up = false;
+  Warp::promise_type* p = nullptr;
   bool await_ready() { return false; }
-  void await_suspend(std::coroutine_handle<Warp::promise_type> h) { h.promise().until = f; }
-  void await_resume() {}
+  void await_suspend(std::coroutine_handle<Warp::promise_type> h) {
+    p = &h.promise();
+    p->until = f, p->may_give_up = may_give_up;
+  }
+  bool await_resume() { return p->seen; }
 };
 
 template <int ST, bool kFp8>
@@ -87,7 +98,10 @@ struct Model {
   std::vector<Warp> warps;
 
   void fault(const char* what) { if (!wrong) wrong = what; }
-  Until see(Bar& b, uint32_t parity) { return {[&b, parity] { return b.test(parity); }}; }
+  Until see(Bar& b, uint32_t parity) { return {[&b, parity] { return b.test(parity); }, true}; }
+  Until drain(Bar& b, uint32_t parity) { return {[&b, parity] { return b.test(parity); }}; }
+  long patience = -1;                                   // the turn from which on a wait gives up; -1: none does
+  bool abort = false;
   Until pause() { return {}; }
 
   Model(unsigned seed, Plan p) : rng(seed), plan(p) {
@@ -130,11 +144,13 @@ struct Model {
   Warp loader() {
     TreeFeed<kPlaces> feed;
     int chunk = 0;
+    bool ok = true;
     for (const Piece& p : pieces) {
       if (p.empty) continue;
-      for (int c = 0; c < 2 * p.nt; ++c, ++chunk) {
+      for (int c = 0; ok && c < 2 * p.nt; ++c, ++chunk) {
         const uint32_t at = feed.at;
-        if (feed.again) co_await see(kFp8 ? raw_empty[at] : empty[at], feed.ph);
+        if (feed.again) ok = co_await see(kFp8 ? raw_empty[at] : empty[at], feed.ph);
+        if (!ok) break;
         const bool look = !kFp8 && c % 2 && p.edge[c / 2];
         Bar& bar = kFp8 ? raw_full[at] : look ? land[at] : full[at];
         bar.expect(kParts);
@@ -143,9 +159,15 @@ struct Model {
             if (kFp8) raw[at][x] = chunk;
             else for (int w = x; w < kRowWarps; w += kParts) stage[at][w] = chunk;
           }});
-        feed.next();
+        feed.next(look);
         co_await pause();
       }
+    }
+    if (plan.is("no-drain")) co_return;
+    for (uint32_t i = 0; i < kPlaces; ++i) {
+      bool other;
+      uint32_t parity;
+      if (feed.last(i, other, parity)) co_await drain(kFp8 ? raw_full[i] : other ? land[i] : full[i], parity);
     }
   }
 
@@ -157,8 +179,8 @@ struct Model {
       if (p.empty) continue;
       for (int c = 0; c < 2 * p.nt; ++c, ++n) {
         const int slot = n % kTreeRaw, tile = n / 2;
-        co_await see(raw_full[slot], (n / kTreeRaw) & 1);
-        if (n >= ST) co_await see(empty[to.st], to.ph);
+        if (!co_await see(raw_full[slot], (n / kTreeRaw) & 1)) co_return;
+        if (n >= ST && !co_await see(empty[to.st], to.ph)) co_return;
         for (int x : raw[slot]) if (x != n) fault("codes converted that are another chunk's");
         stage[to.st][w] = -1;
         co_await pause();
@@ -186,7 +208,7 @@ struct Model {
       for (int j = 0; j < p.nt; ++j) {
         if (!p.edge[j]) continue;
         const int v = 2 * (jj + j) + 1, st = v % ST;
-        co_await see(land[st], (parity >> st) & 1);
+        if (!co_await see(land[st], (parity >> st) & 1)) co_return;
         parity ^= 1u << st;
         if (stage[st][w] != v) fault("a V looked through that is another chunk");
         co_await pause();
@@ -202,44 +224,44 @@ struct Model {
     int n_q = 0;
     for (size_t i = 0; i < pieces.size(); ++i) {
       if (pieces[i].empty) continue;
-      if (n_q > 0) co_await see(q_empty, (n_q - 1) & 1);
+      if (n_q > 0 && !co_await see(q_empty, (n_q - 1) & 1)) break;
       const int slots = pieces[i].rows[1] ? 2 : 1;
       q_full.expect(slots);
       for (int s = 0; s < slots; ++s) flight.push_back({&q_full, [this, s, i] { q_holds[s] = (int)i; }});
       ++n_q;
       co_await pause();
     }
-    if (n_q > 0) co_await see(q_full, (n_q - 1) & 1);
+    if (n_q > 0) co_await drain(q_full, (n_q - 1) & 1);
   }
 
   Warp issuer(int slot) {
     uint32_t jj = 0, pph = 0, qph = 0;
-    for (size_t i = 0; i < pieces.size(); ++i) {
+    bool ok = true;
+    for (size_t i = 0; ok && i < pieces.size(); ++i) {
       const Piece& p = pieces[i];
       if (p.empty) continue;
       if (!p.rows[slot]) {
         TreePlace<ST> c;
         c.set(2 * jj);
-        for (int x = 0; x < 2 * p.nt; ++x, c.move(1)) {
-          if (!plan.is("unseen")) co_await see(full[c.st], c.ph);
-          empty[c.st].arrive();
+        for (int x = 0; ok && x < 2 * p.nt; ++x, c.move(1)) {
+          if (!plan.is("unseen")) ok = co_await see(full[c.st], c.ph);
+          if (ok) empty[c.st].arrive();
           co_await pause();
         }
-        co_await see(q_full, qph);
-        q_empty.arrive();
+        if (ok) ok = co_await see(q_full, qph);
+        if (ok) q_empty.arrive();
       } else {
         TreePlace<ST> k, v;
         k.set(2 * jj);
         v.set(2 * jj + 1);
-        co_await see(q_full, qph);
-        for (int j = -1; j < p.nt; ++j) {
+        ok = co_await see(q_full, qph);
+        for (int j = -1; ok && j < p.nt; ++j) {
           const bool out = j >= 0, in = j + 1 < p.nt;
-          if (in) co_await see(full[k.st], k.ph);
-          if (out) {
-            co_await see(full[v.st], v.ph);
-            co_await see(p_full[slot], pph);
-            pph ^= 1;
-          }
+          if (in) ok = co_await see(full[k.st], k.ph);
+          if (ok && out) ok = co_await see(full[v.st], v.ph);
+          if (ok && out) ok = co_await see(p_full[slot], pph);
+          if (out) pph ^= 1;
+          if (!ok) break;
           Batch b;
           b.slot = slot, b.piece = (int)i;
           if (out) b.v = 2 * ((int)jj + j) + 1;
@@ -301,10 +323,10 @@ struct Model {
       if (p.rows[slot]) {
         for (int j = 0; j < p.nt; ++j) {
           const int at = jj + j;
-          co_await see(s_full[slot], n_s++ & 1);
+          if (!co_await see(s_full[slot], n_s++ & 1)) co_return;
           ++reading[slot];
           if (scores[slot] != at) fault("scores that are another tile's");
-          if (kFp8) co_await see(sc_full[at % kTreeScales], (at / kTreeScales) & 1);
+          if (kFp8 && !co_await see(sc_full[at % kTreeScales], (at / kTreeScales) & 1)) co_return;
           for (int turn = 0; turn < 2; ++turn) {        // K's scales, later V's
             if (kFp8) for (int x : scales[at % scale_slots]) if (x != at) fault("scales that are another tile's");
             co_await pause();
@@ -313,14 +335,14 @@ struct Model {
           if (p.edge[j]) {
             TreePlace<ST> v;
             v.set(2 * at + 1);
-            if (!plan.is("unlooked")) co_await see(full[v.st], v.ph);
+            if (!plan.is("unlooked") && !co_await see(full[v.st], v.ph)) co_return;
             for (int x : bad[v.st]) if (x != 2 * at + 1) fault("a V's rows apart that are another chunk's");
           }
           --reading[slot];
           p_full[slot].arrive();
           co_await pause();
         }
-        co_await see(o_full[slot], n_o++ & 1);
+        if (!co_await see(o_full[slot], n_o++ & 1)) co_return;
         if (output[slot] != (int)i || added[slot] != p.nt) fault("an output that is not its piece's");
         co_await pause();
         taken[slot][w] = (int)i;
@@ -330,7 +352,12 @@ struct Model {
   }
 
   bool turn(size_t actor) {
-    if (actor < warps.size()) return warps[actor].step();
+    if (actor < warps.size()) {
+      const bool waits = !warps[actor].done() && warps[actor].h.promise().until && !warps[actor].h.promise().until();
+      const bool out = abort || (patience >= 0 && turns >= patience);
+      if (out && waits && warps[actor].h.promise().may_give_up) abort = true;
+      return warps[actor].step(out);
+    }
     actor -= warps.size();
     if (actor < 2) {
       const bool some = !pipe[actor].empty();
@@ -349,13 +376,15 @@ struct Model {
     for (const Warp& w : warps) if (!w.done()) return false;
     return true;
   }
+  long turns = 0;
   const char* run() {
+    if (rng() % 2) patience = rng() % 2000;
     // how often each actor gets a turn: some almost never, for a while
     const size_t actors = warps.size() + 3;
     std::vector<int> weight(actors);
     long idle = 0;
-    for (long n = 0; !wrong && !over(); ++n) {
-      if (n % 64 == 0)
+    for (; !wrong && !over(); ++turns) {
+      if (turns % 64 == 0)
         for (int& w : weight) w = rng() % 4 == 0 ? 1 : 1 + rng() % 40;
       int all = 0;
       for (int w : weight) all += w;
@@ -396,7 +425,7 @@ int main(int argc, char** argv) {
   const int orders = argc > 1 ? std::atoi(argv[1]) : 1000;
   Plan plan;
   // none; unseen: a slot without rows gives back what has not come; one-slot: a stage is free when either slot is done
-  // with it; unlooked: a V's rows apart are read before it was looked through; few-scales
+  // with it; no-drain: the loader leaves with copies under way; unlooked: a V's rows apart are read before it was looked through; few-scales
   if (argc > 2) plan.mistake = argv[2];
   return check<tree_stages(64, false), false>("64", orders, plan) + check<tree_stages(128, false), false>("128", orders, plan) +
          check<tree_stages(128, true), true>("128 E4M3", orders, plan);
