@@ -568,6 +568,7 @@ __global__ void __launch_bounds__(kTtThreads, 1)
         }
       }
     }
+    tc5::tmem_wait_st();   // a wait that gave up may have left stores under way
   } else {
     setmaxnreg_dec<kRegsOthers<kFp8>>();
     if (warp < kMmaWarp) {
