@@ -1116,8 +1116,8 @@ size_t tree_attn_workspace(int dim, int num_sms) {
 
 int launch_tree_attn(const PagedArgs& a, bool fp8, int num_sms, cudaStream_t st, bool pdl) {
   const int group = a.heads / a.kv_heads, qrows = a.S * group;
-  // a slot takes whole tokens' heads; the coordinates of tokens and rows are ints
-  if (a.dim == 256 || group > 128 || (int64_t)a.B * a.S > 0x7fffffff || a.rows > 0x7fffffff) return launch_paged_attn(a, fp8, num_sms, st, pdl);
+  // a slot takes whole tokens' heads; the coordinates of tokens are ints (a pool's rows are, see run_paged)
+  if (a.dim == 256 || group > 128 || (int64_t)a.B * a.S > 0x7fffffff) return launch_paged_attn(a, fp8, num_sms, st, pdl);
   // The warps' kernel reads the rows again for every 32 query rows, this one for 256; a
   // pass over a tile takes about as long there as here (E4M3: 1 / 1.75 of it, the codes
   // need not be converted for it), but joining a request's pieces takes it longer here,
