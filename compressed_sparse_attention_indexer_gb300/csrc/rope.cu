@@ -22,8 +22,9 @@
 //
 // Measured: 16384 tokens of 32 + 8 heads of 128, bf16, 59 us (5.66 TB/s; with their
 // values and into pages 70 us, 5.74 TB/s); 64 tokens of 65 heads of 576, 4.5 us; one
-// token 3.5 .. 3.9 us, which is a launch.  E4M3 is bound by its instructions (maximum,
-// quotient and its correction, code): 131072 keys of 128 in 23 us (2.2 TB/s).
+// token 3.5 .. 3.9 us, which is a launch.  131072 keys of 128 (64 dims turned) to E4M3 in 23 us
+// (2.2 TB/s): 19 with 16 dims turned, 21 without the norm, 19 into a bf16 pool.  Regions off
+// whole units: 16384 tokens as above with 24 dims turned 131 us (2.6 TB/s).
 #include "csa_internal.cuh"
 #include "ptx.cuh"
 #include "rows.cuh"

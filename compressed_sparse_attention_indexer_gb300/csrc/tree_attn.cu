@@ -43,7 +43,7 @@
 //
 // Measured: 64 x 16 drafts over 1024 .. 65536 bf16 rows, 32 / 4 heads of 128, 761 us
 // (6.2 TB/s: HBM); 8 x 64 drafts over 8192 .. 16384, 95 us (1000 TFLOP/s: softmax and
-// products in turn); 16 x 64 drafts over E4M3 rows, 64 / 8 heads, 503 us (780 TFLOP/s:
+// products in turn); 16 x 64 drafts over E4M3 rows, 64 / 8 heads, 512 us (765 TFLOP/s:
 // softmax and conversion share the issue slots and the instruction cache); 48 x 21 drafts
 // with a window of 1000, 16 / 8 heads of 64, 56 us (starts of units).
 //
@@ -83,7 +83,8 @@ constexpr float kGrow = 8.f;               // the reference maximum moves when e
 // 2^-126 are normal bf16 numbers down to 2^-lift of the largest, and off by 2^-(lift + 8) of it
 // below that.  Weights of up to 2^8 times codes of up to 2^9 and scales of up to 2^80 over L rows
 // stay in fp32 for lift <= 30 - log2 L.  (A lift that ended with the first tile of larger
-// scales, known from its converters: 579 us instead of 503 for 16 x 64 drafts.)
+// scales, known from its converters: 579 us instead of 512 for 16 x 64 drafts; by max_len, a
+// constant of the launch: 507, but bits that go with it.)
 constexpr int kLift = 16;
 __device__ __forceinline__ int lift_of(int L) { return min(kLift, __clz(L - 1) - 2); }
 __device__ __forceinline__ float pow2(int e) { return __int_as_float((127 + e) << 23); }
@@ -1128,9 +1129,9 @@ int launch_tree_attn(const PagedArgs& a, bool fp8, int num_sms, cudaStream_t st,
   //   4 x 1000                   16 / 18    18 / 18    24 / 20    33 / 23
   //   4 x 4000                   21 / 23    29 / 23    41 / 24    68 / 29
   //   32 x 8192 .. 16384        160 / 150  319 / 152  614 / 157  1202 / 187
-  //   E4M3, 1 x 16000            23 / 39    29 / 40    39 / 41    62 / 45
-  //   E4M3, 4 x 4000             22 / 28    28 / 28    42 / 29    69 / 34
-  //   E4M3, 32 x 8192 .. 16384  157 / 257  301 / 256  576 / 256  1124 / 279
+  //   E4M3, 1 x 16000            23 / 40    29 / 41    40 / 42    61 / 46
+  //   E4M3, 4 x 4000             23 / 28    29 / 28    43 / 30    70 / 34
+  //   E4M3, 32 x 8192 .. 16384  152 / 267  293 / 269  557 / 271  1074 / 283
   const int rs = 128 / group * group;
   const int passes = (qrows + 31) / 32, chunks = (qrows + 2 * rs - 1) / (2 * rs);
   const double more = passes - (fp8 ? 1.75 : 1.) * chunks;
