@@ -703,7 +703,10 @@ __global__ void __launch_bounds__(PaShape<D, MT, kFp8>::kThreads, 1)
               e[x] = t == -INFINITY ? t : t - lv - ref;
               most = fmaxf(most, e[x]);
             }
-            if (most > kFarTerm && !(sum < 0.f)) sum = -fmaxf(sum * (1.f / kFarBy), kMinScale);   // (see kFar)
+            if (most > kFarTerm && !(sum < 0.f)) {   // (see kFar; a NaN stays)
+              sum *= 1.f / kFarBy;
+              sum = sum < kMinScale ? -kMinScale : -sum;
+            }
             const float off = sum < 0.f ? kFar : 0.f;
             if (off > 0.f) high_sh[warp] = 1;
             float to = fabsf(sum);

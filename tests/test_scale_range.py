@@ -151,6 +151,25 @@ def test_causal_attention(s, h, hk, lens, power):
 
 @pytest.mark.gpu
 @pytest.mark.parametrize("s,h,hk,max_len", SHAPES)
+@pytest.mark.parametrize("at", [0, 3, 700, 1499])
+def test_a_nan_key_beside_the_smallest_scales(s, h, hk, max_len, at):
+    # it reaches out and lse, whether the rows that take the sum to fp32's end come before or behind it (enough
+    # requests for a block to have several tiles of one)
+    _gpu()
+    lens = [1500 + s] * 80
+    pool, k, codes, q, r = _rows(lens, s, h, hk, 47, 1.0)
+    masks = _tree(len(lens), s, 2)
+    vs = torch.where((r < at) == (at > 100), 2.0 ** -126, 1.0).double()[:, None].expand(-1, hk).contiguous()
+    row = pool["table"][::2, at // 64].long() * 64 + at % 64
+    pool["k_scale"][row] = float("nan")
+    got = _attend(pool, codes, vs, q, lens, masks, max_len=max_len)
+    torch.cuda.synchronize()
+    for x in ("out", "lse"):
+        assert got[x][::2].isnan().all() and got[x][1::2].isfinite().all(), x
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("s,h,hk,max_len", SHAPES)
 def test_tiny_values_from_append_to_attention(s, h, hk, max_len):
     """Keys and values as csa_kv_append writes them: values whose scale is the smallest that it writes."""
     _gpu()
