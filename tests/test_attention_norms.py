@@ -133,6 +133,7 @@ def test_planted_mistakes_are_found(sample, mistake):
 # GPU
 
 LONG = [[20011], [9000, 200, 101, 12001, 640], [177] * 40]
+MANY = [(130 + 37 * i) % 700 + 70 for i in range(650)]     # more requests than a block has threads
 SHAPES = [(8, 8, 2, 128, False), (6, 4, 1, 256, False), (64, 4, 1, 128, False), (30, 16, 2, 64, False), (64, 8, 2, 128, True),
           (16, 8, 1, 128, True), (9, 4, 2, 128, True)]
 
@@ -155,6 +156,14 @@ def _tree_faults(lens, s, h, hk, d, fp8, block, max_len, seed, counts=None, win=
 @pytest.mark.parametrize("max_len", [None, 1 << 20])
 def test_long_requests_that_are_split_and_joined(lens, s, h, hk, d, fp8, max_len):
     assert _tree_faults(lens, s, h, hk, d, fp8, 128, max_len, d) == []
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("s,h,hk,d,fp8", [(8, 8, 1, 128, False), (64, 1, 1, 64, False), (40, 2, 1, 128, True), (3, 2, 1, 128, True)])
+@pytest.mark.parametrize("max_len", [None, 1 << 20])
+def test_many_requests(s, h, hk, d, fp8, max_len):
+    counts = [s if i % 5 else i % (s + 1) for i in range(len(MANY))]
+    assert _tree_faults(MANY, s, h, hk, d, fp8, 64, max_len, 13, counts) == []
 
 
 @pytest.mark.gpu
